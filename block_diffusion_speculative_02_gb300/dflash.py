@@ -29,6 +29,7 @@ STATUS_BITS = {
     "bad_token": 1 << 4,
     "capacity": 1 << 5,
     "timeout": 1 << 6,
+    "bad_value": 1 << 7,
 }
 
 EXPORTED = ["dflash_workspace_bytes", "dflash_workspace_init", "dflash_ctx_project",
@@ -38,7 +39,9 @@ EXPORTED = ["dflash_workspace_bytes", "dflash_workspace_init", "dflash_ctx_proje
             "dflash_draft_workspace_bytes", "dflash_draft_qkv", "dflash_draft_mlp",
             "dflash_draft_tokens", "dflash_verify_attention", "dflash_gdn_replay",
             "dflash_prefill_workspace_bytes", "dflash_ctx_prefill", "dflash_selftest_wait",
-            "dflash_prefill_attention", "dflash_prefill_staged"]
+            "dflash_prefill_attention", "dflash_prefill_staged",
+            "dflash_kv4_workspace_bytes", "dflash_kv_reserve", "dflash_qk_norm_rope",
+            "dflash_kv4_append", "dflash_kv4_gather", "dflash_kv4_attention"]
 
 
 class DFlashError(RuntimeError):
@@ -62,6 +65,16 @@ class KVViewC(ctypes.Structure):
                 ("free_list", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
                 ("capacity", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
+class KV4Dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class KV4ViewC(ctypes.Structure):
+    _fields_ = [("kv", KVViewC), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
 
 
 _lib = None
@@ -130,6 +143,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_draft_mlp.argtypes = [ctypes.POINTER(Dims), i32] + [vp] * 8 + [vp, sz, vp]
     lib.dflash_draft_tokens.restype = ctypes.c_int
     lib.dflash_draft_tokens.argtypes = [ctypes.POINTER(Dims)] + [vp] * 6 + [vp, sz, vp]
+    dims4, view4, i64, f32 = (ctypes.POINTER(KV4Dims), ctypes.POINTER(KV4ViewC), ctypes.c_int64,
+                              ctypes.c_float)
+    lib.dflash_kv4_workspace_bytes.restype = sz
+    lib.dflash_kv4_workspace_bytes.argtypes = [dims4]
+    lib.dflash_kv_reserve.restype = ctypes.c_int
+    lib.dflash_kv_reserve.argtypes = [dims4, ctypes.POINTER(KVViewC)] + [vp] * 6 + [sz, vp]
+    lib.dflash_qk_norm_rope.restype = ctypes.c_int
+    lib.dflash_qk_norm_rope.argtypes = [dims4, vp, i64, vp, i64, vp, vp, vp, f32, f32, vp, i64, vp,
+                                        i64, vp]
+    lib.dflash_kv4_append.restype = ctypes.c_int
+    lib.dflash_kv4_append.argtypes = [dims4, vp, i64, vp, i64, vp, view4, vp, sz, vp]
+    lib.dflash_kv4_gather.restype = ctypes.c_int
+    lib.dflash_kv4_gather.argtypes = [dims4, vp, view4, vp, vp, vp, sz, vp]
+    lib.dflash_kv4_attention.restype = ctypes.c_int
+    lib.dflash_kv4_attention.argtypes = [dims4, vp, vp, view4, f32, ctypes.c_int, vp, vp, sz, vp]
     lib.dflash_cycle_sm_split.restype = ctypes.c_int
     lib.dflash_cycle_sm_split.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(i32),
                                           ctypes.POINTER(i32)]
@@ -421,3 +449,162 @@ def dflash_gdn_replay(state, tape_k, tape_v, tape_beta, tape_g, accept_len, ws, 
         _dev(tape_beta, torch.float32, "tape_beta"), _dev(tape_g, torch.float32, "tape_g"),
         _dev(accept_len, torch.int32, "accept_len"), _dev(ws, name="ws"), ws.numel(),
         _stream(stream)), "dflash_gdn_replay")
+
+
+# ---------------------------------------------------------------------------
+# serving over a KV cache held in 4 bits
+# ---------------------------------------------------------------------------
+def make_kv4_dims(batch, n_tokens, max_tokens, n_q_heads, n_kv_heads, head_dim) -> KV4Dims:
+    return KV4Dims(batch, n_tokens, max_tokens, n_q_heads, n_kv_heads, head_dim)
+
+
+@dataclass
+class KV4View:
+    """A KV cache in 4-bit cells (see dflash_kv4_view in include/dflash.h).
+
+    ``cells``: uint8 [n_pages, Hkv, page_size / 16, 18 D] (paged) or
+    [B, Hkv, capacity / 16, 18 D].  ``pages()`` is the view that
+    dflash_kv_reserve and dflash_kv_crop take."""
+    cells: torch.Tensor
+    seq_len: torch.Tensor                      # int32 [B]
+    capacity: int
+    page_table: Optional[torch.Tensor] = None  # int32 [B, max_pages]
+    free_list: Optional[torch.Tensor] = None   # int32 [n_pages]
+    free_count: Optional[torch.Tensor] = None  # int32 [1]
+    page_size: int = 16
+    k_exp: Optional[torch.Tensor] = None       # int32 [Hkv]
+    v_exp: Optional[torch.Tensor] = None
+
+    def pages(self) -> KVView:
+        return KVView(None, None, self.seq_len, self.capacity, self.page_table, self.free_list,
+                      self.free_count, self.page_size)
+
+
+def alloc_kv4_cells(n_slabs: int, n_kv_heads: int, rows: int, head_dim: int,
+                    device="cuda") -> torch.Tensor:
+    """Zeroed cells for ``n_slabs`` pages (or sequences) of ``rows`` rows (a multiple of 16)."""
+    if rows < 16 or rows % 16 or head_dim not in (64, 128):
+        raise ValueError("rows must be a multiple of 16 and head_dim 64 or 128")
+    return torch.zeros(n_slabs, n_kv_heads, rows // 16, 18 * head_dim, dtype=torch.uint8,
+                       device=device)
+
+
+def dflash_kv4_workspace_bytes(dims: KV4Dims) -> int:
+    n = load_library().dflash_kv4_workspace_bytes(ctypes.byref(dims))
+    if n == 0:
+        raise DFlashError(-3, "dflash_kv4_workspace_bytes")
+    return int(n)
+
+
+def alloc_kv4_workspace(dims: KV4Dims, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for the calls over a 4-bit cache."""
+    return torch.zeros(dflash_kv4_workspace_bytes(dims), dtype=torch.uint8, device=device)
+
+
+def _on(t, device: int, dtype, numel: int, name: str, least: bool = False) -> Optional[int]:
+    """Pointer of a contiguous tensor on this device with this type and size (``least``: at least
+    this size)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
+    if t.numel() != numel and not (least and t.numel() > numel):
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
+    """(pointer, row pitch) of a bf16 [rows, heads, D] tensor whose rows are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+        raise ValueError(f"{name} must be a bf16 tensor on cuda:{device}")
+    if t.dim() != 3 or t.shape != (rows, heads, d):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (st[1] != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), st[0] if rows > 1 else max(st[0], heads * d)
+
+
+def _pages_on(v, device: int, batch: int, k: Optional[int]) -> KVViewC:
+    i32 = torch.int32
+    seq = _on(v.seq_len, device, i32, batch, "seq_len")
+    table = v.page_table
+    if table is None:
+        return KVViewC(k, None, seq, None, None, None, v.capacity, 0, 0, 0)
+    if table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError(f"page_table must be [{batch}, max_pages]")
+    n = v.free_list.numel()
+    return KVViewC(k, None, seq, _on(table, device, i32, table.numel(), "page_table"),
+                   _on(v.free_list, device, i32, n, "free_list"),
+                   _on(v.free_count, device, i32, 1, "free_count"),
+                   v.capacity, v.page_size, table.shape[1], n)
+
+
+def _view4_on(v: KV4View, device: int, dims: KV4Dims) -> KV4ViewC:
+    cells = v.cells
+    rows = v.page_size if v.page_table is not None else v.capacity
+    slabs = v.free_list.numel() if v.page_table is not None else dims.batch
+    k = _on(cells, device, torch.uint8,
+            slabs * dims.n_kv_heads * (rows // 16) * 18 * dims.head_dim, "cells")
+    return KV4ViewC(_pages_on(v, device, dims.batch, k),
+                    _on(v.k_exp, device, torch.int32, dims.n_kv_heads, "k_exp"),
+                    _on(v.v_exp, device, torch.int32, dims.n_kv_heads, "v_exp"))
+
+
+def dflash_kv_reserve(dims: KV4Dims, cache, n_new, start, pos, slot, new_len, ws, stream=None):
+    """Pages, positions and slots of the batch's new rows.  ``cache``: a KVView or KV4View."""
+    dev, i32, b, n = torch.cuda.current_device(), torch.int32, dims.batch, dims.n_tokens
+    view = _pages_on(cache, dev, b, None)
+    _check(load_library().dflash_kv_reserve(
+        dims, view, _on(n_new, dev, i32, b, "n_new"), _on(start, dev, i32, b + 1, "start"),
+        _on(pos, dev, i32, n, "pos"), _on(slot, dev, i32, n, "slot"),
+        _on(new_len, dev, i32, b, "new_len"), _on(ws, dev, torch.uint8, 0, "ws", True),
+        ws.numel(), _stream(stream)), "dflash_kv_reserve")
+
+
+def dflash_qk_norm_rope(dims: KV4Dims, q, k, q_norm_w, k_norm_w, pos, rope_theta: float,
+                        rms_eps: float, q_out, k_out, stream=None):
+    """Per-head norms of q [N, Hq, D] and k [N, Hkv, D], rotated at ``pos``; rows may be strided."""
+    dev, bf, n, d = torch.cuda.current_device(), torch.bfloat16, dims.n_tokens, dims.head_dim
+    q_p, q_s = _rows_on(q, dev, n, dims.n_q_heads, d, "q")
+    k_p, k_s = _rows_on(k, dev, n, dims.n_kv_heads, d, "k")
+    qo_p, qo_s = _rows_on(q_out, dev, n, dims.n_q_heads, d, "q_out")
+    ko_p, ko_s = _rows_on(k_out, dev, n, dims.n_kv_heads, d, "k_out")
+    _check(load_library().dflash_qk_norm_rope(
+        dims, q_p, q_s, k_p, k_s, _on(q_norm_w, dev, bf, d, "q_norm_w"),
+        _on(k_norm_w, dev, bf, d, "k_norm_w"), _on(pos, dev, torch.int32, n, "pos"), rope_theta,
+        rms_eps, qo_p, qo_s, ko_p, ko_s, _stream(stream)), "dflash_qk_norm_rope")
+
+
+def dflash_kv4_append(dims: KV4Dims, k, v, slot, cache: KV4View, ws, stream=None):
+    """Quantise k, v [N, Hkv, D] (rows may be strided) into the rows ``slot`` of the cache."""
+    dev, n = torch.cuda.current_device(), dims.n_tokens
+    k_p, k_s = _rows_on(k, dev, n, dims.n_kv_heads, dims.head_dim, "k")
+    v_p, v_s = _rows_on(v, dev, n, dims.n_kv_heads, dims.head_dim, "v")
+    _check(load_library().dflash_kv4_append(
+        dims, k_p, k_s, v_p, v_s, _on(slot, dev, torch.int32, n, "slot"),
+        _view4_on(cache, dev, dims), _on(ws, dev, torch.uint8, 0, "ws", True), ws.numel(),
+        _stream(stream)), "dflash_kv4_append")
+
+
+def dflash_kv4_gather(dims: KV4Dims, slot, cache: KV4View, k_out, v_out, ws, stream=None):
+    """Rows ``slot`` of the cache as bf16 [N, Hkv, D]."""
+    dev, bf, n = torch.cuda.current_device(), torch.bfloat16, dims.n_tokens
+    size = n * dims.n_kv_heads * dims.head_dim
+    _check(load_library().dflash_kv4_gather(
+        dims, _on(slot, dev, torch.int32, n, "slot"), _view4_on(cache, dev, dims),
+        _on(k_out, dev, bf, size, "k_out"), _on(v_out, dev, bf, size, "v_out"),
+        _on(ws, dev, torch.uint8, 0, "ws", True), ws.numel(), _stream(stream)),
+        "dflash_kv4_gather")
+
+
+def dflash_kv4_attention(dims: KV4Dims, q, start, cache: KV4View, scale: float, causal: bool, out,
+                         ws, stream=None):
+    """Attention of the rows q [N, Hq, D] over the 4-bit cache that holds them already."""
+    dev, bf, n = torch.cuda.current_device(), torch.bfloat16, dims.n_tokens
+    size = n * dims.n_q_heads * dims.head_dim
+    _check(load_library().dflash_kv4_attention(
+        dims, _on(q, dev, bf, size, "q"), _on(start, dev, torch.int32, dims.batch + 1, "start"),
+        _view4_on(cache, dev, dims), scale, 1 if causal else 0, _on(out, dev, bf, size, "out"),
+        _on(ws, dev, torch.uint8, 0, "ws", True), ws.numel(), _stream(stream)),
+        "dflash_kv4_attention")

@@ -79,6 +79,7 @@ typedef struct CUstream_st* dflash_stream_t;
 #define DFLASH_ST_BAD_TOKEN (1u << 4)     /* block id outside [0, vocab)            */
 #define DFLASH_ST_CAPACITY (1u << 5)      /* length or write past the cache capacity */
 #define DFLASH_ST_TIMEOUT (1u << 6)       /* a bounded in-kernel wait gave up       */
+#define DFLASH_ST_BAD_VALUE (1u << 7)     /* NaN or infinity quantised to 4 bits     */
 
 /* Model and cycle shapes.  block must be 16 (staged token + 15 masks,
  * [P2] 块扩散草稿 step 1).  Supported: head_dim in {64, 128};
@@ -424,6 +425,147 @@ DFLASH_API int dflash_gdn_replay(int32_t batch, int32_t n_heads, int32_t dk, int
                                  const int32_t* accept_len, void* ws, size_t ws_bytes,
                                  dflash_stream_t stream);
 
+/*
+ * Serving over a KV cache held in 4 bits: the calls of one layer for a ragged
+ * batch ([P2] 保证三: what the caches hold bounds the batch).  The batch's new
+ * rows lie back to back, sequence after sequence: rows start[b] ..
+ * start[b + 1] - 1 of q, k, v and out belong to sequence b.  Rows behind the
+ * last sequence (a batch padded to a fixed n_tokens) are left as they were.
+ *   dflash_kv_reserve   pages for the new rows; start, pos, slot, new_len
+ *   dflash_qk_norm_rope per-head norms of q and k, rotated at pos
+ *   dflash_kv4_append   k, v rows quantised into the cells named by slot
+ *   dflash_kv4_attention  the new rows' attention over the whole cache
+ *   dflash_kv4_gather   cached rows back as bf16
+ * A verify forward appends its block and attends with causal = 1; the drafter
+ * appends its block, attends with causal = 0 and crops it off again; a token
+ * by token decode passes one row a sequence; a prompt any number.  The crop
+ * is dflash_kv_crop on the view's `kv` member.
+ */
+typedef struct {
+  int32_t batch;         /* B: sequences, 1..4096                               */
+  int32_t n_tokens;      /* N: rows of this call, padding included              */
+  int32_t max_tokens;    /* upper bound on the new rows of any one sequence     */
+  int32_t n_q_heads;     /* Hq: a multiple of Hkv, at most 64 Hkv               */
+  int32_t n_kv_heads;    /* Hkv                                                 */
+  int32_t head_dim;      /* D: 64 or 128                                        */
+} dflash_kv4_dims;
+
+/* A KV cache in 4 bits.  Its unit is the cell: 16 consecutive rows of one KV
+ * head, 18 D bytes, so that one copy moves what the attention needs of them:
+ *   K codes  [D/32][16 rows][16]  byte j of a 16-byte piece: dims 2j (low
+ *                                 nibble) and 2j + 1 of the piece's 32 dims
+ *   V codes  [D/2][16 rows]       byte (p, r): dims 2p (low nibble), 2p + 1
+ *   K scales [16 rows][D/16]      e4m3, one for 16 consecutive dims
+ *   V scales [D/16][16 rows]
+ * An element is 2^exp[head] * scale * code; codes are e2m1 (sign, 2 exponent
+ * bits, 1 mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6), exponents -64..64 (others
+ * count as the nearer end).  kv.k points at the cells, kv.v is NULL:
+ *   paged:      [n_pages][Hkv][page_size / 16][18 D], page_size a multiple of 16
+ *   contiguous: [B][Hkv][capacity / 16][18 D], capacity a multiple of 16
+ * The other members of kv are those of a bf16 cache. */
+typedef struct {
+  dflash_kv_view kv;
+  const int32_t* k_exp;  /* int32 [Hkv] device, or NULL: all 0 */
+  const int32_t* v_exp;
+} dflash_kv4_view;
+
+/* Bytes of the workspace that serves all of these calls for these dims on the
+ * current device (zeroed once with dflash_workspace_init; its status word
+ * reads with dflash_read_status).  0 on bad dims. */
+DFLASH_API size_t dflash_kv4_workspace_bytes(const dflash_kv4_dims* dims);
+
+/*
+ * dflash_kv_reserve — block tables and slot maps from lengths, for a bf16 or a
+ * 4-bit cache.  With L_b = cache->seq_len[b] and n_b = n_new[b]:
+ *   start[b]   = n_0 + .. + n_{b-1}, b = 0..B
+ *   pos[start[b] + i]  = L_b + i, i < n_b
+ *   slot[start[b] + i] = the row of the pool where row L_b + i is kept: page *
+ *                        page_size + row in the page (paged), b * capacity +
+ *                        row (contiguous)
+ *   new_len[b] = L_b + n_b   (may alias cache->seq_len)
+ * Pages that rows L_b .. L_b + n_b - 1 lack are taken from the top of the free
+ * list, in order of the sequence and then of the page, so the tables depend on
+ * the lengths alone; a page already mapped stays, and a second call with the
+ * same lengths changes nothing.  pos and slot of the rows behind the last
+ * sequence are -1.
+ *   n_new, new_len: int32 [B]; start: int32 [B + 1]; pos, slot: int32 [N].
+ * A sequence that cannot be served is left as it was: new_len[b] = L_b, its
+ * pos and slot are -1 (start still counts its rows).  That is a sequence with
+ * n_b < 0 (counted as 0 rows), L_b < 0, L_b + n_b past the capacity, n_b >
+ * max_tokens or rows past n_tokens (DFLASH_ST_CAPACITY), or one that needs more
+ * pages than the earlier ones leave (DFLASH_ST_POOL_EMPTY).
+ * cache->k and cache->v may be NULL.
+ */
+DFLASH_API int dflash_kv_reserve(const dflash_kv4_dims* dims, const dflash_kv_view* cache,
+                                 const int32_t* n_new, int32_t* start, int32_t* pos,
+                                 int32_t* slot, int32_t* new_len, void* ws, size_t ws_bytes,
+                                 dflash_stream_t stream);
+
+/*
+ * dflash_qk_norm_rope — for every row n with pos[n] >= 0 and every head:
+ *   q_out = RoPE_pos(RMSNorm_head(q) * q_norm_w), k_out likewise,
+ * in fp32 with one rounding to bf16 (rotate-half; a norm is skipped when its
+ * weight is NULL).  Rows with pos[n] < 0 are left as they were.
+ *   q, q_out: bf16 [N, Hq, D], k, k_out: bf16 [N, Hkv, D], rows q_pitch, .. elements
+ *   apart (a multiple of 8, at least heads * D: slices of a fused projection's
+ *   rows); q_norm_w, k_norm_w: bf16 [D] or NULL; pos: int32 [N].
+ *   q_out and k_out may be q and k themselves (same pitch), else must not
+ *   overlap the inputs.
+ */
+DFLASH_API int dflash_qk_norm_rope(const dflash_kv4_dims* dims, const void* q, int64_t q_pitch,
+                                   const void* k, int64_t k_pitch, const void* q_norm_w,
+                                   const void* k_norm_w, const int32_t* pos, float rope_theta,
+                                   float rms_eps, void* q_out, int64_t q_out_pitch, void* k_out,
+                                   int64_t k_out_pitch, dflash_stream_t stream);
+
+/*
+ * dflash_kv4_append — quantise row n of k (normed and rotated) and v into row
+ * slot[n] of the cache.  For 16 consecutive dims x (times 2^-exp[head]):
+ *   scale = e4m3(max |x| / 6), code = e2m1(x / scale), both to nearest, ties to
+ * even, saturating (scale 0: all codes 0).  Infinite elements are stored as
+ * the largest, NaN as 0; both set DFLASH_ST_BAD_VALUE, so the cells hold finite
+ * values only.  Rows with slot[n] < 0 are skipped; a slot past the pool sets
+ * DFLASH_ST_CAPACITY and is skipped.  Slots that are not negative must differ.
+ * seq_len is not touched (dflash_kv_reserve's new_len holds the lengths).
+ *   k, v: bf16 [N, Hkv, D], rows k_pitch, v_pitch elements apart (a multiple
+ *   of 8, at least Hkv * D); slot: int32 [N].
+ */
+DFLASH_API int dflash_kv4_append(const dflash_kv4_dims* dims, const void* k, int64_t k_pitch,
+                                 const void* v, int64_t v_pitch, const int32_t* slot,
+                                 const dflash_kv4_view* cache, void* ws, size_t ws_bytes,
+                                 dflash_stream_t stream);
+
+/*
+ * dflash_kv4_gather — rows slot[n] of the cache as bf16 k_out[n], v_out[n],
+ * [N, Hkv, D].  Every 4-bit value is a bf16 value, and appending what was
+ * gathered gives the same values again wherever the scale is a normal e4m3
+ * number (2^-6 and up) or 0: the largest code is then 6.  Rows with slot[n] < 0
+ * are left as they were; a slot past the pool sets DFLASH_ST_CAPACITY and
+ * is left too.  A slot may occur more than once.
+ */
+DFLASH_API int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slot,
+                                 const dflash_kv4_view* cache, void* k_out, void* v_out, void* ws,
+                                 size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * dflash_kv4_attention — attention of the batch's new rows over the cache that
+ * holds them already.  With L = cache->seq_len[b] (new rows included) and T =
+ * start[b + 1] - start[b], row t of sequence b and query head h:
+ *   out = softmax(q K^T * scale) V over the cache rows 0 .. m - 1 of KV head
+ *   h / (Hq/Hkv), m = L - T + t + 1 when causal != 0, else m = L
+ * (q rotated already, as dflash_qk_norm_rope leaves it).  A row that sees
+ * nothing (m <= 0) is zero.
+ *   q, out: bf16 [N, Hq, D]; start: int32 [B + 1]; scale finite.
+ * A sequence whose rows do not lie in 0..N, with T > max_tokens, or with L < 0
+ * or past the capacity sets DFLASH_ST_CAPACITY and its output is left unwritten;
+ * unmapped pages inside the length set DFLASH_ST_PAGE_MISSING and read as zeros,
+ * as do pages numbered past the pool.  Cells past the length are not used.
+ */
+DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
+                                    const int32_t* start, const dflash_kv4_view* cache,
+                                    float scale, int causal, void* out, void* ws,
+                                    size_t ws_bytes, dflash_stream_t stream);
+
 /* Copy the status word to *host_status (synchronises `stream`); if clear != 0
  * reset it to zero afterwards. */
 DFLASH_API int dflash_read_status(void* ws, uint32_t* host_status, int clear, dflash_stream_t stream);
@@ -440,7 +582,7 @@ DFLASH_API const char* dflash_status_string(int code);
  */
 DFLASH_API int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes, dflash_stream_t stream);
 
-/* Library ABI version (major * 100 + minor): 108. */
+/* Library ABI version (major * 100 + minor): 109. */
 DFLASH_API int dflash_version(void);
 
 #ifdef __cplusplus

@@ -1,0 +1,693 @@
+"""GPU parity of the serving calls over a 4-bit KV cache against the float64
+oracle, through the public binding."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+I32, BF, U8 = torch.int32, torch.bfloat16, torch.uint8
+
+
+def _dfl():
+    import block_diffusion_speculative_02_gb300 as dfl
+    return dfl
+
+
+def i32(x):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(x, np.int32))).cuda()
+
+
+def bf16(x):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(x, np.float32))).to(BF).cuda()
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def status(ws):
+    return _dfl().dflash_read_status(ws)
+
+
+def bits(*names):
+    return sum(_dfl().dflash.STATUS_BITS[n] for n in names)
+
+
+class Cache:
+    """A 4-bit cache with its float64 image: lengths, shuffled pages, random rows.
+
+    Cell bytes no row was written to hold 0xFF (NaN scales, code -6)."""
+
+    def __init__(self, rng, lens, hkv, d, page_size=16, spare=3, exps=True, extra_rows=0,
+                 contiguous=0):
+        dfl = _dfl()
+        B = len(lens)
+        self.hkv, self.d, self.page, self.lens = hkv, d, page_size, list(lens)
+        self.k_exp = rng.integers(-3, 4, hkv) if exps else np.zeros(hkv, int)
+        self.v_exp = rng.integers(-8, 2, hkv) if exps else np.zeros(hkv, int)
+        self.k = [np.zeros((n, hkv, d)) for n in lens]
+        self.v = [np.zeros((n, hkv, d)) for n in lens]
+        if contiguous:
+            self.table = None
+            slabs, rows, cap = B, contiguous, contiguous
+            slot = lambda b, i: (b, i)  # noqa: E731
+        else:
+            per = [-(-n // page_size) for n in lens]
+            width = max(-(-(n + extra_rows) // page_size) for n in lens) + 1
+            n_pages = sum(per) + B * -(-extra_rows // page_size) + spare
+            order = rng.permutation(n_pages)
+            self.table = np.full((B, width), -1)
+            at = 0
+            for b in range(B):
+                self.table[b, :per[b]] = order[at:at + per[b]]
+                at += per[b]
+            self.free = np.concatenate([order[at:], order[:at]])
+            self.count = n_pages - at
+            slabs, rows, cap = n_pages, page_size, width * page_size
+            slot = lambda b, i: (self.table[b, i // page_size], i % page_size)  # noqa: E731
+        cells = np.full((slabs, hkv, rows // 16, 18 * d), 0xFF, np.uint8)
+        for b, n in enumerate(lens):
+            kx = np.ldexp(rng.normal(size=(n, hkv, d)), self.k_exp[:, None])
+            vx = np.ldexp(rng.normal(size=(n, hkv, d)), self.v_exp[:, None])
+            kc, ks = O.quantise(kx, self.k_exp)
+            vc, vs = O.quantise(vx, self.v_exp)
+            self.k[b], self.v[b] = O.values(kc, ks, self.k_exp), O.values(vc, vs, self.v_exp)
+            for i in range(n):
+                s, r = slot(b, i)
+                for h in range(hkv):
+                    O.put_row(cells[s, h, r // 16], r % 16, kc[i, h], ks[i, h], vc[i, h], vs[i, h])
+        self.view = dfl.KV4View(
+            torch.from_numpy(cells).cuda(), i32(lens), cap,
+            None if contiguous else i32(self.table), None if contiguous else i32(self.free),
+            None if contiguous else i32([self.count]), page_size,
+            i32(self.k_exp) if exps else None, i32(self.v_exp) if exps else None)
+
+
+def check_attention(rng, cache, new, hq, causal, pad=0, scale=None, q_gain=1.0, q=None):
+    """Runs the call on fresh queries and compares every row.
+
+    The bound, element by element, with A = sum p |v| / sum p and e = scale max sum
+    |q||k| (the oracle's):
+      2^-8 |ref|     the rounding to bf16 (half a step)
+      A 2^-11 * 2    probabilities kept in 16 bits for the second product, in
+                     numerator and weight
+      A 2^-22 * 4    exponentials (2^-22 relative)
+      A e 2^-16      scores: 128 products summed in 32 bits (128 * 2^-24 of their
+                     absolute sum) and one more rounding each of scale and subtraction
+      A 2^-16        the same for the sums of the second product
+    """
+    dfl = _dfl()
+    B, d, hkv = len(new), cache.d, cache.hkv
+    n = sum(new) + pad
+    scale = 1 / np.sqrt(d) if scale is None else scale
+    dims = dfl.make_kv4_dims(B, n, max(max(new), 1), hq, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    if q is None:
+        gain = np.ldexp(q_gain, -np.repeat(cache.k_exp, hq // hkv))[:, None]
+        q = bf16(rng.normal(size=(n, hq, d)) * gain)
+    start = np.concatenate([[0], np.cumsum(new)])
+    out = torch.full((n, hq, d), -7.0, dtype=BF, device="cuda")
+    dfl.dflash_kv4_attention(dims, q, i32(start), cache.view, float(scale), causal, out, ws)
+    torch.cuda.synchronize()
+    assert status(ws) == 0
+    got, qd = f64(out), f64(q)
+    for b, T in enumerate(new):
+        lo, L = start[b], cache.lens[b]
+        seen = [min(L, L - T + t + 1) if causal else L for t in range(T)]
+        ref, avg, e = O.attention(qd[lo:lo + T], cache.k[b], cache.v[b], seen, scale)
+        tol = 2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+        err = np.abs(got[lo:lo + T] - ref)
+        assert (err <= tol).all(), (b, np.argwhere(err > tol)[:5], (err - tol).max())
+    assert (got[start[-1]:] == -7).all()                # padding rows are left
+    return out
+
+
+# ---------------------------------------------------------------------------
+# page reservation
+# ---------------------------------------------------------------------------
+def run_reserve(lens, new, table, free, count, page, n_tokens, max_tokens, limit, alias=False):
+    dfl = _dfl()
+    B = len(lens)
+    dims = dfl.make_kv4_dims(B, n_tokens, max_tokens, 1, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    seq = i32(lens)
+    view = dfl.KVView(None, None, seq, limit, None if table is None else i32(table),
+                      None if table is None else i32(free),
+                      None if table is None else i32([count]), page)
+    start, pos, slot = (torch.full((m,), -9, dtype=I32, device="cuda")
+                        for m in (B + 1, n_tokens, n_tokens))
+    new_len = seq if alias else torch.full((B,), -9, dtype=I32, device="cuda")
+    dfl.dflash_kv_reserve(dims, view, i32(new), start, pos, slot, new_len, ws)
+    torch.cuda.synchronize()
+    ref = O.reserve(lens, new, None if table is None else np.array(table), np.array(free), count,
+                    page, n_tokens, max_tokens, limit)
+    assert status(ws) == bits(*ref["status"])
+    for name, t in (("start", start), ("pos", pos), ("slot", slot), ("new_len", new_len)):
+        np.testing.assert_array_equal(t.cpu().numpy(), ref[name], err_msg=name)
+    if table is not None:
+        np.testing.assert_array_equal(view.page_table.cpu().numpy(), ref["table"])
+        assert int(view.free_count) == ref["free_count"]
+    return ref
+
+
+@pytest.mark.parametrize("B,page,new_hi,pad", [(1, 16, 1, 0), (1, 16, 900, 5), (5, 16, 40, 0),
+                                               (33, 32, 17, 9), (300, 16, 3, 2), (70, 1, 9, 0),
+                                               (40, 16, 700, 0), (1100, 16, 2, 0)])
+def test_reserve(B, page, new_hi, pad):
+    rng = np.random.default_rng(B + page)
+    lens = rng.integers(0, 200, B)
+    new = rng.integers(0, new_hi + 1, B)
+    new[0] = new_hi
+    width = int((lens + new).max()) // page + 2
+    per = -(-lens // page)
+    n_pages = int(per.sum() + (new // page + 2).sum())
+    order = rng.permutation(n_pages)
+    table, at = np.full((B, width), -1), 0
+    for b in range(B):
+        table[b, :per[b]] = order[at:at + per[b]]
+        at += per[b]
+        if rng.random() < 0.3 and per[b] < width:       # a page mapped ahead of the rows
+            table[b, min(per[b] + 1, width - 1)] = order[at]
+            at += 1
+    run_reserve(lens, new, table, np.concatenate([order[at:], order[:at]]), n_pages - at, page,
+                int(new.sum()) + pad, new_hi, width * page, alias=B == 5)
+
+
+@pytest.mark.parametrize("count", [0, 1, 2, 3, 5, 6])
+def test_reserve_short_pool(count):
+    """What fits is served in order; a sequence that lacks pages is left as it was."""
+    lens, new = [3, 0, 16, 40, 15, 8], [4, 33, 20, 8, 2, 0]
+    table = np.full((6, 5), -1)
+    table[0, 0], table[2, 0], table[3, :3], table[4, 0], table[5, 0] = 20, 21, (22, 23, 24), 25, 26
+    run_reserve(lens, new, table, np.arange(30), count, 16, 67, 64, 80)
+
+
+def test_reserve_refuses_bad_sequences():
+    """Negative counts and lengths, rows past the capacity, the array and max_tokens."""
+    lens, new = [0, -1, 70, 5, 81, 0, 10], [2, 3, 11, -4, 1, 17, 6]
+    table = np.full((7, 5), -1)
+    ref = run_reserve(lens, new, table, np.arange(40), 40, 16, 36, 16, 80)
+    assert ref["new_len"].tolist() == [2, -1, 70, 5, 81, 0, 10]
+
+
+def test_reserve_contiguous_and_again():
+    run_reserve([0, 7, 30], [4, 16, 2], None, [], 0, 0, 24, 16, 32)
+    dfl = _dfl()
+    table = np.full((2, 4), -1)
+    dims = dfl.make_kv4_dims(2, 20, 16, 1, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    view = dfl.KVView(None, None, i32([0, 3]), 64, i32(table), i32(np.arange(9)), i32([9]), 16)
+    got = []
+    for _ in range(2):                                  # the same lengths: nothing changes
+        o = [torch.zeros(m, dtype=I32, device="cuda") for m in (3, 20, 20, 2)]
+        dfl.dflash_kv_reserve(dims, view, i32([4, 16]), *o, ws)
+        got.append([x.tolist() for x in o] + [view.page_table.tolist(), int(view.free_count)])
+    assert got[0] == got[1]
+
+
+# ---------------------------------------------------------------------------
+# norms and rotation
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("n,hq,hkv,d", [(1, 4, 2, 64), (3, 5, 5, 128), (17, 32, 8, 128),
+                                        (130, 7, 1, 64), (40, 64, 8, 128)])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("place", ["own", "fused", "inplace"])
+def test_qk_norm_rope(n, hq, hkv, d, norm, place):
+    dfl = _dfl()
+    rng = np.random.default_rng(n * d + hq)
+    qkv = bf16(rng.normal(size=(n, (hq + 2 * hkv) * d)))
+    q = qkv[:, :hq * d].unflatten(1, (hq, d))
+    k = qkv[:, hq * d:(hq + hkv) * d].unflatten(1, (hkv, d))
+    if place == "own":
+        q, k = q.contiguous(), k.contiguous()
+    q0, k0, rest = f64(q), f64(k), f64(qkv[:, (hq + hkv) * d:])
+    qw, kw = (bf16(1 + 0.2 * rng.normal(size=d)) for _ in range(2)) if norm else (None, None)
+    pos = rng.integers(0, 300000, n)
+    pos[0] = 2 ** 31 - 1 if n == 17 else 0
+    pos[n // 2::7] = -1
+    if place == "inplace":
+        q_out, k_out = q, k
+    else:
+        q_out = torch.full((n, hq, d), 3.0, dtype=BF, device="cuda")
+        k_out = torch.full((n, hkv, d), 3.0, dtype=BF, device="cuda")
+    dims = dfl.make_kv4_dims(1, n, n, hq, hkv, d)
+    dfl.dflash_qk_norm_rope(dims, q, k, qw, kw, i32(pos), 1e6, 1e-6, q_out, k_out)
+    torch.cuda.synchronize()
+    for x, w, y in ((q0, qw, q_out), (k0, kw, k_out)):
+        ref = O.norm_rope(x, None if w is None else f64(w), pos, 1e6, 1e-6)
+        # half a bf16 step, and for the arithmetic in 32 bits 2^-16 of the rotated pair:
+        # (D + 8) roundings of 2^-24 in the norm, 2^-21 in the angle and its sine; the float64
+        # angle itself is off by pos 2^-53
+        pair = np.abs(ref) + np.abs(np.roll(ref, d // 2, axis=-1))
+        tol = 2.0 ** -8 * np.abs(ref) + pair * (2.0 ** -16 + np.abs(pos)[:, None, None] * 2.0 ** -52)
+        got = f64(y)
+        keep = pos < 0
+        assert (np.abs(got - ref) <= tol)[~keep].all()
+        same = x if place == "inplace" else np.full_like(x, 3.0)
+        np.testing.assert_array_equal(got[keep], same[keep])
+    np.testing.assert_array_equal(f64(qkv[:, (hq + hkv) * d:]), rest)
+
+
+# ---------------------------------------------------------------------------
+# append and gather
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("hkv,d,page,contiguous", [(2, 64, 16, 0), (8, 128, 16, 0), (3, 128, 48, 0),
+                                                   (1, 64, 0, 80)])
+@pytest.mark.parametrize("n", [1, 15, 16, 100])
+def test_append_and_gather(hkv, d, page, contiguous, n):
+    """Rows at scattered slots, whole cells in order among them: the values are the oracle's
+    exactly, other rows' bytes stay, and what is gathered goes in again."""
+    dfl = _dfl()
+    rng = np.random.default_rng(n + d + page)
+    lens = [160] if not contiguous else [80, 80]
+    cache = Cache(rng, lens, hkv, d, page or 16, spare=2, contiguous=contiguous)
+    before = cache.view.cells.cpu().numpy().copy()
+    rows = 160 if contiguous else int(cache.free.size) * page
+    slot = rng.permutation(rows)[:n]
+    if n == 100:
+        slot = np.concatenate([np.arange(32, 80), np.setdiff1d(rng.permutation(rows), np.arange(
+            32, 80), assume_unique=True)[:52]])
+        slot[[50, 99]] = -1
+    live = slot >= 0
+    scale = np.exp2(rng.integers(-12, 13, (n, hkv, 1)))          # past both ends of the scales
+    qkv = bf16(np.concatenate([rng.normal(size=(n, hkv, d)) * scale] * 3, 1))
+    qkv[:, hkv:] *= 0.5
+    k, v = qkv[:, :hkv], qkv[:, hkv:2 * hkv]
+    if n > 1:
+        k[1] = 0
+    dims = dfl.make_kv4_dims(len(lens), n, n, hkv, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    dfl.dflash_kv4_append(dims, k, v, i32(slot), cache.view, ws)
+    ko = torch.full((n, hkv, d), 5.0, dtype=BF, device="cuda")
+    vo = torch.full((n, hkv, d), 5.0, dtype=BF, device="cuda")
+    dfl.dflash_kv4_gather(dims, i32(slot), cache.view, ko, vo, ws)
+    torch.cuda.synchronize()
+    assert status(ws) == 0
+    kc, ks = O.quantise(f64(k), cache.k_exp)
+    vc, vs = O.quantise(f64(v), cache.v_exp)
+    np.testing.assert_array_equal(f64(ko)[live], O.values(kc, ks, cache.k_exp)[live])
+    np.testing.assert_array_equal(f64(vo)[live], O.values(vc, vs, cache.v_exp)[live])
+    assert (f64(ko)[~live] == 5).all() and (f64(vo)[~live] == 5).all()
+    # the bytes: the oracle's cells, up to the sign of zero codes
+    slab_rows = contiguous or page
+    for i in np.nonzero(live)[0]:
+        s, r = divmod(int(slot[i]), slab_rows)
+        for h in range(hkv):
+            O.put_row(before[s, h, r // 16], r % 16, kc[i, h], ks[i, h], vc[i, h], vs[i, h])
+    after = cache.view.cells.cpu().numpy()
+    codes = lambda x: np.stack([x & 15, x >> 4])  # noqa: E731
+    a, b = codes(after[..., :16 * d]), codes(before[..., :16 * d])
+    assert ((a == b) | ((a & 7 == 0) & (b & 7 == 0))).all()
+    np.testing.assert_array_equal(after[..., 16 * d:], before[..., 16 * d:])
+    dfl.dflash_kv4_append(dims, ko, vo, i32(slot), cache.view, ws)
+    k2, v2 = torch.zeros_like(ko), torch.zeros_like(vo)
+    dfl.dflash_kv4_gather(dims, i32(slot), cache.view, k2, v2, ws)
+    # again the same values where the scale is normal (code 8 and up) or 0.  A normal scale is
+    # within 2^-4 of max / 6, so max / scale >= 6 / (1 + 2^-4) > 5.6 has code 6, the values'
+    # maximum is 6 scale, and the same scale and codes follow.  A subnormal scale (a multiple
+    # of 2^-9) may be up to half larger than max / 6: the largest code may be 4.
+    for a, b, sc in ((k2, ko, ks), (v2, vo, vs)):
+        sure = np.repeat((sc >= 8) | (sc == 0), 16, axis=-1) & live[:, None, None]
+        assert sure.any() or n == 1
+        np.testing.assert_array_equal(f64(a)[sure], f64(b)[sure])
+
+
+def test_append_halfway_cases_and_every_scale():
+    """Each row's largest element is 6 times a scale; the others lie halfway between codes."""
+    dfl = _dfl()
+    d, rows = 64, []
+    for s in range(8, 127):                                       # normal scales
+        row = np.zeros(d)
+        for g in range(4):
+            half = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+            row[16 * g:16 * g + 8] = np.array([6.0] + half) * O.E4M3[s] * (-1) ** g
+            row[16 * g + 8] = O.E4M3[s] * 3
+        rows.append(row)
+    # and rows whose scale itself is halfway between two
+    for s in range(8, 126):
+        row = np.zeros(d)
+        row[0], row[5] = 3 * (O.E4M3[s] + O.E4M3[s + 1]), 1.0
+        rows.append(row)
+    x = np.array(rows)[:, None, :]
+    n = len(x)
+    assert (f64(bf16(x)) == x).all()                              # bf16 holds them
+    cache = Cache(np.random.default_rng(0), [n + 20], 1, d, exps=False)
+    slot = np.array([cache.table[0, i // 16] * 16 + i % 16 for i in range(n)])
+    dims = dfl.make_kv4_dims(1, n, n, 1, 1, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    ko, vo = (torch.zeros(n, 1, d, dtype=BF, device="cuda") for _ in range(2))
+    dfl.dflash_kv4_append(dims, bf16(x), bf16(-x), i32(slot), cache.view, ws)
+    dfl.dflash_kv4_gather(dims, i32(slot), cache.view, ko, vo, ws)
+    ref = O.values(*O.quantise(x, [0]), [0])
+    np.testing.assert_array_equal(f64(ko), ref)
+    np.testing.assert_array_equal(f64(vo), -ref)
+    assert status(ws) == 0
+
+
+def test_append_bad_values_and_slots():
+    dfl = _dfl()
+    d = 64
+    cache = Cache(np.random.default_rng(0), [16], 1, d, exps=False, spare=1)
+    k = np.ones((4, 1, d))
+    k[0, 0, 3], k[1, 0, 20], k[1, 0, 21] = np.nan, np.inf, -np.inf
+    dims = dfl.make_kv4_dims(1, 4, 4, 1, 1, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    base = int(cache.table[0, 0]) * 16
+    slot = i32([base, base + 1, 10 ** 6, base + 2])
+    ko, vo = (torch.full((4, 1, d), 9.0, dtype=BF, device="cuda") for _ in range(2))
+    dfl.dflash_kv4_append(dims, bf16(k), bf16(np.ones((4, 1, d))), slot, cache.view, ws)
+    assert status(ws) == bits("bad_value", "capacity")
+    dfl.dflash_kv4_gather(dims, slot, cache.view, ko, vo, ws)
+    assert status(ws) == bits("capacity")
+    got = f64(ko)[:, 0]
+    one = O.values(*O.quantise(np.ones((1, 16)), [0]), [0])[0]
+    assert got[0, 3] == 0 and (got[0, :3] == one[0]).all()
+    assert got[1, 20] == 2688 and got[1, 21] == -2688 and (got[1, 32:] == one[0]).all()
+    assert (got[2] == 9).all() and (got[3] == one[0]).all()
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 2, 128), (8, 1, 128), (3, 3, 64),
+                                      (16, 1, 128), (64, 1, 64)])
+@pytest.mark.parametrize("T", [1, 2, 5, 16])
+def test_attention_lengths(causal, hq, hkv, d, T):
+    """Lengths around the edges of cells, tiles of keys and pages; a length below T."""
+    rng = np.random.default_rng(d * T + hq)
+    lens = [T, 1, 15, 17, 64, 127, 128, 130, 257, 0]
+    cache = Cache(rng, lens, hkv, d)
+    check_attention(rng, cache, [T] * len(lens), hq, causal, pad=2)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (16, 4, 128)])
+def test_attention_ragged(causal, hq, hkv, d):
+    """Rows per sequence from none to more than one tile of query rows."""
+    rng = np.random.default_rng(hq)
+    new = [0, 70, 1, 0, 16, 33, 3, 0]
+    lens = [40, 70, 300, 0, 500, 90, 3, 12]
+    check_attention(rng, Cache(rng, lens, hkv, d), new, hq, causal, pad=3)
+
+
+@pytest.mark.parametrize("page", [32, 48, 128])
+def test_attention_larger_pages(page):
+    rng = np.random.default_rng(page)
+    check_attention(rng, Cache(rng, [1, 200, 333], 2, 128, page_size=page), [1, 4, 9], 8, True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_contiguous(causal):
+    rng = np.random.default_rng(5)
+    check_attention(rng, Cache(rng, [3, 272, 150], 2, 128, contiguous=272, exps=False),
+                    [2, 16, 1], 8, causal)
+
+
+def test_attention_many_sequences():
+    """More sequences than there are SMs, most of them short."""
+    rng = np.random.default_rng(11)
+    lens = rng.integers(1, 40, 170)
+    lens[7] = 700
+    check_attention(rng, Cache(rng, lens, 1, 64), [1] * 170, 2, True)
+
+
+@pytest.mark.parametrize("q_gain", [40.0, 1e-3])
+def test_attention_sharp_and_flat(q_gain):
+    """Scores of a few hundred (one key takes all) and of next to nothing."""
+    rng = np.random.default_rng(3)
+    check_attention(rng, Cache(rng, [700, 1, 129], 2, 128), [16, 1, 16], 8, True, q_gain=q_gain)
+
+
+def test_attention_rows_of_unlike_size():
+    """Queries of one call a factor 2^30 apart, and rows of zeros."""
+    rng = np.random.default_rng(4)
+    cache = Cache(rng, [300], 1, 128, exps=False)
+    q = rng.normal(size=(16, 4, 128)) * np.exp2(rng.integers(-15, 16, (16, 4, 1)))
+    q[3] = 0
+    check_attention(rng, cache, [16], 4, True, q=bf16(q), scale=2.0 ** -14)
+
+
+def test_attention_rising_scores():
+    """Keys ordered so that the running maximum moves again and again, and falls."""
+    rng = np.random.default_rng(6)
+    cache = Cache(rng, [2000], 1, 128, exps=False)
+    q = rng.normal(size=(16, 4, 128)) * 8
+    for order in (1, -1):
+        rank = np.argsort(order * (cache.k[0][:, 0] @ q[5, 2]))
+        kk, vv = cache.k[0][rank], cache.v[0][rank]
+        again = Cache(rng, [2000], 1, 128, exps=False)
+        dfl = _dfl()
+        dims = dfl.make_kv4_dims(1, 2000, 2000, 1, 1, 128)
+        ws = dfl.alloc_kv4_workspace(dims)
+        slot = [again.table[0, i // 16] * 16 + i % 16 for i in range(2000)]
+        dfl.dflash_kv4_append(dims, bf16(kk), bf16(vv), i32(slot), again.view, ws)
+        again.k[0], again.v[0] = kk, vv
+        check_attention(rng, again, [16], 4, False, q=bf16(q))
+
+
+def test_attention_nan_query_stays_in_its_row():
+    rng = np.random.default_rng(8)
+    cache = Cache(rng, [200], 1, 64)
+    dfl = _dfl()
+    q = bf16(rng.normal(size=(16, 4, 64)))
+    clean = check_attention(rng, cache, [16], 4, True, q=q)
+    bad = q.clone()
+    bad[5, 2, 7] = float("nan")
+    out = torch.zeros_like(q)
+    dims = dfl.make_kv4_dims(1, 16, 16, 4, 1, 64)
+    dfl.dflash_kv4_attention(dims, bad, i32([0, 16]), cache.view, 0.125, True, out,
+                             dfl.alloc_kv4_workspace(dims))
+    got, ref = f64(out), f64(clean)
+    assert np.isnan(got[5, 2]).all()
+    got[5, 2] = ref[5, 2]
+    np.testing.assert_array_equal(got, ref)
+
+
+def test_attention_bad_sequences_and_pages():
+    """Bad lengths leave the output; pages that are missing or numbered past the pool read
+    as zeros; the other sequences of the batch are right."""
+    dfl = _dfl()
+    rng = np.random.default_rng(9)
+    cache = Cache(rng, [100, 100, 100, 40, 60], 1, 64)
+    new = [2, 2, 2, 9, 2]
+    start = np.concatenate([[0], np.cumsum(new)])
+    cache.view.seq_len.copy_(i32([100, -1, 10 ** 6, 40, 60]))
+    cache.view.page_table[0, 2] = -1
+    cache.view.page_table[4, 1] = 10 ** 6
+    for b, page in ((0, 2), (4, 1)):
+        cache.k[b][16 * page:16 * page + 16] = cache.v[b][16 * page:16 * page + 16] = 0
+    dims = dfl.make_kv4_dims(5, 17, 8, 4, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    q = bf16(rng.normal(size=(17, 4, 64)))
+    out = torch.full_like(q, 2.0)
+    dfl.dflash_kv4_attention(dims, q, i32(start), cache.view, 0.125, True, out, ws)
+    assert status(ws) == bits("capacity", "page_missing")
+    got = f64(out)
+    assert (got[2:15] == 2).all()
+    for b, lo, L in ((0, 0, 100), (4, 15, 60)):
+        ref, avg, _ = O.attention(f64(q)[lo:lo + 2], cache.k[b], cache.v[b], [L - 1, L], 0.125)
+        assert (np.abs(got[lo:lo + 2] - ref) <= 2.0 ** -8 * np.abs(ref) + avg * 2.0 ** -9).all()
+    # row offsets outside the batch's rows
+    cache.view.seq_len.copy_(i32([100, 100, 100, 40, 60]))
+    for bad in ([-2, 2, 4, 6, 8, 10], [0, 2, 1, 3, 5, 30]):
+        out.fill_(2.0)
+        dfl.dflash_kv4_attention(dims, q, i32(bad), cache.view, 0.125, True, out, ws)
+        assert status(ws) & bits("capacity")
+        assert not (f64(out)[4 if bad[0] < 0 else 1] == 2).all()
+
+
+@pytest.mark.parametrize("T,causal", [(1, True), (16, False), (200, True)])
+def test_attention_repeats_its_bits(T, causal):
+    """Split work is joined in a fixed order: two runs give the same bits."""
+    dfl = _dfl()
+    rng = np.random.default_rng(T)
+    cache = Cache(rng, [1500, 700], 2, 128)
+    dims = dfl.make_kv4_dims(2, 2 * T, T, 8, 2, 128)
+    ws = dfl.alloc_kv4_workspace(dims)
+    q = bf16(rng.normal(size=(2 * T, 8, 128)))
+    outs = []
+    for _ in range(5):
+        out = torch.zeros_like(q)
+        dfl.dflash_kv4_attention(dims, q, i32([0, T, 2 * T]), cache.view, 0.1, causal, out, ws)
+        outs.append(out)
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+def test_attention_far_pool():
+    """Cells past 2^31 and 2^32 bytes of the pool, and slots written and read there."""
+    dfl = _dfl()
+    rng = np.random.default_rng(12)
+    hkv, d = 8, 128
+    small = Cache(rng, [50, 300], hkv, d)
+    per = 18 * d * hkv
+    n_pages = 2 ** 32 // per + 4096
+    cells = torch.zeros(n_pages, hkv, 1, 18 * d, dtype=U8, device="cuda")
+    far = small.table.copy()
+    used = sorted(far[far >= 0])
+    for i, page in enumerate(used):
+        to = n_pages - 1 - 7 * i if i % 2 else 2 ** 31 // per + 3 * i
+        cells[to] = small.view.cells[int(page)]
+        far[small.table == page] = to
+    small.view.cells = cells
+    small.view.page_table = i32(far)
+    small.view.free_list = torch.zeros(n_pages, dtype=I32, device="cuda")
+    check_attention(rng, small, [3, 16], 32, True)
+    n = 20
+    dims = dfl.make_kv4_dims(2, n, n, hkv, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    slot = i32([int(far[1, 18 - i // 16]) * 16 + i % 16 for i in range(n)])
+    ko, vo = (torch.zeros(n, hkv, d, dtype=BF, device="cuda") for _ in range(2))
+    dfl.dflash_kv4_gather(dims, slot, small.view, ko, vo, ws)
+    for i in range(min(n, 12)):
+        np.testing.assert_array_equal(f64(ko)[i], small.k[1][18 * 16 + i])
+    x = bf16(rng.normal(size=(n, hkv, d)))
+    dfl.dflash_kv4_append(dims, x, x, slot, small.view, ws)
+    dfl.dflash_kv4_gather(dims, slot, small.view, ko, vo, ws)
+    ref = O.values(*O.quantise(f64(x), small.k_exp), small.k_exp)
+    np.testing.assert_array_equal(f64(ko), ref)
+
+
+# ---------------------------------------------------------------------------
+# the calls together
+# ---------------------------------------------------------------------------
+def test_serving_steps_end_to_end():
+    """Prompts of uneven lengths, a token each, blocks with a crop, a sequence that joins: each
+    step reserves, norms and rotates, appends, attends and (after a block) crops, on one stream
+    that is not the default one; every output against the oracle's own cache."""
+    dfl = _dfl()
+    rng = np.random.default_rng(21)
+    B, hq, hkv, d, theta, eps = 4, 8, 2, 128, 1e6, 1e-6
+    n_pages, width = 60, 20
+    view = dfl.KV4View(dfl.alloc_kv4_cells(n_pages, hkv, 16, d), i32([0] * B), width * 16,
+                       i32(np.full((B, width), -1)), i32(rng.permutation(n_pages)), i32([n_pages]),
+                       16, i32([1, -1]), i32([-2, 0]))
+    k_exp, v_exp = np.array([1, -1]), np.array([-2, 0])
+    K, V = [np.zeros((0, hkv, d))] * B, [np.zeros((0, hkv, d))] * B
+    qw, kw = bf16(1 + 0.1 * rng.normal(size=d)), bf16(1 + 0.1 * rng.normal(size=d))
+    side = torch.cuda.Stream()
+    steps = [([37, 100, 0, 16], True, None), ([1, 1, 1, 1], True, None),
+             ([16, 16, 16, 16], True, [3, 16, 0, 9]), ([16, 16, 0, 16], False, [0, 0, 0, 0]),
+             ([1, 0, 60, 1], True, None)]
+    for new, causal, keep in steps:
+        n, pad = sum(new), 3
+        dims = dfl.make_kv4_dims(B, n + pad, max(new), hq, hkv, d)
+        ws = dfl.alloc_kv4_workspace(dims)
+        qkv = bf16(rng.normal(size=(n + pad, (hq + 2 * hkv) * d)))
+        q = qkv[:, :hq * d].unflatten(1, (hq, d))
+        k = qkv[:, hq * d:(hq + hkv) * d].unflatten(1, (hkv, d))
+        v = qkv[:, (hq + hkv) * d:].unflatten(1, (hkv, d))
+        start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda")
+                            for m in (B + 1, n + pad, n + pad))
+        q_out = torch.zeros(n + pad, hq, d, dtype=BF, device="cuda")
+        out = torch.zeros_like(q_out)
+        n_new, before = i32(new), view.seq_len.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        dfl.dflash_kv_reserve(dims, view, n_new, start, pos, slot, view.seq_len, ws, stream=side)
+        dfl.dflash_qk_norm_rope(dims, q, k, qw, kw, pos, theta, eps, q_out, k, stream=side)
+        dfl.dflash_kv4_append(dims, k, v, slot, view, ws, stream=side)
+        dfl.dflash_kv4_attention(dims, q_out, start, view, d ** -0.5, causal, out, ws, stream=side)
+        kept = None
+        if keep is not None:
+            kept = before + i32(keep)
+            side.wait_stream(torch.cuda.current_stream())
+            dfl.dflash_kv_crop([view.pages()], kept, B, ws, stream=side)
+        side.synchronize()
+        assert status(ws) == 0
+        kd, vd, qd, got, at = f64(k), f64(v), f64(q_out), f64(out), 0
+        for b, T in enumerate(new):
+            rows = slice(at, at + T)
+            K[b] = np.concatenate([K[b], O.values(*O.quantise(kd[rows], k_exp), k_exp)])
+            V[b] = np.concatenate([V[b], O.values(*O.quantise(vd[rows], v_exp), v_exp)])
+            L = len(K[b])
+            seen = [L - T + t + 1 if causal else L for t in range(T)]
+            ref, avg, e = O.attention(qd[rows], K[b], V[b], seen, d ** -0.5)
+            tol = 2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+            assert (np.abs(got[rows] - ref) <= tol).all(), (new, b)
+            if keep is not None:
+                K[b], V[b] = K[b][:L - T + keep[b]], V[b][:L - T + keep[b]]
+            at += T
+        assert view.seq_len.tolist() == [len(x) for x in K]
+    held = sum(-(-len(x) // 16) for x in K)
+    assert int(view.free_count) == n_pages - held
+
+
+def test_captured_step_replays_with_other_lengths():
+    """A decode step captured once and replayed: lengths, pages and rows are read on the
+    device each time; two graphs that share a workspace, replayed in turn."""
+    dfl = _dfl()
+    rng = np.random.default_rng(22)
+    B, hq, hkv, d, pad = 3, 4, 1, 64, 4
+    view = dfl.KV4View(dfl.alloc_kv4_cells(64, hkv, 16, d), i32([0] * B), 20 * 16,
+                       i32(np.full((B, 20), -1)), i32(np.arange(64)), i32([64]), 16)
+    n = 3 * 16 + pad
+    dims = dfl.make_kv4_dims(B, n, 16, hq, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    n_new = i32([1] * B)
+    start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda") for m in (B + 1, n, n))
+    q, k, v = (torch.zeros(n, h, d, dtype=BF, device="cuda") for h in (hq, hkv, hkv))
+    outs = [torch.zeros_like(q) for _ in range(2)]
+
+    def step(out, causal):
+        dfl.dflash_kv_reserve(dims, view, n_new, start, pos, slot, view.seq_len, ws)
+        dfl.dflash_kv4_append(dims, k, v, slot, view, ws)
+        dfl.dflash_kv4_attention(dims, q, start, view, 0.125, causal, out, ws)
+
+    graphs = []
+    for out, causal in zip(outs, (True, False)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(out, causal)
+        graphs.append(g)
+    assert view.seq_len.tolist() == [0] * B                       # capture runs nothing
+    K, V = [np.zeros((0, hkv, d))] * B, [np.zeros((0, hkv, d))] * B
+    for i, new in enumerate([[16, 3, 0], [1, 1, 1], [16, 16, 16], [0, 5, 1], [1, 1, 1]]):
+        m = sum(new)
+        n_new.copy_(i32(new))
+        for t in (q, k, v):
+            t.copy_(bf16(rng.normal(size=t.shape)))
+        outs[i % 2].fill_(4.0)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert status(ws) == 0
+        at = 0
+        for b, T in enumerate(new):
+            rows = slice(at, at + T)
+            K[b] = np.concatenate([K[b], O.values(*O.quantise(f64(k)[rows], [0]), [0])])
+            V[b] = np.concatenate([V[b], O.values(*O.quantise(f64(v)[rows], [0]), [0])])
+            L = len(K[b])
+            seen = [L - T + t + 1 if i % 2 == 0 else L for t in range(T)]
+            ref, avg, e = O.attention(f64(q)[rows], K[b], V[b], seen, 0.125)
+            tol = 2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+            assert (np.abs(f64(outs[i % 2])[rows] - ref) <= tol).all(), (i, b)
+            at += T
+        assert (f64(outs[i % 2])[m:] == 4).all()
+
+
+def test_refuses_wrong_tensors():
+    dfl = _dfl()
+    rng = np.random.default_rng(1)
+    cache = Cache(rng, [20], 1, 64)
+    dims = dfl.make_kv4_dims(1, 2, 2, 2, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    q = torch.zeros(2, 2, 64, dtype=BF, device="cuda")
+    call = lambda q, out, start, w=ws: dfl.dflash_kv4_attention(  # noqa: E731
+        dims, q, start, cache.view, 1.0, True, out, w)
+    s = i32([0, 2])
+    for bad in (q.float(), q.cpu(), q[:1], q.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            call(bad, q, s)
+        with pytest.raises(ValueError):
+            call(q, bad, s)
+    with pytest.raises(ValueError):
+        call(q, q, s[:1])
+    with pytest.raises(dfl.DFlashError):
+        call(q, torch.zeros_like(q), s, ws[:128])
+    with pytest.raises(ValueError):
+        dfl.dflash_kv4_append(dims, q, q, s[:2], cache.view, ws)     # two heads, one expected
+    with pytest.raises(ValueError):
+        cache.view.cells = cache.view.cells[:1]
+        call(q, torch.zeros_like(q), s)

@@ -87,3 +87,66 @@ def test_fault_injection_returns_before_any_check(monkeypatch):
     assert lib.dflash_kv_crop(None, 0, None, 0, None, 0, None) == E_ARG
     monkeypatch.delenv("DFLASH_FAULT_INJECT")
     assert lib.dflash_selftest_wait(1, None, 0, None) == -4                 # no workspace
+
+
+def test_kv4_calls_reject_bad_arguments_before_launching():
+    """Every case fails a host check: the pointers are never dereferenced."""
+    dflash, lib = _lib()
+    p = 0x1000
+
+    def dims(**kw):
+        a = dict(batch=2, n_tokens=8, max_tokens=4, n_q_heads=8, n_kv_heads=2, head_dim=128)
+        a.update(kw)
+        return dflash.KV4Dims(**a)
+
+    def view(**kw):
+        a = dict(k=p, v=None, seq_len=p, page_table=p, free_list=p, free_count=p, capacity=64,
+                 page_size=16, max_pages=4, n_pages=9)
+        a.update(kw)
+        return dflash.KV4ViewC(dflash.KVViewC(**a), None, None)
+
+    def attention(d=None, v=None, q=p, start=p, scale=1.0, out=p, ws=p, n=1 << 40):
+        return lib.dflash_kv4_attention(d or dims(), q, start, v or view(), scale, 1, out, ws, n,
+                                        None)
+
+    def append(d=None, v=None, k=p, pitch=256, ws=p):
+        return lib.dflash_kv4_append(d or dims(), k, pitch, p, 256, p, v or view(), ws, 1 << 40,
+                                     None)
+
+    def norm(d=None, q=p, pitch=1024, theta=1e6, eps=1e-6, out=p):
+        return lib.dflash_qk_norm_rope(d or dims(), q, pitch, p, 256, None, None, p, theta, eps,
+                                       out, 1024, p, 256, None)
+
+    def reserve(d=None, v=None, n_new=p, ws=p):
+        return lib.dflash_kv_reserve(d or dims(), (v or view()).kv, n_new, p, p, p, p, ws, 1 << 40,
+                                     None)
+
+    for f in (attention, append, norm, reserve):
+        for bad in (dict(batch=0), dict(n_tokens=0), dict(max_tokens=0), dict(n_kv_heads=0)):
+            assert f(dims(**bad)) == E_ARG, (f, bad)
+        for bad in (dict(head_dim=96), dict(n_q_heads=9), dict(n_q_heads=1), dict(batch=4097),
+                    dict(n_q_heads=130, n_kv_heads=2)):
+            assert f(dims(**bad)) == E_UNSUPPORTED, (f, bad)
+    for f in (attention, append):
+        assert f(v=view(k=None)) == E_ARG
+        assert f(v=view(k=p + 8)) == E_ALIGN
+        assert f(v=view(page_size=24)) == E_UNSUPPORTED
+        assert f(v=view(page_size=0)) == E_ARG
+        assert f(v=view(n_pages=1 << 28)) == E_UNSUPPORTED            # rows past int32
+        assert f(v=view(page_table=None, capacity=100)) == E_UNSUPPORTED
+        assert f(v=view(page_table=None, capacity=1 << 30)) == E_UNSUPPORTED
+    assert attention(q=None) == attention(out=None) == attention(start=None) == E_ARG
+    assert attention(scale=float("nan")) == attention(scale=float("inf")) == E_ARG
+    assert attention(q=p + 2) == attention(out=p + 2) == E_ALIGN
+    assert attention(v=view(seq_len=None)) == E_ARG
+    assert append(k=None) == append(pitch=248) == E_ARG
+    assert append(pitch=260) == append(k=p + 2) == E_ALIGN
+    assert append(ws=None) == -4
+    assert norm(q=None) == norm(out=None) == norm(pitch=1016) == E_ARG
+    assert norm(theta=0.5) == norm(theta=float("nan")) == norm(eps=-1.0) == E_ARG
+    assert norm(pitch=1028) == norm(q=p + 8) == E_ALIGN
+    assert reserve(n_new=None) == reserve(v=view(seq_len=None)) == E_ARG
+    assert reserve(v=view(free_list=None)) == reserve(v=view(page_size=0)) == E_ARG
+    assert reserve(v=view(max_pages=1 << 28)) == E_UNSUPPORTED
+    bad = dims(head_dim=32)
+    assert lib.dflash_kv4_workspace_bytes(ctypes.byref(bad)) == 0
