@@ -83,16 +83,24 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   return r;
 }
 
+// The two e2m1 codes of byte B of a word as f16x2 (exact).
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b%2;}"
+      : "=r"(r)
+      : "r"(w), "n"(B));
+  return r;
+}
+
 // The eight e2m1 codes of a word as four f16x2 (exact).
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&o)[4]) {
-  asm("{.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
+  o[0] = e2m1x2_to_f16x2<0>(w);
+  o[1] = e2m1x2_to_f16x2<1>(w);
+  o[2] = e2m1x2_to_f16x2<2>(w);
+  o[3] = e2m1x2_to_f16x2<3>(w);
 }
 
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {

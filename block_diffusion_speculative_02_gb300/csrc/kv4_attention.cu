@@ -7,9 +7,32 @@
 //   out[t, h] = softmax(q[t, h] K^T scale) V over the rows below
 //   m = L - T + t + 1 (causal) or L.
 //
-// One CTA per (sequence, KV head, 16 query rows); keys come in tiles of 32, are
-// expanded to fp32 in shared memory, and the running maximum and sum of the softmax
-// are kept in fp32.
+// Work.  A unit is one KV head of one sequence with a tile of up to NQ query rows
+// (its G query heads times some of its T rows); its keys come in tiles of 128.
+// The tiles of all units, in order, are cut into one equal run per CTA (one CTA
+// per SM), whatever the lengths are; the plan is made on the device from the
+// lengths.  A unit that lies in one CTA is written out by it; the pieces of a cut
+// one go to the workspace as (O, max, sum) and a second kernel joins them in order,
+// so results do not depend on timing.
+//
+// Products.  Both run on the tensor cores with the keys or dims as the 128 rows
+// and the query rows as the columns, so that few query rows cost little:
+//   S^T [128 keys x NQ]  = K [128 x D] Q^T         A = K  from TMEM, B = Q  (shared)
+//   O^T [D x NQ]        += V^T [D x 128] P^T       A = V^T from TMEM, B = P (shared)
+// The 4-bit values never pass through shared memory again after they came: each
+// thread of one warpgroup expands its key's row of K, each of another its dim's
+// row of V^T (the cell keeps V's 16 rows side by side for that), to fp16 (exact:
+// 6 significant bits) straight into TMEM.  With them in shared memory its traffic,
+// not DRAM, would bound the kernel: 128 KB written and read a tile of 18 KB.
+// Q is scaled by a power of two to [1, 2) per row and kept in fp16 (11 bits: exact
+// for bf16 values within 2^-7 of the row's largest, 2^-25 of it for smaller ones);
+// P in fp16 (2^-12 of its value), O, the maximum and the sum in fp32.
+// Softmax: a thread owns a key and walks the query columns.  The running maximum m
+// of a column only moves when a tile passes it by 2^8, which one vote per tile
+// finds out; until then exp2(x - m) needs no reduction over keys at all, and the
+// column sums stay in registers until the unit ends.
+#include <cuda_fp16.h>
+
 #include <cmath>
 
 #include "kv4.cuh"
@@ -17,149 +40,931 @@
 namespace dflash {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 16;
-constexpr int kTile = 32;
+constexpr int kTile = 128;              // keys
+constexpr int kGran = kTile / kCellRows;
+// P = 2^(x - m + kLift): 2^7 at the maximum, so that fp16 keeps probabilities down to 2^-31
+// of it, and below 2^15 until the maximum moves.
+constexpr float kLift = 7.0f;
+constexpr float kMoveLog2 = 8.0f;       // a column passes its maximum by so much before it moves
+constexpr float kNoMax = -1.0e30f;      // running maximum of a column that has seen nothing
+
+template <int D, int NQ>
+struct Cfg {
+  static constexpr int kCell = Cell<D>::kBytes;
+  static constexpr int kStage = kGran * kCell;
+  static constexpr int kSoftWgs = NQ >= 32 ? 2 : 1;
+  static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
+  static constexpr int kVWarps = D / 32;               // warps that hold rows of V^T
+  static constexpr int kThreads = 32 * (8 + 4 * kSoftWgs + 2);
+  // TMEM columns
+  static constexpr int kKCols = D / 2, kVCols = kTile / 2;
+  static constexpr int kSBufs = NQ <= 64 ? 2 : 1;
+  static constexpr int kV0 = 2 * kKCols, kS0 = kV0 + 2 * kVCols, kO0 = kS0 + kSBufs * NQ;
+  static_assert(kO0 + NQ <= 512, "TMEM columns");
+  // shared memory
+  static constexpr int kPBytes = (NQ + 63) / 64 * kTile * 128;
+  static constexpr int kQBytes = NQ * D * 2;
+  static constexpr int kFixed = 2 * kPBytes + 2 * kQBytes;
+  static constexpr int kTables = 12 * 1024;
+  static constexpr int kFit = (226 * 1024 - kFixed - kTables) / kStage;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kSmem = 1024 + kFixed + kTables + kStages * kStage;
+  static_assert(kStages >= 3, "shared memory");
+};
 
 struct Kv4AttnParams {
   Kv4Store s;
   int batch, n_tokens, max_tokens, n_q_heads, group, causal;
+  int tile_rows;             // rows of a sequence in one unit
   int paged, page_size, max_pages, limit;
   const int32_t* seq_len;
   const int32_t* start;
   const int32_t* page_table;
   const uint16_t* q;
   uint16_t* out;
-  float scale;
+  float scale_log2;
   uint32_t* status;
+  int* meta;                 // [CTAs][8]: the unit that starts in a CTA and ends in a later one
+  float* part_ml;            // [2 CTAs][NQ][2]
+  float* part_o;             // [2 CTAs][NQ][D]
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_attention_kernel(const Kv4AttnParams p) {
-  __shared__ float ks[kTile][D + 1], vs[kTile][D], qs[kRows][D], ps[kRows][kTile];
-  __shared__ float row_m[kRows], row_l[kRows], row_f[kRows];
+// ----------------------------------------------------------------------------
+// plan: which tiles this CTA takes
+// ----------------------------------------------------------------------------
+struct Seq {
+  int lo, T, len, n_qt;      // first row, rows, length, units per head (0: nothing to do)
+};
+
+__device__ __forceinline__ Seq load_seq(const Kv4AttnParams& p, int b, bool* bad = nullptr) {
+  Seq s = {0, 0, 0, 0};
+  const int lo = p.start[b], hi = p.start[b + 1], len = p.seq_len[b];
+  if (lo < 0 || hi < lo || hi > p.n_tokens || hi - lo > p.max_tokens || len < 0 ||
+      len > p.limit) {
+    if (bad) *bad = true;
+    return s;
+  }
+  s.lo = lo;
+  s.T = hi - lo;
+  s.len = len;
+  s.n_qt = (s.T + p.tile_rows - 1) / p.tile_rows;
+  return s;
+}
+
+// Keys that some row of unit qt sees, and its tiles (at least one: its rows are written).
+__device__ __forceinline__ int unit_end(const Kv4AttnParams& p, const Seq& s, int qt) {
+  if (!p.causal) return s.len;
+  return max(0, min(s.len, s.len - s.T + min(s.T, (qt + 1) * p.tile_rows)));
+}
+__device__ __forceinline__ int unit_tiles(int end) { return max(1, (end + kTile - 1) / kTile); }
+
+__device__ __forceinline__ long long seq_tiles(const Kv4AttnParams& p, const Seq& s) {
+  long long n = 0;
+  if (!p.causal) {
+    n = static_cast<long long>(s.n_qt) * unit_tiles(s.len);
+  } else {
+    for (int i = 0; i < s.n_qt; ++i) n += unit_tiles(unit_end(p, s, i));
+  }
+  return n * p.s.n_kv_heads;
+}
+
+struct Start {
+  long long left;            // tiles of this CTA
+  int b, qt, h, tile;        // the first of them
+  int c_last;                // CTA that ends the unit which this one starts and does not end
+};
+
+// One segment: consecutive tiles of one unit.
+struct Seg {
+  int b, h, t0, lo, T, len, end, tile, n, nt;
+};
+
+struct Walk {
+  long long left;
+  int b, qt, h, tile, end, nt;
+  Seq s;
+  __device__ __forceinline__ Walk(const Kv4AttnParams& p, const Start& st)
+      : left(st.left), b(st.b), qt(st.qt), h(st.h), tile(st.tile) {
+    if (left > 0) {
+      s = load_seq(p, b);
+      end = unit_end(p, s, qt);
+      nt = unit_tiles(end);
+    }
+  }
+  __device__ __forceinline__ bool next(const Kv4AttnParams& p, Seg* g) {
+    if (left <= 0) return false;
+    if (tile == nt) {        // the unit after the last one
+      tile = 0;
+      if (++h == p.s.n_kv_heads) {
+        h = 0;
+        ++qt;
+        while (qt >= s.n_qt) {
+          qt = 0;
+          if (++b >= p.batch) return false;
+          s = load_seq(p, b);
+        }
+        end = unit_end(p, s, qt);
+        nt = unit_tiles(end);
+      }
+    }
+    g->b = b;
+    g->h = h;
+    g->t0 = qt * p.tile_rows;
+    g->lo = s.lo;
+    g->T = s.T;
+    g->len = s.len;
+    g->end = end;
+    g->tile = tile;
+    g->nt = nt;
+    g->n = static_cast<int>(min(left, static_cast<long long>(nt - tile)));
+    tile += g->n;
+    left -= g->n;
+    return true;
+  }
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// By one warp.  CTA c of n takes tiles [W c / n, W (c + 1) / n) of the W in all.
+__device__ void make_start(const Kv4AttnParams& p, Start* out) {
+  const int lane = lane_id();
+  long long all = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < p.batch; b0 += 32)
+    if (b0 + lane < p.batch) all += seq_tiles(p, load_seq(p, b0 + lane, &bad));
+  if (bad && blockIdx.x == 0) set_status(p.status, DFLASH_ST_CAPACITY);
+  const long long W = warp_sum(all);
+  const long long n = min(static_cast<long long>(gridDim.x), W), c = blockIdx.x;
+  Start st = {};
+  long long first = 0;
+  if (c < n) {
+    first = W * c / n;
+    st.left = W * (c + 1) / n - first;
+  }
+  long long unit0 = 0;       // first tile of the unit that this CTA leaves unfinished
+  if (st.left > 0) {
+    long long before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const long long mine =
+          b0 + lane < p.batch ? seq_tiles(p, load_seq(p, b0 + lane)) : 0;
+      long long inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > first);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        st.b = b0 + l;
+        before += __shfl_sync(0xffffffffu, inc - mine, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    Seq s = load_seq(p, st.b);
+    long long rem = first - before;
+    int nt = unit_tiles(unit_end(p, s, 0));
+    while (rem >= static_cast<long long>(nt) * p.s.n_kv_heads) {
+      rem -= static_cast<long long>(nt) * p.s.n_kv_heads;
+      nt = unit_tiles(unit_end(p, s, ++st.qt));
+    }
+    st.h = static_cast<int>(rem / nt);
+    st.tile = static_cast<int>(rem - static_cast<long long>(st.h) * nt);
+  }
+  // the segments once over, for the unit that is left unfinished
+  st.c_last = -1;
+  Seg g = {};
+  Walk w(p, st);
+  int meta[4] = {0, 0, 0, 0};
+  long long at = first;
+  while (w.next(p, &g)) {
+    if (g.tile == 0 && g.n < g.nt) {
+      unit0 = at;
+      st.c_last = static_cast<int>(((unit0 + g.nt) * n - 1) / W);
+      meta[0] = g.lo + g.t0;
+      meta[1] = min(p.tile_rows, g.T - g.t0) * p.group;
+      meta[2] = g.h;
+    }
+    at += g.n;
+  }
+  if (lane == 0) {
+    *out = st;
+    int* m = p.meta + 8 * blockIdx.x;
+    m[0] = st.c_last;
+    m[1] = meta[0];
+    m[2] = meta[1];
+    m[3] = meta[2];
+  }
+}
+
+// ----------------------------------------------------------------------------
+// small device pieces
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Named barrier of n threads that also ORs a flag over them.
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %1, 0;\n\t"
+      "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, issued by one thread.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f16: A = B = fp16, D = fp32; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// A wait of a role that goes on regardless: once one gave up, the rest are skipped, so
+// every role still runs its loops to their end (named barriers included).
+struct Waiter {
+  volatile int* abort_flag;
+  uint32_t* status;
+  bool dead;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !mbar_wait(bar, parity, abort_flag, status);
+    __syncwarp();
+  }
+};
+
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+}
+
+// ----------------------------------------------------------------------------
+// the kernel
+// ----------------------------------------------------------------------------
+template <int D, int NQ>
+__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
+    kv4_attention_kernel(const Kv4AttnParams p) {
+  using C = Cfg<D, NQ>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint8_t* pbuf = smem;
+  uint8_t* qbuf = pbuf + 2 * C::kPBytes;
+  uint8_t* stages = qbuf + 2 * C::kQBytes;
+  uint8_t* tables = stages + C::kStages * C::kStage;
+  float* col_sc = reinterpret_cast<float*>(tables);        // [2][NQ] log2 units per score
+  int* col_vis = reinterpret_cast<int*>(col_sc + 2 * NQ);  // [2][NQ] keys a column sees
+  float* col_nm = reinterpret_cast<float*>(col_vis + 2 * NQ);  // [NQ] kLift - running maximum
+  float* col_f = col_nm + NQ;                              // [NQ] rescale factor, then 1 / sum
+  float* red = col_f + NQ;                                 // [4][NQ]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(red + 4 * NQ);
+  uint64_t* full = bars;
+  uint64_t* empty = full + C::kStages;
+  uint64_t* kd_full = empty + C::kStages;  // [2] K tile in TMEM (and Q staged)
+  uint64_t* kd_empty = kd_full + 2;        // [2] S product done
+  uint64_t* vd_full = kd_empty + 2;        // [2] V^T tile in TMEM
+  uint64_t* s_full = vd_full + 2;          // [kSBufs] S in TMEM
+  uint64_t* s_empty = s_full + 2;          // [kSBufs] S read
+  uint64_t* p_full = s_empty + 2;          // [2] P in shared memory
+  uint64_t* pv_done = p_full + 2;          // [2] P V product done
+  uint64_t* q_empty = pv_done + 2;         // [2] column tables of a segment read
+  uint64_t* o_empty = q_empty + 2;         // O of a segment read
+  uint64_t* mdrain = o_empty + 1;
+  Start* start = reinterpret_cast<Start*>(mdrain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducer = 8 + 4 * C::kSoftWgs, kMma = kProducer + 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 4 + C::kVWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&kd_full[i], 4);
+      mbar_init(&kd_empty[i], 1);
+      mbar_init(&vd_full[i], C::kVWarps);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4 * C::kSoftWgs);
+      mbar_init(&p_full[i], 4 * C::kSoftWgs);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&q_empty[i], 4 * C::kSoftWgs);
+    }
+    mbar_init(o_empty, 4 * C::kSoftWgs);
+    mbar_init(mdrain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  if (warp == kProducer) make_start(p, start);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+  const int G = p.group;
+  Walk walk(p, *start);
+  Seg g;
+  Waiter wait{abort_flag, p.status, false};
+
+  if (warp == kProducer) {
+    // ---------------- cells of a tile, one bulk copy each ----------------
+    // (a cache that several units of a sequence read stays in L2)
+    const uint64_t pol =
+        p.max_tokens > p.tile_rows ? l2_policy_evict_normal() : l2_policy_evict_first();
+    int j = 0;
+    bool go = true;
+    while (go && walk.next(p, &g)) {
+      int slab4 = -1;                               // lane: page of cell `lane` of four tiles
+      for (int i = 0; i < g.n; ++i, ++j) {
+        const int st = j % C::kStages;
+        if ((i & 3) == 0) {
+          const int key = (g.tile + i) * kTile + lane * kCellRows;
+          slab4 = g.b;
+          if (p.paged && key < g.end) {
+            slab4 = p.page_table[static_cast<size_t>(g.b) * p.max_pages + key / p.page_size];
+            if (slab4 >= p.s.n_slabs) slab4 = -1;
+          }
+        }
+        const int slab = __shfl_sync(0xffffffffu, slab4, (i & 3) * kGran + (lane & (kGran - 1)));
+        const int key = (g.tile + i) * kTile + lane * kCellRows;
+        const bool use = lane < kGran && key < g.end;
+        const uint32_t have = __ballot_sync(0xffffffffu, use && slab >= 0);
+        const uint32_t miss = __ballot_sync(0xffffffffu, use && slab < 0);
+        if (!mbar_wait(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status)) go = false;
+        if (!__all_sync(0xffffffffu, go)) {
+          go = false;
+          break;
+        }
+        uint8_t* dst = stages + st * C::kStage;
+        if (miss) {                                 // pages that are missing read as zeros
+          if (lane == 0) set_status(p.status, DFLASH_ST_PAGE_MISSING);
+          for (int c = 0; c < kGran; ++c)
+            if (miss >> c & 1)
+              for (int o = lane * 16; o < C::kCell; o += 512)
+                *reinterpret_cast<uint4*>(dst + c * C::kCell + o) = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(have) * C::kCell);
+        __syncwarp();
+        if (have >> lane & 1) {
+          const int row = p.paged ? key % p.page_size : key;
+          bulk_load(dst + lane * C::kCell, p.s.cells + cell_index(p.s, slab, g.h, row) * C::kCell,
+                    C::kCell, &full[st], pol);
+        }
+      }
+    }
+    // no copy may still be landing when the CTA exits
+    for (int st = 0; st < C::kStages && st < j; ++st) {
+      const int last = st + (j - 1 - st) / C::kStages * C::kStages;
+      mbar_wait_drain(&full[st], (last / C::kStages) & 1, p.status);
+    }
+  } else if (warp == kMma) {
+    // ---------------- the products ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = umma_idesc_f16(128, NQ, false);
+      constexpr uint32_t idesc_o = umma_idesc_f16(128, NQ, true);
+      const uint32_t q_addr = smem_u32(qbuf), p_addr = smem_u32(pbuf);
+      auto issue_pv = [&](int j, bool first, int seg) -> bool {
+        if (!mbar_wait(&p_full[j & 1], (j >> 1) & 1, abort_flag, p.status) ||
+            !mbar_wait(&vd_full[j & 1], (j >> 1) & 1, abort_flag, p.status))
+          return false;
+        if (first && seg > 0 && !mbar_wait(o_empty, (seg - 1) & 1, abort_flag, p.status))
+          return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks)
+          umma_f16_ts(tmem + C::kO0, tmem + C::kV0 + (j & 1) * C::kVCols + ks * 8,
+                      umma_sdesc_sw128_mn(p_addr + (j & 1) * C::kPBytes + ks * 2048, kTile * 128,
+                                          1024),
+                      idesc_o, !first || ks > 0);
+        umma_commit(&pv_done[j & 1]);
+        return true;
+      };
+      int j = 0, seg = 0, last_seg = 0;
+      bool ok = true, last_first = false;
+      while (ok && walk.next(p, &g)) {
+        for (int i = 0; ok && i < g.n; ++i, ++j) {
+          const int sb = j % C::kSBufs;
+          ok = mbar_wait(&kd_full[j & 1], (j >> 1) & 1, abort_flag, p.status);
+          if (ok && j >= C::kSBufs)
+            ok = mbar_wait(&s_empty[sb], (j / C::kSBufs - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_f16_ts(tmem + C::kS0 + sb * NQ, tmem + (j & 1) * C::kKCols + ks * 8,
+                        umma_sdesc_sw128(q_addr + (seg & 1) * C::kQBytes + (ks >> 2) * NQ * 128 +
+                                         (ks & 3) * 32),
+                        idesc_s, ks > 0);
+          umma_commit(&s_full[sb]);
+          umma_commit(&kd_empty[j & 1]);
+          if (j > 0) ok = issue_pv(j - 1, last_first, last_seg);
+          last_first = i == 0;
+          last_seg = seg;
+        }
+        ++seg;
+      }
+      if (ok && j > 0) issue_pv(j - 1, last_first, last_seg);
+      umma_commit(mdrain);
+      mbar_wait_drain(mdrain, 0, p.status);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------- K to fp16: a thread expands its key's row ----------------
+    const int r = threadIdx.x;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    int j = 0, seg = 0;
+    for (; walk.next(p, &g); ++seg) {
+      const int par = seg & 1;
+      if (seg >= 2) wait(&q_empty[par], ((seg >> 1) - 1) & 1);
+      {  // the unit's query rows, D / 8 lanes a row
+        constexpr int kPer = D / 8;
+        const int rows = min(p.tile_rows, g.T - g.t0) * G;
+        uint8_t* qs = qbuf + par * C::kQBytes;
+        const float kx = p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h));
+#pragma unroll 2
+        for (int it = r; it < NQ * kPer; it += 128) {
+          const int q = it / kPer, pc = it % kPer, t = q / G;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (q < rows)
+            x = *reinterpret_cast<const uint4*>(
+                p.q + (static_cast<size_t>(g.lo + g.t0 + t) * p.n_q_heads + g.h * G + q - t * G) *
+                          D +
+                8 * pc);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m = max(m, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+#pragma unroll
+          for (int o = kPer / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const int ex = max(-126, min(126, 127 - static_cast<int>(m >> 7)));
+          const float f = pow2(ex);
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
+                            __uint_as_float(w[e] & 0xFFFF0000u) * f);
+          *reinterpret_cast<uint4*>(qs + (pc >> 3) * NQ * 128 + q * 128 +
+                                    (((pc & 7) ^ (q & 7)) << 4)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+          if (pc == 0) {
+            col_sc[par * NQ + q] = kx * pow2(-ex);
+            col_vis[par * NQ + q] =
+                p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      for (int i = 0; i < g.n; ++i, ++j) {
+        const int st = j % C::kStages;
+        wait(&full[st], (j / C::kStages) & 1);
+        if (j >= 2) wait(&kd_empty[j & 1], ((j >> 1) - 1) & 1);
+        tc_fence_after();
+        const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
+        const int rr = r % kCellRows;
+        uint4 w[D / 32];
+        uint32_t sc[D / 64];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          w[c] = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * c));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          sc[c] = *reinterpret_cast<const uint32_t*>(cell + Cell<D>::k_scale(rr, 4 * c));
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint32_t s2 = e4m3x2_to_f16x2(sc[c / 2] >> (c & 1) * 16);
+          const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
+          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t o[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t f[4];
+            e2m1x8_to_f16x2(u[e], f);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[4 * e + x] = hmul2(f[x], e < 2 ? s_lo : s_hi);
+          }
+          tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + c * 16, o);
+        }
+        warp_arrive(&empty[st]);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&kd_full[j & 1]);
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------- V^T to fp16: a thread expands its dim's row ----------------
+    if (warp - 4 < C::kVWarps) {
+      const int d = threadIdx.x - 128;
+      const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + C::kV0;
+      const int shift = 4 * (d & 1);
+      int j = 0;
+      while (walk.next(p, &g)) {
+        for (int i = 0; i < g.n; ++i, ++j) {
+          const int st = j % C::kStages;
+          wait(&full[st], (j / C::kStages) & 1);
+          if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);
+          tc_fence_after();
+          const uint8_t* base = stages + st * C::kStage;
+          const int left = g.end - (g.tile + i) * kTile;     // keys in use from here on
+#pragma unroll
+          for (int c2 = 0; c2 < kGran / 2; ++c2) {
+            uint32_t o[16];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int c = 2 * c2 + half;
+              const uint4 w4 = *reinterpret_cast<const uint4*>(base + c * C::kCell +
+                                                               Cell<D>::v_codes(0, d / 2));
+              const uint4 s4 = *reinterpret_cast<const uint4*>(base + c * C::kCell +
+                                                               Cell<D>::v_scale(0, d / 16));
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // this dim's nibbles of four keys, two to a byte
+                const uint32_t u = w[e] >> shift;
+                const uint32_t x = (u & 0x000F000Fu) | (u >> 4 & 0x00F000F0u);
+                o[8 * half + 2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), e4m3x2_to_f16x2(s[e]));
+                o[8 * half + 2 * e + 1] =
+                    hmul2(e2m1x2_to_f16x2<2>(x), e4m3x2_to_f16x2(s[e] >> 16));
+              }
+              if (left < (c + 1) * kCellRows) {              // rows past the length count as 0
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int key = c * kCellRows + 2 * e;
+                  if (key >= left) o[8 * half + e] = 0;
+                  else if (key + 1 >= left) o[8 * half + e] &= 0xFFFFu;
+                }
+              }
+            }
+            tmem_st_32x32b_x16(lane_base + (j & 1) * C::kVCols + c2 * 16, o);
+          }
+          warp_arrive(&empty[st]);
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(&vd_full[j & 1]);
+        }
+      }
+    }
+  } else {
+    // ---------------- softmax: a thread owns a key ----------------
+    constexpr int CW = C::kCols;
+    const int wg = (warp - 8) >> 2, q4 = warp & 3;
+    const int r = q4 * 32 + lane, col0 = wg * CW;
+    const uint32_t bar = 1 + wg;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+    float* nm = col_nm + col0;
+    float* fac = col_f + col0;
+    int j = 0, seg = 0;
+    for (; walk.next(p, &g); ++seg) {
+      const int par = seg & 1;
+      const float* sc = col_sc + par * NQ + col0;
+      const int* vis = col_vis + par * NQ + col0;
+      // keys that every row of the unit sees
+      const int sure = p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len;
+      float2 l[CW / 2];
+#pragma unroll
+      for (int c = 0; c < CW / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      if (r < CW) nm[r] = kLift - kNoMax;
+      for (int i = 0; i < g.n; ++i, ++j) {
+        const int sb = j % C::kSBufs;
+        const uint32_t s_addr = lane_base + C::kS0 + sb * NQ + col0;
+        const int key = (g.tile + i) * kTile + r;
+        const bool masked = (g.tile + i + 1) * kTile > sure;
+        wait(&s_full[sb], (j / C::kSBufs) & 1);
+        tc_fence_after();
+        // 16 columns: scores in log2 units, minus the running maximum if `sub`
+        auto scores = [&](int c0, bool sub, float (&x)[16]) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(s_addr + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(sc + c0 + e);
+            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (sub) b = *reinterpret_cast<const float4*>(nm + c0 + e);
+            const float2 lo = __ffma2_rn(
+                make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                make_float2(a.x, a.y), make_float2(b.x, b.y));
+            const float2 hi = __ffma2_rn(
+                make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                make_float2(a.z, a.w), make_float2(b.z, b.w));
+            x[e] = lo.x;
+            x[e + 1] = lo.y;
+            x[e + 2] = hi.x;
+            x[e + 3] = hi.y;
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const int4 n = *reinterpret_cast<const int4*>(vis + c0 + e);
+              x[e] = key < n.x ? x[e] : -INFINITY;
+              x[e + 1] = key < n.y ? x[e + 1] : -INFINITY;
+              x[e + 2] = key < n.z ? x[e + 2] : -INFINITY;
+              x[e + 3] = key < n.w ? x[e + 3] : -INFINITY;
+            }
+          }
+        };
+        bool move = i == 0;
+        if (i > 0) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c0 = 0; c0 < CW; c0 += 16) {
+            float x[16];
+            scores(c0, true, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
+          }
+          move = bar_or(bar, 128, mx > kMoveLog2 + kLift);
+        } else {
+          named_bar_sync(bar, 128);                // nm is set
+        }
+        if (move) {
+          // the columns' maxima over the tile, and new running maxima
+          for (int c0 = 0; c0 < CW; c0 += 16) {
+            float x[16];
+            scores(c0, false, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float m = warp_max(x[e]);
+              if (lane == 0) red[q4 * NQ + col0 + c0 + e] = m;
+            }
+          }
+          named_bar_sync(bar, 128);
+          if (r < CW) {
+            const float* m4 = red + col0 + r;
+            const float was = kLift - nm[r];
+            const float now = fmaxf(fmaxf(fmaxf(m4[0], m4[NQ]), fmaxf(m4[2 * NQ], m4[3 * NQ])), was);
+            fac[r] = i == 0 ? 0.f : ex2(was - now);
+            nm[r] = kLift - now;
+          }
+          named_bar_sync(bar, 128);
+          if (i > 0) {
+            wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < CW; c0 += 16) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(lane_base + C::kO0 + col0 + c0, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * fac[c0 + e]);
+              tmem_st_32x32b_x16(lane_base + C::kO0 + col0 + c0, v);
+            }
+            tmem_st_wait();
+#pragma unroll
+            for (int c = 0; c < CW / 2; ++c) {
+              l[c].x *= fac[2 * c];
+              l[c].y *= fac[2 * c + 1];
+            }
+          }
+        }
+        if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);     // P buffer free
+        uint8_t* prow = pbuf + (j & 1) * C::kPBytes + (col0 / 64) * kTile * 128 + r * 128;
+#pragma unroll
+        for (int c0 = 0; c0 < CW; c0 += 16) {
+          float x[16];
+          scores(c0, true, x);
+          if (c0 + 16 == CW) {
+            tc_fence_before();
+            warp_arrive(&s_empty[sb]);
+          }
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float a = ex2(x[e]), b = ex2(x[e + 1]);
+            l[(c0 + e) / 2] = __fadd2_rn(l[(c0 + e) / 2], make_float2(a, b));
+            pk[e / 2] = pack_f16(a, b);
+          }
+#pragma unroll
+          for (int c8 = 0; c8 < 2; ++c8) {
+            const int ch = (col0 % 64 + c0) / 8 + c8;
+            *reinterpret_cast<uint4*>(prow + ((ch ^ (r & 7)) << 4)) =
+                make_uint4(pk[4 * c8], pk[4 * c8 + 1], pk[4 * c8 + 2], pk[4 * c8 + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(&p_full[j & 1]);
+      }
+      // ---- the unit's (or piece's) result ----
+#pragma unroll
+      for (int c = 0; c < CW / 2; ++c) {
+        float a = l[c].x, b = l[c].y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if (lane == 0) {
+          red[q4 * NQ + col0 + 2 * c] = a;
+          red[q4 * NQ + col0 + 2 * c + 1] = b;
+        }
+      }
+      named_bar_sync(bar, 128);
+      const bool whole = g.tile == 0 && g.n == g.nt;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (g.tile == 0 ? 1 : 0);
+      if (r < CW) {
+        const float* s4 = red + col0 + r;
+        const float sum = (s4[0] + s4[NQ]) + (s4[2 * NQ] + s4[3 * NQ]);
+        // a row that sees nothing is zero (its sum is 0; NaN for a row with NaN)
+        fac[r] = whole ? (sum == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, g.h)) / sum) : 1.f;
+        if (!whole) {
+          float* ml = p.part_ml + (static_cast<size_t>(slot) * NQ + col0 + r) * 2;
+          ml[0] = -nm[r];
+          ml[1] = sum;
+        }
+      }
+      named_bar_sync(bar, 128);
+      warp_arrive(&q_empty[par]);
+      wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
+      tc_fence_after();
+      const int rows = min(p.tile_rows, g.T - g.t0) * G;
+#pragma unroll 1
+      for (int c0 = 0; c0 < CW; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(lane_base + C::kO0 + col0 + c0, v);
+        tmem_ld_wait();
+        if (r < D) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int q = col0 + c0 + e;
+            if (q < rows) {
+              const float y = fac[c0 + e] == 0.f ? 0.f : __uint_as_float(v[e]) * fac[c0 + e];
+              if (whole) {
+                const int t = q / G;
+                p.out[(static_cast<size_t>(g.lo + g.t0 + t) * p.n_q_heads + g.h * G + q - t * G) *
+                          D +
+                      r] = float_to_bf16_bits(y);
+              } else {
+                p.part_o[(static_cast<size_t>(slot) * NQ + q) * D + r] = y;
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      warp_arrive(o_empty);
+      named_bar_sync(bar, 128);                    // nm, fac and red are read
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMma) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the unit that starts in CTA blockIdx.x of the kernel above
+// and ends in a later one: a warp per query row.
+template <int D, int NQ>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-  const int lo = p.start[b], hi = p.start[b + 1], len = p.seq_len[b];
-  const int T = hi - lo;
-  if (lo < 0 || hi < lo || hi > p.n_tokens || T > p.max_tokens || len < 0 || len > p.limit) {
-    if (blockIdx.x == 0 && h == 0 && tid == 0) set_status(p.status, DFLASH_ST_CAPACITY);
-    return;
-  }
-  const int G = p.group, r0 = blockIdx.x * kRows, rows = min(kRows, T * G - r0);
-  if (rows <= 0) return;
-  auto seen = [&](int r) {
-    return max(0, p.causal ? min(len, len - T + (r0 + r) / G + 1) : len);
-  };
-  auto at = [&](int r) {
-    return (static_cast<size_t>(lo + (r0 + r) / G) * p.n_q_heads + h * G + (r0 + r) % G) * D;
-  };
-  for (int i = tid; i < kRows * D; i += kThreads)
-    qs[i / D][i % D] = i / D < rows ? bf16_bits_to_float(p.q[at(i / D) + i % D]) : 0.f;
-  if (tid < kRows) {
-    row_m[tid] = -INFINITY;
-    row_l[tid] = 0.f;
-  }
-  constexpr int kPer = kRows * D / kThreads;
-  const int d = tid % D, or0 = tid / D * kPer;
-  float o[kPer];
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int* meta = p.meta + 8 * c0;
+  const int c1 = meta[0];
+  const int q = blockIdx.y * 4 + (threadIdx.x >> 5);
+  if (c1 < 0 || q >= meta[2]) return;
+  const int row0 = meta[1], h = meta[3];
+  constexpr int kV = D / 32;
+  float o[kV], L = 0.f, M = kNoMax;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-  const float qk = p.scale * 1.4426950408889634f * pow2(gain_exp(p.s.k_exp, h));
-  const int end = seen(rows - 1);
-  for (int key0 = 0; key0 < end; key0 += kTile) {
-    __syncthreads();
-    for (int i = tid; i < kTile * (D / 16); i += kThreads) {
-      const int j = i / (D / 16), g = i % (D / 16), key = key0 + j;
-      int slab = b, row = key;
-      bool ok = key < len;
-      if (ok && p.paged) {
-        slab = p.page_table[static_cast<size_t>(b) * p.max_pages + key / p.page_size];
-        row = key % p.page_size;
-        if (slab < 0 || slab >= p.s.n_slabs) {
-          ok = false;
-          set_status(p.status, DFLASH_ST_PAGE_MISSING);
-        }
-      }
-      float fk = 0.f, fv = 0.f;
-      uint2 kc = make_uint2(0, 0);
-      uint32_t vc[2] = {0, 0};
-      if (ok) {
-        const uint8_t* cell = p.s.cells + cell_index(p.s, slab, h, row) * Cell<D>::kBytes;
-        const int r = row % kCellRows;
-        kc = *reinterpret_cast<const uint2*>(cell + Cell<D>::k_codes(r, g));
-        for (int e = 0; e < 8; ++e)
-          vc[e / 4] |= static_cast<uint32_t>(cell[Cell<D>::v_codes(r, 8 * g + e)]) << (8 * (e & 3));
-        const uint32_t sc = cell[Cell<D>::k_scale(r, g)] | cell[Cell<D>::v_scale(r, g)] << 8;
-        const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(sc));
-        fk = f.x;
-        fv = f.y;
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t kx[4], vx[4];
-        e2m1x8_to_f16x2(half ? kc.y : kc.x, kx);
-        e2m1x8_to_f16x2(vc[half], vx);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 a = f16x2_to_float2(kx[e]), c = f16x2_to_float2(vx[e]);
-          ks[j][16 * g + 8 * half + 2 * e] = a.x * fk;
-          ks[j][16 * g + 8 * half + 2 * e + 1] = a.y * fk;
-          vs[j][16 * g + 8 * half + 2 * e] = c.x * fv;
-          vs[j][16 * g + 8 * half + 2 * e + 1] = c.y * fv;
-        }
-      }
+  for (int e = 0; e < kV; ++e) o[e] = 0.f;
+  auto slot = [&](int c) { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * NQ + q; };
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[2 * slot(c)]);
+  M = warp_max(M);
+  for (int cb = c0; cb <= c1; cb += 32) {
+    float w = 0.f;
+    if (cb + lane <= c1) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot(cb + lane));
+      w = ex2(ml.x - M);
+      L += w * ml.y;
     }
-    __syncthreads();
-    // a warp takes two rows, a lane one key
-    const int lane = tid & 31;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (tid >> 5) * 2 + i;
-      float s = 0.f;
-      for (int e = 0; e < D; ++e) s = fmaf(qs[r][e], ks[lane][e], s);
-      s = r < rows && key0 + lane < seen(r) ? s * qk : -INFINITY;
-      float m = s;
-#pragma unroll
-      for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-      const float old = row_m[r], now = fmaxf(old, m);
-      const float base = now == -INFINITY ? 0.f : now;
-      const float e = exp2f(s - base);
-      float sum = e;
-#pragma unroll
-      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      ps[r][lane] = e;
-      __syncwarp();
-      if (lane == 0) {
-        const float f = exp2f(old - base);
-        row_f[r] = f;
-        row_l[r] = row_l[r] * f + sum;
-        row_m[r] = now;
+#pragma unroll 4
+    for (int i = 0; i < min(32, c1 - cb + 1); ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* src = p.part_o + slot(cb + i) * D + lane * kV;
+      if (kV == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        o[0] += wi * x.x;
+        o[1] += wi * x.y;
+        o[2 % kV] += wi * x.z;
+        o[3 % kV] += wi * x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        o[0] += wi * x.x;
+        o[1] += wi * x.y;
       }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      float a = o[i] * row_f[or0 + i];
-      for (int j = 0; j < kTile; ++j) a = fmaf(ps[or0 + i][j], vs[j][d], a);
-      o[i] = a;
     }
   }
-  __syncthreads();
-  const float gv = pow2(gain_exp(p.s.v_exp, h));
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (or0 + i < rows) {
-      const float l = row_l[or0 + i];
-      // a row that sees nothing is zero (l is NaN, not 0, for a row with NaN)
-      p.out[at(or0 + i) + d] = float_to_bf16_bits(l == 0.f ? 0.f : o[i] / l * gv);
-    }
+  for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+  const float f = L == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, h)) / L;
+  const int t = q / p.group;
+  uint16_t* out =
+      p.out + (static_cast<size_t>(row0 + t) * p.n_q_heads + h * p.group + q - t * p.group) * D +
+      lane * kV;
+  uint32_t y[kV / 2];
+#pragma unroll
+  for (int e = 0; e < kV / 2; ++e)
+    y[e] = L == 0.f ? 0u
+                    : static_cast<uint32_t>(float_to_bf16_bits(o[2 * e] * f)) |
+                          static_cast<uint32_t>(float_to_bf16_bits(o[2 * e + 1] * f)) << 16;
+  if (kV == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[kV / 2 - 1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = y[0];
+}
+
+// Query columns of a unit: the fewest that hold the rows of the longest sequence.
+int query_columns(const dflash_kv4_dims& d) {
+  const long long rows =
+      static_cast<long long>(d.max_tokens) * (d.n_q_heads / d.n_kv_heads);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+struct AttnLayout {
+  int ctas, nq;
+  size_t off_ml, off_o, total;
+};
+
+AttnLayout attn_layout(const dflash_kv4_dims& d) {
+  AttnLayout a = {};
+  a.ctas = current_num_sms();
+  a.nq = query_columns(d);
+  const size_t rows = 2 * static_cast<size_t>(a.ctas) * a.nq;
+  a.off_ml = (32 * static_cast<size_t>(a.ctas) + 255) / 256 * 256;
+  a.off_o = a.off_ml + (8 * rows + 255) / 256 * 256;
+  a.total = a.ctas > 0 ? a.off_o + 4 * rows * d.head_dim : 0;
+  return a;
+}
+
+template <int D, int NQ>
+int run(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
+  using C = Cfg<D, NQ>;
+  int rc = set_smem_limit(reinterpret_cast<const void*>(kv4_attention_kernel<D, NQ>), C::kSmem);
+  if (rc) return rc;
+  if ((rc = launch(kv4_attention_kernel<D, NQ>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, p)))
+    return rc;
+  return launch(kv4_join_kernel<D, NQ>, dim3(ctas, NQ / 4), dim3(128), 0, st, p);
 }
 
 }  // namespace
 
-size_t kv4_attention_bytes(const dflash_kv4_dims&) { return 256; }
+size_t kv4_attention_bytes(const dflash_kv4_dims& d) { return attn_layout(d).total; }
 
 }  // namespace dflash
 
@@ -180,12 +985,15 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   Kv4Plan plan;
   if ((rc = make_kv4_plan(*dims, &plan))) return rc;
   if (!ws || ws_bytes < plan.total) return DFLASH_E_WORKSPACE;
+  if (!aligned16(ws)) return DFLASH_E_ALIGN;
+  const AttnLayout a = attn_layout(*dims);
   p.batch = dims->batch;
   p.n_tokens = dims->n_tokens;
   p.max_tokens = dims->max_tokens;
   p.n_q_heads = dims->n_q_heads;
   p.group = dims->n_q_heads / dims->n_kv_heads;
   p.causal = causal != 0;
+  p.tile_rows = a.nq / p.group;
   p.paged = cache->kv.page_table != nullptr;
   p.page_size = cache->kv.page_size;
   p.max_pages = cache->kv.max_pages;
@@ -195,14 +1003,17 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.page_table = cache->kv.page_table;
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
-  p.scale = scale;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.status = ws_at<uint32_t>(ws, plan.off_status);
-  const long long rows = static_cast<long long>(p.max_tokens) * p.group;
-  const long long tiles = (rows + kRows - 1) / kRows;
-  if (tiles > INT32_MAX) return DFLASH_E_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(tiles), dims->n_kv_heads, p.batch);
+  p.meta = ws_at<int>(ws, plan.off_att);
+  p.part_ml = ws_at<float>(ws, plan.off_att + a.off_ml);
+  p.part_o = ws_at<float>(ws, plan.off_att + a.off_o);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dims->head_dim == 128
-             ? launch(kv4_attention_kernel<128>, grid, dim3(kThreads), 0, st, p)
-             : launch(kv4_attention_kernel<64>, grid, dim3(kThreads), 0, st, p);
+  const bool wide = dims->head_dim == 128;
+  switch (a.nq) {
+    case 16: return wide ? run<128, 16>(p, a.ctas, st) : run<64, 16>(p, a.ctas, st);
+    case 32: return wide ? run<128, 32>(p, a.ctas, st) : run<64, 32>(p, a.ctas, st);
+    case 64: return wide ? run<128, 64>(p, a.ctas, st) : run<64, 64>(p, a.ctas, st);
+    default: return wide ? run<128, 128>(p, a.ctas, st) : run<64, 128>(p, a.ctas, st);
+  }
 }

@@ -86,19 +86,29 @@ class Cache:
             i32(self.k_exp) if exps else None, i32(self.v_exp) if exps else None)
 
 
-def check_attention(rng, cache, new, hq, causal, pad=0, scale=None, q_gain=1.0, q=None):
-    """Runs the call on fresh queries and compares every row.
-
-    The bound, element by element, with A = sum p |v| / sum p and e = scale max sum
-    |q||k| (the oracle's):
+def bound(ref, avg, e, v):
+    """Element by element, with A = avg = sum p |v| / sum p and e = scale max sum |q||k| (the
+    oracle's), n keys:
       2^-8 |ref|     the rounding to bf16 (half a step)
-      A 2^-11 * 2    probabilities kept in 16 bits for the second product, in
-                     numerator and weight
+      A 2^-11 * 2    probabilities kept in fp16 for the second product, in numerator and
+                     weight
+      n 2^-32 max|v|  and small ones of them in steps of 2^-24, half a step each, where the
+                     largest is at least 2^7 (so the weights' sum is too): a probability
+                     below 2^-21 of the largest has no relative bound.  It shows where the
+                     keys that matter have v = 0 in a dim.
       A 2^-22 * 4    exponentials (2^-22 relative)
       A e 2^-16      scores: 128 products summed in 32 bits (128 * 2^-24 of their
                      absolute sum) and one more rounding each of scale and subtraction
       A 2^-16        the same for the sums of the second product
     """
+    return (2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+            + len(v) * 2.0 ** -32 * np.abs(v).max(initial=0.0))
+
+
+def check_attention(rng, cache, new, hq, causal, pad=0, scale=None, q_gain=1.0, q=None):
+    """Runs the call on fresh queries and compares every row.
+
+    See bound()."""
     dfl = _dfl()
     B, d, hkv = len(new), cache.d, cache.hkv
     n = sum(new) + pad
@@ -118,7 +128,7 @@ def check_attention(rng, cache, new, hq, causal, pad=0, scale=None, q_gain=1.0, 
         lo, L = start[b], cache.lens[b]
         seen = [min(L, L - T + t + 1) if causal else L for t in range(T)]
         ref, avg, e = O.attention(qd[lo:lo + T], cache.k[b], cache.v[b], seen, scale)
-        tol = 2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+        tol = bound(ref, avg, e, cache.v[b])
         err = np.abs(got[lo:lo + T] - ref)
         assert (err <= tol).all(), (b, np.argwhere(err > tol)[:5], (err - tol).max())
     assert (got[start[-1]:] == -7).all()                # padding rows are left
@@ -605,7 +615,7 @@ def test_serving_steps_end_to_end():
             L = len(K[b])
             seen = [L - T + t + 1 if causal else L for t in range(T)]
             ref, avg, e = O.attention(qd[rows], K[b], V[b], seen, d ** -0.5)
-            tol = 2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+            tol = bound(ref, avg, e, V[b])
             assert (np.abs(got[rows] - ref) <= tol).all(), (new, b)
             if keep is not None:
                 K[b], V[b] = K[b][:L - T + keep[b]], V[b][:L - T + keep[b]]
@@ -661,7 +671,7 @@ def test_captured_step_replays_with_other_lengths():
             L = len(K[b])
             seen = [L - T + t + 1 if i % 2 == 0 else L for t in range(T)]
             ref, avg, e = O.attention(f64(q)[rows], K[b], V[b], seen, 0.125)
-            tol = 2.0 ** -8 * np.abs(ref) + avg * (2.0 ** -10 + 2.0 ** -20 + (e + 1) * 2.0 ** -16)
+            tol = bound(ref, avg, e, V[b])
             assert (np.abs(f64(outs[i % 2])[rows] - ref) <= tol).all(), (i, b)
             at += T
         assert (f64(outs[i % 2])[m:] == 4).all()
