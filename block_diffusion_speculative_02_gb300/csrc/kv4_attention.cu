@@ -64,7 +64,8 @@ struct Cfg {
   // shared memory
   static constexpr int kPBytes = (NQ + 63) / 64 * kTile * 128;
   static constexpr int kQBytes = NQ * D * 2;
-  static constexpr int kFixed = 2 * kPBytes + 2 * kQBytes;
+  static constexpr int kVScale = kTile * (D / 16) * 2;  // fp16 scales of a V tile
+  static constexpr int kFixed = 2 * kPBytes + 2 * kQBytes + 2 * kVScale;
   static constexpr int kTables = 12 * 1024;
   static constexpr int kFit = (226 * 1024 - kFixed - kTables) / kStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -137,6 +138,11 @@ struct Start {
 // One segment: consecutive tiles of one unit.
 struct Seg {
   int b, h, t0, lo, T, len, end, tile, n, nt;
+};
+
+// What the softmax needs of a segment, left in shared memory beside its query rows.
+struct Piece {
+  int tile, n, nt, sure, rows, h;   // sure: keys that every row sees
 };
 
 struct Walk {
@@ -312,6 +318,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, issued by one thread.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -331,12 +344,23 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
 
 // A wait of a role that goes on regardless: once one gave up, the rest are skipped, so
 // every role still runs its loops to their end (named barriers included).
+// (The loop is kept out of line: five roles share the instruction cache.)
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                       uint32_t* status) {
+  return mbar_wait(bar, parity, abort_flag, status);
+}
+
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                        uint32_t* status) {
+  return mbar_try_wait(bar, parity) || slow_wait(bar, parity, abort_flag, status);
+}
+
 struct Waiter {
   volatile int* abort_flag;
   uint32_t* status;
   bool dead;
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (!dead) dead = !mbar_wait(bar, parity, abort_flag, status);
+    if (!dead) dead = !wait_on(bar, parity, abort_flag, status);
     __syncwarp();
   }
 };
@@ -357,14 +381,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* pbuf = smem;
   uint8_t* qbuf = pbuf + 2 * C::kPBytes;
-  uint8_t* stages = qbuf + 2 * C::kQBytes;
+  uint8_t* vscale = qbuf + 2 * C::kQBytes;
+  uint8_t* stages = vscale + 2 * C::kVScale;
   uint8_t* tables = stages + C::kStages * C::kStage;
   float* col_sc = reinterpret_cast<float*>(tables);        // [2][NQ] log2 units per score
   int* col_vis = reinterpret_cast<int*>(col_sc + 2 * NQ);  // [2][NQ] keys a column sees
-  float* col_nm = reinterpret_cast<float*>(col_vis + 2 * NQ);  // [NQ] kLift - running maximum
+  int* col_row = col_vis + 2 * NQ;                         // [2][NQ] row of q and out
+  float* col_nm = reinterpret_cast<float*>(col_row + 2 * NQ);  // [NQ] kLift - running maximum
   float* col_f = col_nm + NQ;                              // [NQ] rescale factor, then 1 / sum
   float* red = col_f + NQ;                                 // [4][NQ]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(red + 4 * NQ);
+  Piece* piece = reinterpret_cast<Piece*>(red + 4 * NQ);   // [2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(piece + 2);
   uint64_t* full = bars;
   uint64_t* empty = full + C::kStages;
   uint64_t* kd_full = empty + C::kStages;  // [2] K tile in TMEM (and Q staged)
@@ -443,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const bool use = lane < kGran && key < g.end;
         const uint32_t have = __ballot_sync(0xffffffffu, use && slab >= 0);
         const uint32_t miss = __ballot_sync(0xffffffffu, use && slab < 0);
-        if (!mbar_wait(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status)) go = false;
+        if (!wait_on(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status)) go = false;
         if (!__all_sync(0xffffffffu, go)) {
           go = false;
           break;
@@ -478,10 +505,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       constexpr uint32_t idesc_o = umma_idesc_f16(128, NQ, true);
       const uint32_t q_addr = smem_u32(qbuf), p_addr = smem_u32(pbuf);
       auto issue_pv = [&](int j, bool first, int seg) -> bool {
-        if (!mbar_wait(&p_full[j & 1], (j >> 1) & 1, abort_flag, p.status) ||
-            !mbar_wait(&vd_full[j & 1], (j >> 1) & 1, abort_flag, p.status))
+        if (!wait_on(&p_full[j & 1], (j >> 1) & 1, abort_flag, p.status) ||
+            !wait_on(&vd_full[j & 1], (j >> 1) & 1, abort_flag, p.status))
           return false;
-        if (first && seg > 0 && !mbar_wait(o_empty, (seg - 1) & 1, abort_flag, p.status))
+        if (first && seg > 0 && !wait_on(o_empty, (seg - 1) & 1, abort_flag, p.status))
           return false;
         tc_fence_after();
 #pragma unroll
@@ -498,9 +525,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       while (ok && walk.next(p, &g)) {
         for (int i = 0; ok && i < g.n; ++i, ++j) {
           const int sb = j % C::kSBufs;
-          ok = mbar_wait(&kd_full[j & 1], (j >> 1) & 1, abort_flag, p.status);
+          ok = wait_on(&kd_full[j & 1], (j >> 1) & 1, abort_flag, p.status);
           if (ok && j >= C::kSBufs)
-            ok = mbar_wait(&s_empty[sb], (j / C::kSBufs - 1) & 1, abort_flag, p.status);
+            ok = wait_on(&s_empty[sb], (j / C::kSBufs - 1) & 1, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -533,17 +560,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       {  // the unit's query rows, D / 8 lanes a row
         constexpr int kPer = D / 8;
         const int rows = min(p.tile_rows, g.T - g.t0) * G;
+        if (r == 0) {
+          Piece pc = {g.tile, g.n, g.nt,
+                      p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows, g.h};
+          piece[par] = pc;
+        }
         uint8_t* qs = qbuf + par * C::kQBytes;
         const float kx = p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h));
 #pragma unroll 2
         for (int it = r; it < NQ * kPer; it += 128) {
           const int q = it / kPer, pc = it % kPer, t = q / G;
+          const int row = (g.lo + g.t0 + t) * p.n_q_heads + g.h * G + q - t * G;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (q < rows)
-            x = *reinterpret_cast<const uint4*>(
-                p.q + (static_cast<size_t>(g.lo + g.t0 + t) * p.n_q_heads + g.h * G + q - t * G) *
-                          D +
-                8 * pc);
+            x = *reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(row) * D + 8 * pc);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
           uint32_t m = 0;
 #pragma unroll
@@ -563,6 +593,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               make_uint4(y[0], y[1], y[2], y[3]);
           if (pc == 0) {
             col_sc[par * NQ + q] = kx * pow2(-ex);
+            col_row[par * NQ + q] = row;
             col_vis[par * NQ + q] =
                 p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
           }
@@ -576,28 +607,27 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         tc_fence_after();
         const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
         const int rr = r % kCellRows;
-        uint4 w[D / 32];
-        uint32_t sc[D / 64];
+#pragma unroll 1
+        for (int c2 = 0; c2 < D / 64; ++c2) {          // 64 dims a round
+          const uint4 wa = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 4 * c2));
+          const uint4 wb = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 4 * c2 + 2));
+          const uint32_t sc = *reinterpret_cast<const uint32_t*>(cell + Cell<D>::k_scale(rr, 4 * c2));
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          w[c] = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * c));
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t s2 = e4m3x2_to_f16x2(c ? sc >> 16 : sc);
+            const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
+            const uint32_t u[4] = {c ? wb.x : wa.x, c ? wb.y : wa.y, c ? wb.z : wa.z,
+                                   c ? wb.w : wa.w};
+            uint32_t o[16];
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          sc[c] = *reinterpret_cast<const uint32_t*>(cell + Cell<D>::k_scale(rr, 4 * c));
+            for (int e = 0; e < 4; ++e) {
+              uint32_t f[4];
+              e2m1x8_to_f16x2(u[e], f);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const uint32_t s2 = e4m3x2_to_f16x2(sc[c / 2] >> (c & 1) * 16);
-          const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
-          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-          uint32_t o[16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t f[4];
-            e2m1x8_to_f16x2(u[e], f);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[4 * e + x] = hmul2(f[x], e < 2 ? s_lo : s_hi);
+              for (int x = 0; x < 4; ++x) o[4 * e + x] = hmul2(f[x], e < 2 ? s_lo : s_hi);
+            }
+            tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + c2 * 32 + c * 16, o);
           }
-          tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + c * 16, o);
         }
         warp_arrive(&empty[st]);
         tmem_st_wait();
@@ -607,7 +637,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     }
   } else if (warp < 8) {
     // ---------------- V^T to fp16: a thread expands its dim's row ----------------
+    // The 16 threads of a group of dims share their scales, so each scale is turned to
+    // fp16 once, by all threads together, and read back.
     if (warp - 4 < C::kVWarps) {
+      constexpr int kN = 32 * C::kVWarps;
       const int d = threadIdx.x - 128;
       const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + C::kV0;
       const int shift = 4 * (d & 1);
@@ -616,40 +649,46 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         for (int i = 0; i < g.n; ++i, ++j) {
           const int st = j % C::kStages;
           wait(&full[st], (j / C::kStages) & 1);
+          const uint8_t* base = stages + st * C::kStage;
+          uint8_t* vsc = vscale + (j & 1) * C::kVScale;
+          {  // 8 scales a thread: half the rows of a cell, one group of dims
+            const int c = d / (D / 8), x = d % (D / 8);
+            const uint2 s8 = *reinterpret_cast<const uint2*>(base + c * C::kCell +
+                                                             Cell<D>::v_scale(0, 0) + x * 8);
+            *reinterpret_cast<uint4*>(vsc + d * 16) =
+                make_uint4(e4m3x2_to_f16x2(s8.x), e4m3x2_to_f16x2(s8.x >> 16),
+                           e4m3x2_to_f16x2(s8.y), e4m3x2_to_f16x2(s8.y >> 16));
+          }
           if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);
           tc_fence_after();
-          const uint8_t* base = stages + st * C::kStage;
+          named_bar_sync(3, kN);
           const int left = g.end - (g.tile + i) * kTile;     // keys in use from here on
+          const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
+          const uint4* scl = reinterpret_cast<const uint4*>(vsc + d / 16 * 32);
+#pragma unroll 2
+          for (int c = 0; c < kGran; ++c) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
+            const uint4 sa = scl[c * (D / 8)], sb = scl[c * (D / 8) + 1];
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            const uint32_t s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+            uint32_t o[8];
 #pragma unroll
-          for (int c2 = 0; c2 < kGran / 2; ++c2) {
-            uint32_t o[16];
+            for (int e = 0; e < 4; ++e) {
+              // this dim's nibbles of four keys, two to a byte
+              const uint32_t u = w[e] >> shift;
+              const uint32_t x = (u & 0x000F000Fu) | (u >> 4 & 0x00F000F0u);
+              o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), s[2 * e]);
+              o[2 * e + 1] = hmul2(e2m1x2_to_f16x2<2>(x), s[2 * e + 1]);
+            }
+            if (left < (c + 1) * kCellRows) {                // rows past the length count as 0
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int c = 2 * c2 + half;
-              const uint4 w4 = *reinterpret_cast<const uint4*>(base + c * C::kCell +
-                                                               Cell<D>::v_codes(0, d / 2));
-              const uint4 s4 = *reinterpret_cast<const uint4*>(base + c * C::kCell +
-                                                               Cell<D>::v_scale(0, d / 16));
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                // this dim's nibbles of four keys, two to a byte
-                const uint32_t u = w[e] >> shift;
-                const uint32_t x = (u & 0x000F000Fu) | (u >> 4 & 0x00F000F0u);
-                o[8 * half + 2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), e4m3x2_to_f16x2(s[e]));
-                o[8 * half + 2 * e + 1] =
-                    hmul2(e2m1x2_to_f16x2<2>(x), e4m3x2_to_f16x2(s[e] >> 16));
-              }
-              if (left < (c + 1) * kCellRows) {              // rows past the length count as 0
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int key = c * kCellRows + 2 * e;
-                  if (key >= left) o[8 * half + e] = 0;
-                  else if (key + 1 >= left) o[8 * half + e] &= 0xFFFFu;
-                }
+              for (int e = 0; e < 8; ++e) {
+                const int key = c * kCellRows + 2 * e;
+                if (key >= left) o[e] = 0;
+                else if (key + 1 >= left) o[e] &= 0xFFFFu;
               }
             }
-            tmem_st_32x32b_x16(lane_base + (j & 1) * C::kVCols + c2 * 16, o);
+            tmem_st_32x32b_x8(lane_base + (j & 1) * C::kVCols + c * 8, o);
           }
           warp_arrive(&empty[st]);
           tmem_st_wait();
@@ -661,40 +700,38 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   } else {
     // ---------------- softmax: a thread owns a key ----------------
     constexpr int CW = C::kCols;
+    constexpr bool kKeep = CW <= 32;       // the tile's scores stay in registers
     const int wg = (warp - 8) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, col0 = wg * CW;
     const uint32_t bar = 1 + wg;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     float* nm = col_nm + col0;
     float* fac = col_f + col0;
-    int j = 0, seg = 0;
-    for (; walk.next(p, &g); ++seg) {
+    const int total = static_cast<int>(start->left);
+    for (int j = 0, seg = 0; j < total; ++seg) {
       const int par = seg & 1;
       const float* sc = col_sc + par * NQ + col0;
       const int* vis = col_vis + par * NQ + col0;
-      // keys that every row of the unit sees
-      const int sure = p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len;
+      wait(&s_full[j % C::kSBufs], (j / C::kSBufs) & 1);     // the segment's tables are there
+      const int n = piece[par].n, tile0 = piece[par].tile, sure = piece[par].sure;
       float2 l[CW / 2];
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) l[c] = make_float2(0.f, 0.f);
       if (r < CW) nm[r] = kLift - kNoMax;
-      for (int i = 0; i < g.n; ++i, ++j) {
+      named_bar_sync(bar, 128);
+      for (int i = 0; i < n; ++i, ++j) {
         const int sb = j % C::kSBufs;
         const uint32_t s_addr = lane_base + C::kS0 + sb * NQ + col0;
-        const int key = (g.tile + i) * kTile + r;
-        const bool masked = (g.tile + i + 1) * kTile > sure;
+        const int key = (tile0 + i) * kTile + r;
+        const bool masked = (tile0 + i + 1) * kTile > sure;
         wait(&s_full[sb], (j / C::kSBufs) & 1);
         tc_fence_after();
-        // 16 columns: scores in log2 units, minus the running maximum if `sub`
-        auto scores = [&](int c0, bool sub, float (&x)[16]) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(s_addr + c0, v);
-          tmem_ld_wait();
+        // 16 columns of S times their scale, minus the running maximum
+        auto scores = [&](const uint32_t (&v)[16], int c0, float* x) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 a = *reinterpret_cast<const float4*>(sc + c0 + e);
-            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (sub) b = *reinterpret_cast<const float4*>(nm + c0 + e);
+            const float4 b = *reinterpret_cast<const float4*>(nm + c0 + e);
             const float2 lo = __ffma2_rn(
                 make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
                 make_float2(a.x, a.y), make_float2(b.x, b.y));
@@ -708,38 +745,46 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const int4 n = *reinterpret_cast<const int4*>(vis + c0 + e);
-              x[e] = key < n.x ? x[e] : -INFINITY;
-              x[e + 1] = key < n.y ? x[e + 1] : -INFINITY;
-              x[e + 2] = key < n.z ? x[e + 2] : -INFINITY;
-              x[e + 3] = key < n.w ? x[e + 3] : -INFINITY;
-            }
+            for (int e = 0; e < 16; ++e)
+              if (key >= vis[c0 + e]) x[e] = -INFINITY;
           }
         };
-        bool move = i == 0;
-        if (i > 0) {
-          float mx = -INFINITY;
+        float x[kKeep ? CW : 16], mx = -INFINITY;
+        auto load_all = [&] {
+          uint32_t v[CW / 16][16];
 #pragma unroll
+          for (int c = 0; c < CW / 16; ++c) tmem_ld_32x32b_x16(s_addr + c * 16, v[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < CW / 16; ++c) scores(v[c], c * 16, x + c * 16);
+        };
+        if (kKeep) {
+          load_all();
+#pragma unroll
+          for (int e = 0; e < (kKeep ? CW : 0); ++e) mx = fmaxf(mx, x[e]);
+        } else if (i > 0) {
+#pragma unroll 1
           for (int c0 = 0; c0 < CW; c0 += 16) {
-            float x[16];
-            scores(c0, true, x);
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(s_addr + c0, v);
+            tmem_ld_wait();
+            scores(v, c0, x);
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
           }
-          move = bar_or(bar, 128, mx > kMoveLog2 + kLift);
-        } else {
-          named_bar_sync(bar, 128);                // nm is set
         }
-        if (move) {
+        if (bar_or(bar, 128, i == 0 || mx > kMoveLog2 + kLift)) {
           // the columns' maxima over the tile, and new running maxima
+#pragma unroll 1
           for (int c0 = 0; c0 < CW; c0 += 16) {
-            float x[16];
-            scores(c0, false, x);
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(s_addr + c0, v);
+            tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float m = warp_max(x[e]);
-              if (lane == 0) red[q4 * NQ + col0 + c0 + e] = m;
+              const float y = __uint_as_float(v[e]) * sc[c0 + e];
+              const float m = warp_max(masked && key >= vis[c0 + e] ? -INFINITY : y);
+              if (lane == e) red[q4 * NQ + col0 + c0 + e] = m;
             }
           }
           named_bar_sync(bar, 128);
@@ -766,26 +811,34 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             }
             tmem_st_wait();
 #pragma unroll
-            for (int c = 0; c < CW / 2; ++c) {
-              l[c].x *= fac[2 * c];
-              l[c].y *= fac[2 * c + 1];
-            }
+            for (int c = 0; c < CW / 2; ++c)
+              l[c] = __fmul2_rn(l[c], *reinterpret_cast<const float2*>(fac + 2 * c));
           }
+          if (kKeep) load_all();
+        }
+        if (kKeep) {
+          tc_fence_before();
+          warp_arrive(&s_empty[sb]);
         }
         if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);     // P buffer free
         uint8_t* prow = pbuf + (j & 1) * C::kPBytes + (col0 / 64) * kTile * 128 + r * 128;
 #pragma unroll
         for (int c0 = 0; c0 < CW; c0 += 16) {
-          float x[16];
-          scores(c0, true, x);
-          if (c0 + 16 == CW) {
-            tc_fence_before();
-            warp_arrive(&s_empty[sb]);
+          float* xc = kKeep ? x + c0 : x;
+          if (!kKeep) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(s_addr + c0, v);
+            tmem_ld_wait();
+            if (c0 + 16 == CW) {
+              tc_fence_before();
+              warp_arrive(&s_empty[sb]);
+            }
+            scores(v, c0, xc);
           }
           uint32_t pk[8];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float a = ex2(x[e]), b = ex2(x[e + 1]);
+            const float a = ex2(xc[e]), b = ex2(xc[e + 1]);
             l[(c0 + e) / 2] = __fadd2_rn(l[(c0 + e) / 2], make_float2(a, b));
             pk[e / 2] = pack_f16(a, b);
           }
@@ -801,27 +854,35 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         warp_arrive(&p_full[j & 1]);
       }
       // ---- the unit's (or piece's) result ----
+      // column sums over the warp's keys: halves of the columns change hands at each
+      // step, so lane x ends with column x (of the first 32, then of the next)
+      {
+        float* lf = reinterpret_cast<float*>(l);
 #pragma unroll
-      for (int c = 0; c < CW / 2; ++c) {
-        float a = l[c].x, b = l[c].y;
+        for (int c32 = 0; c32 < CW; c32 += 32) {
+          constexpr int kN = CW < 32 ? CW : 32;
+          float* y = lf + c32;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        if (lane == 0) {
-          red[q4 * NQ + col0 + 2 * c] = a;
-          red[q4 * NQ + col0 + 2 * c + 1] = b;
+          for (int n = kN / 2; n; n >>= 1) {
+            const bool up = lane & n;
+#pragma unroll
+            for (int c = 0; c < n; ++c) {
+              const float other = __shfl_xor_sync(0xffffffffu, up ? y[c] : y[c + n], n);
+              y[c] = (up ? y[c + n] : y[c]) + other;
+            }
+          }
+          if (kN == 16) y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
+          if (lane < kN) red[q4 * NQ + col0 + c32 + lane] = y[0];
         }
       }
       named_bar_sync(bar, 128);
-      const bool whole = g.tile == 0 && g.n == g.nt;
-      const int slot = 2 * static_cast<int>(blockIdx.x) + (g.tile == 0 ? 1 : 0);
+      const bool whole = tile0 == 0 && n == piece[par].nt;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (tile0 == 0 ? 1 : 0);
       if (r < CW) {
         const float* s4 = red + col0 + r;
         const float sum = (s4[0] + s4[NQ]) + (s4[2 * NQ] + s4[3 * NQ]);
         // a row that sees nothing is zero (its sum is 0; NaN for a row with NaN)
-        fac[r] = whole ? (sum == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, g.h)) / sum) : 1.f;
+        fac[r] = whole ? (sum == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, piece[par].h)) / sum) : 1.f;
         if (!whole) {
           float* ml = p.part_ml + (static_cast<size_t>(slot) * NQ + col0 + r) * 2;
           ml[0] = -nm[r];
@@ -829,35 +890,33 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
       }
       named_bar_sync(bar, 128);
-      warp_arrive(&q_empty[par]);
+      const int* row = col_row + par * NQ + col0;
+      const int rows = piece[par].rows - col0;                      // of this warpgroup
       wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
       tc_fence_after();
-      const int rows = min(p.tile_rows, g.T - g.t0) * G;
 #pragma unroll 1
       for (int c0 = 0; c0 < CW; c0 += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(lane_base + C::kO0 + col0 + c0, v);
         tmem_ld_wait();
-        if (r < D) {
+        if (r < D && c0 < rows) {
+          float* po = p.part_o + (static_cast<size_t>(slot) * NQ + col0 + c0) * D + r;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int q = col0 + c0 + e;
-            if (q < rows) {
-              const float y = fac[c0 + e] == 0.f ? 0.f : __uint_as_float(v[e]) * fac[c0 + e];
-              if (whole) {
-                const int t = q / G;
-                p.out[(static_cast<size_t>(g.lo + g.t0 + t) * p.n_q_heads + g.h * G + q - t * G) *
-                          D +
-                      r] = float_to_bf16_bits(y);
-              } else {
-                p.part_o[(static_cast<size_t>(slot) * NQ + q) * D + r] = y;
-              }
+            const float f = fac[c0 + e];
+            const float y = f == 0.f ? 0.f : __uint_as_float(v[e]) * f;
+            if (whole) {
+              if (c0 + e < rows)
+                p.out[static_cast<size_t>(row[c0 + e]) * D + r] = float_to_bf16_bits(y);
+            } else {
+              po[e * D] = y;
             }
           }
         }
       }
       tc_fence_before();
       warp_arrive(o_empty);
+      warp_arrive(&q_empty[par]);
       named_bar_sync(bar, 128);                    // nm, fac and red are read
     }
   }
@@ -987,6 +1046,8 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   if (!ws || ws_bytes < plan.total) return DFLASH_E_WORKSPACE;
   if (!aligned16(ws)) return DFLASH_E_ALIGN;
   const AttnLayout a = attn_layout(*dims);
+  if (static_cast<long long>(dims->n_tokens) * dims->n_q_heads > INT32_MAX)
+    return DFLASH_E_UNSUPPORTED;
   p.batch = dims->batch;
   p.n_tokens = dims->n_tokens;
   p.max_tokens = dims->max_tokens;
