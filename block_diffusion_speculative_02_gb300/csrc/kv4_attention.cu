@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int kSoftWgs = NQ >= 32 ? 2 : 1;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
   static constexpr int kVWarps = D / 32;               // warps that hold rows of V^T
-  static constexpr int kThreads = 32 * (8 + 4 * kSoftWgs + 2);
+  static constexpr int kThreads = 32 * (8 + 4 * kSoftWgs + 4);
   // TMEM columns
   static constexpr int kKCols = D / 2, kVCols = kTile / 2;
   static constexpr int kSBufs = NQ <= 64 ? 2 : 1;
@@ -85,7 +85,7 @@ struct Kv4AttnParams {
   uint16_t* out;
   float scale_log2;
   uint32_t* status;
-  int* meta;                 // [CTAs][8]: the unit that starts in a CTA and ends in a later one
+  int* meta;                 // [CTAs][4]: the unit that starts in a CTA and ends in a later one
   float* part_ml;            // [2 CTAs][NQ][2]
   float* part_o;             // [2 CTAs][NQ][D]
 };
@@ -119,20 +119,26 @@ __device__ __forceinline__ int unit_end(const Kv4AttnParams& p, const Seq& s, in
 }
 __device__ __forceinline__ int unit_tiles(int end) { return max(1, (end + kTile - 1) / kTile); }
 
-__device__ __forceinline__ long long seq_tiles(const Kv4AttnParams& p, const Seq& s) {
+// A unit also costs kUnitCost tiles of time that are not tiles (its query rows, the
+// drain of its O); the run of a CTA is cut from tiles plus those.
+constexpr int kUnitCost = 2;
+
+__device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const Seq& s) {
   long long n = 0;
   if (!p.causal) {
     n = static_cast<long long>(s.n_qt) * unit_tiles(s.len);
   } else {
     for (int i = 0; i < s.n_qt; ++i) n += unit_tiles(unit_end(p, s, i));
   }
-  return n * p.s.n_kv_heads;
+  return (n + static_cast<long long>(s.n_qt) * kUnitCost) * p.s.n_kv_heads;
 }
 
 struct Start {
-  long long left;            // tiles of this CTA
-  int b, qt, h, tile;        // the first of them
-  int c_last;                // CTA that ends the unit which this one starts and does not end
+  long long left;            // cost of this CTA's run
+  Seq s;                     // sequence of its first unit
+  int b, qt, h;
+  long long off;             // cost of that unit before the run
+  int tiles;                 // of the run
 };
 
 // One segment: consecutive tiles of one unit.
@@ -146,46 +152,49 @@ struct Piece {
 };
 
 struct Walk {
-  long long left;
-  int b, qt, h, tile, end, nt;
+  long long left, off;
+  int b, qt, h, end, nt;
   Seq s;
   __device__ __forceinline__ Walk(const Kv4AttnParams& p, const Start& st)
-      : left(st.left), b(st.b), qt(st.qt), h(st.h), tile(st.tile) {
-    if (left > 0) {
-      s = load_seq(p, b);
-      end = unit_end(p, s, qt);
-      nt = unit_tiles(end);
-    }
+      : left(st.left), off(st.off), b(st.b), qt(st.qt), h(st.h), s(st.s) {
+    end = unit_end(p, s, qt);
+    nt = unit_tiles(end);
   }
   __device__ __forceinline__ bool next(const Kv4AttnParams& p, Seg* g) {
-    if (left <= 0) return false;
-    if (tile == nt) {        // the unit after the last one
-      tile = 0;
-      if (++h == p.s.n_kv_heads) {
-        h = 0;
-        ++qt;
-        while (qt >= s.n_qt) {
-          qt = 0;
-          if (++b >= p.batch) return false;
-          s = load_seq(p, b);
+    while (left > 0) {
+      if (off == nt + kUnitCost) {        // the unit after this one
+        off = 0;
+        if (++h == p.s.n_kv_heads) {
+          h = 0;
+          ++qt;
+          while (qt >= s.n_qt) {
+            qt = 0;
+            if (++b >= p.batch) return false;
+            s = load_seq(p, b);
+          }
+          end = unit_end(p, s, qt);
+          nt = unit_tiles(end);
         }
-        end = unit_end(p, s, qt);
-        nt = unit_tiles(end);
       }
+      const int o = static_cast<int>(off);
+      const int take = static_cast<int>(min(left, static_cast<long long>(nt + kUnitCost - o)));
+      off += take;
+      left -= take;
+      const int from = max(0, o - kUnitCost), to = o + take - kUnitCost;
+      if (to <= from) continue;
+      g->b = b;
+      g->h = h;
+      g->t0 = qt * p.tile_rows;
+      g->lo = s.lo;
+      g->T = s.T;
+      g->len = s.len;
+      g->end = end;
+      g->tile = from;
+      g->nt = nt;
+      g->n = to - from;
+      return true;
     }
-    g->b = b;
-    g->h = h;
-    g->t0 = qt * p.tile_rows;
-    g->lo = s.lo;
-    g->T = s.T;
-    g->len = s.len;
-    g->end = end;
-    g->tile = tile;
-    g->nt = nt;
-    g->n = static_cast<int>(min(left, static_cast<long long>(nt - tile)));
-    tile += g->n;
-    left -= g->n;
-    return true;
+    return false;
   }
 };
 
@@ -195,13 +204,17 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-// By one warp.  CTA c of n takes tiles [W c / n, W (c + 1) / n) of the W in all.
+// By one warp.  CTA c of n takes [W c / n, W (c + 1) / n) of the cost W of all units.
 __device__ void make_start(const Kv4AttnParams& p, Start* out) {
   const int lane = lane_id();
-  long long all = 0;
+  long long all = 0, mine = 0;
+  Seq s = {0, 0, 0, 0};      // of sequence `lane` of a group of 32
   bool bad = false;
-  for (int b0 = 0; b0 < p.batch; b0 += 32)
-    if (b0 + lane < p.batch) all += seq_tiles(p, load_seq(p, b0 + lane, &bad));
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    if (b0 + lane < p.batch) s = load_seq(p, b0 + lane, &bad);
+    mine = b0 + lane < p.batch ? seq_cost(p, s) : 0;
+    all += mine;
+  }
   if (bad && blockIdx.x == 0) set_status(p.status, DFLASH_ST_CAPACITY);
   const long long W = warp_sum(all);
   const long long n = min(static_cast<long long>(gridDim.x), W), c = blockIdx.x;
@@ -211,12 +224,13 @@ __device__ void make_start(const Kv4AttnParams& p, Start* out) {
     first = W * c / n;
     st.left = W * (c + 1) / n - first;
   }
-  long long unit0 = 0;       // first tile of the unit that this CTA leaves unfinished
   if (st.left > 0) {
     long long before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const long long mine =
-          b0 + lane < p.batch ? seq_tiles(p, load_seq(p, b0 + lane)) : 0;
+      if (p.batch > 32) {
+        if (b0 + lane < p.batch) s = load_seq(p, b0 + lane);
+        mine = b0 + lane < p.batch ? seq_cost(p, s) : 0;
+      }
       long long inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -227,44 +241,42 @@ __device__ void make_start(const Kv4AttnParams& p, Start* out) {
       if (hit) {
         const int l = __ffs(hit) - 1;
         st.b = b0 + l;
+        st.s.lo = __shfl_sync(0xffffffffu, s.lo, l);
+        st.s.T = __shfl_sync(0xffffffffu, s.T, l);
+        st.s.len = __shfl_sync(0xffffffffu, s.len, l);
+        st.s.n_qt = __shfl_sync(0xffffffffu, s.n_qt, l);
         before += __shfl_sync(0xffffffffu, inc - mine, l);
         break;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    Seq s = load_seq(p, st.b);
     long long rem = first - before;
-    int nt = unit_tiles(unit_end(p, s, 0));
-    while (rem >= static_cast<long long>(nt) * p.s.n_kv_heads) {
-      rem -= static_cast<long long>(nt) * p.s.n_kv_heads;
-      nt = unit_tiles(unit_end(p, s, ++st.qt));
+    int cost = unit_tiles(unit_end(p, st.s, 0)) + kUnitCost;
+    while (rem >= static_cast<long long>(cost) * p.s.n_kv_heads) {
+      rem -= static_cast<long long>(cost) * p.s.n_kv_heads;
+      cost = unit_tiles(unit_end(p, st.s, ++st.qt)) + kUnitCost;
     }
-    st.h = static_cast<int>(rem / nt);
-    st.tile = static_cast<int>(rem - static_cast<long long>(st.h) * nt);
+    st.h = static_cast<int>(rem / cost);
+    st.off = rem - static_cast<long long>(st.h) * cost;
   }
-  // the segments once over, for the unit that is left unfinished
-  st.c_last = -1;
+  // the segments once over: their tiles, and the unit that is left unfinished
+  int meta[4] = {-1, 0, 0, 0};
   Seg g = {};
   Walk w(p, st);
-  int meta[4] = {0, 0, 0, 0};
-  long long at = first;
   while (w.next(p, &g)) {
-    if (g.tile == 0 && g.n < g.nt) {
-      unit0 = at;
-      st.c_last = static_cast<int>(((unit0 + g.nt) * n - 1) / W);
-      meta[0] = g.lo + g.t0;
-      meta[1] = min(p.tile_rows, g.T - g.t0) * p.group;
-      meta[2] = g.h;
+    st.tiles += g.n;
+    if (g.tile == 0 && g.n < g.nt) {   // its last tile ends where the run does plus the rest
+      const long long end = first + st.left + (g.nt - g.n);
+      meta[0] = static_cast<int>((end * n - 1) / W);
+      meta[1] = g.lo + g.t0;
+      meta[2] = min(p.tile_rows, g.T - g.t0) * p.group;
+      meta[3] = g.h;
     }
-    at += g.n;
   }
   if (lane == 0) {
     *out = st;
-    int* m = p.meta + 8 * blockIdx.x;
-    m[0] = st.c_last;
-    m[1] = meta[0];
-    m[2] = meta[1];
-    m[3] = meta[2];
+    *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) =
+        make_int4(meta[0], meta[1], meta[2], meta[3]);
   }
 }
 
@@ -394,14 +406,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(piece + 2);
   uint64_t* full = bars;
   uint64_t* empty = full + C::kStages;
-  uint64_t* kd_full = empty + C::kStages;  // [2] K tile in TMEM (and Q staged)
+  uint64_t* kd_full = empty + C::kStages;  // [2] K tile in TMEM
   uint64_t* kd_empty = kd_full + 2;        // [2] S product done
   uint64_t* vd_full = kd_empty + 2;        // [2] V^T tile in TMEM
   uint64_t* s_full = vd_full + 2;          // [kSBufs] S in TMEM
   uint64_t* s_empty = s_full + 2;          // [kSBufs] S read
   uint64_t* p_full = s_empty + 2;          // [2] P in shared memory
   uint64_t* pv_done = p_full + 2;          // [2] P V product done
-  uint64_t* q_empty = pv_done + 2;         // [2] column tables of a segment read
+  uint64_t* q_full = pv_done + 2;          // [2] query rows and tables of a segment
+  uint64_t* q_empty = q_full + 2;          // [2] read
   uint64_t* o_empty = q_empty + 2;         // O of a segment read
   uint64_t* mdrain = o_empty + 1;
   Start* start = reinterpret_cast<Start*>(mdrain + 1);
@@ -409,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducer = 8 + 4 * C::kSoftWgs, kMma = kProducer + 1;
+  constexpr int kProducer = 8 + 4 * C::kSoftWgs, kMma = kProducer + 1, kQuery = kMma + 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -423,6 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       mbar_init(&s_empty[i], 4 * C::kSoftWgs);
       mbar_init(&p_full[i], 4 * C::kSoftWgs);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&q_full[i], 2);
       mbar_init(&q_empty[i], 4 * C::kSoftWgs);
     }
     mbar_init(o_empty, 4 * C::kSoftWgs);
@@ -453,17 +467,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         p.max_tokens > p.tile_rows ? l2_policy_evict_normal() : l2_policy_evict_first();
     int j = 0;
     bool go = true;
+    // lane: page of cell `lane` of the four tiles from `tile` on
+    auto pages = [&](int tile) {
+      const int key = tile * kTile + lane * kCellRows;
+      int slab = g.b;
+      if (p.paged && key < g.end) {
+        slab = p.page_table[static_cast<size_t>(g.b) * p.max_pages + key / p.page_size];
+        if (slab >= p.s.n_slabs) slab = -1;
+      }
+      return slab;
+    };
     while (go && walk.next(p, &g)) {
-      int slab4 = -1;                               // lane: page of cell `lane` of four tiles
+      int slab4 = 0, ahead = pages(g.tile);
       for (int i = 0; i < g.n; ++i, ++j) {
         const int st = j % C::kStages;
         if ((i & 3) == 0) {
-          const int key = (g.tile + i) * kTile + lane * kCellRows;
-          slab4 = g.b;
-          if (p.paged && key < g.end) {
-            slab4 = p.page_table[static_cast<size_t>(g.b) * p.max_pages + key / p.page_size];
-            if (slab4 >= p.s.n_slabs) slab4 = -1;
-          }
+          slab4 = ahead;
+          ahead = pages(g.tile + i + 4);
         }
         const int slab = __shfl_sync(0xffffffffu, slab4, (i & 3) * kGran + (lane & (kGran - 1)));
         const int key = (g.tile + i) * kTile + lane * kCellRows;
@@ -526,6 +546,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         for (int i = 0; ok && i < g.n; ++i, ++j) {
           const int sb = j % C::kSBufs;
           ok = wait_on(&kd_full[j & 1], (j >> 1) & 1, abort_flag, p.status);
+          if (ok && i == 0) ok = wait_on(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.status);
           if (ok && j >= C::kSBufs)
             ok = wait_on(&s_empty[sb], (j / C::kSBufs - 1) & 1, abort_flag, p.status);
           if (!ok) break;
@@ -549,32 +570,33 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       mbar_wait_drain(mdrain, 0, p.status);
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // ---------------- K to fp16: a thread expands its key's row ----------------
-    const int r = threadIdx.x;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    int j = 0, seg = 0;
-    for (; walk.next(p, &g); ++seg) {
+  } else if (warp >= kQuery) {
+    // ---------------- query rows of a unit, D / 8 lanes a row ----------------
+    constexpr int kPer = D / 8, kItems = NQ * kPer / 64, kLoads = kItems < 8 ? kItems : 8;
+    const int tid = threadIdx.x - 32 * kQuery;
+    for (int seg = 0; walk.next(p, &g); ++seg) {
       const int par = seg & 1;
-      if (seg >= 2) wait(&q_empty[par], ((seg >> 1) - 1) & 1);
-      {  // the unit's query rows, D / 8 lanes a row
-        constexpr int kPer = D / 8;
-        const int rows = min(p.tile_rows, g.T - g.t0) * G;
-        if (r == 0) {
-          Piece pc = {g.tile, g.n, g.nt,
-                      p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows, g.h};
-          piece[par] = pc;
-        }
-        uint8_t* qs = qbuf + par * C::kQBytes;
-        const float kx = p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h));
-#pragma unroll 2
-        for (int it = r; it < NQ * kPer; it += 128) {
-          const int q = it / kPer, pc = it % kPer, t = q / G;
-          const int row = (g.lo + g.t0 + t) * p.n_q_heads + g.h * G + q - t * G;
-          uint4 x = make_uint4(0, 0, 0, 0);
+      const int rows = min(p.tile_rows, g.T - g.t0) * G;
+      const int row0 = (g.lo + g.t0) * p.n_q_heads + g.h * G;
+      const float kx = p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h));
+      uint8_t* qs = qbuf + par * C::kQBytes;
+#pragma unroll 1
+      for (int it0 = 0; it0 < kItems; it0 += kLoads) {
+        uint4 x[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int q = ((it0 + u) * 64 + tid) / kPer, t = q / G;
+          x[u] = make_uint4(0, 0, 0, 0);
           if (q < rows)
-            x = *reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(row) * D + 8 * pc);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            x[u] = *reinterpret_cast<const uint4*>(
+                p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D +
+                8 * (tid % kPer));
+        }
+        if (it0 == 0 && seg >= 2) wait(&q_empty[par], ((seg >> 1) - 1) & 1);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int q = ((it0 + u) * 64 + tid) / kPer, pc = tid % kPer, t = q / G;
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
           uint32_t m = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -593,13 +615,26 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               make_uint4(y[0], y[1], y[2], y[3]);
           if (pc == 0) {
             col_sc[par * NQ + q] = kx * pow2(-ex);
-            col_row[par * NQ + q] = row;
+            col_row[par * NQ + q] = row0 + t * p.n_q_heads + q - t * G;
             col_vis[par * NQ + q] =
                 p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
           }
         }
-        fence_proxy_async_smem();
       }
+      if (tid == 0) {
+        Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows,
+                    g.h};
+        piece[par] = pc;
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&q_full[par]);
+    }
+  } else if (warp < 4) {
+    // ---------------- K to fp16: a thread expands its key's row ----------------
+    const int r = threadIdx.x;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    int j = 0;
+    while (walk.next(p, &g)) {
       for (int i = 0; i < g.n; ++i, ++j) {
         const int st = j % C::kStages;
         wait(&full[st], (j / C::kStages) & 1);
@@ -707,7 +742,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     float* nm = col_nm + col0;
     float* fac = col_f + col0;
-    const int total = static_cast<int>(start->left);
+    const int total = start->tiles;
     for (int j = 0, seg = 0; j < total; ++seg) {
       const int par = seg & 1;
       const float* sc = col_sc + par * NQ + col0;
@@ -933,11 +968,10 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
-  const int* meta = p.meta + 8 * c0;
-  const int c1 = meta[0];
+  const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * c0);
+  const int c1 = meta.x, row0 = meta.y, h = meta.w;
   const int q = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (c1 < 0 || q >= meta[2]) return;
-  const int row0 = meta[1], h = meta[3];
+  if (c1 < 0 || q >= meta.z) return;
   constexpr int kV = D / 32;
   float o[kV], L = 0.f, M = kNoMax;
 #pragma unroll
@@ -1005,7 +1039,7 @@ AttnLayout attn_layout(const dflash_kv4_dims& d) {
   a.ctas = current_num_sms();
   a.nq = query_columns(d);
   const size_t rows = 2 * static_cast<size_t>(a.ctas) * a.nq;
-  a.off_ml = (32 * static_cast<size_t>(a.ctas) + 255) / 256 * 256;
+  a.off_ml = (16 * static_cast<size_t>(a.ctas) + 255) / 256 * 256;
   a.off_o = a.off_ml + (8 * rows + 255) / 256 * 256;
   a.total = a.ctas > 0 ? a.off_o + 4 * rows * d.head_dim : 0;
   return a;
