@@ -52,10 +52,25 @@ template <int D, int NQ>
 struct Cfg {
   static constexpr int kCell = Cell<D>::kBytes;
   static constexpr int kStage = kGran * kCell;
-  static constexpr int kSoftWgs = NQ >= 32 ? 2 : 1;
+  // Warpgroups of each role.  A lane of the first three holds a key or a dim in TMEM, so
+  // a role grows by sharing out dims (K), cells (V^T) or query columns (softmax).  Few
+  // query rows leave the expansion of K and V as the longest step: two each then.
+  static constexpr int kKWgs = NQ <= 32 ? 2 : 1;
+  static constexpr int kVWgs = NQ <= 64 ? 2 : 1;
+  static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
-  static constexpr int kVWarps = D / 32;               // warps that hold rows of V^T
-  static constexpr int kThreads = 32 * (8 + 4 * kSoftWgs + 4);
+  static constexpr int kVWarps = D / 32;               // warps of it that hold rows of V^T
+  static constexpr int kV = 4 * kKWgs, kSoft = kV + 4 * kVWgs, kMisc = kSoft + 4 * kSoftWgs;
+  static constexpr int kThreads = 32 * (kMisc + 4);
+  // Registers: the launch's share, and what the roles make of it (0: left alone).  The
+  // softmax holds scores, sums and maxima of its columns.
+  static constexpr int kRegsSoft = NQ == 16 ? 0 : NQ == 128 ? 80 : 128;
+  static constexpr int kRegsRest = NQ == 128 ? 56 : 56;
+  static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+  static_assert(kRegsSoft * 128 * kSoftWgs + kRegsRest * (kThreads - 128 * kSoftWgs) <=
+                    kRegsLaunch * kThreads,
+                "register split");
+  static constexpr bool kKeep = NQ <= 64;              // scores and maxima in registers too
   // TMEM columns
   static constexpr int kKCols = D / 2, kVCols = kTile / 2;
   static constexpr int kSBufs = NQ <= 64 ? 2 : 1;
@@ -65,18 +80,25 @@ struct Cfg {
   static constexpr int kPBytes = (NQ + 63) / 64 * kTile * 128;
   static constexpr int kQBytes = NQ * D * 2;
   static constexpr int kVScale = kTile * (D / 16) * 2;  // fp16 scales of a V tile
+  static constexpr int kVGran = kGran / kVWgs;          // cells of a V warpgroup
   static constexpr int kFixed = 2 * kPBytes + 2 * kQBytes + 2 * kVScale;
   static constexpr int kTables = 12 * 1024;
   static constexpr int kFit = (226 * 1024 - kFixed - kTables) / kStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kSmem = 1024 + kFixed + kTables + kStages * kStage;
   static_assert(kStages >= 3, "shared memory");
+  // A tile's record is read up to softmax time, at most four tiles after its cells were let
+  // go: the copies of tile j wait for the cells of j - kStages, those for S of kStages + 2
+  // tiles back, and that for the softmax two further back.
+  static constexpr int kRing = 16;
+  static_assert(kRing >= kStages + 5, "tile records");
 };
 
 struct Kv4AttnParams {
   Kv4Store s;
   int batch, n_tokens, max_tokens, n_q_heads, group, causal;
   int tile_rows;             // rows of a sequence in one unit
+  int group_inv;             // ceil(2^16 / group): x * group_inv >> 16 = x / group, x < 128
   int paged, page_size, max_pages, limit;
   const int32_t* seq_len;
   const int32_t* start;
@@ -128,59 +150,137 @@ __device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const Seq&
   if (!p.causal) {
     n = static_cast<long long>(s.n_qt) * unit_tiles(s.len);
   } else {
+#pragma unroll 1
     for (int i = 0; i < s.n_qt; ++i) n += unit_tiles(unit_end(p, s, i));
   }
   return (n + static_cast<long long>(s.n_qt) * kUnitCost) * p.s.n_kv_heads;
 }
 
-struct Start {
-  long long left;            // cost of this CTA's run
-  Seq s;                     // sequence of its first unit
-  int b, qt, h;
-  long long off;             // cost of that unit before the run
-  int tiles;                 // of the run
-};
-
 // One segment: consecutive tiles of one unit.
 struct Seg {
   int b, h, t0, lo, T, len, end, tile, n, nt;
+  int final;                 // the last of the CTA
 };
+
+// A tile, as the warps that work on it read it.
+struct Tile {
+  int left;                  // keys in use from its first one on
+  int flags;                 // of its segment: the first, the last; the last of the CTA
+};
+constexpr int kFirst = 1, kLast = 2, kFinal = 4;
 
 // What the softmax needs of a segment, left in shared memory beside its query rows.
 struct Piece {
   int tile, n, nt, sure, rows, h;   // sure: keys that every row sees
+  float scale;                      // log2 units per score
 };
 
+// The run of this CTA, by one warp.  With W the cost of all units, every CTA takes W / n
+// (the first W % n one more), n = min(CTAs, W).
 struct Walk {
-  long long left, off;
+  int left, off;             // cost left, and of the unit at hand before that
   int b, qt, h, end, nt;
   Seq s;
-  __device__ __forceinline__ Walk(const Kv4AttnParams& p, const Start& st)
-      : left(st.left), off(st.off), b(st.b), qt(st.qt), h(st.h), s(st.s) {
+  int per, rem, here;        // shares; where the run stands among all costs
+
+  __device__ __forceinline__ void unit(const Kv4AttnParams& p) {
     end = unit_end(p, s, qt);
     nt = unit_tiles(end);
   }
+  __device__ __forceinline__ int owner(int pos) const {
+    const int big = rem * (per + 1);
+    return pos < big ? pos / (per + 1) : rem + (pos - big) / per;
+  }
+
+  __device__ __forceinline__ explicit Walk(const Kv4AttnParams& p)
+      : left(0), off(0), b(0), qt(0), h(0), end(0), nt(0), per(0), rem(0), here(0) {
+    const int lane = lane_id();
+    long long all = 0, mine = 0;
+    Seq t = {0, 0, 0, 0};    // of sequence `lane` of a group of 32
+    bool bad = false;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      mine = 0;
+      if (b0 + lane < p.batch) {
+        t = load_seq(p, b0 + lane, &bad);
+        mine = seq_cost(p, t);
+      }
+      all += mine;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (all > INT32_MAX) bad = true;
+    if (bad && blockIdx.x == 0) set_status(p.status, DFLASH_ST_CAPACITY);
+    if (all > INT32_MAX) return;
+    const int W = static_cast<int>(all), n = min(static_cast<int>(gridDim.x), W);
+    const int c = blockIdx.x;
+    if (c >= n) return;
+    per = W / n;
+    rem = W - per * n;
+    here = c * per + min(c, rem);
+    left = per + (c < rem ? 1 : 0);
+    int before = 0;
+#pragma unroll 1
+    for (int b0 = 0;; b0 += 32) {
+      if (p.batch > 32) {
+        mine = 0;
+        if (b0 + lane < p.batch) {
+          t = load_seq(p, b0 + lane);
+          mine = seq_cost(p, t);
+        }
+      }
+      int inc = static_cast<int>(mine);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > here);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        b = b0 + l;
+        s.lo = __shfl_sync(0xffffffffu, t.lo, l);
+        s.T = __shfl_sync(0xffffffffu, t.T, l);
+        s.len = __shfl_sync(0xffffffffu, t.len, l);
+        s.n_qt = __shfl_sync(0xffffffffu, t.n_qt, l);
+        before += __shfl_sync(0xffffffffu, inc - static_cast<int>(mine), l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    off = here - before;
+    unit(p);
+#pragma unroll 1
+    while (off >= (nt + kUnitCost) * p.s.n_kv_heads) {
+      off -= (nt + kUnitCost) * p.s.n_kv_heads;
+      ++qt;
+      unit(p);
+    }
+    h = off / (nt + kUnitCost);
+    off -= h * (nt + kUnitCost);
+  }
+
   __device__ __forceinline__ bool next(const Kv4AttnParams& p, Seg* g) {
+#pragma unroll 1
     while (left > 0) {
       if (off == nt + kUnitCost) {        // the unit after this one
         off = 0;
         if (++h == p.s.n_kv_heads) {
           h = 0;
           ++qt;
+#pragma unroll 1
           while (qt >= s.n_qt) {
             qt = 0;
-            if (++b >= p.batch) return false;
-            s = load_seq(p, b);
+            s = load_seq(p, ++b);
           }
-          end = unit_end(p, s, qt);
-          nt = unit_tiles(end);
+          unit(p);
         }
       }
-      const int o = static_cast<int>(off);
-      const int take = static_cast<int>(min(left, static_cast<long long>(nt + kUnitCost - o)));
+      const int take = min(left, nt + kUnitCost - off);
+      const int from = max(0, off - kUnitCost), to = off + take - kUnitCost;
       off += take;
       left -= take;
-      const int from = max(0, o - kUnitCost), to = o + take - kUnitCost;
+      here += take;
       if (to <= from) continue;
       g->b = b;
       g->h = h;
@@ -197,88 +297,6 @@ struct Walk {
     return false;
   }
 };
-
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// By one warp.  CTA c of n takes [W c / n, W (c + 1) / n) of the cost W of all units.
-__device__ void make_start(const Kv4AttnParams& p, Start* out) {
-  const int lane = lane_id();
-  long long all = 0, mine = 0;
-  Seq s = {0, 0, 0, 0};      // of sequence `lane` of a group of 32
-  bool bad = false;
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    if (b0 + lane < p.batch) s = load_seq(p, b0 + lane, &bad);
-    mine = b0 + lane < p.batch ? seq_cost(p, s) : 0;
-    all += mine;
-  }
-  if (bad && blockIdx.x == 0) set_status(p.status, DFLASH_ST_CAPACITY);
-  const long long W = warp_sum(all);
-  const long long n = min(static_cast<long long>(gridDim.x), W), c = blockIdx.x;
-  Start st = {};
-  long long first = 0;
-  if (c < n) {
-    first = W * c / n;
-    st.left = W * (c + 1) / n - first;
-  }
-  if (st.left > 0) {
-    long long before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      if (p.batch > 32) {
-        if (b0 + lane < p.batch) s = load_seq(p, b0 + lane);
-        mine = b0 + lane < p.batch ? seq_cost(p, s) : 0;
-      }
-      long long inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > first);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        st.b = b0 + l;
-        st.s.lo = __shfl_sync(0xffffffffu, s.lo, l);
-        st.s.T = __shfl_sync(0xffffffffu, s.T, l);
-        st.s.len = __shfl_sync(0xffffffffu, s.len, l);
-        st.s.n_qt = __shfl_sync(0xffffffffu, s.n_qt, l);
-        before += __shfl_sync(0xffffffffu, inc - mine, l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    long long rem = first - before;
-    int cost = unit_tiles(unit_end(p, st.s, 0)) + kUnitCost;
-    while (rem >= static_cast<long long>(cost) * p.s.n_kv_heads) {
-      rem -= static_cast<long long>(cost) * p.s.n_kv_heads;
-      cost = unit_tiles(unit_end(p, st.s, ++st.qt)) + kUnitCost;
-    }
-    st.h = static_cast<int>(rem / cost);
-    st.off = rem - static_cast<long long>(st.h) * cost;
-  }
-  // the segments once over: their tiles, and the unit that is left unfinished
-  int meta[4] = {-1, 0, 0, 0};
-  Seg g = {};
-  Walk w(p, st);
-  while (w.next(p, &g)) {
-    st.tiles += g.n;
-    if (g.tile == 0 && g.n < g.nt) {   // its last tile ends where the run does plus the rest
-      const long long end = first + st.left + (g.nt - g.n);
-      meta[0] = static_cast<int>((end * n - 1) / W);
-      meta[1] = g.lo + g.t0;
-      meta[2] = min(p.tile_rows, g.T - g.t0) * p.group;
-      meta[3] = g.h;
-    }
-  }
-  if (lane == 0) {
-    *out = st;
-    *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) =
-        make_int4(meta[0], meta[1], meta[2], meta[3]);
-  }
-}
 
 // ----------------------------------------------------------------------------
 // small device pieces
@@ -337,6 +355,16 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
       : "memory");
 }
 
+// Registers per thread of this warpgroup from here on.
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -364,21 +392,28 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// A wait of a role that goes on regardless: once one gave up, the rest are skipped, so
-// every role still runs its loops to their end (named barriers included).
-// (The loop is kept out of line: five roles share the instruction cache.  Reading the
-// global timer takes longer than most waits, so the bounded wait comes after some tries.)
-__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                       uint32_t* status) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort_flag, status);
-}
-
+// A wait of a warp; once one gave up the rest are skipped.  Warps that meet at named
+// barriers vote there on who gave up, and leave their loops together.
+// The bounded wait of this kernel: the timer, slower to read than most waits take, is
+// looked at every 64 tries only, and the loop is small (five roles share the instruction
+// cache; a call would rule out the register split).
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                         uint32_t* status) {
-  return mbar_try_wait(bar, parity) || slow_wait(bar, parity, abort_flag, status);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (n % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (n == 64) t0 = now;
+      if (*abort_flag) return false;
+      if (now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        set_status(status, DFLASH_ST_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
 }
 
 struct Waiter {
@@ -387,7 +422,7 @@ struct Waiter {
   bool dead;
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !wait_on(bar, parity, abort_flag, status);
-    __syncwarp();
+    dead = __any_sync(0xffffffffu, dead);
   }
 };
 
@@ -410,14 +445,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint8_t* vscale = qbuf + 2 * C::kQBytes;
   uint8_t* stages = vscale + 2 * C::kVScale;
   uint8_t* tables = stages + C::kStages * C::kStage;
-  float* col_sc = reinterpret_cast<float*>(tables);        // [2][NQ] log2 units per score
-  int* col_vis = reinterpret_cast<int*>(col_sc + 2 * NQ);  // [2][NQ] keys a column sees
+  int* col_vis = reinterpret_cast<int*>(tables);           // [2][NQ] keys a column sees
   int* col_row = col_vis + 2 * NQ;                         // [2][NQ] row of q and out
   float* col_nm = reinterpret_cast<float*>(col_row + 2 * NQ);  // [NQ] kLift - running maximum
   float* col_f = col_nm + NQ;                              // [NQ] rescale factor, then 1 / sum
   float* red = col_f + NQ;                                 // [4][NQ]
   Piece* piece = reinterpret_cast<Piece*>(red + 4 * NQ);   // [2]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(piece + 2);
+  Seg* segs = reinterpret_cast<Seg*>(piece + 2);           // [2] for the query rows
+  Tile* tiles = reinterpret_cast<Tile*>(segs + 2);         // [kRing]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + C::kRing);
   uint64_t* full = bars;
   uint64_t* empty = full + C::kStages;
   uint64_t* kd_full = empty + C::kStages;  // [2] K tile in TMEM
@@ -430,30 +466,39 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint64_t* q_full = pv_done + 2;          // [2] query rows and tables of a segment
   uint64_t* q_empty = q_full + 2;          // [2] read
   uint64_t* o_empty = q_empty + 2;         // O of a segment read
-  uint64_t* mdrain = o_empty + 1;
-  Start* start = reinterpret_cast<Start*>(mdrain + 1);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 1);
+  uint64_t* seg_full = o_empty + 1;        // [2] segs
+  uint64_t* seg_empty = seg_full + 2;      // [2]
+  uint64_t* planned = seg_empty + 2;       // *any is there
+  uint64_t* mdrain = planned + 1;
+  uint32_t* q_max = reinterpret_cast<uint32_t*>(mdrain + 1);   // [2]
+  uint32_t* tmem_slot = q_max + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* any = abort_flag + 1;      // this CTA has tiles
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducer = 8 + 4 * C::kSoftWgs, kMma = kProducer + 1, kQuery = kMma + 1;
+  constexpr int kProducer = C::kMisc, kMma = kProducer + 1, kQuery = kMma + 1;
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4 + C::kVWarps);
+      mbar_init(&empty[i], 4 * C::kKWgs + C::kVWarps * C::kVWgs);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kd_full[i], 4);
+      mbar_init(&kd_full[i], 4 * C::kKWgs);
       mbar_init(&kd_empty[i], 1);
-      mbar_init(&vd_full[i], C::kVWarps);
+      mbar_init(&vd_full[i], C::kVWarps * C::kVWgs);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4 * C::kSoftWgs);
       mbar_init(&p_full[i], 4 * C::kSoftWgs);
       mbar_init(&pv_done[i], 1);
       mbar_init(&q_full[i], 2);
       mbar_init(&q_empty[i], 4 * C::kSoftWgs);
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 2);
     }
     mbar_init(o_empty, 4 * C::kSoftWgs);
+    mbar_init(planned, 1);
     mbar_init(mdrain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -462,49 +507,71 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  griddep_wait();
-  if (warp == kProducer) make_start(p, start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_launch_dependents();
-  constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
-  const int G = p.group;
-  Walk walk(p, *start);
-  Seg g;
+  if (C::kRegsSoft && (warp < C::kSoft || warp >= C::kMisc)) regs_down<C::kRegsRest>();
+  griddep_wait();
   Waiter wait{abort_flag, p.status, false};
+  const int G = p.group;
+  constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
 
   if (warp == kProducer) {
-    // ---------------- cells of a tile, one bulk copy each ----------------
+    // ---------------- the run, and the cells of its tiles, one bulk copy each ----------------
+    Walk walk(p);
+    Seg g = {}, after = {};
+    bool more = walk.next(p, &g);
+    if (lane == 0) {
+      *any = more;
+      *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(-1, 0, 0, 0);
+    }
+    warp_arrive(planned);
+    griddep_launch_dependents();
     // (a cache that several units of a sequence read stays in L2)
     const uint64_t pol =
         p.max_tokens > p.tile_rows ? l2_policy_evict_normal() : l2_policy_evict_first();
+    const int per_slab = p.s.slab_rows / kCellRows;
+    // lane: cell `lane` of the four tiles from `tile` on (negative: no such page)
+    auto cells_at = [&](int tile) {
+      const int key16 = tile * kGran + lane;
+      int slab = g.b, row16 = key16;
+      if (p.paged) {
+        const int page = key16 / per_slab;
+        row16 = key16 - page * per_slab;
+        slab = -1;
+        if (key16 * kCellRows < g.end)
+          slab = p.page_table[static_cast<size_t>(g.b) * p.max_pages + page];
+        if (slab < 0 || slab >= p.s.n_slabs) return -1;
+      }
+      return (slab * p.s.n_kv_heads + g.h) * per_slab + row16;
+    };
     int j = 0;
     bool go = true;
-    // lane: page of cell `lane` of the four tiles from `tile` on
-    auto pages = [&](int tile) {
-      const int key = tile * kTile + lane * kCellRows;
-      int slab = g.b;
-      if (p.paged && key < g.end) {
-        slab = p.page_table[static_cast<size_t>(g.b) * p.max_pages + key / p.page_size];
-        if (slab >= p.s.n_slabs) slab = -1;
-      }
-      return slab;
-    };
-    while (go && walk.next(p, &g)) {
-      int slab4 = 0, ahead = pages(g.tile);
+#pragma unroll 1
+    for (int seg = 0; go && more; ++seg) {
+      if (g.tile == 0 && g.n < g.nt && lane == 0)     // the rest of this unit is others'
+        *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) =
+            make_int4(walk.owner(walk.here + g.nt - g.n - 1), g.lo + g.t0,
+                      min(p.tile_rows, g.T - g.t0) * G, g.h);
+      more = walk.next(p, &after);
+      g.final = !more;
+      if (seg >= 2) go = wait_on(&seg_empty[seg & 1], ((seg >> 1) - 1) & 1, abort_flag, p.status);
+      if (lane == 0) segs[seg & 1] = g;
+      warp_arrive(&seg_full[seg & 1]);
+      int cell4 = 0, ahead = cells_at(g.tile);
+#pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++j) {
         const int st = j % C::kStages;
         if ((i & 3) == 0) {
-          slab4 = ahead;
-          ahead = pages(g.tile + i + 4);
+          cell4 = ahead;
+          ahead = cells_at(g.tile + i + 4);
         }
-        const int slab = __shfl_sync(0xffffffffu, slab4, (i & 3) * kGran + (lane & (kGran - 1)));
-        const int key = (g.tile + i) * kTile + lane * kCellRows;
-        const bool use = lane < kGran && key < g.end;
-        const uint32_t have = __ballot_sync(0xffffffffu, use && slab >= 0);
-        const uint32_t miss = __ballot_sync(0xffffffffu, use && slab < 0);
-        if (!wait_on(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status)) go = false;
+        const int left = g.end - (g.tile + i) * kTile;
+        const int cell = __shfl_sync(0xffffffffu, cell4, (i & 3) * kGran + (lane & (kGran - 1)));
+        const bool use = lane < kGran && lane * kCellRows < left;
+        const uint32_t have = __ballot_sync(0xffffffffu, use && cell >= 0);
+        const uint32_t miss = __ballot_sync(0xffffffffu, use && cell < 0);
+        go = go && wait_on(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status);
         if (!__all_sync(0xffffffffu, go)) {
           go = false;
           break;
@@ -512,27 +579,37 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         uint8_t* dst = stages + st * C::kStage;
         if (miss) {                                 // pages that are missing read as zeros
           if (lane == 0) set_status(p.status, DFLASH_ST_PAGE_MISSING);
-          for (int c = 0; c < kGran; ++c)
-            if (miss >> c & 1)
-              for (int o = lane * 16; o < C::kCell; o += 512)
-                *reinterpret_cast<uint4*>(dst + c * C::kCell + o) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+          for (int o = lane * 16; o < C::kStage; o += 512)
+            if (miss >> (o / C::kCell) & 1)
+              *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], __popc(have) * C::kCell);
-        __syncwarp();
-        if (have >> lane & 1) {
-          const int row = p.paged ? key % p.page_size : key;
-          bulk_load(dst + lane * C::kCell, p.s.cells + cell_index(p.s, slab, g.h, row) * C::kCell,
-                    C::kCell, &full[st], pol);
+        if (lane == 0) {
+          Tile t = {left, (i == 0 ? kFirst : 0) |
+                              (i + 1 == g.n ? kLast | (more ? 0 : kFinal) : 0)};
+          tiles[j % C::kRing] = t;
+          mbar_arrive_expect_tx(&full[st], __popc(have) * C::kCell);
         }
+        __syncwarp();
+        if (have >> lane & 1)
+          bulk_load(dst + lane * C::kCell, p.s.cells + static_cast<size_t>(cell) * C::kCell,
+                    C::kCell, &full[st], pol);
       }
+      g = after;
     }
     // no copy may still be landing when the CTA exits
+#pragma unroll 1
     for (int st = 0; st < C::kStages && st < j; ++st) {
       const int last = st + (j - 1 - st) / C::kStages * C::kStages;
       mbar_wait_drain(&full[st], (last / C::kStages) & 1, p.status);
     }
-  } else if (warp == kMma) {
+    goto done;
+  }
+  wait(planned, 0);
+  griddep_launch_dependents();
+  if (wait.dead || *any == 0) goto done;
+  if (warp == kMma) {
     // ---------------- the products ----------------
     // The whole warp runs the loop and one elected lane issues, so that the operands stay
     // in uniform registers: 23 clocks an instruction, against 46 when one lane runs alone.
@@ -545,6 +622,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       ok = __all_sync(0xffffffffu, ok && wait_on(bar, parity, abort_flag, p.status));
     };
     auto issue_pv = [&](int j, bool first, int seg) {
+      if (!ok) return;
       need(&p_full[j & 1], (j >> 1) & 1);
       need(&vd_full[j & 1], (j >> 1) & 1);
       if (first && seg > 0) need(o_empty, (seg - 1) & 1);
@@ -559,118 +637,149 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         umma_commit(&pv_done[par]);
       }
     };
-    int j = 0, seg = 0, last_seg = 0;
-    bool last_first = false;
-    while (ok && walk.next(p, &g)) {
-      for (int i = 0; ok && i < g.n; ++i, ++j) {
-        const uint32_t sb = j % C::kSBufs, par = j & 1, qpar = seg & 1;
-        need(&kd_full[par], (j >> 1) & 1);
-        if (i == 0) need(&q_full[qpar], (seg >> 1) & 1);
-        if (j >= C::kSBufs) need(&s_empty[sb], (j / C::kSBufs - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
+    int seg = -1, flags = 0;
+#pragma unroll 1
+    for (int j = 0;; ++j) {
+      const uint32_t sb = j % C::kSBufs, par = j & 1;
+      const int was = flags;
+      need(&kd_full[par], (j >> 1) & 1);
+      if (!ok) break;
+      flags = tiles[j % C::kRing].flags;
+      const int qs = seg + (flags & kFirst);
+      if (flags & kFirst) need(&q_full[qs & 1], (qs >> 1) & 1);
+      if (j >= C::kSBufs) need(&s_empty[sb], (j / C::kSBufs - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t q0 = q_desc + ((qs & 1) * C::kQBytes >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_f16_ts(C::kS0 + sb * NQ, par * C::kKCols + ks * 8,
-                        q_desc + ((qpar * C::kQBytes + (ks >> 2) * NQ * 128 + (ks & 3) * 32) >> 4),
-                        idesc_s, ks > 0);
-          umma_commit(&s_full[sb]);
-          umma_commit(&kd_empty[par]);
-        }
-        if (j > 0) issue_pv(j - 1, last_first, last_seg);
-        last_first = i == 0;
-        last_seg = seg;
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_f16_ts(C::kS0 + sb * NQ, par * C::kKCols + ks * 8,
+                      q0 + (((ks >> 2) * NQ * 128 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+        umma_commit(&s_full[sb]);
+        umma_commit(&kd_empty[par]);
       }
-      ++seg;
+      if (j > 0) issue_pv(j - 1, was & kFirst, seg);
+      seg = qs;
+      if (flags & kFinal) {
+        issue_pv(j, flags & kFirst, seg);
+        break;
+      }
     }
-    if (ok && j > 0) issue_pv(j - 1, last_first, last_seg);
     if (elect_one()) umma_commit(mdrain);
     if (lane == 0) mbar_wait_drain(mdrain, 0, p.status);
     __syncwarp();
   } else if (warp >= kQuery) {
     // ---------------- query rows of a unit, D / 8 lanes a row ----------------
+    // Twice over them: for the largest finite magnitude of all, which goes to [2^14, 2^15),
+    // and to convert.
     constexpr int kPer = D / 8, kItems = NQ * kPer / 64, kLoads = kItems < 8 ? kItems : 8;
     const int tid = threadIdx.x - 32 * kQuery;
-    for (int seg = 0; walk.next(p, &g); ++seg) {
+    const int pc = tid % kPer;
+    bool go = true;
+#pragma unroll 1
+    for (int seg = 0; go; ++seg) {
       const int par = seg & 1;
+      wait(&seg_full[par], (seg >> 1) & 1);
+      if (bar_or(15, 64, wait.dead)) break;                      // (and q_max is read)
+      const Seg g = segs[par];
+      go = !g.final;
+      warp_arrive(&seg_empty[par]);
       const int rows = min(p.tile_rows, g.T - g.t0) * G;
       const int row0 = (g.lo + g.t0) * p.n_q_heads + g.h * G;
-      const float kx = p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h));
       uint8_t* qs = qbuf + par * C::kQBytes;
+      uint32_t m = 0;
+      float f = 0.f;
 #pragma unroll 1
-      for (int it0 = 0; it0 < kItems; it0 += kLoads) {
+      for (int it0 = 0; it0 < 2 * kItems; it0 += kLoads) {
+        const bool second = it0 >= kItems;
+        if (it0 == kItems) {
+#pragma unroll
+          for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) q_max[warp - kQuery] = m;
+          if (seg >= 2) wait(&q_empty[par], ((seg >> 1) - 1) & 1);
+          named_bar_sync(15, 64);
+          m = max(q_max[0], q_max[1]);
+          const int ex = max(-126, min(126, 141 - static_cast<int>(m >> 7)));
+          f = pow2(ex);
+          if (tid == 0) {
+            Piece pc = {g.tile, g.n, g.nt,
+                        p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows, g.h,
+                        p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h)) * pow2(-ex)};
+            piece[par] = pc;
+          }
+        }
         uint4 x[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-          const int q = ((it0 + u) * 64 + tid) / kPer, t = q / G;
+          const int q = ((it0 - (second ? kItems : 0) + u) * 64 + tid) / kPer;
+          const int t = q * p.group_inv >> 16;                     // q / G
           x[u] = make_uint4(0, 0, 0, 0);
           if (q < rows)
             x[u] = *reinterpret_cast<const uint4*>(
-                p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D +
-                8 * (tid % kPer));
+                p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D + 8 * pc);
         }
-        if (it0 == 0 && seg >= 2) wait(&q_empty[par], ((seg >> 1) - 1) & 1);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-          const int q = ((it0 + u) * 64 + tid) / kPer, pc = tid % kPer, t = q / G;
           const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          uint32_t m = 0;
+          if (!second) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            m = max(m, max(w[e] & 0x7FFFu, w[e] >> 16 & 0x7FFFu));
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t a = w[e] & 0x7FFFu, c = w[e] >> 16 & 0x7FFFu;
+              m = max(m, max(a < 0x7F80u ? a : 0u, c < 0x7F80u ? c : 0u));
+            }
+          } else {
+            const int q = ((it0 - kItems + u) * 64 + tid) / kPer;
+            uint32_t y[4];
 #pragma unroll
-          for (int o = kPer / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const int ex = max(-126, min(126, 127 - static_cast<int>(m >> 7)));
-          const float f = pow2(ex);
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            y[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
-                            __uint_as_float(w[e] & 0xFFFF0000u) * f);
-          *reinterpret_cast<uint4*>(qs + (pc >> 3) * NQ * 128 + q * 128 +
-                                    (((pc & 7) ^ (q & 7)) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
-          if (pc == 0) {
-            col_sc[par * NQ + q] = kx * pow2(-ex);
-            col_row[par * NQ + q] = row0 + t * p.n_q_heads + q - t * G;
-            col_vis[par * NQ + q] =
-                p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
+                              __uint_as_float(w[e] & 0xFFFF0000u) * f);
+            *reinterpret_cast<uint4*>(qs + (pc >> 3) * NQ * 128 + q * 128 +
+                                      (((pc & 7) ^ (q & 7)) << 4)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+            if (pc == 0) {
+              const int t = q * p.group_inv >> 16;
+              col_row[par * NQ + q] = row0 + t * p.n_q_heads + q - t * G;
+              col_vis[par * NQ + q] =
+                  p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
+            }
           }
         }
-      }
-      if (tid == 0) {
-        Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows,
-                    g.h};
-        piece[par] = pc;
       }
       fence_proxy_async_smem();
       warp_arrive(&q_full[par]);
     }
-  } else if (warp < 4) {
+  } else if (warp < C::kV) {
     // ---------------- K to fp16: a thread expands its key's row ----------------
-    const int r = threadIdx.x;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    int j = 0;
-    while (walk.next(p, &g)) {
-      for (int i = 0; i < g.n; ++i, ++j) {
+    const int r = threadIdx.x & 127, wg = warp >> 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    bool go = true;
+    {
+#pragma unroll 1
+      for (int j = 0; go; ++j) {
         const int st = j % C::kStages;
         wait(&full[st], (j / C::kStages) & 1);
+        go = !(tiles[j % C::kRing].flags & kFinal) && !wait.dead;
         if (j >= 2) wait(&kd_empty[j & 1], ((j >> 1) - 1) & 1);
         tc_fence_after();
         const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
         const int rr = r % kCellRows;
+        // 64 dims a round (D = 64 with two warpgroups: 32 each)
+        constexpr int kParts = D / 32 / C::kKWgs, kC = kParts < 2 ? 1 : 2;
 #pragma unroll 1
-        for (int c2 = 0; c2 < D / 64; ++c2) {          // 64 dims a round
-          const uint4 wa = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 4 * c2));
-          const uint4 wb = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 4 * c2 + 2));
-          const uint32_t sc = *reinterpret_cast<const uint32_t*>(cell + Cell<D>::k_scale(rr, 4 * c2));
+        for (int c2 = 0; c2 < kParts / kC; ++c2) {
+          const int c0 = wg * kParts + c2 * kC;        // first 32 dims
+          uint4 w[kC];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t s2 = e4m3x2_to_f16x2(c ? sc >> 16 : sc);
+          for (int c = 0; c < kC; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * (c0 + c)));
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            const uint32_t s2 = e4m3x2_to_f16x2(
+                *reinterpret_cast<const uint16_t*>(cell + Cell<D>::k_scale(rr, 2 * (c0 + c))));
             const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
-            const uint32_t u[4] = {c ? wb.x : wa.x, c ? wb.y : wa.y, c ? wb.z : wa.z,
-                                   c ? wb.w : wa.w};
+            const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
             uint32_t o[16];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -679,7 +788,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll
               for (int x = 0; x < 4; ++x) o[4 * e + x] = hmul2(f[x], e < 2 ? s_lo : s_hi);
             }
-            tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + c2 * 32 + c * 16, o);
+            tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + (c0 + c) * 16, o);
           }
         }
         warp_arrive(&empty[st]);
@@ -688,38 +797,50 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         warp_arrive(&kd_full[j & 1]);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < C::kSoft) {
     // ---------------- V^T to fp16: a thread expands its dim's row ----------------
     // The 16 threads of a group of dims share their scales, so each scale is turned to
     // fp16 once, by all threads together, and read back.
-    if (warp - 4 < C::kVWarps) {
+    if ((warp & 3) < C::kVWarps) {
       constexpr int kN = 32 * C::kVWarps;
-      const int d = threadIdx.x - 128;
-      const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp - 4) * 32) << 16) + C::kV0;
+      const int d = threadIdx.x & 127, wg = (warp - C::kV) >> 2, g0 = wg * C::kVGran;
+      const uint32_t lane_base =
+          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kV0 + g0 * 8;
       const int shift = 4 * (d & 1);
-      int j = 0;
-      while (walk.next(p, &g)) {
-        for (int i = 0; i < g.n; ++i, ++j) {
+      bool go = true;
+      {
+#pragma unroll 1
+        for (int j = 0; go; ++j) {
           const int st = j % C::kStages;
           wait(&full[st], (j / C::kStages) & 1);
-          const uint8_t* base = stages + st * C::kStage;
-          uint8_t* vsc = vscale + (j & 1) * C::kVScale;
-          {  // 8 scales a thread: half the rows of a cell, one group of dims
-            const int c = d / (D / 8), x = d % (D / 8);
-            const uint2 s8 = *reinterpret_cast<const uint2*>(base + c * C::kCell +
-                                                             Cell<D>::v_scale(0, 0) + x * 8);
-            *reinterpret_cast<uint4*>(vsc + d * 16) =
-                make_uint4(e4m3x2_to_f16x2(s8.x), e4m3x2_to_f16x2(s8.x >> 16),
-                           e4m3x2_to_f16x2(s8.y), e4m3x2_to_f16x2(s8.y >> 16));
+          const Tile t = tiles[j % C::kRing];
+          go = !(t.flags & kFinal);
+          const uint8_t* base = stages + st * C::kStage + g0 * C::kCell;
+          uint8_t* vsc = vscale + (j & 1) * C::kVScale + wg * (C::kVScale / C::kVWgs);
+          {  // kVGran scales a thread
+            constexpr int kT = D / C::kVGran;                  // threads a cell
+            const uint8_t* src = base + d / kT * C::kCell + Cell<D>::v_scale(0, 0) +
+                                 d % kT * C::kVGran;
+            if (C::kVGran == 8) {
+              const uint2 s8 = *reinterpret_cast<const uint2*>(src);
+              *reinterpret_cast<uint4*>(vsc + d * 16) =
+                  make_uint4(e4m3x2_to_f16x2(s8.x), e4m3x2_to_f16x2(s8.x >> 16),
+                             e4m3x2_to_f16x2(s8.y), e4m3x2_to_f16x2(s8.y >> 16));
+            } else {
+              const uint32_t s4 = *reinterpret_cast<const uint32_t*>(src);
+              *reinterpret_cast<uint2*>(vsc + d * 8) =
+                  make_uint2(e4m3x2_to_f16x2(s4), e4m3x2_to_f16x2(s4 >> 16));
+            }
           }
           if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);
           tc_fence_after();
-          named_bar_sync(3, kN);
-          const int left = g.end - (g.tile + i) * kTile;     // keys in use from here on
+          if (bar_or(8 + wg, kN, wait.dead)) break;            // the scales are there
+          // keys in use from this warpgroup's first cell on
+          const int left = t.left - g0 * kCellRows;
           const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
           const uint4* scl = reinterpret_cast<const uint4*>(vsc + d / 16 * 32);
 #pragma unroll 2
-          for (int c = 0; c < kGran; ++c) {
+          for (int c = 0; c < C::kVGran; ++c) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
             const uint4 sa = scl[c * (D / 8)], sb = scl[c * (D / 8) + 1];
             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -728,8 +849,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               // this dim's nibbles of four keys, two to a byte
-              const uint32_t u = w[e] >> shift;
-              const uint32_t x = (u & 0x000F000Fu) | (u >> 4 & 0x00F000F0u);
+              // (only bytes 0 and 2 of x are used)
+              const uint32_t a = w[e] >> shift, b = w[e] >> (shift + 4);
+              const uint32_t x = (a & 0x000F000Fu) | (b & ~0x000F000Fu);
               o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), s[2 * e]);
               o[2 * e + 1] = hmul2(e2m1x2_to_f16x2<2>(x), s[2 * e + 1]);
             }
@@ -752,26 +874,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     }
   } else {
     // ---------------- softmax: a thread owns a key ----------------
+    if (C::kRegsSoft) regs_up<C::kRegsSoft ? C::kRegsSoft : 24>();
     constexpr int CW = C::kCols;
-    constexpr bool kKeep = CW <= 32;       // the tile's scores stay in registers
-    const int wg = (warp - 8) >> 2, q4 = warp & 3;
+    constexpr bool kKeep = C::kKeep;
+    const int wg = (warp - C::kSoft) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, col0 = wg * CW;
     const uint32_t bar = 1 + wg;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     float* nm = col_nm + col0;
     float* fac = col_f + col0;
-    const int total = start->tiles;
-    for (int j = 0, seg = 0; j < total; ++seg) {
+    int j = 0;
+    bool go = true;
+#pragma unroll 1
+    for (int seg = 0; go; ++seg) {
       const int par = seg & 1;
-      const float* sc = col_sc + par * NQ + col0;
       const int* vis = col_vis + par * NQ + col0;
       wait(&s_full[j % C::kSBufs], (j / C::kSBufs) & 1);     // the segment's tables are there
+      if (bar_or(bar, 128, wait.dead)) break;
       const int n = piece[par].n, tile0 = piece[par].tile, sure = piece[par].sure;
-      float2 l[CW / 2];
+      const float scale = piece[par].scale;
+      float2 l[CW / 2], mr[kKeep ? CW / 2 : 1];        // sums; kLift - maxima
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) l[c] = make_float2(0.f, 0.f);
-      if (r < CW) nm[r] = kLift - kNoMax;
-      named_bar_sync(bar, 128);
+#pragma unroll 1
       for (int i = 0; i < n; ++i, ++j) {
         const int sb = j % C::kSBufs;
         const uint32_t s_addr = lane_base + C::kS0 + sb * NQ + col0;
@@ -779,22 +904,30 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const bool masked = (tile0 + i + 1) * kTile > sure;
         wait(&s_full[sb], (j / C::kSBufs) & 1);
         tc_fence_after();
-        // 16 columns of S times their scale, minus the running maximum
-        auto scores = [&](const uint32_t (&v)[16], int c0, float* x) {
+        // 16 columns of this key's scores in log2 units, minus the running maxima if `sub`
+        auto scores = [&](const uint32_t (&v)[16], int c0, bool sub, float* x) {
+          const float2 s2 = make_float2(scale, scale);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(sc + c0 + e);
-            const float4 b = *reinterpret_cast<const float4*>(nm + c0 + e);
-            const float2 lo = __ffma2_rn(
-                make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                make_float2(a.x, a.y), make_float2(b.x, b.y));
-            const float2 hi = __ffma2_rn(
-                make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                make_float2(a.z, a.w), make_float2(b.z, b.w));
-            x[e] = lo.x;
-            x[e + 1] = lo.y;
-            x[e + 2] = hi.x;
-            x[e + 3] = hi.y;
+            float2 m0 = make_float2(0.f, 0.f), m1 = m0;
+            if (sub) {
+              if (kKeep) {
+                m0 = mr[kKeep ? (c0 + e) / 2 : 0];
+                m1 = mr[kKeep ? (c0 + e) / 2 + 1 : 0];
+              } else {
+                const float4 m = *reinterpret_cast<const float4*>(nm + c0 + e);
+                m0 = make_float2(m.x, m.y);
+                m1 = make_float2(m.z, m.w);
+              }
+            }
+            const float2 a = __ffma2_rn(
+                make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), s2, m0);
+            const float2 b = __ffma2_rn(
+                make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), s2, m1);
+            x[e] = a.x;
+            x[e + 1] = a.y;
+            x[e + 2] = b.x;
+            x[e + 3] = b.y;
           }
           if (masked) {
 #pragma unroll
@@ -802,50 +935,59 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               if (key >= vis[c0 + e]) x[e] = -INFINITY;
           }
         };
-        float x[kKeep ? CW : 16], mx = -INFINITY;
+        auto load16 = [&](int c0, bool sub, float* x) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(s_addr + c0, v);
+          tmem_ld_wait();
+          scores(v, c0, sub, x);
+        };
+        float x[kKeep ? CW : 16];
         auto load_all = [&] {
           uint32_t v[CW / 16][16];
 #pragma unroll
           for (int c = 0; c < CW / 16; ++c) tmem_ld_32x32b_x16(s_addr + c * 16, v[c]);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < CW / 16; ++c) scores(v[c], c * 16, x + c * 16);
+          for (int c = 0; c < CW / 16; ++c) scores(v[c], c * 16, true, x + c * 16);
         };
-        if (kKeep) {
-          load_all();
+        bool move = i == 0;
+        if (i > 0) {
+          float mx = -INFINITY;
+          if (kKeep) {
+            load_all();
 #pragma unroll
-          for (int e = 0; e < (kKeep ? CW : 0); ++e) mx = fmaxf(mx, x[e]);
-        } else if (i > 0) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < CW; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(s_addr + c0, v);
-            tmem_ld_wait();
-            scores(v, c0, x);
+            for (int e = 0; e < (kKeep ? CW : 0); ++e) mx = fmaxf(mx, x[e]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
-          }
-        }
-        if (bar_or(bar, 128, i == 0 || mx > kMoveLog2 + kLift)) {
-          // the columns' maxima over the tile, and new running maxima
-#pragma unroll 1
-          for (int c0 = 0; c0 < CW; c0 += 16) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(s_addr + c0, v);
-            tmem_ld_wait();
+            for (int c0 = 0; c0 < CW; c0 += 16) {
+              load16(c0, true, x);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float y = __uint_as_float(v[e]) * sc[c0 + e];
-              const float m = warp_max(masked && key >= vis[c0 + e] ? -INFINITY : y);
-              if (lane == e) red[q4 * NQ + col0 + c0 + e] = m;
+              for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
             }
           }
+          move = bar_or(bar, 128, wait.dead || mx > kMoveLog2 + kLift);
+        }
+        if (move) {
+          if (bar_or(bar, 128, wait.dead)) goto done;
+          // the columns' maxima over the tile (lane c: column c), and new running maxima
+          float mine = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < CW; c0 += 16) {
+            float y[16];
+            load16(c0, false, y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float m = warp_max(y[e]);
+              if (lane == c0 + e) mine = m;
+            }
+          }
+          if (lane < CW) red[q4 * NQ + col0 + lane] = mine;
           named_bar_sync(bar, 128);
           if (r < CW) {
             const float* m4 = red + col0 + r;
-            const float was = kLift - nm[r];
+            const float was = i == 0 ? kNoMax : kLift - nm[r];
             const float now = fmaxf(fmaxf(fmaxf(m4[0], m4[NQ]), fmaxf(m4[2 * NQ], m4[3 * NQ])), was);
-            fac[r] = i == 0 ? 0.f : ex2(was - now);
+            fac[r] = ex2(was - now);
             nm[r] = kLift - now;
           }
           named_bar_sync(bar, 128);
@@ -867,7 +1009,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             for (int c = 0; c < CW / 2; ++c)
               l[c] = __fmul2_rn(l[c], *reinterpret_cast<const float2*>(fac + 2 * c));
           }
-          if (kKeep) load_all();
+          if (kKeep) {
+#pragma unroll
+            for (int c = 0; c < (kKeep ? CW / 2 : 0); ++c)
+              mr[c] = *reinterpret_cast<const float2*>(nm + 2 * c);
+            load_all();
+          }
         }
         if (kKeep) {
           tc_fence_before();
@@ -876,57 +1023,49 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);     // P buffer free
         uint8_t* prow = pbuf + (j & 1) * C::kPBytes + (col0 / 64) * kTile * 128 + r * 128;
 #pragma unroll
-        for (int c0 = 0; c0 < CW; c0 += 16) {
-          float* xc = kKeep ? x + c0 : x;
-          if (!kKeep) {
-            uint32_t v[16];
-            tmem_ld_32x32b_x16(s_addr + c0, v);
-            tmem_ld_wait();
+        for (int c0 = 0; c0 < CW; c0 += 8) {
+          if (!kKeep && c0 % 16 == 0) {
+            load16(c0, true, x);
             if (c0 + 16 == CW) {
               tc_fence_before();
               warp_arrive(&s_empty[sb]);
             }
-            scores(v, c0, xc);
           }
-          uint32_t pk[8];
+          const float* xc = x + (kKeep ? c0 : c0 % 16);
+          uint32_t pk[4];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
+          for (int e = 0; e < 8; e += 2) {
             const float a = ex2(xc[e]), b = ex2(xc[e + 1]);
             l[(c0 + e) / 2] = __fadd2_rn(l[(c0 + e) / 2], make_float2(a, b));
             pk[e / 2] = pack_f16(a, b);
           }
-#pragma unroll
-          for (int c8 = 0; c8 < 2; ++c8) {
-            const int ch = (col0 % 64 + c0) / 8 + c8;
-            *reinterpret_cast<uint4*>(prow + ((ch ^ (r & 7)) << 4)) =
-                make_uint4(pk[4 * c8], pk[4 * c8 + 1], pk[4 * c8 + 2], pk[4 * c8 + 3]);
-          }
+          const int ch = (col0 % 64 + c0) / 8;
+          *reinterpret_cast<uint4*>(prow + ((ch ^ (r & 7)) << 4)) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         warp_arrive(&p_full[j & 1]);
       }
       // ---- the unit's (or piece's) result ----
-      // column sums over the warp's keys: halves of the columns change hands at each
-      // step, so lane x ends with column x (of the first 32, then of the next)
+      go = !(tiles[(j - 1) % C::kRing].flags & kFinal);
+      // column sums over the warp's keys: half of the columns change hands at each step,
+      // so lane c ends with column c
       {
-        float* lf = reinterpret_cast<float*>(l);
+        float y[CW];
 #pragma unroll
-        for (int c32 = 0; c32 < CW; c32 += 32) {
-          constexpr int kN = CW < 32 ? CW : 32;
-          float* y = lf + c32;
+        for (int c = 0; c < CW; ++c) y[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
 #pragma unroll
-          for (int n = kN / 2; n; n >>= 1) {
-            const bool up = lane & n;
+        for (int n = CW / 2; n; n >>= 1) {
+          const bool up = lane & n;
 #pragma unroll
-            for (int c = 0; c < n; ++c) {
-              const float other = __shfl_xor_sync(0xffffffffu, up ? y[c] : y[c + n], n);
-              y[c] = (up ? y[c + n] : y[c]) + other;
-            }
+          for (int c = 0; c < n; ++c) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? y[c] : y[c + n], n);
+            y[c] = (up ? y[c + n] : y[c]) + other;
           }
-          if (kN == 16) y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
-          if (lane < kN) red[q4 * NQ + col0 + c32 + lane] = y[0];
         }
+        if (CW == 16) y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
+        if (lane < CW) red[q4 * NQ + col0 + lane] = y[0];
       }
       named_bar_sync(bar, 128);
       const bool whole = tile0 == 0 && n == piece[par].nt;
@@ -973,6 +1112,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       named_bar_sync(bar, 128);                    // nm, fac and red are read
     }
   }
+done:
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1107,6 +1247,7 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.group = dims->n_q_heads / dims->n_kv_heads;
   p.causal = causal != 0;
   p.tile_rows = a.nq / p.group;
+  p.group_inv = (65536 + p.group - 1) / p.group;
   p.paged = cache->kv.page_table != nullptr;
   p.page_size = cache->kv.page_size;
   p.max_pages = cache->kv.max_pages;
