@@ -79,9 +79,8 @@ struct Cfg {
   // shared memory
   static constexpr int kPBytes = (NQ + 63) / 64 * kTile * 128;
   static constexpr int kQBytes = NQ * D * 2;
-  static constexpr int kVScale = kTile * (D / 16) * 2;  // fp16 scales of a V tile
   static constexpr int kVGran = kGran / kVWgs;          // cells of a V warpgroup
-  static constexpr int kFixed = 2 * kPBytes + 2 * kQBytes + 2 * kVScale;
+  static constexpr int kFixed = 2 * kPBytes + 2 * kQBytes;
   static constexpr int kTables = 12 * 1024;
   static constexpr int kFit = (226 * 1024 - kFixed - kTables) / kStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -392,43 +391,72 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// A wait of a warp; once one gave up the rest are skipped.  Warps that meet at named
-// barriers vote there on who gave up, and leave their loops together.
-// The bounded wait of this kernel: the timer, slower to read than most waits take, is
-// looked at every 64 tries only, and the loop is small (five roles share the instruction
-// cache; a call would rule out the register split).
+// Tries at two instructions each: what waiting warps issue is taken from those that work.
+// With kSleep, 40 to 80 ns of sleep between them, where being that late costs nothing.
+template <bool kSleep>
+__device__ __forceinline__ bool tries(uint64_t* bar, uint32_t parity) {
+#define DFLASH_TRY "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra done;\n\t"
+#define DFLASH_NAP DFLASH_TRY "nanosleep.u32 40;\n\t"
+  uint32_t ok;
+  if (kSleep)
+    asm volatile("{\n\t.reg .pred p;\n\t" DFLASH_TRY DFLASH_NAP DFLASH_NAP DFLASH_NAP DFLASH_NAP
+                 "done:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\t" DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY
+                     DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY
+                 "done:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+#undef DFLASH_TRY
+#undef DFLASH_NAP
+  return ok != 0;
+}
+
+// The bounded wait of this kernel (a call would rule out the register split).
+template <bool kSleep = false>
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                         uint32_t* status) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-    if (n % 64 == 0) {
-      const uint64_t now = globaltimer_ns();
-      if (n == 64) t0 = now;
-      if (*abort_flag) return false;
-      if (now - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        set_status(status, DFLASH_ST_TIMEOUT);
-        return false;
-      }
+  while (!tries<kSleep>(bar, parity)) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort_flag) return false;
+    if (now - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      set_status(status, DFLASH_ST_TIMEOUT);
+      return false;
     }
   }
   return true;
 }
 
+// A wait of a warp; once one gave up the rest are skipped.  Warps that meet at named
+// barriers vote there on who gave up, and leave their loops together.
 struct Waiter {
   volatile int* abort_flag;
   uint32_t* status;
   bool dead;
+  template <bool kSleep = false>
+  __device__ __forceinline__ void on(uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !wait_on<kSleep>(bar, parity, abort_flag, status);
+  }
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (!dead) dead = !wait_on(bar, parity, abort_flag, status);
+    on(bar, parity);
+  }
+  __device__ __forceinline__ bool gave_up() {     // by the whole warp
     dead = __any_sync(0xffffffffu, dead);
+    return dead;
   }
 };
 
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
-  if (lane_id() == 0) mbar_arrive(bar);
+  if (elect_one()) mbar_arrive(bar);
 }
 
 // ----------------------------------------------------------------------------
@@ -442,8 +470,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* pbuf = smem;
   uint8_t* qbuf = pbuf + 2 * C::kPBytes;
-  uint8_t* vscale = qbuf + 2 * C::kQBytes;
-  uint8_t* stages = vscale + 2 * C::kVScale;
+  uint8_t* stages = qbuf + 2 * C::kQBytes;
   uint8_t* tables = stages + C::kStages * C::kStage;
   int* col_vis = reinterpret_cast<int*>(tables);           // [2][NQ] keys a column sees
   int* col_row = col_vis + 2 * NQ;                         // [2][NQ] row of q and out
@@ -475,7 +502,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* any = abort_flag + 1;      // this CTA has tiles
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the index is the same all over the warp)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kProducer = C::kMisc, kMma = kProducer + 1, kQuery = kMma + 1;
   if (threadIdx.x == 0) {
 #pragma unroll 1
@@ -555,7 +583,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
                       min(p.tile_rows, g.T - g.t0) * G, g.h);
       more = walk.next(p, &after);
       g.final = !more;
-      if (seg >= 2) go = wait_on(&seg_empty[seg & 1], ((seg >> 1) - 1) & 1, abort_flag, p.status);
+      if (seg >= 2) go = wait_on<true>(&seg_empty[seg & 1], ((seg >> 1) - 1) & 1, abort_flag, p.status);
       if (lane == 0) segs[seg & 1] = g;
       warp_arrive(&seg_full[seg & 1]);
       int cell4 = 0, ahead = cells_at(g.tile);
@@ -571,7 +599,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const bool use = lane < kGran && lane * kCellRows < left;
         const uint32_t have = __ballot_sync(0xffffffffu, use && cell >= 0);
         const uint32_t miss = __ballot_sync(0xffffffffu, use && cell < 0);
-        go = go && wait_on(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status);
+        go = go && wait_on<true>(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status);
         if (!__all_sync(0xffffffffu, go)) {
           go = false;
           break;
@@ -608,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   }
   wait(planned, 0);
   griddep_launch_dependents();
-  if (wait.dead || *any == 0) goto done;
+  if (wait.gave_up() || *any == 0) goto done;
   if (warp == kMma) {
     // ---------------- the products ----------------
     // The whole warp runs the loop and one elected lane issues, so that the operands stay
@@ -680,7 +708,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll 1
     for (int seg = 0; go; ++seg) {
       const int par = seg & 1;
-      wait(&seg_full[par], (seg >> 1) & 1);
+      wait.on<true>(&seg_full[par], (seg >> 1) & 1);
       if (bar_or(15, 64, wait.dead)) break;                      // (and q_max is read)
       const Seg g = segs[par];
       go = !g.final;
@@ -697,7 +725,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll
           for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
           if (lane == 0) q_max[warp - kQuery] = m;
-          if (seg >= 2) wait(&q_empty[par], ((seg >> 1) - 1) & 1);
+          if (seg >= 2) wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
           named_bar_sync(15, 64);
           m = max(q_max[0], q_max[1]);
           const int ex = max(-126, min(126, 141 - static_cast<int>(m >> 7)));
@@ -759,9 +787,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll 1
       for (int j = 0; go; ++j) {
         const int st = j % C::kStages;
-        wait(&full[st], (j / C::kStages) & 1);
-        go = !(tiles[j % C::kRing].flags & kFinal) && !wait.dead;
-        if (j >= 2) wait(&kd_empty[j & 1], ((j >> 1) - 1) & 1);
+        wait.on<true>(&full[st], (j / C::kStages) & 1);
+        wait.on<true>(&kd_empty[j & 1], ((j >> 1) & 1) ^ 1);
+        if (wait.gave_up()) break;
+        go = !(tiles[j % C::kRing].flags & kFinal);
         tc_fence_after();
         const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
         const int rr = r % kCellRows;
@@ -783,10 +812,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             uint32_t o[16];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              uint32_t f[4];
-              e2m1x8_to_f16x2(u[e], f);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) o[4 * e + x] = hmul2(f[x], e < 2 ? s_lo : s_hi);
+              // (bytes 0 and 2 convert as they lie; 1 and 3 would take a shift each)
+              const uint32_t sc = e < 2 ? s_lo : s_hi, up = u[e] >> 8;
+              o[4 * e] = hmul2(e2m1x2_to_f16x2<0>(u[e]), sc);
+              o[4 * e + 1] = hmul2(e2m1x2_to_f16x2<0>(up), sc);
+              o[4 * e + 2] = hmul2(e2m1x2_to_f16x2<2>(u[e]), sc);
+              o[4 * e + 3] = hmul2(e2m1x2_to_f16x2<2>(up), sc);
             }
             tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + (c0 + c) * 16, o);
           }
@@ -799,61 +830,44 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     }
   } else if (warp < C::kSoft) {
     // ---------------- V^T to fp16: a thread expands its dim's row ----------------
-    // The 16 threads of a group of dims share their scales, so each scale is turned to
-    // fp16 once, by all threads together, and read back.
     if ((warp & 3) < C::kVWarps) {
-      constexpr int kN = 32 * C::kVWarps;
       const int d = threadIdx.x & 127, wg = (warp - C::kV) >> 2, g0 = wg * C::kVGran;
       const uint32_t lane_base =
           tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kV0 + g0 * 8;
-      const int shift = 4 * (d & 1);
+      uint32_t mul = d & 1 ? 1 : 16, mul16 = 16 * mul;         // to the byte's high nibble
+      asm volatile("" : "+r"(mul), "+r"(mul16));               // (factors, not shifts)
       bool go = true;
       {
 #pragma unroll 1
         for (int j = 0; go; ++j) {
           const int st = j % C::kStages;
-          wait(&full[st], (j / C::kStages) & 1);
+          wait.on<true>(&full[st], (j / C::kStages) & 1);
+          wait.on<true>(&pv_done[j & 1], ((j >> 1) & 1) ^ 1);
+          if (wait.gave_up()) break;
           const Tile t = tiles[j % C::kRing];
           go = !(t.flags & kFinal);
-          const uint8_t* base = stages + st * C::kStage + g0 * C::kCell;
-          uint8_t* vsc = vscale + (j & 1) * C::kVScale + wg * (C::kVScale / C::kVWgs);
-          {  // kVGran scales a thread
-            constexpr int kT = D / C::kVGran;                  // threads a cell
-            const uint8_t* src = base + d / kT * C::kCell + Cell<D>::v_scale(0, 0) +
-                                 d % kT * C::kVGran;
-            if (C::kVGran == 8) {
-              const uint2 s8 = *reinterpret_cast<const uint2*>(src);
-              *reinterpret_cast<uint4*>(vsc + d * 16) =
-                  make_uint4(e4m3x2_to_f16x2(s8.x), e4m3x2_to_f16x2(s8.x >> 16),
-                             e4m3x2_to_f16x2(s8.y), e4m3x2_to_f16x2(s8.y >> 16));
-            } else {
-              const uint32_t s4 = *reinterpret_cast<const uint32_t*>(src);
-              *reinterpret_cast<uint2*>(vsc + d * 8) =
-                  make_uint2(e4m3x2_to_f16x2(s4), e4m3x2_to_f16x2(s4 >> 16));
-            }
-          }
-          if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);
           tc_fence_after();
-          if (bar_or(8 + wg, kN, wait.dead)) break;            // the scales are there
+          const uint8_t* base = stages + st * C::kStage + g0 * C::kCell;
           // keys in use from this warpgroup's first cell on
           const int left = t.left - g0 * kCellRows;
           const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
-          const uint4* scl = reinterpret_cast<const uint4*>(vsc + d / 16 * 32);
+          const uint8_t* scl = base + Cell<D>::v_scale(0, d / 16);
 #pragma unroll 2
           for (int c = 0; c < C::kVGran; ++c) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
-            const uint4 sa = scl[c * (D / 8)], sb = scl[c * (D / 8) + 1];
+            const uint4 s4 = *reinterpret_cast<const uint4*>(scl + c * C::kCell);
             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            const uint32_t s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+            const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // this dim's nibbles of four keys, two to a byte
-              // (only bytes 0 and 2 of x are used)
-              const uint32_t a = w[e] >> shift, b = w[e] >> (shift + 4);
-              const uint32_t x = (a & 0x000F000Fu) | (b & ~0x000F000Fu);
-              o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), s[2 * e]);
-              o[2 * e + 1] = hmul2(e2m1x2_to_f16x2<2>(x), s[2 * e + 1]);
+              // this dim's nibbles of four keys, two to a byte (0 and 2, which convert as they
+              // lie): shifts as products leave the integer pipe to the conversions
+              const uint32_t x =
+                  ((w[e] * mul & 0xF000F000u) | (w[e] * mul16 & ~0xF000F000u)) >> 8;
+              o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), e4m3x2_to_f16x2(s[e]));
+              o[2 * e + 1] =
+                  hmul2(e2m1x2_to_f16x2<2>(x), e4m3x2_to_f16x2(s[e] >> 16));
             }
             if (left < (c + 1) * kCellRows) {                // rows past the length count as 0
 #pragma unroll
@@ -903,6 +917,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const int key = (tile0 + i) * kTile + r;
         const bool masked = (tile0 + i + 1) * kTile > sure;
         wait(&s_full[sb], (j / C::kSBufs) & 1);
+        __syncwarp();
         tc_fence_after();
         // 16 columns of this key's scores in log2 units, minus the running maxima if `sub`
         auto scores = [&](const uint32_t (&v)[16], int c0, bool sub, float* x) {
@@ -993,6 +1008,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           named_bar_sync(bar, 128);
           if (i > 0) {
             wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
+            __syncwarp();
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < CW; c0 += 16) {
@@ -1020,7 +1036,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           tc_fence_before();
           warp_arrive(&s_empty[sb]);
         }
-        if (j >= 2) wait(&pv_done[j & 1], ((j >> 1) - 1) & 1);     // P buffer free
+        // (the P buffer is free: the products run in order, and S of this tile came after
+        // the P V of two tiles back)
         uint8_t* prow = pbuf + (j & 1) * C::kPBytes + (col0 / 64) * kTile * 128 + r * 128;
 #pragma unroll
         for (int c0 = 0; c0 < CW; c0 += 8) {
@@ -1085,6 +1102,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const int* row = col_row + par * NQ + col0;
       const int rows = piece[par].rows - col0;                      // of this warpgroup
       wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
+      __syncwarp();
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < CW; c0 += 16) {
