@@ -60,8 +60,10 @@ struct Cfg {
   static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
   static constexpr int kVWarps = D / 32;               // warps of it that hold rows of V^T
-  static constexpr int kV = 4 * kKWgs, kSoft = kV + 4 * kVWgs, kMisc = kSoft + 4 * kSoftWgs;
-  static constexpr int kThreads = 32 * (kMisc + 4);
+  // First warps of the roles.  The lowest warps go first when several could issue: those
+  // that feed the others come first.
+  static constexpr int kMisc = 0, kSoft = 4, kV = kSoft + 4 * kSoftWgs, kK = kV + 4 * kVWgs;
+  static constexpr int kThreads = 32 * (kK + 4 * kKWgs);
   // Registers: the launch's share, and what the roles make of it (0: left alone).  The
   // softmax holds scores, sums and maxima of its columns.
   static constexpr int kRegsSoft = NQ == 16 ? 0 : NQ == 128 ? 80 : 128;
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (C::kRegsSoft && (warp < C::kSoft || warp >= C::kMisc)) regs_down<C::kRegsRest>();
+  if (C::kRegsSoft && (warp < C::kSoft || warp >= C::kV)) regs_down<C::kRegsRest>();
   griddep_wait();
   Waiter wait{abort_flag, p.status, false};
   const int G = p.group;
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     if (elect_one()) umma_commit(mdrain);
     if (lane == 0) mbar_wait_drain(mdrain, 0, p.status);
     __syncwarp();
-  } else if (warp >= kQuery) {
+  } else if (warp < C::kSoft) {
     // ---------------- query rows of a unit, D / 8 lanes a row ----------------
     // Twice over them: for the largest finite magnitude of all, which goes to [2^14, 2^15),
     // and to convert.
@@ -778,9 +780,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       fence_proxy_async_smem();
       warp_arrive(&q_full[par]);
     }
-  } else if (warp < C::kV) {
+  } else if (warp >= C::kK) {
     // ---------------- K to fp16: a thread expands its key's row ----------------
-    const int r = threadIdx.x & 127, wg = warp >> 2;
+    const int r = threadIdx.x & 127, wg = (warp - C::kK) >> 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool go = true;
     {
@@ -828,7 +830,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         warp_arrive(&kd_full[j & 1]);
       }
     }
-  } else if (warp < C::kSoft) {
+  } else if (warp >= C::kV) {
     // ---------------- V^T to fp16: a thread expands its dim's row ----------------
     if ((warp & 3) < C::kVWarps) {
       const int d = threadIdx.x & 127, wg = (warp - C::kV) >> 2, g0 = wg * C::kVGran;
@@ -1159,17 +1161,18 @@ done:
 //         and 16 i + 2 g + 1: one word holds both for four keys, under one scale for each key
 template <int D, int kTiles>
 struct RowsCfg {
-  static constexpr int kWarps = kTiles == 1 ? 15 : 11;   // and one that plans
+  static constexpr int kWarps = kTiles == 1 ? 19 : 14;   // and one that plans
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 8 * kTiles;
-  static constexpr int kStages = 4;    // cells of a warp's ring
+  static constexpr int kStages = 3;    // cells of a warp's ring
   static constexpr int kCell = Cell<D>::kBytes;
   static constexpr int kRing = kWarps * kStages * kCell;
   static constexpr int kPitch = D + 4;                   // floats, of a row of `join`
   static constexpr int kJoin = kWarps * kRows * kPitch * 4;
   static constexpr int kSegs = 4;
-  static constexpr int kSmem = 128 + kRing + kJoin + kWarps * kRows * 8 + 64 * kSegs +
-                               8 * (kWarps * kStages + 2 * kSegs) + 64;
+  static constexpr int kQuery = kTiles * (D / 32) * 512; // fragments of the query rows
+  static constexpr int kSmem = 128 + kRing + kQuery + kJoin + kWarps * kRows * 8 + kRows * 8 +
+                               64 * kSegs + 8 * (kWarps * kStages + 2 * kSegs) + 64;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -1179,17 +1182,14 @@ struct RowSeg {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+__device__ __forceinline__ uint32_t word(const uint8_t* p) {
+  return *reinterpret_cast<const uint32_t*>(p);
 }
 
 template <int D, int kTiles>
@@ -1199,9 +1199,12 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
   constexpr int kP = D / 32, kI = D / 16;          // pieces of K, tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
-  float* join = reinterpret_cast<float*>(smem + C::kRing);             // [warp][row][kPitch]
-  float2* wml = reinterpret_cast<float2*>(smem + C::kRing + C::kJoin);  // [warp][row] max, sum
-  RowSeg* segs = reinterpret_cast<RowSeg*>(wml + C::kWarps * C::kRows);
+  uint4* qf = reinterpret_cast<uint4*>(smem + C::kRing);   // [tile][piece][lane]
+  float* join = reinterpret_cast<float*>(smem + C::kRing + C::kQuery);  // [warp][row][kPitch]
+  float2* wml = reinterpret_cast<float2*>(join + C::kWarps * C::kRows * C::kPitch);
+                                                           // [warp][row] maximum, sum
+  float* row_sc = reinterpret_cast<float*>(wml + C::kWarps * C::kRows);  // [row]
+  RowSeg* segs = reinterpret_cast<RowSeg*>(row_sc + 2 * C::kRows);
   uint64_t* full = reinterpret_cast<uint64_t*>(segs + C::kSegs);       // [warp][stage]
   uint64_t* seg_full = full + C::kWarps * C::kStages;
   uint64_t* seg_empty = seg_full + C::kSegs;
@@ -1299,7 +1302,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
       const int key16 = l_cell0 + lc;
       int slab = l_b, row16 = key16;
       if (p.paged) {
-        const int page = key16 / per_slab;
+        const int page = per_slab == 1 ? key16 : key16 / per_slab;
         row16 = key16 - page * per_slab;
         slab = p.page_table[static_cast<size_t>(l_b) * p.max_pages + page];
       }
@@ -1333,12 +1336,8 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
     go = !r.final;
     if (r.b < 0) break;
     // ---- query rows as fragments, each scaled to [1, 2) by a power of two ----
-    uint32_t q[kP][2][2][kTiles];      // piece, step, dims 0-1 or 2-3 of it, rows 8 x + g
-    float sc[kTiles][2];               // of rows 8 x + 2 t, 8 x + 2 t + 1, as all below
-    int vis[kTiles][2];
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-      const int row = gl + 8 * x, tq = row * p.group_inv >> 16;
+    if (warp < kTiles) {
+      const int row = gl + 8 * warp, tq = row * p.group_inv >> 16;
       uint4 v[kP];
       uint32_t m = 0;
 #pragma unroll
@@ -1362,21 +1361,27 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          q[i][e >> 1][e & 1][x] = pack_f16(__uint_as_float(w[e] << 16) * f,
-                                            __uint_as_float(w[e] & 0xFFFF0000u) * f);
+          y[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
+        qf[(warp * kP + i) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
       }
-      const float kx = p.scale_log2 * pow2(gain_exp(p.s.k_exp, r.h)) * pow2(-ex);
+      if (t == 0) row_sc[row] = p.scale_log2 * pow2(gain_exp(p.s.k_exp, r.h)) * pow2(-ex);
+    }
+    named_bar_sync(1, 32 * C::kWarps);
+    float sc[kTiles][2];               // of rows 8 x + 2 t, 8 x + 2 t + 1, as all below
+    int vis[kTiles][2];
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int mr = 8 * x + 2 * t + e;
-        sc[x][e] = __shfl_sync(0xffffffffu, kx, 4 * (2 * t + e));
+        sc[x][e] = row_sc[mr];
         vis[x][e] = p.causal && mr < r.rows
                         ? max(0, min(r.len, r.len - r.T + r.t0 + (mr * p.group_inv >> 16) + 1))
                         : r.len;
       }
-    }
     const int sure = p.causal ? max(0, r.len - r.T + r.t0 + 1) : r.len;
     float o[kI][kTiles][4], l[kTiles][2], nm[kTiles][2];   // nm: kLift - running maximum
 #pragma unroll
@@ -1389,44 +1394,51 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
       nm[x][0] = nm[x][1] = kLift - kNoMax;
     }
     const int kr = 4 * (gl >> 1) + (gl & 1);                // S^T rows g, g + 8: keys kr, kr + 2
+    // the scale byte of this thread's dims, twice, of two pieces' four
+    const uint32_t pick0 = t & 2 ? 0x4411u : 0x4400u, pick1 = t & 2 ? 0x4433u : 0x4422u;
 #pragma unroll 1
     for (int c = warp; c < r.cells; c += C::kWarps, ++done) {
       const int st = done % C::kStages;
       wait(&mine[st], (done / C::kStages) & 1);
       if (wait.gave_up()) break;
-      const uint32_t cell = ring + st * C::kCell;
+      const uint8_t* cell = smem + (warp * C::kStages + st) * C::kCell;
       const int key0 = (r.cell0 + c) * kCellRows;
       // ---- scores of 16 keys: element e is key kr + 2 (e >> 1), row 2 t + (e & 1) ----
-      float s[kTiles][4];
+      float s[kTiles][4], s_odd[kTiles][4];                 // (two chains of products)
 #pragma unroll
       for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[x][e] = s_odd[x][e] = 0.f;
       uint32_t ks[2][kP / 2];
 #pragma unroll
       for (int i = 0; i < kP / 2; ++i) {
-        ks[0][i] = lds32(cell + Cell<D>::k_scale(kr, 4 * i));
-        ks[1][i] = lds32(cell + Cell<D>::k_scale(kr + 2, 4 * i));
+        ks[0][i] = word(cell + Cell<D>::k_scale(kr, 4 * i));
+        ks[1][i] = word(cell + Cell<D>::k_scale(kr + 2, 4 * i));
       }
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
         uint32_t a[2][4];                                   // step; a0 .. a3
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t w = lds32(cell + i * 256 + (kr + 2 * u) * 16 + 4 * t), up = w >> 8;
-          const uint32_t s2 = e4m3x2_to_f16x2(i & 1 ? ks[u][i / 2] >> 16 : ks[u][i / 2]);
-          const uint32_t f = __byte_perm(s2, 0, t & 2 ? 0x3232 : 0x1010);
+          const uint32_t w = word(cell + i * 256 + (kr + 2 * u) * 16 + 4 * t);
+          const uint32_t up = w >> 8;
+          const uint32_t f = e4m3x2_to_f16x2(__byte_perm(ks[u][i / 2], 0, i & 1 ? pick1 : pick0));
           a[0][u] = hmul2(e2m1x2_to_f16x2<0>(w), f);
           a[0][2 + u] = hmul2(e2m1x2_to_f16x2<0>(up), f);
           a[1][u] = hmul2(e2m1x2_to_f16x2<2>(w), f);
           a[1][2 + u] = hmul2(e2m1x2_to_f16x2<2>(up), f);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int x = 0; x < kTiles; ++x)
-            mma16816(s[x], a[e][0], a[e][1], a[e][2], a[e][3], q[i][e][0][x], q[i][e][1][x]);
+        for (int x = 0; x < kTiles; ++x) {
+          const uint4 q = qf[(x * kP + i) * 32 + lane];
+          mma16816(s[x], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
+          mma16816(s_odd[x], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
+        }
       }
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[x][e] += s_odd[x][e];
       // ---- probabilities ----
       if (key0 + kCellRows > sure) {   // (a masked score is minus infinity whatever its scale)
 #pragma unroll
@@ -1479,26 +1491,22 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
                        : "r"(pack_f16(p0, p1)));
         }
       // ---- O^T += V^T P^T ----
-      const int left = r.end - key0;   // rows past the length count as 0
+      const int left = r.end - key0 - 4 * t;                // of this thread's four keys
+      const uint32_t in_use = left >= 4 ? ~0u : left > 0 ? (1u << 8 * left) - 1u : 0u;
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        const uint32_t w = lds32(cell + Cell<D>::kV + (8 * i + gl) * 16 + 4 * t);
-        const uint32_t vs = lds32(cell + Cell<D>::v_scale(4 * t, i));
+        const uint32_t w = word(cell + Cell<D>::kV + (8 * i + gl) * 16 + 4 * t);
+        // (scales of rows past the length become 0; codes are finite whatever they hold)
+        const uint32_t vs = word(cell + Cell<D>::v_scale(4 * t, i)) & in_use;
         const uint32_t f0 = e4m3x2_to_f16x2(vs), f1 = e4m3x2_to_f16x2(vs >> 16);
         // low (even dim) and high nibbles of two keys to a byte, bytes 0 and 2
         const uint32_t w4 = w >> 4, w8 = w >> 8;
         const uint32_t lo = (w & 0x000F000Fu) | (w4 & ~0x000F000Fu);
         const uint32_t hi = (w4 & 0x000F000Fu) | (w8 & ~0x000F000Fu);
-        uint32_t a[4] = {hmul2(e2m1x2_to_f16x2<0>(lo), f0), hmul2(e2m1x2_to_f16x2<0>(hi), f0),
-                         hmul2(e2m1x2_to_f16x2<2>(lo), f1), hmul2(e2m1x2_to_f16x2<2>(hi), f1)};
-        if (left < kCellRows) {
-          const uint32_t m0 = left > 4 * t + 1 ? ~0u : left > 4 * t ? 0xFFFFu : 0u;
-          const uint32_t m1 = left > 4 * t + 3 ? ~0u : left > 4 * t + 2 ? 0xFFFFu : 0u;
-          a[0] &= m0;
-          a[1] &= m0;
-          a[2] &= m1;
-          a[3] &= m1;
-        }
+        const uint32_t a[4] = {hmul2(e2m1x2_to_f16x2<0>(lo), f0),
+                               hmul2(e2m1x2_to_f16x2<0>(hi), f0),
+                               hmul2(e2m1x2_to_f16x2<2>(lo), f1),
+                               hmul2(e2m1x2_to_f16x2<2>(hi), f1)};
 #pragma unroll
         for (int x = 0; x < kTiles; ++x)
           mma16816(o[i][x], a[0], a[1], a[2], a[3], b[x][0], b[x][1]);
