@@ -393,48 +393,31 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Tries at two instructions each: what waiting warps issue is taken from those that work.
-// With kSleep, 40 to 80 ns of sleep between them, where being that late costs nothing.
-template <bool kSleep>
-__device__ __forceinline__ bool tries(uint64_t* bar, uint32_t parity) {
-#define DFLASH_TRY "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra done;\n\t"
-#define DFLASH_NAP DFLASH_TRY "nanosleep.u32 40;\n\t"
-  uint32_t ok;
-  if (kSleep)
-    asm volatile("{\n\t.reg .pred p;\n\t" DFLASH_TRY DFLASH_NAP DFLASH_NAP DFLASH_NAP DFLASH_NAP
-                 "done:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-  else
-    asm volatile("{\n\t.reg .pred p;\n\t" DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY
-                     DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY
-                 "done:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-#undef DFLASH_TRY
-#undef DFLASH_NAP
-  return ok != 0;
-}
-
-// The bounded wait of this kernel (a call would rule out the register split).
-template <bool kSleep = false>
+// The bounded wait of this kernel.  A try by a whole warp sleeps up to 4 us (measured), so
+// 2^18 of them are a second; the loop is small, because five roles share the
+// instruction cache, and a call would rule out the register split.
+template <bool kNap = false>
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                         uint32_t* status) {
-  uint64_t t0 = 0;
-#pragma unroll 1
-  while (!tries<kSleep>(bar, parity)) {
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (*abort_flag) return false;
-    if (now - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      set_status(status, DFLASH_ST_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
+#define DFLASH_TRY "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra done;\n\t"
+#define DFLASH_LOOP(body)                                                           \
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 65536;\n\tagain:\n\t" body \
+               "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra again;\n\tdone:\n\t"     \
+               "selp.u32 %0, 1, 0, p;\n\t}\n"                                        \
+               : "=r"(ok)                                                           \
+               : "r"(smem_u32(bar)), "r"(parity)                                    \
+               : "memory")
+  uint32_t ok;
+  if (kNap)      // where 100 ns late costs nothing
+    DFLASH_LOOP(DFLASH_TRY "nanosleep.u32 60;\n\t");
+  else
+    DFLASH_LOOP(DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY);
+#undef DFLASH_TRY
+#undef DFLASH_LOOP
+  if (ok) return true;
+  *abort_flag = 1;
+  set_status(status, DFLASH_ST_TIMEOUT);
+  return false;
 }
 
 // A wait of a warp; once one gave up the rest are skipped.  Warps that meet at named
@@ -443,9 +426,9 @@ struct Waiter {
   volatile int* abort_flag;
   uint32_t* status;
   bool dead;
-  template <bool kSleep = false>
+  template <bool kNap = false>
   __device__ __forceinline__ void on(uint64_t* bar, uint32_t parity) {
-    if (!dead) dead = !wait_on<kSleep>(bar, parity, abort_flag, status);
+    if (!dead) dead = !wait_on<kNap>(bar, parity, abort_flag, status);
   }
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
     on(bar, parity);
@@ -486,12 +469,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint64_t* full = bars;
   uint64_t* empty = full + C::kStages;
   uint64_t* kd_full = empty + C::kStages;  // [2] K tile in TMEM
-  uint64_t* kd_empty = kd_full + 2;        // [2] S product done
-  uint64_t* vd_full = kd_empty + 2;        // [2] V^T tile in TMEM
-  uint64_t* s_full = vd_full + 2;          // [kSBufs] S in TMEM
-  uint64_t* s_empty = s_full + 2;          // [kSBufs] S read
-  uint64_t* p_full = s_empty + 2;          // [2] P in shared memory
-  uint64_t* pv_done = p_full + 2;          // [2] P V product done
+  uint64_t* kd_empty = kd_full + 2;        // [2] S product done (with one S buffer)
+  uint64_t* s_full = kd_empty + 2;         // [kSBufs] S in TMEM
+  uint64_t* s_empty = s_full + 2;          // S read
+  uint64_t* pv_full = s_empty + 1;         // [2] V^T tile in TMEM, P in shared memory
+  uint64_t* pv_done = pv_full + 2;         // [2] P V product done
   uint64_t* q_full = pv_done + 2;          // [2] query rows and tables of a segment
   uint64_t* q_empty = q_full + 2;          // [2] read
   uint64_t* o_empty = q_empty + 2;         // O of a segment read
@@ -517,16 +499,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&kd_full[i], 4 * C::kKWgs);
       mbar_init(&kd_empty[i], 1);
-      mbar_init(&vd_full[i], C::kVWarps * C::kVWgs);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4 * C::kSoftWgs);
-      mbar_init(&p_full[i], 4 * C::kSoftWgs);
+      mbar_init(&pv_full[i], C::kVWarps * C::kVWgs + 4 * C::kSoftWgs);
       mbar_init(&pv_done[i], 1);
       mbar_init(&q_full[i], 2);
       mbar_init(&q_empty[i], 4 * C::kSoftWgs);
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 2);
     }
+    mbar_init(s_empty, 4 * C::kSoftWgs);
     mbar_init(o_empty, 4 * C::kSoftWgs);
     mbar_init(planned, 1);
     mbar_init(mdrain, 1);
@@ -653,14 +634,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     };
     auto issue_pv = [&](int j, bool first, int seg) {
       if (!ok) return;
-      need(&p_full[j & 1], (j >> 1) & 1);
-      need(&vd_full[j & 1], (j >> 1) & 1);
+      need(&pv_full[j & 1], (j >> 1) & 1);
       if (first && seg > 0) need(o_empty, (seg - 1) & 1);
       if (!ok) return;
       tc_fence_after();
       const uint32_t par = j & 1;
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
         for (int ks = 0; ks < kTile / 16; ++ks)
           umma_f16_ts(C::kO0, C::kV0 + par * C::kVCols + ks * 8,
                       p_desc + ((par * C::kPBytes + ks * 2048) >> 4), idesc_o, !first || ks > 0);
@@ -677,17 +657,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       flags = tiles[j % C::kRing].flags;
       const int qs = seg + (flags & kFirst);
       if (flags & kFirst) need(&q_full[qs & 1], (qs >> 1) & 1);
-      if (j >= C::kSBufs) need(&s_empty[sb], (j / C::kSBufs - 1) & 1);
+      // (two buffers: S of two tiles back was read before its P came, waited for already)
+      if (C::kSBufs == 1) need(s_empty, (j & 1) ^ 1);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t q0 = q_desc + ((qs & 1) * C::kQBytes >> 4);
-#pragma unroll
+#pragma unroll 1
         for (int ks = 0; ks < D / 16; ++ks)
           umma_f16_ts(C::kS0 + sb * NQ, par * C::kKCols + ks * 8,
                       q0 + (((ks >> 2) * NQ * 128 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
         umma_commit(&s_full[sb]);
-        umma_commit(&kd_empty[par]);
+        if (C::kSBufs == 1) umma_commit(&kd_empty[par]);
       }
       if (j > 0) issue_pv(j - 1, was & kFirst, seg);
       seg = qs;
@@ -790,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       for (int j = 0; go; ++j) {
         const int st = j % C::kStages;
         wait.on<true>(&full[st], (j / C::kStages) & 1);
-        wait.on<true>(&kd_empty[j & 1], ((j >> 1) & 1) ^ 1);
+        wait.on<true>(&(C::kSBufs == 2 ? s_full : kd_empty)[j & 1], ((j >> 1) & 1) ^ 1);
         if (wait.gave_up()) break;
         go = !(tiles[j % C::kRing].flags & kFinal);
         tc_fence_after();
@@ -854,7 +835,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           const int left = t.left - g0 * kCellRows;
           const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
           const uint8_t* scl = base + Cell<D>::v_scale(0, d / 16);
-#pragma unroll 2
+#pragma unroll 1
           for (int c = 0; c < C::kVGran; ++c) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
             const uint4 s4 = *reinterpret_cast<const uint4*>(scl + c * C::kCell);
@@ -884,7 +865,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           warp_arrive(&empty[st]);
           tmem_st_wait();
           tc_fence_before();
-          warp_arrive(&vd_full[j & 1]);
+          warp_arrive(&pv_full[j & 1]);
         }
       }
     }
@@ -1034,10 +1015,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             load_all();
           }
         }
-        if (kKeep) {
-          tc_fence_before();
-          warp_arrive(&s_empty[sb]);
-        }
         // (the P buffer is free: the products run in order, and S of this tile came after
         // the P V of two tiles back)
         uint8_t* prow = pbuf + (j & 1) * C::kPBytes + (col0 / 64) * kTile * 128 + r * 128;
@@ -1045,9 +1022,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         for (int c0 = 0; c0 < CW; c0 += 8) {
           if (!kKeep && c0 % 16 == 0) {
             load16(c0, true, x);
-            if (c0 + 16 == CW) {
+            if (c0 + 16 == CW && C::kSBufs == 1) {
               tc_fence_before();
-              warp_arrive(&s_empty[sb]);
+              warp_arrive(s_empty);
             }
           }
           const float* xc = x + (kKeep ? c0 : c0 % 16);
@@ -1064,7 +1041,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        warp_arrive(&p_full[j & 1]);
+        warp_arrive(&pv_full[j & 1]);
       }
       // ---- the unit's (or piece's) result ----
       go = !(tiles[(j - 1) % C::kRing].flags & kFinal);
