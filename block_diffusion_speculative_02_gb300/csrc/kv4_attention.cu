@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       tc_fence_after();
       const uint32_t par = j & 1;
       if (elect_one()) {
-#pragma unroll 1
+#pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
           umma_f16_ts(C::kO0, C::kV0 + par * C::kVCols + ks * 8,
                       p_desc + ((par * C::kPBytes + ks * 2048) >> 4), idesc_o, !first || ks > 0);
@@ -648,32 +648,36 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
     };
     int seg = -1, flags = 0;
+    bool opened = false;
 #pragma unroll 1
     for (int j = 0;; ++j) {
       const uint32_t sb = j % C::kSBufs, par = j & 1;
-      const int was = flags;
       need(&kd_full[par], (j >> 1) & 1);
       if (!ok) break;
+      // (votes, so that what follows from the flags is the same all over the warp)
       flags = tiles[j % C::kRing].flags;
-      const int qs = seg + (flags & kFirst);
-      if (flags & kFirst) need(&q_full[qs & 1], (qs >> 1) & 1);
+      const bool opens = __any_sync(0xffffffffu, flags & kFirst);
+      const bool final = __any_sync(0xffffffffu, flags & kFinal);
+      const int qs = opens ? seg + 1 : seg;
+      if (opens) need(&q_full[qs & 1], (qs >> 1) & 1);
       // (two buffers: S of two tiles back was read before its P came, waited for already)
       if (C::kSBufs == 1) need(s_empty, (j & 1) ^ 1);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t q0 = q_desc + ((qs & 1) * C::kQBytes >> 4);
-#pragma unroll 1
+#pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
           umma_f16_ts(C::kS0 + sb * NQ, par * C::kKCols + ks * 8,
                       q0 + (((ks >> 2) * NQ * 128 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
         umma_commit(&s_full[sb]);
         if (C::kSBufs == 1) umma_commit(&kd_empty[par]);
       }
-      if (j > 0) issue_pv(j - 1, was & kFirst, seg);
+      if (j > 0) issue_pv(j - 1, opened, seg);
       seg = qs;
-      if (flags & kFinal) {
-        issue_pv(j, flags & kFirst, seg);
+      opened = opens;
+      if (final) {
+        issue_pv(j, opened, seg);
         break;
       }
     }
