@@ -33,6 +33,7 @@
 // column sums stay in registers until the unit ends.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "kv4.cuh"
@@ -56,7 +57,7 @@ struct Cfg {
   // a role grows by sharing out dims (K), cells (V^T) or query columns (softmax).  Few
   // query rows leave the expansion of K and V as the longest step: two each then.
   static constexpr int kKWgs = NQ <= 32 ? 2 : 1;
-  static constexpr int kVWgs = NQ <= 64 ? 2 : 1;
+  static constexpr int kVWgs = 2;
   static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
   static constexpr int kVWarps = D / 32;               // warps of it that hold rows of V^T
@@ -67,7 +68,7 @@ struct Cfg {
   // Registers: the launch's share, and what the roles make of it (0: left alone).  The
   // softmax holds scores, sums and maxima of its columns.
   static constexpr int kRegsSoft = NQ == 16 ? 0 : NQ == 128 ? 80 : 128;
-  static constexpr int kRegsRest = NQ == 128 ? 56 : 56;
+  static constexpr int kRegsRest = NQ == 128 ? 48 : 56;
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static_assert(kRegsSoft * 128 * kSoftWgs + kRegsRest * (kThreads - 128 * kSoftWgs) <=
                     kRegsLaunch * kThreads,
@@ -408,6 +409,7 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
                : "r"(smem_u32(bar)), "r"(parity)                                    \
                : "memory")
   uint32_t ok;
+  __syncwarp();  // (a warp that is not together does not sleep in a try)
   if (kNap)      // where 100 ns late costs nothing
     DFLASH_LOOP(DFLASH_TRY "nanosleep.u32 60;\n\t");
   else
@@ -828,8 +830,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll 1
         for (int j = 0; go; ++j) {
           const int st = j % C::kStages;
-          wait.on<true>(&full[st], (j / C::kStages) & 1);
-          wait.on<true>(&pv_done[j & 1], ((j >> 1) & 1) ^ 1);
+          wait(&full[st], (j / C::kStages) & 1);
+          wait(&pv_done[j & 1], ((j >> 1) & 1) ^ 1);
           if (wait.gave_up()) break;
           const Tile t = tiles[j % C::kRing];
           go = !(t.flags & kFinal);
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           const int left = t.left - g0 * kCellRows;
           const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
           const uint8_t* scl = base + Cell<D>::v_scale(0, d / 16);
-#pragma unroll 1
+#pragma unroll 2
           for (int c = 0; c < C::kVGran; ++c) {
             const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
             const uint4 s4 = *reinterpret_cast<const uint4*>(scl + c * C::kCell);
@@ -1622,10 +1624,23 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
     *reinterpret_cast<uint32_t*>(out) = y[0];
 }
 
+// set_smem_limit, the first time on each device (a bit of *ready; past 64 every time).
+int smem_limit_once(std::atomic<uint64_t>* ready, const void* kernel, int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH_E_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready->load(std::memory_order_acquire) & bit) return DFLASH_OK;
+  const int rc = set_smem_limit(kernel, bytes);
+  if (rc == DFLASH_OK) ready->fetch_or(bit, std::memory_order_release);
+  return rc;
+}
+
 template <int D, int kTiles>
 int run_rows(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
   using C = RowsCfg<D, kTiles>;
-  int rc = set_smem_limit(reinterpret_cast<const void*>(kv4_rows_kernel<D, kTiles>), C::kSmem);
+  static std::atomic<uint64_t> ready{0};
+  int rc = smem_limit_once(&ready, reinterpret_cast<const void*>(kv4_rows_kernel<D, kTiles>),
+                           C::kSmem);
   if (rc) return rc;
   if ((rc = launch(kv4_rows_kernel<D, kTiles>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, p)))
     return rc;
@@ -1658,7 +1673,9 @@ AttnLayout attn_layout(const dflash_kv4_dims& d) {
 template <int D, int NQ>
 int run(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
   using C = Cfg<D, NQ>;
-  int rc = set_smem_limit(reinterpret_cast<const void*>(kv4_attention_kernel<D, NQ>), C::kSmem);
+  static std::atomic<uint64_t> ready{0};
+  int rc = smem_limit_once(&ready, reinterpret_cast<const void*>(kv4_attention_kernel<D, NQ>),
+                           C::kSmem);
   if (rc) return rc;
   if ((rc = launch(kv4_attention_kernel<D, NQ>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, p)))
     return rc;

@@ -9,6 +9,7 @@ module refuses to load when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -501,23 +502,37 @@ def alloc_kv4_workspace(dims: KV4Dims, device="cuda") -> torch.Tensor:
     return torch.zeros(dflash_kv4_workspace_bytes(dims), dtype=torch.uint8, device=device)
 
 
-def _on(t, device: int, dtype, numel: int, name: str, least: bool = False) -> Optional[int]:
-    """Pointer of a contiguous tensor on this device with this type and size (``least``: at least
-    this size)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+def _bad(t, device: int, dtype, numel, name: str):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device \
+            or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
-    if t.numel() != numel and not (least and t.numel() > numel):
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+
+
+def _on(t, device: int, dtype, numel: int, name: str) -> int:
+    """Pointer of a contiguous tensor on this device with this type and size."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() \
+            or t.numel() != numel:
+        _bad(t, device, dtype, numel, name)
     return t.data_ptr()
+
+
+def _opt(t, device: int, dtype, numel: int, name: str) -> Optional[int]:
+    return None if t is None else _on(t, device, dtype, numel, name)
+
+
+def _ws_on(ws, device: int):
+    """(pointer, bytes) of a workspace."""
+    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+        _bad(ws, device, torch.uint8, None, "ws")
+    return ws.data_ptr(), ws.numel()
 
 
 def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
     """(pointer, row pitch) of a bf16 [rows, heads, D] tensor whose rows are contiguous."""
     if t.dtype is not torch.bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be a bf16 tensor on cuda:{device}")
-    if t.dim() != 3 or t.shape != (rows, heads, d):
+    if t.shape != (rows, heads, d):
         raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
     st = t.stride()
     if st[2] != 1 or (st[1] != d and heads > 1):
@@ -525,86 +540,113 @@ def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
     return t.data_ptr(), st[0] if rows > 1 else max(st[0], heads * d)
 
 
-def _pages_on(v, device: int, batch: int, k: Optional[int]) -> KVViewC:
+_VIEW_TENSORS = ("seq_len", "page_table", "free_list", "free_count", "cells", "k_exp", "v_exp")
+
+
+def _view_struct(v, device: int, batch: int, hkv: int, d: int):
+    """The C struct of a view (KVView: its lengths and pages; hkv 0), checked.
+
+    The struct is kept on the view for the next call, and used again as long as the view holds
+    the same tensors, at the same addresses, and the same sizes."""
+    get = v.__dict__.get
+    tensors = tuple([get(f) for f in _VIEW_TENSORS])
+    key = (device, batch, hkv, d, v.capacity, v.page_size,
+           *[0 if t is None else t.data_ptr() for t in tensors])
+    memo = get("_struct")
+    if memo is not None and memo[0] == key and all(map(operator.is_, memo[1], tensors)):
+        return memo[2]
     i32 = torch.int32
     seq = _on(v.seq_len, device, i32, batch, "seq_len")
-    table = v.page_table
+    table, n, k = v.page_table, 0, None
+    if table is not None:
+        if table.dim() != 2 or table.shape[0] != batch:
+            raise ValueError(f"page_table must be [{batch}, max_pages]")
+        n = v.free_list.numel()
+    if hkv:
+        rows, slabs = (v.page_size, n) if table is not None else (v.capacity, batch)
+        k = _on(v.cells, device, torch.uint8, slabs * hkv * (rows // 16) * 18 * d, "cells")
     if table is None:
-        return KVViewC(k, None, seq, None, None, None, v.capacity, 0, 0, 0)
-    if table.dim() != 2 or table.shape[0] != batch:
-        raise ValueError(f"page_table must be [{batch}, max_pages]")
-    n = v.free_list.numel()
-    return KVViewC(k, None, seq, _on(table, device, i32, table.numel(), "page_table"),
-                   _on(v.free_list, device, i32, n, "free_list"),
-                   _on(v.free_count, device, i32, 1, "free_count"),
-                   v.capacity, v.page_size, table.shape[1], n)
+        c = KVViewC(k, None, seq, None, None, None, v.capacity, 0, 0, 0)
+    else:
+        c = KVViewC(k, None, seq, _on(table, device, i32, table.numel(), "page_table"),
+                    _on(v.free_list, device, i32, n, "free_list"),
+                    _on(v.free_count, device, i32, 1, "free_count"),
+                    v.capacity, v.page_size, table.shape[1], n)
+    if hkv:
+        c = KV4ViewC(c, _opt(v.k_exp, device, i32, hkv, "k_exp"),
+                     _opt(v.v_exp, device, i32, hkv, "v_exp"))
+    v.__dict__["_struct"] = (key, tensors, c)
+    return c
 
 
-def _view4_on(v: KV4View, device: int, dims: KV4Dims) -> KV4ViewC:
-    cells = v.cells
-    rows = v.page_size if v.page_table is not None else v.capacity
-    slabs = v.free_list.numel() if v.page_table is not None else dims.batch
-    k = _on(cells, device, torch.uint8,
-            slabs * dims.n_kv_heads * (rows // 16) * 18 * dims.head_dim, "cells")
-    return KV4ViewC(_pages_on(v, device, dims.batch, k),
-                    _on(v.k_exp, device, torch.int32, dims.n_kv_heads, "k_exp"),
-                    _on(v.v_exp, device, torch.int32, dims.n_kv_heads, "v_exp"))
+def _here(stream):
+    """(current device, the stream to launch on)."""
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def dflash_kv_reserve(dims: KV4Dims, cache, n_new, start, pos, slot, new_len, ws, stream=None):
     """Pages, positions and slots of the batch's new rows.  ``cache``: a KVView or KV4View."""
-    dev, i32, b, n = torch.cuda.current_device(), torch.int32, dims.batch, dims.n_tokens
-    view = _pages_on(cache, dev, b, None)
-    _check(load_library().dflash_kv_reserve(
-        dims, view, _on(n_new, dev, i32, b, "n_new"), _on(start, dev, i32, b + 1, "start"),
+    dev, st = _here(stream)
+    i32, b, n = torch.int32, dims.batch, dims.n_tokens
+    rc = load_library().dflash_kv_reserve(
+        dims, _view_struct(cache.pages() if isinstance(cache, KV4View) else cache, dev, b, 0, 0),
+        _on(n_new, dev, i32, b, "n_new"), _on(start, dev, i32, b + 1, "start"),
         _on(pos, dev, i32, n, "pos"), _on(slot, dev, i32, n, "slot"),
-        _on(new_len, dev, i32, b, "new_len"), _on(ws, dev, torch.uint8, 0, "ws", True),
-        ws.numel(), _stream(stream)), "dflash_kv_reserve")
+        _on(new_len, dev, i32, b, "new_len"), *_ws_on(ws, dev), st)
+    if rc:
+        _check(rc, "dflash_kv_reserve")
 
 
 def dflash_qk_norm_rope(dims: KV4Dims, q, k, q_norm_w, k_norm_w, pos, rope_theta: float,
                         rms_eps: float, q_out, k_out, stream=None):
     """Per-head norms of q [N, Hq, D] and k [N, Hkv, D], rotated at ``pos``; rows may be strided."""
-    dev, bf, n, d = torch.cuda.current_device(), torch.bfloat16, dims.n_tokens, dims.head_dim
-    q_p, q_s = _rows_on(q, dev, n, dims.n_q_heads, d, "q")
-    k_p, k_s = _rows_on(k, dev, n, dims.n_kv_heads, d, "k")
-    qo_p, qo_s = _rows_on(q_out, dev, n, dims.n_q_heads, d, "q_out")
-    ko_p, ko_s = _rows_on(k_out, dev, n, dims.n_kv_heads, d, "k_out")
-    _check(load_library().dflash_qk_norm_rope(
-        dims, q_p, q_s, k_p, k_s, _on(q_norm_w, dev, bf, d, "q_norm_w"),
-        _on(k_norm_w, dev, bf, d, "k_norm_w"), _on(pos, dev, torch.int32, n, "pos"), rope_theta,
-        rms_eps, qo_p, qo_s, ko_p, ko_s, _stream(stream)), "dflash_qk_norm_rope")
+    dev, st = _here(stream)
+    bf, n, d, hq, hkv = torch.bfloat16, dims.n_tokens, dims.head_dim, dims.n_q_heads, \
+        dims.n_kv_heads
+    rc = load_library().dflash_qk_norm_rope(
+        dims, *_rows_on(q, dev, n, hq, d, "q"), *_rows_on(k, dev, n, hkv, d, "k"),
+        _opt(q_norm_w, dev, bf, d, "q_norm_w"), _opt(k_norm_w, dev, bf, d, "k_norm_w"),
+        _on(pos, dev, torch.int32, n, "pos"), rope_theta, rms_eps,
+        *_rows_on(q_out, dev, n, hq, d, "q_out"), *_rows_on(k_out, dev, n, hkv, d, "k_out"), st)
+    if rc:
+        _check(rc, "dflash_qk_norm_rope")
 
 
 def dflash_kv4_append(dims: KV4Dims, k, v, slot, cache: KV4View, ws, stream=None):
     """Quantise k, v [N, Hkv, D] (rows may be strided) into the rows ``slot`` of the cache."""
-    dev, n = torch.cuda.current_device(), dims.n_tokens
-    k_p, k_s = _rows_on(k, dev, n, dims.n_kv_heads, dims.head_dim, "k")
-    v_p, v_s = _rows_on(v, dev, n, dims.n_kv_heads, dims.head_dim, "v")
-    _check(load_library().dflash_kv4_append(
-        dims, k_p, k_s, v_p, v_s, _on(slot, dev, torch.int32, n, "slot"),
-        _view4_on(cache, dev, dims), _on(ws, dev, torch.uint8, 0, "ws", True), ws.numel(),
-        _stream(stream)), "dflash_kv4_append")
+    dev, st = _here(stream)
+    n, hkv, d = dims.n_tokens, dims.n_kv_heads, dims.head_dim
+    rc = load_library().dflash_kv4_append(
+        dims, *_rows_on(k, dev, n, hkv, d, "k"), *_rows_on(v, dev, n, hkv, d, "v"),
+        _on(slot, dev, torch.int32, n, "slot"), _view_struct(cache, dev, dims.batch, hkv, d),
+        *_ws_on(ws, dev), st)
+    if rc:
+        _check(rc, "dflash_kv4_append")
 
 
 def dflash_kv4_gather(dims: KV4Dims, slot, cache: KV4View, k_out, v_out, ws, stream=None):
     """Rows ``slot`` of the cache as bf16 [N, Hkv, D]."""
-    dev, bf, n = torch.cuda.current_device(), torch.bfloat16, dims.n_tokens
-    size = n * dims.n_kv_heads * dims.head_dim
-    _check(load_library().dflash_kv4_gather(
-        dims, _on(slot, dev, torch.int32, n, "slot"), _view4_on(cache, dev, dims),
-        _on(k_out, dev, bf, size, "k_out"), _on(v_out, dev, bf, size, "v_out"),
-        _on(ws, dev, torch.uint8, 0, "ws", True), ws.numel(), _stream(stream)),
-        "dflash_kv4_gather")
+    dev, st = _here(stream)
+    bf, n, hkv, d = torch.bfloat16, dims.n_tokens, dims.n_kv_heads, dims.head_dim
+    size = n * hkv * d
+    rc = load_library().dflash_kv4_gather(
+        dims, _on(slot, dev, torch.int32, n, "slot"), _view_struct(cache, dev, dims.batch, hkv, d),
+        _on(k_out, dev, bf, size, "k_out"), _on(v_out, dev, bf, size, "v_out"), *_ws_on(ws, dev),
+        st)
+    if rc:
+        _check(rc, "dflash_kv4_gather")
 
 
 def dflash_kv4_attention(dims: KV4Dims, q, start, cache: KV4View, scale: float, causal: bool, out,
                          ws, stream=None):
     """Attention of the rows q [N, Hq, D] over the 4-bit cache that holds them already."""
-    dev, bf, n = torch.cuda.current_device(), torch.bfloat16, dims.n_tokens
-    size = n * dims.n_q_heads * dims.head_dim
-    _check(load_library().dflash_kv4_attention(
-        dims, _on(q, dev, bf, size, "q"), _on(start, dev, torch.int32, dims.batch + 1, "start"),
-        _view4_on(cache, dev, dims), scale, 1 if causal else 0, _on(out, dev, bf, size, "out"),
-        _on(ws, dev, torch.uint8, 0, "ws", True), ws.numel(), _stream(stream)),
-        "dflash_kv4_attention")
+    dev, st = _here(stream)
+    bf, b, hkv, d = torch.bfloat16, dims.batch, dims.n_kv_heads, dims.head_dim
+    size = dims.n_tokens * dims.n_q_heads * d
+    rc = load_library().dflash_kv4_attention(
+        dims, _on(q, dev, bf, size, "q"), _on(start, dev, torch.int32, b + 1, "start"),
+        _view_struct(cache, dev, b, hkv, d), scale, 1 if causal else 0,
+        _on(out, dev, bf, size, "out"), *_ws_on(ws, dev), st)
+    if rc:
+        _check(rc, "dflash_kv4_attention")
