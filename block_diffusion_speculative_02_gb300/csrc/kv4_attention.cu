@@ -24,9 +24,8 @@
 // row of V^T (the cell keeps V's 16 rows side by side for that), to fp16 (exact:
 // 6 significant bits) straight into TMEM.  With them in shared memory its traffic,
 // not DRAM, would bound the kernel: 128 KB written and read a tile of 18 KB.
-// Q is scaled by a power of two to [1, 2) per row and kept in fp16 (11 bits: exact
-// for bf16 values within 2^-7 of the row's largest, 2^-25 of it for smaller ones);
-// P in fp16 (2^-12 of its value), O, the maximum and the sum in fp32.
+// Q is kept in fp16, where need be times a power of two (exact for bf16 values down to
+// 2^-12 of the unit's largest at least, 2^-23 of it off for smaller ones); P in fp16 (2^-12 of its value), O, the maximum and the sum in fp32.
 // Softmax: a thread owns a key and walks the query columns.  The running maximum m
 // of a column only moves when a tile passes it by 2^8, which one vote per tile
 // finds out; until then exp2(x - m) needs no reduction over keys at all, and the
@@ -688,8 +687,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     __syncwarp();
   } else if (warp < C::kSoft) {
     // ---------------- query rows of a unit, D / 8 lanes a row ----------------
-    // Twice over them: for the largest finite magnitude of all, which goes to [2^14, 2^15),
-    // and to convert.
+    // Converted as they are if the largest finite magnitude lies in [2^-2, 2^15): then
+    // fp16 holds them to 2^-23 of it.  Else a second time, with a power of two that
+    // brings it to [2^14, 2^15).
     constexpr int kPer = D / 8, kItems = NQ * kPer / 64, kLoads = kItems < 8 ? kItems : 8;
     const int tid = threadIdx.x - 32 * kQuery;
     const int pc = tid % kPer;
@@ -705,57 +705,40 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const int rows = min(p.tile_rows, g.T - g.t0) * G;
       const int row0 = (g.lo + g.t0) * p.n_q_heads + g.h * G;
       uint8_t* qs = qbuf + par * C::kQBytes;
-      uint32_t m = 0;
-      float f = 0.f;
+      float f = 1.f;
+      int ex = 0;
+      bool again = true;
 #pragma unroll 1
-      for (int it0 = 0; it0 < 2 * kItems; it0 += kLoads) {
-        const bool second = it0 >= kItems;
-        if (it0 == kItems) {
+      for (int pass = 0; again; ++pass) {
+        uint32_t m = 0;
+#pragma unroll 1
+        for (int it0 = 0; it0 < kItems; it0 += kLoads) {
+          uint4 x[kLoads];
 #pragma unroll
-          for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0) q_max[warp - kQuery] = m;
-          if (seg >= 2) wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
-          named_bar_sync(15, 64);
-          m = max(q_max[0], q_max[1]);
-          const int ex = max(-126, min(126, 141 - static_cast<int>(m >> 7)));
-          f = pow2(ex);
-          if (tid == 0) {
-            Piece pc = {g.tile, g.n, g.nt,
-                        p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows, g.h,
-                        p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h)) * pow2(-ex)};
-            piece[par] = pc;
+          for (int u = 0; u < kLoads; ++u) {
+            const int q = ((it0 + u) * 64 + tid) / kPer, t = q * p.group_inv >> 16;   // q / G
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (q < rows)
+              x[u] = *reinterpret_cast<const uint4*>(
+                  p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D + 8 * pc);
           }
-        }
-        uint4 x[kLoads];
+          if (pass == 0 && it0 == 0 && seg >= 2) wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          const int q = ((it0 - (second ? kItems : 0) + u) * 64 + tid) / kPer;
-          const int t = q * p.group_inv >> 16;                     // q / G
-          x[u] = make_uint4(0, 0, 0, 0);
-          if (q < rows)
-            x[u] = *reinterpret_cast<const uint4*>(
-                p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D + 8 * pc);
-        }
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          if (!second) {
+          for (int u = 0; u < kLoads; ++u) {
+            const int q = ((it0 + u) * 64 + tid) / kPer;
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t a = w[e] & 0x7FFFu, c = w[e] >> 16 & 0x7FFFu;
               m = max(m, max(a < 0x7F80u ? a : 0u, c < 0x7F80u ? c : 0u));
-            }
-          } else {
-            const int q = ((it0 - kItems + u) * 64 + tid) / kPer;
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
               y[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
                               __uint_as_float(w[e] & 0xFFFF0000u) * f);
+            }
             *reinterpret_cast<uint4*>(qs + (pc >> 3) * NQ * 128 + q * 128 +
                                       (((pc & 7) ^ (q & 7)) << 4)) =
                 make_uint4(y[0], y[1], y[2], y[3]);
-            if (pc == 0) {
+            if (pc == 0 && pass == 0) {
               const int t = q * p.group_inv >> 16;
               col_row[par * NQ + q] = row0 + t * p.n_q_heads + q - t * G;
               col_vis[par * NQ + q] =
@@ -763,6 +746,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             }
           }
         }
+        again = false;
+        if (pass == 0) {
+#pragma unroll
+          for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) q_max[warp - kQuery] = m;
+          named_bar_sync(15, 64);
+          const int e = static_cast<int>(max(q_max[0], q_max[1]) >> 7);   // exponent + 127
+          if (e != 0 && (e < 125 || e > 141)) {
+            ex = max(-126, min(126, 141 - e));
+            f = pow2(ex);
+            again = true;
+          }
+        }
+      }
+      if (tid == 0) {
+        Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows,
+                    g.h, p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h)) * pow2(-ex)};
+        piece[par] = pc;
       }
       fence_proxy_async_smem();
       warp_arrive(&q_full[par]);

@@ -2,16 +2,17 @@
 //
 // For 16 consecutive dims x of one head, times the power of two 2^-exp[head]:
 //   scale = e4m3(max |x| / 6),  code = e2m1(x / scale),  x ~ 2^exp scale code.
-// Both quotients are divided with one rounding (IEEE), so a quotient that lies
-// halfway between two codes stays there and rounds to even: x has 8 significant
-// bits, 6 times an e4m3 midpoint 7 and an e2m1 midpoint times a scale 7, so a
-// quotient is either a midpoint or at least 2^-8 of its size away from it.
+// A quotient that lies halfway between two codes has to stay there, to round to even: x has
+// 8 significant bits, 6 times an e4m3 midpoint 7 and an e2m1 midpoint times a scale 7, so
+// a quotient is either a midpoint or at least 2^-8 of its size away from it.  max / 6 is
+// divided (one rounding keeps a midpoint).  x / scale is a product with the scale's
+// reciprocal, within 2^-22 of its size, then rounded to a multiple of 2^-14: midpoints
+// (0.25 and up) are such multiples, and every other quotient up to 6 is 2^-10 or more
+// away from them.  (IEEE divisions for all sixteen took most of the kernel's time.)
 #include "kv4.cuh"
 
 namespace dflash {
 namespace {
-
-constexpr int kThreads = 128;
 
 // Row of the pool -> slab and row in it; false for rows outside it.
 __device__ __forceinline__ bool find_slot(const Kv4Store& s, int slot, int* slab, int* row,
@@ -41,45 +42,98 @@ __device__ __forceinline__ uint2 quantise16(const uint16_t* x, float gain, uint3
   }
   *scale = to_e4m3(__fdiv_rn(m, 6.f));
   if (*scale == 0) return make_uint2(0, 0);
-  const float s = f16x2_to_float2(e4m3x2_to_f16x2(*scale)).x;
+  const float inv = __frcp_rn(f16x2_to_float2(e4m3x2_to_f16x2(*scale)).x);
+  // (an ulp between 512 and 1024 is 2^-14; quotients past 6 saturate, rounded or not)
+  auto snap = [inv](float x) { return __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 768.f), -768.f); };
   uint32_t o[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 16; i += 2)
-    o[i / 8] |= to_e2m1x2(__fdiv_rn(v[i], s), __fdiv_rn(v[i + 1], s)) << (i % 8 * 4);
+    o[i / 8] |= to_e2m1x2(snap(v[i]), snap(v[i + 1])) << (i % 8 * 4);
   return make_uint2(o[0], o[1]);
 }
 
+// Sixteen rows of the batch and one head to a CTA: a thread holds 16 dims of one row of K
+// and V.  Their codes meet in shared memory in the cell's own layout, so that the rows'
+// bytes, which lie 16 apart in a cell of V, leave 16 rows side by side; sixteen rows that
+// are one whole cell leave as it is, 16 bytes a store.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(
+struct CellIo {
+  static constexpr int kG = D / 16;
+  static constexpr int kThreads = kCellRows * kG;
+  static constexpr int kBytes = Cell<D>::kBytes;
+};
+
+// The rows' places; true if they are rows 0 .. 15 of one cell.
+template <int D>
+__device__ __forceinline__ bool find_rows(const Kv4Store& s, const int32_t* slot, long long n0,
+                                          long long n_tokens, int h, uint8_t** cells, int* rows,
+                                          uint32_t* status) {
+  if (threadIdx.x < kCellRows) {
+    uint8_t* c = nullptr;
+    int slab, row = 0;
+    const long long n = n0 + threadIdx.x;
+    if (n < n_tokens && find_slot(s, slot[n], &slab, &row, status))
+      c = s.cells + cell_index(s, slab, h, row) * Cell<D>::kBytes;
+    cells[threadIdx.x] = c;
+    rows[threadIdx.x] = row % kCellRows;
+  }
+  __syncthreads();
+  const int i = threadIdx.x % kCellRows;
+  return __syncthreads_and(cells[0] != nullptr && cells[i] == cells[0] && rows[i] == i);
+}
+
+template <int D>
+__global__ void __launch_bounds__(CellIo<D>::kThreads) kv4_append_kernel(
     const Kv4Store s, const uint16_t* __restrict__ k, long long k_pitch,
     const uint16_t* __restrict__ v, long long v_pitch, const int32_t* __restrict__ slot,
-    long long units, uint32_t* status) {
-  constexpr int kG = D / 16;
+    long long n_tokens, uint32_t* status) {
+  using C = CellIo<D>;
+  __shared__ __align__(16) uint8_t image[C::kBytes];     // row i of the CTA in row i
+  __shared__ uint8_t* cells[kCellRows];
+  __shared__ int rows[kCellRows];
   griddep_wait();
   griddep_launch_dependents();
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= units) return;
-  const int g = static_cast<int>(i % kG);
-  const int h = static_cast<int>(i / kG % s.n_kv_heads);
-  const long long n = i / kG / s.n_kv_heads;
-  int slab, row;
-  if (!find_slot(s, slot[n], &slab, &row, status)) return;
-  uint8_t* cell = s.cells + cell_index(s, slab, h, row) * Cell<D>::kBytes;
-  const int r = row % kCellRows;
-  bool bad = false;
-  uint32_t ks, vs;
-  const uint2 kc = quantise16(k + n * k_pitch + h * D + 16 * g, pow2(-gain_exp(s.k_exp, h)), &ks,
-                              &bad);
-  const uint2 vc = quantise16(v + n * v_pitch + h * D + 16 * g, pow2(-gain_exp(s.v_exp, h)), &vs,
-                              &bad);
-  *reinterpret_cast<uint2*>(cell + Cell<D>::k_codes(r, g)) = kc;
-  cell[Cell<D>::k_scale(r, g)] = static_cast<uint8_t>(ks);
+  // (heads vary fastest: neighbours read and write next to each other)
+  const int h = blockIdx.x % s.n_kv_heads, r = threadIdx.x / C::kG, g = threadIdx.x % C::kG;
+  const long long n0 = static_cast<long long>(blockIdx.x / s.n_kv_heads) * kCellRows, n = n0 + r;
+  const bool whole = find_rows<D>(s, slot, n0, n_tokens, h, cells, rows, status);
+  if (cells[r]) {
+    bool bad = false;
+    uint32_t ks, vs;
+    const uint2 kc = quantise16(k + n * k_pitch + h * D + 16 * g, pow2(-gain_exp(s.k_exp, h)),
+                                &ks, &bad);
+    const uint2 vc = quantise16(v + n * v_pitch + h * D + 16 * g, pow2(-gain_exp(s.v_exp, h)),
+                                &vs, &bad);
+    *reinterpret_cast<uint2*>(image + Cell<D>::k_codes(r, g)) = kc;
+    image[Cell<D>::k_scale(r, g)] = static_cast<uint8_t>(ks);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      image[Cell<D>::v_codes(r, 8 * g + j)] =
+          static_cast<uint8_t>((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
+    image[Cell<D>::v_scale(r, g)] = static_cast<uint8_t>(vs);
+    if (bad) set_status(status, DFLASH_ST_BAD_VALUE);
+  }
+  __syncthreads();
+  if (whole) {
+    for (int i = threadIdx.x; i < C::kBytes / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(cells[0])[i] = reinterpret_cast<const uint4*>(image)[i];
+    return;
+  }
+  // 16 lanes, 16 rows: K in pieces of 16 bytes, its scales in words, V byte by byte
+  const int lr = threadIdx.x % kCellRows, lu = threadIdx.x / kCellRows;
+  uint8_t* cell = cells[lr];
+  if (!cell) return;
+  const int to = rows[lr];
+  for (int i = lu; i < D / 32; i += C::kG)
+    *reinterpret_cast<uint4*>(cell + Cell<D>::k_codes(to, 2 * i)) =
+        *reinterpret_cast<const uint4*>(image + Cell<D>::k_codes(lr, 2 * i));
+  for (int i = lu; i < D / 64; i += C::kG)
+    *reinterpret_cast<uint32_t*>(cell + Cell<D>::k_scale(to, 4 * i)) =
+        *reinterpret_cast<const uint32_t*>(image + Cell<D>::k_scale(lr, 4 * i));
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    cell[Cell<D>::v_codes(r, 8 * g + j)] =
-        static_cast<uint8_t>((j < 4 ? vc.x : vc.y) >> (8 * (j & 3)));
-  cell[Cell<D>::v_scale(r, g)] = static_cast<uint8_t>(vs);
-  if (bad) set_status(status, DFLASH_ST_BAD_VALUE);
+    cell[Cell<D>::v_codes(to, lu + j * C::kG)] = image[Cell<D>::v_codes(lr, lu + j * C::kG)];
+  cell[Cell<D>::v_scale(to, lu)] = image[Cell<D>::v_scale(lr, lu)];
 }
 
 // Eight codes with their scale and gain as eight bf16 (exact).
@@ -96,31 +150,51 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, float f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_gather_kernel(
+__global__ void __launch_bounds__(CellIo<D>::kThreads) kv4_gather_kernel(
     const Kv4Store s, const int32_t* __restrict__ slot, uint16_t* __restrict__ k,
-    uint16_t* __restrict__ v, long long units, uint32_t* status) {
-  constexpr int kG = D / 16;
+    uint16_t* __restrict__ v, long long n_tokens, uint32_t* status) {
+  using C = CellIo<D>;
+  __shared__ __align__(16) uint8_t image[C::kBytes];
+  __shared__ uint8_t* cells[kCellRows];
+  __shared__ int rows[kCellRows];
   griddep_wait();
   griddep_launch_dependents();
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= units) return;
-  const int g = static_cast<int>(i % kG);
-  const int h = static_cast<int>(i / kG % s.n_kv_heads);
-  const long long n = i / kG / s.n_kv_heads;
-  int slab, row;
-  if (!find_slot(s, slot[n], &slab, &row, status)) return;
-  const uint8_t* cell = s.cells + cell_index(s, slab, h, row) * Cell<D>::kBytes;
-  const int r = row % kCellRows;
-  const uint2 kc = *reinterpret_cast<const uint2*>(cell + Cell<D>::k_codes(r, g));
+  const int h = blockIdx.x % s.n_kv_heads;
+  const long long n0 = static_cast<long long>(blockIdx.x / s.n_kv_heads) * kCellRows;
+  if (find_rows<D>(s, slot, n0, n_tokens, h, cells, rows, status)) {
+    for (int i = threadIdx.x; i < C::kBytes / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(image)[i] = reinterpret_cast<const uint4*>(cells[0])[i];
+  } else {
+    const int lr = threadIdx.x % kCellRows, lu = threadIdx.x / kCellRows;
+    const uint8_t* cell = cells[lr];
+    if (cell) {
+      const int to = rows[lr];
+      for (int i = lu; i < D / 32; i += C::kG)
+        *reinterpret_cast<uint4*>(image + Cell<D>::k_codes(lr, 2 * i)) =
+            *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(to, 2 * i));
+      for (int i = lu; i < D / 64; i += C::kG)
+        *reinterpret_cast<uint32_t*>(image + Cell<D>::k_scale(lr, 4 * i)) =
+            *reinterpret_cast<const uint32_t*>(cell + Cell<D>::k_scale(to, 4 * i));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        image[Cell<D>::v_codes(lr, lu + j * C::kG)] = cell[Cell<D>::v_codes(to, lu + j * C::kG)];
+      image[Cell<D>::v_scale(lr, lu)] = cell[Cell<D>::v_scale(to, lu)];
+    }
+  }
+  __syncthreads();
+  const int r = threadIdx.x / C::kG, g = threadIdx.x % C::kG;
+  if (!cells[r]) return;
+  const uint2 kc = *reinterpret_cast<const uint2*>(image + Cell<D>::k_codes(r, g));
   uint32_t vc[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    vc[j / 4] |= static_cast<uint32_t>(cell[Cell<D>::v_codes(r, 8 * g + j)]) << (8 * (j & 3));
-  const uint32_t sc = cell[Cell<D>::k_scale(r, g)] | cell[Cell<D>::v_scale(r, g)] << 8;
+    vc[j / 4] |= static_cast<uint32_t>(image[Cell<D>::v_codes(r, 8 * g + j)]) << (8 * (j & 3));
+  const uint32_t sc = image[Cell<D>::k_scale(r, g)] | image[Cell<D>::v_scale(r, g)] << 8;
   const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(sc));
   const float fk = f.x * pow2(gain_exp(s.k_exp, h)), fv = f.y * pow2(gain_exp(s.v_exp, h));
-  uint4* ko = reinterpret_cast<uint4*>(k + (n * s.n_kv_heads + h) * D + 16 * g);
-  uint4* vo = reinterpret_cast<uint4*>(v + (n * s.n_kv_heads + h) * D + 16 * g);
+  const size_t at = (static_cast<size_t>(n0 + r) * s.n_kv_heads + h) * D + 16 * g;
+  uint4* ko = reinterpret_cast<uint4*>(k + at);
+  uint4* vo = reinterpret_cast<uint4*>(v + at);
   ko[0] = values8(kc.x, fk);
   ko[1] = values8(kc.y, fk);
   vo[0] = values8(vc[0], fv);
@@ -173,16 +247,17 @@ extern "C" int dflash_kv4_append(const dflash_kv4_dims* dims, const void* k, int
   if (k_pitch < width || v_pitch < width) return DFLASH_E_ARG;
   if (((k_pitch | v_pitch) & 7) || !aligned16(k) || !aligned16(v)) return DFLASH_E_ALIGN;
   if (!ws || ws_bytes < 64) return DFLASH_E_WORKSPACE;
-  const long long units =
-      static_cast<long long>(dims->n_tokens) * dims->n_kv_heads * (dims->head_dim / 16);
-  const long long ctas = (units + kThreads - 1) / kThreads;
+  const long long ctas =
+      static_cast<long long>((dims->n_tokens - 1) / kCellRows + 1) * dims->n_kv_heads;
   if (ctas > INT32_MAX) return DFLASH_E_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(ctas)), block(kThreads);
+  const dim3 grid(static_cast<unsigned>(ctas));
+  const dim3 block(kCellRows * (dims->head_dim / 16));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto* kernel = dims->head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>;
   return launch(kernel, grid, block, 0, st, s, static_cast<const uint16_t*>(k),
                 static_cast<long long>(k_pitch), static_cast<const uint16_t*>(v),
-                static_cast<long long>(v_pitch), slot, units, ws_at<uint32_t>(ws, 0));
+                static_cast<long long>(v_pitch), slot,
+                static_cast<long long>(dims->n_tokens), ws_at<uint32_t>(ws, 0));
 }
 
 extern "C" int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slot,
@@ -196,13 +271,13 @@ extern "C" int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slo
   if ((rc = kv4_store(*dims, cache, &s))) return rc;
   if (!aligned16(k_out) || !aligned16(v_out)) return DFLASH_E_ALIGN;
   if (!ws || ws_bytes < 64) return DFLASH_E_WORKSPACE;
-  const long long units =
-      static_cast<long long>(dims->n_tokens) * dims->n_kv_heads * (dims->head_dim / 16);
-  const long long ctas = (units + kThreads - 1) / kThreads;
+  const long long ctas =
+      static_cast<long long>((dims->n_tokens - 1) / kCellRows + 1) * dims->n_kv_heads;
   if (ctas > INT32_MAX) return DFLASH_E_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(ctas)), block(kThreads);
+  const dim3 grid(static_cast<unsigned>(ctas));
+  const dim3 block(kCellRows * (dims->head_dim / 16));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto* kernel = dims->head_dim == 128 ? kv4_gather_kernel<128> : kv4_gather_kernel<64>;
   return launch(kernel, grid, block, 0, st, s, slot, static_cast<uint16_t*>(k_out),
-                static_cast<uint16_t*>(v_out), units, ws_at<uint32_t>(ws, 0));
+                static_cast<uint16_t*>(v_out), static_cast<long long>(dims->n_tokens), ws_at<uint32_t>(ws, 0));
 }

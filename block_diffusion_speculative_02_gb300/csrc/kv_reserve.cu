@@ -4,7 +4,10 @@
 // cut back to the committed length; with paged caches that takes pages from the
 // pool and gives them back (the crop).
 //
-// Two launches.  The first counts, one CTA per sequence, the pages the new rows
+// Small batches (at most 256 sequences and 8192 rows) take one CTA, a warp to a sequence:
+// the pages that the new rows lack are counted, the counts added up, the pages taken and
+// the maps written in one launch, whose time is launch and latency.
+// Larger ones take two launches.  The first counts, one CTA per sequence, the pages the new rows
 // lack; the second adds up the counts of the sequences before its own (that,
 // not an atomic counter, decides which page of the free list a row gets, so
 // the tables depend on the lengths alone), takes the pages, and writes the
@@ -173,6 +176,128 @@ __global__ void __launch_bounds__(kThreads) reserve_assign_kernel(const ReserveP
   griddep_launch_dependents();
 }
 
+// ---- small batches: everything in one CTA ----
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallBatch = 256;
+constexpr int kSmallRows = 8192;
+
+__global__ void __launch_bounds__(kSmallThreads) reserve_small_kernel(const ReserveParams p) {
+  __shared__ int first[kSmallBatch + 1];   // rows before the sequence
+  __shared__ int base[kSmallBatch];        // pages taken before it; -1: not served
+  __shared__ int need[kSmallBatch];
+  __shared__ int s_avail;
+  griddep_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 0) {                         // rows: an exclusive sum over the sequences
+    long long at = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const long long n = b < p.batch ? max(p.n_new[b], 0) : 0;
+      long long inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (b < p.batch)
+        first[b] = static_cast<int>(min(at + inc - n, static_cast<long long>(INT32_MAX)));
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      first[p.batch] = static_cast<int>(min(at, static_cast<long long>(INT32_MAX)));
+      s_avail = p.paged ? max(0, min(*p.free_count, p.n_pages)) : 0;
+    }
+  }
+  __syncthreads();
+  for (int b = warp; b < p.batch; b += kSmallThreads / 32) {
+    const int n = p.n_new[b], len = p.seq_len[b];
+    const bool ok = n >= 0 && n <= p.max_tokens && len >= 0 && len <= p.limit &&
+                    n <= p.limit - len && first[b] <= p.n_tokens - n;
+    int missing = 0;
+    if (ok && n > 0 && p.paged) {
+      const int32_t* row = p.page_table + static_cast<size_t>(b) * p.max_pages;
+      const int last = (len + n - 1) / p.page_size;
+      for (int pg = len / p.page_size + lane; pg <= last; pg += 32) missing += row[pg] < 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) missing += __shfl_xor_sync(0xffffffffu, missing, o);
+    }
+    if (lane == 0) {
+      need[b] = ok ? missing : kInvalid;
+      if (!ok) set_status(p.status, DFLASH_ST_CAPACITY);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {                         // pages: in order, what fits
+    const int avail = s_avail;
+    int at = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane, x = b < p.batch ? max(need[b], 0) : 0;
+      int inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const int all = __shfl_sync(0xffffffffu, inc, 31);
+      if (!p.paged || all <= avail - at) {
+        if (b < p.batch) base[b] = need[b] == kInvalid ? -1 : at + inc - x;
+        at += all;
+      } else {                             // one by one
+        for (int l = 0; l < 32 && b0 + l < p.batch; ++l) {
+          const int y = __shfl_sync(0xffffffffu, x, l);
+          const bool fits = y <= avail - at;
+          if (lane == l) {
+            base[b] = need[b] == kInvalid || !fits ? -1 : at;
+            if (!fits) set_status(p.status, DFLASH_ST_POOL_EMPTY);
+          }
+          if (fits) at += y;
+        }
+      }
+    }
+    if (lane == 0 && p.paged) *p.free_count = avail - at;
+  }
+  __syncthreads();
+  for (int b = warp; b < p.batch; b += kSmallThreads / 32) {
+    const bool served = base[b] >= 0;
+    const int n = max(p.n_new[b], 0), len = p.seq_len[b], row0 = first[b];
+    int32_t* row = p.page_table + static_cast<size_t>(b) * p.max_pages;
+    if (served && n > 0 && p.paged) {
+      const int last = (len + n - 1) / p.page_size;
+      int taken = base[b];
+      for (int pg0 = len / p.page_size; pg0 <= last; pg0 += 32) {
+        const int pg = pg0 + lane;
+        const bool miss = pg <= last && row[pg] < 0;
+        const uint32_t votes = __ballot_sync(0xffffffffu, miss);
+        if (miss)
+          row[pg] = p.free_list[s_avail - 1 - (taken + __popc(votes & ((1u << lane) - 1u)))];
+        taken += __popc(votes);
+      }
+      __syncwarp();
+    }
+    for (int i = lane; i < n && row0 + i < p.n_tokens; i += 32) {
+      int pos = -1, slot = -1;
+      if (served) {
+        pos = len + i;
+        slot = p.paged ? row[pos / p.page_size] * p.page_size + pos % p.page_size
+                       : b * p.limit + pos;
+      }
+      p.pos[row0 + i] = pos;
+      p.slot[row0 + i] = slot;
+    }
+    __syncwarp();                          // (new_len may be seq_len)
+    if (lane == 0) {
+      p.start[b] = row0;
+      p.new_len[b] = served ? len + n : len;
+    }
+  }
+  for (int i = first[p.batch] + tid; i < p.n_tokens; i += kSmallThreads) {
+    p.pos[i] = -1;                         // rows behind the last sequence
+    p.slot[i] = -1;
+  }
+  if (tid == 0) p.start[p.batch] = first[p.batch];
+  griddep_launch_dependents();
+}
+
 }  // namespace
 
 int check_kv4_dims(const dflash_kv4_dims* d) {
@@ -254,6 +379,8 @@ extern "C" int dflash_kv_reserve(const dflash_kv4_dims* dims, const dflash_kv_vi
   p.need = ws_at<int32_t>(ws, plan.off_need);
   p.status = ws_at<uint32_t>(ws, plan.off_status);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p.batch <= kSmallBatch && p.n_tokens <= kSmallRows)
+    return launch(reserve_small_kernel, dim3(1), dim3(kSmallThreads), 0, st, p);
   if ((rc = launch(reserve_count_kernel, dim3(p.batch), dim3(kThreads), 0, st, p))) return rc;
   return launch(reserve_assign_kernel, dim3(p.batch), dim3(kThreads), 0, st, p);
 }

@@ -33,17 +33,46 @@ struct NormRopeParams {
   TurnTable turns;
 };
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 
-// One CTA per row: 16 threads a head, each with D/32 dims of either half.
+// One CTA per row: 16 threads a head, each with D/32 dims of either half (8 or 4 bytes at
+// a time, both halves of a rotated pair in one thread), kBatch heads in flight.  Bound
+// by the 4 bytes an element moves.
 template <int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopeParams p) {
-  constexpr int kHalf = D / 2, kE = kHalf / 16;
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const NormRopeParams p) {
+  constexpr int kHalf = D / 2, kE = kHalf / 16, kW = kE / 2, kBatch = 3;
   __shared__ float2 sc[kHalf];
   griddep_wait();
   griddep_launch_dependents();
-  const int n = blockIdx.x;
+  const long long n = blockIdx.x;
   const int pos = p.pos[n];
+  const int l = threadIdx.x & 15, d0 = l * kE;
+  const int total = p.heads[0] + p.heads[1];
+  uint32_t x[kBatch][2][kW];             // of a head: both halves, two dims to a word
+  auto place = [&](int hh, int* which) {
+    *which = hh >= p.heads[0];
+    return static_cast<long long>(hh - (*which ? p.heads[0] : 0)) * D + d0;
+  };
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int hh = h0 + u * (kThreads / 16);
+      if (hh >= total) continue;
+      int which;
+      const long long at = place(hh, &which);
+      const uint16_t* src = p.x[which] + n * p.x_pitch[which] + at;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (kW == 2)
+          *reinterpret_cast<uint2*>(x[u][half]) =
+              *reinterpret_cast<const uint2*>(src + half * kHalf);
+        else
+          x[u][half][0] = *reinterpret_cast<const uint32_t*>(src + half * kHalf);
+      }
+    }
+  };
+  const int h_first = threadIdx.x >> 4;
+  load(h_first);                         // (before the position is known to be one)
   if (pos < 0) return;
   for (int d = threadIdx.x; d < kHalf; d += kThreads) {
     const unsigned long long turns = p.turns.f[d] * static_cast<unsigned long long>(pos);
@@ -53,38 +82,65 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormRopePa
     sincospif(a, &sn, &cs);
     sc[d] = make_float2(cs, sn);
   }
-  __syncthreads();
-  const int l = threadIdx.x & 15, d0 = l * kE;
-  const int total = p.heads[0] + p.heads[1];
-  // (whole warps run the same number of times: a warp holds two heads)
-  for (int hh = threadIdx.x >> 4; hh < ((total + 1) & ~1); hh += kThreads / 16) {
-    const bool live = hh < total;
-    const int which = live && hh >= p.heads[0], h = live ? hh - (which ? p.heads[0] : 0) : 0;
-    const uint16_t* x = p.x[which] + n * p.x_pitch[which] + static_cast<long long>(h) * D;
-    float a[kE], b[kE];
-    float ss = 0.f;
+  float2 cs[kE];
+  float w[2][2][kE];                     // gains: q or k, half, dim
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      a[i] = bf16_bits_to_float(x[d0 + i]);
-      b[i] = bf16_bits_to_float(x[kHalf + d0 + i]);
-      ss += a[i] * a[i] + b[i] * b[i];
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      w[i][0][e] = p.w[i] ? bf16_bits_to_float(p.w[i][d0 + e]) : 1.f;
+      w[i][1][e] = p.w[i] ? bf16_bits_to_float(p.w[i][kHalf + d0 + e]) : 1.f;
     }
+  __syncthreads();
 #pragma unroll
-    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const uint16_t* w = p.w[which];
-    const float r = w ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
-    uint16_t* y = p.y[which] + n * p.y_pitch[which] + static_cast<long long>(h) * D;
+  for (int e = 0; e < kE; ++e) cs[e] = sc[d0 + e];
+  for (int h0 = h_first; h0 < ((total + 1) & ~1); h0 += kBatch * (kThreads / 16)) {
+    if (h0 != h_first) load(h0);
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      float u = a[i], v = b[i];
-      if (w) {
-        u *= r * bf16_bits_to_float(w[d0 + i]);
-        v *= r * bf16_bits_to_float(w[kHalf + d0 + i]);
+    for (int u = 0; u < kBatch; ++u) {
+      // (whole warps go on together: a warp holds two heads)
+      const int hh = h0 + u * (kThreads / 16);
+      if (hh >= ((total + 1) & ~1)) break;
+      const bool live = hh < total;
+      int which;
+      const long long at = place(live ? hh : 0, &which);
+      float a[kE], b[kE], ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const uint32_t lo = x[u][0][e / 2], hi = x[u][1][e / 2];
+        a[e] = __uint_as_float(e & 1 ? lo & 0xFFFF0000u : lo << 16);
+        b[e] = __uint_as_float(e & 1 ? hi & 0xFFFF0000u : hi << 16);
+        if (!live) a[e] = b[e] = 0.f;
+        ss += a[e] * a[e] + b[e] * b[e];
       }
-      const float2 cs = sc[d0 + i];
+#pragma unroll
+      for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = p.w[which] ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
+      uint32_t y[2][kW];
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        float o0[2], o1[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float g = a[e + i] * (r * (which ? w[1][0][e + i] : w[0][0][e + i]));
+          const float v = b[e + i] * (r * (which ? w[1][1][e + i] : w[0][1][e + i]));
+          o0[i] = g * cs[e + i].x - v * cs[e + i].y;
+          o1[i] = v * cs[e + i].x + g * cs[e + i].y;
+        }
+        y[0][e / 2] = static_cast<uint32_t>(float_to_bf16_bits(o0[0])) |
+                      static_cast<uint32_t>(float_to_bf16_bits(o0[1])) << 16;
+        y[1][e / 2] = static_cast<uint32_t>(float_to_bf16_bits(o1[0])) |
+                      static_cast<uint32_t>(float_to_bf16_bits(o1[1])) << 16;
+      }
       if (live) {
-        y[d0 + i] = float_to_bf16_bits(u * cs.x - v * cs.y);
-        y[kHalf + d0 + i] = float_to_bf16_bits(v * cs.x + u * cs.y);
+        uint16_t* dst = p.y[which] + n * p.y_pitch[which] + at;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (kW == 2)
+            *reinterpret_cast<uint2*>(dst + half * kHalf) = make_uint2(y[half][0], y[half][kW - 1]);
+          else
+            *reinterpret_cast<uint32_t*>(dst + half * kHalf) = y[half][0];
+        }
       }
     }
   }
