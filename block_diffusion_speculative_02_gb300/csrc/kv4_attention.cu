@@ -56,7 +56,7 @@ struct Cfg {
   // a role grows by sharing out dims (K), cells (V^T) or query columns (softmax).  Few
   // query rows leave the expansion of K and V as the longest step: two each then.
   static constexpr int kKWgs = NQ <= 32 ? 2 : 1;
-  static constexpr int kVWgs = 2;
+  static constexpr int kVWgs = NQ <= 64 ? 2 : 1;
   static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
   static constexpr int kVWarps = D / 32;               // warps of it that hold rows of V^T
@@ -67,12 +67,13 @@ struct Cfg {
   // Registers: the launch's share, and what the roles make of it (0: left alone).  The
   // softmax holds scores, sums and maxima of its columns.
   static constexpr int kRegsSoft = NQ == 16 ? 0 : NQ == 128 ? 80 : 128;
-  static constexpr int kRegsRest = NQ == 128 ? 48 : 56;
+  static constexpr int kRegsRest = 56;
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static_assert(kRegsSoft * 128 * kSoftWgs + kRegsRest * (kThreads - 128 * kSoftWgs) <=
                     kRegsLaunch * kThreads,
                 "register split");
-  static constexpr bool kKeep = NQ <= 64;              // scores and maxima in registers too
+  static constexpr bool kKeepMax = NQ <= 64;           // maxima in registers too
+  static constexpr bool kKeep = true;                  // and scores
   // TMEM columns
   static constexpr int kKCols = D / 2, kVCols = kTile / 2;
   static constexpr int kSBufs = NQ <= 64 ? 2 : 1;
@@ -880,7 +881,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // ---------------- softmax: a thread owns a key ----------------
     if (C::kRegsSoft) regs_up<C::kRegsSoft ? C::kRegsSoft : 24>();
     constexpr int CW = C::kCols;
-    constexpr bool kKeep = C::kKeep;
+    constexpr bool kKeep = C::kKeep, kKeepMax = C::kKeepMax;
     const int wg = (warp - C::kSoft) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, col0 = wg * CW;
     const uint32_t bar = 1 + wg;
@@ -897,7 +898,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       if (bar_or(bar, 128, wait.dead)) break;
       const int n = piece[par].n, tile0 = piece[par].tile, sure = piece[par].sure;
       const float scale = piece[par].scale;
-      float2 l[CW / 2], mr[kKeep ? CW / 2 : 1];        // sums; kLift - maxima
+      float2 l[CW / 2], mr[kKeepMax ? CW / 2 : 1];        // sums; kLift - maxima
 #pragma unroll
       for (int c = 0; c < CW / 2; ++c) l[c] = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -916,9 +917,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           for (int e = 0; e < 16; e += 4) {
             float2 m0 = make_float2(0.f, 0.f), m1 = m0;
             if (sub) {
-              if (kKeep) {
-                m0 = mr[kKeep ? (c0 + e) / 2 : 0];
-                m1 = mr[kKeep ? (c0 + e) / 2 + 1 : 0];
+              if (kKeepMax) {
+                m0 = mr[kKeepMax ? (c0 + e) / 2 : 0];
+                m1 = mr[kKeepMax ? (c0 + e) / 2 + 1 : 0];
               } else {
                 const float4 m = *reinterpret_cast<const float4*>(nm + c0 + e);
                 m0 = make_float2(m.x, m.y);
@@ -1015,12 +1016,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             for (int c = 0; c < CW / 2; ++c)
               l[c] = __fmul2_rn(l[c], *reinterpret_cast<const float2*>(fac + 2 * c));
           }
-          if (kKeep) {
+          if (kKeepMax) {
 #pragma unroll
-            for (int c = 0; c < (kKeep ? CW / 2 : 0); ++c)
+            for (int c = 0; c < (kKeepMax ? CW / 2 : 0); ++c)
               mr[c] = *reinterpret_cast<const float2*>(nm + 2 * c);
-            load_all();
           }
+          if (kKeep) load_all();
+        }
+        if (kKeep && C::kSBufs == 1) {
+          tc_fence_before();
+          warp_arrive(s_empty);
         }
         // (the P buffer is free: the products run in order, and S of this tile came after
         // the P V of two tiles back)
