@@ -100,6 +100,9 @@ struct Kv4AttnParams {
   Kv4Store s;
   int batch, n_tokens, max_tokens, n_q_heads, group, causal;
   int tile_rows;             // rows of a sequence in one unit
+  // A unit also costs some tiles' time that is not tiles (its query rows, the first
+  // maxima, the drain of its O): the runs are cut from tiles plus those.
+  int unit_cost;
   int group_inv;             // ceil(2^16 / group): x * group_inv >> 16 = x / group, x < 128
   int paged, page_size, max_pages, limit;
   const int32_t* seq_len;
@@ -143,10 +146,6 @@ __device__ __forceinline__ int unit_end(const Kv4AttnParams& p, const Seq& s, in
 }
 __device__ __forceinline__ int unit_tiles(int end) { return max(1, (end + kTile - 1) / kTile); }
 
-// A unit also costs kUnitCost tiles of time that are not tiles (its query rows, the
-// drain of its O); the run of a CTA is cut from tiles plus those.
-constexpr int kUnitCost = 2;
-
 __device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const Seq& s) {
   long long n = 0;
   if (!p.causal) {
@@ -155,7 +154,7 @@ __device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const Seq&
 #pragma unroll 1
     for (int i = 0; i < s.n_qt; ++i) n += unit_tiles(unit_end(p, s, i));
   }
-  return (n + static_cast<long long>(s.n_qt) * kUnitCost) * p.s.n_kv_heads;
+  return (n + static_cast<long long>(s.n_qt) * p.unit_cost) * p.s.n_kv_heads;
 }
 
 // One segment: consecutive tiles of one unit.
@@ -253,19 +252,19 @@ struct Walk {
     off = here - before;
     unit(p);
 #pragma unroll 1
-    while (off >= (nt + kUnitCost) * p.s.n_kv_heads) {
-      off -= (nt + kUnitCost) * p.s.n_kv_heads;
+    while (off >= (nt + p.unit_cost) * p.s.n_kv_heads) {
+      off -= (nt + p.unit_cost) * p.s.n_kv_heads;
       ++qt;
       unit(p);
     }
-    h = off / (nt + kUnitCost);
-    off -= h * (nt + kUnitCost);
+    h = off / (nt + p.unit_cost);
+    off -= h * (nt + p.unit_cost);
   }
 
   __device__ __forceinline__ bool next(const Kv4AttnParams& p, Seg* g) {
 #pragma unroll 1
     while (left > 0) {
-      if (off == nt + kUnitCost) {        // the unit after this one
+      if (off == nt + p.unit_cost) {        // the unit after this one
         off = 0;
         if (++h == p.s.n_kv_heads) {
           h = 0;
@@ -278,8 +277,8 @@ struct Walk {
           unit(p);
         }
       }
-      const int take = min(left, nt + kUnitCost - off);
-      const int from = max(0, off - kUnitCost), to = off + take - kUnitCost;
+      const int take = min(left, nt + p.unit_cost - off);
+      const int from = max(0, off - p.unit_cost), to = off + take - p.unit_cost;
       off += take;
       left -= take;
       here += take;
@@ -1383,8 +1382,9 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
       nm[x][0] = nm[x][1] = kLift - kNoMax;
     }
     const int kr = 4 * (gl >> 1) + (gl & 1);                // S^T rows g, g + 8: keys kr, kr + 2
-    // the scale byte of this thread's dims, twice, of two pieces' four
-    const uint32_t pick0 = t & 2 ? 0x4411u : 0x4400u, pick1 = t & 2 ? 0x4433u : 0x4422u;
+    // this warp's slice of `join`, free until the segment ends: [key][group], [group][key / 2]
+    uint32_t* k_sc = reinterpret_cast<uint32_t*>(join + warp * C::kRows * C::kPitch);
+    uint32_t* v_sc = k_sc + D;
 #pragma unroll 1
     for (int c = warp; c < r.cells; c += C::kWarps, ++done) {
       const int st = done % C::kStages;
@@ -1398,12 +1398,27 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
       for (int x = 0; x < kTiles; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[x][e] = s_odd[x][e] = 0.f;
-      uint32_t ks[2][kP / 2];
+      // every scale to fp16 once, by all lanes, for the eight that share it: those of K
+      // doubled, those of V in pairs of keys (0 past the length; codes are finite
+      // whatever they hold)
+      const int left = r.end - key0;
 #pragma unroll
-      for (int i = 0; i < kP / 2; ++i) {
-        ks[0][i] = word(cell + Cell<D>::k_scale(kr, 4 * i));
-        ks[1][i] = word(cell + Cell<D>::k_scale(kr + 2, 4 * i));
+      for (int i = 0; i < D / 128 + (D < 128); ++i) {
+        const int w = i * 32 + lane;                        // four scales each
+        if (w < D / 4) {
+          const uint32_t ks = word(cell + Cell<D>::kKScale + 4 * w);
+          const uint32_t a = e4m3x2_to_f16x2(ks), b = e4m3x2_to_f16x2(ks >> 16);
+          *reinterpret_cast<uint4*>(k_sc + 4 * w) =
+              make_uint4(__byte_perm(a, 0, 0x1010), __byte_perm(a, 0, 0x3232),
+                         __byte_perm(b, 0, 0x1010), __byte_perm(b, 0, 0x3232));
+          const int in = left - 4 * (w & 3);                // of these four keys
+          const uint32_t vs = word(cell + Cell<D>::kVScale + 4 * w) &
+                              (in >= 4 ? ~0u : in > 0 ? (1u << 8 * in) - 1u : 0u);
+          *reinterpret_cast<uint2*>(v_sc + 2 * w) =
+              make_uint2(e4m3x2_to_f16x2(vs), e4m3x2_to_f16x2(vs >> 16));
+        }
       }
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i < kP; ++i) {
         uint32_t a[2][4];                                   // step; a0 .. a3
@@ -1411,7 +1426,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
         for (int u = 0; u < 2; ++u) {
           const uint32_t w = word(cell + i * 256 + (kr + 2 * u) * 16 + 4 * t);
           const uint32_t up = w >> 8;
-          const uint32_t f = e4m3x2_to_f16x2(__byte_perm(ks[u][i / 2], 0, i & 1 ? pick1 : pick0));
+          const uint32_t f = k_sc[(kr + 2 * u) * (D / 16) + 2 * i + (t >> 1)];
           a[0][u] = hmul2(e2m1x2_to_f16x2<0>(w), f);
           a[0][2 + u] = hmul2(e2m1x2_to_f16x2<0>(up), f);
           a[1][u] = hmul2(e2m1x2_to_f16x2<2>(w), f);
@@ -1480,14 +1495,11 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
                        : "r"(pack_f16(p0, p1)));
         }
       // ---- O^T += V^T P^T ----
-      const int left = r.end - key0 - 4 * t;                // of this thread's four keys
-      const uint32_t in_use = left >= 4 ? ~0u : left > 0 ? (1u << 8 * left) - 1u : 0u;
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
         const uint32_t w = word(cell + Cell<D>::kV + (8 * i + gl) * 16 + 4 * t);
-        // (scales of rows past the length become 0; codes are finite whatever they hold)
-        const uint32_t vs = word(cell + Cell<D>::v_scale(4 * t, i)) & in_use;
-        const uint32_t f0 = e4m3x2_to_f16x2(vs), f1 = e4m3x2_to_f16x2(vs >> 16);
+        const uint2 f = *reinterpret_cast<const uint2*>(v_sc + 8 * i + 2 * t);
+        const uint32_t f0 = f.x, f1 = f.y;
         // low (even dim) and high nibbles of two keys to a byte, bytes 0 and 2
         const uint32_t w4 = w >> 4, w8 = w >> 8;
         const uint32_t lo = (w & 0x000F000Fu) | (w4 & ~0x000F000Fu);
@@ -1723,6 +1735,11 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.causal = causal != 0;
   p.tile_rows = a.nq / p.group;
   p.group_inv = (65536 + p.group - 1) / p.group;
+  // Measured in tiles: with 2, 4, 5, 6, 8, 10 of them prompt chunks (128 columns) took 330,
+  // 235, 206, 191, 194, 199 us and a prompt of 4096 rows 414, 295, 267, 246, 247, 252; with
+  // 2, 4, 6, 8 blocks of 16 rows at batch 32 (64 columns) 134, 132, 134, 138 and single
+  // rows 91, 88, 89, 91.
+  p.unit_cost = a.nq == 128 ? 6 : 4;
   p.paged = cache->kv.page_table != nullptr;
   p.page_size = cache->kv.page_size;
   p.max_pages = cache->kv.max_pages;
