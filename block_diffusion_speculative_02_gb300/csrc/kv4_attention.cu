@@ -1382,7 +1382,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
       nm[x][0] = nm[x][1] = kLift - kNoMax;
     }
     const int kr = 4 * (gl >> 1) + (gl & 1);                // S^T rows g, g + 8: keys kr, kr + 2
-    // this warp's slice of `join`, free until the segment ends: [key][group], [group][key / 2]
+    // this warp's slice of `join`, free until the segment ends: [group][key], [group][key / 2]
     uint32_t* k_sc = reinterpret_cast<uint32_t*>(join + warp * C::kRows * C::kPitch);
     uint32_t* v_sc = k_sc + D;
 #pragma unroll 1
@@ -1408,9 +1408,12 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
         if (w < D / 4) {
           const uint32_t ks = word(cell + Cell<D>::kKScale + 4 * w);
           const uint32_t a = e4m3x2_to_f16x2(ks), b = e4m3x2_to_f16x2(ks >> 16);
-          *reinterpret_cast<uint4*>(k_sc + 4 * w) =
-              make_uint4(__byte_perm(a, 0, 0x1010), __byte_perm(a, 0, 0x3232),
-                         __byte_perm(b, 0, 0x1010), __byte_perm(b, 0, 0x3232));
+          constexpr int kW = D / 64;                        // words of a key
+          uint32_t* to = k_sc + w % kW * 64 + w / kW;
+          to[0] = __byte_perm(a, 0, 0x1010);
+          to[16] = __byte_perm(a, 0, 0x3232);
+          to[32] = __byte_perm(b, 0, 0x1010);
+          to[48] = __byte_perm(b, 0, 0x3232);
           const int in = left - 4 * (w & 3);                // of these four keys
           const uint32_t vs = word(cell + Cell<D>::kVScale + 4 * w) &
                               (in >= 4 ? ~0u : in > 0 ? (1u << 8 * in) - 1u : 0u);
@@ -1426,7 +1429,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
         for (int u = 0; u < 2; ++u) {
           const uint32_t w = word(cell + i * 256 + (kr + 2 * u) * 16 + 4 * t);
           const uint32_t up = w >> 8;
-          const uint32_t f = k_sc[(kr + 2 * u) * (D / 16) + 2 * i + (t >> 1)];
+          const uint32_t f = k_sc[(2 * i + (t >> 1)) * 16 + kr + 2 * u];
           a[0][u] = hmul2(e2m1x2_to_f16x2<0>(w), f);
           a[0][2 + u] = hmul2(e2m1x2_to_f16x2<0>(up), f);
           a[1][u] = hmul2(e2m1x2_to_f16x2<2>(w), f);
