@@ -261,6 +261,12 @@ struct Walk {
     off -= h * (nt + p.unit_cost);
   }
 
+  // Whether next() will find another segment: what is left is more than the part of the
+  // next unit's cost that is not tiles.
+  __device__ __forceinline__ bool more(const Kv4AttnParams& p) const {
+    return left > p.unit_cost;
+  }
+
   __device__ __forceinline__ bool next(const Kv4AttnParams& p, Seg* g) {
 #pragma unroll 1
     while (left > 0) {
@@ -293,6 +299,7 @@ struct Walk {
       g->tile = from;
       g->nt = nt;
       g->n = to - from;
+      g->final = !more(p);
       return true;
     }
     return false;
@@ -530,25 +537,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 
   if (warp == kProducer) {
     // ---------------- the run, and the cells of its tiles, one bulk copy each ----------------
-    Walk walk(p);
-    Seg g = {}, after = {};
-    bool more = walk.next(p, &g);
-    if (lane == 0) {
-      *any = more;
-      *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(-1, 0, 0, 0);
-    }
-    warp_arrive(planned);
-    griddep_launch_dependents();
-    // (a cache that several units of a sequence read stays in L2)
-    const uint64_t pol =
-        p.max_tokens > p.tile_rows ? l2_policy_evict_normal() : l2_policy_evict_first();
     const int per_slab = p.s.slab_rows / kCellRows;
+    Walk walk(p);
+    Seg g = {};
+    bool have_seg = walk.next(p, &g);
+    if (lane == 0) {
+      *any = have_seg;
+      segs[0] = g;
+    }
+    __syncwarp();
+    if (have_seg) warp_arrive(&seg_full[0]);
+    warp_arrive(planned);
     // lane: cell `lane` of the four tiles from `tile` on (negative: no such page)
     auto cells_at = [&](int tile) {
       const int key16 = tile * kGran + lane;
       int slab = g.b, row16 = key16;
       if (p.paged) {
-        const int page = key16 / per_slab;
+        const int page = per_slab == 1 ? key16 : key16 / per_slab;
         row16 = key16 - page * per_slab;
         slab = -1;
         if (key16 * kCellRows < g.end)
@@ -557,20 +562,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       return (slab * p.s.n_kv_heads + g.h) * per_slab + row16;
     };
+    int ahead = cells_at(g.tile);
+    if (lane == 0) *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(-1, 0, 0, 0);
+    griddep_launch_dependents();
+    // (a cache that several units of a sequence read stays in L2)
+    const uint64_t pol =
+        p.max_tokens > p.tile_rows ? l2_policy_evict_normal() : l2_policy_evict_first();
     int j = 0;
     bool go = true;
 #pragma unroll 1
-    for (int seg = 0; go && more; ++seg) {
+    for (int seg = 0; go && have_seg; ++seg) {
       if (g.tile == 0 && g.n < g.nt && lane == 0)     // the rest of this unit is others'
         *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) =
             make_int4(walk.owner(walk.here + g.nt - g.n - 1), g.lo + g.t0,
                       min(p.tile_rows, g.T - g.t0) * G, g.h);
-      more = walk.next(p, &after);
-      g.final = !more;
-      if (seg >= 2) go = wait_on<true>(&seg_empty[seg & 1], ((seg >> 1) - 1) & 1, abort_flag, p.status);
-      if (lane == 0) segs[seg & 1] = g;
-      warp_arrive(&seg_full[seg & 1]);
-      int cell4 = 0, ahead = cells_at(g.tile);
+      int cell4 = 0;
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++j) {
         const int st = j % C::kStages;
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
         if (lane == 0) {
           Tile t = {left, (i == 0 ? kFirst : 0) |
-                              (i + 1 == g.n ? kLast | (more ? 0 : kFinal) : 0)};
+                              (i + 1 == g.n ? kLast | (g.final ? kFinal : 0) : 0)};
           tiles[j % C::kRing] = t;
           mbar_arrive_expect_tx(&full[st], __popc(have) * C::kCell);
         }
@@ -608,7 +614,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           bulk_load(dst + lane * C::kCell, p.s.cells + static_cast<size_t>(cell) * C::kCell,
                     C::kCell, &full[st], pol);
       }
-      g = after;
+      if (!go) break;
+      have_seg = walk.next(p, &g);
+      if (!have_seg) break;
+      const int par = (seg + 1) & 1;
+      if (seg >= 1)
+        go = wait_on<true>(&seg_empty[par], (((seg + 1) >> 1) - 1) & 1, abort_flag, p.status);
+      if (lane == 0) segs[par] = g;
+      warp_arrive(&seg_full[par]);
+      ahead = cells_at(g.tile);
     }
     // no copy may still be landing when the CTA exits
 #pragma unroll 1
@@ -697,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
 #pragma unroll 1
     for (int seg = 0; go; ++seg) {
       const int par = seg & 1;
-      wait.on<true>(&seg_full[par], (seg >> 1) & 1);
+      wait(&seg_full[par], (seg >> 1) & 1);
       if (bar_or(15, 64, wait.dead)) break;                      // (and q_max is read)
       const Seg g = segs[par];
       go = !g.final;
@@ -1213,7 +1227,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
   if (warp == C::kWarps) {
     // ---------------- the segments of this CTA ----------------
     Walk walk(p);
-    Seg g = {}, after = {};
+    Seg g = {};
     bool more = walk.next(p, &g);
     const bool any = more;
     if (lane == 0) *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(-1, 0, 0, 0);
@@ -1241,9 +1255,8 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
         r.rows = rows;
         r.whole = g.tile == 0 && g.n == g.nt;
         r.slot = 2 * static_cast<int>(blockIdx.x) + (g.tile == 0 ? 1 : 0);
-        more = walk.next(p, &after);
-        r.final = !more;
-        g = after;
+        r.final = g.final;
+        more = walk.next(p, &g);
       } else {
         r.b = -1;
       }
