@@ -25,28 +25,19 @@
 // 6 significant bits) straight into TMEM.  With them in shared memory its traffic,
 // not DRAM, would bound the kernel: 128 KB written and read a tile of 18 KB.
 // Q is kept in fp16, where need be times a power of two (exact for bf16 values down to
-// 2^-12 of the unit's largest at least, 2^-23 of it off for smaller ones); P in fp16 (2^-12 of its value), O, the maximum and the sum in fp32.
+// 2^-12 of the unit's largest at least, 2^-23 of it off for smaller ones); P in fp16
+// (2^-12 of its value), O, the maximum and the sum in fp32.
 // Softmax: a thread owns a key and walks the query columns.  The running maximum m
 // of a column only moves when a tile passes it by 2^8, which one vote per tile
 // finds out; until then exp2(x - m) needs no reduction over keys at all, and the
 // column sums stay in registers until the unit ends.
-#include <cuda_fp16.h>
-
-#include <atomic>
 #include <cmath>
 
-#include "kv4.cuh"
+#include "kv4_attention.cuh"
 
 namespace dflash {
+namespace kv4 {
 namespace {
-
-constexpr int kTile = 128;              // keys
-constexpr int kGran = kTile / kCellRows;
-// P = 2^(x - m + kLift): 2^7 at the maximum, so that fp16 keeps probabilities down to 2^-31
-// of it, and below 2^15 until the maximum moves.
-constexpr float kLift = 7.0f;
-constexpr float kMoveLog2 = 8.0f;       // a column passes its maximum by so much before it moves
-constexpr float kNoMax = -1.0e30f;      // running maximum of a column that has seen nothing
 
 template <int D, int NQ>
 struct Cfg {
@@ -60,20 +51,18 @@ struct Cfg {
   static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
   static constexpr int kVWarps = D / 32;               // warps of it that hold rows of V^T
-  // First warps of the roles.  The lowest warps go first when several could issue: those
-  // that feed the others come first.
+  // First warps of the roles.
   static constexpr int kMisc = 0, kSoft = 4, kV = kSoft + 4 * kSoftWgs, kK = kV + 4 * kVWgs;
   static constexpr int kThreads = 32 * (kK + 4 * kKWgs);
-  // Registers: the launch's share, and what the roles make of it (0: left alone).  The
-  // softmax holds scores, sums and maxima of its columns.
-  static constexpr int kRegsSoft = NQ == 16 ? 0 : NQ == 128 ? 80 : 128;
+  // Registers: the launch's share, and what the roles make of it.  The softmax holds
+  // scores, sums and maxima of its columns.
+  static constexpr int kRegsSoft = NQ == 128 ? 80 : 128;
   static constexpr int kRegsRest = 56;
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static_assert(kRegsSoft * 128 * kSoftWgs + kRegsRest * (kThreads - 128 * kSoftWgs) <=
                     kRegsLaunch * kThreads,
                 "register split");
-  static constexpr bool kKeepMax = NQ <= 64;           // maxima in registers too
-  static constexpr bool kKeep = true;                  // and scores
+  static constexpr bool kKeepMax = NQ <= 64;           // the columns' maxima in registers too
   // TMEM columns
   static constexpr int kKCols = D / 2, kVCols = kTile / 2;
   static constexpr int kSBufs = NQ <= 64 ? 2 : 1;
@@ -89,372 +78,13 @@ struct Cfg {
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kSmem = 1024 + kFixed + kTables + kStages * kStage;
   static_assert(kStages >= 3, "shared memory");
-  // A tile's record is read up to softmax time, at most four tiles after its cells were let
-  // go: the copies of tile j wait for the cells of j - kStages, those for S of kStages + 2
-  // tiles back, and that for the softmax two further back.
+  // The record of tile j replaces that of j - kRing once the V warps let go of the cells of
+  // tile j - kStages.  They began it after the product P V of two tiles before, whose P the
+  // softmax had brought, so by then it had left tile j - kStages - 3 and its record.
   static constexpr int kRing = 16;
-  static_assert(kRing >= kStages + 5, "tile records");
+  static_assert(kRing >= kStages + 3, "tile records");
 };
 
-struct Kv4AttnParams {
-  Kv4Store s;
-  int batch, n_tokens, max_tokens, n_q_heads, group, causal;
-  int tile_rows;             // rows of a sequence in one unit
-  // A unit also costs some tiles' time that is not tiles (its query rows, the first
-  // maxima, the drain of its O): the runs are cut from tiles plus those.
-  int unit_cost;
-  int group_inv;             // ceil(2^16 / group): x * group_inv >> 16 = x / group, x < 128
-  int paged, page_size, max_pages, limit;
-  const int32_t* seq_len;
-  const int32_t* start;
-  const int32_t* page_table;
-  const uint16_t* q;
-  uint16_t* out;
-  float scale_log2;
-  uint32_t* status;
-  int* meta;                 // [CTAs][4]: the unit that starts in a CTA and ends in a later one
-  float* part_ml;            // [2 CTAs][NQ][2]
-  float* part_o;             // [2 CTAs][NQ][D]
-};
-
-// ----------------------------------------------------------------------------
-// plan: which tiles this CTA takes
-// ----------------------------------------------------------------------------
-struct Seq {
-  int lo, T, len, n_qt;      // first row, rows, length, units per head (0: nothing to do)
-};
-
-__device__ __forceinline__ Seq load_seq(const Kv4AttnParams& p, int b, bool* bad = nullptr) {
-  Seq s = {0, 0, 0, 0};
-  const int lo = p.start[b], hi = p.start[b + 1], len = p.seq_len[b];
-  if (lo < 0 || hi < lo || hi > p.n_tokens || hi - lo > p.max_tokens || len < 0 ||
-      len > p.limit) {
-    if (bad) *bad = true;
-    return s;
-  }
-  s.lo = lo;
-  s.T = hi - lo;
-  s.len = len;
-  s.n_qt = (s.T + p.tile_rows - 1) / p.tile_rows;
-  return s;
-}
-
-// Keys that some row of unit qt sees, and its tiles (at least one: its rows are written).
-__device__ __forceinline__ int unit_end(const Kv4AttnParams& p, const Seq& s, int qt) {
-  if (!p.causal) return s.len;
-  return max(0, min(s.len, s.len - s.T + min(s.T, (qt + 1) * p.tile_rows)));
-}
-__device__ __forceinline__ int unit_tiles(int end) { return max(1, (end + kTile - 1) / kTile); }
-
-__device__ __forceinline__ long long seq_cost(const Kv4AttnParams& p, const Seq& s) {
-  long long n = 0;
-  if (!p.causal) {
-    n = static_cast<long long>(s.n_qt) * unit_tiles(s.len);
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < s.n_qt; ++i) n += unit_tiles(unit_end(p, s, i));
-  }
-  return (n + static_cast<long long>(s.n_qt) * p.unit_cost) * p.s.n_kv_heads;
-}
-
-// One segment: consecutive tiles of one unit.
-struct Seg {
-  int b, h, t0, lo, T, len, end, tile, n, nt;
-  int final;                 // the last of the CTA
-};
-
-// A tile, as the warps that work on it read it.
-struct Tile {
-  int left;                  // keys in use from its first one on
-  int flags;                 // of its segment: the first, the last; the last of the CTA
-};
-constexpr int kFirst = 1, kLast = 2, kFinal = 4;
-
-// What the softmax needs of a segment, left in shared memory beside its query rows.
-struct Piece {
-  int tile, n, nt, sure, rows, h;   // sure: keys that every row sees
-  float scale;                      // log2 units per score
-};
-
-// The run of this CTA, by one warp.  With W the cost of all units, every CTA takes W / n
-// (the first W % n one more), n = min(CTAs, W).
-struct Walk {
-  int left, off;             // cost left, and of the unit at hand before that
-  int b, qt, h, end, nt;
-  Seq s;
-  int per, rem, here;        // shares; where the run stands among all costs
-
-  __device__ __forceinline__ void unit(const Kv4AttnParams& p) {
-    end = unit_end(p, s, qt);
-    nt = unit_tiles(end);
-  }
-  __device__ __forceinline__ int owner(int pos) const {
-    const int big = rem * (per + 1);
-    return pos < big ? pos / (per + 1) : rem + (pos - big) / per;
-  }
-
-  __device__ __forceinline__ explicit Walk(const Kv4AttnParams& p)
-      : left(0), off(0), b(0), qt(0), h(0), end(0), nt(0), per(0), rem(0), here(0) {
-    const int lane = lane_id();
-    long long all = 0, mine = 0;
-    Seq t = {0, 0, 0, 0};    // of sequence `lane` of a group of 32
-    bool bad = false;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      mine = 0;
-      if (b0 + lane < p.batch) {
-        t = load_seq(p, b0 + lane, &bad);
-        mine = seq_cost(p, t);
-      }
-      all += mine;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (all > INT32_MAX) bad = true;
-    if (bad && blockIdx.x == 0) set_status(p.status, DFLASH_ST_CAPACITY);
-    if (all > INT32_MAX) return;
-    const int W = static_cast<int>(all), n = min(static_cast<int>(gridDim.x), W);
-    const int c = blockIdx.x;
-    if (c >= n) return;
-    per = W / n;
-    rem = W - per * n;
-    here = c * per + min(c, rem);
-    left = per + (c < rem ? 1 : 0);
-    int before = 0;
-#pragma unroll 1
-    for (int b0 = 0;; b0 += 32) {
-      if (p.batch > 32) {
-        mine = 0;
-        if (b0 + lane < p.batch) {
-          t = load_seq(p, b0 + lane);
-          mine = seq_cost(p, t);
-        }
-      }
-      int inc = static_cast<int>(mine);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > here);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        b = b0 + l;
-        s.lo = __shfl_sync(0xffffffffu, t.lo, l);
-        s.T = __shfl_sync(0xffffffffu, t.T, l);
-        s.len = __shfl_sync(0xffffffffu, t.len, l);
-        s.n_qt = __shfl_sync(0xffffffffu, t.n_qt, l);
-        before += __shfl_sync(0xffffffffu, inc - static_cast<int>(mine), l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    off = here - before;
-    unit(p);
-#pragma unroll 1
-    while (off >= (nt + p.unit_cost) * p.s.n_kv_heads) {
-      off -= (nt + p.unit_cost) * p.s.n_kv_heads;
-      ++qt;
-      unit(p);
-    }
-    h = off / (nt + p.unit_cost);
-    off -= h * (nt + p.unit_cost);
-  }
-
-  // Whether next() will find another segment: what is left is more than the part of the
-  // next unit's cost that is not tiles.
-  __device__ __forceinline__ bool more(const Kv4AttnParams& p) const {
-    return left > p.unit_cost;
-  }
-
-  __device__ __forceinline__ bool next(const Kv4AttnParams& p, Seg* g) {
-#pragma unroll 1
-    while (left > 0) {
-      if (off == nt + p.unit_cost) {        // the unit after this one
-        off = 0;
-        if (++h == p.s.n_kv_heads) {
-          h = 0;
-          ++qt;
-#pragma unroll 1
-          while (qt >= s.n_qt) {
-            qt = 0;
-            s = load_seq(p, ++b);
-          }
-          unit(p);
-        }
-      }
-      const int take = min(left, nt + p.unit_cost - off);
-      const int from = max(0, off - p.unit_cost), to = off + take - p.unit_cost;
-      off += take;
-      left -= take;
-      here += take;
-      if (to <= from) continue;
-      g->b = b;
-      g->h = h;
-      g->t0 = qt * p.tile_rows;
-      g->lo = s.lo;
-      g->T = s.T;
-      g->len = s.len;
-      g->end = end;
-      g->tile = from;
-      g->nt = nt;
-      g->n = to - from;
-      g->final = !more(p);
-      return true;
-    }
-    return false;
-  }
-};
-
-// ----------------------------------------------------------------------------
-// small device pieces
-// ----------------------------------------------------------------------------
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Named barrier of n threads that also ORs a flag over them.
-__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\t"
-      "setp.ne.u32 a, %1, 0;\n\t"
-      "barrier.cta.red.or.pred b, %2, %3, a;\n\t"
-      "selp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-
-// Registers per thread of this warpgroup from here on.
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, issued by one thread.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Instruction descriptor, kind::f16: A = B = fp16, D = fp32; b_mn: B is MN-major.
-__host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// The bounded wait of this kernel.  A try by a whole warp sleeps up to 4 us (measured), so
-// 2^18 of them are a second; the loop is small, because five roles share the
-// instruction cache, and a call would rule out the register split.
-template <bool kNap = false>
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                        uint32_t* status) {
-#define DFLASH_TRY "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra done;\n\t"
-#define DFLASH_LOOP(body)                                                           \
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 65536;\n\tagain:\n\t" body \
-               "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra again;\n\tdone:\n\t"     \
-               "selp.u32 %0, 1, 0, p;\n\t}\n"                                        \
-               : "=r"(ok)                                                           \
-               : "r"(smem_u32(bar)), "r"(parity)                                    \
-               : "memory")
-  uint32_t ok;
-  __syncwarp();  // (a warp that is not together does not sleep in a try)
-  if (kNap)      // where 100 ns late costs nothing
-    DFLASH_LOOP(DFLASH_TRY "nanosleep.u32 60;\n\t");
-  else
-    DFLASH_LOOP(DFLASH_TRY DFLASH_TRY DFLASH_TRY DFLASH_TRY);
-#undef DFLASH_TRY
-#undef DFLASH_LOOP
-  if (ok) return true;
-  *abort_flag = 1;
-  set_status(status, DFLASH_ST_TIMEOUT);
-  return false;
-}
-
-// A wait of a warp; once one gave up the rest are skipped.  Warps that meet at named
-// barriers vote there on who gave up, and leave their loops together.
-struct Waiter {
-  volatile int* abort_flag;
-  uint32_t* status;
-  bool dead;
-  template <bool kNap = false>
-  __device__ __forceinline__ void on(uint64_t* bar, uint32_t parity) {
-    if (!dead) dead = !wait_on<kNap>(bar, parity, abort_flag, status);
-  }
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    on(bar, parity);
-  }
-  __device__ __forceinline__ bool gave_up() {     // by the whole warp
-    dead = __any_sync(0xffffffffu, dead);
-    return dead;
-  }
-};
-
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if (elect_one()) mbar_arrive(bar);
-}
-
-// ----------------------------------------------------------------------------
-// the kernel
-// ----------------------------------------------------------------------------
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     kv4_attention_kernel(const Kv4AttnParams p) {
@@ -491,8 +121,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   uint64_t* mdrain = planned + 1;
   uint32_t* q_max = reinterpret_cast<uint32_t*>(mdrain + 1);   // [2]
   uint32_t* tmem_slot = q_max + 2;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* any = abort_flag + 1;      // this CTA has tiles
+  volatile int* any = reinterpret_cast<volatile int*>(tmem_slot + 1);  // this CTA has tiles
 
   // (the shuffle tells the compiler that the index is the same all over the warp)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -519,7 +148,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     mbar_init(o_empty, 4 * C::kSoftWgs);
     mbar_init(planned, 1);
     mbar_init(mdrain, 1);
-    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMma) {
@@ -529,9 +157,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (C::kRegsSoft && (warp < C::kSoft || warp >= C::kV)) regs_down<C::kRegsRest>();
+  if (warp < C::kSoft || warp >= C::kV) regs_down<C::kRegsRest>();
   griddep_wait();
-  Waiter wait{abort_flag, p.status, false};
+  Waiter wait{p.status, false};
   const int G = p.group;
   constexpr uint32_t tmem = 0;   // all 512 columns are this CTA's: they start at 0
 
@@ -589,7 +217,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const bool use = lane < kGran && lane * kCellRows < left;
         const uint32_t have = __ballot_sync(0xffffffffu, use && cell >= 0);
         const uint32_t miss = __ballot_sync(0xffffffffu, use && cell < 0);
-        go = go && wait_on<true>(&empty[st], ((j / C::kStages) & 1) ^ 1, abort_flag, p.status);
+        go = go && wait_on<true>(&empty[st], ((j / C::kStages) & 1) ^ 1, p.status);
         if (!__all_sync(0xffffffffu, go)) {
           go = false;
           break;
@@ -604,8 +232,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           __syncwarp();
         }
         if (lane == 0) {
-          Tile t = {left, (i == 0 ? kFirst : 0) |
-                              (i + 1 == g.n ? kLast | (g.final ? kFinal : 0) : 0)};
+          Tile t = {left, (i == 0 ? kFirst : 0) | (i + 1 == g.n && g.final ? kFinal : 0)};
           tiles[j % C::kRing] = t;
           mbar_arrive_expect_tx(&full[st], __popc(have) * C::kCell);
         }
@@ -619,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       if (!have_seg) break;
       const int par = (seg + 1) & 1;
       if (seg >= 1)
-        go = wait_on<true>(&seg_empty[par], (((seg + 1) >> 1) - 1) & 1, abort_flag, p.status);
+        go = wait_on<true>(&seg_empty[par], (((seg + 1) >> 1) - 1) & 1, p.status);
       if (lane == 0) segs[par] = g;
       warp_arrive(&seg_full[par]);
       ahead = cells_at(g.tile);
@@ -645,7 +272,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const uint64_t p_desc = umma_sdesc_sw128_mn(smem_u32(pbuf), kTile * 128, 1024);
     bool ok = true;
     auto need = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && wait_on(bar, parity, abort_flag, p.status));
+      ok = __all_sync(0xffffffffu, ok && wait_on(bar, parity, p.status));
     };
     auto issue_pv = [&](int j, bool first, int seg) {
       if (!ok) return;
@@ -736,7 +363,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               x[u] = *reinterpret_cast<const uint4*>(
                   p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D + 8 * pc);
           }
-          if (pass == 0 && it0 == 0 && seg >= 2) wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
+          if (pass == 0 && it0 == 0 && seg >= 2)
+            wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
 #pragma unroll
           for (int u = 0; u < kLoads; ++u) {
             const int q = ((it0 + u) * 64 + tid) / kPer;
@@ -787,50 +415,48 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     const int r = threadIdx.x & 127, wg = (warp - C::kK) >> 2;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool go = true;
-    {
 #pragma unroll 1
-      for (int j = 0; go; ++j) {
-        const int st = j % C::kStages;
-        wait.on<true>(&full[st], (j / C::kStages) & 1);
-        wait.on<true>(&(C::kSBufs == 2 ? s_full : kd_empty)[j & 1], ((j >> 1) & 1) ^ 1);
-        if (wait.gave_up()) break;
-        go = !(tiles[j % C::kRing].flags & kFinal);
-        tc_fence_after();
-        const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
-        const int rr = r % kCellRows;
-        // 64 dims a round (D = 64 with two warpgroups: 32 each)
-        constexpr int kParts = D / 32 / C::kKWgs, kC = kParts < 2 ? 1 : 2;
+    for (int j = 0; go; ++j) {
+      const int st = j % C::kStages;
+      wait.on<true>(&full[st], (j / C::kStages) & 1);
+      wait.on<true>(&(C::kSBufs == 2 ? s_full : kd_empty)[j & 1], ((j >> 1) & 1) ^ 1);
+      if (wait.gave_up()) break;
+      go = !(tiles[j % C::kRing].flags & kFinal);
+      tc_fence_after();
+      const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
+      const int rr = r % kCellRows;
+      // 64 dims a round (D = 64 with two warpgroups: 32 each)
+      constexpr int kParts = D / 32 / C::kKWgs, kC = kParts < 2 ? 1 : 2;
 #pragma unroll 1
-        for (int c2 = 0; c2 < kParts / kC; ++c2) {
-          const int c0 = wg * kParts + c2 * kC;        // first 32 dims
-          uint4 w[kC];
+      for (int c2 = 0; c2 < kParts / kC; ++c2) {
+        const int c0 = wg * kParts + c2 * kC;        // first 32 dims
+        uint4 w[kC];
 #pragma unroll
-          for (int c = 0; c < kC; ++c)
-            w[c] = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * (c0 + c)));
+        for (int c = 0; c < kC; ++c)
+          w[c] = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * (c0 + c)));
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            const uint32_t s2 = e4m3x2_to_f16x2(
-                *reinterpret_cast<const uint16_t*>(cell + Cell<D>::k_scale(rr, 2 * (c0 + c))));
-            const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
-            const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-            uint32_t o[16];
+        for (int c = 0; c < kC; ++c) {
+          const uint32_t s2 = e4m3x2_to_f16x2(
+              *reinterpret_cast<const uint16_t*>(cell + Cell<D>::k_scale(rr, 2 * (c0 + c))));
+          const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
+          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t o[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // (bytes 0 and 2 convert as they lie; 1 and 3 would take a shift each)
-              const uint32_t sc = e < 2 ? s_lo : s_hi, up = u[e] >> 8;
-              o[4 * e] = hmul2(e2m1x2_to_f16x2<0>(u[e]), sc);
-              o[4 * e + 1] = hmul2(e2m1x2_to_f16x2<0>(up), sc);
-              o[4 * e + 2] = hmul2(e2m1x2_to_f16x2<2>(u[e]), sc);
-              o[4 * e + 3] = hmul2(e2m1x2_to_f16x2<2>(up), sc);
-            }
-            tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + (c0 + c) * 16, o);
+          for (int e = 0; e < 4; ++e) {
+            // (bytes 0 and 2 convert as they lie; 1 and 3 would take a shift each)
+            const uint32_t sc = e < 2 ? s_lo : s_hi, up = u[e] >> 8;
+            o[4 * e] = hmul2(e2m1x2_to_f16x2<0>(u[e]), sc);
+            o[4 * e + 1] = hmul2(e2m1x2_to_f16x2<0>(up), sc);
+            o[4 * e + 2] = hmul2(e2m1x2_to_f16x2<2>(u[e]), sc);
+            o[4 * e + 3] = hmul2(e2m1x2_to_f16x2<2>(up), sc);
           }
+          tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + (c0 + c) * 16, o);
         }
-        warp_arrive(&empty[st]);
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&kd_full[j & 1]);
       }
+      warp_arrive(&empty[st]);
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&kd_full[j & 1]);
     }
   } else if (warp >= C::kV) {
     // ---------------- V^T to fp16: a thread expands its dim's row ----------------
@@ -841,60 +467,58 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       uint32_t mul = d & 1 ? 1 : 16, mul16 = 16 * mul;         // to the byte's high nibble
       asm volatile("" : "+r"(mul), "+r"(mul16));               // (factors, not shifts)
       bool go = true;
-      {
 #pragma unroll 1
-        for (int j = 0; go; ++j) {
-          const int st = j % C::kStages;
-          wait(&full[st], (j / C::kStages) & 1);
-          wait(&pv_done[j & 1], ((j >> 1) & 1) ^ 1);
-          if (wait.gave_up()) break;
-          const Tile t = tiles[j % C::kRing];
-          go = !(t.flags & kFinal);
-          tc_fence_after();
-          const uint8_t* base = stages + st * C::kStage + g0 * C::kCell;
-          // keys in use from this warpgroup's first cell on
-          const int left = t.left - g0 * kCellRows;
-          const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
-          const uint8_t* scl = base + Cell<D>::v_scale(0, d / 16);
+      for (int j = 0; go; ++j) {
+        const int st = j % C::kStages;
+        wait(&full[st], (j / C::kStages) & 1);
+        wait(&pv_done[j & 1], ((j >> 1) & 1) ^ 1);
+        if (wait.gave_up()) break;
+        const Tile t = tiles[j % C::kRing];
+        go = !(t.flags & kFinal);
+        tc_fence_after();
+        const uint8_t* base = stages + st * C::kStage + g0 * C::kCell;
+        // keys in use from this warpgroup's first cell on
+        const int left = t.left - g0 * kCellRows;
+        const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
+        const uint8_t* scl = base + Cell<D>::v_scale(0, d / 16);
 #pragma unroll 2
-          for (int c = 0; c < C::kVGran; ++c) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
-            const uint4 s4 = *reinterpret_cast<const uint4*>(scl + c * C::kCell);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-            uint32_t o[8];
+        for (int c = 0; c < C::kVGran; ++c) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
+          const uint4 s4 = *reinterpret_cast<const uint4*>(scl + c * C::kCell);
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+          const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
+          uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // this dim's nibbles of four keys, two to a byte (0 and 2, which convert as they
-              // lie): shifts as products leave the integer pipe to the conversions
-              const uint32_t x =
-                  ((w[e] * mul & 0xF000F000u) | (w[e] * mul16 & ~0xF000F000u)) >> 8;
-              o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), e4m3x2_to_f16x2(s[e]));
-              o[2 * e + 1] =
-                  hmul2(e2m1x2_to_f16x2<2>(x), e4m3x2_to_f16x2(s[e] >> 16));
-            }
-            if (left < (c + 1) * kCellRows) {                // rows past the length count as 0
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int key = c * kCellRows + 2 * e;
-                if (key >= left) o[e] = 0;
-                else if (key + 1 >= left) o[e] &= 0xFFFFu;
-              }
-            }
-            tmem_st_32x32b_x8(lane_base + (j & 1) * C::kVCols + c * 8, o);
+          for (int e = 0; e < 4; ++e) {
+            // this dim's nibbles of four keys, two to a byte (0 and 2, which convert as they
+            // lie): shifts as products leave the integer pipe to the conversions
+            const uint32_t x =
+                ((w[e] * mul & 0xF000F000u) | (w[e] * mul16 & ~0xF000F000u)) >> 8;
+            o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), e4m3x2_to_f16x2(s[e]));
+            o[2 * e + 1] =
+                hmul2(e2m1x2_to_f16x2<2>(x), e4m3x2_to_f16x2(s[e] >> 16));
           }
-          warp_arrive(&empty[st]);
-          tmem_st_wait();
-          tc_fence_before();
-          warp_arrive(&pv_full[j & 1]);
+          if (left < (c + 1) * kCellRows) {                // rows past the length count as 0
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int key = c * kCellRows + 2 * e;
+              if (key >= left) o[e] = 0;
+              else if (key + 1 >= left) o[e] &= 0xFFFFu;
+            }
+          }
+          tmem_st_32x32b_x8(lane_base + (j & 1) * C::kVCols + c * 8, o);
         }
+        warp_arrive(&empty[st]);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&pv_full[j & 1]);
       }
     }
   } else {
     // ---------------- softmax: a thread owns a key ----------------
-    if (C::kRegsSoft) regs_up<C::kRegsSoft ? C::kRegsSoft : 24>();
+    regs_up<C::kRegsSoft>();
     constexpr int CW = C::kCols;
-    constexpr bool kKeep = C::kKeep, kKeepMax = C::kKeepMax;
+    constexpr bool kKeepMax = C::kKeepMax;
     const int wg = (warp - C::kSoft) >> 2, q4 = warp & 3;
     const int r = q4 * 32 + lane, col0 = wg * CW;
     const uint32_t bar = 1 + wg;
@@ -954,13 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
               if (key >= vis[c0 + e]) x[e] = -INFINITY;
           }
         };
-        auto load16 = [&](int c0, bool sub, float* x) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(s_addr + c0, v);
-          tmem_ld_wait();
-          scores(v, c0, sub, x);
-        };
-        float x[kKeep ? CW : 16];
+        float x[CW];
         auto load_all = [&] {
           uint32_t v[CW / 16][16];
 #pragma unroll
@@ -971,19 +589,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         };
         bool move = i == 0;
         if (i > 0) {
-          float mx = -INFINITY;
-          if (kKeep) {
-            load_all();
+          load_all();
+          float mx = x[0];
 #pragma unroll
-            for (int e = 0; e < (kKeep ? CW : 0); ++e) mx = fmaxf(mx, x[e]);
-          } else {
-#pragma unroll
-            for (int c0 = 0; c0 < CW; c0 += 16) {
-              load16(c0, true, x);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
-            }
-          }
+          for (int e = 1; e < CW; ++e) mx = fmaxf(mx, x[e]);
           move = bar_or(bar, 128, wait.dead || mx > kMoveLog2 + kLift);
         }
         if (move) {
@@ -992,8 +601,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           float mine = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < CW; c0 += 16) {
+            uint32_t v[16];
             float y[16];
-            load16(c0, false, y);
+            tmem_ld_32x32b_x16(s_addr + c0, v);
+            tmem_ld_wait();
+            scores(v, c0, false, y);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float m = warp_max(y[e]);
@@ -1005,7 +617,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           if (r < CW) {
             const float* m4 = red + col0 + r;
             const float was = i == 0 ? kNoMax : kLift - nm[r];
-            const float now = fmaxf(fmaxf(fmaxf(m4[0], m4[NQ]), fmaxf(m4[2 * NQ], m4[3 * NQ])), was);
+            const float now =
+                fmaxf(fmaxf(fmaxf(m4[0], m4[NQ]), fmaxf(m4[2 * NQ], m4[3 * NQ])), was);
             fac[r] = ex2(was - now);
             nm[r] = kLift - now;
           }
@@ -1034,9 +647,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             for (int c = 0; c < (kKeepMax ? CW / 2 : 0); ++c)
               mr[c] = *reinterpret_cast<const float2*>(nm + 2 * c);
           }
-          if (kKeep) load_all();
+          load_all();
         }
-        if (kKeep && C::kSBufs == 1) {
+        if (C::kSBufs == 1) {
           tc_fence_before();
           warp_arrive(s_empty);
         }
@@ -1045,18 +658,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         uint8_t* prow = pbuf + (j & 1) * C::kPBytes + (col0 / 64) * kTile * 128 + r * 128;
 #pragma unroll
         for (int c0 = 0; c0 < CW; c0 += 8) {
-          if (!kKeep && c0 % 16 == 0) {
-            load16(c0, true, x);
-            if (c0 + 16 == CW && C::kSBufs == 1) {
-              tc_fence_before();
-              warp_arrive(s_empty);
-            }
-          }
-          const float* xc = x + (kKeep ? c0 : c0 % 16);
           uint32_t pk[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const float a = ex2(xc[e]), b = ex2(xc[e + 1]);
+            const float a = ex2(x[c0 + e]), b = ex2(x[c0 + e + 1]);
             l[(c0 + e) / 2] = __fadd2_rn(l[(c0 + e) / 2], make_float2(a, b));
             pk[e / 2] = pack_f16(a, b);
           }
@@ -1085,7 +690,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
             y[c] = (up ? y[c + n] : y[c]) + other;
           }
         }
-        if (CW == 16) y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
         if (lane < CW) red[q4 * NQ + col0 + lane] = y[0];
       }
       named_bar_sync(bar, 128);
@@ -1139,462 +743,6 @@ done:
   __syncthreads();
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(*tmem_slot, 512);
-}
-
-// ----------------------------------------------------------------------------
-// few query rows (single tokens): no more than 16 to a unit
-// ----------------------------------------------------------------------------
-// With so few rows the tensor cores have little to do and the way through TMEM costs
-// more than the products: every hand-over between roles is paid per tile, whatever the rows
-// are.  Here a warp does all of it for a cell at a time, alone: its own copies into its
-// own ring, K and V expanded in registers as the fragments of m16n8k16 products, its own
-// maximum, sum and O; the warps of a CTA meet at the end of a segment only, where their
-// results are joined in order.
-//
-// The products are turned round, S^T = K Q^T and O^T = V^T P^T, so that the expanded
-// fragments serve every eight query rows (kTiles of them) and few rows cost little.
-// Which dim is the products' k index and which key is a row of S^T is free as long as both
-// factors agree, so each is chosen to make a thread's part of the cell a 32-bit word
-// (g = lane / 4, t = lane % 4):
-//   S^T   row g is key 4 (g / 2) + g % 2, row g + 8 the key two further; steps 2 p, 2 p + 1
-//         take the dims 32 p + 8 t .. + 7, one word of codes of one key
-//   O^T   k 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are then the keys 4 t .. 4 t + 3, and P^T comes
-//         from S^T by an 8 x 8 transpose; rows g and g + 8 of tile i are the dims 16 i + 2 g
-//         and 16 i + 2 g + 1: one word holds both for four keys, under one scale for each key
-template <int D, int kTiles>
-struct RowsCfg {
-  static constexpr int kWarps = kTiles == 1 ? 19 : 14;   // and one that plans
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kRows = 8 * kTiles;
-  static constexpr int kStages = 3;    // cells of a warp's ring
-  static constexpr int kCell = Cell<D>::kBytes;
-  static constexpr int kRing = kWarps * kStages * kCell;
-  static constexpr int kPitch = D + 4;                   // floats, of a row of `join`
-  static constexpr int kJoin = kWarps * kRows * kPitch * 4;
-  static constexpr int kSegs = 4;
-  static constexpr int kQuery = kTiles * (D / 32) * 512; // fragments of the query rows
-  static constexpr int kSmem = 128 + kRing + kQuery + kJoin + kWarps * kRows * 8 + kRows * 8 +
-                               64 * kSegs + 8 * (kWarps * kStages + 2 * kSegs) + 64;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
-};
-
-struct RowSeg {
-  int b, h, row0, T, len, end, t0, cell0, cells, rows, whole, slot, final;
-};
-
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t word(const uint8_t* p) {
-  return *reinterpret_cast<const uint32_t*>(p);
-}
-
-template <int D, int kTiles>
-__global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
-    kv4_rows_kernel(const Kv4AttnParams p) {
-  using C = RowsCfg<D, kTiles>;
-  constexpr int kP = D / 32, kI = D / 16;          // pieces of K, tiles of O^T
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((128 - (smem_u32(smem_raw) & 127)) & 127);
-  uint4* qf = reinterpret_cast<uint4*>(smem + C::kRing);   // [tile][piece][lane]
-  float* join = reinterpret_cast<float*>(smem + C::kRing + C::kQuery);  // [warp][row][kPitch]
-  float2* wml = reinterpret_cast<float2*>(join + C::kWarps * C::kRows * C::kPitch);
-                                                           // [warp][row] maximum, sum
-  float* row_sc = reinterpret_cast<float*>(wml + C::kWarps * C::kRows);  // [row]
-  RowSeg* segs = reinterpret_cast<RowSeg*>(row_sc + 2 * C::kRows);
-  uint64_t* full = reinterpret_cast<uint64_t*>(segs + C::kSegs);       // [warp][stage]
-  uint64_t* seg_full = full + C::kWarps * C::kStages;
-  uint64_t* seg_empty = seg_full + C::kSegs;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(seg_empty + C::kSegs);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < C::kWarps * C::kStages; i += C::kThreads) mbar_init(&full[i], 1);
-  if (threadIdx.x < C::kSegs) {
-    mbar_init(&seg_full[threadIdx.x], 1);
-    mbar_init(&seg_empty[threadIdx.x], C::kWarps);
-  }
-  if (threadIdx.x == 0) *abort_flag = 0;
-  fence_mbar_init();
-  __syncthreads();
-  griddep_wait();
-  Waiter wait{abort_flag, p.status, false};
-  const int G = p.group;
-
-  if (warp == C::kWarps) {
-    // ---------------- the segments of this CTA ----------------
-    Walk walk(p);
-    Seg g = {};
-    bool more = walk.next(p, &g);
-    const bool any = more;
-    if (lane == 0) *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(-1, 0, 0, 0);
-#pragma unroll 1
-    for (int s = 0; more || s == 0; ++s) {
-      if (s >= C::kSegs) wait.on<true>(&seg_empty[s % C::kSegs], ((s / C::kSegs) & 1) ^ 1);
-      if (wait.gave_up()) break;
-      RowSeg r = {};
-      r.final = 1;
-      if (any) {
-        const int rows = min(p.tile_rows, g.T - g.t0) * G;
-        const int cells = (g.end + kCellRows - 1) / kCellRows;     // of the unit
-        if (g.tile == 0 && g.n < g.nt && lane == 0)   // the rest of this unit is others'
-          *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(
-              walk.owner(walk.here + g.nt - g.n - 1), g.lo + g.t0, rows, g.h);
-        r.b = g.b;
-        r.h = g.h;
-        r.row0 = (g.lo + g.t0) * p.n_q_heads + g.h * G;
-        r.T = g.T;
-        r.len = g.len;
-        r.end = g.end;
-        r.t0 = g.t0;
-        r.cell0 = g.tile * kGran;
-        r.cells = max(0, min(g.n * kGran, cells - r.cell0));
-        r.rows = rows;
-        r.whole = g.tile == 0 && g.n == g.nt;
-        r.slot = 2 * static_cast<int>(blockIdx.x) + (g.tile == 0 ? 1 : 0);
-        r.final = g.final;
-        more = walk.next(p, &g);
-      } else {
-        r.b = -1;
-      }
-      if (lane == 0) segs[s % C::kSegs] = r;
-      warp_arrive(&seg_full[s % C::kSegs]);
-    }
-    griddep_launch_dependents();
-    return;
-  }
-
-  const int gl = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kCell;
-  uint64_t* mine = full + warp * C::kStages;
-  const uint64_t pol =
-      p.max_tokens > p.tile_rows ? l2_policy_evict_normal() : l2_policy_evict_first();
-  const int per_slab = p.s.slab_rows / kCellRows;
-  // the cell that is copied next: segment ls (at hand or the one after), its cell lc
-  int ls = 0, lc = warp, issued = 0;
-  bool known = false;                  // segment ls is out (and read below)
-  int l_b = 0, l_h = 0, l_cell0 = 0, l_cells = 0, l_final = 0;
-  // copies ahead of cell number `done` of this warp, as far as the ring and the segments go
-  auto issue = [&](int done, int seg) {
-#pragma unroll 1
-    while (issued < done + C::kStages) {
-      if (!known) {
-        if (ls > seg + 1 ||
-            !__all_sync(0xffffffffu, mbar_try_wait(&seg_full[ls % C::kSegs], (ls / C::kSegs) & 1)))
-          return;
-        const RowSeg& r = segs[ls % C::kSegs];
-        l_b = r.b;
-        l_h = r.h;
-        l_cell0 = r.cell0;
-        l_cells = r.cells;
-        l_final = r.final;
-        known = true;
-      }
-      if (lc >= l_cells) {
-        if (l_final) return;
-        ++ls;
-        lc = warp;
-        known = false;
-        continue;
-      }
-      const int key16 = l_cell0 + lc;
-      int slab = l_b, row16 = key16;
-      if (p.paged) {
-        const int page = per_slab == 1 ? key16 : key16 / per_slab;
-        row16 = key16 - page * per_slab;
-        slab = p.page_table[static_cast<size_t>(l_b) * p.max_pages + page];
-      }
-      const int st = issued % C::kStages;
-      const uint32_t dst = ring + st * C::kCell;
-      if (slab < 0 || slab >= p.s.n_slabs) {        // a page that is missing reads as zeros
-        if (lane == 0) set_status(p.status, DFLASH_ST_PAGE_MISSING);
-        for (int o = lane * 16; o < C::kCell; o += 512)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + o), "r"(0) : "memory");
-        warp_arrive(&mine[st]);
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(&mine[st], C::kCell);
-        bulk_load(smem + (dst - smem_u32(smem)),
-                  p.s.cells + static_cast<size_t>((slab * p.s.n_kv_heads + l_h) * per_slab + row16) *
-                                  C::kCell,
-                  C::kCell, &mine[st], pol);
-      }
-      ++issued;
-      lc += C::kWarps;
-    }
-  };
-
-  int done = 0;
-  bool go = true;
-#pragma unroll 1
-  for (int seg = 0; go; ++seg) {
-    wait(&seg_full[seg % C::kSegs], (seg / C::kSegs) & 1);
-    if (bar_or(1, 32 * C::kWarps, wait.dead)) break;
-    issue(done, seg);
-    const RowSeg r = segs[seg % C::kSegs];
-    go = !r.final;
-    if (r.b < 0) break;
-    // ---- query rows as fragments, each scaled to [1, 2) by a power of two ----
-    if (warp < kTiles) {
-      const int row = gl + 8 * warp, tq = row * p.group_inv >> 16;
-      uint4 v[kP];
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (row < r.rows)
-          v[i] = *reinterpret_cast<const uint4*>(
-              p.q + static_cast<size_t>(r.row0 + tq * p.n_q_heads + row - tq * G) * D + 32 * i +
-              8 * t);
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t a = w[e] & 0x7FFFu, b = w[e] >> 16 & 0x7FFFu;
-          m = max(m, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
-        }
-      }
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int ex = max(-126, min(126, 127 - static_cast<int>(m >> 7)));
-      const float f = pow2(ex);
-#pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[e] = pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xFFFF0000u) * f);
-        qf[(warp * kP + i) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
-      }
-      if (t == 0) row_sc[row] = p.scale_log2 * pow2(gain_exp(p.s.k_exp, r.h)) * pow2(-ex);
-    }
-    named_bar_sync(1, 32 * C::kWarps);
-    float sc[kTiles][2];               // of rows 8 x + 2 t, 8 x + 2 t + 1, as all below
-    int vis[kTiles][2];
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int mr = 8 * x + 2 * t + e;
-        sc[x][e] = row_sc[mr];
-        vis[x][e] = p.causal && mr < r.rows
-                        ? max(0, min(r.len, r.len - r.T + r.t0 + (mr * p.group_inv >> 16) + 1))
-                        : r.len;
-      }
-    const int sure = p.causal ? max(0, r.len - r.T + r.t0 + 1) : r.len;
-    float o[kI][kTiles][4], l[kTiles][2], nm[kTiles][2];   // nm: kLift - running maximum
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-#pragma unroll
-      for (int i = 0; i < kI; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][x][e] = 0.f;
-      l[x][0] = l[x][1] = 0.f;
-      nm[x][0] = nm[x][1] = kLift - kNoMax;
-    }
-    const int kr = 4 * (gl >> 1) + (gl & 1);                // S^T rows g, g + 8: keys kr, kr + 2
-    // this warp's slice of `join`, free until the segment ends: [group][key], [group][key / 2]
-    uint32_t* k_sc = reinterpret_cast<uint32_t*>(join + warp * C::kRows * C::kPitch);
-    uint32_t* v_sc = k_sc + D;
-#pragma unroll 1
-    for (int c = warp; c < r.cells; c += C::kWarps, ++done) {
-      const int st = done % C::kStages;
-      wait(&mine[st], (done / C::kStages) & 1);
-      if (wait.gave_up()) break;
-      const uint8_t* cell = smem + (warp * C::kStages + st) * C::kCell;
-      const int key0 = (r.cell0 + c) * kCellRows;
-      // ---- scores of 16 keys: element e is key kr + 2 (e >> 1), row 2 t + (e & 1) ----
-      float s[kTiles][4], s_odd[kTiles][4];                 // (two chains of products)
-#pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = s_odd[x][e] = 0.f;
-      // every scale to fp16 once, by all lanes, for the eight that share it: those of K
-      // doubled, those of V in pairs of keys (0 past the length; codes are finite
-      // whatever they hold)
-      const int left = r.end - key0;
-#pragma unroll
-      for (int i = 0; i < D / 128 + (D < 128); ++i) {
-        const int w = i * 32 + lane;                        // four scales each
-        if (w < D / 4) {
-          const uint32_t ks = word(cell + Cell<D>::kKScale + 4 * w);
-          const uint32_t a = e4m3x2_to_f16x2(ks), b = e4m3x2_to_f16x2(ks >> 16);
-          constexpr int kW = D / 64;                        // words of a key
-          uint32_t* to = k_sc + w % kW * 64 + w / kW;
-          to[0] = __byte_perm(a, 0, 0x1010);
-          to[16] = __byte_perm(a, 0, 0x3232);
-          to[32] = __byte_perm(b, 0, 0x1010);
-          to[48] = __byte_perm(b, 0, 0x3232);
-          const int in = left - 4 * (w & 3);                // of these four keys
-          const uint32_t vs = word(cell + Cell<D>::kVScale + 4 * w) &
-                              (in >= 4 ? ~0u : in > 0 ? (1u << 8 * in) - 1u : 0u);
-          *reinterpret_cast<uint2*>(v_sc + 2 * w) =
-              make_uint2(e4m3x2_to_f16x2(vs), e4m3x2_to_f16x2(vs >> 16));
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kP; ++i) {
-        uint32_t a[2][4];                                   // step; a0 .. a3
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t w = word(cell + i * 256 + (kr + 2 * u) * 16 + 4 * t);
-          const uint32_t up = w >> 8;
-          const uint32_t f = k_sc[(2 * i + (t >> 1)) * 16 + kr + 2 * u];
-          a[0][u] = hmul2(e2m1x2_to_f16x2<0>(w), f);
-          a[0][2 + u] = hmul2(e2m1x2_to_f16x2<0>(up), f);
-          a[1][u] = hmul2(e2m1x2_to_f16x2<2>(w), f);
-          a[1][2 + u] = hmul2(e2m1x2_to_f16x2<2>(up), f);
-        }
-#pragma unroll
-        for (int x = 0; x < kTiles; ++x) {
-          const uint4 q = qf[(x * kP + i) * 32 + lane];
-          mma16816(s[x], a[0][0], a[0][1], a[0][2], a[0][3], q.x, q.y);
-          mma16816(s_odd[x], a[1][0], a[1][1], a[1][2], a[1][3], q.z, q.w);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] += s_odd[x][e];
-      // ---- probabilities ----
-      if (key0 + kCellRows > sure) {   // (a masked score is minus infinity whatever its scale)
-#pragma unroll
-        for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key0 + kr + (e & 2) >= vis[x][e & 1])
-              s[x][e] = sc[x][e & 1] < 0.f ? INFINITY : -INFINITY;
-      }
-      float pr[kTiles][4];
-      float mx = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[x][e] = fmaf(s[x][e], sc[x][e & 1], nm[x][e & 1]);
-          mx = fmaxf(mx, pr[x][e]);
-        }
-      if (__any_sync(0xffffffffu, mx > kMoveLog2 + kLift)) {
-#pragma unroll
-        for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = fmaxf(s[x][e] * sc[x][e], s[x][e + 2] * sc[x][e]);
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
-            const float was = kLift - nm[x][e], now = fmaxf(was, y);
-            const float f = ex2(was - now);
-            nm[x][e] = kLift - now;
-            l[x][e] *= f;
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-              o[i][x][e] *= f;
-              o[i][x][e + 2] *= f;
-            }
-            pr[x][e] = fmaf(s[x][e], sc[x][e], nm[x][e]);
-            pr[x][e + 2] = fmaf(s[x][e + 2], sc[x][e], nm[x][e]);
-          }
-      }
-      uint32_t b[kTiles][2];
-#pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float p0 = ex2(pr[x][2 * u]), p1 = ex2(pr[x][2 * u + 1]);
-          l[x][0] += p0;
-          l[x][1] += p1;
-          asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;"
-                       : "=r"(b[x][u])
-                       : "r"(pack_f16(p0, p1)));
-        }
-      // ---- O^T += V^T P^T ----
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        const uint32_t w = word(cell + Cell<D>::kV + (8 * i + gl) * 16 + 4 * t);
-        const uint2 f = *reinterpret_cast<const uint2*>(v_sc + 8 * i + 2 * t);
-        const uint32_t f0 = f.x, f1 = f.y;
-        // low (even dim) and high nibbles of two keys to a byte, bytes 0 and 2
-        const uint32_t w4 = w >> 4, w8 = w >> 8;
-        const uint32_t lo = (w & 0x000F000Fu) | (w4 & ~0x000F000Fu);
-        const uint32_t hi = (w4 & 0x000F000Fu) | (w8 & ~0x000F000Fu);
-        const uint32_t a[4] = {hmul2(e2m1x2_to_f16x2<0>(lo), f0),
-                               hmul2(e2m1x2_to_f16x2<0>(hi), f0),
-                               hmul2(e2m1x2_to_f16x2<2>(lo), f1),
-                               hmul2(e2m1x2_to_f16x2<2>(hi), f1)};
-#pragma unroll
-        for (int x = 0; x < kTiles; ++x)
-          mma16816(o[i][x], a[0], a[1], a[2], a[3], b[x][0], b[x][1]);
-      }
-      __syncwarp();
-      issue(done + 1, seg);
-    }
-    // ---- the warps' results, joined in order ----
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 8 * x + 2 * t + e;
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], w);
-        if (gl == 0) wml[warp * C::kRows + row] = make_float2(-nm[x][e], l[x][e]);
-        float* dst = join + (warp * C::kRows + row) * C::kPitch + 2 * gl;
-#pragma unroll
-        for (int i = 0; i < kI; ++i)
-          *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[i][x][e], o[i][x][e + 2]);
-      }
-    if (bar_or(1, 32 * C::kWarps, wait.gave_up())) break;
-    if (!go) griddep_launch_dependents();
-    const int n_el = min(r.rows, C::kRows) * (D / 4);
-#pragma unroll 1
-    for (int i = threadIdx.x; i < n_el; i += 32 * C::kWarps) {
-      const int row = i / (D / 4), d = i % (D / 4) * 4;
-      float M = 2.f * kNoMax, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, wml[w * C::kRows + row].x);
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        const float2 ml = wml[w * C::kRows + row];
-        const float f = ex2(ml.x - M);
-        const float4 v =
-            *reinterpret_cast<const float4*>(join + (w * C::kRows + row) * C::kPitch + d);
-        L += f * ml.y;
-        y.x += f * v.x;
-        y.y += f * v.y;
-        y.z += f * v.z;
-        y.w += f * v.w;
-      }
-      if (r.whole) {
-        const float f = L == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, r.h)) / L;
-        const int tq = row * p.group_inv >> 16;
-        uint2 u = make_uint2(0, 0);
-        if (L != 0.f) {
-          u.x = static_cast<uint32_t>(float_to_bf16_bits(y.x * f)) |
-                static_cast<uint32_t>(float_to_bf16_bits(y.y * f)) << 16;
-          u.y = static_cast<uint32_t>(float_to_bf16_bits(y.z * f)) |
-                static_cast<uint32_t>(float_to_bf16_bits(y.w * f)) << 16;
-        }
-        *reinterpret_cast<uint2*>(
-            p.out + static_cast<size_t>(r.row0 + tq * p.n_q_heads + row - tq * G) * D + d) = u;
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(r.slot) * 16 + row) * D + d) = y;
-        if (d == 0) {
-          float* ml = p.part_ml + (static_cast<size_t>(r.slot) * 16 + row) * 2;
-          ml[0] = M;
-          ml[1] = L;
-        }
-      }
-    }
-    warp_arrive(&seg_empty[seg % C::kSegs]);
-    named_bar_sync(1, 32 * C::kWarps);              // join and wml are read
-  }
-  // no copy may still be landing when the CTA exits
-#pragma unroll 1
-  for (int k = done; k < issued; ++k)
-    mbar_wait_drain(&mine[k % C::kStages], (k / C::kStages) & 1, p.status);
 }
 
 // Joins the pieces of the unit that starts in CTA blockIdx.x of the kernel above
@@ -1658,29 +806,6 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
     *reinterpret_cast<uint32_t*>(out) = y[0];
 }
 
-// set_smem_limit, the first time on each device (a bit of *ready; past 64 every time).
-int smem_limit_once(std::atomic<uint64_t>* ready, const void* kernel, int bytes) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH_E_CUDA;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (ready->load(std::memory_order_acquire) & bit) return DFLASH_OK;
-  const int rc = set_smem_limit(kernel, bytes);
-  if (rc == DFLASH_OK) ready->fetch_or(bit, std::memory_order_release);
-  return rc;
-}
-
-template <int D, int kTiles>
-int run_rows(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
-  using C = RowsCfg<D, kTiles>;
-  static std::atomic<uint64_t> ready{0};
-  int rc = smem_limit_once(&ready, reinterpret_cast<const void*>(kv4_rows_kernel<D, kTiles>),
-                           C::kSmem);
-  if (rc) return rc;
-  if ((rc = launch(kv4_rows_kernel<D, kTiles>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, p)))
-    return rc;
-  return launch(kv4_join_kernel<D, 16>, dim3(ctas, C::kRows / 4), dim3(128), 0, st, p);
-}
-
 // Query columns of a unit: the fewest that hold the rows of the longest sequence.
 int query_columns(const dflash_kv4_dims& d) {
   const long long rows =
@@ -1717,12 +842,14 @@ int run(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
 }
 
 }  // namespace
+}  // namespace kv4
 
-size_t kv4_attention_bytes(const dflash_kv4_dims& d) { return attn_layout(d).total; }
+size_t kv4_attention_bytes(const dflash_kv4_dims& d) { return kv4::attn_layout(d).total; }
 
 }  // namespace dflash
 
 using namespace dflash;
+using namespace dflash::kv4;
 
 extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
                                     const int32_t* start, const dflash_kv4_view* cache,
@@ -1734,6 +861,8 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   if (!q || !start || !out || !cache || !cache->kv.seq_len || !std::isfinite(scale))
     return DFLASH_E_ARG;
   Kv4AttnParams p = {};
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  if (!std::isfinite(p.scale_log2)) return DFLASH_E_ARG;
   if ((rc = kv4_store(*dims, cache, &p.s))) return rc;
   if (!aligned16(q) || !aligned16(out)) return DFLASH_E_ALIGN;
   Kv4Plan plan;
@@ -1765,7 +894,6 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.page_table = cache->kv.page_table;
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.status = ws_at<uint32_t>(ws, plan.off_status);
   p.meta = ws_at<int>(ws, plan.off_att);
   p.part_ml = ws_at<float>(ws, plan.off_att + a.off_ml);
@@ -1773,10 +901,12 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool wide = dims->head_dim == 128;
   switch (a.nq) {
-    case 16:
-      if (static_cast<long long>(p.max_tokens) * p.group <= 8)
-        return wide ? run_rows<128, 1>(p, a.ctas, st) : run_rows<64, 1>(p, a.ctas, st);
-      return wide ? run_rows<128, 2>(p, a.ctas, st) : run_rows<64, 2>(p, a.ctas, st);
+    case 16: {
+      const int tiles = static_cast<long long>(p.max_tokens) * p.group <= 8 ? 1 : 2;
+      if ((rc = launch_rows(p, dims->head_dim, tiles, a.ctas, st))) return rc;
+      return launch(wide ? kv4_join_kernel<128, 16> : kv4_join_kernel<64, 16>,
+                    dim3(a.ctas, 2 * tiles), dim3(128), 0, st, p);
+    }
     case 32: return wide ? run<128, 32>(p, a.ctas, st) : run<64, 32>(p, a.ctas, st);
     case 64: return wide ? run<128, 64>(p, a.ctas, st) : run<64, 64>(p, a.ctas, st);
     default: return wide ? run<128, 128>(p, a.ctas, st) : run<64, 128>(p, a.ctas, st);

@@ -206,11 +206,9 @@ __global__ void __launch_bounds__(CellIo<D>::kThreads) kv4_gather_kernel(
 int kv4_store(const dflash_kv4_dims& d, const dflash_kv4_view* v, Kv4Store* s) {
   if (!v || !v->kv.k) return DFLASH_E_ARG;
   const dflash_kv_view& c = v->kv;
-  long long rows;
   if (c.page_table) {
     if (c.page_size < 1 || c.max_pages < 1 || c.n_pages < 1) return DFLASH_E_ARG;
     if (c.page_size % kCellRows) return DFLASH_E_UNSUPPORTED;
-    if (static_cast<long long>(c.max_pages) * c.page_size > INT32_MAX) return DFLASH_E_UNSUPPORTED;
     s->slab_rows = c.page_size;
     s->n_slabs = c.n_pages;
   } else {
@@ -219,8 +217,12 @@ int kv4_store(const dflash_kv4_dims& d, const dflash_kv4_view* v, Kv4Store* s) {
     s->slab_rows = c.capacity;
     s->n_slabs = d.batch;
   }
-  rows = static_cast<long long>(s->slab_rows) * s->n_slabs;
-  if (rows > INT32_MAX) return DFLASH_E_UNSUPPORTED;   // slots are int32
+  const long long rows = static_cast<long long>(s->slab_rows) * s->n_slabs;
+  // slots and cell numbers are int32, and the tiles of a longest sequence end below 2^31
+  const long long limit =
+      c.page_table ? static_cast<long long>(c.max_pages) * c.page_size : c.capacity;
+  if (rows > INT32_MAX || rows / kCellRows * d.n_kv_heads > INT32_MAX || limit > INT32_MAX - 512)
+    return DFLASH_E_UNSUPPORTED;
   if (!aligned16(c.k)) return DFLASH_E_ALIGN;
   s->cells = static_cast<uint8_t*>(c.k);
   s->k_exp = v->k_exp;
@@ -279,5 +281,6 @@ extern "C" int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slo
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto* kernel = dims->head_dim == 128 ? kv4_gather_kernel<128> : kv4_gather_kernel<64>;
   return launch(kernel, grid, block, 0, st, s, slot, static_cast<uint16_t*>(k_out),
-                static_cast<uint16_t*>(v_out), static_cast<long long>(dims->n_tokens), ws_at<uint32_t>(ws, 0));
+                static_cast<uint16_t*>(v_out), static_cast<long long>(dims->n_tokens),
+                ws_at<uint32_t>(ws, 0));
 }

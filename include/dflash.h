@@ -462,7 +462,8 @@ typedef struct {
  * count as the nearer end).  kv.k points at the cells, kv.v is NULL:
  *   paged:      [n_pages][Hkv][page_size / 16][18 D], page_size a multiple of 16
  *   contiguous: [B][Hkv][capacity / 16][18 D], capacity a multiple of 16
- * The other members of kv are those of a bf16 cache. */
+ * The other members of kv are those of a bf16 cache.  Rows and cells of the pool
+ * count below 2^31, a sequence's capacity below 2^31 - 512. */
 typedef struct {
   dflash_kv_view kv;
   const int32_t* k_exp;  /* int32 [Hkv] device, or NULL: all 0 */
@@ -555,11 +556,16 @@ DFLASH_API int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slo
  *   h / (Hq/Hkv), m = L - T + t + 1 when causal != 0, else m = L
  * (q rotated already, as dflash_qk_norm_rope leaves it).  A row that sees
  * nothing (m <= 0) is zero.
- *   q, out: bf16 [N, Hq, D]; start: int32 [B + 1]; scale finite.
+ *   q, out: bf16 [N, Hq, D]; start: int32 [B + 1]; scale finite, in units of log 2
+ *   too (times 1.4427).  Queries enter the products to 2^-12 of an element or
+ *   2^-23 of the largest one among the up to 128 rows that share a KV head's
+ *   unit of work, whichever is more; N * Hq must be below 2^31.
  * A sequence whose rows do not lie in 0..N, with T > max_tokens, or with L < 0
  * or past the capacity sets DFLASH_ST_CAPACITY and its output is left unwritten;
  * unmapped pages inside the length set DFLASH_ST_PAGE_MISSING and read as zeros,
  * as do pages numbered past the pool.  Cells past the length are not used.
+ * A batch with more than 2^31 - 1 tiles of 128 rows in all (with 4 to 6 more for
+ * each unit of up to 128 query rows) sets DFLASH_ST_CAPACITY and writes nothing.
  */
 DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
                                     const int32_t* start, const dflash_kv4_view* cache,

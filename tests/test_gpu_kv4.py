@@ -477,6 +477,59 @@ def test_attention_nan_query_stays_in_its_row():
     np.testing.assert_array_equal(got, ref)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("group,T", [(1, 1), (4, 1), (8, 1), (3, 5), (16, 1), (7, 4), (4, 16), (5, 12),
+                                     (8, 16), (16, 13)])
+def test_attention_long_and_uneven(group, T, causal, d):
+    """Contexts that many CTAs share beside short ones: units cut at any tile, CTAs with
+    several units, at every number of query rows to a unit."""
+    rng = np.random.default_rng(group * T)
+    lens = [int(x) for x in rng.integers(1, 900, 12)] + [6000, 1, 129, 2500]
+    new = [min(T, n) if i % 5 else 0 for i, n in enumerate(lens)]
+    check_attention(rng, Cache(rng, lens, 1, d), new, group, causal, pad=1)
+
+
+@pytest.mark.parametrize("group,T", [(2, 1), (4, 4), (8, 4), (4, 16), (4, 30)])
+def test_attention_scale_zero_and_negative(group, T):
+    """Scale 0 weighs every row alike; a negative one turns the order round."""
+    rng = np.random.default_rng(T)
+    cache = Cache(rng, [300, 40], 2, 64)
+    for scale in (0.0, -0.125):
+        check_attention(rng, cache, [T, T], 2 * group, True, scale=scale)
+
+
+@pytest.mark.parametrize("group,T", [(2, 1), (4, 4), (8, 4), (4, 16), (4, 30)])
+def test_attention_zero_rows_at_the_smallest_gain(group, T):
+    """Factors of a score below 2^-149: rows past the length and masked ones still count nothing."""
+    rng = np.random.default_rng(T)
+    cache = Cache(rng, [37, 200], 1, 128)
+    cache.k = [np.ldexp(k, -64 - cache.k_exp[:, None]) for k in cache.k]
+    cache.view.k_exp = i32([-64])
+    q = torch.zeros(2 * T, group, 128, dtype=BF, device="cuda")
+    check_attention(rng, cache, [T, T], group, True, q=q)
+
+
+@pytest.mark.parametrize("T", [1, 4, 16])
+def test_attention_infinite_and_nan_queries_stay_in_their_rows(T):
+    dfl = _dfl()
+    rng = np.random.default_rng(T)
+    cache = Cache(rng, [200, 31], 1, 64)
+    q = bf16(rng.normal(size=(2 * T, 4, 64)))
+    clean = f64(check_attention(rng, cache, [T, T], 4, True, q=q))
+    bad = q.clone()
+    bad[0, 2, 7], bad[T, 1, 3], bad[T, 3, 0] = float("inf"), float("nan"), float("-inf")
+    out = torch.zeros_like(q)
+    dims = dfl.make_kv4_dims(2, 2 * T, T, 4, 1, 64)
+    dfl.dflash_kv4_attention(dims, bad, i32([0, T, 2 * T]), cache.view, 0.125, True, out,
+                             dfl.alloc_kv4_workspace(dims))
+    got = f64(out)
+    for row in ((0, 2), (T, 1), (T, 3)):
+        assert np.isnan(got[row]).all()
+        got[row] = clean[row]
+    np.testing.assert_array_equal(got, clean)
+
+
 def test_attention_bad_sequences_and_pages():
     """Bad lengths leave the output; pages that are missing or numbered past the pool read
     as zeros; the other sequences of the batch are right."""

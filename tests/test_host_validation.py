@@ -135,8 +135,12 @@ def test_kv4_calls_reject_bad_arguments_before_launching():
         assert f(v=view(n_pages=1 << 28)) == E_UNSUPPORTED            # rows past int32
         assert f(v=view(page_table=None, capacity=100)) == E_UNSUPPORTED
         assert f(v=view(page_table=None, capacity=1 << 30)) == E_UNSUPPORTED
+        assert f(v=view(max_pages=(1 << 27) - 1)) == E_UNSUPPORTED    # lengths near 2^31
+        many = dims(n_q_heads=4096, n_kv_heads=4096)                  # cells past int32
+        assert f(many, view(n_pages=1 << 19)) == E_UNSUPPORTED
     assert attention(q=None) == attention(out=None) == attention(start=None) == E_ARG
     assert attention(scale=float("nan")) == attention(scale=float("inf")) == E_ARG
+    assert attention(scale=3e38) == E_ARG                             # in units of log 2
     assert attention(q=p + 2) == attention(out=p + 2) == E_ALIGN
     assert attention(v=view(seq_len=None)) == E_ARG
     assert append(k=None) == append(pitch=248) == E_ARG
