@@ -47,7 +47,7 @@ struct Cfg {
   // a role grows by sharing out dims (K), cells (V^T) or query columns (softmax).  Few
   // query rows leave the expansion of K and V as the longest step: two each then.
   static constexpr int kKWgs = NQ <= 32 ? 2 : 1;
-  static constexpr int kVWgs = NQ <= 64 ? 2 : 1;
+  static constexpr int kVWgs = NQ <= 32 ? 2 : 1;
   static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;
   static constexpr int kCols = NQ / kSoftWgs;          // query columns of a softmax warpgroup
   static constexpr int kVWarps = D / 32;               // warps of it that hold rows of V^T
@@ -85,6 +85,13 @@ struct Cfg {
   static_assert(kRing >= kStages + 3, "tile records");
 };
 
+// Which key of a tile lies in TMEM lane r of S^T (and is r in the second product's k index), and
+// which dim in lane r of O^T.
+__device__ __forceinline__ int lane_key(int r) {
+  return (r & ~15) | (r & 6) << 1 | (r >> 2 & 2) | (r & 1);
+}
+__device__ __forceinline__ int lane_dim(int r) { return (r & ~15) | (r & 7) << 1 | (r >> 3 & 1); }
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     kv4_attention_kernel(const Kv4AttnParams p) {
@@ -100,7 +107,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
   float* col_nm = reinterpret_cast<float*>(col_row + 2 * NQ);  // [NQ] kLift - running maximum
   float* col_f = col_nm + NQ;                              // [NQ] rescale factor, then 1 / sum
   float* red = col_f + NQ;                                 // [4][NQ]
-  Piece* piece = reinterpret_cast<Piece*>(red + 4 * NQ);   // [2]
+  uint2* v_scales = reinterpret_cast<uint2*>(red + 4 * NQ);  // [8 kGran * 4] of the V warps
+  Piece* piece = reinterpret_cast<Piece*>(v_scales + 32 * kGran);   // [2]
   Seg* segs = reinterpret_cast<Seg*>(piece + 2);           // [2] for the query rows
   Tile* tiles = reinterpret_cast<Tile*>(segs + 2);         // [kRing]
   uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + C::kRing);
@@ -176,21 +184,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     __syncwarp();
     if (have_seg) warp_arrive(&seg_full[0]);
     warp_arrive(planned);
-    // lane: cell `lane` of the four tiles from `tile` on (negative: no such page)
-    auto cells_at = [&](int tile) {
+    // lane: page (or sequence) of cell `lane` of the four tiles from `tile` on; nothing looks
+    // at it before those tiles' turn
+    auto slab_at = [&](int tile) {
       const int key16 = tile * kGran + lane;
-      int slab = g.b, row16 = key16;
-      if (p.paged) {
-        const int page = per_slab == 1 ? key16 : key16 / per_slab;
-        row16 = key16 - page * per_slab;
-        slab = -1;
-        if (key16 * kCellRows < g.end)
-          slab = p.page_table[static_cast<size_t>(g.b) * p.max_pages + page];
-        if (slab < 0 || slab >= p.s.n_slabs) return -1;
-      }
-      return (slab * p.s.n_kv_heads + g.h) * per_slab + row16;
+      if (!p.paged) return g.b;
+      if (key16 >= (g.end + kCellRows - 1) / kCellRows) return -1;
+      return p.page_table[static_cast<size_t>(g.b) * p.max_pages +
+                          (per_slab == 1 ? key16 : key16 / per_slab)];
     };
-    int ahead = cells_at(g.tile);
+    int ahead = slab_at(g.tile);
     if (lane == 0) *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) = make_int4(-1, 0, 0, 0);
     griddep_launch_dependents();
     // (a cache that several units of a sequence read stays in L2)
@@ -204,52 +207,66 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         *reinterpret_cast<int4*>(p.meta + 4 * blockIdx.x) =
             make_int4(walk.owner(walk.here + g.nt - g.n - 1), g.lo + g.t0,
                       min(p.tile_rows, g.T - g.t0) * G, g.h);
-      int cell4 = 0;
+      const int look = min(3, g.n - 1), next_par = (seg + 1) & 1;
+      const uint8_t* src = nullptr;        // this lane's cell of four tiles
+      uint32_t have = 0, miss = 0;
 #pragma unroll 1
       for (int i = 0; i < g.n; ++i, ++j) {
-        const int st = j % C::kStages;
-        if ((i & 3) == 0) {
-          cell4 = ahead;
-          ahead = cells_at(g.tile + i + 4);
+        const int st = j % C::kStages, l0 = (i & 3) * kGran, at = lane - l0;
+        if (l0 == 0) {
+          const int key16 = (g.tile + i) * kGran + lane;
+          const bool use = key16 < (g.end + kCellRows - 1) / kCellRows;
+          const bool there = ahead >= 0 && ahead < p.s.n_slabs;
+          const int row16 = p.paged && per_slab > 1 ? key16 % per_slab : p.paged ? 0 : key16;
+          src = p.s.cells +
+                static_cast<size_t>((ahead * p.s.n_kv_heads + g.h) * per_slab + row16) * C::kCell;
+          have = __ballot_sync(0xffffffffu, use && there);
+          miss = __ballot_sync(0xffffffffu, use && !there);
+          ahead = slab_at(g.tile + i + 4);
         }
-        const int left = g.end - (g.tile + i) * kTile;
-        const int cell = __shfl_sync(0xffffffffu, cell4, (i & 3) * kGran + (lane & (kGran - 1)));
-        const bool use = lane < kGran && lane * kCellRows < left;
-        const uint32_t have = __ballot_sync(0xffffffffu, use && cell >= 0);
-        const uint32_t miss = __ballot_sync(0xffffffffu, use && cell < 0);
         go = go && wait_on<true>(&empty[st], ((j / C::kStages) & 1) ^ 1, p.status);
         if (!__all_sync(0xffffffffu, go)) {
           go = false;
           break;
         }
         uint8_t* dst = stages + st * C::kStage;
-        if (miss) {                                 // pages that are missing read as zeros
+        if (miss >> l0 & ((1u << kGran) - 1)) {     // pages that are missing read as zeros
           if (lane == 0) set_status(p.status, DFLASH_ST_PAGE_MISSING);
 #pragma unroll 1
           for (int o = lane * 16; o < C::kStage; o += 512)
-            if (miss >> (o / C::kCell) & 1)
+            if (miss >> (l0 + o / C::kCell) & 1)
               *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
           __syncwarp();
         }
-        if (lane == 0) {
-          Tile t = {left, (i == 0 ? kFirst : 0) | (i + 1 == g.n && g.final ? kFinal : 0)};
+        if (at == 0) {
+          Tile t = {g.end - (g.tile + i) * kTile,
+                    (i == 0 ? kFirst : 0) | (i + 1 == g.n && g.final ? kFinal : 0)};
           tiles[j % C::kRing] = t;
-          mbar_arrive_expect_tx(&full[st], __popc(have) * C::kCell);
+          mbar_arrive_expect_tx(&full[st],
+                                __popc(have >> l0 & ((1u << kGran) - 1)) * C::kCell);
         }
         __syncwarp();
-        if (have >> lane & 1)
-          bulk_load(dst + lane * C::kCell, p.s.cells + static_cast<size_t>(cell) * C::kCell,
-                    C::kCell, &full[st], pol);
+        // (eight lanes at once: a copy from each takes the warp 60 to 80 clocks, copies from
+        // one lane 150 each)
+        if (at >= 0 && at < kGran && have >> lane & 1)
+          bulk_load(dst + at * C::kCell, src, C::kCell, &full[st], pol);
+        if (i == look) {
+          // the next segment goes out while this one is read, so that its query rows are ready
+          // in time (128 of them take as long as six tiles)
+          Seg next = {};
+          have_seg = walk.next(p, &next);
+          if (have_seg) {
+            if (seg >= 1)
+              go = wait_on<true>(&seg_empty[next_par], (((seg + 1) >> 1) - 1) & 1, p.status);
+            if (lane == 0) segs[next_par] = next;
+            warp_arrive(&seg_full[next_par]);
+          }
+        }
       }
       if (!go) break;
-      have_seg = walk.next(p, &g);
       if (!have_seg) break;
-      const int par = (seg + 1) & 1;
-      if (seg >= 1)
-        go = wait_on<true>(&seg_empty[par], (((seg + 1) >> 1) - 1) & 1, p.status);
-      if (lane == 0) segs[par] = g;
-      warp_arrive(&seg_full[par]);
-      ahead = cells_at(g.tile);
+      g = segs[next_par];
+      ahead = slab_at(g.tile);
     }
     // no copy may still be landing when the CTA exits
 #pragma unroll 1
@@ -279,6 +296,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       need(&pv_full[j & 1], (j >> 1) & 1);
       if (first && seg > 0) need(o_empty, (seg - 1) & 1);
       if (!ok) return;
+      // P came through the generic proxy.  Its fence stands here, between the wait and the
+      // products, once a tile: in the softmax warps it took 400 clocks of each.
+      fence_proxy_async_smem();
       tc_fence_after();
       const uint32_t par = j & 1;
       if (elect_one()) {
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     // Converted as they are if the largest finite magnitude lies in [2^-2, 2^15): then
     // fp16 holds them to 2^-23 of it.  Else a second time, with a power of two that
     // brings it to [2^14, 2^15).
-    constexpr int kPer = D / 8, kItems = NQ * kPer / 64, kLoads = kItems < 8 ? kItems : 8;
+    constexpr int kPer = D / 8, kItems = NQ * kPer / 64, kLoads = 8;
     const int tid = threadIdx.x - 32 * kQuery;
     const int pc = tid % kPer;
     bool go = true;
@@ -346,52 +366,70 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       const int rows = min(p.tile_rows, g.T - g.t0) * G;
       const int row0 = (g.lo + g.t0) * p.n_q_heads + g.h * G;
       uint8_t* qs = qbuf + par * C::kQBytes;
+      auto load = [&](int q) {           // 8 dims of query row q
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (q < rows)
+          x = *reinterpret_cast<const uint4*>(
+              p.q +
+              static_cast<size_t>(row0 + q + (q * p.group_inv >> 16) * (p.n_q_heads - G)) * D +
+              8 * pc);
+        return x;
+      };
       float f = 1.f;
       int ex = 0;
       bool again = true;
 #pragma unroll 1
       for (int pass = 0; again; ++pass) {
-        uint32_t m = 0;
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        uint32_t m2 = 0;                 // largest magnitudes of the even and of the odd dims
 #pragma unroll 1
         for (int it0 = 0; it0 < kItems; it0 += kLoads) {
           uint4 x[kLoads];
 #pragma unroll
-          for (int u = 0; u < kLoads; ++u) {
-            const int q = ((it0 + u) * 64 + tid) / kPer, t = q * p.group_inv >> 16;   // q / G
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (q < rows)
-              x[u] = *reinterpret_cast<const uint4*>(
-                  p.q + static_cast<size_t>(row0 + t * p.n_q_heads + q - t * G) * D + 8 * pc);
+          for (int u = 0; u < kLoads; ++u) x[u] = load(((it0 + u) * 64 + tid) / kPer);
+          if (pass == 0 && it0 == 0) {
+            if (seg >= 2) wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
+#pragma unroll 1
+            for (int q = tid; q < NQ; q += 64) {
+              const int t = q * p.group_inv >> 16;
+              col_row[par * NQ + q] = row0 + q + t * (p.n_q_heads - G);
+              col_vis[par * NQ + q] =
+                  p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
+            }
           }
-          if (pass == 0 && it0 == 0 && seg >= 2)
-            wait.on<true>(&q_empty[par], ((seg >> 1) - 1) & 1);
 #pragma unroll
           for (int u = 0; u < kLoads; ++u) {
             const int q = ((it0 + u) * 64 + tid) / kPer;
             const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
             uint32_t y[4];
+            m2 = __vimax3_u16x2(m2, w[0] & kAbs, w[1] & kAbs);
+            m2 = __vimax3_u16x2(m2, w[2] & kAbs, w[3] & kAbs);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t a = w[e] & 0x7FFFu, c = w[e] >> 16 & 0x7FFFu;
-              m = max(m, max(a < 0x7F80u ? a : 0u, c < 0x7F80u ? c : 0u));
+            for (int e = 0; e < 4; ++e)
               y[e] = pack_f16(__uint_as_float(w[e] << 16) * f,
                               __uint_as_float(w[e] & 0xFFFF0000u) * f);
-            }
             *reinterpret_cast<uint4*>(qs + (pc >> 3) * NQ * 128 + q * 128 +
                                       (((pc & 7) ^ (q & 7)) << 4)) =
                 make_uint4(y[0], y[1], y[2], y[3]);
-            if (pc == 0 && pass == 0) {
-              const int t = q * p.group_inv >> 16;
-              col_row[par * NQ + q] = row0 + t * p.n_q_heads + q - t * G;
-              col_vis[par * NQ + q] =
-                  p.causal && q < rows ? max(0, min(g.len, g.len - g.T + g.t0 + t + 1)) : g.len;
-            }
           }
         }
         again = false;
         if (pass == 0) {
+          uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+          if (m >= 0x7F80u) {            // infinities or NaN: the largest finite one
+            m = 0;
+#pragma unroll 1
+            for (int it = 0; it < kItems; ++it) {
+              const uint4 x = load((it * 64 + tid) / kPer);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[e] & 0x7FFFu, c = w[e] >> 16 & 0x7FFFu;
+                m = max(m, max(a < 0x7F80u ? a : 0u, c < 0x7F80u ? c : 0u));
+              }
+            }
+            m = __reduce_max_sync(0xffffffffu, m);
+          }
           if (lane == 0) q_max[warp - kQuery] = m;
           named_bar_sync(15, 64);
           const int e = static_cast<int>(max(q_max[0], q_max[1]) >> 7);   // exponent + 127
@@ -404,7 +442,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       if (tid == 0) {
         Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows,
-                    g.h, p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h)) * pow2(-ex)};
+                    p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h)) * pow2(-ex),
+                    pow2(gain_exp(p.s.v_exp, g.h))};
         piece[par] = pc;
       }
       fence_proxy_async_smem();
@@ -424,34 +463,26 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       go = !(tiles[j % C::kRing].flags & kFinal);
       tc_fence_after();
       const uint8_t* cell = stages + st * C::kStage + (r / kCellRows) * C::kCell;
-      const int rr = r % kCellRows;
-      // 64 dims a round (D = 64 with two warpgroups: 32 each)
-      constexpr int kParts = D / 32 / C::kKWgs, kC = kParts < 2 ? 1 : 2;
+      const int rr = lane_key(r) % kCellRows;
+      constexpr int kParts = D / 32 / C::kKWgs;          // of 32 dims, a round each
 #pragma unroll 1
-      for (int c2 = 0; c2 < kParts / kC; ++c2) {
-        const int c0 = wg * kParts + c2 * kC;        // first 32 dims
-        uint4 w[kC];
+      for (int c = wg * kParts; c < (wg + 1) * kParts; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * c));
+        const uint32_t s2 = e4m3x2_to_f16x2(
+            *reinterpret_cast<const uint16_t*>(cell + Cell<D>::k_scale(rr, 2 * c)));
+        const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[16];
 #pragma unroll
-        for (int c = 0; c < kC; ++c)
-          w[c] = *reinterpret_cast<const uint4*>(cell + Cell<D>::k_codes(rr, 2 * (c0 + c)));
-#pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          const uint32_t s2 = e4m3x2_to_f16x2(
-              *reinterpret_cast<const uint16_t*>(cell + Cell<D>::k_scale(rr, 2 * (c0 + c))));
-          const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
-          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-          uint32_t o[16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // (bytes 0 and 2 convert as they lie; 1 and 3 would take a shift each)
-            const uint32_t sc = e < 2 ? s_lo : s_hi, up = u[e] >> 8;
-            o[4 * e] = hmul2(e2m1x2_to_f16x2<0>(u[e]), sc);
-            o[4 * e + 1] = hmul2(e2m1x2_to_f16x2<0>(up), sc);
-            o[4 * e + 2] = hmul2(e2m1x2_to_f16x2<2>(u[e]), sc);
-            o[4 * e + 3] = hmul2(e2m1x2_to_f16x2<2>(up), sc);
-          }
-          tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + (c0 + c) * 16, o);
+        for (int e = 0; e < 4; ++e) {
+          // (bytes 0 and 2 convert as they lie; 1 and 3 would take a shift each)
+          const uint32_t sc = e < 2 ? s_lo : s_hi, up = u[e] >> 8;
+          o[4 * e] = hmul2(e2m1x2_to_f16x2<0>(u[e]), sc);
+          o[4 * e + 1] = hmul2(e2m1x2_to_f16x2<0>(up), sc);
+          o[4 * e + 2] = hmul2(e2m1x2_to_f16x2<2>(u[e]), sc);
+          o[4 * e + 3] = hmul2(e2m1x2_to_f16x2<2>(up), sc);
         }
+        tmem_st_32x32b_x16(lane_base + (j & 1) * C::kKCols + c * 16, o);
       }
       warp_arrive(&empty[st]);
       tmem_st_wait();
@@ -459,13 +490,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       warp_arrive(&kd_full[j & 1]);
     }
   } else if (warp >= C::kV) {
-    // ---------------- V^T to fp16: a thread expands its dim's row ----------------
+    // ---------------- V^T to fp16: a thread expands two dims of every fourth key pair -------
+    // A byte of V holds two dims of one key, so a thread that takes both uses every bit of
+    // its words.  The store that puts row g of sixteen lanes, and row g + 8, in lanes 4 g ..
+    // 4 g + 3 fits: TMEM lane 16 i + g is dim 16 i + 2 g, lane 16 i + 8 + g the next one, and
+    // the 16 keys of a cell go to the columns in the order of lane_key().
     if ((warp & 3) < C::kVWarps) {
-      const int d = threadIdx.x & 127, wg = (warp - C::kV) >> 2, g0 = wg * C::kVGran;
+      const int w4 = warp & 3, wg = (warp - C::kV) >> 2, g0 = wg * C::kVGran;
+      const int t = lane & 3;
       const uint32_t lane_base =
-          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + C::kV0 + g0 * 8;
-      uint32_t mul = d & 1 ? 1 : 16, mul16 = 16 * mul;         // to the byte's high nibble
-      asm volatile("" : "+r"(mul), "+r"(mul16));               // (factors, not shifts)
+          tmem + (static_cast<uint32_t>(w4 * 32) << 16) + C::kV0 + g0 * 8;
+      uint2* scales = v_scales + (warp - C::kV) * 8 * C::kVGran;   // [16 dims][cell][4 keys]
       bool go = true;
 #pragma unroll 1
       for (int j = 0; go; ++j) {
@@ -473,40 +508,43 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         wait(&full[st], (j / C::kStages) & 1);
         wait(&pv_done[j & 1], ((j >> 1) & 1) ^ 1);
         if (wait.gave_up()) break;
-        const Tile t = tiles[j % C::kRing];
-        go = !(t.flags & kFinal);
+        const Tile tile = tiles[j % C::kRing];
+        go = !(tile.flags & kFinal);
         tc_fence_after();
         const uint8_t* base = stages + st * C::kStage + g0 * C::kCell;
         // keys in use from this warpgroup's first cell on
-        const int left = t.left - g0 * kCellRows;
-        const uint8_t* code = base + Cell<D>::v_codes(0, d / 2);
-        const uint8_t* scl = base + Cell<D>::v_scale(0, d / 16);
+        const int left = tile.left - g0 * kCellRows;
+        // the scales to fp16 once for the sixteen that share one, 0 past the length (codes are
+        // finite whatever they hold)
+#pragma unroll
+        for (int u = lane; u < 8 * C::kVGran; u += 32) {
+          const int c = u / 4 % C::kVGran, i = u / (4 * C::kVGran), key = 4 * (u & 3);
+          const int in = left - c * kCellRows - key;              // of these four keys
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                                 base + c * C::kCell + Cell<D>::v_scale(key, 2 * w4 + i)) &
+                             (in >= 4 ? ~0u : in > 0 ? (1u << 8 * in) - 1u : 0u);
+          scales[u] = make_uint2(e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
+        }
+        __syncwarp();
+        const uint8_t* code = base + Cell<D>::v_codes(4 * t, 16 * w4 + (lane >> 2));
 #pragma unroll 2
         for (int c = 0; c < C::kVGran; ++c) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(code + c * C::kCell);
-          const uint4 s4 = *reinterpret_cast<const uint4*>(scl + c * C::kCell);
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-          const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
-          uint32_t o[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // this dim's nibbles of four keys, two to a byte (0 and 2, which convert as they
-            // lie): shifts as products leave the integer pipe to the conversions
-            const uint32_t x =
-                ((w[e] * mul & 0xF000F000u) | (w[e] * mul16 & ~0xF000F000u)) >> 8;
-            o[2 * e] = hmul2(e2m1x2_to_f16x2<0>(x), e4m3x2_to_f16x2(s[e]));
-            o[2 * e + 1] =
-                hmul2(e2m1x2_to_f16x2<2>(x), e4m3x2_to_f16x2(s[e] >> 16));
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w =
+                *reinterpret_cast<const uint32_t*>(code + c * C::kCell + i * 8 * kCellRows);
+            const uint2 f = scales[(i * C::kVGran + c) * 4 + t];
+            // low (even dim) and high nibbles of two keys to a byte, bytes 0 and 2
+            const uint32_t x4 = w >> 4, x8 = w >> 8;
+            const uint32_t lo = (w & 0x000F000Fu) | (x4 & ~0x000F000Fu);
+            const uint32_t hi = (x4 & 0x000F000Fu) | (x8 & ~0x000F000Fu);
+            tmem_st_16x128b_x2(lane_base + (static_cast<uint32_t>(16 * i) << 16) +
+                                   (j & 1) * C::kVCols + c * 8,
+                               hmul2(e2m1x2_to_f16x2<0>(lo), f.x),
+                               hmul2(e2m1x2_to_f16x2<0>(hi), f.x),
+                               hmul2(e2m1x2_to_f16x2<2>(lo), f.y),
+                               hmul2(e2m1x2_to_f16x2<2>(hi), f.y));
           }
-          if (left < (c + 1) * kCellRows) {                // rows past the length count as 0
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int key = c * kCellRows + 2 * e;
-              if (key >= left) o[e] = 0;
-              else if (key + 1 >= left) o[e] &= 0xFFFFu;
-            }
-          }
-          tmem_st_32x32b_x8(lane_base + (j & 1) * C::kVCols + c * 8, o);
         }
         warp_arrive(&empty[st]);
         tmem_st_wait();
@@ -520,7 +558,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     constexpr int CW = C::kCols;
     constexpr bool kKeepMax = C::kKeepMax;
     const int wg = (warp - C::kSoft) >> 2, q4 = warp & 3;
-    const int r = q4 * 32 + lane, col0 = wg * CW;
+    const int r = q4 * 32 + lane, col0 = wg * CW, d = lane_dim(r), my_key = lane_key(r);
     const uint32_t bar = 1 + wg;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     float* nm = col_nm + col0;
@@ -542,7 +580,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       for (int i = 0; i < n; ++i, ++j) {
         const int sb = j % C::kSBufs;
         const uint32_t s_addr = lane_base + C::kS0 + sb * NQ + col0;
-        const int key = (tile0 + i) * kTile + r;
+        const int key = (tile0 + i) * kTile + my_key;
         const bool masked = (tile0 + i + 1) * kTile > sure;
         wait(&s_full[sb], (j / C::kSBufs) & 1);
         __syncwarp();
@@ -669,9 +707,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           *reinterpret_cast<uint4*>(prow + ((ch ^ (r & 7)) << 4)) =
               make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        fence_proxy_async_smem();
         tc_fence_before();
-        warp_arrive(&pv_full[j & 1]);
+        warp_arrive(&pv_full[j & 1]);              // (the reader fences the proxies)
       }
       // ---- the unit's (or piece's) result ----
       go = !(tiles[(j - 1) % C::kRing].flags & kFinal);
@@ -699,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         const float* s4 = red + col0 + r;
         const float sum = (s4[0] + s4[NQ]) + (s4[2 * NQ] + s4[3 * NQ]);
         // a row that sees nothing is zero (its sum is 0; NaN for a row with NaN)
-        fac[r] = whole ? (sum == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, piece[par].h)) / sum) : 1.f;
+        fac[r] = whole ? (sum == 0.f ? 0.f : piece[par].v_gain / sum) : 1.f;
         if (!whole) {
           float* ml = p.part_ml + (static_cast<size_t>(slot) * NQ + col0 + r) * 2;
           ml[0] = -nm[r];
@@ -708,28 +745,30 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       named_bar_sync(bar, 128);
       const int* row = col_row + par * NQ + col0;
-      const int rows = piece[par].rows - col0;                      // of this warpgroup
+      const int rows = min(CW, piece[par].rows - col0);             // of this warpgroup
       wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
       __syncwarp();
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < CW; c0 += 16) {
+      for (int c0 = 0; c0 < rows; c0 += 16) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(lane_base + C::kO0 + col0 + c0, v);
         tmem_ld_wait();
-        if (r < D && c0 < rows) {
-          float* po = p.part_o + (static_cast<size_t>(slot) * NQ + col0 + c0) * D + r;
+        if (r >= D) continue;
+        if (whole) {                       // (O is 0 where the sum is)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float f = fac[c0 + e];
-            const float y = f == 0.f ? 0.f : __uint_as_float(v[e]) * f;
-            if (whole) {
-              if (c0 + e < rows)
-                p.out[static_cast<size_t>(row[c0 + e]) * D + r] = float_to_bf16_bits(y);
-            } else {
-              po[e * D] = y;
-            }
+          for (int e = 0; e < 16; e += 2) {
+            const uint32_t y = pack_bf16(__uint_as_float(v[e]) * fac[c0 + e],
+                                         __uint_as_float(v[e + 1]) * fac[c0 + e + 1]);
+            if (c0 + e < rows)
+              p.out[static_cast<size_t>(row[c0 + e]) * D + d] = static_cast<uint16_t>(y);
+            if (c0 + e + 1 < rows)
+              p.out[static_cast<size_t>(row[c0 + e + 1]) * D + d] = static_cast<uint16_t>(y >> 16);
           }
+        } else {
+          float* po = p.part_o + (static_cast<size_t>(slot) * NQ + col0 + c0) * D + d;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) po[e * D] = __uint_as_float(v[e]);
         }
       }
       tc_fence_before();

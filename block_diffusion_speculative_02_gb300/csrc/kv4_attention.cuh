@@ -95,8 +95,8 @@ constexpr int kFirst = 1, kFinal = 2;
 
 // What the softmax needs of a segment, left in shared memory beside its query rows.
 struct Piece {
-  int tile, n, nt, sure, rows, h;   // sure: keys that every row sees
-  float scale;                      // log2 units per score
+  int tile, n, nt, sure, rows;      // sure: keys that every row sees
+  float scale, v_gain;              // log2 units per score; 2^exp of V's head
 };
 
 // The run of this CTA, by one warp.  With W the cost of all units, every CTA takes W / n
@@ -257,6 +257,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Named barrier of n threads that also ORs a flag over them.
 __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool v) {
   uint32_t r;
@@ -280,11 +286,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
+// Rows g (a, c) and g + 8 (b, d) of sixteen lanes, columns t and t + 4, g = lane / 4, t = lane % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, uint32_t a, uint32_t b,
+                                                   uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // Registers per thread of this warpgroup from here on.
