@@ -919,11 +919,11 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.causal = causal != 0;
   p.tile_rows = a.nq / p.group;
   p.group_inv = (65536 + p.group - 1) / p.group;
-  // Measured in tiles: with 2, 4, 5, 6, 8, 10 of them prompt chunks (128 columns) took 330,
-  // 235, 206, 191, 194, 199 us and a prompt of 4096 rows 414, 295, 267, 246, 247, 252; with
-  // 2, 4, 6, 8 blocks of 16 rows at batch 32 (64 columns) 134, 132, 134, 138 and single
-  // rows 91, 88, 89, 91.
-  p.unit_cost = a.nq == 128 ? 6 : 4;
+  // Measured in tiles: with 2, 3, 4, 5, 6 of them prompt chunks (128 columns) took 261, 201,
+  // 186, 168, 171 us and a prompt of 4096 rows 325, 277, 229, 208, 209; with 2, 3, 4 four
+  // blocks at 32K (64 columns) 90, 89, 88 us and blocks at batch 32 123, 120, 121, and single
+  // rows (the kernel for few rows) 88, 87, 84.
+  p.unit_cost = a.nq == 128 ? 5 : a.nq == 16 ? 4 : 3;
   p.paged = cache->kv.page_table != nullptr;
   p.page_size = cache->kv.page_size;
   p.max_pages = cache->kv.max_pages;
