@@ -54,6 +54,13 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// Two bf16, to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // e4m3 code of x, to nearest even, saturating at 448.
 __device__ __forceinline__ uint32_t to_e4m3(float x) {
   uint16_t r;

@@ -257,12 +257,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Named barrier of n threads that also ORs a flag over them.
 __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool v) {
   uint32_t r;

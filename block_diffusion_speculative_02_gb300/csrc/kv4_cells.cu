@@ -4,11 +4,12 @@
 //   scale = e4m3(max |x| / 6),  code = e2m1(x / scale),  x ~ 2^exp scale code.
 // A quotient that lies halfway between two codes has to stay there, to round to even: x has
 // 8 significant bits, 6 times an e4m3 midpoint 7 and an e2m1 midpoint times a scale 7, so
-// a quotient is either a midpoint or at least 2^-8 of its size away from it.  max / 6 is
-// divided (one rounding keeps a midpoint).  x / scale is a product with the scale's
-// reciprocal, within 2^-22 of its size, then rounded to a multiple of 2^-14: midpoints
-// (0.25 and up) are such multiples, and every other quotient up to 6 is 2^-10 or more
-// away from them.  (IEEE divisions for all sixteen took most of the kernel's time.)
+// a quotient is either a midpoint or at least 2^-8 of its size away from it.  Products with
+// the reciprocals, within 2^-22 of the quotients, are therefore rounded once more, to fewer
+// bits than would lose a midpoint: max / 6 to 12 significant ones (a midpoint has 5, and the
+// others stay on their side), x / scale to a multiple of 2^-14 (midpoints, 0.25 and up,
+// are such multiples, every other quotient up to 6 is 2^-10 or more away from them).  (IEEE
+// divisions took most of the kernel's time.)
 #include "kv4.cuh"
 
 namespace dflash {
@@ -27,28 +28,44 @@ __device__ __forceinline__ bool find_slot(const Kv4Store& s, int slot, int* slab
   return true;
 }
 
-// 16 bf16 (two 16-byte loads) to 16 codes (8 bytes) and their scale.
-__device__ __forceinline__ uint2 quantise16(const uint16_t* x, float gain, uint32_t* scale,
-                                            bool* bad) {
-  const uint4 a = reinterpret_cast<const uint4*>(x)[0], b = reinterpret_cast<const uint4*>(x)[1];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float v[16], m = 0.f;
+// 16 bf16 to 16 codes (8 bytes) and their scale.
+__device__ __forceinline__ uint2 quantise16(const uint4& a, const uint4& b, float gain,
+                                            uint32_t* scale, bool* bad) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  // the largest magnitude among the bits (two halves at once): they order as the values do
+  auto largest = [&w] {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = __uint_as_float(i & 1 ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16)) * gain;
-    if (!(fabsf(v[i]) <= 3.4028234e38f)) *bad = true;
-    if (isnan(v[i])) v[i] = 0.f;
-    m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < 8; i += 2)
+      m = __vimax3_u16x2(m, w[i] & 0x7FFF7FFFu, w[i + 1] & 0x7FFF7FFFu);
+    return max(m & 0xFFFFu, m >> 16);
+  };
+  float m = __uint_as_float(largest() << 16) * gain;
+  if (!(m <= 3.4028234e38f)) {           // infinite (also times the gain) or NaN
+    *bad = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((w[i] & 0x7FFFu) > 0x7F80u) w[i] &= 0xFFFF0000u;
+      if ((w[i] >> 16 & 0x7FFFu) > 0x7F80u) w[i] &= 0xFFFFu;
+    }
+    m = __uint_as_float(largest() << 16) * gain;
   }
-  *scale = to_e4m3(__fdiv_rn(m, 6.f));
+  // (4097 q less what it is past q: q in 12 bits; past 448 the scale saturates)
+  const float q = fminf(m * (1.f / 6.f), 1024.f), t = __fmul_rn(q, 4097.f);
+  *scale = to_e4m3(__fsub_rn(t, __fsub_rn(t, q)));
   if (*scale == 0) return make_uint2(0, 0);
-  const float inv = __frcp_rn(f16x2_to_float2(e4m3x2_to_f16x2(*scale)).x);
+  // (the gain is a power of two: its product with the reciprocal rounds nothing)
+  float inv = f16x2_to_float2(e4m3x2_to_f16x2(*scale)).x;
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(inv));             // within 2^-23
+  inv *= gain;
   // (an ulp between 512 and 1024 is 2^-14; quotients past 6 saturate, rounded or not)
-  auto snap = [inv](float x) { return __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 768.f), -768.f); };
+  auto snap = [inv](uint32_t x) {
+    return __fadd_rn(__fadd_rn(__fmul_rn(__uint_as_float(x), inv), 768.f), -768.f);
+  };
   uint32_t o[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 16; i += 2)
-    o[i / 8] |= to_e2m1x2(snap(v[i]), snap(v[i + 1])) << (i % 8 * 4);
+  for (int i = 0; i < 8; ++i)
+    o[i / 4] |= to_e2m1x2(snap(w[i] << 16), snap(w[i] & 0xFFFF0000u)) << (i % 4 * 8);
   return make_uint2(o[0], o[1]);
 }
 
@@ -96,14 +113,23 @@ __global__ void __launch_bounds__(CellIo<D>::kThreads) kv4_append_kernel(
   // (heads vary fastest: neighbours read and write next to each other)
   const int h = blockIdx.x % s.n_kv_heads, r = threadIdx.x / C::kG, g = threadIdx.x % C::kG;
   const long long n0 = static_cast<long long>(blockIdx.x / s.n_kv_heads) * kCellRows, n = n0 + r;
+  // (the rows are on their way before their places are known: two latencies side by side)
+  uint4 kx[2] = {}, vx[2] = {};
+  if (n < n_tokens) {
+    const uint4* ks = reinterpret_cast<const uint4*>(k + n * k_pitch + h * D + 16 * g);
+    const uint4* vs = reinterpret_cast<const uint4*>(v + n * v_pitch + h * D + 16 * g);
+    kx[0] = ks[0];
+    kx[1] = ks[1];
+    vx[0] = vs[0];
+    vx[1] = vs[1];
+  }
+  const float k_gain = pow2(-gain_exp(s.k_exp, h)), v_gain = pow2(-gain_exp(s.v_exp, h));
   const bool whole = find_rows<D>(s, slot, n0, n_tokens, h, cells, rows, status);
   if (cells[r]) {
     bool bad = false;
     uint32_t ks, vs;
-    const uint2 kc = quantise16(k + n * k_pitch + h * D + 16 * g, pow2(-gain_exp(s.k_exp, h)),
-                                &ks, &bad);
-    const uint2 vc = quantise16(v + n * v_pitch + h * D + 16 * g, pow2(-gain_exp(s.v_exp, h)),
-                                &vs, &bad);
+    const uint2 kc = quantise16(kx[0], kx[1], k_gain, &ks, &bad);
+    const uint2 vc = quantise16(vx[0], vx[1], v_gain, &vs, &bad);
     *reinterpret_cast<uint2*>(image + Cell<D>::k_codes(r, g)) = kc;
     image[Cell<D>::k_scale(r, g)] = static_cast<uint8_t>(ks);
 #pragma unroll

@@ -39,7 +39,7 @@ constexpr int kThreads = 256;
 // a time, both halves of a rotated pair in one thread), kBatch heads in flight.  Bound
 // by the 4 bytes an element moves.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 5) qk_norm_rope_kernel(const NormRopeParams p) {
   constexpr int kHalf = D / 2, kE = kHalf / 16, kW = kE / 2, kBatch = 3;
   __shared__ float2 sc[kHalf];
   griddep_wait();
@@ -83,13 +83,19 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const NormRop
     sc[d] = make_float2(cs, sn);
   }
   float2 cs[kE];
-  float w[2][2][kE];                     // gains: q or k, half, dim
+  uint32_t w[2][2][kW];                  // gains: q or k, half, two dims to a word
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      w[i][0][e] = p.w[i] ? bf16_bits_to_float(p.w[i][d0 + e]) : 1.f;
-      w[i][1][e] = p.w[i] ? bf16_bits_to_float(p.w[i][kHalf + d0 + e]) : 1.f;
+    for (int half = 0; half < 2; ++half) {
+      const uint16_t* src = p.w[i] + half * kHalf + d0;
+#pragma unroll
+      for (int e = 0; e < kW; ++e) w[i][half][e] = 0x3F803F80u;          // 1, 1
+      if (!p.w[i]) continue;
+      if (kW == 2)
+        *reinterpret_cast<uint2*>(w[i][half]) = *reinterpret_cast<const uint2*>(src);
+      else
+        w[i][half][0] = *reinterpret_cast<const uint32_t*>(src);
     }
   __syncthreads();
 #pragma unroll
@@ -122,15 +128,15 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const NormRop
         float o0[2], o1[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float g = a[e + i] * (r * (which ? w[1][0][e + i] : w[0][0][e + i]));
-          const float v = b[e + i] * (r * (which ? w[1][1][e + i] : w[0][1][e + i]));
+          const uint32_t w0 = which ? w[1][0][e / 2] : w[0][0][e / 2];
+          const uint32_t w1 = which ? w[1][1][e / 2] : w[0][1][e / 2];
+          const float g = a[e + i] * (r * __uint_as_float(i ? w0 & 0xFFFF0000u : w0 << 16));
+          const float v = b[e + i] * (r * __uint_as_float(i ? w1 & 0xFFFF0000u : w1 << 16));
           o0[i] = g * cs[e + i].x - v * cs[e + i].y;
           o1[i] = v * cs[e + i].x + g * cs[e + i].y;
         }
-        y[0][e / 2] = static_cast<uint32_t>(float_to_bf16_bits(o0[0])) |
-                      static_cast<uint32_t>(float_to_bf16_bits(o0[1])) << 16;
-        y[1][e / 2] = static_cast<uint32_t>(float_to_bf16_bits(o1[0])) |
-                      static_cast<uint32_t>(float_to_bf16_bits(o1[1])) << 16;
+        y[0][e / 2] = pack_bf16(o0[0], o0[1]);
+        y[1][e / 2] = pack_bf16(o1[0], o1[1]);
       }
       if (live) {
         uint16_t* dst = p.y[which] + n * p.y_pitch[which] + at;
