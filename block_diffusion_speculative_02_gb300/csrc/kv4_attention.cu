@@ -19,9 +19,9 @@
 // and the query rows as the columns, so that few query rows cost little:
 //   S^T [128 keys x NQ]  = K [128 x D] Q^T         A = K  from TMEM, B = Q  (shared)
 //   O^T [D x NQ]        += V^T [D x 128] P^T       A = V^T from TMEM, B = P (shared)
-// The 4-bit values never pass through shared memory again after they came: each
-// thread of one warpgroup expands its key's row of K, each of another its dim's
-// row of V^T (the cell keeps V's 16 rows side by side for that), to fp16 (exact:
+// The 4-bit values never pass through shared memory again after they came: the
+// threads of one role expand a key's row of K each, those of another two dims of V^T
+// at a time (the cell keeps V's 16 rows side by side for that), to fp16 (exact:
 // 6 significant bits) straight into TMEM.  With them in shared memory its traffic,
 // not DRAM, would bound the kernel: 128 KB written and read a tile of 18 KB.
 // Q is kept in fp16, where need be times a power of two (exact for bf16 values down to
@@ -31,6 +31,19 @@
 // of a column only moves when a tile passes it by 2^8, which one vote per tile
 // finds out; until then exp2(x - m) needs no reduction over keys at all, and the
 // column sums stay in registers until the unit ends.
+//
+// What bounds it.  Per tile of 128 keys the instruction slots: 4,900 warp instructions at
+// 64 query columns (K and V^T expansion 800 and 1,100, softmax 2,000, waits and
+// hand-overs the rest) and 7,500 at 128, so 1,230 and 1,870 clocks of the SM's four slots
+// against 1,700 and 2,450 measured; the products themselves take 512 and 1,024.  Beside the
+// tiles a unit costs three to five tiles' time: its first maxima, the drain of O, code that
+// is fetched anew.  Measured: 32 blocks of 16 rows over 512 to 16,384 keys (32 + 8 heads of
+// 128 dims) 120 us, 2.7 TB/s of cells and 590 TFLOP/s; 4 blocks at 32,768 keys, 64 heads,
+// 90 us, 765 TFLOP/s; prompt chunks of 257 to 1,024 rows 169 us, 690 TFLOP/s.
+// Tried and slower: two warpgroups that expand V at 128 columns (the registers of the
+// softmax), a second S buffer at 128 in place of those of K and V (201 us against 188 then),
+// one copy of the code that reads the scores (195 against 187: the loop costs more than the
+// instruction cache gains), scalar instead of packed products (175 against 169).
 #include <cmath>
 
 #include "kv4_attention.cuh"
@@ -44,8 +57,9 @@ struct Cfg {
   static constexpr int kCell = Cell<D>::kBytes;
   static constexpr int kStage = kGran * kCell;
   // Warpgroups of each role.  A lane of the first three holds a key or a dim in TMEM, so
-  // a role grows by sharing out dims (K), cells (V^T) or query columns (softmax).  Few
-  // query rows leave the expansion of K and V as the longest step: two each then.
+  // a role grows by sharing out dims (K), cells (V^T) or query columns (softmax).  Up to 32
+  // query rows leave the expansion of K and V as the longest step: two each then (at 64
+  // columns a second one for V is no faster).
   static constexpr int kKWgs = NQ <= 32 ? 2 : 1;
   static constexpr int kVWgs = NQ <= 32 ? 2 : 1;
   static constexpr int kSoftWgs = NQ <= 32 ? 1 : NQ / 32;

@@ -73,7 +73,7 @@ __device__ __forceinline__ uint2 quantise16(const uint4& a, const uint4& b, floa
 // and V.  Their codes meet in shared memory in the cell's own layout, so that the rows'
 // bytes, which lie 16 apart in a cell of V, leave 16 rows side by side; sixteen rows that
 // are one whole cell leave as it is, 16 bytes a store.
-// Floor: 2 bytes an element in, 0.5625 out (or back).  Prompts of 15,000 rows in all, 8 heads of
+// Floor: 2 bytes an element in, 0.5625 out (or back).  Prompts of 17,600 rows in all, 8 heads of
 // 128 dims, take 24 us each way, 3.8 TB/s: what bounds them is the passage through shared
 // memory (its barriers and byte accesses) and the conversions, not the copies.  A few rows
 // per sequence (blocks at batch 32) are launch and two dependent loads.
