@@ -887,7 +887,7 @@ int run(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
   using C = Cfg<D, NQ>;
   static std::atomic<uint64_t> ready{0};
   int rc = smem_limit_once(&ready, reinterpret_cast<const void*>(kv4_attention_kernel<D, NQ>),
-                           C::kSmem);
+                           C::kSmem, C::kRegsLaunch);
   if (rc) return rc;
   if ((rc = launch(kv4_attention_kernel<D, NQ>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, p)))
     return rc;

@@ -374,12 +374,18 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if (elect_one()) mbar_arrive(bar);
 }
 
-// set_smem_limit, the first time on each device (a bit of *ready; past 64 every time).
-inline int smem_limit_once(std::atomic<uint64_t>* ready, const void* kernel, int bytes) {
+// set_smem_limit, the first time on each device (a bit of *ready; past 64 every time).  A
+// kernel that takes registers from one role for another is refused unless it was compiled to
+// start with at least `regs` a thread: it would wait for the rest for ever.
+inline int smem_limit_once(std::atomic<uint64_t>* ready, const void* kernel, int bytes,
+                           int regs = 0) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH_E_CUDA;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (ready->load(std::memory_order_acquire) & bit) return DFLASH_OK;
+  cudaFuncAttributes at;
+  if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess) return DFLASH_E_CUDA;
+  if (at.numRegs < regs) return DFLASH_E_UNSUPPORTED;
   const int rc = set_smem_limit(kernel, bytes);
   if (rc == DFLASH_OK) ready->fetch_or(bit, std::memory_order_release);
   return rc;

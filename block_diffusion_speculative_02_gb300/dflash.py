@@ -547,11 +547,11 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     """The C struct of a view (KVView: its lengths and pages; hkv 0), checked.
 
     The struct is kept on the view for the next call, and used again as long as the view holds
-    the same tensors, at the same addresses, and the same sizes."""
+    the same tensors, at the same addresses and of the same shapes, and the same sizes."""
     get = v.__dict__.get
     tensors = tuple([get(f) for f in _VIEW_TENSORS])
     key = (device, batch, hkv, d, v.capacity, v.page_size,
-           *[0 if t is None else t.data_ptr() for t in tensors])
+           *[0 if t is None else (t.data_ptr(), t.shape) for t in tensors])
     memo = get("_struct")
     if memo is not None and memo[0] == key and all(map(operator.is_, memo[1], tensors)):
         return memo[2]

@@ -754,3 +754,49 @@ def test_refuses_wrong_tensors():
     with pytest.raises(ValueError):
         cache.view.cells = cache.view.cells[:1]
         call(q, torch.zeros_like(q), s)
+
+
+def test_view_follows_its_tensors():
+    """A view whose tensors are exchanged, moved or resized between calls is read anew."""
+    rng = np.random.default_rng(31)
+    cache = Cache(rng, [40, 70], 1, 64)
+    check_attention(rng, cache, [1, 1], 2, True)
+    wide = torch.full((2, 12), -1, dtype=I32, device="cuda")
+    wide[:, :cache.view.page_table.shape[1]] = cache.view.page_table
+    old, cache.view.page_table = cache.view.page_table, wide
+    check_attention(rng, cache, [1, 1], 2, True)
+    width = old.shape[1]
+    wide.resize_(2, width)                              # the same tensor at the same address
+    wide.copy_(old)
+    check_attention(rng, cache, [1, 1], 2, True)
+    other = Cache(rng, [40, 70], 1, 64)
+    cache.view.cells, cache.view.page_table = other.view.cells, other.view.page_table
+    cache.view.k_exp, cache.view.v_exp = other.view.k_exp, other.view.v_exp
+    cache.k, cache.v, cache.k_exp = other.k, other.v, other.k_exp
+    check_attention(rng, cache, [1, 1], 2, True)
+
+
+def test_two_streams_at_once():
+    """Two attentions on two streams with a workspace each, over one cache."""
+    dfl = _dfl()
+    rng = np.random.default_rng(32)
+    cache = Cache(rng, [900, 500, 1300], 2, 128)
+    outs, refs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for T in (16, 1):
+        gain = np.ldexp(1.0, -np.repeat(cache.k_exp, 4))[:, None]
+        q = bf16(rng.normal(size=(3 * T, 8, 128)) * gain)
+        refs.append(check_attention(rng, cache, [T] * 3, 8, True, q=q))
+        outs.append((T, q, torch.zeros_like(q)))
+    jobs = []
+    for (T, q, out), st in zip(outs, streams):
+        dims = dfl.make_kv4_dims(3, 3 * T, T, 8, 2, 128)
+        jobs.append((dims, q, i32(np.arange(4) * T), out, dfl.alloc_kv4_workspace(dims), st))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for dims, q, start, out, ws, st in jobs:
+            dfl.dflash_kv4_attention(dims, q, start, cache.view, 1 / np.sqrt(128), True, out, ws,
+                                     stream=st)
+    torch.cuda.synchronize()
+    for (dims, q, start, out, ws, st), ref in zip(jobs, refs):
+        assert status(ws) == 0
+        assert torch.equal(out, ref)
