@@ -33,6 +33,24 @@ struct NormRopeParams {
   TurnTable turns;
 };
 
+// The table of (theta, D), kept for the thread's next call: 64 powers take as long as the launch.
+const TurnTable& turn_table(float theta, int D) {
+  struct Kept {
+    float theta = 0.f;
+    int D = 0;
+    TurnTable table;
+  };
+  static thread_local Kept kept;
+  if (kept.theta != theta || kept.D != D) {
+    for (int d = 0; d < D / 2; ++d)
+      kept.table.f[d] = static_cast<unsigned long long>(std::llround(std::ldexp(
+          std::pow(static_cast<double>(theta), -2.0 * d / D) / 6.283185307179586476925, 64)));
+    kept.theta = theta;
+    kept.D = D;
+  }
+  return kept.table;
+}
+
 constexpr int kThreads = 256, kGroups = kThreads / 16;
 
 // 16 threads take a head, each D / 32 dims of either half (8 or 4 bytes at a time, both halves
@@ -213,9 +231,7 @@ extern "C" int dflash_qk_norm_rope(const dflash_kv4_dims* dims, const void* q, i
   p.heads[0] = dims->n_q_heads;
   p.heads[1] = dims->n_kv_heads;
   p.eps = rms_eps;
-  for (int d = 0; d < D / 2; ++d)
-    p.turns.f[d] = static_cast<unsigned long long>(std::llround(std::ldexp(
-        std::pow(static_cast<double>(rope_theta), -2.0 * d / D) / 6.283185307179586476925, 64)));
+  p.turns = turn_table(rope_theta, D);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(dims->n_tokens), block(kThreads);
   return D == 128 ? launch(qk_norm_rope_kernel<128>, grid, block, 0, st, p)

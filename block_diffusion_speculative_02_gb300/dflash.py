@@ -544,7 +544,7 @@ _VIEW_TENSORS = ("seq_len", "page_table", "free_list", "free_count", "cells", "k
 
 
 def _view_struct(v, device: int, batch: int, hkv: int, d: int):
-    """The C struct of a view (KVView: its lengths and pages; hkv 0), checked.
+    """The C struct of a view (with hkv 0: of its lengths and pages only), checked.
 
     The struct is kept on the view for the next call, and used again as long as the view holds
     the same tensors, at the same addresses and of the same shapes, and the same sizes."""
@@ -552,7 +552,8 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     tensors = tuple([get(f) for f in _VIEW_TENSORS])
     key = (device, batch, hkv, d, v.capacity, v.page_size,
            *[0 if t is None else (t.data_ptr(), t.shape) for t in tensors])
-    memo = get("_struct")
+    slot = "_struct" if hkv else "_pages"
+    memo = get(slot)
     if memo is not None and memo[0] == key and all(map(operator.is_, memo[1], tensors)):
         return memo[2]
     i32 = torch.int32
@@ -575,7 +576,7 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     if hkv:
         c = KV4ViewC(c, _opt(v.k_exp, device, i32, hkv, "k_exp"),
                      _opt(v.v_exp, device, i32, hkv, "v_exp"))
-    v.__dict__["_struct"] = (key, tensors, c)
+    v.__dict__[slot] = (key, tensors, c)
     return c
 
 
@@ -590,7 +591,7 @@ def dflash_kv_reserve(dims: KV4Dims, cache, n_new, start, pos, slot, new_len, ws
     dev, st = _here(stream)
     i32, b, n = torch.int32, dims.batch, dims.n_tokens
     rc = load_library().dflash_kv_reserve(
-        dims, _view_struct(cache.pages() if isinstance(cache, KV4View) else cache, dev, b, 0, 0),
+        dims, _view_struct(cache, dev, b, 0, 0),
         _on(n_new, dev, i32, b, "n_new"), _on(start, dev, i32, b + 1, "start"),
         _on(pos, dev, i32, n, "pos"), _on(slot, dev, i32, n, "slot"),
         _on(new_len, dev, i32, b, "new_len"), *_ws_on(ws, dev), st)

@@ -800,3 +800,23 @@ def test_two_streams_at_once():
     for (dims, q, start, out, ws, st), ref in zip(jobs, refs):
         assert status(ws) == 0
         assert torch.equal(out, ref)
+
+
+def test_norm_rope_follows_theta_and_head_dim():
+    """Calls in turn with other bases and head dims: each has its own angles."""
+    dfl = _dfl()
+    rng = np.random.default_rng(33)
+    for d, theta in ((64, 1e4), (128, 1e4), (128, 1e6), (64, 1e4), (64, 5e5)):
+        q, k = bf16(rng.normal(size=(5, 2, d))), bf16(rng.normal(size=(5, 1, d)))
+        pos = [0, 1, 77, 4095, 100000]
+        qo, ko = torch.zeros_like(q), torch.zeros_like(k)
+        dims = dfl.make_kv4_dims(1, 5, 5, 2, 1, d)
+        dfl.dflash_qk_norm_rope(dims, q, k, None, None, i32(pos), theta, 1e-6, qo, ko)
+        for x, y in ((q, qo), (k, ko)):
+            a = np.array(pos)[:, None] * theta ** (-2.0 * np.arange(d // 2) / d)
+            c, s = np.cos(a)[:, None], np.sin(a)[:, None]
+            lo, hi = f64(x)[..., :d // 2], f64(x)[..., d // 2:]
+            ref = np.concatenate([lo * c - hi * s, hi * c + lo * s], -1)
+            mag = np.concatenate([np.abs(lo) + np.abs(hi)] * 2, -1)
+            # half a step of bf16; angles off by 2^-23 turns, cosines and products by a few 2^-24
+            assert (np.abs(f64(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * mag).all()
