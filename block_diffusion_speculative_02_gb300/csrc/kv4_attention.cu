@@ -38,8 +38,8 @@
 // against 1,700 and 2,450 measured; the products themselves take 512 and 1,024.  Beside the
 // tiles a unit costs three to five tiles' time: its first maxima, the drain of O, code that
 // is fetched anew.  Measured: 32 blocks of 16 rows over 512 to 16,384 keys (32 + 8 heads of
-// 128 dims) 120 us, 2.7 TB/s of cells and 590 TFLOP/s; 4 blocks at 32,768 keys, 64 heads,
-// 90 us, 765 TFLOP/s; prompt chunks of 257 to 1,024 rows 169 us, 690 TFLOP/s.
+// 128 dims) 119 us, 2.7 TB/s of cells and 595 TFLOP/s; 4 blocks at 32,768 keys, 64 heads,
+// 86 us, 800 TFLOP/s; prompt chunks of 257 to 1,024 rows 163 us, 715 TFLOP/s.
 // Tried and slower: two warpgroups that expand V at 128 columns (the registers of the
 // softmax), a second S buffer at 128 in place of those of K and V (201 us against 188 then),
 // one copy of the code that reads the scores (195 against 187: the loop costs more than the
@@ -798,65 +798,117 @@ done:
   if (warp == kMma) tmem_dealloc(*tmem_slot, 512);
 }
 
-// Joins the pieces of the unit that starts in CTA blockIdx.x of the kernel above
-// and ends in a later one: a warp per query row.
-template <int D, int NQ>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
+// Joins the pieces of the unit that starts in CTA blockIdx.x of the kernel above and ends in a
+// later one, in their order: a warp takes kR query rows and reads 4 or 8 pieces at a time.
+// (Joined by whichever CTA writes the last piece, a block at 8192 keys, 19 pieces a unit, took
+// 23 us in place of 18: one SM then reads them all.)
+template <int NQ, int kR>
+constexpr int kJoinWarps = NQ / kR < 8 ? NQ / kR : 8;
+
+template <int D, int NQ, int kR>
+__global__ void __launch_bounds__(32 * kJoinWarps<NQ, kR>) kv4_join_kernel(const Kv4AttnParams p) {
   griddep_wait();
   griddep_launch_dependents();
+  constexpr int kV = D / 32, kAhead = kR == 1 ? 8 : 4;
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 meta = *reinterpret_cast<const int4*>(p.meta + 4 * c0);
-  const int c1 = meta.x, row0 = meta.y, h = meta.w;
-  const int q = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (c1 < 0 || q >= meta.z) return;
-  constexpr int kV = D / 32;
-  float o[kV], L = 0.f, M = kNoMax;
+  const int c1 = meta.x, row0 = meta.y, rows = meta.z, h = meta.w;
+  const int q0 = (blockIdx.y * kJoinWarps<NQ, kR> + (threadIdx.x >> 5)) * kR;
+  if (c1 < 0 || q0 >= rows) return;
+  const float gain = pow2(gain_exp(p.s.v_exp, h));
+  auto slot = [&](int c) { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * NQ + q0; };
+  auto ml_of = [&](int c, int u) {
+    return *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot(c) + u));
+  };
+  float o[kR][kV], L[kR], M[kR];
 #pragma unroll
-  for (int e = 0; e < kV; ++e) o[e] = 0.f;
-  auto slot = [&](int c) { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * NQ + q; };
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[2 * slot(c)]);
-  M = warp_max(M);
+  for (int u = 0; u < kR; ++u) {
+    L[u] = 0.f;
+    M[u] = kNoMax;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) o[u][e] = 0.f;
+  }
+#pragma unroll 1
+  for (int c = c0 + lane; c <= c1; c += 32)
+#pragma unroll
+    for (int u = 0; u < kR; ++u) M[u] = fmaxf(M[u], ml_of(c, u).x);
+#pragma unroll
+  for (int u = 0; u < kR; ++u) M[u] = warp_max(M[u]);
+#pragma unroll 1
   for (int cb = c0; cb <= c1; cb += 32) {
-    float w = 0.f;
-    if (cb + lane <= c1) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * slot(cb + lane));
-      w = ex2(ml.x - M);
-      L += w * ml.y;
+    float w[kR];                           // of piece cb + lane
+#pragma unroll
+    for (int u = 0; u < kR; ++u) {
+      const float2 ml = cb + lane <= c1 ? ml_of(cb + lane, u) : make_float2(kNoMax, 0.f);
+      w[u] = cb + lane <= c1 ? ex2(ml.x - M[u]) : 0.f;
+      L[u] += w[u] * ml.y;
     }
-#pragma unroll 4
-    for (int i = 0; i < min(32, c1 - cb + 1); ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.part_o + slot(cb + i) * D + lane * kV;
-      if (kV == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        o[0] += wi * x.x;
-        o[1] += wi * x.y;
-        o[2 % kV] += wi * x.z;
-        o[3 % kV] += wi * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        o[0] += wi * x.x;
-        o[1] += wi * x.y;
+    const int n = min(32, c1 - cb + 1);
+#pragma unroll 1
+    for (int i = 0; i < n; i += kAhead) {
+      float x[kAhead][kR][kV];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i + k >= n) break;
+        const float* src = p.part_o + slot(cb + i + k) * D + lane * kV;
+#pragma unroll
+        for (int u = 0; u < kR; ++u) {
+          if (kV == 4)
+            *reinterpret_cast<float4*>(x[k][u]) = *reinterpret_cast<const float4*>(src + u * D);
+          else
+            *reinterpret_cast<float2*>(x[k][u]) = *reinterpret_cast<const float2*>(src + u * D);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i + k >= n) break;
+#pragma unroll
+        for (int u = 0; u < kR; ++u) {
+          const float f = __shfl_sync(0xffffffffu, w[u], i + k);
+#pragma unroll
+          for (int e = 0; e < kV; ++e) o[u][e] += f * x[k][u][e];
+        }
       }
     }
   }
 #pragma unroll
-  for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-  const float f = L == 0.f ? 0.f : pow2(gain_exp(p.s.v_exp, h)) / L;
-  const int t = q / p.group;
-  uint16_t* out =
-      p.out + (static_cast<size_t>(row0 + t) * p.n_q_heads + h * p.group + q - t * p.group) * D +
-      lane * kV;
-  uint32_t y[kV / 2];
+  for (int u = 0; u < kR; ++u) {
+    const int q = q0 + u, t = q * p.group_inv >> 16;
+    if (q >= rows) break;
 #pragma unroll
-  for (int e = 0; e < kV / 2; ++e)
-    y[e] = L == 0.f ? 0u
-                    : static_cast<uint32_t>(float_to_bf16_bits(o[2 * e] * f)) |
-                          static_cast<uint32_t>(float_to_bf16_bits(o[2 * e + 1] * f)) << 16;
-  if (kV == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[kV / 2 - 1]);
-  else
-    *reinterpret_cast<uint32_t*>(out) = y[0];
+    for (int x = 16; x; x >>= 1) L[u] += __shfl_xor_sync(0xffffffffu, L[u], x);
+    const float f = L[u] == 0.f ? 0.f : gain / L[u];     // (O is 0 where the sum is)
+    uint32_t y[kV / 2];
+#pragma unroll
+    for (int e = 0; e < kV / 2; ++e) y[e] = pack_bf16(o[u][2 * e] * f, o[u][2 * e + 1] * f);
+    uint16_t* out =
+        p.out +
+        (static_cast<size_t>(row0 + t) * p.n_q_heads + h * p.group + q - t * p.group) * D +
+        lane * kV;
+    if (kV == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[kV / 2 - 1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = y[0];
+  }
+}
+
+template <int D, int NQ, int kR>
+int launch_join(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
+  constexpr int kWarps = kJoinWarps<NQ, kR>;
+  return launch(kv4_join_kernel<D, NQ, kR>, dim3(ctas, NQ / kR / kWarps), dim3(32 * kWarps), 0, st,
+                p);
+}
+
+// Four rows a warp; one where a unit is small or cut into eight pieces or more.  Measured with
+// one and four: a block at 8192 keys (19 pieces) 16.5 and 18.8 us, single rows (units of 16)
+// 83.2 and 83.7; four blocks at 32,768 keys (5 pieces) 87.0 and 85.8, prompt chunks (2 to 3)
+// 167.1 and 163.5: there CTAs without work cost more than they save.
+template <int D, int NQ>
+int run_join(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
+  const long long units = static_cast<long long>(p.batch) * p.s.n_kv_heads *
+                          ((p.max_tokens + p.tile_rows - 1) / p.tile_rows);
+  return NQ == 16 || units * 8 <= ctas ? launch_join<D, NQ, 1>(p, ctas, st)
+                                       : launch_join<D, NQ, 4>(p, ctas, st);
 }
 
 // Query columns of a unit: the fewest that hold the rows of the longest sequence.
@@ -891,7 +943,7 @@ int run(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
   if (rc) return rc;
   if ((rc = launch(kv4_attention_kernel<D, NQ>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, p)))
     return rc;
-  return launch(kv4_join_kernel<D, NQ>, dim3(ctas, NQ / 4), dim3(128), 0, st, p);
+  return run_join<D, NQ>(p, ctas, st);
 }
 
 }  // namespace
@@ -957,8 +1009,7 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
     case 16: {
       const int tiles = static_cast<long long>(p.max_tokens) * p.group <= 8 ? 1 : 2;
       if ((rc = launch_rows(p, dims->head_dim, tiles, a.ctas, st))) return rc;
-      return launch(wide ? kv4_join_kernel<128, 16> : kv4_join_kernel<64, 16>,
-                    dim3(a.ctas, 2 * tiles), dim3(128), 0, st, p);
+      return wide ? run_join<128, 16>(p, a.ctas, st) : run_join<64, 16>(p, a.ctas, st);
     }
     case 32: return wide ? run<128, 32>(p, a.ctas, st) : run<64, 32>(p, a.ctas, st);
     case 64: return wide ? run<128, 64>(p, a.ctas, st) : run<64, 64>(p, a.ctas, st);
