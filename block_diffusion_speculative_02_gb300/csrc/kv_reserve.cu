@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kSmallThreads) reserve_small_kernel(const Rese
       }
       __syncwarp();
     }
-    for (int i = lane; i < n && row0 + i < p.n_tokens; i += 32) {
+    for (int i = lane; i < min(n, p.n_tokens - row0); i += 32) {   // (row0 may be near 2^31)
       int pos = -1, slot = -1;
       if (served) {
         pos = len + i;
@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kSmallThreads) reserve_small_kernel(const Rese
       p.new_len[b] = served ? len + n : len;
     }
   }
-  for (int i = first[p.batch] + tid; i < p.n_tokens; i += kSmallThreads) {
+  for (long long i = static_cast<long long>(first[p.batch]) + tid; i < p.n_tokens;
+       i += kSmallThreads) {
     p.pos[i] = -1;                         // rows behind the last sequence
     p.slot[i] = -1;
   }

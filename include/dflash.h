@@ -526,7 +526,8 @@ DFLASH_API int dflash_qk_norm_rope(const dflash_kv4_dims* dims, const void* q, i
  * even, saturating (scale 0: all codes 0).  Infinite elements are stored as
  * the largest, NaN as 0; both set DFLASH_ST_BAD_VALUE, so the cells hold finite
  * values only.  Rows with slot[n] < 0 are skipped; a slot past the pool sets
- * DFLASH_ST_CAPACITY and is skipped.  Slots that are not negative must differ.
+ * DFLASH_ST_CAPACITY and is skipped.  Slots that are not negative must differ
+ * (one given twice ends up with codes of either row).
  * seq_len is not touched (dflash_kv_reserve's new_len holds the lengths).
  *   k, v: bf16 [N, Hkv, D], rows k_pitch, v_pitch elements apart (a multiple
  *   of 8, at least Hkv * D); slot: int32 [N].

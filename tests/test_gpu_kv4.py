@@ -820,3 +820,28 @@ def test_norm_rope_follows_theta_and_head_dim():
             mag = np.concatenate([np.abs(lo) + np.abs(hi)] * 2, -1)
             # half a step of bf16; angles off by 2^-23 turns, cosines and products by a few 2^-24
             assert (np.abs(f64(y) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * mag).all()
+
+
+@pytest.mark.parametrize("n_tokens", [40, 8300])              # one launch, and two
+def test_reserve_counts_past_int32(n_tokens):
+    """Counts whose sum passes 2^31 (offsets stop there): every sequence behind is refused."""
+    dfl = _dfl()
+    lens, new = [4, 0, 7, 3], [5, 2 ** 31 - 3, 40, 2 ** 31 - 1]
+    dims = dfl.make_kv4_dims(4, n_tokens, 16, 1, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    view = dfl.KVView(None, None, i32(lens), 64, i32(np.full((4, 4), -1)), i32(range(9)), i32([9]),
+                      16)
+    guard = 4096
+    start, new_len = (torch.full((m,), -9, dtype=I32, device="cuda") for m in (5, 4))
+    pos, slot = (torch.full((n_tokens + 2 * guard,), -9, dtype=I32, device="cuda")
+                 for _ in range(2))
+    inner = slice(guard, guard + n_tokens)
+    dfl.dflash_kv_reserve(dims, view, i32(new), start, pos[inner], slot[inner], new_len, ws)
+    assert status(ws) == bits("capacity")
+    top = 2 ** 31 - 1
+    assert start.tolist() == [0, 5, top, top, top] and new_len.tolist() == [9, 0, 7, 3]
+    assert pos[inner].tolist() == [4, 5, 6, 7, 8] + [-1] * (n_tokens - 5)
+    assert slot[inner].tolist() == [8 * 16 + i for i in range(4, 9)] + [-1] * (n_tokens - 5)
+    for t in (pos, slot):
+        assert (t[:guard] == -9).all() and (t[guard + n_tokens:] == -9).all()
+    assert int(view.free_count) == 8 and view.page_table[0].tolist() == [8, -1, -1, -1]
