@@ -38,8 +38,8 @@
 // against 1,700 and 2,450 measured; the products themselves take 512 and 1,024.  Beside the
 // tiles a unit costs three to five tiles' time: its first maxima, the drain of O, code that
 // is fetched anew.  Measured: 32 blocks of 16 rows over 512 to 16,384 keys (32 + 8 heads of
-// 128 dims) 119 us, 2.7 TB/s of cells and 595 TFLOP/s; 4 blocks at 32,768 keys, 64 heads,
-// 86 us, 800 TFLOP/s; prompt chunks of 257 to 1,024 rows 163 us, 715 TFLOP/s.
+// 128 dims) 118 us, 2.7 TB/s of cells and 600 TFLOP/s; 4 blocks at 32,768 keys, 64 heads,
+// 84 us, 820 TFLOP/s; prompt chunks of 257 to 1,024 rows 158 us, 740 TFLOP/s.
 // Tried and slower: two warpgroups that expand V at 128 columns (the registers of the
 // softmax), a second S buffer at 128 in place of those of K and V (201 us against 188 then),
 // one copy of the code that reads the scores (195 against 187: the loop costs more than the
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           move = bar_or(bar, 128, wait.dead || mx > kMoveLog2 + kLift);
         }
         if (move) {
-          if (bar_or(bar, 128, wait.dead)) goto done;
+          if (i > 0 && bar_or(bar, 128, wait.dead)) goto done;
           // the columns' maxima over the tile (lane c: column c), and new running maxima
           float mine = -INFINITY;
 #pragma unroll 1
@@ -770,14 +770,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         tmem_ld_wait();
         if (r >= D) continue;
         if (whole) {                       // (O is 0 where the sum is)
+          // lanes r and r + 8 hold dims d and d + 1: of two columns each takes one, both dims
+          const int odd = r >> 3 & 1;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const uint32_t y = pack_bf16(__uint_as_float(v[e]) * fac[c0 + e],
-                                         __uint_as_float(v[e + 1]) * fac[c0 + e + 1]);
-            if (c0 + e < rows)
-              p.out[static_cast<size_t>(row[c0 + e]) * D + d] = static_cast<uint16_t>(y);
-            if (c0 + e + 1 < rows)
-              p.out[static_cast<size_t>(row[c0 + e + 1]) * D + d] = static_cast<uint16_t>(y >> 16);
+            const float a = __uint_as_float(v[e]), b = __uint_as_float(v[e + 1]);
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+            const float f = fac[c0 + e + odd];
+            const uint32_t y = pack_bf16((odd ? got : a) * f, (odd ? b : got) * f);
+            if (c0 + e + odd < rows)
+              *reinterpret_cast<uint32_t*>(p.out + static_cast<size_t>(row[c0 + e + odd]) * D +
+                                           (d & ~1)) = y;
           }
         } else {
           float* po = p.part_o + (static_cast<size_t>(slot) * NQ + col0 + c0) * D + d;
@@ -986,9 +989,9 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.tile_rows = a.nq / p.group;
   p.group_inv = (65536 + p.group - 1) / p.group;
   // Measured in tiles: with 2, 3, 4, 5, 6 of them prompt chunks (128 columns) took 261, 201,
-  // 186, 168, 171 us and a prompt of 4096 rows 325, 277, 229, 208, 209; with 2, 3, 4 four
-  // blocks at 32K (64 columns) 90, 89, 88 us and blocks at batch 32 123, 120, 121, and single
-  // rows (the kernel for few rows) 88, 87, 84.
+  // 186, 168, 171 us and a prompt of 4096 rows 325, 277, 229, 208, 209 (with 4 and 5 and today's
+  // drain of O 174, 158 and 212, 193); with 2, 3, 4 four blocks at 32K (64 columns) 90, 89, 88
+  // us and blocks at batch 32 123, 120, 121, and single rows (the kernel for few rows) 88, 87, 84.
   p.unit_cost = a.nq == 128 ? 5 : a.nq == 16 ? 4 : 3;
   p.paged = cache->kv.page_table != nullptr;
   p.page_size = cache->kv.page_size;
