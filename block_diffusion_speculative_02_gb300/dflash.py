@@ -213,8 +213,18 @@ def dflash_cycle_sm_split(dims: Dims):
     return int(v.value), int(p.value)
 
 
+class _View:
+    """A view's fields, and the C structs that _view_struct keeps on it: these hold addresses, so
+    they stay out of copies and pickles."""
+
+    _KEPT = ("_struct", "_pages")
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in self._KEPT}
+
+
 @dataclass
-class KVView:
+class KVView(_View):
     """A KV cache held in torch tensors (see dflash_kv_view in include/dflash.h)."""
     k: Optional[torch.Tensor]
     v: Optional[torch.Tensor]
@@ -460,7 +470,7 @@ def make_kv4_dims(batch, n_tokens, max_tokens, n_q_heads, n_kv_heads, head_dim) 
 
 
 @dataclass
-class KV4View:
+class KV4View(_View):
     """A KV cache in 4-bit cells (see dflash_kv4_view in include/dflash.h).
 
     ``cells``: uint8 [n_pages, Hkv, page_size / 16, 18 D] (paged) or

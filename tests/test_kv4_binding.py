@@ -1,0 +1,53 @@
+"""The binding of the calls over a 4-bit cache on the host: what a view keeps between calls, and
+what it refuses.  (CPU tensors are on "device" -1.)"""
+import copy
+import pickle
+
+import pytest
+import torch
+
+HOST = -1
+
+
+def _dflash():
+    from block_diffusion_speculative_02_gb300 import dflash
+    return dflash
+
+
+def _i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def _view4(pages=9, batch=2, hkv=2, d=64):
+    dflash = _dflash()
+    return dflash.KV4View(dflash.alloc_kv4_cells(pages, hkv, 16, d, device="cpu"), _i32(batch), 64,
+                          _i32(batch, 4), _i32(pages), _i32(1), 16, _i32(hkv), _i32(hkv))
+
+
+def _view16(pages=9, batch=2):
+    dflash = _dflash()
+    return dflash.KVView(None, None, _i32(batch), 64, _i32(batch, 4), _i32(pages), _i32(1), 16)
+
+
+def _use(view):
+    """What a call over the cells, or the page reservation, makes of a view."""
+    dflash = _dflash()
+    if isinstance(view, dflash.KV4View):
+        dflash._view_struct(view, HOST, 2, 0, 0)
+        return dflash._view_struct(view, HOST, 2, 2, 64)
+    return dflash._view_struct(view, HOST, 2, 0, 0)
+
+
+@pytest.mark.parametrize("make", [_view4, _view16])
+@pytest.mark.parametrize("clone", [copy.deepcopy, copy.copy,
+                                   lambda v: pickle.loads(pickle.dumps(v))])
+def test_used_views_copy_and_pickle(make, clone):
+    view = make()
+    _use(view)
+    other = clone(view)
+    assert type(other) is type(view) and other.capacity == view.capacity
+    assert torch.equal(other.page_table, view.page_table)
+    c = _use(other)
+    pages = c.kv if hasattr(c, "kv") else c
+    assert pages.page_table == other.page_table.data_ptr()
+    assert pages.seq_len == other.seq_len.data_ptr()
