@@ -9,8 +9,8 @@ module refuses to load when the library has not been built.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
+import weakref
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -550,21 +550,24 @@ def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
     return t.data_ptr(), st[0] if rows > 1 else max(st[0], heads * d)
 
 
-_VIEW_TENSORS = ("seq_len", "page_table", "free_list", "free_count", "cells", "k_exp", "v_exp")
+_PAGE_TENSORS = ("seq_len", "page_table", "free_list", "free_count")
+_VIEW_TENSORS = _PAGE_TENSORS + ("cells", "k_exp", "v_exp")
 
 
 def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     """The C struct of a view (with hkv 0: of its lengths and pages only), checked.
 
     The struct is kept on the view for the next call, and used again as long as the view holds
-    the same tensors, at the same addresses and of the same shapes, and the same sizes."""
+    the same tensors, at the same addresses and of the same shapes, and the same sizes.  It holds
+    none of them alive."""
     get = v.__dict__.get
-    tensors = tuple([get(f) for f in _VIEW_TENSORS])
+    tensors = [get(f) for f in (_VIEW_TENSORS if hkv else _PAGE_TENSORS)]
     key = (device, batch, hkv, d, v.capacity, v.page_size,
            *[0 if t is None else (t.data_ptr(), t.shape) for t in tensors])
     slot = "_struct" if hkv else "_pages"
     memo = get(slot)
-    if memo is not None and memo[0] == key and all(map(operator.is_, memo[1], tensors)):
+    if memo is not None and memo[0] == key and \
+            all([r is t if t is None else r() is t for r, t in zip(memo[1], tensors)]):
         return memo[2]
     i32 = torch.int32
     seq = _on(v.seq_len, device, i32, batch, "seq_len")
@@ -586,7 +589,7 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     if hkv:
         c = KV4ViewC(c, _opt(v.k_exp, device, i32, hkv, "k_exp"),
                      _opt(v.v_exp, device, i32, hkv, "v_exp"))
-    v.__dict__[slot] = (key, tensors, c)
+    v.__dict__[slot] = (key, [t if t is None else weakref.ref(t) for t in tensors], c)
     return c
 
 

@@ -2,6 +2,7 @@
 what it refuses.  (CPU tensors are on "device" -1.)"""
 import copy
 import pickle
+import weakref
 
 import pytest
 import torch
@@ -51,3 +52,38 @@ def test_used_views_copy_and_pickle(make, clone):
     pages = c.kv if hasattr(c, "kv") else c
     assert pages.page_table == other.page_table.data_ptr()
     assert pages.seq_len == other.seq_len.data_ptr()
+
+
+@pytest.mark.parametrize("field", ["cells", "page_table", "free_list", "k_exp"])
+def test_exchanged_tensors_are_let_go(field):
+    """A tensor that leaves a view is freed then, not at the view's next call."""
+    view = _view4()
+    _use(view)
+    old = weakref.ref(getattr(view, field))
+    setattr(view, field, getattr(view, field).clone())
+    assert old() is None
+    c = _use(view)
+    here = {"cells": c.kv.k, "page_table": c.kv.page_table, "free_list": c.kv.free_list,
+            "k_exp": c.k_exp}
+    assert here[field] == getattr(view, field).data_ptr()
+    old = weakref.ref(view.cells)
+    view.cells = None
+    assert old() is None
+
+
+def test_page_struct_is_kept_whatever_the_cells_are():
+    """The reservation's struct does not depend on the cells: exchanging them leaves it valid."""
+    dflash = _dflash()
+    view = _view4()
+    c = dflash._view_struct(view, HOST, 2, 0, 0)
+    view.cells = None
+    assert dflash._view_struct(view, HOST, 2, 0, 0) is c
+
+
+def test_another_tensor_at_the_same_address_is_checked():
+    """The kept struct belongs to the tensors it was made of, not to their addresses."""
+    view = _view4()
+    _use(view)
+    view.k_exp = view.k_exp.view(torch.float32)
+    with pytest.raises(ValueError):
+        _use(view)
