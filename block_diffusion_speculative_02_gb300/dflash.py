@@ -558,12 +558,12 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     """The C struct of a view (with hkv 0: of its lengths and pages only), checked.
 
     The struct is kept on the view for the next call, and used again as long as the view holds
-    the same tensors, at the same addresses and of the same shapes, and the same sizes.  It holds
-    none of them alive."""
+    the same tensors, at the same addresses and of the same shapes, contiguous still, and the same
+    sizes.  It holds none of them alive."""
     get = v.__dict__.get
     tensors = [get(f) for f in (_VIEW_TENSORS if hkv else _PAGE_TENSORS)]
     key = (device, batch, hkv, d, v.capacity, v.page_size,
-           *[0 if t is None else (t.data_ptr(), t.shape) for t in tensors])
+           *[0 if t is None else (t.data_ptr(), t.shape, t.is_contiguous()) for t in tensors])
     slot = "_struct" if hkv else "_pages"
     memo = get(slot)
     if memo is not None and memo[0] == key and \

@@ -87,3 +87,14 @@ def test_another_tensor_at_the_same_address_is_checked():
     view.k_exp = view.k_exp.view(torch.float32)
     with pytest.raises(ValueError):
         _use(view)
+
+
+def test_a_tensor_turned_in_place_is_refused():
+    """A table transposed in place keeps its address and, if square, its shape."""
+    view = _view4(batch=4)
+    dflash = _dflash()
+    use = lambda: dflash._view_struct(view, HOST, 4, 2, 64)  # noqa: E731
+    use()
+    view.page_table.t_()
+    with pytest.raises(ValueError, match="page_table"):
+        use()
