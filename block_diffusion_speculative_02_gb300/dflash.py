@@ -474,7 +474,8 @@ class KV4View(_View):
     """A KV cache in 4-bit cells (see dflash_kv4_view in include/dflash.h).
 
     ``cells``: uint8 [n_pages, Hkv, page_size / 16, 18 D] (paged) or
-    [B, Hkv, capacity / 16, 18 D].  ``pages()`` is the view that
+    [B, Hkv, capacity / 16, 18 D].  A paged view has its ``free_list`` in every
+    call: its length is n_pages.  ``pages()`` is the view that
     dflash_kv_reserve and dflash_kv_crop take."""
     cells: torch.Tensor
     seq_len: torch.Tensor                      # int32 [B]
@@ -521,8 +522,8 @@ def _bad(t, device: int, dtype, numel, name: str):
 
 def _on(t, device: int, dtype, numel: int, name: str) -> int:
     """Pointer of a contiguous tensor on this device with this type and size."""
-    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() \
-            or t.numel() != numel:
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != device \
+            or not t.is_contiguous() or t.numel() != numel:
         _bad(t, device, dtype, numel, name)
     return t.data_ptr()
 
@@ -533,14 +534,15 @@ def _opt(t, device: int, dtype, numel: int, name: str) -> Optional[int]:
 
 def _ws_on(ws, device: int):
     """(pointer, bytes) of a workspace."""
-    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+    if getattr(ws, "dtype", None) is not torch.uint8 or ws.get_device() != device \
+            or not ws.is_contiguous():
         _bad(ws, device, torch.uint8, None, "ws")
     return ws.data_ptr(), ws.numel()
 
 
 def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
     """(pointer, row pitch) of a bf16 [rows, heads, D] tensor whose rows are contiguous."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+    if getattr(t, "dtype", None) is not torch.bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be a bf16 tensor on cuda:{device}")
     if t.shape != (rows, heads, d):
         raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
@@ -562,8 +564,11 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     sizes.  It holds none of them alive."""
     get = v.__dict__.get
     tensors = [get(f) for f in (_VIEW_TENSORS if hkv else _PAGE_TENSORS)]
-    key = (device, batch, hkv, d, v.capacity, v.page_size,
-           *[0 if t is None else (t.data_ptr(), t.shape, t.is_contiguous()) for t in tensors])
+    try:
+        key = (device, batch, hkv, d, v.capacity, v.page_size,
+               *[0 if t is None else (t.data_ptr(), t.shape, t.is_contiguous()) for t in tensors])
+    except AttributeError:                    # not a tensor: the checks below say which
+        key = None
     slot = "_struct" if hkv else "_pages"
     memo = get(slot)
     if memo is not None and memo[0] == key and \
@@ -573,8 +578,10 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     seq = _on(v.seq_len, device, i32, batch, "seq_len")
     table, n, k = v.page_table, 0, None
     if table is not None:
-        if table.dim() != 2 or table.shape[0] != batch:
-            raise ValueError(f"page_table must be [{batch}, max_pages]")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[0] != batch:
+            raise ValueError(f"page_table must be an int32 tensor [{batch}, max_pages]")
+        if not isinstance(v.free_list, torch.Tensor):
+            raise ValueError("free_list must be a tensor: its length is the pool's number of pages")
         n = v.free_list.numel()
     if hkv:
         rows, slabs = (v.page_size, n) if table is not None else (v.capacity, batch)

@@ -98,3 +98,27 @@ def test_a_tensor_turned_in_place_is_refused():
     view.page_table.t_()
     with pytest.raises(ValueError, match="page_table"):
         use()
+
+
+@pytest.mark.parametrize("field", ["cells", "seq_len", "free_list", "free_count"])
+def test_a_view_without_a_tensor_is_a_value_error(field):
+    view = _view4()
+    setattr(view, field, None)
+    with pytest.raises(ValueError, match=field):
+        _use(view)
+
+
+def test_a_missing_or_foreign_argument_is_a_value_error():
+    dflash = _dflash()
+    for bad in (None, [0, 0], 7):
+        with pytest.raises(ValueError, match="start"):
+            dflash._on(bad, HOST, torch.int32, 2, "start")
+        with pytest.raises(ValueError, match="ws"):
+            dflash._ws_on(bad, HOST)
+        with pytest.raises(ValueError, match="q must"):
+            dflash._rows_on(bad, HOST, 2, 1, 64, "q")
+    assert dflash._opt(None, HOST, torch.int32, 2, "k_exp") is None
+    view = _view4()
+    view.page_table = [[0] * 4] * 2
+    with pytest.raises(ValueError, match="page_table"):
+        _use(view)
