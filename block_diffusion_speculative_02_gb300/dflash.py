@@ -549,7 +549,7 @@ def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
     st = t.stride()
     if st[2] != 1 or (st[1] != d and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), st[0] if rows > 1 else max(st[0], heads * d)
+    return t.data_ptr(), st[0] if rows > 1 else heads * d
 
 
 _PAGE_TENSORS = ("seq_len", "page_table", "free_list", "free_count")

@@ -122,3 +122,14 @@ def test_a_missing_or_foreign_argument_is_a_value_error():
     view.page_table = [[0] * 4] * 2
     with pytest.raises(ValueError, match="page_table"):
         _use(view)
+
+
+def test_a_single_row_has_any_pitch():
+    """The stride of an axis of one row says nothing: slices of one odd row are taken."""
+    dflash = _dflash()
+    for width in (8 * 64 + 3, 1000):
+        row = torch.zeros(1, width, dtype=torch.bfloat16)
+        heads = row[:, 64:64 + 2 * 64].unflatten(1, (2, 64))
+        assert dflash._rows_on(heads, HOST, 1, 2, 64, "q")[1] % 8 == 0
+    two = torch.zeros(2, 515, dtype=torch.bfloat16)[:, :128].unflatten(1, (2, 64))
+    assert dflash._rows_on(two, HOST, 2, 2, 64, "q")[1] == 515
