@@ -128,8 +128,9 @@ def test_a_single_row_has_any_pitch():
     """The stride of an axis of one row says nothing: slices of one odd row are taken."""
     dflash = _dflash()
     for width in (8 * 64 + 3, 1000):
-        row = torch.zeros(1, width, dtype=torch.bfloat16)
-        heads = row[:, 64:64 + 2 * 64].unflatten(1, (2, 64))
+        rows = torch.zeros(3, width, dtype=torch.bfloat16)
+        heads = rows[:, 64:64 + 2 * 64].unflatten(1, (2, 64))[1:2]
+        assert heads.stride(0) == width
         assert dflash._rows_on(heads, HOST, 1, 2, 64, "q")[1] % 8 == 0
     two = torch.zeros(2, 515, dtype=torch.bfloat16)[:, :128].unflatten(1, (2, 64))
     assert dflash._rows_on(two, HOST, 2, 2, 64, "q")[1] == 515
