@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "host.h"
+#include "kv4_attention.cuh"
 #include "streamk_gemm.cuh"
 
 namespace dflash {
@@ -52,20 +53,42 @@ int injected_failure(const char* entry) {
 
 namespace {
 
-// One warp waits on an mbarrier with the same bounded wait every kernel uses.
-// With arrive == 0 nothing ever arrives: the wait gives up after its time
-// limit and records DFLASH_ST_TIMEOUT, and the kernel returns normally.
+// A warp each waits on an mbarrier of its own with the bounded waits that the kernels use: the
+// one of common.cuh and both forms of the 4-bit attention's.  With arrive == 0 nothing ever
+// arrives: each gives up after its time limit, and the kernel returns normally.  The status
+// word gets DFLASH_ST_TIMEOUT if one of them gave up although its arrival came, or if all did
+// without one, none of them before 0.9 of the limit.
 __global__ void selftest_wait_kernel(int arrive, uint32_t* status) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar[3];
+  __shared__ uint32_t gave_up[3], early;
   __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&bar, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&bar[i], 1);
+      gave_up[i] = 0;
+    }
     abort_flag = 0;
+    early = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0 && arrive) mbar_arrive(&bar);
-  if (threadIdx.x == 0) mbar_wait(&bar, 0, &abort_flag, status);
+  if (arrive && lane == 0) mbar_arrive(&bar[warp]);
+  const uint64_t t0 = globaltimer_ns();
+  if (warp == 0) {
+    if (lane == 0) mbar_wait(&bar[0], 0, &abort_flag, &gave_up[0]);
+  } else if (warp == 1) {
+    kv4::wait_on<false>(&bar[1], 0, &gave_up[1]);
+  } else {
+    kv4::wait_on<true>(&bar[2], 0, &gave_up[2]);
+  }
+  if (lane == 0 && globaltimer_ns() - t0 < kWaitLimitNs / 10 * 9) early = 1;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t any = gave_up[0] | gave_up[1] | gave_up[2];
+    const uint32_t all = gave_up[0] & gave_up[1] & gave_up[2];
+    set_status(status, arrive ? any : early ? 0 : all);
+  }
 }
 
 }  // namespace
@@ -253,7 +276,7 @@ extern "C" int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes,
                                     dflash_stream_t stream) {
   DFLASH_ENTRY("dflash_selftest_wait");
   if (!ws || ws_bytes < 64) return DFLASH_E_WORKSPACE;
-  selftest_wait_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  selftest_wait_kernel<<<1, 96, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       arrive, static_cast<uint32_t*>(ws));
   return cuda_err(cudaGetLastError());
 }

@@ -325,18 +325,23 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// The bounded wait of these kernels.  A try by a whole warp sleeps up to 4 us (measured), so
-// 2^18 of them are a second; the loop is small, because five roles share the instruction
-// cache, and a call would rule out the register split.
+// The bounded wait of these kernels: it gives up once kWaitLimitNs have passed by the clock, read
+// after every four tries or nap.  A try by a whole warp sleeps up to 4 us (measured), so a wait that
+// is over soon never reads it.  The loop is small and holds one register, because five roles
+// share the instruction cache and the softmax has none to spare (with a counter of tries
+// beside the clock it spilled 300 bytes at 128 columns); a call would rule out the register split.
 template <bool kNap = false>
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  static_assert(kWaitLimitNs < 1ull << 32, "the low word of the clock");
 #define DFLASH_TRY "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra done;\n\t"
-#define DFLASH_LOOP(body)                                                           \
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 65536;\n\tagain:\n\t" body \
-               "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra again;\n\tdone:\n\t"     \
-               "selp.u32 %0, 1, 0, p;\n\t}\n"                                        \
-               : "=r"(ok)                                                           \
-               : "r"(smem_u32(bar)), "r"(parity)                                    \
+// (t0: the low word of the clock at the first reading, 0 before it)
+#define DFLASH_LOOP(body)                                                              \
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .u32 t, t0;\n\tmov.u32 t0, 0;\n\tagain:\n\t" body \
+               "mov.u32 t, %%globaltimer_lo;\n\tsetp.eq.u32 q, t0, 0;\n\t"            \
+               "@q mov.u32 t0, t;\n\tsub.u32 t, t, t0;\n\tsetp.lt.u32 q, t, %3;\n\t"  \
+               "@q bra again;\n\tdone:\n\tselp.u32 %0, 1, 0, p;\n\t}\n"             \
+               : "=r"(ok)                                                              \
+               : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitLimitNs)                    \
                : "memory")
   uint32_t ok;
   __syncwarp();  // (a warp that is not together does not sleep in a try)

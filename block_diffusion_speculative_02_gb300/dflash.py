@@ -279,7 +279,7 @@ def dflash_ctx_project(dims: Dims, layer_hidden: Sequence[torch.Tensor], w_fc, h
 
 
 def dflash_selftest_wait(arrive: bool, ws, stream=None):
-    """One bounded wait: completed at once (arrive) or timed out after ~1 s (status bit)."""
+    """The bounded waits: completed at once (arrive) or timed out after ~1 s (status bit)."""
     _check(load_library().dflash_selftest_wait(1 if arrive else 0, _dev(ws, name="ws"),
                                                ws.numel(), _stream(stream)),
            "dflash_selftest_wait")

@@ -581,11 +581,11 @@ DFLASH_API int dflash_read_status(void* ws, uint32_t* host_status, int clear, df
 DFLASH_API const char* dflash_status_string(int code);
 
 /*
- * Self-test of the bounded wait every kernel uses: one warp waits on an
- * mbarrier; with arrive != 0 one arrival completes it at once, with
- * arrive == 0 nothing arrives and the wait gives up after its time limit
- * (about a second), records DFLASH_ST_TIMEOUT in the status word of `ws`
- * and the kernel returns; the context stays usable.  ws: at least 64 bytes.
+ * Self-test of the bounded waits that the kernels use: a warp each waits on an
+ * mbarrier; with arrive != 0 one arrival completes it at once, with arrive == 0
+ * nothing arrives and every wait gives up after its time limit (about a second),
+ * the kernel records DFLASH_ST_TIMEOUT in the status word of `ws` (not if one of
+ * them gave up before) and returns; the context stays usable.  ws: at least 64 bytes.
  */
 DFLASH_API int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes, dflash_stream_t stream);
 
