@@ -9,8 +9,8 @@ module refuses to load when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
-import weakref
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -215,12 +215,23 @@ def dflash_cycle_sm_split(dims: Dims):
 
 class _View:
     """A view's fields, and the C structs that _view_struct keeps on it: these hold addresses, so
-    they stay out of copies and pickles."""
+    they stay out of copies and pickles, and go when a field that they are made of is set."""
 
     _KEPT = ("_struct", "_pages")
 
     def __getstate__(self):
         return {k: v for k, v in self.__dict__.items() if k not in self._KEPT}
+
+    def __setattr__(self, name, value):
+        d = self.__dict__
+        d.pop("_struct", None)
+        if name not in ("cells", "k_exp", "v_exp"):
+            d.pop("_pages", None)
+        d[name] = value
+
+    def __delattr__(self, name):
+        setattr(self, name, None)
+        del self.__dict__[name]
 
 
 @dataclass
@@ -552,28 +563,27 @@ def _rows_on(t, device: int, rows: int, heads: int, d: int, name: str):
     return t.data_ptr(), st[0] if rows > 1 else heads * d
 
 
-_PAGE_TENSORS = ("seq_len", "page_table", "free_list", "free_count")
-_VIEW_TENSORS = _PAGE_TENSORS + ("cells", "k_exp", "v_exp")
+_PAGE_TENSORS = operator.attrgetter("seq_len", "page_table", "free_list", "free_count")
+_VIEW_TENSORS = operator.attrgetter("seq_len", "page_table", "free_list", "free_count", "cells",
+                                    "k_exp", "v_exp")
 
 
 def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     """The C struct of a view (with hkv 0: of its lengths and pages only), checked.
 
-    The struct is kept on the view for the next call, and used again as long as the view holds
-    the same tensors, at the same addresses and of the same shapes, contiguous still, and the same
-    sizes.  It holds none of them alive."""
-    get = v.__dict__.get
-    tensors = [get(f) for f in (_VIEW_TENSORS if hkv else _PAGE_TENSORS)]
+    The struct is kept on the view until one of its fields is set, and used again as long as the
+    tensors lie where they did, have the shapes they had, and are contiguous still.  It holds
+    none of them alive."""
+    tensors = (_VIEW_TENSORS if hkv else _PAGE_TENSORS)(v)
     try:
-        key = (device, batch, hkv, d, v.capacity, v.page_size,
-               *[0 if t is None else (t.data_ptr(), t.shape, t.is_contiguous()) for t in tensors])
+        key = [device, batch, hkv, d,
+               *[t if t is None else (t.data_ptr(), t.shape, t.is_contiguous()) for t in tensors]]
     except AttributeError:                    # not a tensor: the checks below say which
         key = None
     slot = "_struct" if hkv else "_pages"
-    memo = get(slot)
-    if memo is not None and memo[0] == key and \
-            all([r is t if t is None else r() is t for r, t in zip(memo[1], tensors)]):
-        return memo[2]
+    memo = v.__dict__.get(slot)
+    if memo is not None and memo[0] == key:
+        return memo[1]
     i32 = torch.int32
     seq = _on(v.seq_len, device, i32, batch, "seq_len")
     table, n, k = v.page_table, 0, None
@@ -596,7 +606,7 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     if hkv:
         c = KV4ViewC(c, _opt(v.k_exp, device, i32, hkv, "k_exp"),
                      _opt(v.v_exp, device, i32, hkv, "v_exp"))
-    v.__dict__[slot] = (key, [t if t is None else weakref.ref(t) for t in tensors], c)
+    v.__dict__[slot] = (key, c)
     return c
 
 
