@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           for (int o = lane * 16; o < C::kStage; o += 512)
             if (miss >> (l0 + o / C::kCell) & 1)
               *reinterpret_cast<uint4*>(dst + o) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();        // (before the copies that come here next)
           __syncwarp();
         }
         if (at == 0) {

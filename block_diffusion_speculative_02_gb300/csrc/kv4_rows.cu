@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
         for (int o = lane * 16; o < C::kCell; o += 512)
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + o), "r"(0)
                        : "memory");
+        fence_proxy_async_smem();                   // (before the copy that comes here next)
         warp_arrive(&mine[st]);
       } else if (lane == 0) {
         mbar_arrive_expect_tx(&mine[st], C::kCell);

@@ -845,3 +845,36 @@ def test_reserve_counts_past_int32(n_tokens):
     for t in (pos, slot):
         assert (t[:guard] == -9).all() and (t[guard + n_tokens:] == -9).all()
     assert int(view.free_count) == 8 and view.page_table[0].tolist() == [8, -1, -1, -1]
+
+
+@pytest.mark.parametrize("T,group", [(1, 4), (3, 4), (8, 4), (16, 4), (32, 4)])
+@pytest.mark.parametrize("page", [16, 48])
+def test_attention_missing_pages_among_copies(T, group, page):
+    """Missing pages throughout long contexts: the zeros that stand for them lie where copies
+    landed before and land again after, at every width of a unit."""
+    dfl = _dfl()
+    rng = np.random.default_rng(T + page)
+    lens = [6000, 900]
+    cache = Cache(rng, lens, 1, 128, page_size=page)
+    for b, n in enumerate(lens):
+        gone = rng.random(-(-n // page)) < 0.3
+        gone[-1] = False
+        for i in np.nonzero(gone)[0]:
+            cache.view.page_table[b, i] = -1 if i % 2 else 10 ** 6
+            cache.k[b][page * i:page * (i + 1)] = cache.v[b][page * i:page * (i + 1)] = 0
+    dims = dfl.make_kv4_dims(2, 2 * T, T, group, 1, 128)
+    ws = dfl.alloc_kv4_workspace(dims)
+    q = bf16(rng.normal(size=(2 * T, group, 128)) * np.ldexp(1.0, -cache.k_exp[0]))
+    scale, outs = 128 ** -0.5, []
+    for _ in range(3):
+        out = torch.zeros_like(q)
+        dfl.dflash_kv4_attention(dims, q, i32([0, T, 2 * T]), cache.view, scale, True, out, ws)
+        assert status(ws) == bits("page_missing")
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    got = f64(outs[0])
+    for b, L in enumerate(lens):
+        rows = slice(b * T, b * T + T)
+        ref, avg, e = O.attention(f64(q)[rows], cache.k[b], cache.v[b],
+                                  [L - T + t + 1 for t in range(T)], scale)
+        assert (np.abs(got[rows] - ref) <= bound(ref, avg, e, cache.v[b])).all(), b
