@@ -878,3 +878,89 @@ def test_attention_missing_pages_among_copies(T, group, page):
         ref, avg, e = O.attention(f64(q)[rows], cache.k[b], cache.v[b],
                                   [L - T + t + 1 for t in range(T)], scale)
         assert (np.abs(got[rows] - ref) <= bound(ref, avg, e, cache.v[b])).all(), b
+
+
+# one launch (at most 256 sequences and 8192 rows), and the two launches of larger batches
+TWO_LAUNCHES = [0, 8300]
+
+
+def _grown(lens, new, table, batch):
+    """The same sequences, with sequences of length 0 without new rows behind them."""
+    more = batch - len(lens)
+    return (list(lens) + [0] * more, list(new) + [0] * more,
+            np.concatenate([table, np.full((more, table.shape[1]), -1)]))
+
+
+@pytest.mark.parametrize("pad", TWO_LAUNCHES)
+@pytest.mark.parametrize("batch", [6, 300])
+@pytest.mark.parametrize("count", [0, 1, 2, 3, 5, 6])
+def test_reserve_short_pool_both_ways(count, batch, pad):
+    lens, new = [3, 0, 16, 40, 15, 8], [4, 33, 20, 8, 2, 0]
+    table = np.full((6, 5), -1)
+    table[0, 0], table[2, 0], table[3, :3], table[4, 0], table[5, 0] = 20, 21, (22, 23, 24), 25, 26
+    lens, new, table = _grown(lens, new, table, batch)
+    for alias in (False, True):
+        ref = run_reserve(lens, new, table, np.arange(30), count, 16, 67 + pad, 64, 80, alias=alias)
+        assert ("pool_empty" in ref["status"]) == (count < 6)
+
+
+@pytest.mark.parametrize("pad", TWO_LAUNCHES)
+@pytest.mark.parametrize("batch", [7, 300])
+def test_reserve_refuses_bad_sequences_both_ways(batch, pad):
+    lens, new = [0, -1, 70, 5, 81, 0, 10], [2, 3, 11, -4, 1, 17, 6]
+    lens, new, table = _grown(lens, new, np.full((7, 5), -1), batch)
+    for alias in (False, True):
+        ref = run_reserve(lens, new, table, np.arange(40), 40, 16, 36 + pad, 16, 80, alias=alias)
+        # (the last one's rows fit the array once it is padded)
+        assert ref["new_len"][:7].tolist() == [2, -1, 70, 5, 81, 0, 16 if pad else 10]
+
+
+@pytest.mark.parametrize("pad", TWO_LAUNCHES)
+@pytest.mark.parametrize("batch", [3, 300])
+def test_reserve_contiguous_both_ways(batch, pad):
+    lens, new, _ = _grown([0, 7, 30], [4, 16, 2], np.full((3, 1), -1), batch)
+    for alias in (False, True):
+        run_reserve(lens, new, None, [], 0, 0, 24 + pad, 16, 32, alias=alias)
+
+
+@pytest.mark.parametrize("pad", TWO_LAUNCHES)
+def test_reserve_again_both_ways(pad):
+    """A second call with the same lengths changes nothing; one in place goes on from there."""
+    dfl = _dfl()
+    n = 20 + pad
+    dims = dfl.make_kv4_dims(2, n, 16, 1, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    view = dfl.KVView(None, None, i32([0, 3]), 64, i32(np.full((2, 4), -1)), i32(np.arange(9)),
+                      i32([9]), 16)
+    got = []
+    for _ in range(2):
+        o = [torch.zeros(m, dtype=I32, device="cuda") for m in (3, n, n, 2)]
+        dfl.dflash_kv_reserve(dims, view, i32([4, 16]), *o, ws)
+        got.append([x.tolist() for x in o] + [view.page_table.tolist(), int(view.free_count)])
+    assert got[0] == got[1]
+    for lens in ([4, 19], [8, 35], [12, 51]):
+        o = [torch.zeros(m, dtype=I32, device="cuda") for m in (3, n, n)]
+        dfl.dflash_kv_reserve(dims, view, i32([4, 16]), *o, view.seq_len, ws)
+        assert view.seq_len.tolist() == lens
+        assert o[1][:4].tolist() == list(range(lens[0] - 4, lens[0]))
+    assert status(ws) == 0
+
+
+@pytest.mark.parametrize("B,pad", [(20, 8300), (280, 0)])
+def test_reserve_random_two_launches(B, pad):
+    """Random lengths, counts (bad ones among them), tables and pools, some of them too small."""
+    rng = np.random.default_rng(B)
+    for _ in range(8):
+        lens = rng.integers(0, 90, B)
+        new = rng.integers(0, 40, B)
+        new[rng.random(B) < 0.1] = -3
+        lens[rng.random(B) < 0.05] = -2
+        table, at = np.full((B, 7), -1), 0
+        order = rng.permutation(10 * B)
+        for b in range(B):
+            per = -(-max(lens[b], 0) // 16)
+            table[b, :per] = order[at:at + per]
+            at += per
+        count = int(rng.integers(0, 3 * B))
+        run_reserve(lens, new, table, np.concatenate([order[at:], order[:at]]), count, 16,
+                    int(np.maximum(new, 0).sum()) + pad, 38, 112, alias=rng.random() < 0.5)
