@@ -565,8 +565,9 @@ DFLASH_API int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slo
  * or past the capacity sets DFLASH_ST_CAPACITY and its output is left unwritten;
  * unmapped pages inside the length set DFLASH_ST_PAGE_MISSING and read as zeros,
  * as do pages numbered past the pool.  Cells past the length are not used.
- * A batch with more than 2^31 - 1 tiles of 128 rows in all (with 4 to 6 more for
- * each unit of up to 128 query rows) sets DFLASH_ST_CAPACITY and writes nothing.
+ * A batch with more than 2^31 - 1 tiles of 128 rows in all (for every unit of up to 128
+ * query rows of one KV head, and 3 to 5 more each) sets DFLASH_ST_CAPACITY and writes
+ * nothing.
  */
 DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
                                     const int32_t* start, const dflash_kv4_view* cache,

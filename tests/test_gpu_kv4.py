@@ -964,3 +964,29 @@ def test_reserve_random_two_launches(B, pad):
         count = int(rng.integers(0, 3 * B))
         run_reserve(lens, new, table, np.concatenate([order[at:], order[:at]]), count, 16,
                     int(np.maximum(new, 0).sum()) + pad, 38, 112, alias=rng.random() < 0.5)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("T", [1, 6, 16, 40])
+def test_attention_refuses_more_tiles_than_int32(T, causal):
+    """64 sequences of 2^29 rows and 8 KV heads: 2^31 tiles and more.  Nothing is written;
+    with short lengths the next call over the same workspace is right."""
+    dfl = _dfl()
+    rng = np.random.default_rng(T)
+    B, hkv, d, page = 64, 8, 64, 2 ** 16
+    cells = dfl.alloc_kv4_cells(1, hkv, page, d)
+    table = torch.full((B, 2 ** 13), -1, dtype=I32, device="cuda")
+    view = dfl.KV4View(cells, i32([2 ** 29] * B), 2 ** 29, table, i32([0]), i32([0]), page)
+    dims = dfl.make_kv4_dims(B, B * T, T, 4 * hkv, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    q = bf16(rng.normal(size=(B * T, 4 * hkv, d)))
+    out = torch.full_like(q, 5.0)
+    start = i32(np.arange(B + 1) * T)
+    dfl.dflash_kv4_attention(dims, q, start, view, 0.1, causal, out, ws)
+    assert status(ws) == bits("capacity")
+    assert (f64(out) == 5).all()
+    view.seq_len.fill_(T)
+    table[:, 0] = 0
+    dfl.dflash_kv4_attention(dims, q, start, view, 0.1, causal, out, ws)
+    assert status(ws) == 0
+    assert (f64(out) == 0).all()                       # (cells of zeros)
