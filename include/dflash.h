@@ -494,7 +494,9 @@ DFLASH_API size_t dflash_kv4_workspace_bytes(const dflash_kv4_dims* dims);
  * pos and slot are -1 (start still counts its rows).  That is a sequence with
  * n_b < 0 (counted as 0 rows), L_b < 0, L_b + n_b past the capacity, n_b >
  * max_tokens or rows past n_tokens (DFLASH_ST_CAPACITY), or one that needs more
- * pages than the earlier ones leave (DFLASH_ST_POOL_EMPTY).
+ * pages than the earlier ones leave (DFLASH_ST_POOL_EMPTY).  Its rows stay in the batch:
+ * dflash_qk_norm_rope, dflash_kv4_append and dflash_kv4_gather skip them (pos and slot
+ * are -1), dflash_kv4_attention cannot (see there).
  * cache->k and cache->v may be NULL.
  */
 DFLASH_API int dflash_kv_reserve(const dflash_kv4_dims* dims, const dflash_kv_view* cache,
@@ -565,6 +567,11 @@ DFLASH_API int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slo
  * or past the capacity sets DFLASH_ST_CAPACITY and its output is left unwritten;
  * unmapped pages inside the length set DFLASH_ST_PAGE_MISSING and read as zeros,
  * as do pages numbered past the pool.  Cells past the length are not used.
+ * Only start and seq_len say which rows are new.  A sequence that dflash_kv_reserve did not
+ * serve kept its length, so its last T cached rows are taken for the new ones, and its
+ * output rows, finite or not, stand for nothing; those of the others, and the cache, are not
+ * touched by it.  The caller knows it by pos < 0 at its first row (or new_len = L_b with
+ * n_b > 0) and drops or repeats its rows.
  * A batch with more than 2^31 - 1 tiles of 128 rows in all (for every unit of up to 128
  * query rows of one KV head, and 3 to 5 more each) sets DFLASH_ST_CAPACITY and writes
  * nothing.

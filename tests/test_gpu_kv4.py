@@ -990,3 +990,70 @@ def test_attention_refuses_more_tiles_than_int32(T, causal):
     dfl.dflash_kv4_attention(dims, q, start, view, 0.1, causal, out, ws)
     assert status(ws) == 0
     assert (f64(out) == 0).all()                       # (cells of zeros)
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_step_with_a_sequence_that_was_not_served(T):
+    """The chain after a reservation that ran out of pages: the other sequences' outputs are
+    right, no cell of the one left out changes, its norms are skipped, and once it was served its
+    step comes out as if nothing had been."""
+    dfl = _dfl()
+    rng = np.random.default_rng(T)
+    hq, hkv, d = 4, 1, 64
+    cache = Cache(rng, [32, 16, 30], hkv, d, spare=0)
+    view = cache.view
+    wide = torch.full((3, 6), -1, dtype=I32, device="cuda")
+    wide[:, :view.page_table.shape[1]] = view.page_table
+    view.page_table = wide
+    lens = [32 - T, 16, 30 - T]                          # the first and last have their pages
+    view.seq_len.copy_(i32(lens))
+    view.free_count.zero_()
+    dims = dfl.make_kv4_dims(3, 3 * T, T, hq, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda") for m in (4, 3 * T, 3 * T))
+    q0, k0, v0 = (bf16(rng.normal(size=(3 * T, h, d))) for h in (hq, hkv, hkv))
+    before = view.cells.clone()
+
+    def step(q, k):
+        out = torch.full_like(q, 9.0)
+        dfl.dflash_kv_reserve(dims, view, i32([T] * 3), start, pos, slot, view.seq_len, ws)
+        st = status(ws)
+        dfl.dflash_qk_norm_rope(dims, q, k, None, None, pos, 1e6, 1e-6, q, k)
+        dfl.dflash_kv4_append(dims, k, v0, slot, view, ws)
+        dfl.dflash_kv4_attention(dims, q, start, view, 0.125, True, out, ws)
+        assert status(ws) == 0
+        return st, out
+
+    q, k = q0.clone(), k0.clone()
+    st, out = step(q, k)
+    assert st == bits("pool_empty")
+    assert view.seq_len.tolist() == [32, 16, 30] and pos[T] == -1 and slot[T] == -1
+    mid = slice(T, 2 * T)
+    assert torch.equal(q[mid], q0[mid]) and torch.equal(k[mid], k0[mid])
+    page = int(cache.table[1, 0])
+    assert torch.equal(view.cells[page], before[page])
+    kd, vd, qd, got = f64(k), f64(v0), f64(q), f64(out)
+
+    def check(b, rows, got, keep):
+        kk = np.concatenate([cache.k[b][:keep], O.values(*O.quantise(kd[rows], cache.k_exp),
+                                                         cache.k_exp)])
+        vv = np.concatenate([cache.v[b][:keep], O.values(*O.quantise(vd[rows], cache.v_exp),
+                                                         cache.v_exp)])
+        ref, avg, e = O.attention(qd[rows], kk, vv, [keep + t + 1 for t in range(T)], 0.125)
+        assert (np.abs(got[rows] - ref) <= bound(ref, avg, e, vv)).all(), b
+
+    for b in (0, 2):
+        check(b, slice(b * T, b * T + T), got, lens[b])
+    # a page comes free: the crop takes the step back, and all three are served
+    dfl.dflash_kv_crop([view.pages()], i32(lens), 3, ws)
+    new_page = torch.zeros(1, *view.cells.shape[1:], dtype=U8, device="cuda")
+    view.cells = torch.cat([view.cells, new_page])
+    view.free_list = torch.cat([view.free_list, i32([0])])
+    view.free_list[int(view.free_count)] = len(view.cells) - 1
+    view.free_count += 1
+    q, k = q0.clone(), k0.clone()
+    st, out = step(q, k)
+    assert st == 0 and view.seq_len.tolist() == [32, 16 + T, 30]
+    kd, qd, got = f64(k), f64(q), f64(out)
+    for b in range(3):
+        check(b, slice(b * T, b * T + T), got, lens[b])
