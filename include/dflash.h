@@ -426,12 +426,13 @@ DFLASH_API int dflash_gdn_replay(int32_t batch, int32_t n_heads, int32_t dk, int
                                  dflash_stream_t stream);
 
 /*
- * Serving over a KV cache held in 4 bits: the calls of one layer for a ragged
+ * Serving over a KV cache held in 4 bits: the calls of a step for a ragged
  * batch ([P2] 保证三: what the caches hold bounds the batch).  The batch's new
  * rows lie back to back, sequence after sequence: rows start[b] ..
  * start[b + 1] - 1 of q, k, v and out belong to sequence b.  Rows behind the
  * last sequence (a batch padded to a fixed n_tokens) are left as they were.
- *   dflash_kv_reserve   pages for the new rows; start, pos, slot, new_len
+ *   dflash_kv_reserve   pages for the new rows; start, pos, slot, new_len: once a step, for
+ *                       all layers that share lengths and page table
  *   dflash_qk_norm_rope per-head norms of q and k, rotated at pos
  *   dflash_kv4_append   k, v rows quantised into the cells named by slot
  *   dflash_kv4_attention  the new rows' attention over the whole cache

@@ -1057,3 +1057,44 @@ def test_step_with_a_sequence_that_was_not_served(T):
     kd, qd, got = f64(k), f64(q), f64(out)
     for b in range(3):
         check(b, slice(b * T, b * T + T), got, lens[b])
+
+
+def test_layers_share_one_reservation():
+    """Two layers' cells over one set of lengths and pages: reserved and cropped once a step, as
+    the documentation has it, over three steps."""
+    dfl = _dfl()
+    rng = np.random.default_rng(41)
+    B, hq, hkv, d, n_pages = 2, 4, 2, 64, 20
+    seq, table, free, count = (i32([0] * B), i32(np.full((B, 8), -1)),
+                               i32(rng.permutation(n_pages)), i32([n_pages]))
+    views = [dfl.KV4View(dfl.alloc_kv4_cells(n_pages, hkv, 16, d), seq, 128, table, free, count, 16)
+             for _ in range(2)]
+    K, V = ([[np.zeros((0, hkv, d))] * B for _ in views] for _ in range(2))
+    for new, kept in (([20, 5], [20, 5]), ([16, 16], [3, 16]), ([1, 1], [1, 1])):
+        T, n = max(new), sum(new)
+        dims = dfl.make_kv4_dims(B, n, T, hq, hkv, d)
+        ws = dfl.alloc_kv4_workspace(dims)
+        start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda") for m in (B + 1, n, n))
+        before = seq.clone()
+        dfl.dflash_kv_reserve(dims, views[0], i32(new), start, pos, slot, seq, ws)
+        for i, view in enumerate(views):
+            q, k, v = (bf16(rng.normal(size=(n, h, d))) for h in (hq, hkv, hkv))
+            out = torch.zeros_like(q)
+            dfl.dflash_qk_norm_rope(dims, q, k, None, None, pos, 1e6, 1e-6, q, k)
+            dfl.dflash_kv4_append(dims, k, v, slot, view, ws)
+            dfl.dflash_kv4_attention(dims, q, start, view, 0.125, True, out, ws)
+            at = 0
+            for b, t in enumerate(new):
+                rows = slice(at, at + t)
+                K[i][b] = np.concatenate([K[i][b], O.values(*O.quantise(f64(k)[rows], [0]), [0])])
+                V[i][b] = np.concatenate([V[i][b], O.values(*O.quantise(f64(v)[rows], [0]), [0])])
+                L = len(K[i][b])
+                ref, avg, e = O.attention(f64(q)[rows], K[i][b], V[i][b],
+                                          [L - t + j + 1 for j in range(t)], 0.125)
+                assert (np.abs(f64(out)[rows] - ref) <= bound(ref, avg, e, V[i][b])).all(), (i, b)
+                K[i][b], V[i][b] = (x[:L - t + kept[b]] for x in (K[i][b], V[i][b]))
+                at += t
+        dfl.dflash_kv_crop([views[0].pages()], before + i32(kept), B, ws)
+        assert status(ws) == 0
+        assert seq.tolist() == [len(x) for x in K[0]]
+    assert int(count) == n_pages - sum(-(-len(x) // 16) for x in K[0])
