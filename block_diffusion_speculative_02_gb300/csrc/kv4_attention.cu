@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
           }
           if (lane == 0) q_max[warp - kQuery] = m;
           named_bar_sync(15, 64);
-          const int e = static_cast<int>(max(q_max[0], q_max[1]) >> 7);   // exponent + 127
-          if (e != 0 && (e < 125 || e > 141)) {
+          const int most = static_cast<int>(max(q_max[0], q_max[1])), e = most >> 7;
+          if (most != 0 && (e < 125 || e > 141)) {                        // e: exponent + 127
             ex = max(-126, min(126, 141 - e));
             f = pow2(ex);
             again = true;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       if (tid == 0) {
         Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows,
-                    p.scale_log2 * pow2(gain_exp(p.s.k_exp, g.h)) * pow2(-ex),
+                    times_pow2(p.scale_log2, gain_exp(p.s.k_exp, g.h) - ex),
                     pow2(gain_exp(p.s.v_exp, g.h))};
         piece[par] = pc;
       }

@@ -239,6 +239,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// s 2^e, |e| <= 190; half of the power at a time, so that nothing overflows or vanishes on the way
+// to a result that does not.
+__device__ __forceinline__ float times_pow2(float s, int e) {
+  return s * pow2(e / 2) * pow2(e - e / 2);
+}
+
 __device__ __forceinline__ float warp_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(RowsCfg<D, kTiles>::kThreads, 1)
       if (t == 0) {
         // (never 0, so that a masked score stays minus infinity: 2^-149 leaves every finite
         // score below 2^-100)
-        const float y = p.scale_log2 * pow2(gain_exp(p.s.k_exp, r.h)) * pow2(-ex);
+        const float y = times_pow2(p.scale_log2, gain_exp(p.s.k_exp, r.h) - ex);
         row_sc[row] = y == 0.f ? __int_as_float(1) : y;
       }
     }

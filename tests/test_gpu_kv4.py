@@ -1098,3 +1098,21 @@ def test_layers_share_one_reservation():
         assert status(ws) == 0
         assert seq.tolist() == [len(x) for x in K[0]]
     assert int(count) == n_pages - sum(-(-len(x) // 16) for x in K[0])
+
+
+@pytest.mark.parametrize("T", [1, 4, 8, 16, 32])
+def test_attention_smallest_queries_and_largest_scale(T):
+    """Queries of subnormal numbers, the scale near the largest number, gains either way: the
+    scores are of size 1, whatever the factors between are."""
+    rng = np.random.default_rng(T)
+    cache = Cache(rng, [300, 40], 4, 128)
+    gain = np.array([0, 12, 1, -2])
+    cache.k = [np.ldexp(k, (gain - cache.k_exp)[:, None]) for k in cache.k]
+    cache.k_exp = gain
+    cache.view.k_exp = i32(cache.k_exp)
+    whole = rng.integers(-8, 9, (2 * T, 16, 128))
+    whole[:, 4:8] = np.sign(whole[:, 4:8]) * (rng.random((2 * T, 4, 128)) < 2.0 ** -6)
+    whole[0, 0] = whole[-1, -1] = 0
+    q = bf16(np.ldexp(whole.astype(np.float64), -133))
+    assert (f64(q) == np.ldexp(whole.astype(np.float64), -133)).all()
+    check_attention(rng, cache, [T, T], 16, True, q=q, scale=2.0 ** 126)
