@@ -25,8 +25,8 @@
 // 6 significant bits) straight into TMEM.  With them in shared memory its traffic,
 // not DRAM, would bound the kernel: 128 KB written and read a tile of 18 KB.
 // Q is kept in fp16, where need be times a power of two (exact for bf16 values down to
-// 2^-12 of the unit's largest at least, 2^-23 of it off for smaller ones); P in fp16
-// (2^-12 of its value), O, the maximum and the sum in fp32.
+// 2^-15 of the unit's largest at least, 2^-23 of it off for smaller ones); P in fp16
+// (half a step is 2^-11 of its value), O, the maximum and the sum in fp32.
 // Softmax: a thread owns a key and walks the query columns.  The running maximum m
 // of a column only moves when a tile passes it by 2^8, which one vote per tile
 // finds out; until then exp2(x - m) needs no reduction over keys at all, and the

@@ -561,9 +561,13 @@ DFLASH_API int dflash_kv4_gather(const dflash_kv4_dims* dims, const int32_t* slo
  * (q rotated already, as dflash_qk_norm_rope leaves it).  A row that sees
  * nothing (m <= 0) is zero.
  *   q, out: bf16 [N, Hq, D]; start: int32 [B + 1]; scale finite, in units of log 2
- *   too (times 1.4427).  Queries enter the products to 2^-12 of an element or
- *   2^-23 of the largest one among the up to 128 rows that share a KV head's
- *   unit of work, whichever is more; N * Hq must be below 2^31.
+ *   too (times 1.4427); N * Hq must be below 2^31.
+ * Queries enter the products in fp16, times a power of two: exact down to 2^-15 of the
+ * largest finite one among the up to 128 rows (of 16 and fewer: of the row) that share a KV
+ * head's unit of work, and below that off by at most 2^-23 of it.  Probabilities enter the
+ * second product in fp16, off by at most 2^-11 of their value (and 2^-32 of the row's largest
+ * below 2^-21 of it); their sum is that of the unrounded ones.  Scores, sums and outputs are
+ * fp32 until the output's one rounding.
  * A sequence whose rows do not lie in 0..N, with T > max_tokens, or with L < 0
  * or past the capacity sets DFLASH_ST_CAPACITY and its output is left unwritten;
  * unmapped pages inside the length set DFLASH_ST_PAGE_MISSING and read as zeros,

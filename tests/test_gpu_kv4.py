@@ -1116,3 +1116,43 @@ def test_attention_smallest_queries_and_largest_scale(T):
     q = bf16(np.ldexp(whole.astype(np.float64), -133))
     assert (f64(q) == np.ldexp(whole.astype(np.float64), -133)).all()
     check_attention(rng, cache, [T, T], 16, True, q=q, scale=2.0 ** 126)
+
+
+@pytest.mark.parametrize("fine", [False, True])
+@pytest.mark.parametrize("T", [1, 4, 8, 16, 32])
+def test_attention_small_rows_beside_large_ones(T, fine):
+    """Rows of one unit down to 2^-18 of its largest, which lies just above 2^-2 (where queries
+    are left as they are), under a scale that gives the small rows scores of a few units.
+
+    A query element is off by at most e = 2^-23 of the unit's largest, so every score of a row by
+    at most s = scale sum |k| e, a weight by a factor of exp(+-2 s): added to bound() is
+    A (exp(2 s) - 1).  Elements that are multiples of 2^-24 are exact (`fine`): nothing is added."""
+    dfl = _dfl()
+    rng = np.random.default_rng(T)
+    hq, d, lens = 4, 128, [300, 77]
+    cache = Cache(rng, lens, 1, d, exps=False)
+    q = rng.uniform(0.25, 0.4375, (2 * T, hq, d)) * rng.choice([-1, 1], (2 * T, hq, d))
+    small = rng.random((2 * T, hq)) < 0.7
+    if fine:
+        q[small] = rng.integers(-8, 9, (int(small.sum()), d)) * 2.0 ** -20
+    else:
+        q[small] *= np.exp2(rng.integers(-16, -11, (int(small.sum()), 1)))
+    qt = bf16(q)
+    scale = 2.0 ** 14
+    dims = dfl.make_kv4_dims(2, 2 * T, T, hq, 1, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    out = torch.zeros_like(qt)
+    dfl.dflash_kv4_attention(dims, qt, i32([0, T, 2 * T]), cache.view, scale, True, out, ws)
+    assert status(ws) == 0
+    qd, got = f64(qt), f64(out)
+    for b, L in enumerate(lens):
+        for t in range(T):
+            row, m = b * T + t, L - T + t + 1
+            for h in range(hq):
+                ref, avg, e = O.attention(qd[row:row + 1, h:h + 1], cache.k[b], cache.v[b], [m],
+                                          scale)
+                tol = bound(ref, avg, e, cache.v[b])
+                if not fine and small[row, h]:
+                    s = scale * np.abs(cache.k[b][:m, 0]).sum(-1).max() * 2.0 ** -23 * 0.4375
+                    tol = tol + avg * np.expm1(2 * s)
+                assert (np.abs(got[row, h] - ref) <= tol).all(), (b, t, h, bool(small[row, h]))
