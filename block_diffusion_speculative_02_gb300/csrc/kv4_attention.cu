@@ -38,8 +38,11 @@
 // against 1,700 and 2,450 measured; the products themselves take 512 and 1,024.  Beside the
 // tiles a unit costs three to five tiles' time: its first maxima, the drain of O, code that
 // is fetched anew.  Measured: 32 blocks of 16 rows over 512 to 16,384 keys (32 + 8 heads of
-// 128 dims) 118 us, 2.7 TB/s of cells and 600 TFLOP/s; 4 blocks at 32,768 keys, 64 heads,
-// 84 us, 820 TFLOP/s; prompt chunks of 257 to 1,024 rows 158 us, 740 TFLOP/s.
+// 128 dims) 118 us, 2.7 TB/s of cells and 600 TFLOP/s (109 us at 64 dims); 4 blocks at 32,768
+// keys, 64 heads (128 columns), 84 to 88 us over several runs, 780 to 820 TFLOP/s; prompt chunks of
+// 257 to 1,024 rows 158 to 170 us, 690 to 740 TFLOP/s (148 us at 64 dims).  The registers of a
+// role are few: some 40 bytes of a thread go to local memory at 64 columns, 130 at 128 (one warp
+// instruction in 100 there loads from it).
 // Tried and slower: two warpgroups that expand V at 128 columns (the registers of the
 // softmax), a second S buffer at 128 in place of those of K and V (201 us against 188 then),
 // one copy of the code that reads the scores (195 against 187: the loop costs more than the
@@ -903,7 +906,9 @@ int launch_join(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
                 p);
 }
 
-// Four rows a warp; one where a unit is small or cut into eight pieces or more.  Measured with
+// Four rows a warp; one where a unit is small, or cut into eight pieces or more on the average over
+// the units (their lengths are on the device and not looked at: one long unit among many short
+// ones has the four-row join, which is slower and no less right).  Measured with
 // one and four: a block at 8192 keys (19 pieces) 16.5 and 18.8 us, single rows (units of 16)
 // 83.2 and 83.7; four blocks at 32,768 keys (5 pieces) 87.0 and 85.8, prompt chunks (2 to 3)
 // 167.1 and 163.5: there CTAs without work cost more than they save.
@@ -915,7 +920,12 @@ int run_join(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
                                        : launch_join<D, NQ, 4>(p, ctas, st);
 }
 
-// Query columns of a unit: the fewest that hold the rows of the longest sequence.
+// Query columns of a unit: the fewest that hold the rows of the longest sequence, for every unit of
+// the batch.  So a prompt among tokens puts the tokens' units into 128 columns too: one prompt
+// of 1,024 rows among 63 tokens over 512 to 16,384 keys takes 343 us, in two calls the prompt 34
+// and the tokens 154.  Units of 9 to 16 rows (32 x 4 rows, 32 + 8 heads, same keys) take 77 us by the
+// kernel for few rows and 103 through 32 columns at 64 dims, 118 and 109 at 128; 17 to 32 rows
+// (32 x 8) 104 and 110 us.
 int query_columns(const dflash_kv4_dims& d) {
   const long long rows =
       static_cast<long long>(d.max_tokens) * (d.n_q_heads / d.n_kv_heads);
@@ -991,8 +1001,11 @@ extern "C" int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
   p.group_inv = (65536 + p.group - 1) / p.group;
   // Measured in tiles: with 2, 3, 4, 5, 6 of them prompt chunks (128 columns) took 261, 201,
   // 186, 168, 171 us and a prompt of 4096 rows 325, 277, 229, 208, 209 (with 4 and 5 and today's
-  // drain of O 174, 158 and 212, 193); with 2, 3, 4 four blocks at 32K (64 columns) 90, 89, 88
-  // us and blocks at batch 32 123, 120, 121, and single rows (the kernel for few rows) 88, 87, 84.
+  // drain of O 174, 158 and 212, 193), four blocks at 32K (128 columns too, units of equal
+  // length) 88.0, 86.9, 87.0, 87.6, 88.0; at batch 32 over 512 to 16,384 keys blocks of 16 rows
+  // (64 columns) 118.1, 118.3, 119.4, 119.8, 122.0, of 8 rows (32 columns) 109.3, 110.0, 111.0,
+  // 111.3, 113.8, of 4 (the kernel for few rows) 121.1, 117.8, 118.1, 118.8, 119.6, single rows
+  // 86.8, 86.6, 83.3, 83.2, 83.5.  (At 64 dims 8 rows 103.3 to 106.8, in the same order.)
   p.unit_cost = a.nq == 128 ? 5 : a.nq == 16 ? 4 : 3;
   p.paged = cache->kv.page_table != nullptr;
   p.page_size = cache->kv.page_size;

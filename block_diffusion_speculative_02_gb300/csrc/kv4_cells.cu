@@ -74,8 +74,9 @@ __device__ __forceinline__ uint2 quantise16(const uint4& a, const uint4& b, floa
 // bytes, which lie 16 apart in a cell of V, leave 16 rows side by side; sixteen rows that
 // are one whole cell leave as it is, 16 bytes a store.
 // Floor: 2 bytes an element in, 0.5625 out (or back).  Prompts of 17,600 rows in all, 8 heads of
-// 128 dims, take 24 us each way, 3.8 TB/s: what bounds them is the passage through shared
-// memory (its barriers and byte accesses) and the conversions, not the copies.  A few rows
+// 128 dims, take 21 us in and 33 back (48 one after the other: the way back then finds cells in
+// L2), 4.3 and 2.8 TB/s: what bounds them is the passage through shared memory (its barriers and
+// byte accesses) and the conversions, not the copies.  A few rows
 // per sequence (blocks at batch 32) are launch and two dependent loads.
 template <int D>
 struct CellIo {

@@ -22,8 +22,8 @@
 // What bounds it: some 400 instructions a cell (about 100 to expand K, 120 for V, 40 for the
 // softmax), 58% of the issue slots and 54% of the integer pipe in use.  Measured: one token
 // of each of 32 sequences over 512 to 16,384 keys (32 + 8 heads of 128 dims) 84 us, 3.7 TB/s
-// of cells; with 15 or 17 warps on cells 86 and 90 us, by the tensor kernel with units of 16
-// columns 108 us at best.
+// of cells (61 us at 64 dims); with 15 or 17 warps on cells 86 and 90 us, by the tensor kernel
+// with units of 16 columns 108 us at best.  Four rows each (kTiles = 2) 118 us, 77 at 64 dims.
 #include "kv4_attention.cuh"
 
 namespace dflash {

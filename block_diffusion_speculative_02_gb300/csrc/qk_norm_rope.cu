@@ -162,7 +162,8 @@ struct Heads {
 // One CTA per row, five of them to an SM.  Floor: the 4 bytes an element moves.  8191 rows of
 // 64 + 8 heads of 128 dims take 56.5 us, 5.35 TB/s; before the products above were formed
 // once a row the instruction slots were the bound (69% of them, 60 us).  Two heads of a
-// thread in flight in place of four 59 us, six CTAs to an SM 58 us.
+// thread in flight in place of four 59 us, six CTAs to an SM 58 us.  (Five CTAs leave 48
+// registers a thread: 56 bytes of it go to local memory at 128 dims.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 5) qk_norm_rope_kernel(const NormRopeParams p) {
   using H = Heads<D>;
