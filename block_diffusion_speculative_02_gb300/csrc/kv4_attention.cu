@@ -915,7 +915,7 @@ int launch_join(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
 template <int D, int NQ>
 int run_join(const Kv4AttnParams& p, int ctas, cudaStream_t st) {
   const long long units = static_cast<long long>(p.batch) * p.s.n_kv_heads *
-                          ((p.max_tokens + p.tile_rows - 1) / p.tile_rows);
+                          ((p.max_tokens - 1) / p.tile_rows + 1);
   return NQ == 16 || units * 8 <= ctas ? launch_join<D, NQ, 1>(p, ctas, st)
                                        : launch_join<D, NQ, 4>(p, ctas, st);
 }

@@ -1156,3 +1156,35 @@ def test_attention_small_rows_beside_large_ones(T, fine):
                     s = scale * np.abs(cache.k[b][:m, 0]).sum(-1).max() * 2.0 ** -23 * 0.4375
                     tol = tol + avg * np.expm1(2 * s)
                 assert (np.abs(got[row, h] - ref) <= tol).all(), (b, t, h, bool(small[row, h]))
+
+
+def test_no_bound_on_new_rows():
+    """max_tokens 2^31 - 1: every call takes it as no bound."""
+    dfl = _dfl()
+    rng = np.random.default_rng(51)
+    cache = Cache(rng, [40, 300, 2], 2, 64, spare=8, extra_rows=20)
+    view, new = cache.view, [20, 1, 7]
+    n = sum(new)
+    outs = []
+    lens = view.seq_len.clone()
+    for top in (2 ** 31 - 1, 20):
+        dims = dfl.make_kv4_dims(3, n, top, 8, 2, 64)
+        ws = dfl.alloc_kv4_workspace(dims)
+        start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda") for m in (4, n, n))
+        view.seq_len.copy_(lens)
+        g = np.random.default_rng(1)
+        q, k, v = (bf16(g.normal(size=(n, h, 64))) for h in (8, 2, 2))
+        out = torch.zeros_like(q)
+        dfl.dflash_kv_reserve(dims, view, i32(new), start, pos, slot, view.seq_len, ws)
+        dfl.dflash_qk_norm_rope(dims, q, k, None, None, pos, 1e6, 1e-6, q, k)
+        dfl.dflash_kv4_append(dims, k, v, slot, view, ws)
+        dfl.dflash_kv4_attention(dims, q, start, view, 0.125, True, out, ws)
+        assert status(ws) == 0
+        outs.append(out)
+    # A unit takes 32 rows or 16: the same sums in other tiles.  Each run is within bound() of the
+    # exact value: with A <= V, the largest |v| (a value of 4 bits is at most 1 + 2^-4 of what it stands
+    # for, or half a smallest step), and e < 64 (0.125 * 64 dims * |q| |k| of 8 on the average):
+    # 2^-8 of the value and V (2^-10 + 2^-20 + 65 * 2^-16) < V 2^-8 for each of the two
+    V = max(1.07 * np.abs(f64(v)).max() + 2.0 ** -9, max(np.abs(x).max() for x in cache.v))
+    a, b = (f64(x) for x in outs)
+    assert (np.abs(a - b) <= 2.0 ** -7 * np.maximum(np.abs(a), np.abs(b)) + 2.0 ** -7 * V).all()
