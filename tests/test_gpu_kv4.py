@@ -1188,3 +1188,160 @@ def test_no_bound_on_new_rows():
     V = max(1.07 * np.abs(f64(v)).max() + 2.0 ** -9, max(np.abs(x).max() for x in cache.v))
     a, b = (f64(x) for x in outs)
     assert (np.abs(a - b) <= 2.0 ** -7 * np.maximum(np.abs(a), np.abs(b)) + 2.0 ** -7 * V).all()
+
+
+def test_largest_batch():
+    """4096 sequences: reserved, appended and attended in one step, from a prompt's rows to none."""
+    dfl = _dfl()
+    rng = np.random.default_rng(61)
+    B, hq, hkv, d, width = 4096, 2, 1, 64, 4
+    new = rng.integers(0, 4, B)
+    new[[0, 77, B - 1]] = 50, 0, 33
+    n = int(new.sum()) + 5
+    pages = int((-(-new // 16)).sum()) + 9
+    view = dfl.KV4View(dfl.alloc_kv4_cells(pages, hkv, 16, d), i32([0] * B), width * 16,
+                       i32(np.full((B, width), -1)), i32(rng.permutation(pages)), i32([pages]), 16)
+    dims = dfl.make_kv4_dims(B, n, 50, hq, hkv, d)
+    ws = dfl.alloc_kv4_workspace(dims)
+    start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda") for m in (B + 1, n, n))
+    q, k, v = (bf16(rng.normal(size=(n, h, d))) for h in (hq, hkv, hkv))
+    out = torch.full_like(q, 3.0)
+    dfl.dflash_kv_reserve(dims, view, i32(new), start, pos, slot, view.seq_len, ws)
+    dfl.dflash_kv4_append(dims, k, v, slot, view, ws)
+    dfl.dflash_kv4_attention(dims, q, start, view, 0.125, True, out, ws)
+    assert status(ws) == 0 and int(view.free_count) == 9
+    assert (view.seq_len.cpu().numpy() == new).all()
+    at = np.concatenate([[0], np.cumsum(new)])
+    assert (start.cpu().numpy() == at).all()
+    K, V = (O.values(*O.quantise(f64(x), [0]), [0]) for x in (k, v))
+    got, qd = f64(out), f64(q)
+    for b in [0, 1, 31, 32, 33, 77, 1000, 2047, 2048, *rng.integers(0, B, 200), B - 2, B - 1]:
+        rows = slice(at[b], at[b + 1])
+        ref, avg, e = O.attention(qd[rows], K[rows], V[rows], range(1, new[b] + 1), 0.125)
+        assert (np.abs(got[rows] - ref) <= bound(ref, avg, e, V[rows])).all(), b
+    assert (got[at[-1]:] == 3).all()
+
+
+@pytest.mark.parametrize("T", [1, 16, 64])
+def test_a_batch_without_new_rows(T):
+    """Nothing but padding: nothing is taken, written or read."""
+    dfl = _dfl()
+    rng = np.random.default_rng(T)
+    cache = Cache(rng, [40, 0, 17], 1, 64)
+    dims = dfl.make_kv4_dims(3, T, T, 4, 1, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    cells, table = cache.view.cells.clone(), cache.view.page_table.clone()
+    start, pos, slot = (torch.full((m,), 9, dtype=I32, device="cuda") for m in (4, T, T))
+    q, k = (torch.full((T, h, 64), 2.0, dtype=BF, device="cuda") for h in (4, 1))
+    out = torch.full_like(q, 5.0)
+    dfl.dflash_kv_reserve(dims, cache.view, i32([0, 0, 0]), start, pos, slot, cache.view.seq_len, ws)
+    dfl.dflash_qk_norm_rope(dims, q, k, None, None, pos, 1e6, 1e-6, q, k)
+    dfl.dflash_kv4_append(dims, k, k, slot, cache.view, ws)
+    dfl.dflash_kv4_attention(dims, q, start, cache.view, 0.125, True, out, ws)
+    dfl.dflash_kv4_gather(dims, slot, cache.view, k, k.clone(), ws)
+    assert status(ws) == 0
+    assert start.tolist() == [0] * 4 and pos.tolist() == slot.tolist() == [-1] * T
+    assert torch.equal(cache.view.cells, cells) and torch.equal(cache.view.page_table, table)
+    assert (out == 5).all() and (q == 2).all() and (k == 2).all()
+    assert cache.view.seq_len.tolist() == [40, 0, 17]
+
+
+def test_shared_pages_and_repeated_slots():
+    """Two sequences over the same full pages of a prefix, each going on in pages of its own; rows
+    gathered more than once."""
+    dfl = _dfl()
+    rng = np.random.default_rng(71)
+    cache = Cache(rng, [48, 64], 2, 64, spare=6, extra_rows=20)
+    view = cache.view
+    view.page_table[1, :3] = view.page_table[0, :3]
+    view.page_table[1, 3] = -1
+    view.seq_len.fill_(48)
+    cache.k[1], cache.v[1] = cache.k[0], cache.v[0]
+    T, n = 5, 10
+    dims = dfl.make_kv4_dims(2, n, T, 8, 2, 64)
+    ws = dfl.alloc_kv4_workspace(dims)
+    start, pos, slot = (torch.zeros(m, dtype=I32, device="cuda") for m in (3, n, n))
+    gain = np.ldexp(1.0, -np.repeat(cache.k_exp, 4))[:, None]
+    q = bf16(rng.normal(size=(n, 8, 64)) * gain)
+    k, v = (bf16(rng.normal(size=(n, 2, 64)) * np.ldexp(1.0, e)[:, None])
+            for e in (cache.k_exp, cache.v_exp))
+    out = torch.zeros_like(q)
+    dfl.dflash_kv_reserve(dims, view, i32([T, T]), start, pos, slot, view.seq_len, ws)
+    dfl.dflash_kv4_append(dims, k, v, slot, view, ws)
+    dfl.dflash_kv4_attention(dims, q, start, view, 0.125, True, out, ws)
+    assert status(ws) == 0
+    kq, vq = (O.values(*O.quantise(f64(x), e), e) for x, e in ((k, cache.k_exp), (v, cache.v_exp)))
+    for b in range(2):
+        rows = slice(b * T, b * T + T)
+        kk, vv = (np.concatenate([x[b], y[rows]]) for x, y in ((cache.k, kq), (cache.v, vq)))
+        ref, avg, e = O.attention(f64(q)[rows], kk, vv, range(49, 49 + T), 0.125)
+        assert (np.abs(f64(out)[rows] - ref) <= bound(ref, avg, e, vv)).all(), b
+    again = slot[torch.tensor([0, 0, 9, 3, 9, 9, 1, 0, 3, 2])].contiguous()
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    dfl.dflash_kv4_gather(dims, again, view, ko, vo, ws)
+    pick = [0, 0, 9, 3, 9, 9, 1, 0, 3, 2]
+    np.testing.assert_array_equal(f64(ko), kq[pick])
+    np.testing.assert_array_equal(f64(vo), vq[pick])
+
+
+def test_gains_past_their_ends_count_as_the_ends():
+    dfl = _dfl()
+    rng = np.random.default_rng(81)
+    far, near = i32([100, -2 ** 31]), i32([64, -64])
+    got = []
+    x = bf16(rng.normal(size=(20, 2, 64)) * np.ldexp(1.0, [64, -64])[:, None])
+    q = bf16(rng.normal(size=(20, 4, 64)) * np.ldexp(1.0, [-64, -64, 64, 64])[:, None])
+    for exp in (far, near):
+        view = dfl.KV4View(dfl.alloc_kv4_cells(2, 2, 16, 64), i32([20]), 32, i32([[1, 0]]),
+                           i32([0, 0]), i32([0]), 16, exp, exp)
+        dims = dfl.make_kv4_dims(1, 20, 20, 4, 2, 64)
+        ws = dfl.alloc_kv4_workspace(dims)
+        slot = i32([16 + i if i < 16 else i - 16 for i in range(20)])
+        dfl.dflash_kv4_append(dims, x, x, slot, view, ws)
+        ko, vo, out = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(q)
+        dfl.dflash_kv4_gather(dims, slot, view, ko, vo, ws)
+        dfl.dflash_kv4_attention(dims, q, i32([0, 20]), view, 0.125, True, out, ws)
+        assert status(ws) == 0
+        got.append((view.cells, ko, vo, out))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    e = np.array([64, -64])
+    ref = O.values(*O.quantise(f64(x), e), e)
+    np.testing.assert_array_equal(f64(got[0][1]), ref)
+    ref, avg, s = O.attention(f64(q), ref, ref, range(1, 21), 0.125)
+    for h in range(4):                                   # (bound() head by head: sizes 2^128 apart)
+        tol = bound(ref[:, h], avg[:, h], s, f64(x)[:, h // 2])
+        assert (np.abs(f64(got[0][3])[:, h] - ref[:, h]) <= tol).all(), h
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_norm_rope_keeps_bad_values_in_their_heads(d):
+    """NaN and infinities of one head leave the head beside it in the warp, and other rows, alone;
+    a row of zeros stays zero; subnormal and large values are normed like others."""
+    dfl = _dfl()
+    rng = np.random.default_rng(d)
+    n, hq, hkv = 4, 6, 3
+    q0, k0 = rng.normal(size=(n, hq, d)), rng.normal(size=(n, hkv, d))
+    q0[2, 1], k0[1, 2] = 0, 0
+    q0[1, 2] *= 2.0 ** 40
+    w = bf16(1 + 0.2 * rng.normal(size=d))
+    pos = [5, 0, 70000, 1]
+    dims = dfl.make_kv4_dims(1, n, n, hq, hkv, d)
+    runs = []
+    for bad in (False, True):
+        q, k = bf16(q0), bf16(k0)
+        if bad:
+            q[0, 3, 7], q[3, 0, d - 1], k[2, 0, 0] = float("nan"), float("inf"), float("-inf")
+        qo, ko = torch.zeros_like(q), torch.zeros_like(k)
+        dfl.dflash_qk_norm_rope(dims, q, k, w, w, i32(pos), 1e6, 1e-6, qo, ko)
+        runs.append((qo, ko))
+    (qa, ka), (qb, kb) = runs
+    for a, b, at in ((qa, qb, [(0, 3), (3, 0)]), (ka, kb, [(2, 0)])):
+        for i in at:
+            assert torch.isnan(b[i]).any()
+            b[i] = a[i]
+        assert torch.equal(a, b)
+    assert (qa[2, 1] == 0).all() and (ka[1, 2] == 0).all()
+    ref = O.norm_rope(f64(bf16(q0)), f64(w), pos, 1e6, 1e-6)
+    pair = np.abs(ref) + np.abs(np.roll(ref, d // 2, axis=-1))
+    tol = 2.0 ** -8 * np.abs(ref) + pair * (2.0 ** -16 + np.abs(pos)[:, None, None] * 2.0 ** -52)
+    assert (np.abs(f64(qa) - ref) <= tol).all()
