@@ -222,16 +222,19 @@ class _View:
     def __getstate__(self):
         return {k: v for k, v in self.__dict__.items() if k not in self._KEPT}
 
-    def __setattr__(self, name, value):
+    def _drop(self, name):
         d = self.__dict__
         d.pop("_struct", None)
         if name not in ("cells", "k_exp", "v_exp"):
             d.pop("_pages", None)
-        d[name] = value
+
+    def __setattr__(self, name, value):
+        self._drop(name)
+        super().__setattr__(name, value)
 
     def __delattr__(self, name):
-        setattr(self, name, None)
-        del self.__dict__[name]
+        self._drop(name)
+        super().__delattr__(name)
 
 
 @dataclass

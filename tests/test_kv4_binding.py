@@ -134,3 +134,27 @@ def test_a_single_row_has_any_pitch():
         assert dflash._rows_on(heads, HOST, 1, 2, 64, "q")[1] % 8 == 0
     two = torch.zeros(2, 515, dtype=torch.bfloat16)[:, :128].unflatten(1, (2, 64))
     assert dflash._rows_on(two, HOST, 2, 2, 64, "q")[1] == 515
+
+
+def test_a_view_subclass_keeps_its_properties():
+    """Setting and deleting fields goes through a subclass's own descriptors."""
+    dflash = _dflash()
+    seen = []
+
+    class Watched(dflash.KV4View):
+        @property
+        def note(self):
+            return len(seen)
+
+        @note.setter
+        def note(self, value):
+            seen.append(value)
+
+    view = _view4()
+    watched = Watched(*(getattr(view, f) for f in ("cells", "seq_len", "capacity", "page_table",
+                                                   "free_list", "free_count", "page_size")))
+    watched.note = 5
+    assert seen == [5] and watched.note == 1
+    _use(watched)
+    del watched.k_exp                                   # back to the class's None
+    assert watched.k_exp is None and _use(watched).k_exp is None
