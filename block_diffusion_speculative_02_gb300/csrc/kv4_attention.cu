@@ -95,11 +95,11 @@ struct Cfg {
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kSmem = 1024 + kFixed + kTables + kStages * kStage;
   static_assert(kStages >= 3, "shared memory");
-  // The record of tile j replaces that of j - kRing once the V warps let go of the cells of
-  // tile j - kStages.  They began it after the product P V of two tiles before, whose P the
-  // softmax had brought, so by then it had left tile j - kStages - 3 and its record.
+  // The record of tile j replaces that of j - kRing once the K and V warps let go of the cells
+  // of tile j - kStages, and with them of its record.  The V warps began it after the product P V
+  // of two tiles before, which the MMA warp issues after it read the record of the tile between.
   static constexpr int kRing = 16;
-  static_assert(kRing >= kStages + 3, "tile records");
+  static_assert(kRing > kStages, "tile records");
 };
 
 // Which key of a tile lies in TMEM lane r of S^T (and is r in the second product's k index), and
@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         }
       }
       if (tid == 0) {
-        Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len, rows,
+        Piece pc = {g.tile, g.n, g.nt, p.causal ? max(0, g.len - g.T + g.t0 + 1) : g.len,
+                    rows | (go ? 0 : kFinalPiece),
                     times_pow2(p.scale_log2, gain_exp(p.s.k_exp, g.h) - ex),
                     pow2(gain_exp(p.s.v_exp, g.h))};
         piece[par] = pc;
@@ -587,7 +588,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
     for (int seg = 0; go; ++seg) {
       const int par = seg & 1;
       const int* vis = col_vis + par * NQ + col0;
-      wait(&s_full[j % C::kSBufs], (j / C::kSBufs) & 1);     // the segment's tables are there
+      // the segment's tables are there (that a product is done would not order their writes)
+      wait(&q_full[par], (seg >> 1) & 1);
       if (bar_or(bar, 128, wait.dead)) break;
       const int n = piece[par].n, tile0 = piece[par].tile, sure = piece[par].sure;
       const float scale = piece[par].scale;
@@ -729,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
         warp_arrive(&pv_full[j & 1]);              // (the reader fences the proxies)
       }
       // ---- the unit's (or piece's) result ----
-      go = !(tiles[(j - 1) % C::kRing].flags & kFinal);
+      go = !(piece[par].rows & kFinalPiece);
       // column sums over the warp's keys: half of the columns change hands at each step,
       // so lane c ends with column c
       {
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1)
       }
       named_bar_sync(bar, 128);
       const int* row = col_row + par * NQ + col0;
-      const int rows = min(CW, piece[par].rows - col0);             // of this warpgroup
+      const int rows = min(CW, (piece[par].rows & ~kFinalPiece) - col0);    // of this warpgroup
       wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
       __syncwarp();
       tc_fence_after();

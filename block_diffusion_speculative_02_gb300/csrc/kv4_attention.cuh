@@ -91,11 +91,12 @@ struct Tile {
   int left;                  // keys in use from its first one on
   int flags;                 // the first of its segment; the last of the CTA
 };
-constexpr int kFirst = 1, kFinal = 2;
+constexpr int kFirst = 1, kFinal = 2, kFinalPiece = 256;
 
 // What the softmax needs of a segment, left in shared memory beside its query rows.
 struct Piece {
-  int tile, n, nt, sure, rows;      // sure: keys that every row sees
+  int tile, n, nt, sure;            // sure: keys that every row sees
+  int rows;                         // and kFinalPiece, if it is the last of the CTA
   float scale, v_gain;              // log2 units per score; 2^exp of V's head
 };
 
