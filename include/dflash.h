@@ -440,7 +440,8 @@ DFLASH_API int dflash_gdn_replay(int32_t batch, int32_t n_heads, int32_t dk, int
  * A verify forward appends its block and attends with causal = 1; the drafter
  * appends its block, attends with causal = 0 and crops it off again; a token
  * by token decode passes one row a sequence; a prompt any number.  The crop
- * is dflash_kv_crop on the view's `kv` member.
+ * is dflash_kv_crop on the view's `kv` member.  (dflash_ctx_project and dflash_ctx_prefill
+ * write bf16 caches only: a drafter's context rows reach this cache by dflash_kv4_append.)
  */
 typedef struct {
   int32_t batch;         /* B: sequences, 1..4096                               */
