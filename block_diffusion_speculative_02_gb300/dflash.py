@@ -577,11 +577,14 @@ def _view_struct(v, device: int, batch: int, hkv: int, d: int):
     The struct is kept on the view until one of its fields is set, and used again as long as the
     tensors lie where they did, have the shapes they had, and are contiguous still.  It holds
     none of them alive."""
-    tensors = (_VIEW_TENSORS if hkv else _PAGE_TENSORS)(v)
     try:
+        tensors = (_VIEW_TENSORS if hkv else _PAGE_TENSORS)(v)
         key = [device, batch, hkv, d,
                *[t if t is None else (t.data_ptr(), t.shape, t.is_contiguous()) for t in tensors]]
-    except AttributeError:                    # not a tensor: the checks below say which
+    except AttributeError:                    # not a view, or not a tensor: see below
+        if not isinstance(v, KV4View) and (hkv or not isinstance(v, KVView)):
+            raise ValueError("the cache must be a KV4View" + ("" if hkv else " or a KVView")) \
+                from None
         key = None
     slot = "_struct" if hkv else "_pages"
     memo = v.__dict__.get(slot)

@@ -158,3 +158,13 @@ def test_a_view_subclass_keeps_its_properties():
     _use(watched)
     del watched.k_exp                                   # back to the class's None
     assert watched.k_exp is None and _use(watched).k_exp is None
+
+
+@pytest.mark.parametrize("cache", [None, "view", _view16])
+def test_a_cache_that_is_no_4_bit_view_is_a_value_error(cache):
+    dflash = _dflash()
+    with pytest.raises(ValueError, match="KV4View"):
+        dflash._view_struct(cache() if callable(cache) else cache, HOST, 2, 2, 64)
+    if not callable(cache):
+        with pytest.raises(ValueError, match="KVView"):
+            dflash._view_struct(cache, HOST, 2, 0, 0)
