@@ -170,19 +170,34 @@ int make_plan(const dflash_dims& d, Plan* p) {
   return DFLASH_OK;
 }
 
-int make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                      uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
+namespace {
+
+int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t cols,
+                 uint64_t rows, uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
   auto enc = encode_fn();
   if (!enc) return DFLASH_E_CUDA;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {row_pitch_bytes};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, DFLASH_TMAP_L2_PROMOTION,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   DFLASH_TMAP_L2_PROMOTION, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_E_ALIGN;
+}
+
+}  // namespace
+
+int make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                      uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
+  return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, row_pitch_bytes,
+                      box_cols, box_rows);
+}
+
+int make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                    uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
+  return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, cols, rows, row_pitch_bytes,
+                      box_cols, box_rows);
 }
 
 int make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
@@ -270,7 +285,7 @@ extern "C" const char* dflash_status_string(int code) {
   }
 }
 
-extern "C" int dflash_version(void) { return 109; }
+extern "C" int dflash_version(void) { return 110; }
 
 extern "C" int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes,
                                     dflash_stream_t stream) {

@@ -1,0 +1,312 @@
+// Rows and weights rounded to 8 bits (e4m3) with a scale for each block of 128.
+//
+// For a block with the largest magnitude a (at least 2^-117):
+//   scale = a / 448,  code = e4m3(h * (448 / a)),  a value is scale * code.
+// Everything before the codes is fp32.  All three calls are bound by memory: each element is
+// read once and written once, 16 of them (32 bytes in, 16 out) to a thread, so that 8
+// neighbouring lanes hold a block and find its maximum in three shuffles.
+#include <cmath>
+
+#include "fp8.cuh"
+
+namespace dflash {
+namespace fp8 {
+namespace {
+
+// --------------------------------------------------------------------------------------------
+// rows: h = RMSNorm(x + residual) * norm_w
+// --------------------------------------------------------------------------------------------
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const uint16_t* norm_w;
+  uint16_t* sum;
+  uint8_t* q;
+  float* scale;
+  long long x_pitch, residual_pitch, sum_pitch;
+  int rows, cols;
+  float eps;
+};
+
+constexpr int kWarpRows = 8;    // rows of a CTA where a warp takes one
+
+// A row to a CTA (or, up to 512 columns, to a warp): kChunks pieces of 16 columns stay
+// in the thread's registers from the sum of squares to the codes, so the row is read once.
+template <int kChunks, bool kWarp>
+__global__ void norm_rows_kernel(const NormParams p) {
+  const int t = threadIdx.x, step = blockDim.x;
+  const int row = kWarp ? blockIdx.x * kWarpRows + threadIdx.y : blockIdx.x;
+  const int pieces = p.cols / 16;
+  griddep_wait();
+  if (row >= p.rows) return;                                  // whole warps
+  float v[kChunks][16];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int i = t + c * step;
+    uint4 x[2] = {}, r[2] = {};
+    if (i < pieces) {
+      load16(p.x + row * p.x_pitch + 16 * i, x);
+      if (p.residual) load16(p.residual + row * p.residual_pitch + 16 * i, r);
+    }
+    widen16(x, v[c]);
+    if (p.residual) {
+      float w[16];
+      widen16(r, w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[c][j] += w[j];
+    }
+    if (p.norm_w) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) ss = fmaf(v[c][j], v[c][j], ss);
+    }
+  }
+  if (p.sum) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int i = t + c * step;
+      if (i >= pieces) continue;
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        o[j] = static_cast<uint32_t>(float_to_bf16_bits(v[c][2 * j])) |
+               static_cast<uint32_t>(float_to_bf16_bits(v[c][2 * j + 1])) << 16;
+      uint4* dst = reinterpret_cast<uint4*>(p.sum + row * p.sum_pitch + 16 * i);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+  if (p.norm_w) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!kWarp) {
+      __shared__ float part[32];
+      if ((t & 31) == 0) part[t >> 5] = ss;
+      __syncthreads();
+      ss = (t & 31) < (step >> 5) ? part[t & 31] : 0.f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
+    const float inv = rsqrtf(ss / p.cols + p.eps);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int i = t + c * step;
+      if (i >= pieces) continue;
+      uint4 w[2];
+      float g[16];
+      load16(p.norm_w + 16 * i, w);
+      widen16(w, g);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[c][j] = v[c][j] * inv * g[j];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int i = t + c * step;
+    const uint32_t m = max8(i < pieces ? max16(v[c]) : 0u);
+    if (i >= pieces) continue;
+    float s, r;
+    scale_of(m, &s, &r);
+    *reinterpret_cast<uint4*>(p.q + static_cast<size_t>(row) * p.cols + 16 * i) =
+        codes16(v[c], r);
+    if ((i & 7) == 0) p.scale[static_cast<size_t>(i >> 3) * p.rows + row] = s;
+  }
+}
+
+// --------------------------------------------------------------------------------------------
+// rows: h = silu(gate) * up
+// --------------------------------------------------------------------------------------------
+struct SiluParams {
+  const uint16_t* x;
+  uint8_t* q;
+  float* scale;
+  long long x_pitch;
+  int rows, cols, blocks;
+};
+
+constexpr int kSiluThreads = 256;
+
+// 8 lanes to a block of 128 columns.
+__global__ void __launch_bounds__(kSiluThreads) silu_rows_kernel(const SiluParams p) {
+  const long long unit = (static_cast<long long>(blockIdx.x) * kSiluThreads + threadIdx.x) >> 3;
+  const long long row = unit / p.blocks;
+  const int b = static_cast<int>(unit - row * p.blocks);
+  const int col = b * kBlockK + (threadIdx.x & 7) * 16;
+  griddep_wait();
+  const bool live = row < p.rows && col < p.cols;
+  uint4 g4[2] = {}, u4[2] = {};
+  if (live) {
+    const uint16_t* src = p.x + row * p.x_pitch + col;
+    load16(src, g4);
+    load16(src + p.cols, u4);
+  }
+  float g[16], u[16];
+  widen16(g4, g);
+  widen16(u4, u);
+  // (an exponential past the largest number leaves -0)
+#pragma unroll
+  for (int j = 0; j < 16; ++j) u[j] *= __fdividef(g[j], 1.f + __expf(-g[j]));
+  const uint32_t m = max8(max16(u));
+  if (!live) return;
+  float s, r;
+  scale_of(m, &s, &r);
+  *reinterpret_cast<uint4*>(p.q + row * p.cols + col) = codes16(u, r);
+  if ((threadIdx.x & 7) == 0) p.scale[static_cast<size_t>(b) * p.rows + row] = s;
+}
+
+// --------------------------------------------------------------------------------------------
+// weights
+// --------------------------------------------------------------------------------------------
+struct WeightParams {
+  const uint16_t* w;
+  uint8_t* q;
+  float* scale;
+  int n, k, n_blocks, k_blocks;
+};
+
+constexpr int kWeightThreads = 256;
+
+// A CTA to a block of 128 x 128, 64 elements to a thread.
+__global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightParams p) {
+  __shared__ uint32_t part[kWeightThreads / 32];
+  const int t = threadIdx.x;
+  const int kb = blockIdx.x % p.k_blocks, rest = blockIdx.x / p.k_blocks;
+  const int nb = rest % p.n_blocks, g = rest / p.n_blocks;
+  const int col = kb * kBlockK + (t & 7) * 16;
+  const size_t base = static_cast<size_t>(g) * p.n * p.k + col;
+  griddep_wait();
+  uint4 x[4][2];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = nb * kBlockK + (t >> 3) + 32 * i;
+    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+    if (row < p.n && col < p.k) load16(p.w + base + static_cast<size_t>(row) * p.k, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[16];
+    widen16(x[i], v);
+    m = max(m, max16(v));
+  }
+  m = warp_max_u32(m);
+  if ((t & 31) == 0) part[t >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWeightThreads / 32; ++i) m = max(m, part[i]);
+  float s, r;
+  scale_of(m, &s, &r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = nb * kBlockK + (t >> 3) + 32 * i;
+    if (row >= p.n || col >= p.k) continue;
+    float v[16];
+    widen16(x[i], v);
+    *reinterpret_cast<uint4*>(p.q + base + static_cast<size_t>(row) * p.k) = codes16(v, r);
+  }
+  if (t == 0) p.scale[blockIdx.x] = s;
+}
+
+constexpr int kMaxCols = 32768;   // of dflash_fp8_norm_rows: 512 threads x 4 pieces of 16
+
+template <int kChunks>
+int launch_norm(const NormParams& p, cudaStream_t st) {
+  const int lanes = (p.cols / 16 + kChunks - 1) / kChunks;
+  return launch(norm_rows_kernel<kChunks, false>, dim3(p.rows), dim3((lanes + 31) / 32 * 32), 0,
+                st, p);
+}
+
+bool bad_pitch(long long pitch, long long least) { return pitch < least; }
+
+}  // namespace
+}  // namespace fp8
+}  // namespace dflash
+
+using namespace dflash;
+using namespace dflash::fp8;
+
+extern "C" int dflash_fp8_norm_rows(int32_t rows, int32_t cols, const void* x, int64_t x_pitch,
+                                    const void* residual, int64_t residual_pitch,
+                                    const void* norm_w, float rms_eps, void* sum_out,
+                                    int64_t sum_pitch, void* q, float* scale,
+                                    dflash_stream_t stream) {
+  DFLASH_ENTRY("dflash_fp8_norm_rows");
+  if (rows < 0 || cols < 1 || !(rms_eps >= 0.f) || std::isinf(rms_eps)) return DFLASH_E_ARG;
+  if (cols % 16 || cols > kMaxCols) return DFLASH_E_UNSUPPORTED;
+  if (rows == 0) return DFLASH_OK;
+  if (!x || !q || !scale) return DFLASH_E_ARG;
+  if (bad_pitch(x_pitch, cols) || (residual && bad_pitch(residual_pitch, cols)) ||
+      (sum_out && bad_pitch(sum_pitch, cols)))
+    return DFLASH_E_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(norm_w) || !aligned16(sum_out) ||
+      !aligned16(q) || x_pitch % 8 || (residual && residual_pitch % 8) ||
+      (sum_out && sum_pitch % 8) || reinterpret_cast<uintptr_t>(scale) % 4)
+    return DFLASH_E_ALIGN;
+  NormParams p = {};
+  p.x = static_cast<const uint16_t*>(x);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.norm_w = static_cast<const uint16_t*>(norm_w);
+  p.sum = static_cast<uint16_t*>(sum_out);
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  p.x_pitch = x_pitch;
+  p.residual_pitch = residual_pitch;
+  p.sum_pitch = sum_pitch;
+  p.rows = rows;
+  p.cols = cols;
+  p.eps = rms_eps;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (cols <= 16 * 32)
+    return launch(norm_rows_kernel<1, true>, dim3((rows + kWarpRows - 1) / kWarpRows),
+                  dim3(32, kWarpRows), 0, st, p);
+  if (cols <= 16 * 512) return launch_norm<1>(p, st);
+  if (cols <= 16 * 1024) return launch_norm<2>(p, st);
+  return launch_norm<4>(p, st);
+}
+
+extern "C" int dflash_fp8_silu_mul(int32_t rows, int32_t cols, const void* gate_up,
+                                   int64_t pitch, void* q, float* scale, dflash_stream_t stream) {
+  DFLASH_ENTRY("dflash_fp8_silu_mul");
+  if (rows < 0 || cols < 1) return DFLASH_E_ARG;
+  if (cols % 16) return DFLASH_E_UNSUPPORTED;
+  if (rows == 0) return DFLASH_OK;
+  if (!gate_up || !q || !scale || bad_pitch(pitch, 2ll * cols)) return DFLASH_E_ARG;
+  if (!aligned16(gate_up) || !aligned16(q) || pitch % 8 || reinterpret_cast<uintptr_t>(scale) % 4)
+    return DFLASH_E_ALIGN;
+  SiluParams p = {};
+  p.x = static_cast<const uint16_t*>(gate_up);
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  p.x_pitch = pitch;
+  p.rows = rows;
+  p.cols = cols;
+  p.blocks = static_cast<int>(blocks(cols));
+  const long long threads = 8ll * rows * p.blocks;
+  const long long grid = (threads + kSiluThreads - 1) / kSiluThreads;
+  if (grid > 0x7FFFFFFFll) return DFLASH_E_UNSUPPORTED;
+  return launch(silu_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(kSiluThreads), 0,
+                reinterpret_cast<cudaStream_t>(stream), p);
+}
+
+extern "C" int dflash_fp8_weight(int32_t n_groups, int32_t n_out, int32_t n_in, const void* w,
+                                 void* q, float* scale, dflash_stream_t stream) {
+  DFLASH_ENTRY("dflash_fp8_weight");
+  if (n_groups < 1 || n_out < 1 || n_in < 1 || !w || !q || !scale) return DFLASH_E_ARG;
+  if (n_in % 16) return DFLASH_E_UNSUPPORTED;
+  if (!aligned16(w) || !aligned16(q) || reinterpret_cast<uintptr_t>(scale) % 4)
+    return DFLASH_E_ALIGN;
+  WeightParams p = {};
+  p.w = static_cast<const uint16_t*>(w);
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  p.n = n_out;
+  p.k = n_in;
+  p.n_blocks = static_cast<int>(blocks(n_out));
+  p.k_blocks = static_cast<int>(blocks(n_in));
+  // (in double: three factors of 31 bits pass 64)
+  if (static_cast<double>(n_groups) * p.n_blocks * p.k_blocks > 2147483647.0)
+    return DFLASH_E_UNSUPPORTED;
+  const long long grid = static_cast<long long>(n_groups) * p.n_blocks * p.k_blocks;
+  return launch(weight_kernel, dim3(static_cast<unsigned>(grid)), dim3(kWeightThreads), 0,
+                reinterpret_cast<cudaStream_t>(stream), p);
+}

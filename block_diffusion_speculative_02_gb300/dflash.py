@@ -42,7 +42,9 @@ EXPORTED = ["dflash_workspace_bytes", "dflash_workspace_init", "dflash_ctx_proje
             "dflash_prefill_workspace_bytes", "dflash_ctx_prefill", "dflash_selftest_wait",
             "dflash_prefill_attention", "dflash_prefill_staged",
             "dflash_kv4_workspace_bytes", "dflash_kv_reserve", "dflash_qk_norm_rope",
-            "dflash_kv4_append", "dflash_kv4_gather", "dflash_kv4_attention"]
+            "dflash_kv4_append", "dflash_kv4_gather", "dflash_kv4_attention",
+            "dflash_fp8_norm_rows", "dflash_fp8_silu_mul", "dflash_fp8_weight",
+            "dflash_fp8_linear", "dflash_fp8_grouped"]
 
 
 class DFlashError(RuntimeError):
@@ -159,6 +161,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_kv4_gather.argtypes = [dims4, vp, view4, vp, vp, vp, sz, vp]
     lib.dflash_kv4_attention.restype = ctypes.c_int
     lib.dflash_kv4_attention.argtypes = [dims4, vp, vp, view4, f32, ctypes.c_int, vp, vp, sz, vp]
+    lib.dflash_fp8_norm_rows.restype = ctypes.c_int
+    lib.dflash_fp8_norm_rows.argtypes = [i32, i32, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, vp]
+    lib.dflash_fp8_silu_mul.restype = ctypes.c_int
+    lib.dflash_fp8_silu_mul.argtypes = [i32, i32, vp, i64, vp, vp, vp]
+    lib.dflash_fp8_weight.restype = ctypes.c_int
+    lib.dflash_fp8_weight.argtypes = [i32, i32, i32, vp, vp, vp, vp]
+    lib.dflash_fp8_linear.restype = ctypes.c_int
+    lib.dflash_fp8_linear.argtypes = [i32] * 3 + [vp] * 5 + [i64, vp, sz, vp]
+    lib.dflash_fp8_grouped.restype = ctypes.c_int
+    lib.dflash_fp8_grouped.argtypes = [i32] * 5 + [vp] * 7 + [i64, vp, sz, vp]
     lib.dflash_cycle_sm_split.restype = ctypes.c_int
     lib.dflash_cycle_sm_split.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(i32),
                                           ctypes.POINTER(i32)]
@@ -687,3 +699,150 @@ def dflash_kv4_attention(dims: KV4Dims, q, start, cache: KV4View, scale: float, 
         _on(out, dev, bf, size, "out"), *_ws_on(ws, dev), st)
     if rc:
         _check(rc, "dflash_kv4_attention")
+
+
+# ---------------------------------------------------------------------------
+# linear layers in 8-bit floating point
+# ---------------------------------------------------------------------------
+F8 = torch.float8_e4m3fn
+
+
+def _up128(n: int) -> int:
+    return -(-n // 128)
+
+
+def alloc_fp8_workspace(device="cuda") -> torch.Tensor:
+    """A zeroed workspace for dflash_fp8_linear and dflash_fp8_grouped (their status word)."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def alloc_fp8_rows(rows: int, cols: int, device="cuda"):
+    """(codes e4m3 [rows, cols], scales fp32 [ceil(cols / 128), rows])."""
+    return (torch.empty(rows, cols, dtype=F8, device=device),
+            torch.empty(_up128(cols), rows, dtype=torch.float32, device=device))
+
+
+def alloc_fp8_weight(*shape, device="cuda"):
+    """(codes e4m3 [.., N, K], scales fp32 [.., ceil(N / 128), ceil(K / 128)])."""
+    *g, n, k = shape
+    return (torch.empty(*g, n, k, dtype=F8, device=device),
+            torch.empty(*g, _up128(n), _up128(k), dtype=torch.float32, device=device))
+
+
+def _whole(t, device: int, dtype, shape, name: str) -> int:
+    """Pointer of a contiguous tensor of this type and shape on this device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device \
+            or not t.is_contiguous():
+        _bad(t, device, dtype, None, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _matrix(t, device: int, name: str, shape=None):
+    """(pointer, row pitch) of a bf16 matrix whose rows are contiguous and may lie apart."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 \
+            or t.get_device() != device or t.dim() != 2:
+        raise ValueError(f"{name} must be a bf16 matrix on cuda:{device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the columns of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _matrix_opt(t, device: int, name: str, shape):
+    return (None, 0) if t is None else _matrix(t, device, name, shape)
+
+
+def dflash_fp8_norm_rows(x, residual, norm_w, rms_eps: float, sum_out, q, scale, stream=None):
+    """q, scale = 8-bit rows of RMSNorm(x + residual) * norm_w; sum_out = x + residual.
+
+    ``residual``, ``norm_w`` and ``sum_out`` may be None: nothing added, not normed, not stored."""
+    dev, st = _here(stream)
+    px = _matrix(x, dev, "x")
+    rows, cols = x.shape
+    rc = load_library().dflash_fp8_norm_rows(
+        rows, cols, *px, *_matrix_opt(residual, dev, "residual", (rows, cols)),
+        None if norm_w is None else _whole(norm_w, dev, torch.bfloat16, (cols,), "norm_w"),
+        rms_eps, *_matrix_opt(sum_out, dev, "sum_out", (rows, cols)),
+        _whole(q, dev, F8, (rows, cols), "q"),
+        _whole(scale, dev, torch.float32, (_up128(cols), rows), "scale"), st)
+    if rc:
+        _check(rc, "dflash_fp8_norm_rows")
+
+
+def dflash_fp8_silu_mul(gate_up, q, scale, stream=None):
+    """q, scale = 8-bit rows of silu(gate) * up, gate_up [M, 2 F]: gate, then up."""
+    dev, st = _here(stream)
+    px = _matrix(gate_up, dev, "gate_up")
+    rows, cols = gate_up.shape
+    if cols % 2:
+        raise ValueError("gate_up must have an even number of columns: gate, then up")
+    cols //= 2
+    rc = load_library().dflash_fp8_silu_mul(
+        rows, cols, *px, _whole(q, dev, F8, (rows, cols), "q"),
+        _whole(scale, dev, torch.float32, (_up128(cols), rows), "scale"), st)
+    if rc:
+        _check(rc, "dflash_fp8_silu_mul")
+
+
+def dflash_fp8_weight(w, q, scale, stream=None):
+    """q, scale = 8-bit weights of w, bf16 [N, K] or, of several experts, [G, N, K]."""
+    dev, st = _here(stream)
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be a tensor [N, K] or [G, N, K]")
+    *g, n, k = w.shape
+    rc = load_library().dflash_fp8_weight(
+        g[0] if g else 1, n, k, _whole(w, dev, torch.bfloat16, w.shape, "w"),
+        _whole(q, dev, F8, w.shape, "q"),
+        _whole(scale, dev, torch.float32, (*g, _up128(n), _up128(k)), "scale"), st)
+    if rc:
+        _check(rc, "dflash_fp8_weight")
+
+
+def _x_and_w(x, w, dims: int):
+    for t, name, d in ((x, "x", 2), (w, "w", dims)):
+        if not isinstance(t, torch.Tensor) or t.dim() != d:
+            raise ValueError(f"{name} must be a tensor of {d} dimensions")
+    if x.shape[1] != w.shape[-1]:
+        raise ValueError(f"x has {x.shape[1]} columns, w {w.shape[-1]}")
+
+
+def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
+    """out [M, N] (bf16, rows may be strided) = x w^T of 8-bit rows x [M, K] and weights w [N, K]."""
+    dev, st = _here(stream)
+    _x_and_w(x, w, 2)
+    (m, k), n = x.shape, w.shape[0]
+    rc = load_library().dflash_fp8_linear(
+        m, n, k, _whole(x, dev, F8, (m, k), "x"),
+        _whole(x_scale, dev, torch.float32, (_up128(k), m), "x_scale"),
+        _whole(w, dev, F8, (n, k), "w"),
+        _whole(w_scale, dev, torch.float32, (_up128(n), _up128(k)), "w_scale"),
+        *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
+    if rc:
+        _check(rc, "dflash_fp8_linear")
+
+
+def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None):
+    """Rows start[e] .. start[e + 1] - 1 of out = x w[e]^T, w [E, N, K]; ``rows``: int32 [len(out)],
+    the row of x that each row of out is made of, or None: the same row."""
+    dev, st = _here(stream)
+    _x_and_w(x, w, 3)
+    (src, k), (e, n, _) = x.shape, w.shape
+    if not isinstance(out, torch.Tensor) or out.dim() != 2:
+        raise ValueError("out must be a matrix")
+    m = out.shape[0]
+    if rows is None and m != src:
+        raise ValueError(f"out has {m} rows, x {src}: rows must say which")
+    rc = load_library().dflash_fp8_grouped(
+        m, src, e, n, k, _whole(x, dev, F8, (src, k), "x"),
+        _whole(x_scale, dev, torch.float32, (_up128(k), src), "x_scale"),
+        _whole(w, dev, F8, (e, n, k), "w"),
+        _whole(w_scale, dev, torch.float32, (e, _up128(n), _up128(k)), "w_scale"),
+        _whole(start, dev, torch.int32, (e + 1,), "start"),
+        None if rows is None else _whole(rows, dev, torch.int32, (m,), "rows"),
+        *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
+    if rc:
+        _check(rc, "dflash_fp8_grouped")

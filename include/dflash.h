@@ -587,6 +587,91 @@ DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
                                     float scale, int causal, void* out, void* ws,
                                     size_t ws_bytes, dflash_stream_t stream);
 
+/*
+ * Linear layers in 8-bit floating point: the products around the attention of a
+ * target whose weights are held in 8 bits ([P2] 单次前向验证 ① and ⑤: the prompt's
+ * chunks and the verify forward go through the target's layers).
+ *   dflash_fp8_norm_rows  residual added, RMS norm, rows in 8 bits (or only the last)
+ *   dflash_fp8_linear     rows times weights
+ *   dflash_fp8_silu_mul   an MLP's silu(gate) * up, in 8 bits
+ *   dflash_fp8_grouped    rows times the weights of the expert that each belongs to
+ *   dflash_fp8_weight     bf16 weights to 8 bits, once
+ * A value is scale * code, the code e4m3 (sign, 4 exponent bits, 3 of mantissa, up to
+ * 448, no infinities), the scale fp32, one for each block of 128:
+ *   rows    [M, K]: 128 columns of a row;  scales [ceil(K / 128)][M]
+ *   weights [N, K]: 128 x 128;             scales [ceil(N / 128)][ceil(K / 128)]
+ * The last block of a row or column may be short.  K is a multiple of 16, everything is
+ * contiguous but for the row pitches given (in elements).  Rounding a block whose largest
+ * magnitude is a (counted as 2^-117 if it is less): scale = a / 448, code =
+ * e4m3(h * (448 / a)), to nearest, ties to even; an infinity or NaN among them makes scale
+ * and codes of the whole block NaN.
+ * No rows (M = 0) is a call that does nothing.  The calls keep nothing between them; the
+ * workspace of the products (64 bytes, zeroed once) is their status word only, and calls on
+ * several streams may share it.
+ */
+
+/*
+ * dflash_fp8_norm_rows — s = x + residual;  sum_out = s;
+ *   h = s / sqrt(mean(s^2) + rms_eps) * norm_w;  (q, scale) = h in 8 bits
+ * in fp32, s not rounded on the way to h.  residual NULL: s = x.  norm_w NULL: h = s (rows
+ * rounded as they are, e.g. an attention's output).  sum_out NULL: not stored.
+ *   x, residual, sum_out: bf16 [rows, cols], pitches a multiple of 8 and at least cols;
+ *   sum_out may be x or residual themselves (same pitch), else overlaps nothing;
+ *   norm_w: bf16 [cols]; q: [rows, cols]; cols a multiple of 16, at most 32768.
+ */
+DFLASH_API int dflash_fp8_norm_rows(int32_t rows, int32_t cols, const void* x, int64_t x_pitch,
+                                    const void* residual, int64_t residual_pitch,
+                                    const void* norm_w, float rms_eps, void* sum_out,
+                                    int64_t sum_pitch, void* q, float* scale,
+                                    dflash_stream_t stream);
+
+/*
+ * dflash_fp8_silu_mul — h = g / (1 + exp(-g)) * u in fp32, (q, scale) = h in 8 bits.
+ *   gate_up: bf16 [rows, 2 cols], g the first cols columns, u the others; pitch a multiple
+ *   of 8, at least 2 cols; q: [rows, cols]; cols a multiple of 16.
+ */
+DFLASH_API int dflash_fp8_silu_mul(int32_t rows, int32_t cols, const void* gate_up,
+                                   int64_t pitch, void* q, float* scale, dflash_stream_t stream);
+
+/*
+ * dflash_fp8_weight — weights w, bf16 [n_groups, n_out, n_in], in 8 bits: q of the same
+ * shape, scale [n_groups][ceil(n_out / 128)][ceil(n_in / 128)].
+ */
+DFLASH_API int dflash_fp8_weight(int32_t n_groups, int32_t n_out, int32_t n_in, const void* w,
+                                 void* q, float* scale, dflash_stream_t stream);
+
+/*
+ * dflash_fp8_linear — out = x w^T:
+ *   out[m, n] = sum_b x_scale[b, m] w_scale[n / 128, b] sum_{k in block b} x[m, k] w[n, k]
+ * with fp32 sums, block by block, and one rounding to bf16.  The product of any two scales
+ * that meet must be a finite fp32 number.
+ *   x: [rows, n_in]; w: [n_out, n_in]; out: bf16 [rows, n_out], rows out_pitch >= n_out
+ *   elements apart (fastest where the pitch is a multiple of 8 and out 16-byte aligned).
+ * DFLASH_ST_TIMEOUT is the only bit that it can set.
+ */
+DFLASH_API int dflash_fp8_linear(int32_t rows, int32_t n_out, int32_t n_in, const void* x,
+                                 const float* x_scale, const void* w, const float* w_scale,
+                                 void* out, int64_t out_pitch, void* ws, size_t ws_bytes,
+                                 dflash_stream_t stream);
+
+/*
+ * dflash_fp8_grouped — rows start[e] .. start[e + 1] - 1 of out are rows of x times the
+ * weights of expert e (of none where start[e] = start[e + 1]).
+ *   w: [n_groups, n_out, n_in], w_scale likewise; start: int32 [n_groups + 1] on the
+ *   device, not decreasing; out: bf16 [n_rows, n_out]; n_groups at most 1024.
+ *   rows: int32 [n_rows] or NULL: row n of out is made of row rows[n] of x, [n_src, n_in]
+ *   (a token that goes to several experts is not copied).  NULL: of row n, n_src = n_rows.
+ * Rows of out before start[0] and from start[n_groups] on are left as they were.  A group
+ * whose rows do not lie in 0 .. n_rows (start decreasing or past n_rows) sets
+ * DFLASH_ST_CAPACITY and is left out; a rows[n] outside 0 .. n_src - 1 sets it too and stands for
+ * a row of zeros.
+ */
+DFLASH_API int dflash_fp8_grouped(int32_t n_rows, int32_t n_src, int32_t n_groups, int32_t n_out,
+                                  int32_t n_in, const void* x, const float* x_scale,
+                                  const void* w, const float* w_scale, const int32_t* start,
+                                  const int32_t* rows, void* out, int64_t out_pitch, void* ws,
+                                  size_t ws_bytes, dflash_stream_t stream);
+
 /* Copy the status word to *host_status (synchronises `stream`); if clear != 0
  * reset it to zero afterwards. */
 DFLASH_API int dflash_read_status(void* ws, uint32_t* host_status, int clear, dflash_stream_t stream);
@@ -603,7 +688,7 @@ DFLASH_API const char* dflash_status_string(int code);
  */
 DFLASH_API int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes, dflash_stream_t stream);
 
-/* Library ABI version (major * 100 + minor): 109. */
+/* Library ABI version (major * 100 + minor): 110. */
 DFLASH_API int dflash_version(void);
 
 #ifdef __cplusplus
