@@ -19,7 +19,28 @@ namespace dflash {
 namespace fp8 {
 namespace {
 
+using kv4::elect_one;
 using kv4::wait_on;
+
+// Both barriers' phases, tried together first: one after the other each try costs the warp
+// that issues the products some 130 clocks.
+__device__ __forceinline__ bool wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                          uint32_t* status) {
+  uint32_t ok;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  ok = wait_on(a, pa, status) && wait_on(b, pb, status);
+  return __all_sync(0xffffffffu, ok);
+}
 
 constexpr int kMaxGroups = 1024;
 
@@ -46,79 +67,179 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+template <bool kPair = false>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+#define DFLASH_MMA(group)                                                              \
+  asm volatile(                                                                        \
+      "{\n\t.reg .pred p;\n\t"                                                     \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                    \
+      "tcgen05.mma." group ".kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),    \
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)                                      \
+      : "memory")
+  if (kPair)
+    DFLASH_MMA("cta_group::2");
+  else
+    DFLASH_MMA("cta_group::1");
+#undef DFLASH_MMA
+}
+
+// Arrive on `bar`, of a pair in both CTAs, once the products issued so far are done.
+template <bool kPair>
+__device__ __forceinline__ void mma_done(uint64_t* bar) {
+  if (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+
+// Likewise, in this CTA only.
+template <bool kPair>
+__device__ __forceinline__ void mma_done_here(uint64_t* bar) {
+  if (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+  else
+    umma_commit(bar);
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_take(uint32_t* slot, uint32_t cols) {
+  if (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(slot, cols);
+    tmem_relinquish();
+  }
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tmem_give(uint32_t taddr, uint32_t cols) {
+  if (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+                 : "memory");
+  else
+    tmem_dealloc(taddr, cols);
+}
+
+// Copy four bytes (size 0: write a zero).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t size) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(size)
+               : "memory");
+}
+
+// Arrive at a named barrier of n threads without waiting at it.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// The barrier of this name in the first CTA of a pair (a single CTA: its own).
+template <bool kPair>
+__device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
+  uint32_t a = smem_u32(bar);
+  if (kPair) asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+
+template <bool kPair>
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  if (kPair)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 2-D tiled load whose bytes count at a barrier of either CTA of a pair.
+template <bool kPair>
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                        int c1, uint64_t policy) {
+#define DFLASH_LOAD(group)                                                                    \
+  asm volatile(                                                                               \
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes" group \
+      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),                 \
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "l"(policy)                                       \
+      : "memory")
+  if (kPair)
+    DFLASH_LOAD(".cta_group::2");
+  else
+    DFLASH_LOAD("");
+#undef DFLASH_LOAD
 }
 
 // Four rows of a map whose box is one row high, one below the other in shared memory.  A row
 // past the map's end reads as zeros.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
+template <bool kPair>
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int r0, int r1, int r2, int r3,
                                             uint64_t policy) {
+#define DFLASH_LOAD(group)                                                                     \
+  asm volatile(                                                                                \
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes" \
+      group ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)), \
+      "l"(map), "r"(bar), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "l"(policy)             \
+      : "memory")
+  if (kPair)
+    DFLASH_LOAD(".cta_group::2");
+  else
+    DFLASH_LOAD("");
+#undef DFLASH_LOAD
+}
+
+// 32 TMEM lanes x 16 columns of fp32; thread i gets lane (base + i), two columns to a word.
+// The load, the wait for it and the pairs are one statement, so that the pairs are made where
+// the load puts them (apart, the compiler moved every value twice).
+__device__ __forceinline__ void tmem_pairs(uint32_t taddr, uint64_t (&d)[8]) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "l"(policy)
+      "{\n\t.reg .b32 r<16>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {r0, r1};\n\tmov.b64 %1, {r2, r3};\n\t"
+      "mov.b64 %2, {r4, r5};\n\tmov.b64 %3, {r6, r7};\n\t"
+      "mov.b64 %4, {r8, r9};\n\tmov.b64 %5, {r10, r11};\n\t"
+      "mov.b64 %6, {r12, r13};\n\tmov.b64 %7, {r14, r15};\n\t}\n"
+      : "=l"(d[0]), "=l"(d[1]), "=l"(d[2]), "=l"(d[3]), "=l"(d[4]), "=l"(d[5]), "=l"(d[6]),
+        "=l"(d[7])
+      : "r"(taddr)
       : "memory");
 }
 
-// 32 TMEM lanes x 32 columns; thread i gets lane (base + i).  The registers hold the values
-// after tmem_wait32 on them.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 halves(uint64_t d) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+  return f;
 }
 
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-  asm volatile(""
-               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
-                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
+// a += f * t, both halves.
+__device__ __forceinline__ void fma_pair(uint64_t& a, uint64_t t, uint64_t f) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(t), "l"(f));
 }
 
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
+// What is the same all over the warp anyway, so that the compiler sees it and keeps what is
+// made of it in uniform registers: where it does not, an instruction of the tensor cores or of
+// the copies costs some 150 clocks to issue (measured), and a block of K takes ten.
+__device__ __forceinline__ int same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool all(bool x) { return __all_sync(0xffffffffu, x); }
 
-// acc += f * t, pairwise (one instruction for two).
-__device__ __forceinline__ void add_scaled(float2* acc, const uint32_t (&t)[32], float f) {
-  const float2 ff = make_float2(f, f);
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    acc[i] = __ffma2_rn(make_float2(__uint_as_float(t[2 * i]), __uint_as_float(t[2 * i + 1])), ff,
-                        acc[i]);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return static_cast<uint32_t>(float_to_bf16_bits(lo)) |
-         static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16;
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t d) {
+  const float2 f = halves(d);
+  return static_cast<uint32_t>(float_to_bf16_bits(f.x)) |
+         static_cast<uint32_t>(float_to_bf16_bits(f.y)) << 16;
 }
 
 // --------------------------------------------------------------------------------------------
@@ -217,102 +338,116 @@ __device__ __forceinline__ void rows_of(const Linear& p, const Tile& tile, int a
 }
 
 // --------------------------------------------------------------------------------------------
-// tiles of 128 rows x kN features
+// tiles of 128 rows (or, of a pair of CTAs, 256) x kN features
 // --------------------------------------------------------------------------------------------
+// One thread issues the products, of a pair (kPair) for both SMs: each holds 128 rows of x and half
+// of the features' weights, and gets the sums of its own rows.  Per block of K a pair of SMs moves
+// and reads half as many bytes of weights as two single ones.
+//
+// A block's sums leave TMEM in the time of the next block's products (512 cycles at 256
+// features): 16 warps take a quarter of the features of 32 rows each, so that four warps of
+// a scheduler cover each other's waits.  (8 warps with twice the features each left the tensor
+// cores idle 60 % of the time.)  They wait at named barriers, where a warp takes no turn: one more
+// warp watches the accumulators' mbarriers for them.  (With all of them trying an mbarrier, a
+// try took the warps that issue the products 400 clocks and more.)
 constexpr int kTileRows = 128;
-constexpr int kTileWarps = 12;        // copies, products, two idle, 8 epilogue warps
-constexpr int kEpiWarp = 4;           // the first epilogue warp
-// Registers a thread: 168 at the start; the accumulators' warps take from the others, within
-// the block's 384 x 168.
-constexpr int kRegsStart = 168, kRegsRest = 72, kRegsEpi = 216;
-static_assert(kEpiWarp * kRegsRest + 8 * kRegsEpi <= kTileWarps * kRegsStart, "register split");
-constexpr int kStoreBytes = 8 * 4096; // 32 rows x 64 features of each epilogue warp
+constexpr int kTileWarps = 20;        // copies, products, watch, products, 16 epilogue warps
+constexpr int kEpiWarp = 4, kEpiWarps = 16;
+// Registers a thread: 96 at the start; the epilogue's warps take from the others, within the
+// block's 640 x 96.
+constexpr int kRegsStart = 96, kRegsRest = 64, kRegsEpi = 104;
+static_assert(kEpiWarp * kRegsRest + kEpiWarps * kRegsEpi <= kTileWarps * kRegsStart,
+              "register split");
+constexpr int kStoreBytes = kEpiWarps * 2048;   // 32 rows x 32 features of each epilogue warp
+constexpr int kRing = 8;                        // blocks whose scales are in shared memory
+constexpr int kScaleRow = kTileRows + 2;        // of the rows, then of the weights
 constexpr int kSmemLimit = 227 * 1024;
 
-template <int kN>
+template <bool kPair, int kN>
 __host__ __device__ constexpr int tile_stage_bytes() {
-  return (kTileRows + kN) * kBlockK;
+  return (kTileRows + kN / (kPair ? 2 : 1)) * kBlockK;
 }
 
-// A lane of a warp's tile: 64 features of 32 rows go through shared memory, so that a row's
+// 32 features of 32 rows, one row to a lane, go through shared memory, so that a row's
 // features leave side by side.
-__device__ __forceinline__ void store_rows(const Linear& p, const float2* acc, uint8_t* buf,
+__device__ __forceinline__ void store_rows(const Linear& p, const uint64_t* acc, uint8_t* buf,
                                            int row, int rows_left, int col, int lane) {
+  const auto at = [&](int r, int c) { return buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const float2* a = acc + 4 * c;
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-        make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y),
-                   pack_bf16(a[2].x, a[2].y), pack_bf16(a[3].x, a[3].y));
+  for (int c = 0; c < 4; ++c) {
+    *reinterpret_cast<uint4*>(at(lane, c)) =
+        make_uint4(pack_bf16(acc[4 * c]), pack_bf16(acc[4 * c + 1]), pack_bf16(acc[4 * c + 2]),
+                   pack_bf16(acc[4 * c + 3]));
   }
   __syncwarp();
   const int most = min(32, rows_left);
-  if (p.vector && col + 64 <= p.n) {
-    const int c = lane & 7;
+  if (p.vector && col + 32 <= p.n) {
+    const int c = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      const uint4 v = *reinterpret_cast<const uint4*>(at(r, c));
       if (r < most)
         *reinterpret_cast<uint4*>(p.out + static_cast<long long>(row + r) * p.out_pitch + col +
                                   8 * c) = v;
     }
-  } else {
-    for (int r = 0; r < most; ++r) {
-      uint16_t* dst = p.out + static_cast<long long>(row + r) * p.out_pitch + col;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
-        if (col + j < p.n)
-          dst[j] = *reinterpret_cast<const uint16_t*>(buf + r * 128 +
-                                                      (((j >> 3) ^ (r & 7)) << 4) + (j & 7) * 2);
-      }
-    }
+  } else if (col + lane < p.n) {
+    for (int r = 0; r < most; ++r)
+      p.out[static_cast<long long>(row + r) * p.out_pitch + col + lane] =
+          *reinterpret_cast<const uint16_t*>(at(r, lane >> 3) + (lane & 7) * 2);
   }
   __syncwarp();
 }
 
-template <int kN>
+template <bool kPair, int kN>
 __global__ void __launch_bounds__(kTileWarps * 32, 1)
 tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
             const Linear p) {
-  constexpr int kStage = tile_stage_bytes<kN>();
-  constexpr int kHalf = kN / 2;          // features of an epilogue warp
-  constexpr int kCols = 2 * kN;          // TMEM columns: two accumulators
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kRows = kTileRows * kCtas;
+  constexpr int kStage = tile_stage_bytes<kPair, kN>();
+  constexpr int kHalf = kN / 2;          // features of a product
+  constexpr int kShare = kHalf / kCtas;  // of these, features whose weights this CTA holds
+  constexpr int kOwn = kN / 4;           // features of an epilogue warp
+  constexpr int kCols = 2 * kN;          // TMEM columns: two accumulators of each half
+  constexpr int kBlocksN = kN / kBlockK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* store = smem + p.n_stages * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(store + kStoreBytes);
+  float* scales = reinterpret_cast<float*>(store + kStoreBytes);   // [kRing][128 rows, weights]
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kRing * kScaleRow);
   uint64_t* empty = full + p.n_stages;
-  uint64_t* tfull = empty + p.n_stages;  // [2]
-  uint64_t* tempty = tfull + 2;          // [2]
-  uint64_t* mdrain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
+  uint64_t* tfull = empty + p.n_stages;  // [2 halves][2] accumulators are there
+  uint64_t* tempty = tfull + 4;          // [2 halves][2] read (of a pair: in the first CTA)
+  uint64_t* mdrain = tempty + 4;         // [2 halves]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 2);
   const Groups groups = groups_at(reinterpret_cast<uint8_t*>(tmem_slot + 1), p.groups);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.n_stages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);           // the products of both halves
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], kEpiWarps / 2 * kCtas);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 8);
+      mbar_init(&mdrain[i], 1);
     }
-    mbar_init(mdrain, 1);
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, kCols);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_take<kPair>(tmem_slot, kCols);
   griddep_wait();
-  if (warp == 2) fill_groups(p, groups, kTileRows, lane);
+  if (warp == 2) fill_groups(p, groups, kRows, lane);
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();             // the other CTA's barriers are there
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = same(*tmem_slot);
   const int total = groups.tiles[p.groups] * p.n_tiles;   // (below 2^31: the host)
   if (warp < kEpiWarp) kv4::regs_down<kRegsRest>();
 
@@ -321,24 +456,30 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     uint32_t stage = 0, phase = 0;
     int issued = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const Tile tile = tile_at<kTileRows>(p, groups, t);
+    for (int t = t_first; all(ok && t < total); t += t_step) {
+      const Tile tile = tile_at<kRows>(p, groups, t);
       int r[4] = {};
-      if (p.rows) rows_of(p, tile, lane * 4, r);
+      if (p.rows) rows_of(p, tile, rank * kTileRows + lane * 4, r);
+      const int x_row = same(tile.row) + rank * kTileRows;
+      const int w_row = same(tile.e * p.n + tile.n * kN) + rank * kShare;
+#pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b) {
-        ok = __all_sync(0xffffffffu, wait_on(&empty[stage], phase ^ 1, p.status));
+        ok = all(wait_on(&empty[stage], phase ^ 1, p.status));
         if (!ok) break;
         uint8_t* a = smem + stage * kStage;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[stage], kStage);
-          if (!p.rows) tma_load_2d(a, &map_x, &full[stage], b * kBlockK, tile.row, pol);
-          tma_load_2d(a + kTileRows * kBlockK, &map_w, &full[stage], b * kBlockK,
-                      tile.e * p.n + tile.n * kN, pol);
+        const uint32_t bar = first_cta<kPair>(&full[stage]);
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], kCtas * kStage);
+          if (!p.rows) tma_box<kPair>(a, &map_x, bar, b * kBlockK, x_row, pol);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tma_box<kPair>(a + (kTileRows + h * kShare) * kBlockK, &map_w, bar, b * kBlockK,
+                           w_row + h * kHalf, pol);
         }
         if (p.rows) {
           __syncwarp();
-          tma_gather4(a + lane * 4 * kBlockK, &map_x, &full[stage], b * kBlockK, r[0], r[1], r[2],
-                      r[3], pol);
+          tma_gather4<kPair>(a + lane * 4 * kBlockK, &map_x, bar, b * kBlockK, r[0], r[1], r[2],
+                             r[3], pol);
         }
         ++issued;
         if (++stage == static_cast<uint32_t>(p.n_stages)) {
@@ -347,117 +488,170 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         }
       }
     }
-    // no copy may still be landing when the CTA exits
+    // No copy may still be landing, and no product's arrival be on its way, when the CTA exits:
+    // every stage has been read.  (Given up: what the first CTA's barriers counted has landed.)
     if (lane == 0)
       for (int st = 0; st < p.n_stages && st < issued; ++st) {
         const int last = st + ((issued - 1 - st) / p.n_stages) * p.n_stages;
-        mbar_wait_drain(&full[st], static_cast<uint32_t>((last / p.n_stages) & 1), p.status);
+        if (!ok && rank) break;
+        if (!mbar_wait_drain(ok ? &empty[st] : &full[st],
+                             static_cast<uint32_t>((last / p.n_stages) & 1), p.status))
+          break;
       }
-  } else if (warp == 1) {
-    const uint32_t base = smem_u32(smem);
-    constexpr uint32_t idesc = idesc_e4m3(kTileRows, kN);
-    uint32_t stage = 0, phase = 0, it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      for (int b = 0; b < p.k_blocks; ++b, ++it) {
-        const uint32_t slot = it & 1;
-        // (the wait for a phase before the first passes at once)
-        ok = wait_on(&tempty[slot], ((it >> 1) & 1) ^ 1, p.status) &&
-             wait_on(&full[stage], phase, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t at = base + stage * kStage;
-          const uint64_t ad = umma_sdesc_sw128(at);
-          const uint64_t bd = umma_sdesc_sw128(at + kTileRows * kBlockK);
+  } else if (warp == 1 || warp == 3) {
+    if (rank == 0) {
+      // a warp to each half of the features
+      const int half = warp >> 1;
+      constexpr uint32_t idesc = idesc_e4m3(kRows, kHalf);
+      const uint64_t a_desc = umma_sdesc_sw128(smem_u32(smem));
+      const uint64_t b_desc =
+          umma_sdesc_sw128(smem_u32(smem) + (kTileRows + half * kShare) * kBlockK);
+      const uint32_t acc = tmem + half * 2 * kHalf;
+      uint64_t* done = tfull + 2 * half;
+      uint64_t* read = tempty + 2 * half;
+      uint32_t stage = 0, phase = 0, slot = 0, tphase = 0;
+      bool ok = true;
+      for (int t = t_first; all(ok && t < total); t += t_step) {
+#pragma unroll 1
+        for (int b = 0; b < p.k_blocks; ++b) {
+          // (the wait for a phase before the first passes at once)
+          ok = wait_both(&read[slot], tphase ^ 1, &full[stage], phase, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = a_desc + stage * (kStage >> 4), bd = b_desc + stage * (kStage >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_e4m3(tmem + slot * kN, ad + 2 * kk, bd + 2 * kk, idesc, kk ? 1u : 0u);
-          umma_commit(&empty[stage]);
-          umma_commit(&tfull[slot]);
-        }
-        __syncwarp();
-        if (++stage == static_cast<uint32_t>(p.n_stages)) {
-          stage = 0;
-          phase ^= 1;
+            for (int kk = 0; kk < 4; ++kk)
+              mma_e4m3<kPair>(acc + slot * kHalf, ad + 2 * kk, bd + 2 * kk, idesc, kk ? 1u : 0u);
+            mma_done<kPair>(&done[slot]);
+            mma_done<kPair>(&empty[stage]);
+          }
+          tphase ^= slot;
+          slot ^= 1;
+          if (++stage == static_cast<uint32_t>(p.n_stages)) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
+      if (elect_one()) mma_done_here<kPair>(&mdrain[half]);
+      if (lane == 0) mbar_wait_drain(&mdrain[half], 0, p.status);
     }
-    if (lane == 0) {
-      umma_commit(mdrain);
-      mbar_wait_drain(mdrain, 0, p.status);
-    }
-  } else if (warp >= kEpiWarp) {
-    kv4::regs_up<kRegsEpi>();
-    const int quad = warp & 3, half = (warp - kEpiWarp) >> 2;
-    uint8_t* buf = store + (warp - kEpiWarp) * 4096;
-    const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * kHalf;
+  } else if (warp < kEpiWarp) {
+    // Watches the accumulators for the epilogue and copies its scales, four rows to a lane,
+    // kAhead blocks ahead.  (That a block's accumulators are there says that those of two blocks
+    // before were read, their scales too: of the ring, kAhead + 2 are in use.)  Once a wait gave
+    // up, the rest are skipped: the epilogue goes through its blocks all the same.
+    constexpr int kAhead = 4;
+    static_assert(kAhead + 2 <= kRing, "scales in use");
+    int t = t_first, b = 0;
+    uint32_t at = 0;
+    const float* xs[4] = {p.xs, p.xs, p.xs, p.xs};
+    const float* ws = p.ws;
+    uint32_t x_size[4] = {}, w_size = 0;
+    auto open = [&] {                      // tile t
+      const Tile tile = tile_at<kRows>(p, groups, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = rank * kTileRows + lane + 32 * i;
+        int src = -1;
+        if (r < tile.count) src = p.rows ? p.rows[tile.row + r] : tile.row + r;
+        x_size[i] = src >= 0 && src < p.n_src ? 4 : 0;          // none: a zero
+        xs[i] = p.xs + (x_size[i] ? src : 0);
+      }
+      const int nb = tile.n * kBlocksN + lane;
+      w_size = lane < kBlocksN && nb < p.n_blocks ? 4 : 0;
+      ws = p.ws + (static_cast<long long>(tile.e) * p.n_blocks + (w_size ? nb : 0)) * p.k_blocks;
+    };
+    auto copy = [&] {                      // the scales of the next block
+      if (t < total) {
+        if (b == 0) open();
+        float* to = scales + (at % kRing) * kScaleRow;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cp_async4(to + lane + 32 * i, xs[i], x_size[i]);
+          xs[i] += p.n_src;
+        }
+        if (lane < kBlocksN) cp_async4(to + kTileRows + lane, ws + b, w_size);
+        ++at;
+        if (++b == p.k_blocks) {
+          b = 0;
+          t += t_step;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) copy();
+    bool ok = true;
     uint32_t it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const Tile tile = tile_at<kTileRows>(p, groups, t);
-      const int at = quad * 32 + lane;                        // this thread's row of the tile
-      const int col = tile.n * kN + half * kHalf;
-      int src = -1;
-      if (at < tile.count) src = p.rows ? p.rows[tile.row + at] : tile.row + at;
-      if (src >= p.n_src) src = -1;
-      const float* xs = p.xs + max(src, 0);
-      const float* ws = p.ws + (static_cast<long long>(tile.e) * p.n_blocks +
-                                min(col / kBlockK, p.n_blocks - 1)) * p.k_blocks;
-      float2 acc[kHalf / 2];
+    for (int u = t_first; all(u < total); u += t_step) {
+#pragma unroll 1
+      for (int i = 0; i < p.k_blocks; ++i, ++it) {
+        const uint32_t slot = it & 1;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      // the scales are read two blocks ahead
-      float x0 = 0.f, x1 = 0.f, w0 = 0.f, w1 = 0.f;
-      const bool there = src >= 0;
-      if (there) {
-        x0 = xs[0];
-        w0 = ws[0];
-        if (p.k_blocks > 1) {
-          x1 = xs[p.n_src];
-          w1 = ws[1];
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && all(wait_on(&tfull[2 * h + slot], (it >> 1) & 1, p.status));
+          tc_fence_after();
+          tc_fence_before();
+          named_bar_arrive(1 + 2 * h + slot, 32 * (kEpiWarps / 2 + 1));
         }
+        copy();
       }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else {
+    kv4::regs_up<kRegsEpi>();
+    const int quad = warp & 3, part = (warp - kEpiWarp) >> 2;
+    uint8_t* buf = store + (warp - kEpiWarp) * 2048;
+    const int half = part >> 1;
+    const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * kHalf +
+                          (part & 1) * kOwn;
+    const float* x_scale = scales + quad * 32 + lane;
+    const float* w_scale = scales + kTileRows + part * kOwn / kBlockK;
+    const uint32_t read = first_cta<kPair>(tempty + 2 * half);
+    uint32_t it = 0;
+    for (int t = t_first; t < total; t += t_step) {
+      uint64_t acc[kOwn / 2];
+#pragma unroll
+      for (int i = 0; i < kOwn / 2; ++i) acc[i] = 0;
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
-        const float f = x0 * w0;
-        x0 = x1;
-        w0 = w1;
-        if (there && b + 2 < p.k_blocks) {
-          x1 = xs[static_cast<long long>(b + 2) * p.n_src];
-          w1 = ws[b + 2];
-        }
         const uint32_t slot = it & 1;
-        ok = __all_sync(0xffffffffu, wait_on(&tfull[slot], (it >> 1) & 1, p.status));
-        if (!ok) break;
+        named_bar_sync(1 + 2 * half + slot, 32 * (kEpiWarps / 2 + 1));
         tc_fence_after();
-        const uint32_t ta = from + slot * kN;
-        uint32_t v[2][32];
-        tmem_ld32(ta, v[0]);
+        const uint32_t in_ring = it % kRing * kScaleRow;
+        const float f1 = x_scale[in_ring] * w_scale[in_ring];
+        const uint64_t f = pair_of(f1, f1);
+        const uint32_t ta = from + slot * kHalf;
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) {
-          tmem_wait32(v[c & 1]);
-          if (c + 1 < kHalf / 32) tmem_ld32(ta + 32 * (c + 1), v[(c + 1) & 1]);
-          if (c + 1 == kHalf / 32) {
+        for (int c = 0; c < kOwn; c += 16) {
+          uint64_t v[8];
+          tmem_pairs(ta + c, v);
+          if (c + 16 == kOwn) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[slot]);
+            if (lane == 0) arrive_at<kPair>(read + slot * 8);
           }
-          add_scaled(acc + 16 * c, v[c & 1], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fma_pair(acc[c / 2 + i], v[i], f);
         }
       }
-      if (!ok) break;
+      const Tile tile = tile_at<kRows>(p, groups, t);
+      const int at = rank * kTileRows + quad * 32;
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 64)
-        store_rows(p, acc + c / 2, buf, tile.row + quad * 32, tile.count - quad * 32, col + c,
-                   lane);
+      for (int c = 0; c < kOwn; c += 32)
+        store_rows(p, acc + c / 2, buf, tile.row + at, tile.count - at,
+                   tile.n * kN + part * kOwn + c, lane);
     }
   }
+  tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();             // neither leaves while the other's products use it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    tmem_give<kPair>(tmem, kCols);
   }
   griddep_launch_dependents();
 }
@@ -505,7 +699,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   uint64_t* mdrain = tempty + kStreamBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 1);
   const Groups groups = groups_at(reinterpret_cast<uint8_t*>(tmem_slot + 1), p.groups);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int b_first = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / split);
   const int b_last = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / split);
@@ -532,7 +726,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = same(*tmem_slot);
   const int total = groups.tiles[p.groups] * p.n_tiles;
 
   if (warp == 0) {
@@ -540,25 +734,27 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     uint32_t stage = 0, phase = 0;
     int issued = 0;
     bool ok = true;
-    for (int t = t_first; ok && t < total; t += t_step) {
+    for (int t = t_first; all(ok && t < total); t += t_step) {
       const Tile tile = tile_at<kT>(p, groups, t);
       int r[4] = {};
       if (p.rows && lane < kT / 4) rows_of(p, tile, lane * 4, r);
+      const int x_row = same(tile.row), w_row = same(tile.e * p.n + tile.n * 128);
+#pragma unroll 1
       for (int b = b_first; b < b_last; ++b) {
-        ok = __all_sync(0xffffffffu, wait_on(&empty[stage], phase ^ 1, p.status));
+        ok = all(wait_on(&empty[stage], phase ^ 1, p.status));
         if (!ok) break;
         uint8_t* a = smem + stage * kStage;
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[stage], kStage);
-          tma_load_2d(a, &map_w, &full[stage], b * kBlockK, tile.e * p.n + tile.n * 128, pol);
+          tma_load_2d(a, &map_w, &full[stage], b * kBlockK, w_row, pol);
           if (!p.rows)
-            tma_load_2d(a + 128 * kBlockK, &map_x, &full[stage], b * kBlockK, tile.row, pol);
+            tma_load_2d(a + 128 * kBlockK, &map_x, &full[stage], b * kBlockK, x_row, pol);
         }
         if (p.rows) {
           __syncwarp();
           if (lane < kT / 4)
-            tma_gather4(a + (128 + lane * 4) * kBlockK, &map_x, &full[stage], b * kBlockK, r[0],
-                        r[1], r[2], r[3], pol);
+            tma_gather4<false>(a + (128 + lane * 4) * kBlockK, &map_x, smem_u32(&full[stage]),
+                               b * kBlockK, r[0], r[1], r[2], r[3], pol);
         }
         ++issued;
         if (++stage == static_cast<uint32_t>(p.n_stages)) {
@@ -574,23 +770,20 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         mbar_wait_drain(&full[st], static_cast<uint32_t>((last / p.n_stages) & 1), p.status);
       }
   } else if (warp == 1) {
-    const uint32_t base = smem_u32(smem);
     constexpr uint32_t idesc = idesc_e4m3(128, kT);
-    uint32_t stage = 0, phase = 0, it = 0;
+    const uint64_t a_desc = umma_sdesc_sw128(smem_u32(smem));
+    const uint64_t b_desc = umma_sdesc_sw128(smem_u32(smem) + 128 * kBlockK);
+    uint32_t stage = 0, phase = 0, slot = 0, tphase = 0;
     bool ok = true;
-    for (int t = t_first; ok && t < total; t += t_step) {
-      for (int b = b_first; b < b_last; ++b, ++it) {
-        const uint32_t slot = it % kStreamBufs;
+    for (int t = t_first; all(ok && t < total); t += t_step) {
+#pragma unroll 1
+      for (int b = b_first; b < b_last; ++b) {
         // (the wait for a phase before the first passes at once)
-        ok = wait_on(&tempty[slot], ((it / kStreamBufs) & 1) ^ 1, p.status) &&
-             wait_on(&full[stage], phase, p.status);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = wait_both(&tempty[slot], tphase ^ 1, &full[stage], phase, p.status);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t at = base + stage * kStage;
-          const uint64_t ad = umma_sdesc_sw128(at);
-          const uint64_t bd = umma_sdesc_sw128(at + 128 * kBlockK);
+        if (elect_one()) {
+          const uint64_t ad = a_desc + stage * (kStage >> 4), bd = b_desc + stage * (kStage >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_e4m3(tmem + slot * kT, ad + 2 * kk, bd + 2 * kk, idesc, kk ? 1u : 0u);
@@ -598,22 +791,24 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           umma_commit(&tfull[slot]);
         }
         __syncwarp();
+        if (++slot == kStreamBufs) {
+          slot = 0;
+          tphase ^= 1;
+        }
         if (++stage == static_cast<uint32_t>(p.n_stages)) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    if (lane == 0) {
-      umma_commit(mdrain);
-      mbar_wait_drain(mdrain, 0, p.status);
-    }
+    if (elect_one()) umma_commit(mdrain);
+    if (lane == 0) mbar_wait_drain(mdrain, 0, p.status);
   }
 
   // TMEM lane = feature, column = row of x
   const int et = (warp & 3) * 32 + lane;
   bool ok = true;
-  float2 acc[kT / 2];
+  uint64_t acc[kT / 2];
   Tile tile = {};
   if (warp >= 2) {
     const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -642,7 +837,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       scales(b_first, x0);
       scales(b_first + 1, x1);
 #pragma unroll
-      for (int i = 0; i < kT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < kT / 2; ++i) acc[i] = 0;
 #pragma unroll 1
       for (int b = b_first; b < b_last; ++b, ++it) {
         float* f = mine + (it & 1) * kT;
@@ -653,29 +848,24 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
         scales(b + 2, x1);
         const uint32_t slot = it % kStreamBufs;
-        ok = __all_sync(0xffffffffu,
-                        wait_on(&tfull[slot], (it / kStreamBufs) & 1, p.status));
+        ok = all(wait_on(&tfull[slot], (it / kStreamBufs) & 1, p.status));
         if (!ok) break;
         tc_fence_after();
         const uint32_t ta = from + slot * kT;
 #pragma unroll
         for (int c = 0; c < kT; c += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(ta + c, v);
-          tmem_wait16(v);
+          uint64_t v[8];
+          tmem_pairs(ta + c, v);
           if (c + 16 == kT) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[slot]);
           }
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(f + c + i);
-            float2* a = acc + (c + i) / 2;
-            a[0] = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
-                              make_float2(g.x, g.y), a[0]);
-            a[1] = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
-                              make_float2(g.z, g.w), a[1]);
+          for (int i = 0; i < 8; i += 2) {
+            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(f + c + 2 * i);
+            fma_pair(acc[c / 2 + i], v[i], g.x);
+            fma_pair(acc[c / 2 + i + 1], v[i + 1], g.y);
           }
         }
       }
@@ -686,7 +876,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           uint16_t* dst = p.out + static_cast<long long>(tile.row) * p.out_pitch + n;
 #pragma unroll
           for (int j = 0; j < kT; ++j) {
-            if (j < tile.count) *dst = float_to_bf16_bits(j & 1 ? acc[j / 2].y : acc[j / 2].x);
+            if (j < tile.count) *dst = float_to_bf16_bits(j & 1 ? halves(acc[j / 2]).y : halves(acc[j / 2]).x);
             dst += p.out_pitch;
           }
         }
@@ -694,7 +884,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         // (every copy and product of this CTA is done: the stages are free)
         float* part = reinterpret_cast<float*>(smem) + et;
 #pragma unroll
-        for (int j = 0; j < kT; ++j) part[j * 128] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+        for (int j = 0; j < kT; ++j) part[j * 128] = j & 1 ? halves(acc[j / 2]).y : halves(acc[j / 2]).x;
       }
     }
   }
@@ -739,27 +929,53 @@ long long most_tiles(const Linear& p, int tile_rows, int tile_cols) {
   return (p.m / tile_rows + static_cast<long long>(p.groups < p.m ? p.groups : p.m)) * n_tiles;
 }
 
-template <int kN>
+template <bool kPair, int kN>
 int run_tiles(Linear p, const void* x, const void* w, int k, cudaStream_t st) {
+  constexpr int kCtas = kPair ? 2 : 1;
+  constexpr int kStage = tile_stage_bytes<kPair, kN>();
   p.n_tiles = (p.n + kN - 1) / kN;
-  const int tail = kStoreBytes + 5 * 8 + 4 + groups_bytes(p.groups);
-  p.n_stages = (kSmemLimit - 1024 - tail) / (tile_stage_bytes<kN>() + 16);
+  const int tail = kStoreBytes + kRing * kScaleRow * 4 + 10 * 8 + 4 + groups_bytes(p.groups);
+  p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
   if (p.n_stages > 8) p.n_stages = 8;
-  const int smem = 1024 + p.n_stages * (tile_stage_bytes<kN>() + 16) + tail;
+  const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
   CUtensorMap mx, mw;
   int rc = make_map(&mx, x, k, p.n_src, p.rows ? 1 : kTileRows);
-  if (!rc) rc = make_map(&mw, w, k, static_cast<long long>(p.groups) * p.n, kN);
+  if (!rc) rc = make_map(&mw, w, k, static_cast<long long>(p.groups) * p.n, kN / 2 / kCtas);
+  const auto kernel = tile_kernel<kPair, kN>;
   static std::atomic<uint64_t> ready{0};
   if (!rc)
-    rc = kv4::smem_limit_once(&ready, reinterpret_cast<const void*>(tile_kernel<kN>), kSmemLimit,
+    rc = kv4::smem_limit_once(&ready, reinterpret_cast<const void*>(kernel), kSmemLimit,
                               kRegsStart);
   if (rc) return rc;
-  const int nsm = current_num_sms();
-  if (nsm <= 0) return DFLASH_E_CUDA;
-  const long long tiles = most_tiles(p, kTileRows, kN);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kTileWarps * 32);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters that fit at once (one CTA to an SM), once per process
+  static const int most = [&] {
+    const int nsm = current_num_sms();
+    if (nsm <= 0) return 0;
+    cudaLaunchConfig_t q = cfg;
+    q.gridDim = dim3(nsm / kCtas * kCtas);
+    q.dynamicSmemBytes = kSmemLimit;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;
+  }();
+  if (most < 1) return DFLASH_E_CUDA;
+  const long long tiles = most_tiles(p, kTileRows * kCtas, kN);
   if (tiles > 0x7FFFFFFF - 256ll * kBand) return DFLASH_E_UNSUPPORTED;
-  const int grid = tiles < nsm ? static_cast<int>(tiles) : nsm;
-  return launch(tile_kernel<kN>, dim3(grid), dim3(kTileWarps * 32), smem, st, mx, mw, p);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * kCtas);
+  cfg.numAttrs = 2;
+  return cuda_err(cudaLaunchKernelEx(&cfg, kernel, mx, mw, p));
 }
 
 // CTAs that share a tile's K: the fewest time units, where a wave (two CTAs to an SM) costs its
@@ -820,12 +1036,21 @@ int run_stream(Linear p, const void* x, const void* w, int k, cudaStream_t st) {
 
 // Few rows (of an expert, on average) stream the weights, many fill the tiles.
 int run(const Linear& p, const void* x, const void* w, int k, cudaStream_t st) {
+  if (const char* v = getenv("VAR")) {
+    if (v[0] == 'p' && v[1] == '2') return run_tiles<true, 256>(p, x, w, k, st);
+    if (v[0] == 'p' && v[1] == '1') return run_tiles<true, 128>(p, x, w, k, st);
+    if (v[0] == 's' && v[1] == '2') return run_tiles<false, 256>(p, x, w, k, st);
+    if (v[0] == 's' && v[1] == '1') return run_tiles<false, 128>(p, x, w, k, st);
+    if (v[0] == 't' && v[1] == '1') return run_stream<16>(p, x, w, k, st);
+    if (v[0] == 't' && v[1] == '3') return run_stream<32>(p, x, w, k, st);
+    if (v[0] == 't' && v[1] == '6') return run_stream<64>(p, x, w, k, st);
+  }
   const int rows = (p.m + p.groups - 1) / p.groups;
   if (rows <= 16) return run_stream<16>(p, x, w, k, st);
   if (rows <= 32) return run_stream<32>(p, x, w, k, st);
   if (rows <= 64) return run_stream<64>(p, x, w, k, st);
-  if (p.n > 128) return run_tiles<256>(p, x, w, k, st);
-  return run_tiles<128>(p, x, w, k, st);
+  if (p.n > 128) return run_tiles<false, 256>(p, x, w, k, st);
+  return run_tiles<false, 128>(p, x, w, k, st);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
