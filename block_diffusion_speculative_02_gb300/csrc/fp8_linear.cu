@@ -138,6 +138,12 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t s
                : "memory");
 }
 
+// Arrive (one of the count) once this thread's copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 // Arrive at a named barrier of n threads without waiting at it.
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t n) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -359,7 +365,10 @@ constexpr int kRegsStart = 96, kRegsRest = 64, kRegsEpi = 104;
 static_assert(kEpiWarp * kRegsRest + kEpiWarps * kRegsEpi <= kTileWarps * kRegsStart,
               "register split");
 constexpr int kStoreBytes = kEpiWarps * 2048;   // 32 rows x 32 features of each epilogue warp
-constexpr int kRing = 8;                        // blocks whose scales are in shared memory
+// Blocks whose scales are in shared memory.  The copies run at most kMaxStages blocks ahead of the
+// products, and those 2 ahead of the epilogue.
+constexpr int kMaxStages = 8, kRing = 16;
+static_assert(kMaxStages + 2 <= kRing, "scales in use");
 constexpr int kScaleRow = kTileRows + 2;        // of the rows, then of the weights
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -420,7 +429,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   uint64_t* tfull = empty + p.n_stages;  // [2 halves][2] accumulators are there
   uint64_t* tempty = tfull + 4;          // [2 halves][2] read (of a pair: in the first CTA)
   uint64_t* mdrain = tempty + 4;         // [2 halves]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdrain + 2);
+  uint64_t* sfull = mdrain + 2;          // [kRing] scales are there
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sfull + kRing);
   const Groups groups = groups_at(reinterpret_cast<uint8_t*>(tmem_slot + 1), p.groups);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
@@ -438,6 +448,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     for (int i = 0; i < 2; ++i) {
       mbar_init(&mdrain[i], 1);
     }
+    for (int i = 0; i < kRing; ++i) mbar_init(&sfull[i], 32);
     fence_mbar_init();
   }
   if (warp == 1) tmem_take<kPair>(tmem_slot, kCols);
@@ -462,6 +473,21 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       if (p.rows) rows_of(p, tile, rank * kTileRows + lane * 4, r);
       const int x_row = same(tile.row) + rank * kTileRows;
       const int w_row = same(tile.e * p.n + tile.n * kN) + rank * kShare;
+      // the scales of four rows to a lane, and of the tile's blocks of features
+      const float* xs[4];
+      uint32_t x_size[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = rank * kTileRows + lane + 32 * i;
+        int src = -1;
+        if (at < tile.count) src = p.rows ? p.rows[tile.row + at] : tile.row + at;
+        x_size[i] = src >= 0 && src < p.n_src ? 4 : 0;          // none: a zero
+        xs[i] = p.xs + (x_size[i] ? src : 0);
+      }
+      const int nb = tile.n * kBlocksN + lane;
+      const uint32_t w_size = lane < kBlocksN && nb < p.n_blocks ? 4 : 0;
+      const float* ws =
+          p.ws + (static_cast<long long>(tile.e) * p.n_blocks + (w_size ? nb : 0)) * p.k_blocks;
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b) {
         ok = all(wait_on(&empty[stage], phase ^ 1, p.status));
@@ -481,6 +507,14 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
           tma_gather4<kPair>(a + lane * 4 * kBlockK, &map_x, bar, b * kBlockK, r[0], r[1], r[2],
                              r[3], pol);
         }
+        float* to = scales + (issued % kRing) * kScaleRow;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cp_async4(to + lane + 32 * i, xs[i], x_size[i]);
+          xs[i] += p.n_src;
+        }
+        if (lane < kBlocksN) cp_async4(to + kTileRows + lane, ws + b, w_size);
+        cp_async_arrive(&sfull[issued % kRing]);
         ++issued;
         if (++stage == static_cast<uint32_t>(p.n_stages)) {
           stage = 0;
@@ -488,6 +522,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         }
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // No copy may still be landing, and no product's arrival be on its way, when the CTA exits:
     // every stage has been read.  (Given up: what the first CTA's barriers counted has landed.)
     if (lane == 0)
@@ -538,69 +573,20 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       if (lane == 0) mbar_wait_drain(&mdrain[half], 0, p.status);
     }
   } else if (warp < kEpiWarp) {
-    // Watches the accumulators for the epilogue and copies its scales, four rows to a lane,
-    // kAhead blocks ahead.  (That a block's accumulators are there says that those of two blocks
-    // before were read, their scales too: of the ring, kAhead + 2 are in use.)  Once a wait gave
-    // up, the rest are skipped: the epilogue goes through its blocks all the same.
-    constexpr int kAhead = 4;
-    static_assert(kAhead + 2 <= kRing, "scales in use");
-    int t = t_first, b = 0;
-    uint32_t at = 0;
-    const float* xs[4] = {p.xs, p.xs, p.xs, p.xs};
-    const float* ws = p.ws;
-    uint32_t x_size[4] = {}, w_size = 0;
-    auto open = [&] {                      // tile t
-      const Tile tile = tile_at<kRows>(p, groups, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = rank * kTileRows + lane + 32 * i;
-        int src = -1;
-        if (r < tile.count) src = p.rows ? p.rows[tile.row + r] : tile.row + r;
-        x_size[i] = src >= 0 && src < p.n_src ? 4 : 0;          // none: a zero
-        xs[i] = p.xs + (x_size[i] ? src : 0);
-      }
-      const int nb = tile.n * kBlocksN + lane;
-      w_size = lane < kBlocksN && nb < p.n_blocks ? 4 : 0;
-      ws = p.ws + (static_cast<long long>(tile.e) * p.n_blocks + (w_size ? nb : 0)) * p.k_blocks;
-    };
-    auto copy = [&] {                      // the scales of the next block
-      if (t < total) {
-        if (b == 0) open();
-        float* to = scales + (at % kRing) * kScaleRow;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cp_async4(to + lane + 32 * i, xs[i], x_size[i]);
-          xs[i] += p.n_src;
-        }
-        if (lane < kBlocksN) cp_async4(to + kTileRows + lane, ws + b, w_size);
-        ++at;
-        if (++b == p.k_blocks) {
-          b = 0;
-          t += t_step;
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) copy();
+    // Watches the accumulators and the scales for the epilogue.  Once a wait gave up, the rest are
+    // skipped: the epilogue goes through its blocks all the same.
     bool ok = true;
     uint32_t it = 0;
-    for (int u = t_first; all(u < total); u += t_step) {
+    for (int t = t_first; all(t < total); t += t_step) {
 #pragma unroll 1
-      for (int i = 0; i < p.k_blocks; ++i, ++it) {
-        const uint32_t slot = it & 1;
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ok = ok && all(wait_on(&tfull[2 * h + slot], (it >> 1) & 1, p.status));
-          tc_fence_after();
-          tc_fence_before();
-          named_bar_arrive(1 + 2 * h + slot, 32 * (kEpiWarps / 2 + 1));
-        }
-        copy();
+      for (int b = 0; b < p.k_blocks; ++b, ++it) {
+        const uint32_t slot = it & 1, phase = (it >> 1) & 1;
+        ok = ok && wait_both(&tfull[slot], phase, &sfull[it % kRing], (it / kRing) & 1, p.status);
+        named_bar_arrive(1 + slot, 32 * (kEpiWarps / 2 + 1));
+        ok = ok && all(wait_on(&tfull[2 + slot], phase, p.status));
+        named_bar_arrive(3 + slot, 32 * (kEpiWarps / 2 + 1));
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else {
     kv4::regs_up<kRegsEpi>();
     const int quad = warp & 3, part = (warp - kEpiWarp) >> 2;
@@ -934,9 +920,9 @@ int run_tiles(Linear p, const void* x, const void* w, int k, cudaStream_t st) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kStage = tile_stage_bytes<kPair, kN>();
   p.n_tiles = (p.n + kN - 1) / kN;
-  const int tail = kStoreBytes + kRing * kScaleRow * 4 + 10 * 8 + 4 + groups_bytes(p.groups);
+  const int tail = kStoreBytes + kRing * kScaleRow * 4 + (10 + kRing) * 8 + 4 + groups_bytes(p.groups);
   p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
-  if (p.n_stages > 8) p.n_stages = 8;
+  if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
   const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
   CUtensorMap mx, mw;
   int rc = make_map(&mx, x, k, p.n_src, p.rows ? 1 : kTileRows);
