@@ -357,18 +357,17 @@ __device__ __forceinline__ void rows_of(const Linear& p, const Tile& tile, int a
 // warp watches the accumulators' mbarriers for them.  (With all of them trying an mbarrier, a
 // try took the warps that issue the products 400 clocks and more.)
 constexpr int kTileRows = 128;
-constexpr int kTileWarps = 20;        // copies, products, watch, products, 16 epilogue warps
-constexpr int kEpiWarp = 4, kEpiWarps = 16;
-// Registers a thread: 96 at the start; the epilogue's warps take from the others, within the
-// block's 640 x 96.
-constexpr int kRegsStart = 96, kRegsRest = 64, kRegsEpi = 104;
+// Warps: 0 copies, 1 and 3 products, 2 scales, 4 and 5 watch, two idle, 16 of the epilogue.
+constexpr int kTileWarps = 24;
+constexpr int kEpiWarp = 8, kEpiWarps = 16;
+// Registers a thread: 80 at the start; the epilogue's warps take from the others, within the
+// block's 768 x 80.
+constexpr int kRegsStart = 80, kRegsRest = 32, kRegsEpi = 104;
 static_assert(kEpiWarp * kRegsRest + kEpiWarps * kRegsEpi <= kTileWarps * kRegsStart,
               "register split");
 constexpr int kStoreBytes = kEpiWarps * 2048;   // 32 rows x 32 features of each epilogue warp
-// Blocks whose scales are in shared memory.  The copies run at most kMaxStages blocks ahead of the
-// products, and those 2 ahead of the epilogue.
-constexpr int kMaxStages = 8, kRing = 16;
-static_assert(kMaxStages + 2 <= kRing, "scales in use");
+constexpr int kMaxStages = 8;
+constexpr int kRing = 8;                        // blocks whose scales are in shared memory
 constexpr int kScaleRow = kTileRows + 2;        // of the rows, then of the weights
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -430,7 +429,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   uint64_t* tempty = tfull + 4;          // [2 halves][2] read (of a pair: in the first CTA)
   uint64_t* mdrain = tempty + 4;         // [2 halves]
   uint64_t* sfull = mdrain + 2;          // [kRing] scales are there
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sfull + kRing);
+  uint64_t* sempty = sfull + kRing;      // [kRing] both halves' sums of that block are there
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kRing);
   const Groups groups = groups_at(reinterpret_cast<uint8_t*>(tmem_slot + 1), p.groups);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
@@ -448,7 +448,10 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     for (int i = 0; i < 2; ++i) {
       mbar_init(&mdrain[i], 1);
     }
-    for (int i = 0; i < kRing; ++i) mbar_init(&sfull[i], 32);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sfull[i], 32);
+      mbar_init(&sempty[i], 2);
+    }
     fence_mbar_init();
   }
   if (warp == 1) tmem_take<kPair>(tmem_slot, kCols);
@@ -473,21 +476,6 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       if (p.rows) rows_of(p, tile, rank * kTileRows + lane * 4, r);
       const int x_row = same(tile.row) + rank * kTileRows;
       const int w_row = same(tile.e * p.n + tile.n * kN) + rank * kShare;
-      // the scales of four rows to a lane, and of the tile's blocks of features
-      const float* xs[4];
-      uint32_t x_size[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = rank * kTileRows + lane + 32 * i;
-        int src = -1;
-        if (at < tile.count) src = p.rows ? p.rows[tile.row + at] : tile.row + at;
-        x_size[i] = src >= 0 && src < p.n_src ? 4 : 0;          // none: a zero
-        xs[i] = p.xs + (x_size[i] ? src : 0);
-      }
-      const int nb = tile.n * kBlocksN + lane;
-      const uint32_t w_size = lane < kBlocksN && nb < p.n_blocks ? 4 : 0;
-      const float* ws =
-          p.ws + (static_cast<long long>(tile.e) * p.n_blocks + (w_size ? nb : 0)) * p.k_blocks;
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b) {
         ok = all(wait_on(&empty[stage], phase ^ 1, p.status));
@@ -507,14 +495,6 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
           tma_gather4<kPair>(a + lane * 4 * kBlockK, &map_x, bar, b * kBlockK, r[0], r[1], r[2],
                              r[3], pol);
         }
-        float* to = scales + (issued % kRing) * kScaleRow;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cp_async4(to + lane + 32 * i, xs[i], x_size[i]);
-          xs[i] += p.n_src;
-        }
-        if (lane < kBlocksN) cp_async4(to + kTileRows + lane, ws + b, w_size);
-        cp_async_arrive(&sfull[issued % kRing]);
         ++issued;
         if (++stage == static_cast<uint32_t>(p.n_stages)) {
           stage = 0;
@@ -522,7 +502,6 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     // No copy may still be landing, and no product's arrival be on its way, when the CTA exits:
     // every stage has been read.  (Given up: what the first CTA's barriers counted has landed.)
     if (lane == 0)
@@ -572,22 +551,63 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       if (elect_one()) mma_done_here<kPair>(&mdrain[half]);
       if (lane == 0) mbar_wait_drain(&mdrain[half], 0, p.status);
     }
-  } else if (warp < kEpiWarp) {
-    // Watches the accumulators and the scales for the epilogue.  Once a wait gave up, the rest are
-    // skipped: the epilogue goes through its blocks all the same.
+  } else if (warp == 2) {
+    // Copies the scales, kRing - 2 blocks ahead of the sums: that those of a block are there says
+    // that those of two blocks before were read, their scales too.
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = t_first; all(ok && t < total); t += t_step) {
+      const Tile tile = tile_at<kRows>(p, groups, t);
+      // the scales of four rows to a lane, and of the tile's blocks of features
+      const float* xs[4];
+      uint32_t x_size[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = rank * kTileRows + lane + 32 * i;
+        int src = -1;
+        if (at < tile.count) src = p.rows ? p.rows[tile.row + at] : tile.row + at;
+        x_size[i] = src >= 0 && src < p.n_src ? 4 : 0;          // none: a zero
+        xs[i] = p.xs + (x_size[i] ? src : 0);
+      }
+      const int nb = tile.n * kBlocksN + lane;
+      const uint32_t w_size = lane < kBlocksN && nb < p.n_blocks ? 4 : 0;
+      const float* ws =
+          p.ws + (static_cast<long long>(tile.e) * p.n_blocks + (w_size ? nb : 0)) * p.k_blocks;
+#pragma unroll 1
+      for (int b = 0; b < p.k_blocks; ++b, ++it) {
+        if (it >= kRing - 2) {
+          const uint32_t seen = it - (kRing - 2);
+          ok = all(wait_on(&sempty[seen % kRing], (seen / kRing) & 1, p.status));
+        }
+        if (!ok) break;
+        float* to = scales + (it % kRing) * kScaleRow;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cp_async4(to + lane + 32 * i, xs[i], x_size[i]);
+          xs[i] += p.n_src;
+        }
+        if (lane < kBlocksN) cp_async4(to + kTileRows + lane, ws + b, w_size);
+        cp_async_arrive(&sfull[it % kRing]);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 4 || warp == 5) {
+    // Watches the accumulators of half of the features, and the scales, for the epilogue.  Once a
+    // wait gave up, the rest are skipped: the epilogue goes through its blocks all the same.
+    const int half = warp & 1;
     bool ok = true;
     uint32_t it = 0;
     for (int t = t_first; all(t < total); t += t_step) {
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
-        const uint32_t slot = it & 1, phase = (it >> 1) & 1;
-        ok = ok && wait_both(&tfull[slot], phase, &sfull[it % kRing], (it / kRing) & 1, p.status);
-        named_bar_arrive(1 + slot, 32 * (kEpiWarps / 2 + 1));
-        ok = ok && all(wait_on(&tfull[2 + slot], phase, p.status));
-        named_bar_arrive(3 + slot, 32 * (kEpiWarps / 2 + 1));
+        const uint32_t slot = it & 1;
+        ok = ok && wait_both(&tfull[2 * half + slot], (it >> 1) & 1, &sfull[it % kRing],
+                             (it / kRing) & 1, p.status);
+        named_bar_arrive(1 + 2 * half + slot, 32 * (kEpiWarps / 2 + 1));
+        if (elect_one()) mbar_arrive(&sempty[it % kRing]);
       }
     }
-  } else {
+  } else if (warp >= kEpiWarp) {
     kv4::regs_up<kRegsEpi>();
     const int quad = warp & 3, part = (warp - kEpiWarp) >> 2;
     uint8_t* buf = store + (warp - kEpiWarp) * 2048;
@@ -920,7 +940,7 @@ int run_tiles(Linear p, const void* x, const void* w, int k, cudaStream_t st) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kStage = tile_stage_bytes<kPair, kN>();
   p.n_tiles = (p.n + kN - 1) / kN;
-  const int tail = kStoreBytes + kRing * kScaleRow * 4 + (10 + kRing) * 8 + 4 + groups_bytes(p.groups);
+  const int tail = kStoreBytes + kRing * kScaleRow * 4 + (10 + 2 * kRing) * 8 + 4 + groups_bytes(p.groups);
   p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
   if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
   const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
