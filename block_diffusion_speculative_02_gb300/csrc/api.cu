@@ -173,7 +173,8 @@ int make_plan(const dflash_dims& d, Plan* p) {
 namespace {
 
 int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t cols,
-                 uint64_t rows, uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
+                 uint64_t rows, uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto enc = encode_fn();
   if (!enc) return DFLASH_E_CUDA;
   cuuint64_t dims[2] = {cols, rows};
@@ -181,12 +182,19 @@ int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, u
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   DFLASH_TMAP_L2_PROMOTION, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, DFLASH_TMAP_L2_PROMOTION,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DFLASH_OK : DFLASH_E_ALIGN;
 }
 
 }  // namespace
+
+int make_tmap_2d_store_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                            uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {
+  return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, row_pitch_bytes,
+                      box_cols, box_rows,
+                      box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
 
 int make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                       uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows) {

@@ -244,8 +244,8 @@ __device__ __forceinline__ bool all(bool x) { return __all_sync(0xffffffffu, x);
 
 __device__ __forceinline__ uint32_t pack_bf16(uint64_t d) {
   const float2 f = halves(d);
-  return static_cast<uint32_t>(float_to_bf16_bits(f.x)) |
-         static_cast<uint32_t>(float_to_bf16_bits(f.y)) << 16;
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // --------------------------------------------------------------------------------------------
@@ -365,7 +365,6 @@ constexpr int kEpiWarp = 8, kEpiWarps = 16;
 constexpr int kRegsStart = 80, kRegsRest = 32, kRegsEpi = 104;
 static_assert(kEpiWarp * kRegsRest + kEpiWarps * kRegsEpi <= kTileWarps * kRegsStart,
               "register split");
-constexpr int kStoreBytes = kEpiWarps * 2048;   // 32 rows x 32 features of each epilogue warp
 constexpr int kMaxStages = 8;
 constexpr int kRing = 8;                        // blocks whose scales are in shared memory
 constexpr int kScaleRow = kTileRows + 2;        // of the rows, then of the weights
@@ -376,33 +375,58 @@ __host__ __device__ constexpr int tile_stage_bytes() {
   return (kTileRows + kN / (kPair ? 2 : 1)) * kBlockK;
 }
 
-// 32 features of 32 rows, one row to a lane, go through shared memory, so that a row's
-// features leave side by side.
-__device__ __forceinline__ void store_rows(const Linear& p, const uint64_t* acc, uint8_t* buf,
-                                           int row, int rows_left, int col, int lane) {
-  const auto at = [&](int r, int c) { return buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
+// kW features of 32 rows, one row to a lane, go through shared memory (in the order that the copies
+// swizzle to) and leave as one copy; where rows of another expert are among the 32, or out
+// is not aligned, row by row.  The copy is on its way when this returns.
+template <int kW>
+__device__ __forceinline__ void store_rows(const Linear& p, const CUtensorMap* map,
+                                           const uint64_t* acc, uint8_t* buf, int row,
+                                           int rows_left, int col, int lane) {
+  static_assert(kW == 64 || kW == 32, "swizzles");
+  const auto at = [&](int r, int c) {
+    return buf + r * kW * 2 + ((kW == 64 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+  };
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < kW / 8; ++c)
     *reinterpret_cast<uint4*>(at(lane, c)) =
         make_uint4(pack_bf16(acc[4 * c]), pack_bf16(acc[4 * c + 1]), pack_bf16(acc[4 * c + 2]),
                    pack_bf16(acc[4 * c + 3]));
+  // (The map ends with out: rows past its end are not written, nor are columns, of which a copy
+  // takes eight or none.)
+  if (p.vector && (rows_left >= 32 || !p.start) && (col + kW <= p.n || p.n % 8 == 0)) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && rows_left > 0 && col < p.n) {
+      asm volatile(
+          "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+          "r"(col), "r"(row), "r"(smem_u32(buf))
+          : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    return;
   }
   __syncwarp();
   const int most = min(32, rows_left);
-  if (p.vector && col + 32 <= p.n) {
-    const int c = lane & 3;
+  if (p.vector && col + kW <= p.n) {
+    constexpr int kLanes = kW / 8;           // to a row
+    const int c = lane % kLanes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
+    for (int i = 0; i < kLanes; ++i) {
+      const int r = i * (32 / kLanes) + lane / kLanes;
       const uint4 v = *reinterpret_cast<const uint4*>(at(r, c));
       if (r < most)
         *reinterpret_cast<uint4*>(p.out + static_cast<long long>(row + r) * p.out_pitch + col +
                                   8 * c) = v;
     }
-  } else if (col + lane < p.n) {
+  } else {
     for (int r = 0; r < most; ++r)
-      p.out[static_cast<long long>(row + r) * p.out_pitch + col + lane] =
-          *reinterpret_cast<const uint16_t*>(at(r, lane >> 3) + (lane & 7) * 2);
+#pragma unroll
+      for (int j = lane; j < kW; j += 32)
+        if (col + j < p.n)
+          p.out[static_cast<long long>(row + r) * p.out_pitch + col + j] =
+              *reinterpret_cast<const uint16_t*>(at(r, j >> 3) + (j & 7) * 2);
   }
   __syncwarp();
 }
@@ -410,20 +434,23 @@ __device__ __forceinline__ void store_rows(const Linear& p, const uint64_t* acc,
 template <bool kPair, int kN>
 __global__ void __launch_bounds__(kTileWarps * 32, 1)
 tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-            const Linear p) {
+            const __grid_constant__ CUtensorMap map_out, const Linear p) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kRows = kTileRows * kCtas;
   constexpr int kStage = tile_stage_bytes<kPair, kN>();
   constexpr int kHalf = kN / 2;          // features of a product
   constexpr int kShare = kHalf / kCtas;  // of these, features whose weights this CTA holds
   constexpr int kOwn = kN / 4;           // features of an epilogue warp
+  constexpr int kStore = 32 * kOwn * 2;  // its rows on their way out
   constexpr int kCols = 2 * kN;          // TMEM columns: two accumulators of each half
   constexpr int kBlocksN = kN / kBlockK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* store = smem + p.n_stages * kStage;
-  float* scales = reinterpret_cast<float*>(store + kStoreBytes);   // [kRing][128 rows, weights]
-  uint64_t* full = reinterpret_cast<uint64_t*>(scales + kRing * kScaleRow);
+  float* scales = reinterpret_cast<float*>(store + kEpiWarps * kStore);   // [kRing][128 rows, weights]
+  int4* tiles = reinterpret_cast<int4*>(scales + kRing * kScaleRow);  // [2 halves][4] for the
+                                                                      // epilogue
+  uint64_t* full = reinterpret_cast<uint64_t*>(tiles + 8);
   uint64_t* empty = full + p.n_stages;
   uint64_t* tfull = empty + p.n_stages;  // [2 halves][2] accumulators are there
   uint64_t* tempty = tfull + 4;          // [2 halves][2] read (of a pair: in the first CTA)
@@ -594,10 +621,18 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   } else if (warp == 4 || warp == 5) {
     // Watches the accumulators of half of the features, and the scales, for the epilogue.  Once a
     // wait gave up, the rest are skipped: the epilogue goes through its blocks all the same.
+    // A tile's place is written down for the epilogue, which needs it at the tile's end, beside its
+    // first block; of the ring, three are in use.
     const int half = warp & 1;
     bool ok = true;
-    uint32_t it = 0;
+    uint32_t it = 0, at = 4 * half;
     for (int t = t_first; all(t < total); t += t_step) {
+      const auto note = [&] {
+        const Tile tile = tile_at<kRows>(p, groups, t);
+        if (lane == 0) tiles[at] = make_int4(tile.row, tile.count, tile.n, 0);
+        at = 4 * half + ((at + 1) & 3);
+      };
+      if (p.k_blocks == 1) note();
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
         const uint32_t slot = it & 1;
@@ -605,19 +640,20 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                              (it / kRing) & 1, p.status);
         named_bar_arrive(1 + 2 * half + slot, 32 * (kEpiWarps / 2 + 1));
         if (elect_one()) mbar_arrive(&sempty[it % kRing]);
+        if (b == 0 && p.k_blocks > 1) note();
       }
     }
   } else if (warp >= kEpiWarp) {
     kv4::regs_up<kRegsEpi>();
     const int quad = warp & 3, part = (warp - kEpiWarp) >> 2;
-    uint8_t* buf = store + (warp - kEpiWarp) * 2048;
+    uint8_t* buf = store + (warp - kEpiWarp) * kStore;
     const int half = part >> 1;
     const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * kHalf +
                           (part & 1) * kOwn;
     const float* x_scale = scales + quad * 32 + lane;
     const float* w_scale = scales + kTileRows + part * kOwn / kBlockK;
     const uint32_t read = first_cta<kPair>(tempty + 2 * half);
-    uint32_t it = 0;
+    uint32_t it = 0, at = 4 * half;
     for (int t = t_first; t < total; t += t_step) {
       uint64_t acc[kOwn / 2];
 #pragma unroll
@@ -644,13 +680,13 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
           for (int i = 0; i < 8; ++i) fma_pair(acc[c / 2 + i], v[i], f);
         }
       }
-      const Tile tile = tile_at<kRows>(p, groups, t);
-      const int at = rank * kTileRows + quad * 32;
-#pragma unroll
-      for (int c = 0; c < kOwn; c += 32)
-        store_rows(p, acc + c / 2, buf, tile.row + at, tile.count - at,
-                   tile.n * kN + part * kOwn + c, lane);
+      const int4 tile = tiles[at];                       // first row, rows, feature tile
+      at = 4 * half + ((at + 1) & 3);
+      const int in = rank * kTileRows + quad * 32;
+      store_rows<kOwn>(p, &map_out, acc, buf, tile.x + in, tile.y - in, tile.z * kN + part * kOwn,
+                       lane);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -940,13 +976,15 @@ int run_tiles(Linear p, const void* x, const void* w, int k, cudaStream_t st) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kStage = tile_stage_bytes<kPair, kN>();
   p.n_tiles = (p.n + kN - 1) / kN;
-  const int tail = kStoreBytes + kRing * kScaleRow * 4 + (10 + 2 * kRing) * 8 + 4 + groups_bytes(p.groups);
+  constexpr int kStoreBytes = kEpiWarps * 32 * (kN / 4) * 2;
+  const int tail = kStoreBytes + kRing * kScaleRow * 4 + 8 * 16 + (10 + 2 * kRing) * 8 + 4 + groups_bytes(p.groups);
   p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
   if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
   const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
-  CUtensorMap mx, mw;
+  CUtensorMap mx, mw, mo = {};
   int rc = make_map(&mx, x, k, p.n_src, p.rows ? 1 : kTileRows);
   if (!rc) rc = make_map(&mw, w, k, static_cast<long long>(p.groups) * p.n, kN / 2 / kCtas);
+  if (!rc && p.vector) rc = make_tmap_2d_store_bf16(&mo, p.out, p.n, p.m, p.out_pitch * 2, kN / 4, 32);
   const auto kernel = tile_kernel<kPair, kN>;
   static std::atomic<uint64_t> ready{0};
   if (!rc)
@@ -981,7 +1019,7 @@ int run_tiles(Linear p, const void* x, const void* w, int k, cudaStream_t st) {
   if (tiles > 0x7FFFFFFF - 256ll * kBand) return DFLASH_E_UNSUPPORTED;
   cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most) * kCtas);
   cfg.numAttrs = 2;
-  return cuda_err(cudaLaunchKernelEx(&cfg, kernel, mx, mw, p));
+  return cuda_err(cudaLaunchKernelEx(&cfg, kernel, mx, mw, mo, p));
 }
 
 // CTAs that share a tile's K: the fewest time units, where a wave (two CTAs to an SM) costs its

@@ -100,6 +100,10 @@ int make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_
 // 2-D map of bytes, likewise (box_cols at most 128, cols and the pitch a multiple of 16).
 int make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                     uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows);
+// 2-D bf16 map to store boxes of 32 or 64 columns from shared memory in the order of the 64-byte or
+// 128-byte swizzle.
+int make_tmap_2d_store_bf16(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                            uint64_t row_pitch_bytes, uint32_t box_cols, uint32_t box_rows);
 // 3-D bf16 tensor map over [d2][d1][d0] with pitches (bytes) for d1 and d2.
 int make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
                       uint64_t d2, uint64_t pitch1, uint64_t pitch2, uint32_t box0,
