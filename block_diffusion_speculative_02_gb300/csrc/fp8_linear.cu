@@ -266,36 +266,45 @@ __device__ __forceinline__ Groups groups_at(uint8_t* smem, int groups) {
   return {p, p + groups, p + 2 * groups};
 }
 
-// By one warp.
+// By the whole block, of n threads.
 __device__ __forceinline__ void fill_groups(const Linear& p, const Groups& g, int tile_rows,
-                                            int lane) {
-  int sum = 0;
-  for (int e0 = 0; e0 < p.groups; e0 += 32) {
-    const int e = e0 + lane;
-    int a = 0, b = 0;
-    if (e < p.groups) {
-      a = p.start ? p.start[e] : 0;
-      b = p.start ? p.start[e + 1] : p.m;
-      if (a < 0 || b < a || b > p.m) {
-        set_status(p.status, DFLASH_ST_CAPACITY);
-        a = b = 0;
-      }
+                                            int n) {
+  if (!p.start) {
+    if (threadIdx.x == 0) {
+      g.first[0] = 0;
+      g.count[0] = p.m;
+      g.tiles[0] = 0;
+      g.tiles[1] = (p.m + tile_rows - 1) / tile_rows;
     }
-    const int own = (b - a + tile_rows - 1) / tile_rows;
-    int t = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += y;
-    }
-    if (e < p.groups) {
-      g.first[e] = a;
-      g.count[e] = b - a;
-      g.tiles[e] = sum + t - own;
-    }
-    sum += __shfl_sync(0xffffffffu, t, 31);
+    return;                              // (the caller's barrier follows)
   }
-  if (lane == 0) g.tiles[p.groups] = sum;
+  for (int e = threadIdx.x; e < p.groups; e += n) {
+    int a = p.start[e], b = p.start[e + 1];
+    if (a < 0 || b < a || b > p.m) {
+      set_status(p.status, DFLASH_ST_CAPACITY);
+      a = b = 0;
+    }
+    g.first[e] = a;
+    g.count[e] = b - a;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int sum = 0;
+    for (int e0 = 0; e0 < p.groups; e0 += 32) {
+      const int e = e0 + lane;
+      const int own = e < p.groups ? (g.count[e] + tile_rows - 1) / tile_rows : 0;
+      int t = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += y;
+      }
+      if (e < p.groups) g.tiles[e] = sum + t - own;
+      sum += __shfl_sync(0xffffffffu, t, 31);
+    }
+    if (lane == 0) g.tiles[p.groups] = sum;
+  }
 }
 
 // The group that row tile i (< tiles[groups]) belongs to: the last one with tiles[e] <= i.
@@ -482,8 +491,14 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     fence_mbar_init();
   }
   if (warp == 1) tmem_take<kPair>(tmem_slot, kCols);
+  if (warp == 2 && elect_one()) {
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+    if (p.vector) tma_prefetch_desc(&map_out);
+  }
   griddep_wait();
-  if (warp == 2) fill_groups(p, groups, kRows, lane);
+  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
+  fill_groups(p, groups, kRows, kTileWarps * 32);
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();             // the other CTA's barriers are there
@@ -695,7 +710,6 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     tc_fence_after();
     tmem_give<kPair>(tmem, kCols);
   }
-  griddep_launch_dependents();
 }
 
 // --------------------------------------------------------------------------------------------
@@ -763,8 +777,13 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
   }
+  if (warp == 2 && elect_one()) {
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
   griddep_wait();
-  if (warp == 2) fill_groups(p, groups, kT, lane);
+  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
+  fill_groups(p, groups, kT, kStreamThreads);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -951,7 +970,6 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
-  griddep_launch_dependents();
 }
 
 // --------------------------------------------------------------------------------------------
