@@ -24,9 +24,7 @@ namespace {
 // 512 rows x 4096 x 4096 take 12.8, 14.6, 14.1 us; 128 rows x 24576 27.3, 23.9, 33.3; 512 rows x 24576
 // 60, 54, 46.
 int choose(const Linear& p, cudaStream_t st) {
-  const int nsm = current_num_sms();
-  if (nsm <= 0) return DFLASH_E_CUDA;
-  const int rows = (p.m + p.groups - 1) / p.groups;
+  const int nsm = p.sms, rows = (p.m + p.groups - 1) / p.groups;
   if (rows <= 16) return run_stream(p, 16, st);
   if (rows <= 32) return run_stream(p, 32, st);
   if (rows <= (!p.start ? 64 : p.rows ? 512 : 192)) return run_stream(p, 64, st);
@@ -75,6 +73,8 @@ int check(int m, int n_src, int groups, int n, int k, const void* x, const float
   p->k_blocks = static_cast<int>(blocks(k));
   p->n_blocks = static_cast<int>(blocks(n));
   p->vector = aligned16(out) && out_pitch % 8 == 0;
+  p->sms = current_num_sms();
+  if (p->sms <= 0) return DFLASH_E_CUDA;
   return DFLASH_OK;
 }
 
@@ -109,6 +109,9 @@ extern "C" int dflash_fp8_grouped(int32_t n_rows, int32_t n_src, int32_t n_group
   if (rc || n_rows == 0) return rc;
   if (!start || (!rows && n_src != n_rows)) return DFLASH_E_ARG;
   if (!aligned4(start) || !aligned4(rows)) return DFLASH_E_ALIGN;
+  // (rows named by an index are found by 32-bit offsets in units of 16 bytes)
+  if (rows && static_cast<long long>(n_src) * (n_in / 16) >= 0xFFFFFFFFll)
+    return DFLASH_E_UNSUPPORTED;
   p.start = start;
   p.rows = rows;
   return choose(p, reinterpret_cast<cudaStream_t>(stream));

@@ -41,6 +41,7 @@ struct Linear {
   int n_tiles;
   int n_stages;
   int vector;            // out and its pitch are aligned to 16 bytes
+  int sms;               // of the device
   int box_rows;          // rows of a copy of x: of a tile, or all there are if they are fewer (rows
                          // past the end of x, which the TMA fills with zeros, cost 2 ns each)
 };
@@ -339,29 +340,45 @@ __device__ __forceinline__ int source_row(const Linear& p, const Tile& tile, int
   return -1;
 }
 
-// By one warp: block columns col .. col + 127 of kRows rows of x, into the order of the 128-byte
-// swizzle.  r[i]: the row of x for row lane + 32 i, or -1: zeros.
+// Where rows named by an index are, for the copies: row r of kRows at sources[place_of(r)], in units
+// of 16 bytes from x on, or kNoRow (zeros).  The rows that eight lanes copy lie side by side.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
 template <int kRows>
+__device__ __forceinline__ int place_of(int r) {
+  return (r & 3) * (kRows / 4) + (r >> 2);
+}
+
+// By one warp: block columns col .. col + 127 of kRows rows of x (from row `first` of kOf on), into
+// the order of the 128-byte swizzle.  Few instructions a copy count here: the warp has few turns and
+// registers.
+template <int kRows, int kOf>
 __device__ __forceinline__ void copy_rows(const Linear& p, uint8_t* dst, int col,
-                                          const int (&r)[(kRows + 31) / 32], int lane) {
+                                          const uint32_t* sources, int first, int lane) {
   const int c = lane & 7, at = col + c * 16;
+  const uint32_t* from = sources + (lane >> 3) * (kOf / 4) + first / 4;
+  const uint8_t* x = p.x + (at < p.k ? at : 0);
+  const uint32_t to = smem_u32(dst) + (first + (lane >> 3)) * kBlockK;
 #pragma unroll
-  for (int i = 0; i < kRows / 4; ++i) {
-    const int row = (lane >> 3) + 4 * i;
-    const int src = __shfl_sync(0xffffffffu, r[i / 8], row & 31);
-    const bool there = src >= 0 && at < p.k;
-    const uint8_t* from = p.x + static_cast<size_t>(there ? src : 0) * p.k + (there ? at : 0);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                     smem_u32(dst + row * kBlockK + ((c ^ (row & 7)) << 4))),
-                 "l"(from), "r"(there ? 16 : 0)
-                 : "memory");
+  for (int i = 0; i < kRows / 4; i += 4) {
+    const uint4 s = *reinterpret_cast<const uint4*>(from + i);
+    const uint32_t v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = (i + j) * 4;                     // and lane >> 3; first is a multiple of 8
+      const bool there = v[j] != kNoRow && at < p.k;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       to + row * kBlockK + ((c ^ ((row + (lane >> 3)) & 7)) << 4)),
+                   "l"(x + (there ? static_cast<size_t>(v[j]) * 16 : 0)), "r"(there ? 16 : 0)
+                   : "memory");
+    }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// By one warp: `blocks` blocks of the rows r of one tile, each into the next stage (its bytes at
-// `offset`), kCopyLag of them on their way at a time.  A block's arrival at its stage's barrier
-// (arrive) comes once its bytes are there for the tensor cores to read.
+// One warp's copies: each block into the next stage, kCopyLag of them on their way at a time.  A
+// block's arrival at its stage's barrier (arrive) comes once its bytes are there for the tensor
+// cores to read.
 constexpr int kCopyLag = 2;
 
 struct RowCopies {
@@ -378,15 +395,15 @@ struct RowCopies {
     --pending;
   }
 
-  template <int kRows, class Arrive>
+  template <int kRows, int kOf, class Arrive>
   __device__ __forceinline__ bool tile(const Linear& p, uint8_t* base, int stage_bytes,
                                        uint64_t* empty, int b_first, int b_last,
-                                       const int (&r)[(kRows + 31) / 32], int lane,
+                                       const uint32_t* sources, int first, int lane,
                                        const Arrive& arrive) {
 #pragma unroll 1
     for (int b = b_first; b < b_last; ++b) {
       if (!all(wait_on(&empty[stage], phase ^ 1, p.status))) return false;
-      copy_rows<kRows>(p, base + stage * stage_bytes, b * kBlockK, r, lane);
+      copy_rows<kRows, kOf>(p, base + stage * stage_bytes, b * kBlockK, sources, first, lane);
       if (++stage == static_cast<uint32_t>(p.n_stages)) {
         stage = 0;
         phase ^= 1;

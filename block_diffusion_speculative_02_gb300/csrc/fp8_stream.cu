@@ -43,7 +43,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   uint8_t* smem = align_smem_1024(smem_raw);
   float* factors = reinterpret_cast<float*>(smem + p.n_stages * kStage);   // [kFactors][kT]
   int4* tiles = reinterpret_cast<int4*>(factors + kFactors * kT);          // [kInfo]
-  int* sources = reinterpret_cast<int*>(tiles + kInfo);                    // [kInfo][kT]
+  uint32_t* sources = reinterpret_cast<uint32_t*>(tiles + kInfo);          // [kInfo][kT]
   uint64_t* full = reinterpret_cast<uint64_t*>(sources + kInfo * kT);
   uint64_t* empty = full + p.n_stages;
   uint64_t* tfull = empty + p.n_stages;            // [kStreamBufs]
@@ -195,7 +195,9 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < kScales; ++i) {
           src[i] = lane + 32 * i < kT ? source_row(p, tile, lane + 32 * i) : -1;
-          if (kIndex && lane + 32 * i < kT) sources[in % kInfo * kT + lane + 32 * i] = src[i];
+          if (kIndex && lane + 32 * i < kT)
+            sources[in % kInfo * kT + place_of<kT>(lane + 32 * i)] =
+                src[i] >= 0 ? static_cast<uint32_t>(src[i]) * (p.k / 16) : kNoRow;
         }
         if (lane == 0)
           tiles[in % kInfo] = make_int4(tile.row, tile.count, tile.n, tile.e * p.n + tile.n * 128);
@@ -241,14 +243,10 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       for (int t = t_first; all(ok && t < total); t += t_step, ++in) {
         ok = all(wait_on(&ifull[in % kInfo], (in / kInfo) & 1, p.status));
         if (!ok) break;
-        int r[kScales];
-#pragma unroll
-        for (int i = 0; i < kScales; ++i)
-          r[i] = lane + 32 * i < kT ? sources[in % kInfo * kT + lane + 32 * i] : -1;
+        ok = copies.tile<kT, kT>(p, smem + 128 * kBlockK, kStage, empty, b_first, b_last,
+                                 sources + in % kInfo * kT, 0, lane, arrive);
         __syncwarp();
         if (elect_one()) mbar_arrive(&iempty[in % kInfo]);
-        ok = copies.tile<kT>(p, smem + 128 * kBlockK, kStage, empty, b_first, b_last, r, lane,
-                             arrive);
       }
       copies.finish(p, arrive);
     }
@@ -389,8 +387,7 @@ int run(Linear p, cudaStream_t st) {
   const void* kernel = reinterpret_cast<const void*>(stream_kernel<kT, kIndex>);
   if (!rc) rc = kv4::smem_limit_once(&ready, kernel, kStreamSmem);
   if (rc) return rc;
-  const int nsm = current_num_sms();
-  if (nsm <= 0) return DFLASH_E_CUDA;
+  const int nsm = p.sms;
   const long long tiles = most_tiles(p, kT, 128);
   if (tiles > 0x7FFFFFFF / 16) return DFLASH_E_UNSUPPORTED;
   const int split = stream_split(p, tiles, nsm);

@@ -109,7 +109,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   uint8_t* store = smem + p.n_stages * kStage;
   float* scales = reinterpret_cast<float*>(store + kEpiWarps * kStore);   // [kRing][128 rows, weights]
   int4* tiles = reinterpret_cast<int4*>(scales + kRing * kScaleRow);  // [kInfo] tiles' places
-  int* sources = reinterpret_cast<int*>(tiles + kInfo);               // [kInfo][128] rows of x
+  uint32_t* sources = reinterpret_cast<uint32_t*>(tiles + kInfo);     // [kInfo][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(sources + kInfo * kTileRows);
   uint64_t* empty = full + p.n_stages;
   uint64_t* tfull = empty + p.n_stages;  // [2 halves][2] accumulators are there
@@ -274,7 +274,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         const int src = source_row(p, tile, rank * kTileRows + lane + 32 * i);
         x_size[i] = src >= 0 ? 4 : 0;                           // none: a zero
         xs[i] = p.xs + max(src, 0);
-        if (kIndex) sources[in % kInfo * kTileRows + lane + 32 * i] = src;
+        if (kIndex)
+          sources[in % kInfo * kTileRows + place_of<kTileRows>(lane + 32 * i)] =
+              src >= 0 ? static_cast<uint32_t>(src) * (p.k / 16) : kNoRow;
       }
       if (lane == 0)
         tiles[in % kInfo] = make_int4(tile.row, tile.count, tile.n, tile.e * p.n + tile.n * kN);
@@ -332,12 +334,10 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       for (int t = t_first; all(ok && t < total); t += t_step, ++in) {
         ok = all(wait_on(&ifull[in % kInfo], (in / kInfo) & 1, p.status));
         if (!ok) break;
-        const int* from = sources + in % kInfo * kTileRows + first + lane;
-        const int r[2] = {from[0], from[32]};
+        ok = copies.tile<64, kTileRows>(p, smem, kStage, empty, 0, p.k_blocks,
+                                        sources + in % kInfo * kTileRows, first, lane, arrive);
         __syncwarp();
         if (elect_one()) mbar_arrive(&iempty[in % kInfo]);
-        ok = copies.tile<64>(p, smem + first * kBlockK, kStage, empty, 0, p.k_blocks, r, lane,
-                             arrive);
       }
       copies.finish(p, arrive);
     }
@@ -438,10 +438,8 @@ int run(Linear p, cudaStream_t st) {
   cfg.numAttrs = 1;
   // clusters that fit at once (one CTA to an SM), once per process
   static const int most = [&] {
-    const int nsm = current_num_sms();
-    if (nsm <= 0) return 0;
     cudaLaunchConfig_t q = cfg;
-    q.gridDim = dim3(nsm / kCtas * kCtas);
+    q.gridDim = dim3(p.sms / kCtas * kCtas);
     q.dynamicSmemBytes = kSmemLimit;
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;

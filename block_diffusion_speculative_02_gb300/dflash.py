@@ -731,7 +731,7 @@ def alloc_fp8_weight(*shape, device="cuda"):
 
 def _whole(t, device: int, dtype, shape, name: str) -> int:
     """Pointer of a contiguous tensor of this type and shape on this device."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device \
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != device \
             or not t.is_contiguous():
         _bad(t, device, dtype, None, name)
     if t.shape != shape:
@@ -739,17 +739,25 @@ def _whole(t, device: int, dtype, shape, name: str) -> int:
     return t.data_ptr()
 
 
-def _matrix(t, device: int, name: str, shape=None):
+def _matrix(t, device: int, name: str, shape):
     """(pointer, row pitch) of a bf16 matrix whose rows are contiguous and may lie apart."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 \
-            or t.get_device() != device or t.dim() != 2:
-        raise ValueError(f"{name} must be a bf16 matrix on cuda:{device}")
-    if shape is not None and t.shape != shape:
+    if getattr(t, "dtype", None) is not torch.bfloat16 or t.get_device() != device:
+        raise ValueError(f"{name} must be a bf16 tensor on cuda:{device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: the columns of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), pitch if rows > 1 else cols
+
+
+def _shape(t, dims: int, name: str):
+    """The shape of a tensor of this many dimensions."""
+    shape = getattr(t, "shape", None)
+    if shape is None or len(shape) != dims:
+        raise ValueError(f"{name} must be a tensor of {dims} dimensions")
+    return shape
 
 
 def _matrix_opt(t, device: int, name: str, shape):
@@ -761,13 +769,11 @@ def dflash_fp8_norm_rows(x, residual, norm_w, rms_eps: float, sum_out, q, scale,
 
     ``residual``, ``norm_w`` and ``sum_out`` may be None: nothing added, not normed, not stored."""
     dev, st = _here(stream)
-    px = _matrix(x, dev, "x")
-    rows, cols = x.shape
+    shape = rows, cols = _shape(x, 2, "x")
     rc = load_library().dflash_fp8_norm_rows(
-        rows, cols, *px, *_matrix_opt(residual, dev, "residual", (rows, cols)),
+        rows, cols, *_matrix(x, dev, "x", shape), *_matrix_opt(residual, dev, "residual", shape),
         None if norm_w is None else _whole(norm_w, dev, torch.bfloat16, (cols,), "norm_w"),
-        rms_eps, *_matrix_opt(sum_out, dev, "sum_out", (rows, cols)),
-        _whole(q, dev, F8, (rows, cols), "q"),
+        rms_eps, *_matrix_opt(sum_out, dev, "sum_out", shape), _whole(q, dev, F8, shape, "q"),
         _whole(scale, dev, torch.float32, (_up128(cols), rows), "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_norm_rows")
@@ -776,13 +782,12 @@ def dflash_fp8_norm_rows(x, residual, norm_w, rms_eps: float, sum_out, q, scale,
 def dflash_fp8_silu_mul(gate_up, q, scale, stream=None):
     """q, scale = 8-bit rows of silu(gate) * up, gate_up [M, 2 F]: gate, then up."""
     dev, st = _here(stream)
-    px = _matrix(gate_up, dev, "gate_up")
-    rows, cols = gate_up.shape
+    shape = rows, cols = _shape(gate_up, 2, "gate_up")
     if cols % 2:
         raise ValueError("gate_up must have an even number of columns: gate, then up")
     cols //= 2
     rc = load_library().dflash_fp8_silu_mul(
-        rows, cols, *px, _whole(q, dev, F8, (rows, cols), "q"),
+        rows, cols, *_matrix(gate_up, dev, "gate_up", shape), _whole(q, dev, F8, (rows, cols), "q"),
         _whole(scale, dev, torch.float32, (_up128(cols), rows), "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_silu_mul")
@@ -802,24 +807,18 @@ def dflash_fp8_weight(w, q, scale, stream=None):
         _check(rc, "dflash_fp8_weight")
 
 
-def _x_and_w(x, w, dims: int):
-    for t, name, d in ((x, "x", 2), (w, "w", dims)):
-        if not isinstance(t, torch.Tensor) or t.dim() != d:
-            raise ValueError(f"{name} must be a tensor of {d} dimensions")
-    if x.shape[1] != w.shape[-1]:
-        raise ValueError(f"x has {x.shape[1]} columns, w {w.shape[-1]}")
-
-
 def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
     """out [M, N] (bf16, rows may be strided) = x w^T of 8-bit rows x [M, K] and weights w [N, K]."""
     dev, st = _here(stream)
-    _x_and_w(x, w, 2)
-    (m, k), n = x.shape, w.shape[0]
+    m, k = _shape(x, 2, "x")
+    n, kw = _shape(w, 2, "w")
+    if kw != k:
+        raise ValueError(f"x has {k} columns, w {kw}")
+    kb = _up128(k)
     rc = load_library().dflash_fp8_linear(
-        m, n, k, _whole(x, dev, F8, (m, k), "x"),
-        _whole(x_scale, dev, torch.float32, (_up128(k), m), "x_scale"),
-        _whole(w, dev, F8, (n, k), "w"),
-        _whole(w_scale, dev, torch.float32, (_up128(n), _up128(k)), "w_scale"),
+        m, n, k, _whole(x, dev, F8, x.shape, "x"),
+        _whole(x_scale, dev, torch.float32, (kb, m), "x_scale"), _whole(w, dev, F8, w.shape, "w"),
+        _whole(w_scale, dev, torch.float32, (_up128(n), kb), "w_scale"),
         *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
     if rc:
         _check(rc, "dflash_fp8_linear")
@@ -829,18 +828,18 @@ def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None
     """Rows start[e] .. start[e + 1] - 1 of out = x w[e]^T, w [E, N, K]; ``rows``: int32 [len(out)],
     the row of x that each row of out is made of, or None: the same row."""
     dev, st = _here(stream)
-    _x_and_w(x, w, 3)
-    (src, k), (e, n, _) = x.shape, w.shape
-    if not isinstance(out, torch.Tensor) or out.dim() != 2:
-        raise ValueError("out must be a matrix")
-    m = out.shape[0]
+    src, k = _shape(x, 2, "x")
+    e, n, kw = _shape(w, 3, "w")
+    if kw != k:
+        raise ValueError(f"x has {k} columns, w {kw}")
+    m, kb = _shape(out, 2, "out")[0], _up128(k)
     if rows is None and m != src:
         raise ValueError(f"out has {m} rows, x {src}: rows must say which")
     rc = load_library().dflash_fp8_grouped(
-        m, src, e, n, k, _whole(x, dev, F8, (src, k), "x"),
-        _whole(x_scale, dev, torch.float32, (_up128(k), src), "x_scale"),
-        _whole(w, dev, F8, (e, n, k), "w"),
-        _whole(w_scale, dev, torch.float32, (e, _up128(n), _up128(k)), "w_scale"),
+        m, src, e, n, k, _whole(x, dev, F8, x.shape, "x"),
+        _whole(x_scale, dev, torch.float32, (kb, src), "x_scale"),
+        _whole(w, dev, F8, w.shape, "w"),
+        _whole(w_scale, dev, torch.float32, (e, _up128(n), kb), "w_scale"),
         _whole(start, dev, torch.int32, (e + 1,), "start"),
         None if rows is None else _whole(rows, dev, torch.int32, (m,), "rows"),
         *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)

@@ -215,7 +215,8 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (1, 4096, 4096), (2, 130, 144), (7, 257, 40
           (17, 384, 1024), (31, 129, 272), (33, 1000, 2048), (63, 640, 784), (64, 256, 12288),
           (65, 255, 512), (100, 1537, 640), (128, 128, 128), (129, 511, 2560), (255, 2567, 256),
           (256, 1024, 1024), (257, 768, 4000), (513, 520, 128), (1000, 136, 1040), (700, 2056, 16),
-          (2048, 2048, 512)]
+          (2048, 2048, 512), (128, 20000, 144), (2148, 2048, 256), (2200, 1500, 272),
+          (1, 24576, 128), (24, 8192, 640), (50, 20000, 384)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -298,7 +299,9 @@ def counts_of(kind, e, m, rng):
 GROUPED = [("even", 4, 4, 130, 144), ("skew", 128, 128, 256, 512), ("skew", 128, 900, 200, 256),
            ("one", 7, 90, 300, 640), ("skew", 9, 1500, 520, 384), ("even", 3, 700, 513, 1040),
            ("one", 1, 50, 128, 128), ("skew", 1024, 700, 16, 128), ("skew", 33, 300, 129, 2048),
-           ("even", 64, 4096, 128, 256)]
+           ("even", 64, 4096, 128, 256), ("even", 2, 3000, 2000, 256),
+           ("even", 2, 1300, 2816, 144), ("even", 2, 1300, 300, 400), ("skew", 40, 800, 5000, 144),
+           ("skew", 3, 200, 1200, 2304), ("skew", 5, 2800, 4096, 16), ("one", 1000, 1500, 512, 272)]
 
 
 @pytest.mark.parametrize("kind,e,m,n,k", GROUPED)
