@@ -9,32 +9,35 @@ namespace {
 // Which kernel takes a call; `rows`: of an expert, on average.
 //
 // Up to 64 rows the weights are streamed, with the smallest tile that holds the rows: 16 rows x
-// 4096 x 4096 take 6.2, 7.0, 11.1 us with tiles of 16, 32, 64 rows (128 x 128 tiles: 18), 64 rows
-// 10.6, 8.7, 8.9 (11.5).  By expert, a tile's rows are seldom full and the weights of an expert
-// come from L2 for its second tile: 32 rows each of 128 experts x 1536 x 2048 take 81, 66, 66 us
-// (128 x 256 tiles: 109), 128 rows 244, 153, 123 (169), 1024 rows of 8 experts x 4096 x 2048 take
-// 132 with 64 rows and 127 with pairs.  Without an index the tiles get their rows sooner: 512 rows
-// each of 64 experts x 2048 x 1408 take 148 us streamed and 105 with pairs.
+// 4096 x 4096 take 6.1, 7.0, 11.1 us with tiles of 16, 32, 64 rows (128 x 128 tiles: 18), 64 rows
+// 10.6, 8.7, 8.9 (11.5).
+//
+// By expert (rows of 128 experts x 1536 x 2048 by index, in us): 32 rows each take 81, 66, 64 with
+// tiles of 16, 32, 64 rows, 109 with 128 x 256; 80 rows 89 and 98; 192 rows 162, 153 and 155 with
+// pairs; 384 rows 292, 247, 231.  Rows in order reach the tiles sooner: 80 rows 80 and 80, 256 rows
+// 150, 126, 131, 512 rows 206 with 128 x 256 and 201 with pairs.
 //
 // Up to 128 rows, where features are so few that four CTAs share a tile's K, the stream is still
 // the better one: 128 rows x 4096 x 12288 take 18 us, 30 with 128 x 128 tiles.
 //
 // Among tiles the fewest waves win, each worth its time: at K = 4096 a wave of 128 x 128 tiles takes
 // 10 us, of 128 x 256 18 (its weights and rows need most of what L2 gives), of pairs 13.7.
-// 512 rows x 4096 x 4096 take 12.8, 14.6, 14.1 us; 128 rows x 24576 27.3, 23.9, 33.3; 512 rows x 24576
-// 60, 54, 46.
+// 512 rows x 4096 x 4096 take 12.6, 14.6, 14.1 us; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60,
+// 54, 46.
 int choose(const Linear& p, cudaStream_t st) {
-  const int nsm = p.sms, rows = (p.m + p.groups - 1) / p.groups;
+  const int rows = (p.m + p.groups - 1) / p.groups;
   if (rows <= 16) return run_stream(p, 16, st);
   if (rows <= 32) return run_stream(p, 32, st);
-  if (rows <= (!p.start ? 64 : p.rows ? 512 : 192)) return run_stream(p, 64, st);
-  if (rows <= 128 && most_tiles(p, 64, 128) <= nsm / 2) return run_stream(p, 64, st);
+  if (rows <= (p.rows ? 96 : 64)) return run_stream(p, 64, st);
+  if (p.start)
+    return run_tiles(p, rows <= 320 ? Tiles::k128x256 : Tiles::k256x256, st);
+  if (rows <= 128 && most_tiles(p, 64, 128) <= p.sms / 2) return run_stream(p, 64, st);
   const auto cost = [&](int tile_rows, int features, int at_once, double wave) {
     const long long tiles = most_tiles(p, tile_rows, features);
     return static_cast<double>((tiles + at_once - 1) / at_once) * wave;
   };
-  const double small = cost(128, 128, nsm, 10), wide = cost(128, 256, nsm, 18),
-               pair = cost(256, 256, nsm / 2, 13.7);
+  const double small = cost(128, 128, p.sms, 10), wide = cost(128, 256, p.sms, 18),
+               pair = cost(256, 256, p.sms / 2, 13.7);
   if (small <= wide && small <= pair) return run_tiles(p, Tiles::k128x128, st);
   return run_tiles(p, wide < pair ? Tiles::k128x256 : Tiles::k256x256, st);
 }

@@ -457,7 +457,8 @@ int run(Linear p, cudaStream_t st) {
 int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st) {
   const bool index = p.rows != nullptr;
 #define DFLASH_RUN(kPair, kN) (index ? run<kPair, kN, true>(p, st) : run<kPair, kN, false>(p, st))
-  if (tiles == Tiles::k128x128) return DFLASH_RUN(false, 128);
+  if (tiles == Tiles::k128x128)          // (plain products only)
+    return index ? DFLASH_E_UNSUPPORTED : run<false, 128, false>(p, st);
   if (tiles == Tiles::k128x256) return DFLASH_RUN(false, 256);
   return DFLASH_RUN(true, 256);
 #undef DFLASH_RUN
