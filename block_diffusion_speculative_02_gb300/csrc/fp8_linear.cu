@@ -24,7 +24,9 @@ namespace {
 // 10 us, of 128 x 256 18 (its weights and rows need most of what L2 gives), of pairs 13.7.
 // 512 rows x 4096 x 4096 take 12.6, 14.6, 14.1 us; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60,
 // 54, 46.
-int choose(const Linear& p, cudaStream_t st) {
+int choose(Linear& p, cudaStream_t st) {
+  p.sms = current_num_sms();
+  if (p.sms <= 0) return DFLASH_E_CUDA;
   const int rows = (p.m + p.groups - 1) / p.groups;
   if (rows <= 16) return run_stream(p, 16, st);
   if (rows <= 32) return run_stream(p, 32, st);
@@ -76,8 +78,6 @@ int check(int m, int n_src, int groups, int n, int k, const void* x, const float
   p->k_blocks = static_cast<int>(blocks(k));
   p->n_blocks = static_cast<int>(blocks(n));
   p->vector = aligned16(out) && out_pitch % 8 == 0;
-  p->sms = current_num_sms();
-  if (p->sms <= 0) return DFLASH_E_CUDA;
   return DFLASH_OK;
 }
 

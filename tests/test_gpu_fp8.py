@@ -534,3 +534,97 @@ def test_large_offsets():
         wv = O.weight_value(codes(w), wscale.cpu().numpy())
         check_product(f64(out[lo:lo + 40]), xv, wv)
     assert bool((out.abs().amax(1) > 0).all())
+
+
+# --------------------------------------------------------------------------------------------
+# refusals of the binding
+# --------------------------------------------------------------------------------------------
+def test_binding_refuses_and_touches_nothing():
+    dfl = _dfl()
+    m, n, k, e = 8, 96, 256, 3
+    x = torch.zeros(m, k, dtype=BF, device="cuda")
+    q, s = dfl.alloc_fp8_rows(m, k)
+    w, wscale = dfl.alloc_fp8_weight(e, n, k)
+    out, ws = torch.full((m, n), 3.0, dtype=BF, device="cuda"), dfl.alloc_fp8_workspace()
+    start = i32([0, 2, 2, m])
+    linear = lambda **c: dfl.dflash_fp8_linear(*{**dict(  # noqa: E731
+        x=q, x_scale=s, w=w[0], w_scale=wscale[0], out=out, ws=ws), **c}.values())
+    grouped = lambda **c: dfl.dflash_fp8_grouped(*{**dict(  # noqa: E731
+        x=q, x_scale=s, w=w, w_scale=wscale, start=start, rows=None, out=out, ws=ws), **c}.values())
+    norm = lambda **c: dfl.dflash_fp8_norm_rows(*{**dict(  # noqa: E731
+        x=x, residual=None, norm_w=None, rms_eps=1e-6, sum_out=None, q=q, scale=s), **c}.values())
+    for f, bad in ((linear, dict(x=x)), (linear, dict(x=q.t())), (linear, dict(x_scale=s.t())),
+                   (linear, dict(w=w)), (linear, dict(w_scale=wscale)), (linear, dict(out=out.t())),
+                   (linear, dict(out=out.float())), (linear, dict(ws=ws.int())),
+                   (linear, dict(w=w[0, :, :128])), (linear, dict(x=q.cpu())),
+                   (linear, dict(x=None)), (linear, dict(out=out[:, :95])),
+                   (grouped, dict(start=start.long())), (grouped, dict(start=start[:3])),
+                   (grouped, dict(rows=start)), (grouped, dict(out=out[:4])),
+                   (grouped, dict(w=w[0])), (grouped, dict(out=None)),
+                   (norm, dict(x=x[:, ::2])), (norm, dict(residual=x[:4])),
+                   (norm, dict(norm_w=x[0, :128])), (norm, dict(q=x)), (norm, dict(scale=s[:1])),
+                   (norm, dict(x=x.cpu())), (norm, dict(sum_out=x.float()))):
+        with pytest.raises(ValueError):
+            f(**bad)
+    for f, bad in ((linear, dict(ws=ws[:32])), (norm, dict(rms_eps=-1.0))):
+        with pytest.raises(dfl.DFlashError):
+            f(**bad)
+    odd = torch.zeros(4, 200, dtype=BF, device="cuda")               # 200 is no multiple of 16
+    with pytest.raises(dfl.DFlashError):
+        dfl.dflash_fp8_norm_rows(odd, None, None, 0.0, None, *dfl.alloc_fp8_rows(4, 200))
+    with pytest.raises(dfl.DFlashError):                             # a pitch of no multiple of 8
+        dfl.dflash_fp8_norm_rows(torch.zeros(4, 250, dtype=BF, device="cuda")[:, :240], None, None,
+                                 0.0, None, *dfl.alloc_fp8_rows(4, 240))
+    with pytest.raises(ValueError):
+        dfl.dflash_fp8_silu_mul(torch.zeros(4, 33, dtype=BF, device="cuda"), q, s)
+    torch.cuda.synchronize()
+    assert bool((out == 3).all()) and dfl.dflash_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("m", [16, 300])
+def test_first_use_inside_a_capture(m):
+    """A graph that holds the calls alone, replayed on a stream of its own."""
+    dfl = _dfl()
+    rng = np.random.default_rng(m)
+    x, xs, xv = random_x(rng, m, 512)
+    w, wscale, wv = random_w(rng, 640, 512)
+    out, ws = torch.zeros(m, 640, dtype=BF, device="cuda"), dfl.alloc_fp8_workspace()
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        dfl.dflash_fp8_linear(x, xs, w, wscale, out, ws)
+        dfl.dflash_fp8_linear(x, xs, w, wscale, out, ws)
+    with torch.cuda.stream(stream):
+        graph.replay()
+    stream.synchronize()
+    check_product(f64(out), xv, wv)
+
+
+def test_rows_of_x_given_many_times():
+    """One row of x for every row of out, and each expert with its own number of them."""
+    dfl = _dfl()
+    rng = np.random.default_rng(8)
+    for m in (64, 2000):
+        x, xs, xv = random_x(rng, 3, 384)
+        w, wscale, wv = random_w(rng, 2, 260, 384)
+        out = torch.zeros(m, 260, dtype=BF, device="cuda")
+        dfl.dflash_fp8_grouped(x, xs, w, wscale, i32([0, m // 3, m]), i32(np.full(m, 2)), out,
+                               dfl.alloc_fp8_workspace())
+        got = f64(out)
+        assert (got[:m // 3] == got[0]).all() and (got[m // 3:] == got[-1]).all()
+        check_product(got[:1], xv[2:], wv[0])
+        check_product(got[-1:], xv[2:], wv[1])
+
+
+def test_neighbours_of_a_small_row_range_stay():
+    """x of fewer rows than a tile, inside a larger array whose other rows hold NaN."""
+    dfl = _dfl()
+    rng = np.random.default_rng(9)
+    for m in (1, 5, 33, 70, 100):
+        x, xs, xv = random_x(rng, m, 256)
+        big = torch.full((m + 300, 256), 0x7F, dtype=torch.uint8, device="cuda")
+        big[:m] = x.view(torch.uint8)
+        w, wscale, wv = random_w(rng, 1300, 256)
+        out = torch.zeros(m, 1300, dtype=BF, device="cuda")
+        dfl.dflash_fp8_linear(big.view(F8)[:m], xs, w, wscale, out, dfl.alloc_fp8_workspace())
+        check_product(f64(out), xv, wv)
