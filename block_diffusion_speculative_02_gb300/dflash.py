@@ -704,7 +704,7 @@ def dflash_kv4_attention(dims: KV4Dims, q, start, cache: KV4View, scale: float, 
 # ---------------------------------------------------------------------------
 # linear layers in 8-bit floating point
 # ---------------------------------------------------------------------------
-F8 = torch.float8_e4m3fn
+F8, _BF, _F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
 
 
 def _up128(n: int) -> int:
@@ -739,17 +739,29 @@ def _whole(t, device: int, dtype, shape, name: str) -> int:
     return t.data_ptr()
 
 
+def _codes(q, scale, device: int, shape, scales, name: str, scale_name: str):
+    """Pointers of e4m3 codes and their fp32 scales, both contiguous.  (Checked in one expression;
+    where it does not hold, one by one, to say what is wrong.)"""
+    try:
+        if q.dtype is F8 and scale.dtype is _F32 and q.shape == shape and scale.shape == scales \
+                and q.is_contiguous() and scale.is_contiguous() and q.get_device() == device \
+                and scale.get_device() == device:
+            return q.data_ptr(), scale.data_ptr()
+    except AttributeError:
+        pass
+    return _whole(q, device, F8, shape, name), _whole(scale, device, _F32, scales, scale_name)
+
+
 def _matrix(t, device: int, name: str, shape):
     """(pointer, row pitch) of a bf16 matrix whose rows are contiguous and may lie apart."""
-    if getattr(t, "dtype", None) is not torch.bfloat16 or t.get_device() != device:
+    if getattr(t, "dtype", None) is not _BF or t.get_device() != device:
         raise ValueError(f"{name} must be a bf16 tensor on cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    rows, cols = shape
     pitch, step = t.stride()
-    if step != 1 and cols > 1:
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the columns of a row must be contiguous")
-    return t.data_ptr(), pitch if rows > 1 else cols
+    return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
 
 
 def _shape(t, dims: int, name: str):
@@ -760,10 +772,6 @@ def _shape(t, dims: int, name: str):
     return shape
 
 
-def _matrix_opt(t, device: int, name: str, shape):
-    return (None, 0) if t is None else _matrix(t, device, name, shape)
-
-
 def dflash_fp8_norm_rows(x, residual, norm_w, rms_eps: float, sum_out, q, scale, stream=None):
     """q, scale = 8-bit rows of RMSNorm(x + residual) * norm_w; sum_out = x + residual.
 
@@ -771,10 +779,11 @@ def dflash_fp8_norm_rows(x, residual, norm_w, rms_eps: float, sum_out, q, scale,
     dev, st = _here(stream)
     shape = rows, cols = _shape(x, 2, "x")
     rc = load_library().dflash_fp8_norm_rows(
-        rows, cols, *_matrix(x, dev, "x", shape), *_matrix_opt(residual, dev, "residual", shape),
-        None if norm_w is None else _whole(norm_w, dev, torch.bfloat16, (cols,), "norm_w"),
-        rms_eps, *_matrix_opt(sum_out, dev, "sum_out", shape), _whole(q, dev, F8, shape, "q"),
-        _whole(scale, dev, torch.float32, (_up128(cols), rows), "scale"), st)
+        rows, cols, *_matrix(x, dev, "x", shape),
+        *((None, 0) if residual is None else _matrix(residual, dev, "residual", shape)),
+        None if norm_w is None else _whole(norm_w, dev, _BF, (cols,), "norm_w"), rms_eps,
+        *((None, 0) if sum_out is None else _matrix(sum_out, dev, "sum_out", shape)),
+        *_codes(q, scale, dev, shape, (-(-cols // 128), rows), "q", "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_norm_rows")
 
@@ -787,8 +796,8 @@ def dflash_fp8_silu_mul(gate_up, q, scale, stream=None):
         raise ValueError("gate_up must have an even number of columns: gate, then up")
     cols //= 2
     rc = load_library().dflash_fp8_silu_mul(
-        rows, cols, *_matrix(gate_up, dev, "gate_up", shape), _whole(q, dev, F8, (rows, cols), "q"),
-        _whole(scale, dev, torch.float32, (_up128(cols), rows), "scale"), st)
+        rows, cols, *_matrix(gate_up, dev, "gate_up", shape),
+        *_codes(q, scale, dev, (rows, cols), (-(-cols // 128), rows), "q", "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_silu_mul")
 
@@ -796,13 +805,13 @@ def dflash_fp8_silu_mul(gate_up, q, scale, stream=None):
 def dflash_fp8_weight(w, q, scale, stream=None):
     """q, scale = 8-bit weights of w, bf16 [N, K] or, of several experts, [G, N, K]."""
     dev, st = _here(stream)
-    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+    shape = getattr(w, "shape", ())
+    if len(shape) not in (2, 3):
         raise ValueError("w must be a tensor [N, K] or [G, N, K]")
-    *g, n, k = w.shape
+    *g, n, k = shape
     rc = load_library().dflash_fp8_weight(
-        g[0] if g else 1, n, k, _whole(w, dev, torch.bfloat16, w.shape, "w"),
-        _whole(q, dev, F8, w.shape, "q"),
-        _whole(scale, dev, torch.float32, (*g, _up128(n), _up128(k)), "scale"), st)
+        g[0] if g else 1, n, k, _whole(w, dev, _BF, shape, "w"),
+        *_codes(q, scale, dev, shape, (*g, -(-n // 128), -(-k // 128)), "q", "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_weight")
 
@@ -814,11 +823,10 @@ def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
     n, kw = _shape(w, 2, "w")
     if kw != k:
         raise ValueError(f"x has {k} columns, w {kw}")
-    kb = _up128(k)
+    kb = -(-k // 128)
     rc = load_library().dflash_fp8_linear(
-        m, n, k, _whole(x, dev, F8, x.shape, "x"),
-        _whole(x_scale, dev, torch.float32, (kb, m), "x_scale"), _whole(w, dev, F8, w.shape, "w"),
-        _whole(w_scale, dev, torch.float32, (_up128(n), kb), "w_scale"),
+        m, n, k, *_codes(x, x_scale, dev, (m, k), (kb, m), "x", "x_scale"),
+        *_codes(w, w_scale, dev, (n, k), (-(-n // 128), kb), "w", "w_scale"),
         *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
     if rc:
         _check(rc, "dflash_fp8_linear")
@@ -832,14 +840,12 @@ def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None
     e, n, kw = _shape(w, 3, "w")
     if kw != k:
         raise ValueError(f"x has {k} columns, w {kw}")
-    m, kb = _shape(out, 2, "out")[0], _up128(k)
+    m, kb = _shape(out, 2, "out")[0], -(-k // 128)
     if rows is None and m != src:
         raise ValueError(f"out has {m} rows, x {src}: rows must say which")
     rc = load_library().dflash_fp8_grouped(
-        m, src, e, n, k, _whole(x, dev, F8, x.shape, "x"),
-        _whole(x_scale, dev, torch.float32, (kb, src), "x_scale"),
-        _whole(w, dev, F8, w.shape, "w"),
-        _whole(w_scale, dev, torch.float32, (e, _up128(n), kb), "w_scale"),
+        m, src, e, n, k, *_codes(x, x_scale, dev, (src, k), (kb, src), "x", "x_scale"),
+        *_codes(w, w_scale, dev, (e, n, k), (e, -(-n // 128), kb), "w", "w_scale"),
         _whole(start, dev, torch.int32, (e + 1,), "start"),
         None if rows is None else _whole(rows, dev, torch.int32, (m,), "rows"),
         *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
