@@ -1,5 +1,7 @@
 // Products of rows and weights held in 8 bits (e4m3) with a scale for each block of 128, plain
 // and grouped by expert: the entry points, and which kernel takes a call.
+#include <algorithm>
+
 #include "fp8_linear.cuh"
 
 namespace dflash {
@@ -8,40 +10,44 @@ namespace {
 
 // Which kernel takes a call; `rows`: of an expert, on average.
 //
-// Up to 64 rows the weights are streamed, with the smallest tile that holds the rows: 16 rows x
-// 4096 x 4096 take 6.1, 7.0, 11.1 us with tiles of 16, 32, 64 rows (128 x 128 tiles: 18), 64 rows
-// 10.6, 8.7, 8.9 (11.5).
+// By expert (rows of 128 experts x 1536 x 2048 by index, in us): 4 rows each take 53, 51, 52 with the
+// stream's tiles of 16, 32, 64 rows; 16 rows 60, 59, 58; 32 rows 81, 64, 65, and 109 with 128 x 256
+// tiles; 80 rows 89 with 64 rows and 98; 192 rows 162, 153, and 155 with pairs; 384 rows 292, 247, 231.
+// (8 experts x 4096 x 2048, 8 rows each: 9.7, 10.7, 13.8; 24 rows 14, 10.8, 13.9.)  Rows in order
+// reach the tiles sooner: 80 rows 80 and 80, 256 rows 150, 126, 131, 512 rows 206 with 128 x 256 and
+// 201 with pairs.
 //
-// By expert (rows of 128 experts x 1536 x 2048 by index, in us): 32 rows each take 81, 66, 64 with
-// tiles of 16, 32, 64 rows, 109 with 128 x 256; 80 rows 89 and 98; 192 rows 162, 153 and 155 with
-// pairs; 384 rows 292, 247, 231.  Rows in order reach the tiles sooner: 80 rows 80 and 80, 256 rows
-// 150, 126, 131, 512 rows 206 with 128 x 256 and 201 with pairs.
-//
-// Up to 128 rows, where features are so few that four CTAs share a tile's K, the stream is still
-// the better one: 128 rows x 4096 x 12288 take 18 us, 30 with 128 x 128 tiles.
-//
-// Among tiles the fewest waves win, each worth its time: at K = 4096 a wave of 128 x 128 tiles takes
-// 10 us, of 128 x 256 18 (its weights and rows need most of what L2 gives), of pairs 13.7.
-// 512 rows x 4096 x 4096 take 12.6, 14.6, 14.1 us; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60,
-// 54, 46.
+// Plain: up to 64 rows the weights are streamed, with the smallest tile that holds the rows (24
+// rows x 4096 x 4096: 7.9, 6.6, 7.5 us, 11.4 with 128 x 128 tiles), or in two of 32 rows; more rows where the
+// estimates say so: few features leave SMs without a tile (128 rows x 4096 x 12288 take 17 us in
+// shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4).  Among tiles the fewest waves win, each
+// worth its time: 512 rows x 4096 x 4096 take 12.6 us with 128 x 128 tiles, 14.6 with 128 x 256, 14.1
+// with pairs; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60, 54, 46.
 int choose(Linear& p, cudaStream_t st) {
   p.sms = current_num_sms();
   if (p.sms <= 0) return DFLASH_E_CUDA;
   const int rows = (p.m + p.groups - 1) / p.groups;
+  if (p.start) {
+    if (rows <= 8) return run_stream(p, 16, st);
+    if (rows <= 32) return run_stream(p, 32, st);
+    if (rows <= (p.rows ? 96 : 64)) return run_stream(p, 64, st);
+    return run_tiles(p, rows <= 320 ? Tiles::k128x256 : Tiles::k256x256, st);
+  }
   if (rows <= 16) return run_stream(p, 16, st);
   if (rows <= 32) return run_stream(p, 32, st);
-  if (rows <= (p.rows ? 96 : 64)) return run_stream(p, 64, st);
-  if (p.start)
-    return run_tiles(p, rows <= 320 ? Tiles::k128x256 : Tiles::k256x256, st);
-  if (rows <= 128 && most_tiles(p, 64, 128) <= p.sms / 2) return run_stream(p, 64, st);
-  const auto cost = [&](int tile_rows, int features, int at_once, double wave) {
+  // us: the start, and the waves of a tile's blocks
+  const auto cost = [&](int tile_rows, int features, int at_once, double start, double block) {
     const long long tiles = most_tiles(p, tile_rows, features);
-    return static_cast<double>((tiles + at_once - 1) / at_once) * wave;
+    return start + static_cast<double>((tiles + at_once - 1) / at_once) * p.k_blocks * block;
   };
-  const double small = cost(128, 128, p.sms, 10), wide = cost(128, 256, p.sms, 18),
-               pair = cost(256, 256, p.sms / 2, 13.7);
-  if (small <= wide && small <= pair) return run_tiles(p, Tiles::k128x128, st);
-  return run_tiles(p, wide < pair ? Tiles::k128x256 : Tiles::k256x256, st);
+  const double small = cost(128, 128, p.sms, 2.6, 0.30), wide = cost(128, 256, p.sms, 5.5, 0.48),
+               pair = cost(256, 256, p.sms / 2, 4.5, 0.43);
+  const double tiles = std::min(small, std::min(wide, pair));
+  const double thin = stream_cost(p, 32), thick = stream_cost(p, 64);
+  if (rows <= 64 || std::min(thin, thick) < tiles)
+    return run_stream(p, thin < thick ? 32 : 64, st);
+  return run_tiles(p, tiles == small ? Tiles::k128x128
+                      : tiles == wide ? Tiles::k128x256 : Tiles::k256x256, st);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

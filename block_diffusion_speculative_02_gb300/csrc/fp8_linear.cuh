@@ -448,6 +448,8 @@ enum class Tiles { k128x128, k128x256, k256x256 };
 int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st);
 // At most `rows` (16, 32 or 64) rows at a time against weights streamed once.
 int run_stream(const Linear& p, int rows, cudaStream_t st);
+// About how many us that takes.
+double stream_cost(const Linear& p, int rows);
 
 }  // namespace fp8
 }  // namespace dflash

@@ -6,6 +6,9 @@
 // end hide behind the other's stream.  Where there are fewer tiles than that, the CTAs of a
 // cluster take a share of K each; they add their sums through distributed shared memory, in the
 // order of the shares.
+#include <algorithm>
+#include <cmath>
+
 #include "fp8_linear.cuh"
 
 namespace dflash {
@@ -30,6 +33,33 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
   return v;
+}
+
+// This CTA's rows of a tile, every kSplit-th: the sums of the kSplit CTAs, in their order.  32 loads
+// are on their way at a time: with two rows' the joining of 128 rows x 2560 features in two shares
+// took 4 us.
+template <int kSplit>
+__device__ __forceinline__ void join_shares(const Linear& p, uint32_t part, int row, int rows,
+                                            int n, int rank) {
+  constexpr int kAtOnce = 32 / kSplit;
+  for (int j = rank; j < rows; j += kAtOnce * kSplit) {
+    float v[kAtOnce][kSplit];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+      for (int r = 0; r < kSplit; ++r)
+        v[i][r] = j + i * kSplit < rows ? ld_cluster(part + (j + i * kSplit) * 512, r) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (j + i * kSplit >= rows) break;
+      float sum = v[i][0];
+#pragma unroll
+      for (int r = 1; r < kSplit; ++r) sum += v[i][r];
+      if (n < p.n)
+        p.out[static_cast<long long>(row + j + i * kSplit) * p.out_pitch + n] =
+            float_to_bf16_bits(sum);
+    }
+  }
 }
 
 template <int kT, bool kIndex>
@@ -321,27 +351,12 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     if (warp >= 2 && warp < 6 && ok && t_first < total) {
       const int n = tile.z * 128 + et;
       const uint32_t part = smem_u32(smem) + et * 4;
-      // two rows at a time, all shares of both on their way together
-      for (int j = rank; j < tile.y; j += 2 * split) {
-        float v[2][kMaxSplit];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < kMaxSplit; ++r)
-            v[i][r] = r < split && j + i * split < tile.y
-                          ? ld_cluster(part + (j + i * split) * 512, r) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (j + i * split >= tile.y) break;
-          float sum = v[i][0];
-#pragma unroll
-          for (int r = 1; r < kMaxSplit; ++r)
-            if (r < split) sum += v[i][r];
-          if (n < p.n)
-            p.out[static_cast<long long>(tile.x + j + i * split) * p.out_pitch + n] =
-                float_to_bf16_bits(sum);
-        }
-      }
+      if (split == 2)
+        join_shares<2>(p, part, tile.x, tile.y, n, rank);
+      else if (split == 4)
+        join_shares<4>(p, part, tile.x, tile.y, n, rank);
+      else
+        join_shares<8>(p, part, tile.x, tile.y, n, rank);
     }
     __syncwarp();
     cluster_sync();
@@ -353,22 +368,33 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   }
 }
 
-// CTAs that share a tile's K: the fewest time units, where a wave (two CTAs to an SM) costs its
-// blocks of K and kStreamStart for the start, the end and the joining.
-constexpr int kStreamStart = 6;
-
-int stream_split(const Linear& p, long long tiles, int nsm) {
-  int best = 1;
-  long long cost = 0;
+// CTAs that share a tile's K, and about how many us the call takes.  A CTA takes some 0.2 us a block
+// (0.33 with 64 rows) where the memory has time for it, a quarter more with another on its SM; all
+// together 2.4 ns a block of weights at the memory's rate, 0.4 where another tile's rows need the
+// same weights.  Whole tiles follow one another without a pause; shares of K are joined in 1 to 2
+// us, and a second wave of them costs 4 more: 16 rows x 4096 x 4096 (32 tiles of 32 blocks) take
+// 7.4, 6.6, 6.3 us in two, four, eight shares, 64 rows 8.2, 8.2, 13.2; 16 rows x 49152 x 4096 (384 tiles)
+// 34 us whole and 43 in two shares.
+double stream_split(const Linear& p, int tile_rows, int* split) {
+  const double tiles = static_cast<double>(most_tiles(p, tile_rows, 128));
+  const double first = static_cast<double>(most_tiles(p, p.m, 128));      // of an expert each
+  const double block = 0.16 + tile_rows * 0.0026, join = 1.0 + tile_rows / 64.0;
+  const double memory = (0.0024 * first + 0.0004 * (tiles - first)) * p.k_blocks;
+  double cost = 0;
   for (int s = 1; s <= kMaxSplit && s <= p.k_blocks; s *= 2) {
-    const long long waves = (tiles * s + 2 * nsm - 1) / (2 * nsm);
-    const long long c = waves * ((p.k_blocks + s - 1) / s + kStreamStart);
+    const double ctas = tiles * s, waves = std::ceil(ctas / (2 * p.sms));
+    const double work =
+        waves * ((p.k_blocks + s - 1) / s) * block * (ctas > p.sms ? 1.25 : 1.0);
+    // (fewer than three CTAs to two SMs do not draw all that the memory gives)
+    const double drawn = memory * (ctas * 2 < 3 * p.sms ? 1.15 : 1.0);
+    double c = 3.0 + std::max(work, drawn);
+    if (s > 1) c += join + 4.0 * (waves - 1);
     if (s == 1 || c < cost) {
-      best = s;
+      *split = s;
       cost = c;
     }
   }
-  return best;
+  return cost;
 }
 
 template <int kT, bool kIndex>
@@ -390,7 +416,8 @@ int run(Linear p, cudaStream_t st) {
   const int nsm = p.sms;
   const long long tiles = most_tiles(p, kT, 128);
   if (tiles > 0x7FFFFFFF / 16) return DFLASH_E_UNSUPPORTED;
-  const int split = stream_split(p, tiles, nsm);
+  int split;
+  stream_split(p, kT, &split);
   // shares of K: one tile to a cluster; whole tiles: two CTAs to an SM walk them
   const long long ctas = split > 1 ? tiles * split : tiles < 2 * nsm ? tiles : 2 * nsm;
   cudaLaunchConfig_t cfg = {};
@@ -411,6 +438,11 @@ int run(Linear p, cudaStream_t st) {
 }
 
 }  // namespace
+
+double stream_cost(const Linear& p, int rows) {
+  int split;
+  return stream_split(p, rows, &split);
+}
 
 int run_stream(const Linear& p, int rows, cudaStream_t st) {
   const bool index = p.rows != nullptr;
