@@ -10,19 +10,19 @@ namespace {
 
 // Which kernel takes a call; `rows`: of an expert, on average.
 //
-// By expert (rows of 128 experts x 1536 x 2048 by index, in us): 4 rows each take 53, 51, 52 with the
-// stream's tiles of 16, 32, 64 rows; 16 rows 60, 59, 58; 32 rows 81, 64, 65, and 109 with 128 x 256
-// tiles; 80 rows 89 with 64 rows and 98; 192 rows 162, 153, and 155 with pairs; 384 rows 292, 247, 231.
-// (8 experts x 4096 x 2048, 8 rows each: 9.7, 10.7, 13.8; 24 rows 14, 10.8, 13.9.)  Rows in order
-// reach the tiles sooner: 80 rows 80 and 80, 256 rows 150, 126, 131, 512 rows 206 with 128 x 256 and
-// 201 with pairs.
+// By expert (rows of 128 experts x 1536 x 2048 by index, in us): 4 rows each take 53, 51, 52 with
+// the stream's tiles of 16, 32, 64 rows; 16 rows 60, 59, 58; 32 rows 81, 64, 65, and 109 with
+// 128 x 256 tiles; 80 rows 89 with 64 rows and 98; 192 rows 162, 153, and 155 with pairs; 384 rows
+// 292, 247, 231.  (8 experts x 4096 x 2048, 8 rows each: 9.7, 10.7, 13.8; 24 rows 14, 10.8, 13.9.)
+// Rows in order reach the tiles sooner: 80 rows 80 and 80, 256 rows 150, 126, 131, 512 rows 206
+// with 128 x 256 and 201 with pairs.
 //
 // Plain: up to 64 rows the weights are streamed, with the smallest tile that holds the rows (24
-// rows x 4096 x 4096: 7.9, 6.6, 7.5 us, 11.4 with 128 x 128 tiles), or in two of 32 rows; more rows where the
-// estimates say so: few features leave SMs without a tile (128 rows x 4096 x 12288 take 17 us in
-// shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4).  Among tiles the fewest waves win, each
-// worth its time: 512 rows x 4096 x 4096 take 12.6 us with 128 x 128 tiles, 14.6 with 128 x 256, 14.1
-// with pairs; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60, 54, 46.
+// rows x 4096 x 4096: 7.9, 6.6, 7.5 us, 11.4 with 128 x 128 tiles), or in two of 32 rows; more
+// rows where the estimates say so: few features leave SMs without a tile (128 rows x 4096 x 12288
+// take 17 us in shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4).  Among tiles the fewest
+// waves win, each worth its time: 512 rows x 4096 x 4096 take 12.6 us with 128 x 128 tiles, 14.6
+// with 128 x 256, 14.1 with pairs; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60, 54, 46.
 int choose(Linear& p, cudaStream_t st) {
   p.sms = current_num_sms();
   if (p.sms <= 0) return DFLASH_E_CUDA;

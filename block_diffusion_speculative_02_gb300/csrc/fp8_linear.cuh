@@ -117,9 +117,10 @@ __device__ __forceinline__ void mma_done(uint64_t* bar) {
 template <bool kPair>
 __device__ __forceinline__ void mma_done_here(uint64_t* bar) {
   if (kPair)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(bar))
+        : "memory");
   else
     umma_commit(bar);
 }
@@ -340,8 +341,8 @@ __device__ __forceinline__ int source_row(const Linear& p, const Tile& tile, int
   return -1;
 }
 
-// Where rows named by an index are, for the copies: row r of kRows at sources[place_of(r)], in units
-// of 16 bytes from x on, or kNoRow (zeros).  The rows that eight lanes copy lie side by side.
+// Where rows named by an index are, for the copies: row r of kRows at sources[place_of(r)], in
+// units of 16 bytes from x on, or kNoRow (zeros).  The rows that eight lanes copy lie side by side.
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 template <int kRows>
@@ -350,8 +351,8 @@ __device__ __forceinline__ int place_of(int r) {
 }
 
 // By one warp: block columns col .. col + 127 of kRows rows of x (from row `first` of kOf on), into
-// the order of the 128-byte swizzle.  Few instructions a copy count here: the warp has few turns and
-// registers.
+// the order of the 128-byte swizzle.  Few instructions a copy count here: the warp has few turns
+// and registers.
 template <int kRows, int kOf>
 __device__ __forceinline__ void copy_rows(const Linear& p, uint8_t* dst, int col,
                                           const uint32_t* sources, int first, int lane) {
@@ -411,8 +412,8 @@ struct RowCopies {
       if (++pending > kCopyLag) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kCopyLag) : "memory");
         land(p, arrive);
-      } else if (pending == static_cast<uint32_t>(p.n_stages)) {   // (the next stage waits for them)
-        finish(p, arrive);
+      } else if (pending == static_cast<uint32_t>(p.n_stages)) {
+        finish(p, arrive);               // (the next stage waits for them)
       }
     }
     return true;

@@ -35,9 +35,9 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// This CTA's rows of a tile, every kSplit-th: the sums of the kSplit CTAs, in their order.  32 loads
-// are on their way at a time: with two rows' the joining of 128 rows x 2560 features in two shares
-// took 4 us.
+// This CTA's rows of a tile, every kSplit-th: the sums of the kSplit CTAs, in their order.  32
+// loads are on their way at a time: with two rows' the joining of 128 rows x 2560 features in two
+// shares took 4 us.
 template <int kSplit>
 __device__ __forceinline__ void join_shares(const Linear& p, uint32_t part, int row, int rows,
                                             int n, int rank) {
@@ -333,7 +333,8 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           uint16_t* dst = p.out + static_cast<long long>(tile.x) * p.out_pitch + n;
 #pragma unroll
           for (int j = 0; j < kT; ++j) {
-            if (j < tile.y) *dst = float_to_bf16_bits(j & 1 ? halves(acc[j / 2]).y : halves(acc[j / 2]).x);
+            if (j < tile.y)
+              *dst = float_to_bf16_bits(j & 1 ? halves(acc[j / 2]).y : halves(acc[j / 2]).x);
             dst += p.out_pitch;
           }
         }
@@ -341,7 +342,8 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         // (every copy and product of this CTA is done: the stages are free)
         float* part = reinterpret_cast<float*>(smem) + et;
 #pragma unroll
-        for (int j = 0; j < kT; ++j) part[j * 128] = j & 1 ? halves(acc[j / 2]).y : halves(acc[j / 2]).x;
+        for (int j = 0; j < kT; ++j)
+          part[j * 128] = j & 1 ? halves(acc[j / 2]).y : halves(acc[j / 2]).x;
       }
     }
   }
@@ -368,13 +370,13 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   }
 }
 
-// CTAs that share a tile's K, and about how many us the call takes.  A CTA takes some 0.2 us a block
-// (0.33 with 64 rows) where the memory has time for it, a quarter more with another on its SM; all
-// together 2.4 ns a block of weights at the memory's rate, 0.4 where another tile's rows need the
-// same weights.  Whole tiles follow one another without a pause; shares of K are joined in 1 to 2
-// us, and a second wave of them costs 4 more: 16 rows x 4096 x 4096 (32 tiles of 32 blocks) take
-// 7.4, 6.6, 6.3 us in two, four, eight shares, 64 rows 8.2, 8.2, 13.2; 16 rows x 49152 x 4096 (384 tiles)
-// 34 us whole and 43 in two shares.
+// CTAs that share a tile's K, and about how many us the call takes.  A CTA takes some 0.2 us a
+// block (0.33 with 64 rows) where the memory has time for it, a quarter more with another on its
+// SM; all together 2.4 ns a block of weights at the memory's rate, 0.4 where another tile's rows
+// need the same weights.  Whole tiles follow one another without a pause; shares of K are joined in
+// 1 to 2 us, and a second wave of them costs 4 more: 16 rows x 4096 x 4096 (32 tiles of 32 blocks)
+// take 7.4, 6.6, 6.3 us in two, four, eight shares, 64 rows 8.2, 8.2, 13.2; 16 rows x 49152 x 4096
+// (384 tiles) 34 us whole and 43 in two shares.
 double stream_split(const Linear& p, int tile_rows, int* split) {
   const double tiles = static_cast<double>(most_tiles(p, tile_rows, 128));
   const double first = static_cast<double>(most_tiles(p, p.m, 128));      // of an expert each
@@ -402,7 +404,8 @@ int run(Linear p, cudaStream_t st) {
   p.n_tiles = (p.n + 127) / 128;
   p.box_rows = p.n_src < kT ? p.n_src : kT;
   const int tail = kFactors * kT * 4 + kInfo * (16 + kT * 4) +
-                   (2 * kStreamBufs + 2 * kFactors + 2 * kInfo + 1) * 8 + 4 + groups_bytes(p.groups);
+                   (2 * kStreamBufs + 2 * kFactors + 2 * kInfo + 1) * 8 + 4 +
+                   groups_bytes(p.groups);
   p.n_stages = (kStreamSmem - 1024 - tail) / (stream_stage_bytes<kT>() + 16);
   if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
   const int smem = 1024 + p.n_stages * (stream_stage_bytes<kT>() + 16) + tail;

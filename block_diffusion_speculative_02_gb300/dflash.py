@@ -817,7 +817,7 @@ def dflash_fp8_weight(w, q, scale, stream=None):
 
 
 def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
-    """out [M, N] (bf16, rows may be strided) = x w^T of 8-bit rows x [M, K] and weights w [N, K]."""
+    """out [M, N] (bf16, rows may be strided) = x w^T of 8-bit rows x [M, K], weights w [N, K]."""
     dev, st = _here(stream)
     m, k = _shape(x, 2, "x")
     n, kw = _shape(w, 2, "w")
