@@ -126,6 +126,17 @@ struct SiluParams {
 
 constexpr int kSiluThreads = 256;
 
+// g / (1 + exp(-g)) as (g / 8) / (1 / 8 + exp(-g) / 8): a divisor past 2^126 has no reciprocal
+// but zero, and exp(-g) reaches 2^128.
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2e = 1.44269504f;
+  const float t = g * 0.125f;
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(t, -8.f * kLog2e, -3.f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.125f + e));
+  return t * r;
+}
+
 // 8 lanes to a block of 128 columns.
 __global__ void __launch_bounds__(kSiluThreads) silu_rows_kernel(const SiluParams p) {
   const long long unit = (static_cast<long long>(blockIdx.x) * kSiluThreads + threadIdx.x) >> 3;
@@ -143,9 +154,8 @@ __global__ void __launch_bounds__(kSiluThreads) silu_rows_kernel(const SiluParam
   float g[16], u[16];
   widen16(g4, g);
   widen16(u4, u);
-  // (an exponential past the largest number leaves -0)
 #pragma unroll
-  for (int j = 0; j < 16; ++j) u[j] *= __fdividef(g[j], 1.f + __expf(-g[j]));
+  for (int j = 0; j < 16; ++j) u[j] *= silu(g[j]);
   const uint32_t m = max8(max16(u));
   if (!live) return;
   float s, r;
@@ -257,7 +267,8 @@ extern "C" int dflash_fp8_norm_rows(int32_t rows, int32_t cols, const void* x, i
   p.eps = rms_eps;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (cols <= 16 * 32)
-    return launch(norm_rows_kernel<1, true>, dim3((rows + kWarpRows - 1) / kWarpRows),
+    return launch(norm_rows_kernel<1, true>,
+                  dim3((static_cast<unsigned>(rows) + kWarpRows - 1) / kWarpRows),
                   dim3(32, kWarpRows), 0, st, p);
   if (cols <= 16 * 512) return launch_norm<1>(p, st);
   if (cols <= 16 * 1024) return launch_norm<2>(p, st);

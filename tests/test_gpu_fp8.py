@@ -192,6 +192,24 @@ def test_silu_mul(m, f):
     s.check()
 
 
+def test_silu_mul_of_gates_near_the_end_of_the_exponential():
+    """exp(-g) from 2^120 to past the largest number, alone in blocks with large u."""
+    dfl = _dfl()
+    g = np.repeat([-83.0, -86.5, -87.5, -88.0, -88.5, 88.0, 100.0, 3e38], 128)[None]
+    x = np.concatenate([g, np.full_like(g, 2.0 ** 100)], axis=1)
+    x[:, 128 * 14:] = 0.5                             # (h of the last two within fp32)
+    gu = bf16(x)
+    q, s = dfl.alloc_fp8_rows(1, 1024)
+    dfl.dflash_fp8_silu_mul(gu, q, s)
+    h = O.silu_mul(f64(gu))
+    # the exponential: 2 + 1.173 |g| units of 2^-23; the division 2, two products and the sum 1 each
+    g = np.minimum(np.abs(f64(gu)[:, :1024]), 104.0)
+    eps = (7 + 1.2 * g) * 2.0 ** -23
+    scale = s.cpu().numpy().astype(np.float64)
+    check_scales(scale, O._maxima(np.abs(h), (1,)).T, eps.max())
+    check_codes(codes(q), O.spread(scale.T, 1024, 1), h, eps)
+
+
 @pytest.mark.parametrize("shape", [(1, 16), (128, 128), (129, 144), (1000, 272), (3, 130, 400)])
 def test_weight(shape):
     dfl = _dfl()
@@ -366,6 +384,25 @@ def test_grouped_bad_groups_and_rows(m):
                 covered[start[e]:start[e + 1]] = True
         assert (got[~covered] == 3).all()
     assert dfl.dflash_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("e,m,n,k", [(64, 384, 300, 2048), (6, 500, 260, 256), (4, 2600, 260, 256)])
+def test_grouped_rows_have_one_owner(e, m, n, k):
+    """Experts that claim rows of one before them are left out."""
+    dfl = _dfl()
+    rng = np.random.default_rng(e)
+    x, xs, xv = random_x(rng, m, k)
+    w, wscale, wv = random_w(rng, e, n, k)
+    last = m - m // 4
+    start = [0] + [last, 0] * (e // 2 - 1) + [m - 40, m]       # the last of 40 rows does not
+    out, ws = Guarded((m, n), BF, fill=3.0), dfl.alloc_fp8_workspace()
+    dfl.dflash_fp8_grouped(x, xs, w, wscale, i32(start), None, out.t, ws)
+    assert dfl.dflash_read_status(ws) == dfl.dflash.STATUS_BITS["capacity"]
+    got = f64(out.t)
+    check_product(got[:last], xv[:last], wv[0])
+    assert (got[last:m - 40] == 3).all()
+    check_product(got[m - 40:], xv[m - 40:], wv[-1])
+    out.check()
 
 
 def test_grouped_equals_linear():
