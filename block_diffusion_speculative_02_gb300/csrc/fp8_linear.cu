@@ -26,7 +26,7 @@ namespace {
 int choose(Linear& p, cudaStream_t st) {
   p.sms = current_num_sms();
   if (p.sms <= 0) return DFLASH_E_CUDA;
-  const int rows = (p.m + p.groups - 1) / p.groups;
+  const int rows = static_cast<int>((static_cast<long long>(p.m) + p.groups - 1) / p.groups);
   if (p.start) {
     if (rows <= 8) return run_stream(p, 16, st);
     if (rows <= 32) return run_stream(p, 32, st);

@@ -244,7 +244,8 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t d) {
 // row tiles of the groups
 // --------------------------------------------------------------------------------------------
 // In shared memory: first row and number of rows of each group, and how many row tiles the
-// groups before it have.  A group whose rows do not lie in 0 .. m counts none.
+// groups before it have.  A group whose rows do not lie in 0 .. m, or that starts before the end of
+// one before it, counts none: no row has two owners, and there are no more tiles than most_tiles.
 struct Groups {
   int* first;   // [groups]
   int* count;   // [groups]
@@ -270,16 +271,30 @@ __device__ __forceinline__ void fill_groups(const Linear& p, const Groups& g, in
     }
     return;                              // (the caller's barrier follows)
   }
+  int bad = 0;
   for (int e = threadIdx.x; e < p.groups; e += n) {
     int a = p.start[e], b = p.start[e + 1];
     if (a < 0 || b < a || b > p.m) {
-      set_status(p.status, DFLASH_ST_CAPACITY);
+      bad = 1;
       a = b = 0;
     }
     g.first[e] = a;
     g.count[e] = b - a;
   }
-  __syncthreads();
+  if (__syncthreads_or(bad)) {           // (where none is, every group starts where one ended)
+    if (threadIdx.x == 0) {
+      set_status(p.status, DFLASH_ST_CAPACITY);
+      int end = 0;
+      for (int e = 0; e < p.groups; ++e) {
+        if (g.count[e] == 0) continue;
+        if (g.first[e] < end)
+          g.count[e] = 0;
+        else
+          end = g.first[e] + g.count[e];
+      }
+    }
+    __syncthreads();
+  }
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int sum = 0;

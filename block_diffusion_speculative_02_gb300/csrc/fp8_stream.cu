@@ -120,10 +120,10 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     tma_prefetch_desc(&map_w);
   }
   griddep_wait();
-  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
   fill_groups(p, groups, kT, kStreamThreads);
   tc_fence_before();
   __syncthreads();
+  griddep_launch_dependents();           // (the next grid's CTAs take TMEM only after this one's)
   tc_fence_after();
   const uint32_t tmem = same(*tmem_slot);
   const int total = groups.tiles[p.groups] * p.n_tiles;

@@ -171,11 +171,11 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     if (p.vector) tma_prefetch_desc(&map_out);
   }
   griddep_wait();
-  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
   fill_groups(p, groups, kRows, kTileWarps * 32);
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();             // the other CTA's barriers are there
+  griddep_launch_dependents();           // (the next grid's CTAs take TMEM only after this one's)
   tc_fence_after();
   const uint32_t tmem = same(*tmem_slot);
   const int total = groups.tiles[p.groups] * p.n_tiles;   // (below 2^31: the host)

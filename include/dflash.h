@@ -662,9 +662,9 @@ DFLASH_API int dflash_fp8_linear(int32_t rows, int32_t n_out, int32_t n_in, cons
  *   rows: int32 [n_rows] or NULL: row n of out is made of row rows[n] of x, [n_src, n_in]
  *   (a token that goes to several experts is not copied).  NULL: of row n, n_src = n_rows.
  * Rows of out before start[0] and from start[n_groups] on are left as they were.  A group
- * whose rows do not lie in 0 .. n_rows (start decreasing or past n_rows) sets
- * DFLASH_ST_CAPACITY and is left out; a rows[n] outside 0 .. n_src - 1 sets it too and stands for
- * a row of zeros.
+ * whose rows do not lie in 0 .. n_rows (start decreasing or past n_rows), or that starts before
+ * the end of one before it, sets DFLASH_ST_CAPACITY and is left out; a rows[n] outside
+ * 0 .. n_src - 1 sets it too and stands for a row of zeros.
  */
 DFLASH_API int dflash_fp8_grouped(int32_t n_rows, int32_t n_src, int32_t n_groups, int32_t n_out,
                                   int32_t n_in, const void* x, const float* x_scale,
