@@ -573,6 +573,28 @@ def test_large_offsets():
     assert bool((out.abs().amax(1) > 0).all())
 
 
+@pytest.mark.parametrize("n", [300, 1400, 2300])
+def test_more_rows_than_a_band(n):
+    """Row tiles past a band of 64, with feature tiles that fill no chunk of four."""
+    dfl = _dfl()
+    rng = np.random.default_rng(n)
+    m, k = 17111, 144
+    x, xs, xv = random_x(rng, m, k)
+    w, wscale, wv = random_w(rng, 2, n, k)
+    out, ws = Guarded((m, n), BF), dfl.alloc_fp8_workspace()
+    dfl.dflash_fp8_linear(x, xs, w[0], wscale[0], out.t, ws)
+    check_product(f64(out.t), xv, wv[0])
+    rows = rng.permutation(m)
+    for index in (None, rows):
+        dfl.dflash_fp8_grouped(x, xs, w, wscale, i32([0, 200, m]),
+                               None if index is None else i32(index), out.t, ws)
+        got, vals = f64(out.t), xv if index is None else xv[index]
+        check_product(got[:200], vals[:200], wv[0])
+        check_product(got[200:], vals[200:], wv[1])
+    out.check()
+    assert dfl.dflash_read_status(ws) == 0
+
+
 # --------------------------------------------------------------------------------------------
 # refusals of the binding
 # --------------------------------------------------------------------------------------------
