@@ -95,13 +95,14 @@ def linear(x, w):
 
 
 def grouped(x, w, start, rows, out):
-    """``out`` with the rows of each expert written."""
+    """``out`` with the rows of each expert written; of those that claim a row twice, the first's."""
     out = out.copy()
-    m = len(out)
+    m, end = len(out), 0
     for e in range(len(w)):
         a, b = int(start[e]), int(start[e + 1])
-        if not 0 <= a <= b <= m:
+        if not 0 <= a <= b <= m or a < end and a < b:
             continue
+        end = max(end, b) if a < b else end
         for n in range(a, b):
             src = n if rows is None else int(rows[n])
             out[n] = w[e] @ x[src] if 0 <= src < len(x) else 0.0

@@ -75,3 +75,9 @@ def test_grouped_by_brute_force(gather):
                 want[n, j] = sum(w[e, j, k] * x[src, k] for k in range(16)) if src < 5 else 0
     assert np.allclose(got, want) and (got[0] == 7).all()
     assert (O.grouped(x, w, [2, 1, 9, 5], rows, out)[:1] == 7).all()   # bad groups left out
+
+
+def test_grouped_rows_have_one_owner():
+    x, w = np.ones((6, 2)), np.arange(1.0, 5.0)[:, None, None] * np.ones((4, 1, 2))
+    got = O.grouped(x, w, [0, 4, 2, 5, 6], None, np.zeros((6, 1)))
+    assert got[:, 0].tolist() == [2, 2, 2, 2, 0, 8]                   # 0 .. 3, not 2 .. 4, then 5
