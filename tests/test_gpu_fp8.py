@@ -500,6 +500,34 @@ def test_mlp_captured_and_replayed_with_other_inputs():
     assert dfl.dflash_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("m", [48, 400, 2600])
+def test_grouped_captured_and_replayed_with_other_experts(m):
+    """start and rows change between replays; rows of the padding name no row of x."""
+    dfl = _dfl()
+    rng = np.random.default_rng(m)
+    e, n, k, pad = 6, 300, 400, 9
+    x, xs, xv = random_x(rng, 50, k)
+    w, wscale, wv = random_w(rng, e, n, k)
+    start, rows = torch.zeros(e + 1, dtype=torch.int32, device="cuda"), i32(np.full(m + pad, -1))
+    out, ws = torch.zeros(m + pad, n, dtype=BF, device="cuda"), dfl.alloc_fp8_workspace()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dfl.dflash_fp8_grouped(x, xs, w, wscale, start, rows, out, ws)
+    for kind in ("even", "one", "skew", "none"):
+        counts = [0] * e if kind == "none" else counts_of(kind, e, m, rng)
+        edge, index = np.cumsum([0] + counts), rng.integers(0, 50, m + pad)
+        index[edge[-1]:] = -1
+        start.copy_(i32(edge))
+        rows.copy_(i32(index))
+        out.fill_(3)
+        graph.replay()
+        got = f64(out)
+        for g in range(e):
+            check_product(got[edge[g]:edge[g + 1]], xv[index[edge[g]:edge[g + 1]]], wv[g])
+        assert (got[edge[-1]:] == 3).all()
+    assert dfl.dflash_read_status(ws) == 0
+
+
 def test_two_streams_share_a_workspace():
     """Products on two streams at once, with one workspace (it is only their status)."""
     dfl = _dfl()
