@@ -1,7 +1,7 @@
 // 8-bit products of many rows: tiles of 128 rows (or, of a pair of CTAs, 256) x kN features.
 //
-// One thread issues the products, of a pair (kPair) for both SMs: each holds 128 rows of x and half
-// of the features' weights, and gets the sums of its own rows.  Per block of K a pair of SMs moves
+// A thread for each half of the features issues the products, of a pair (kPair) for both SMs: each
+// SM holds 128 rows of x and half of the weights, and gets the sums of its own rows.  Per block of K a pair of SMs moves
 // and reads half as many bytes of weights as two single ones.
 //
 // A block's sums leave TMEM in the time of the next block's products (512 cycles at 256
@@ -9,9 +9,13 @@
 // a scheduler cover each other's waits.  (8191 rows x 24576 x 4096: 504 us, 655 with 8 warps of
 // twice the features.)  They wait at named barriers, where a warp takes no turn: one more warp
 // watches the accumulators' mbarriers for them.  (With all of them trying an mbarrier 640 us: a try
-// took the warps that issue the products 400 clocks and more.)  A block's way out
-// takes some 600 clocks beside its products' 513, and a tile's last sums wait for their stores: 476
-// us without those, 436 at the tensor cores' rate.
+// took the warps that issue the products 400 clocks and more.)
+//
+// What bounds it: a block of a pair takes some 640 clocks, of which its products take 513.  That is
+// what shared memory needs for them (48 KB read, the rows twice, once for each half of the
+// features, and 32 KB written by the copies, at 128 bytes a clock).  Products of all 256 features
+// at once read 16 KB less, but leave the epilogue half the time: 536 us.  The rest is power:
+// zeros as operands take 440 us.
 #include "fp8_linear.cuh"
 
 namespace dflash {
@@ -28,9 +32,20 @@ constexpr int kEpiWarp = 8, kEpiWarps = 16;
 constexpr int kRegsStart = 80, kRegsRest = 32, kRegsEpi = 104;
 static_assert(kEpiWarp * kRegsRest + kEpiWarps * kRegsEpi <= kTileWarps * kRegsStart,
               "register split");
-constexpr int kRing = 8;                        // blocks whose scales are in shared memory
 constexpr int kScaleRow = kTileRows + 2;        // of the rows, then of the weights
 constexpr int kSmemLimit = 227 * 1024;
+
+// Accumulators of each half of the features (all that TMEM holds: 512 rows x 12288 x 4096 in tiles
+// of 128 features take 30.5 us with four, 32.2 with two), and blocks whose scales are in shared
+// memory.
+template <int kN>
+__host__ __device__ constexpr int slots() {
+  return 512 / kN;
+}
+template <int kN>
+__host__ __device__ constexpr int ring() {
+  return 4 * slots<kN>();
+}
 
 template <bool kPair, int kN>
 __host__ __device__ constexpr int tile_stage_bytes() {
@@ -118,7 +133,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   constexpr int kShare = kHalf / kCtas;  // of these, features whose weights this CTA holds
   constexpr int kOwn = kN / 4;           // features of an epilogue warp
   constexpr int kStore = 32 * kOwn * 2;  // its rows on their way out
-  constexpr int kCols = 2 * kN;          // TMEM columns: two accumulators of each half
+  constexpr int kSlots = slots<kN>(), kRing = ring<kN>();
+  constexpr int kCols = kSlots * kN;     // TMEM columns
   constexpr int kBlocksN = kN / kBlockK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -129,9 +145,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   uint32_t* sources = reinterpret_cast<uint32_t*>(tiles + kInfo);     // [kInfo][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(sources + kInfo * kTileRows);
   uint64_t* empty = full + p.n_stages;
-  uint64_t* tfull = empty + p.n_stages;  // [2 halves][2] accumulators are there
-  uint64_t* tempty = tfull + 4;          // [2 halves][2] read (of a pair: in the first CTA)
-  uint64_t* mdrain = tempty + 4;         // [2 halves]
+  uint64_t* tfull = empty + p.n_stages;  // [2 halves][kSlots] accumulators are there
+  uint64_t* tempty = tfull + 2 * kSlots;   // likewise: read (of a pair: in the first CTA)
+  uint64_t* mdrain = tempty + 2 * kSlots;  // [2 halves]
   uint64_t* sfull = mdrain + 2;          // [kRing] scales are there
   uint64_t* sempty = sfull + kRing;      // [kRing] both halves' sums of that block are there
   uint64_t* ifull = sempty + kRing;      // [kInfo] a tile's place is written down
@@ -151,7 +167,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       mbar_init(&ifull[i], 1);
       mbar_init(&iempty[i], 1 + (kIndex ? 2 : 0) + kEpiWarps);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * kSlots; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], kEpiWarps / 2 * kCtas);
     }
@@ -242,9 +258,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       const uint64_t a_desc = umma_sdesc_sw128(smem_u32(smem));
       const uint64_t b_desc =
           umma_sdesc_sw128(smem_u32(smem) + (kTileRows + half * kShare) * kBlockK);
-      const uint32_t acc = tmem + half * 2 * kHalf;
-      uint64_t* done = tfull + 2 * half;
-      uint64_t* read = tempty + 2 * half;
+      const uint32_t acc = tmem + half * kSlots * kHalf;
+      uint64_t* done = tfull + kSlots * half;
+      uint64_t* read = tempty + kSlots * half;
       uint32_t stage = 0, phase = 0, slot = 0, tphase = 0;
       bool ok = true;
       for (int t = t_first; all(ok && t < total); t += t_step) {
@@ -262,8 +278,10 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             mma_done<kPair>(&done[slot]);
             mma_done<kPair>(&empty[stage]);
           }
-          tphase ^= slot;
-          slot ^= 1;
+          if (++slot == kSlots) {
+            slot = 0;
+            tphase ^= 1;
+          }
           if (++stage == static_cast<uint32_t>(p.n_stages)) {
             stage = 0;
             phase ^= 1;
@@ -274,8 +292,9 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       if (lane == 0) mbar_wait_drain(&mdrain[half], 0, p.status);
     }
   } else if (warp == 2) {
-    // Writes down the tiles' places and copies the scales, kRing - 2 blocks ahead of the sums: that
-    // those of a block are there says that those of two blocks before were read, their scales too.
+    // Writes down the tiles' places and copies the scales, kRing - kSlots blocks ahead of the sums:
+    // that those of a block are there says that those of kSlots blocks before were read, their
+    // scales too.
     uint32_t it = 0, in = 0;
     bool ok = true;
     for (int t = t_first; all(ok && t < total); t += t_step, ++in) {
@@ -305,8 +324,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
           p.ws + (static_cast<long long>(tile.e) * p.n_blocks + (w_size ? nb : 0)) * p.k_blocks;
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
-        if (it >= kRing - 2) {
-          const uint32_t seen = it - (kRing - 2);
+        if (it >= kRing - kSlots) {
+          const uint32_t seen = it - (kRing - kSlots);
           ok = all(wait_on(&sempty[seen % kRing], (seen / kRing) & 1, p.status));
         }
         if (!ok) break;
@@ -331,13 +350,13 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     for (int t = t_first; all(t < total); t += t_step) {
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
-        const uint32_t slot = it & 1;
-        ok = ok && wait_both(&tfull[2 * half + slot], (it >> 1) & 1, &sfull[it % kRing],
+        const uint32_t slot = kSlots * half + it % kSlots;
+        ok = ok && wait_both(&tfull[slot], (it / kSlots) & 1, &sfull[it % kRing],
                              (it / kRing) & 1, p.status);
         if (ok)
-          named_bar_arrive(1 + 2 * half + slot, 32 * (kEpiWarps / 2 + 1));
+          named_bar_arrive(1 + slot, 32 * (kEpiWarps / 2 + 1));
         else
-          named_bar_sync(1 + 2 * half + slot, 32 * (kEpiWarps / 2 + 1));
+          named_bar_sync(1 + slot, 32 * (kEpiWarps / 2 + 1));
         if (elect_one()) mbar_arrive(&sempty[it % kRing]);
       }
     }
@@ -363,11 +382,11 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     const int quad = warp & 3, part = (warp - kEpiWarp) >> 2;
     uint8_t* buf = store + (warp - kEpiWarp) * kStore;
     const int half = part >> 1;
-    const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 2 * kHalf +
-                          (part & 1) * kOwn;
+    const uint32_t from = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
+                          half * kSlots * kHalf + (part & 1) * kOwn;
     const float* x_scale = scales + quad * 32 + lane;
     const float* w_scale = scales + kTileRows + part * kOwn / kBlockK;
-    const uint32_t read = first_cta<kPair>(tempty + 2 * half);
+    const uint32_t read = first_cta<kPair>(tempty + kSlots * half);
     uint32_t it = 0, in = 0;
     bool known = true;
     for (int t = t_first; t < total; t += t_step) {
@@ -376,8 +395,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       for (int i = 0; i < kOwn / 2; ++i) acc[i] = 0;
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
-        const uint32_t slot = it & 1;
-        named_bar_sync(1 + 2 * half + slot, 32 * (kEpiWarps / 2 + 1));
+        const uint32_t slot = it % kSlots;
+        named_bar_sync(1 + kSlots * half + slot, 32 * (kEpiWarps / 2 + 1));
         tc_fence_after();
         const uint32_t in_ring = it % kRing * kScaleRow;
         const float f1 = x_scale[in_ring] * w_scale[in_ring];
@@ -425,8 +444,9 @@ int run(Linear p, cudaStream_t st) {
   p.n_tiles = (p.n + kN - 1) / kN;
   p.box_rows = p.n_src < kTileRows ? p.n_src : kTileRows;
   constexpr int kStoreBytes = kEpiWarps * 32 * (kN / 4) * 2;
+  constexpr int kRing = ring<kN>();
   const int tail = kStoreBytes + kRing * kScaleRow * 4 + kInfo * (16 + kTileRows * 4) +
-                   (10 + 2 * kRing + 2 * kInfo) * 8 + 4 + groups_bytes(p.groups);
+                   (4 * slots<kN>() + 2 + 2 * kRing + 2 * kInfo) * 8 + 4 + groups_bytes(p.groups);
   p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
   if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
   const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
