@@ -730,22 +730,23 @@ def alloc_fp8_weight(*shape, device="cuda"):
 
 
 def _whole(t, device: int, dtype, shape, name: str) -> int:
-    """Pointer of a contiguous tensor of this type and shape on this device."""
+    """Pointer of a contiguous tensor of this type and shape (None: any) on this device."""
     if getattr(t, "dtype", None) is not dtype or t.get_device() != device \
             or not t.is_contiguous():
         _bad(t, device, dtype, None, name)
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
 def _codes(q, scale, device: int, shape, scales, name: str, scale_name: str):
-    """Pointers of e4m3 codes and their fp32 scales, both contiguous.  (Checked in one expression;
-    where it does not hold, one by one, to say what is wrong.)"""
+    """Pointers of e4m3 codes (shape None: the one the call goes by) and their fp32 scales, both
+    contiguous.  (Checked in one expression; where it does not hold, one by one, to say what is
+    wrong.)"""
     try:
-        if q.dtype is F8 and scale.dtype is _F32 and q.shape == shape and scale.shape == scales \
-                and q.is_contiguous() and scale.is_contiguous() and q.get_device() == device \
-                and scale.get_device() == device:
+        if q.dtype is F8 and scale.dtype is _F32 and (shape is None or q.shape == shape) \
+                and scale.shape == scales and q.is_contiguous() and scale.is_contiguous() \
+                and q.get_device() == device and scale.get_device() == device:
             return q.data_ptr(), scale.data_ptr()
     except AttributeError:
         pass
@@ -810,7 +811,7 @@ def dflash_fp8_weight(w, q, scale, stream=None):
         raise ValueError("w must be a tensor [N, K] or [G, N, K]")
     *g, n, k = shape
     rc = load_library().dflash_fp8_weight(
-        g[0] if g else 1, n, k, _whole(w, dev, _BF, shape, "w"),
+        g[0] if g else 1, n, k, _whole(w, dev, _BF, None, "w"),
         *_codes(q, scale, dev, shape, (*g, -(-n // 128), -(-k // 128)), "q", "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_weight")
@@ -825,8 +826,8 @@ def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
         raise ValueError(f"x has {k} columns, w {kw}")
     kb = -(-k // 128)
     rc = load_library().dflash_fp8_linear(
-        m, n, k, *_codes(x, x_scale, dev, (m, k), (kb, m), "x", "x_scale"),
-        *_codes(w, w_scale, dev, (n, k), (-(-n // 128), kb), "w", "w_scale"),
+        m, n, k, *_codes(x, x_scale, dev, None, (kb, m), "x", "x_scale"),
+        *_codes(w, w_scale, dev, None, (-(-n // 128), kb), "w", "w_scale"),
         *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
     if rc:
         _check(rc, "dflash_fp8_linear")
@@ -844,8 +845,8 @@ def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None
     if rows is None and m != src:
         raise ValueError(f"out has {m} rows, x {src}: rows must say which")
     rc = load_library().dflash_fp8_grouped(
-        m, src, e, n, k, *_codes(x, x_scale, dev, (src, k), (kb, src), "x", "x_scale"),
-        *_codes(w, w_scale, dev, (e, n, k), (e, -(-n // 128), kb), "w", "w_scale"),
+        m, src, e, n, k, *_codes(x, x_scale, dev, None, (kb, src), "x", "x_scale"),
+        *_codes(w, w_scale, dev, None, (e, -(-n // 128), kb), "w", "w_scale"),
         _whole(start, dev, torch.int32, (e + 1,), "start"),
         None if rows is None else _whole(rows, dev, torch.int32, (m,), "rows"),
         *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
