@@ -20,9 +20,10 @@ namespace {
 // Plain: up to 64 rows the weights are streamed, with the smallest tile that holds the rows (24
 // rows x 4096 x 4096: 7.9, 6.6, 7.5 us, 11.4 with 128 x 128 tiles), or in two of 32 rows; more
 // rows where the estimates say so: few features leave SMs without a tile (128 rows x 4096 x 12288
-// take 17 us in shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4).  Among tiles the fewest
-// waves win, each worth its time: 512 rows x 4096 x 4096 take 12.6 us with 128 x 128 tiles, 14.6
-// with 128 x 256, 14.1 with pairs; 128 rows x 24576 27, 24, 33; 512 rows x 24576 60, 54, 46.
+// take 17 us in shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4; 200 rows x 512 x 768 4.4 and
+// 5.3).  Among tiles the fewest waves win, each worth its time: 512 rows x 4096 x 4096 take 12.6 us
+// with 128 x 128 tiles, 14.6 with 128 x 256, 14.1 with pairs; 128 rows x 24576 27, 24, 33; 512 rows
+// x 24576 59, 54, 45; 2000 rows x 12288 x 256 16.0, 13.4, 13.3.
 int choose(Linear& p, cudaStream_t st) {
   p.sms = current_num_sms();
   if (p.sms <= 0) return DFLASH_E_CUDA;
@@ -35,13 +36,16 @@ int choose(Linear& p, cudaStream_t st) {
   }
   if (rows <= 16) return run_stream(p, 16, st);
   if (rows <= 32) return run_stream(p, 32, st);
-  // us: the start, and the waves of a tile's blocks
-  const auto cost = [&](int tile_rows, int features, int at_once, double start, double block) {
+  // us: the start, and the waves of a tile's blocks and its end
+  const auto cost = [&](int tile_rows, int features, int at_once, double start, double block,
+                        double end) {
     const long long tiles = most_tiles(p, tile_rows, features);
-    return start + static_cast<double>((tiles + at_once - 1) / at_once) * p.k_blocks * block;
+    return start + static_cast<double>((tiles + at_once - 1) / at_once) *
+                       (p.k_blocks * block + end);
   };
-  const double small = cost(128, 128, p.sms, 2.6, 0.30), wide = cost(128, 256, p.sms, 5.5, 0.48),
-               pair = cost(256, 256, p.sms / 2, 4.5, 0.43);
+  const double small = cost(128, 128, p.sms, 3.0, 0.28, 0.6),
+               wide = cost(128, 256, p.sms, 3.6, 0.45, 0.8),
+               pair = cost(256, 256, p.sms / 2, 4.2, 0.33, 0.87);
   const double tiles = std::min(small, std::min(wide, pair));
   const double thin = stream_cost(p, 32), thick = stream_cost(p, 64);
   if (rows <= 64 || std::min(thin, thick) < tiles)

@@ -373,10 +373,11 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 // CTAs that share a tile's K, and about how many us the call takes.  A CTA takes some 0.2 us a
 // block (0.33 with 64 rows) where the memory has time for it, a quarter more with another on its
 // SM; all together 2.4 ns a block of weights at the memory's rate, 0.4 where another tile's rows
-// need the same weights.  Whole tiles follow one another without a pause; shares of K are joined in
-// 1 to 2 us, and a second wave of them costs 4 more: 16 rows x 4096 x 4096 (32 tiles of 32 blocks)
-// take 7.4, 6.6, 6.3 us in two, four, eight shares, 64 rows 8.2, 8.2, 13.2; 16 rows x 49152 x 4096
-// (384 tiles) 34 us whole and 43 in two shares.
+// need the same weights.  A tile ends in 0.4 us, or 1.1 where two on an SM end together; shares of
+// K are joined in 1 to 2 us, more where an SM has two clusters' CTAs with many rows (192 rows x
+// 4096 x 4096 in two shares of 96 tiles take 14 us), and a second wave of them costs 4 more: 16
+// rows x 4096 x 4096 (32 tiles of 32 blocks) take 7.4, 6.6, 6.3 us in two, four, eight shares, 64
+// rows 8.2, 8.2, 13.2; 16 rows x 49152 x 4096 (384 tiles) 34 us whole and 43 in two shares.
 double stream_split(const Linear& p, int tile_rows, int* split) {
   const double tiles = static_cast<double>(most_tiles(p, tile_rows, 128));
   const double first = static_cast<double>(most_tiles(p, p.m, 128));      // of an expert each
@@ -385,12 +386,14 @@ double stream_split(const Linear& p, int tile_rows, int* split) {
   double cost = 0;
   for (int s = 1; s <= kMaxSplit && s <= p.k_blocks; s *= 2) {
     const double ctas = tiles * s, waves = std::ceil(ctas / (2 * p.sms));
-    const double work =
-        waves * ((p.k_blocks + s - 1) / s) * block * (ctas > p.sms ? 1.25 : 1.0);
+    const bool two = ctas > p.sms;                                        // CTAs on an SM
+    const double work = waves * (((p.k_blocks + s - 1) / s) * block * (two ? 1.25 : 1.0) +
+                                 (two ? 1.1 : 0.4));
     // (fewer than three CTAs to two SMs do not draw all that the memory gives)
-    const double drawn = memory * (ctas * 2 < 3 * p.sms ? 1.15 : 1.0);
-    double c = 3.0 + std::max(work, drawn);
-    if (s > 1) c += join + 4.0 * (waves - 1);
+    const double drawn = memory * (ctas * 2 < 3 * p.sms ? 1.15 : 1.0) + 0.4;
+    double c = 2.6 + std::max(work, drawn);
+    if (s > 1)
+      c += join + 4.0 * (waves - 1) + (two ? 1.5 * tile_rows * tile_rows / 4096.0 : 0.0);
     if (s == 1 || c < cost) {
       *split = s;
       cost = c;

@@ -234,7 +234,9 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (1, 4096, 4096), (2, 130, 144), (7, 257, 40
           (65, 255, 512), (100, 1537, 640), (128, 128, 128), (129, 511, 2560), (255, 2567, 256),
           (256, 1024, 1024), (257, 768, 4000), (513, 520, 128), (1000, 136, 1040), (700, 2056, 16),
           (2048, 2048, 512), (128, 20000, 144), (2148, 2048, 256), (2200, 1500, 272),
-          (1, 24576, 128), (24, 8192, 640), (50, 20000, 384)]
+          (1, 24576, 128), (24, 8192, 640), (50, 20000, 384), (2500, 387, 144), (200, 5003, 2064),
+          (900, 2600, 144), (1500, 1537, 656), (1000, 2600, 1168), (4000, 1029, 656),
+          (500, 387, 2064), (700, 1300, 4000), (300, 2051, 144), (150, 4096, 8192)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -250,13 +252,15 @@ def test_linear(m, n, k):
     assert dfl.dflash_read_status(ws) == 0 and not bool(ws.any())
 
 
-@pytest.mark.parametrize("m", [5, 40, 200, 600])
-@pytest.mark.parametrize("pitch,offset", [(400, 0), (401, 0), (408, 3), (408, 8)])
-def test_linear_into_strided_rows(m, pitch, offset):
+# (of 387 features: streamed, and tiles of 128 x 128; of 1537 tiles of 128 x 256, and pairs)
+@pytest.mark.parametrize("m,n,k", [(5, 387, 320), (40, 387, 320), (200, 387, 320), (600, 387, 320),
+                                   (2500, 387, 144), (1500, 1537, 144), (1500, 1537, 656)])
+@pytest.mark.parametrize("apart,offset", [(8, 0), (9, 0), (16, 3), (16, 8)])
+def test_linear_into_strided_rows(m, n, k, apart, offset):
     """Rows of out that lie apart, also unaligned: nothing between them is touched."""
     dfl = _dfl()
+    pitch = (n + 7) // 8 * 8 + apart
     rng = np.random.default_rng(m + pitch)
-    n, k = 387, 320
     x, xs, xv = random_x(rng, m, k)
     w, wscale, wv = random_w(rng, n, k)
     buf = torch.full((m * pitch + 64,), 7.0, dtype=BF, device="cuda")
