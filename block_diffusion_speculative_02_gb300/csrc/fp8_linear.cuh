@@ -396,55 +396,30 @@ __device__ __forceinline__ void copy_rows(const Linear& p, uint8_t* dst, int col
                    : "memory");
     }
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// One warp's copies: each block into the next stage, kCopyLag of them on their way at a time.  A
-// block's arrival at its stage's barrier (arrive) comes once its bytes are there for the tensor
-// cores to read.
-constexpr int kCopyLag = 2;
-
+// One warp's copies: each block into the next stage.  They arrive at the stage's barrier themselves
+// (landed, 32 for a warp) when they are there; who hands them on to the tensor cores fences.
+// (Announced by the warp itself two blocks later, 128 experts of 200 rows x 1536 x 2048 took 155 us,
+// 112 this way.)
 struct RowCopies {
   uint32_t stage = 0, phase = 0;   // of the next block to copy
-  uint32_t landed = 0, pending = 0;
 
-  template <class Arrive>
-  __device__ __forceinline__ void land(const Linear& p, const Arrive& arrive) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (elect_one()) arrive(landed);
-    __syncwarp();
-    if (++landed == static_cast<uint32_t>(p.n_stages)) landed = 0;
-    --pending;
-  }
-
-  template <int kRows, int kOf, class Arrive>
+  template <int kRows, int kOf>
   __device__ __forceinline__ bool tile(const Linear& p, uint8_t* base, int stage_bytes,
-                                       uint64_t* empty, int b_first, int b_last,
-                                       const uint32_t* sources, int first, int lane,
-                                       const Arrive& arrive) {
+                                       uint64_t* empty, uint64_t* landed, int b_first, int b_last,
+                                       const uint32_t* sources, int first, int lane) {
 #pragma unroll 1
     for (int b = b_first; b < b_last; ++b) {
       if (!all(wait_on(&empty[stage], phase ^ 1, p.status))) return false;
       copy_rows<kRows, kOf>(p, base + stage * stage_bytes, b * kBlockK, sources, first, lane);
+      cp_async_arrive(&landed[stage]);
       if (++stage == static_cast<uint32_t>(p.n_stages)) {
         stage = 0;
         phase ^= 1;
       }
-      if (++pending > kCopyLag) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kCopyLag) : "memory");
-        land(p, arrive);
-      } else if (pending == static_cast<uint32_t>(p.n_stages)) {
-        finish(p, arrive);               // (the next stage waits for them)
-      }
     }
     return true;
-  }
-
-  template <class Arrive>
-  __device__ __forceinline__ void finish(const Linear& p, const Arrive& arrive) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    while (pending) land(p, arrive);
   }
 };
 

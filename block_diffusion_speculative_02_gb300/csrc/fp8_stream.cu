@@ -93,7 +93,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.n_stages; ++i) {
-      mbar_init(&full[i], kIndex ? 2 : 1);
+      mbar_init(&full[i], 1 + (kIndex ? 32 : 0));
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kFactors; ++i) {
@@ -183,6 +183,7 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         ok = wait_both(&tempty[slot], tphase ^ 1, &full[stage], phase, p.status);
         if (!ok) break;
         tc_fence_after();
+        if (kIndex) fence_proxy_async_smem();
         if (elect_one()) {
           const uint64_t ad = a_desc + stage * (kStage >> 4), bd = b_desc + stage * (kStage >> 4);
 #pragma unroll
@@ -266,19 +267,18 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
   } else if (warp == 7) {
     if (kIndex) {
-      const auto arrive = [&](uint32_t stage) { mbar_arrive(&full[stage]); };
       RowCopies copies;
       uint32_t in = 0;
       bool ok = true;
       for (int t = t_first; all(ok && t < total); t += t_step, ++in) {
         ok = all(wait_on(&ifull[in % kInfo], (in / kInfo) & 1, p.status));
         if (!ok) break;
-        ok = copies.tile<kT, kT>(p, smem + 128 * kBlockK, kStage, empty, b_first, b_last,
-                                 sources + in % kInfo * kT, 0, lane, arrive);
+        ok = copies.tile<kT, kT>(p, smem + 128 * kBlockK, kStage, empty, full, b_first, b_last,
+                                 sources + in % kInfo * kT, 0, lane);
         __syncwarp();
         if (elect_one()) mbar_arrive(&iempty[in % kInfo]);
       }
-      copies.finish(p, arrive);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
 

@@ -1,8 +1,8 @@
 // 8-bit products of many rows: tiles of 128 rows (or, of a pair of CTAs, 256) x kN features.
 //
 // A thread for each half of the features issues the products, of a pair (kPair) for both SMs: each
-// SM holds 128 rows of x and half of the weights, and gets the sums of its own rows.  Per block of K a pair of SMs moves
-// and reads half as many bytes of weights as two single ones.
+// SM holds 128 rows of x and half of the weights, and gets the sums of its own rows.  Per block of
+// K a pair of SMs moves and reads half as many bytes of weights as two single ones.
 //
 // A block's sums leave TMEM in the time of the next block's products (512 cycles at 256
 // features): 16 warps take a quarter of the features of 32 rows each, so that four warps of
@@ -136,6 +136,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   constexpr int kSlots = slots<kN>(), kRing = ring<kN>();
   constexpr int kCols = kSlots * kN;     // TMEM columns
   constexpr int kBlocksN = kN / kBlockK;
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint8_t* store = smem + p.n_stages * kStage;
@@ -152,16 +153,19 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   uint64_t* sempty = sfull + kRing;      // [kRing] both halves' sums of that block are there
   uint64_t* ifull = sempty + kRing;      // [kInfo] a tile's place is written down
   uint64_t* iempty = ifull + kInfo;      // [kInfo] and read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(iempty + kInfo);
+  uint64_t* landed = kIndex && rank ? iempty + kInfo : full;   // a stage's rows by index are there
+  uint32_t* tmem_slot =
+      reinterpret_cast<uint32_t*>(iempty + kInfo + (kIndex && kPair ? p.n_stages : 0));
   const Groups groups = groups_at(reinterpret_cast<uint8_t*>(tmem_slot + 1), p.groups);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.n_stages; ++i) {
-      mbar_init(&full[i], 1 + (kIndex ? 2 * kCtas : 0));
+      // (the bytes of both CTAs count in the first; its rows by index 64, the other CTA's 1)
+      mbar_init(&full[i], 1 + (kIndex ? 64 + kCtas - 1 : 0));
       mbar_init(&empty[i], 2);           // the products of both halves
+      if (kIndex && rank) mbar_init(&landed[i], 64);
     }
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&ifull[i], 1);
@@ -270,6 +274,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
           ok = wait_both(&read[slot], tphase ^ 1, &full[stage], phase, p.status);
           if (!ok) break;
           tc_fence_after();
+          if (kIndex) fence_proxy_async_smem();
           if (elect_one()) {
             const uint64_t ad = a_desc + stage * (kStage >> 4), bd = b_desc + stage * (kStage >> 4);
 #pragma unroll
@@ -290,6 +295,22 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       }
       if (elect_one()) mma_done_here<kPair>(&mdrain[half]);
       if (lane == 0) mbar_wait_drain(&mdrain[half], 0, p.status);
+    } else if (kIndex && warp == 1) {    // hands this CTA's rows by index on to the first
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int t = t_first; all(ok && t < total); t += t_step) {
+#pragma unroll 1
+        for (int b = 0; b < p.k_blocks; ++b) {
+          ok = all(wait_on(&landed[stage], phase, p.status));
+          if (!ok) break;
+          fence_proxy_async_smem();
+          if (elect_one()) arrive_at<kPair>(first_cta<kPair>(&full[stage]));
+          if (++stage == static_cast<uint32_t>(p.n_stages)) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
     }
   } else if (warp == 2) {
     // Writes down the tiles' places and copies the scales, kRing - kSlots blocks ahead of the sums:
@@ -363,19 +384,18 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   } else if (warp == 6 || warp == 7) {
     if (kIndex) {                        // half of the CTA's rows of x to a warp
       const int first = (warp - 6) * 64;
-      const auto arrive = [&](uint32_t stage) { arrive_at<kPair>(first_cta<kPair>(&full[stage])); };
       RowCopies copies;
       uint32_t in = 0;
       bool ok = true;
       for (int t = t_first; all(ok && t < total); t += t_step, ++in) {
         ok = all(wait_on(&ifull[in % kInfo], (in / kInfo) & 1, p.status));
         if (!ok) break;
-        ok = copies.tile<64, kTileRows>(p, smem, kStage, empty, 0, p.k_blocks,
-                                        sources + in % kInfo * kTileRows, first, lane, arrive);
+        ok = copies.tile<64, kTileRows>(p, smem, kStage, empty, landed, 0, p.k_blocks,
+                                        sources + in % kInfo * kTileRows, first, lane);
         __syncwarp();
         if (elect_one()) mbar_arrive(&iempty[in % kInfo]);
       }
-      copies.finish(p, arrive);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp >= kEpiWarp) {
     kv4::regs_up<kRegsEpi>();
@@ -447,9 +467,10 @@ int run(Linear p, cudaStream_t st) {
   constexpr int kRing = ring<kN>();
   const int tail = kStoreBytes + kRing * kScaleRow * 4 + kInfo * (16 + kTileRows * 4) +
                    (4 * slots<kN>() + 2 + 2 * kRing + 2 * kInfo) * 8 + 4 + groups_bytes(p.groups);
-  p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
+  constexpr int kBars = kIndex && kPair ? 24 : 16;   // a stage's
+  p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + kBars);
   if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
-  const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
+  const int smem = 1024 + p.n_stages * (kStage + kBars) + tail;
   CUtensorMap mx, mw, mo = {};
   int rc = make_map(&mx, p.x, p.k, p.n_src, p.box_rows);
   if (!rc) rc = make_map(&mw, p.w, p.k, static_cast<long long>(p.groups) * p.n, kN / 2 / kCtas);
