@@ -1,6 +1,7 @@
 // Products of rows and weights held in 8 bits (e4m3) with a scale for each block of 128, plain
 // and grouped by expert: the entry points, and which kernel takes a call.
 #include <algorithm>
+#include <cmath>
 
 #include "fp8_linear.cuh"
 
@@ -10,45 +11,40 @@ namespace {
 
 // Which kernel takes a call; `rows`: of an expert, on average.
 //
-// By expert (rows of 128 experts x 1536 x 2048 by index, in us): 4 rows each take 53, 51, 52 with
-// the stream's tiles of 16, 32, 64 rows; 16 rows 60, 59, 58; 32 rows 81, 64, 65, and 109 with
-// 128 x 256 tiles; 80 rows 89 with 64 rows and 98; 192 rows 162, 153, and 155 with pairs; 384 rows
-// 292, 247, 231.  (8 experts x 4096 x 2048, 8 rows each: 9.7, 10.7, 13.8; 24 rows 14, 10.8, 13.9.)
-// Rows in order reach the tiles sooner: 80 rows 80 and 80, 256 rows 150, 126, 131, 512 rows 206
-// with 128 x 256 and 201 with pairs.
+// Up to 16 rows (32, if there is one expert) the weights are streamed with the smallest tile that
+// holds the rows: 128 experts of 4 rows by index x 1536 x 2048 take 53, 51, 52 us with tiles of 16,
+// 32, 64 rows; 8 experts of 8 rows x 4096 x 2048 9.7, 10.7, 13.8; 24 rows x 4096 x 4096 7.9, 6.6,
+// 7.5.  More rows: whichever the estimates say is the fastest.  Of 264 sizes of products by expert
+// (4 to 128 experts of 1 to 1000 rows, by index and in order) the choice is 1.7 % slower on average
+// than the fastest kernel.
 //
-// Plain: up to 64 rows the weights are streamed, with the smallest tile that holds the rows (24
-// rows x 4096 x 4096: 7.9, 6.6, 7.5 us, 11.4 with 128 x 128 tiles), or in two of 32 rows; more
-// rows where the estimates say so: few features leave SMs without a tile (128 rows x 4096 x 12288
-// take 17 us in shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4; 200 rows x 512 x 768 4.4 and
-// 5.3).  Among tiles the fewest waves win, each worth its time: 512 rows x 4096 x 4096 take 12.6 us
-// with 128 x 128 tiles, 14.6 with 128 x 256, 14.1 with pairs; 128 rows x 24576 27, 24, 33; 512 rows
-// x 24576 59, 54, 45; 2000 rows x 12288 x 256 16.0, 13.4, 13.3.
+// Examples, in us.  Few features leave SMs without a tile: 128 rows x 4096 x 12288 take 17 streamed
+// in shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4; 200 rows x 512 x 768 4.4 and 5.3.
+// Among tiles the fewest waves win, each worth its time: 512 rows x 4096 x 4096 take 12.6 with
+// 128 x 128 tiles, 14.6 with 128 x 256, 14.1 with pairs; 128 rows x 24576 27, 24, 33; 512 rows x
+// 24576 59, 54, 45; 2000 rows x 12288 x 256 16.0, 13.4, 13.3.  By index the copies of the rows bound
+// the tiles: 16 experts of 80 rows x 1536 x 2048 take 14.5 with 128 x 256 tiles, 16.9 streamed 32
+// rows at a time, 20 64 rows; in order 11.9, 16.3, 16.7; 64 experts of 400 rows 104, in order 91
+// (pairs 88).  (Pairs by index were slower at every size.)
 int choose(Linear& p, cudaStream_t st) {
   p.sms = current_num_sms();
   if (p.sms <= 0) return DFLASH_E_CUDA;
   const int rows = static_cast<int>((static_cast<long long>(p.m) + p.groups - 1) / p.groups);
-  if (p.start) {
-    if (rows <= 8) return run_stream(p, 16, st);
-    if (rows <= 32) return run_stream(p, 32, st);
-    if (rows <= (p.rows ? 96 : 64)) return run_stream(p, 64, st);
-    return run_tiles(p, rows <= 320 ? Tiles::k128x256 : Tiles::k256x256, st);
-  }
-  if (rows <= 16) return run_stream(p, 16, st);
-  if (rows <= 32) return run_stream(p, 32, st);
+  if (rows <= (p.start ? 8 : 16)) return run_stream(p, 16, st);
+  if (rows <= (p.start ? 16 : 32)) return run_stream(p, 32, st);
   // us: the start, and the waves of a tile's blocks and its end
   const auto cost = [&](int tile_rows, int features, int at_once, double start, double block,
                         double end) {
-    const long long tiles = most_tiles(p, tile_rows, features);
-    return start + static_cast<double>((tiles + at_once - 1) / at_once) *
-                       (p.k_blocks * block + end);
+    const double tiles = row_tiles(p, tile_rows) * ((p.n + features - 1) / features);
+    return start + std::ceil(tiles / at_once) * (p.k_blocks * block + end);
   };
-  const double small = cost(128, 128, p.sms, 3.0, 0.28, 0.6),
-               wide = cost(128, 256, p.sms, 3.6, 0.45, 0.8),
-               pair = cost(256, 256, p.sms / 2, 4.2, 0.33, 0.87);
+  const double wide = p.rows ? cost(128, 256, p.sms, 4.2, 0.6, 0.8)
+                             : cost(128, 256, p.sms, 3.6, 0.45, 0.8),
+               pair = p.rows ? wide : cost(256, 256, p.sms / 2, 4.2, 0.33, 0.87),
+               small = p.rows ? wide : cost(128, 128, p.sms, 3.0, 0.28, 0.6);
   const double tiles = std::min(small, std::min(wide, pair));
   const double thin = stream_cost(p, 32), thick = stream_cost(p, 64);
-  if (rows <= 64 || std::min(thin, thick) < tiles)
+  if ((!p.start && rows <= 64) || std::min(thin, thick) < tiles)
     return run_stream(p, thin < thick ? 32 : 64, st);
   return run_tiles(p, tiles == small ? Tiles::k128x128
                       : tiles == wide ? Tiles::k128x256 : Tiles::k256x256, st);

@@ -12,8 +12,8 @@
 // Tiles end with their expert: rows past it are multiplied (they are other rows of x, or zeros
 // past its end), not stored.
 //
-// Rows of x that an index names are copied by two warps, 16 bytes a thread, into the order of the
-// swizzle.  (Copies of four rows by the TMA took 50 to 150 ns each, 8 us a tile of 128 rows.)
+// Rows of x that an index names are copied by one or two warps, 16 bytes a thread, into the order
+// of the swizzle.  (Copies of four rows by the TMA took 50 to 150 ns each, 8 us a tile of 128 rows.)
 #pragma once
 
 #include "fp8.cuh"
@@ -400,8 +400,8 @@ __device__ __forceinline__ void copy_rows(const Linear& p, uint8_t* dst, int col
 
 // One warp's copies: each block into the next stage.  They arrive at the stage's barrier themselves
 // (landed, 32 for a warp) when they are there; who hands them on to the tensor cores fences.
-// (Announced by the warp itself two blocks later, 128 experts of 200 rows x 1536 x 2048 took 155 us,
-// 112 this way.)
+// (Announced by the warp itself two blocks later, 128 experts of 200 rows x 1536 x 2048 took 155
+// us, 112 this way.)
 struct RowCopies {
   uint32_t stage = 0, phase = 0;   // of the next block to copy
 
@@ -441,12 +441,21 @@ inline long long most_tiles(const Linear& p, int tile_rows, int tile_cols) {
   return (p.m / tile_rows + static_cast<long long>(p.groups < p.m ? p.groups : p.m)) * n_tiles;
 }
 
-// Tiles of 128 rows x 128 or 256 features, or, of a pair of CTAs, 256 x 256.
+// Row tiles, about: the rows of an expert are not known here, so that on average 0.6 of a tile of
+// each goes without rows.
+inline double row_tiles(const Linear& p, int tile_rows) {
+  if (!p.start) return (p.m + tile_rows - 1) / tile_rows;
+  const double with_rows = p.groups < p.m ? p.groups : p.m, own = p.m / with_rows / tile_rows + 0.6;
+  return with_rows * (own > 1 ? own : 1);
+}
+
+// Tiles of 128 rows x 128 or 256 features, or, of a pair of CTAs, 256 x 256; of rows by index
+// 128 x 256.
 enum class Tiles { k128x128, k128x256, k256x256 };
 int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st);
 // At most `rows` (16, 32 or 64) rows at a time against weights streamed once.
 int run_stream(const Linear& p, int rows, cudaStream_t st);
-// About how many us that takes.
+// About how many us that takes (32 or 64).
 double stream_cost(const Linear& p, int rows);
 
 }  // namespace fp8

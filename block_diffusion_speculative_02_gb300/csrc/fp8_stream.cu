@@ -378,10 +378,10 @@ stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 // 4096 x 4096 in two shares of 96 tiles take 14 us), and a second wave of them costs 4 more: 16
 // rows x 4096 x 4096 (32 tiles of 32 blocks) take 7.4, 6.6, 6.3 us in two, four, eight shares, 64
 // rows 8.2, 8.2, 13.2; 16 rows x 49152 x 4096 (384 tiles) 34 us whole and 43 in two shares.
-double stream_split(const Linear& p, int tile_rows, int* split) {
-  const double tiles = static_cast<double>(most_tiles(p, tile_rows, 128));
-  const double first = static_cast<double>(most_tiles(p, p.m, 128));      // of an expert each
-  const double block = 0.16 + tile_rows * 0.0026, join = 1.0 + tile_rows / 64.0;
+double stream_split(const Linear& p, int tile_rows, double tiles, int* split) {
+  const double experts = p.start ? std::min(p.groups, p.m) : 1;
+  const double first = experts * ((p.n + 127) / 128);                     // tiles of these
+  const double block = 0.16 + tile_rows * (p.rows ? 0.0036 : 0.0026), join = 1.0 + tile_rows / 64.0;
   const double memory = (0.0024 * first + 0.0004 * (tiles - first)) * p.k_blocks;
   double cost = 0;
   for (int s = 1; s <= kMaxSplit && s <= p.k_blocks; s *= 2) {
@@ -423,7 +423,7 @@ int run(Linear p, cudaStream_t st) {
   const long long tiles = most_tiles(p, kT, 128);
   if (tiles > 0x7FFFFFFF / 16) return DFLASH_E_UNSUPPORTED;
   int split;
-  stream_split(p, kT, &split);
+  stream_split(p, kT, static_cast<double>(tiles), &split);
   // shares of K: one tile to a cluster; whole tiles: two CTAs to an SM walk them
   const long long ctas = split > 1 ? tiles * split : tiles < 2 * nsm ? tiles : 2 * nsm;
   cudaLaunchConfig_t cfg = {};
@@ -447,7 +447,7 @@ int run(Linear p, cudaStream_t st) {
 
 double stream_cost(const Linear& p, int rows) {
   int split;
-  return stream_split(p, rows, &split);
+  return stream_split(p, rows, row_tiles(p, rows) * ((p.n + 127) / 128), &split);
 }
 
 int run_stream(const Linear& p, int rows, cudaStream_t st) {

@@ -126,6 +126,7 @@ template <bool kPair, int kN, bool kIndex>
 __global__ void __launch_bounds__(kTileWarps * 32, 1)
 tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
             const __grid_constant__ CUtensorMap map_out, const Linear p) {
+  static_assert(!(kPair && kIndex), "rows by index: tiles of single CTAs");
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kRows = kTileRows * kCtas;
   constexpr int kStage = tile_stage_bytes<kPair, kN>();
@@ -153,19 +154,15 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   uint64_t* sempty = sfull + kRing;      // [kRing] both halves' sums of that block are there
   uint64_t* ifull = sempty + kRing;      // [kInfo] a tile's place is written down
   uint64_t* iempty = ifull + kInfo;      // [kInfo] and read
-  uint64_t* landed = kIndex && rank ? iempty + kInfo : full;   // a stage's rows by index are there
-  uint32_t* tmem_slot =
-      reinterpret_cast<uint32_t*>(iempty + kInfo + (kIndex && kPair ? p.n_stages : 0));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(iempty + kInfo);
   const Groups groups = groups_at(reinterpret_cast<uint8_t*>(tmem_slot + 1), p.groups);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int t_first = blockIdx.x / kCtas, t_step = gridDim.x / kCtas;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.n_stages; ++i) {
-      // (the bytes of both CTAs count in the first; its rows by index 64, the other CTA's 1)
-      mbar_init(&full[i], 1 + (kIndex ? 64 + kCtas - 1 : 0));
+      mbar_init(&full[i], 1 + (kIndex ? 64 : 0));
       mbar_init(&empty[i], 2);           // the products of both halves
-      if (kIndex && rank) mbar_init(&landed[i], 64);
     }
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&ifull[i], 1);
@@ -295,22 +292,6 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       }
       if (elect_one()) mma_done_here<kPair>(&mdrain[half]);
       if (lane == 0) mbar_wait_drain(&mdrain[half], 0, p.status);
-    } else if (kIndex && warp == 1) {    // hands this CTA's rows by index on to the first
-      uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      for (int t = t_first; all(ok && t < total); t += t_step) {
-#pragma unroll 1
-        for (int b = 0; b < p.k_blocks; ++b) {
-          ok = all(wait_on(&landed[stage], phase, p.status));
-          if (!ok) break;
-          fence_proxy_async_smem();
-          if (elect_one()) arrive_at<kPair>(first_cta<kPair>(&full[stage]));
-          if (++stage == static_cast<uint32_t>(p.n_stages)) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
     }
   } else if (warp == 2) {
     // Writes down the tiles' places and copies the scales, kRing - kSlots blocks ahead of the sums:
@@ -390,7 +371,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       for (int t = t_first; all(ok && t < total); t += t_step, ++in) {
         ok = all(wait_on(&ifull[in % kInfo], (in / kInfo) & 1, p.status));
         if (!ok) break;
-        ok = copies.tile<64, kTileRows>(p, smem, kStage, empty, landed, 0, p.k_blocks,
+        ok = copies.tile<64, kTileRows>(p, smem, kStage, empty, full, 0, p.k_blocks,
                                         sources + in % kInfo * kTileRows, first, lane);
         __syncwarp();
         if (elect_one()) mbar_arrive(&iempty[in % kInfo]);
@@ -467,10 +448,9 @@ int run(Linear p, cudaStream_t st) {
   constexpr int kRing = ring<kN>();
   const int tail = kStoreBytes + kRing * kScaleRow * 4 + kInfo * (16 + kTileRows * 4) +
                    (4 * slots<kN>() + 2 + 2 * kRing + 2 * kInfo) * 8 + 4 + groups_bytes(p.groups);
-  constexpr int kBars = kIndex && kPair ? 24 : 16;   // a stage's
-  p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + kBars);
+  p.n_stages = (kSmemLimit - 1024 - tail) / (kStage + 16);
   if (p.n_stages > kMaxStages) p.n_stages = kMaxStages;
-  const int smem = 1024 + p.n_stages * (kStage + kBars) + tail;
+  const int smem = 1024 + p.n_stages * (kStage + 16) + tail;
   CUtensorMap mx, mw, mo = {};
   int rc = make_map(&mx, p.x, p.k, p.n_src, p.box_rows);
   if (!rc) rc = make_map(&mw, p.w, p.k, static_cast<long long>(p.groups) * p.n, kN / 2 / kCtas);
@@ -514,13 +494,10 @@ int run(Linear p, cudaStream_t st) {
 }  // namespace
 
 int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st) {
-  const bool index = p.rows != nullptr;
-#define DFLASH_RUN(kPair, kN) (index ? run<kPair, kN, true>(p, st) : run<kPair, kN, false>(p, st))
-  if (tiles == Tiles::k128x128)          // (plain products only)
-    return index ? DFLASH_E_UNSUPPORTED : run<false, 128, false>(p, st);
-  if (tiles == Tiles::k128x256) return DFLASH_RUN(false, 256);
-  return DFLASH_RUN(true, 256);
-#undef DFLASH_RUN
+  if (p.rows) return run<false, 256, true>(p, st);
+  if (tiles == Tiles::k128x128) return run<false, 128, false>(p, st);
+  if (tiles == Tiles::k128x256) return run<false, 256, false>(p, st);
+  return run<true, 256, false>(p, st);
 }
 
 }  // namespace fp8

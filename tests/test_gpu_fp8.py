@@ -323,7 +323,12 @@ GROUPED = [("even", 4, 4, 130, 144), ("skew", 128, 128, 256, 512), ("skew", 128,
            ("one", 1, 50, 128, 128), ("skew", 1024, 700, 16, 128), ("skew", 33, 300, 129, 2048),
            ("even", 64, 4096, 128, 256), ("even", 2, 3000, 2000, 256),
            ("even", 2, 1300, 2816, 144), ("even", 2, 1300, 300, 400), ("skew", 40, 800, 5000, 144),
-           ("skew", 3, 200, 1200, 2304), ("skew", 5, 2800, 4096, 16), ("one", 1000, 1500, 512, 272)]
+           ("skew", 3, 200, 1200, 2304), ("skew", 5, 2800, 4096, 16), ("one", 1000, 1500, 512, 272),
+           ("even", 2, 1300, 2816, 656), ("skew", 16, 2900, 1500, 1040),
+           ("even", 4, 330, 1536, 2048),
+           ("skew", 64, 12000, 400, 656), ("even", 6, 2600, 900, 1040), ("skew", 8, 560, 2050, 784),
+           ("skew", 4, 8000, 1050, 656), ("skew", 300, 20000, 140, 144),
+           ("skew", 1024, 40000, 300, 144)]
 
 
 @pytest.mark.parametrize("kind,e,m,n,k", GROUPED)
