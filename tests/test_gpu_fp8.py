@@ -328,7 +328,7 @@ GROUPED = [("even", 4, 4, 130, 144), ("skew", 128, 128, 256, 512), ("skew", 128,
            ("even", 4, 330, 1536, 2048),
            ("skew", 64, 12000, 400, 656), ("even", 6, 2600, 900, 1040), ("skew", 8, 560, 2050, 784),
            ("skew", 4, 8000, 1050, 656), ("skew", 300, 20000, 140, 144),
-           ("skew", 1024, 40000, 300, 144)]
+           ("skew", 1024, 40000, 300, 144), ("skew", 1024, 120000, 140, 272)]
 
 
 @pytest.mark.parametrize("kind,e,m,n,k", GROUPED)
