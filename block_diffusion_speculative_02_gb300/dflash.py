@@ -817,6 +817,29 @@ def dflash_fp8_weight(w, q, scale, stream=None):
         _check(rc, "dflash_fp8_weight")
 
 
+def _product(x, x_scale, w, w_scale, out, ws, device: int, xs_shape, ws_shape, out_shape):
+    """What a product takes: pointers of x, w and their scales, of out with its row pitch, and of
+    the workspace with its size.  (Checked in one expression; where it does not hold, one by one.)"""
+    try:
+        if x.dtype is F8 and w.dtype is F8 and x_scale.dtype is _F32 and w_scale.dtype is _F32 \
+                and out.dtype is _BF and ws.dtype is torch.uint8 \
+                and x_scale.shape == xs_shape and w_scale.shape == ws_shape \
+                and out.shape == out_shape and x.is_contiguous() and w.is_contiguous() \
+                and x_scale.is_contiguous() and w_scale.is_contiguous() and ws.is_contiguous() \
+                and device == x.get_device() == w.get_device() == x_scale.get_device() \
+                == w_scale.get_device() == out.get_device() == ws.get_device():
+            pitch, step = out.stride()
+            if step == 1:
+                return (x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                        out.data_ptr(), pitch if out_shape[0] > 1 else out_shape[1],
+                        ws.data_ptr(), ws.numel())
+    except AttributeError:
+        pass
+    return (*_codes(x, x_scale, device, None, xs_shape, "x", "x_scale"),
+            *_codes(w, w_scale, device, None, ws_shape, "w", "w_scale"),
+            *_matrix(out, device, "out", out_shape), *_ws_on(ws, device))
+
+
 def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
     """out [M, N] (bf16, rows may be strided) = x w^T of 8-bit rows x [M, K], weights w [N, K]."""
     dev, st = _here(stream)
@@ -826,9 +849,8 @@ def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
         raise ValueError(f"x has {k} columns, w {kw}")
     kb = -(-k // 128)
     rc = load_library().dflash_fp8_linear(
-        m, n, k, *_codes(x, x_scale, dev, None, (kb, m), "x", "x_scale"),
-        *_codes(w, w_scale, dev, None, (-(-n // 128), kb), "w", "w_scale"),
-        *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
+        m, n, k, *_product(x, x_scale, w, w_scale, out, ws, dev, (kb, m), (-(-n // 128), kb),
+                           (m, n)), st)
     if rc:
         _check(rc, "dflash_fp8_linear")
 
@@ -844,11 +866,11 @@ def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None
     m, kb = _shape(out, 2, "out")[0], -(-k // 128)
     if rows is None and m != src:
         raise ValueError(f"out has {m} rows, x {src}: rows must say which")
+    xp, xsp, wp, wsp, op, pitch, sp, size = _product(
+        x, x_scale, w, w_scale, out, ws, dev, (kb, src), (e, -(-n // 128), kb), (m, n))
     rc = load_library().dflash_fp8_grouped(
-        m, src, e, n, k, *_codes(x, x_scale, dev, None, (kb, src), "x", "x_scale"),
-        *_codes(w, w_scale, dev, None, (e, -(-n // 128), kb), "w", "w_scale"),
-        _whole(start, dev, torch.int32, (e + 1,), "start"),
-        None if rows is None else _whole(rows, dev, torch.int32, (m,), "rows"),
-        *_matrix(out, dev, "out", (m, n)), *_ws_on(ws, dev), st)
+        m, src, e, n, k, xp, xsp, wp, wsp, _whole(start, dev, torch.int32, (e + 1,), "start"),
+        None if rows is None else _whole(rows, dev, torch.int32, (m,), "rows"), op, pitch, sp,
+        size, st)
     if rc:
         _check(rc, "dflash_fp8_grouped")

@@ -610,6 +610,34 @@ def test_large_offsets():
     assert bool((out.abs().amax(1) > 0).all())
 
 
+@pytest.mark.parametrize("m", [24, 3000])
+def test_weights_past_2_to_the_32_bytes(m):
+    dfl = _dfl()
+    e, n, k = 36, 15000, 8192                          # 4.4 GB
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w, wscale = dfl.alloc_fp8_weight(e, n, k)
+    for i in range(e):
+        part = torch.randn(n, k, generator=g, device="cuda").to(BF)
+        dfl.dflash_fp8_weight(part, w[i], wscale[i])
+    whole, whole_scale = dfl.alloc_fp8_weight(e, n, k)
+    big = torch.zeros(e, n, k, dtype=BF, device="cuda")
+    big[-1] = part
+    dfl.dflash_fp8_weight(big, whole, whole_scale)     # the last past 2^32 of codes and of bf16
+    assert torch.equal(whole[-1].view(torch.uint8), w[-1].view(torch.uint8))
+    assert torch.equal(whole_scale[-1], wscale[-1])
+    del big, whole
+    rng = np.random.default_rng(m)
+    x, xs, xv = random_x(rng, m, k)
+    out, ws = torch.zeros(m, n, dtype=BF, device="cuda"), dfl.alloc_fp8_workspace()
+    start = [0, m // 2] + [m // 2] * (e - 2) + [m]
+    dfl.dflash_fp8_grouped(x, xs, w, wscale, i32(start), None, out, ws)
+    for at, expert in ((0, 0), (m // 2, e - 1)):
+        for col in (0, n - 100):
+            wv = O.weight_value(codes(w[expert]), wscale[expert].cpu().numpy())[col:col + 100]
+            check_product(f64(out[at:at + 12, col:col + 100]), xv[at:at + 12], wv)
+    assert dfl.dflash_read_status(ws) == 0
+
+
 @pytest.mark.parametrize("n", [300, 1400, 2300])
 def test_more_rows_than_a_band(n):
     """Row tiles past a band of 64, with feature tiles that fill no chunk of four."""
