@@ -38,6 +38,7 @@ __global__ void norm_rows_kernel(const NormParams p) {
   const int row = kWarp ? blockIdx.x * kWarpRows + threadIdx.y : blockIdx.x;
   const int pieces = p.cols / 16;
   griddep_wait();
+  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
   if (row >= p.rows) return;                                  // whole warps
   float v[kChunks][16];
   float ss = 0.f;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kSiluThreads) silu_rows_kernel(const SiluParam
   const int b = static_cast<int>(unit - row * p.blocks);
   const int col = b * kBlockK + (threadIdx.x & 7) * 16;
   griddep_wait();
+  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
   const bool live = row < p.rows && col < p.cols;
   uint4 g4[2] = {}, u4[2] = {};
   if (live) {
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightPara
   const int col = kb * kBlockK + (t & 7) * 16;
   const size_t base = static_cast<size_t>(g) * p.n * p.k + col;
   griddep_wait();
+  griddep_launch_dependents();           // (they wait for the end of this grid before they read)
   uint4 x[4][2];
   uint32_t m = 0;
 #pragma unroll
