@@ -68,6 +68,7 @@ int check(int m, int n_src, int groups, int n, int k, const void* x, const float
       (reinterpret_cast<uintptr_t>(out) & 1u))
     return DFLASH_E_ALIGN;
   if (!wsp || ws_bytes < 64) return DFLASH_E_WORKSPACE;
+  if (!aligned4(wsp)) return DFLASH_E_ALIGN;
   *p = Linear{};
   p->x = static_cast<const uint8_t*>(x);
   p->w = static_cast<const uint8_t*>(w);

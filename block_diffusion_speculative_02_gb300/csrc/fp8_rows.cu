@@ -251,6 +251,10 @@ extern "C" int dflash_fp8_norm_rows(int32_t rows, int32_t cols, const void* x, i
   if (bad_pitch(x_pitch, cols) || (residual && bad_pitch(residual_pitch, cols)) ||
       (sum_out && bad_pitch(sum_pitch, cols)))
     return DFLASH_E_ARG;
+  // in place: each row where it was
+  if (sum_out && ((sum_out == x && sum_pitch != x_pitch) ||
+                  (sum_out == residual && sum_pitch != residual_pitch)))
+    return DFLASH_E_ARG;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(norm_w) || !aligned16(sum_out) ||
       !aligned16(q) || x_pitch % 8 || (residual && residual_pitch % 8) ||
       (sum_out && sum_pitch % 8) || reinterpret_cast<uintptr_t>(scale) % 4)

@@ -606,8 +606,8 @@ DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
  * e4m3(h * (448 / a)), to nearest, ties to even; an infinity or NaN among them makes scale
  * and codes of the whole block NaN.
  * No rows (M = 0) is a call that does nothing.  The calls keep nothing between them; the
- * workspace of the products (64 bytes, zeroed once) is their status word only, and calls on
- * several streams may share it.
+ * workspace of the products (64 bytes, aligned to 4, zeroed once) is their status word only,
+ * and calls on several streams may share it.
  */
 
 /*

@@ -28,6 +28,8 @@ def test_norm_rows_refuses():
     assert f(xp=260) == f(x=P + 2) == f(r=P + 8, rp=256) == f(w=P + 2) == E_ALIGN
     assert f(s=P + 4, sp=256) == f(q=P + 1) == f(scale=P + 2) == E_ALIGN
     assert f(rows=0, x=None, q=None, scale=None) == 0                 # nothing to do
+    # sum_out in the place of x or of the residual, its rows elsewhere
+    assert f(s=P, sp=264) == f(x=2 * P, r=P, rp=256, s=P, sp=512) == E_ARG
 
 
 def test_silu_mul_refuses():
@@ -73,6 +75,7 @@ def test_products_refuse():
         assert f(m=2 ** 31 - 1, pitch=64) == f(n=2 ** 31 - 1, pitch=2 ** 31) == E_UNSUPPORTED
         assert f(x=P + 8) == f(w=P + 8) == f(xs=P + 2) == f(ws=P + 2) == f(out=P + 1) == E_ALIGN
         assert f(wsp=None) == f(nws=63) == E_WORKSPACE
+        assert f(wsp=P + 2) == E_ALIGN
         assert f(m=0, x=None, out=None) == 0
     assert grouped(g=0) == grouped(src=-1) == grouped(start=None) == E_ARG
     assert grouped(src=5) == E_ARG                                    # which rows of x?
