@@ -7,6 +7,10 @@ value.  A product's fp32 sum over K is off by at most
 32 products meet in one step of the tensor cores, aligned to the largest with at least 24 bits
 (32 2^-24 = 2^-19 of it), and one rounded addition for each block; then 2^-8 of the value for the
 rounding to bf16."""
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -722,6 +726,44 @@ def test_first_use_inside_a_capture(m):
         graph.replay()
     stream.synchronize()
     check_product(f64(out), xv, wv)
+
+
+FIRST_USE = """
+import sys, torch
+import block_diffusion_speculative_02_gb300 as dfl
+m, n, k, index = map(int, sys.argv[1:])
+x, xs = dfl.alloc_fp8_rows(m, k)
+w, ws = dfl.alloc_fp8_weight(1, n, k)
+x.copy_(torch.eye(m, k))
+xs.fill_(1)
+ws.fill_(1)
+w.copy_((torch.arange(n * k) % 17).view(1, n, k).float())
+out, space = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda"), dfl.alloc_fp8_workspace()
+start = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+rows = torch.arange(m, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    if index:
+        dfl.dflash_fp8_grouped(x, xs, w, ws, start, rows, out, space)
+    else:
+        dfl.dflash_fp8_linear(x, xs, w[0], ws[0], out, space)
+graph.replay()
+torch.cuda.synchronize()
+assert dfl.dflash_read_status(space) == 0
+assert torch.equal(out[:k].float(), w[0].float().T[:m]) and not bool(out[k:].any())
+"""
+
+
+@pytest.mark.parametrize("m,n,k,index", [(2500, 387, 144, 0), (1500, 1537, 144, 0),
+                                         (1500, 1537, 656, 0), (2500, 387, 144, 1),
+                                         (40, 4096, 1024, 1)])
+def test_first_use_of_a_process_inside_a_capture(m, n, k, index):
+    """Each kernel of the products for the first time, while a graph is captured."""
+    done = subprocess.run([sys.executable, "-c", FIRST_USE, str(m), str(n), str(k), str(index)],
+                          capture_output=True, text=True, timeout=120,
+                          cwd=Path(__file__).resolve().parents[1])
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_rows_of_x_given_many_times():
