@@ -122,7 +122,8 @@ __device__ __forceinline__ void store_rows(const Linear& p, const CUtensorMap* m
   __syncwarp();
 }
 
-template <bool kPair, int kN, bool kIndex>
+// kSend: of an epilogue warp's features, those on their way out at a time.
+template <bool kPair, int kN, bool kIndex, int kSend>
 __global__ void __launch_bounds__(kTileWarps * 32, 1)
 tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
             const __grid_constant__ CUtensorMap map_out, const Linear p) {
@@ -133,7 +134,7 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   constexpr int kHalf = kN / 2;          // features of a product
   constexpr int kShare = kHalf / kCtas;  // of these, features whose weights this CTA holds
   constexpr int kOwn = kN / 4;           // features of an epilogue warp
-  constexpr int kStore = 32 * kOwn * 2;  // its rows on their way out
+  constexpr int kStore = 32 * kSend * 2;
   constexpr int kSlots = slots<kN>(), kRing = ring<kN>();
   constexpr int kCols = kSlots * kN;     // TMEM columns
   constexpr int kBlocksN = kN / kBlockK;
@@ -424,8 +425,10 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
       ++in;
       if (!known) continue;
       const int at = rank * kTileRows + quad * 32;
-      store_rows<kOwn>(p, &map_out, acc, buf, tile.x + at, tile.y - at, tile.z * kN + part * kOwn,
-                       lane);
+#pragma unroll
+      for (int c = 0; c < kOwn; c += kSend)
+        store_rows<kSend>(p, &map_out, acc + c / 2, buf, tile.x + at, tile.y - at,
+                          tile.z * kN + part * kOwn + c, lane);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -438,13 +441,13 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
   }
 }
 
-template <bool kPair, int kN, bool kIndex>
+template <bool kPair, int kN, bool kIndex, int kSend = kN / 4>
 int run(Linear p, cudaStream_t st) {
   constexpr int kCtas = kPair ? 2 : 1;
   constexpr int kStage = tile_stage_bytes<kPair, kN>();
   p.n_tiles = (p.n + kN - 1) / kN;
   p.box_rows = p.n_src < kTileRows ? p.n_src : kTileRows;
-  constexpr int kStoreBytes = kEpiWarps * 32 * (kN / 4) * 2;
+  constexpr int kStoreBytes = kEpiWarps * 32 * kSend * 2;
   constexpr int kRing = ring<kN>();
   const int tail = kStoreBytes + kRing * kScaleRow * 4 + kInfo * (16 + kTileRows * 4) +
                    (4 * slots<kN>() + 2 + 2 * kRing + 2 * kInfo) * 8 + 4 + groups_bytes(p.groups);
@@ -455,8 +458,8 @@ int run(Linear p, cudaStream_t st) {
   int rc = make_map(&mx, p.x, p.k, p.n_src, p.box_rows);
   if (!rc) rc = make_map(&mw, p.w, p.k, static_cast<long long>(p.groups) * p.n, kN / 2 / kCtas);
   if (!rc && p.vector)
-    rc = make_tmap_2d_store_bf16(&mo, p.out, p.n, p.m, p.out_pitch * 2, kN / 4, 32);
-  const auto kernel = tile_kernel<kPair, kN, kIndex>;
+    rc = make_tmap_2d_store_bf16(&mo, p.out, p.n, p.m, p.out_pitch * 2, kSend, 32);
+  const auto kernel = tile_kernel<kPair, kN, kIndex, kSend>;
   static std::atomic<uint64_t> ready{0};
   if (!rc)
     rc = kv4::smem_limit_once(&ready, reinterpret_cast<const void*>(kernel), kSmemLimit,
@@ -497,7 +500,11 @@ int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st) {
   if (p.rows) return run<false, 256, true>(p, st);
   if (tiles == Tiles::k128x128) return run<false, 128, false>(p, st);
   if (tiles == Tiles::k128x256) return run<false, 256, false>(p, st);
-  return run<true, 256, false>(p, st);
+  // Many blocks a tile: the way out in two halves leaves shared memory for a fifth stage (512 rows
+  // x 24576 x 4096 41 us, 45 with four; 700 x 12288 x 4096 27 and 28); few: at once (4000 x 12288 x
+  // 768 40 us, 43.5 in halves; 2000 x 12288 x 256 13.2 and 14.5; x 1408 to 2048 alike within the
+  // noise).
+  return p.k_blocks >= 32 ? run<true, 256, false, 32>(p, st) : run<true, 256, false>(p, st);
 }
 
 }  // namespace fp8

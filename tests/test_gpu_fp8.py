@@ -240,7 +240,8 @@ SHAPES = [(1, 1, 16), (1, 128, 128), (1, 4096, 4096), (2, 130, 144), (7, 257, 40
           (2048, 2048, 512), (128, 20000, 144), (2148, 2048, 256), (2200, 1500, 272),
           (1, 24576, 128), (24, 8192, 640), (50, 20000, 384), (2500, 387, 144), (200, 5003, 2064),
           (900, 2600, 144), (1500, 1537, 656), (1000, 2600, 1168), (4000, 1029, 656),
-          (500, 387, 2064), (700, 1300, 4000), (300, 2051, 144), (150, 4096, 8192)]
+          (500, 387, 2064), (700, 1300, 4000), (300, 2051, 144), (150, 4096, 8192),
+          (700, 5003, 4112), (600, 8200, 4096)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -258,7 +259,8 @@ def test_linear(m, n, k):
 
 # (of 387 features: streamed, and tiles of 128 x 128; of 1537 tiles of 128 x 256, and pairs)
 @pytest.mark.parametrize("m,n,k", [(5, 387, 320), (40, 387, 320), (200, 387, 320), (600, 387, 320),
-                                   (2500, 387, 144), (1500, 1537, 144), (1500, 1537, 656)])
+                                   (2500, 387, 144), (1500, 1537, 144), (1500, 1537, 656),
+                                   (1500, 1537, 4112)])
 @pytest.mark.parametrize("apart,offset", [(8, 0), (9, 0), (16, 3), (16, 8)])
 def test_linear_into_strided_rows(m, n, k, apart, offset):
     """Rows of out that lie apart, also unaligned: nothing between them is touched."""
@@ -332,7 +334,8 @@ GROUPED = [("even", 4, 4, 130, 144), ("skew", 128, 128, 256, 512), ("skew", 128,
            ("even", 4, 330, 1536, 2048),
            ("skew", 64, 12000, 400, 656), ("even", 6, 2600, 900, 1040), ("skew", 8, 560, 2050, 784),
            ("skew", 4, 8000, 1050, 656), ("skew", 300, 20000, 140, 144),
-           ("skew", 1024, 40000, 300, 144), ("skew", 1024, 120000, 140, 272)]
+           ("skew", 1024, 40000, 300, 144), ("skew", 1024, 120000, 140, 272),
+           ("skew", 5, 2900, 1030, 4112)]
 
 
 @pytest.mark.parametrize("kind,e,m,n,k", GROUPED)
