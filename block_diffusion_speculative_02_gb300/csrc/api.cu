@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "fp8_linear.cuh"
 #include "host.h"
 #include "kv4_attention.cuh"
 #include "streamk_gemm.cuh"
@@ -53,41 +54,86 @@ int injected_failure(const char* entry) {
 
 namespace {
 
-// A warp each waits on an mbarrier of its own with the bounded waits that the kernels use: the
-// one of common.cuh and both forms of the 4-bit attention's.  With arrive == 0 nothing ever
-// arrives: each gives up after its time limit, and the kernel returns normally.  The status
-// word gets DFLASH_ST_TIMEOUT if one of them gave up although its arrival came, or if all did
-// without one, none of them before 0.9 of the limit.
+// The bounded waits that the kernels use, a warp each:
+//   0       the one of common.cuh
+//   1, 2    both forms of the 4-bit attention's
+//   3 to 6  the 8-bit products' on two barriers, of which without arrivals neither, only the second,
+//           only the first and both are arrived at
+//   7 to 9  their hand-over: a watcher (7) and two warps that it watches for go through kTurns turns
+//           at one named barrier; the two arrive for the next turn, without arrivals up to half
+//           of the turns
+// With arrive == 0 nothing else arrives: each wait gives up after its time limit, and the kernel
+// returns normally.  The status word gets DFLASH_ST_TIMEOUT if one of them gave up although its
+// arrival came, or if all others gave up, none before 0.9 of the limit, and the watched warps went
+// through all their turns.
+constexpr int kTurns = 16;
+constexpr int kSelfWarps = 10;
+
 __global__ void selftest_wait_kernel(int arrive, uint32_t* status) {
-  __shared__ uint64_t bar[3];
-  __shared__ uint32_t gave_up[3], early;
-  __shared__ int abort_flag;
+  __shared__ uint64_t bar[3], both[4][2], turn[kTurns], there;
+  __shared__ uint32_t gave_up[8], early;
+  __shared__ int abort_flag, turns[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(&bar[i], 1);
-      gave_up[i] = 0;
-    }
-    abort_flag = 0;
+    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&both[i >> 1][i & 1], 1);
+    for (int i = 0; i < kTurns; ++i) mbar_init(&turn[i], i ? 2 : 1);
+    mbar_init(&there, 1);
+    for (int i = 0; i < 8; ++i) gave_up[i] = 0;
+    abort_flag = turns[0] = turns[1] = 0;
     early = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  if (arrive && lane == 0) mbar_arrive(&bar[warp]);
+  if (threadIdx.x == 0) {
+    mbar_arrive(&there);
+    for (int i = 0; arrive && i < 3; ++i) mbar_arrive(&bar[i]);
+    for (int i = 0; i < 4; ++i) {
+      if (arrive || i >= 2) mbar_arrive(&both[i][0]);
+      if (arrive || i & 1) mbar_arrive(&both[i][1]);
+    }
+    mbar_arrive(&turn[0]);
+  }
+  __syncthreads();
   const uint64_t t0 = globaltimer_ns();
   if (warp == 0) {
     if (lane == 0) mbar_wait(&bar[0], 0, &abort_flag, &gave_up[0]);
   } else if (warp == 1) {
     kv4::wait_on<false>(&bar[1], 0, &gave_up[1]);
-  } else {
+  } else if (warp == 2) {
     kv4::wait_on<true>(&bar[2], 0, &gave_up[2]);
+  } else if (warp < 7) {
+    const bool ok = fp8::wait_both(&both[warp - 3][0], 0, &both[warp - 3][1], 0, &gave_up[warp]);
+    if (ok != (gave_up[warp] == 0)) early = 1;
+  } else if (warp == 7) {
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < kTurns; ++i)
+      ok = fp8::hand_over(ok, &turn[i], 0, &there, 0, 1, 96, &gave_up[7]);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kTurns; ++i) {
+      named_bar_sync(1, 96);
+      if (lane == 0) {
+        ++turns[warp - 8];
+        if (i + 1 < (arrive ? kTurns : kTurns / 2)) mbar_arrive(&turn[i + 1]);
+      }
+      __syncwarp();
+    }
   }
-  if (lane == 0 && globaltimer_ns() - t0 < kWaitLimitNs / 10 * 9) early = 1;
+  if (warp != 6 && lane == 0 && globaltimer_ns() - t0 < kWaitLimitNs / 10 * 9) early = 1;
   __syncthreads();
   if (threadIdx.x == 0) {
-    const uint32_t any = gave_up[0] | gave_up[1] | gave_up[2];
-    const uint32_t all = gave_up[0] & gave_up[1] & gave_up[2];
-    set_status(status, arrive ? any : early ? 0 : all);
+    uint32_t any = gave_up[6], all = DFLASH_ST_TIMEOUT;
+    for (int i = 0; i < 8; ++i) {
+      any |= gave_up[i];
+      if (i != 6) all &= gave_up[i];
+    }
+    if (turns[0] != kTurns || turns[1] != kTurns) {
+      any = DFLASH_ST_TIMEOUT;
+      all = 0;
+    }
+    set_status(status, arrive ? any : early || gave_up[6] ? 0 : all);
   }
 }
 
@@ -299,7 +345,7 @@ extern "C" int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes,
                                     dflash_stream_t stream) {
   DFLASH_ENTRY("dflash_selftest_wait");
   if (!ws || ws_bytes < 64) return DFLASH_E_WORKSPACE;
-  selftest_wait_kernel<<<1, 96, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  selftest_wait_kernel<<<1, 32 * kSelfWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       arrive, static_cast<uint32_t*>(ws));
   return cuda_err(cudaGetLastError());
 }

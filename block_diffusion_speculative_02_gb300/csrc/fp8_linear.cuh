@@ -71,8 +71,10 @@ __device__ __forceinline__ bool wait_both(uint64_t* a, uint32_t pa, uint64_t* b,
       : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb)
       : "memory");
   if (all(ok)) return true;
-  ok = wait_on(a, pa, status) && wait_on(b, pb, status);
-  return all(ok);
+  // (lanes that saw the phase in the last try and lanes that gave up decide together, before the
+  // second wait, which the warp enters as a whole or not at all)
+  if (!all(wait_on(a, pa, status))) return false;
+  return all(wait_on(b, pb, status));
 }
 
 // --------------------------------------------------------------------------------------------
@@ -164,6 +166,20 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 // Arrive at a named barrier of n threads without waiting at it.
 __device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t n) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// A watcher's turn: waits at both mbarriers for the warps that meet it at named barrier `id` (n
+// threads with its own), and returns whether to go on waiting.  While it does (ok), it only arrives
+// there.  Once a wait gave up, the rest are skipped, and it syncs instead: arriving without a wait
+// between would run ahead of the other warps, and the barrier's count no longer mean one turn.
+__device__ __forceinline__ bool hand_over(bool ok, uint64_t* a, uint32_t pa, uint64_t* b,
+                                          uint32_t pb, uint32_t id, uint32_t n, uint32_t* status) {
+  ok = ok && wait_both(a, pa, b, pb, status);
+  if (ok)
+    named_bar_arrive(id, n);
+  else
+    named_bar_sync(id, n);
+  return ok;
 }
 
 // The barrier of this name in the first CTA of a pair (a single CTA: its own).

@@ -344,9 +344,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 4 || warp == 5) {
-    // Watches the accumulators of half of the features, and the scales, for the epilogue.  Once a
-    // wait gave up, the rest are skipped, and the epilogue is met at the barriers instead (arriving
-    // without a wait between would count twice): it goes through its blocks all the same.
+    // Watches the accumulators of half of the features, and the scales, for the epilogue, which goes
+    // through its blocks to the end also when a wait gave up.
     const int half = warp & 1;
     bool ok = true;
     uint32_t it = 0;
@@ -354,12 +353,8 @@ tile_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll 1
       for (int b = 0; b < p.k_blocks; ++b, ++it) {
         const uint32_t slot = kSlots * half + it % kSlots;
-        ok = ok && wait_both(&tfull[slot], (it / kSlots) & 1, &sfull[it % kRing],
-                             (it / kRing) & 1, p.status);
-        if (ok)
-          named_bar_arrive(1 + slot, 32 * (kEpiWarps / 2 + 1));
-        else
-          named_bar_sync(1 + slot, 32 * (kEpiWarps / 2 + 1));
+        ok = hand_over(ok, &tfull[slot], (it / kSlots) & 1, &sfull[it % kRing], (it / kRing) & 1,
+                       1 + slot, 32 * (kEpiWarps / 2 + 1), p.status);
         if (elect_one()) mbar_arrive(&sempty[it % kRing]);
       }
     }
