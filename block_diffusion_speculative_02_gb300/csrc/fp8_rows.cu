@@ -29,11 +29,68 @@ struct NormParams {
 };
 
 constexpr int kWarpRows = 8;    // rows of a CTA where a warp takes one
+constexpr int kMostLanes = 512; // threads of a CTA that takes one
+
+// Below this mean of squares some of them may have left the range of fp32 (2^-126), and with eps
+// so small they count.
+__device__ __forceinline__ float least_mean() { return __uint_as_float((127 - 100) << 23); }
+
+// The sum over a row of what each of its threads has, the same bits in all of them.
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float x, int t, int step) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (!kWarp) {
+    __shared__ float part[32];           // (between two sums the row's threads meet in row_max)
+    if ((t & 31) == 0) part[t >> 5] = x;
+    __syncthreads();
+    x = (t & 31) < (step >> 5) ? part[t & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  }
+  return x;
+}
+
+// The largest magnitude (as bits) of a row, likewise.
+template <bool kWarp>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, int t, int step) {
+  m = warp_max_u32(m);
+  if (!kWarp) {
+    __shared__ uint32_t part[32];
+    if ((t & 31) == 0) part[t >> 5] = m;
+    __syncthreads();
+    m = warp_max_u32((t & 31) < (step >> 5) ? part[t & 31] : 0u);
+  }
+  return m;
+}
+
+// The mean of squares of a row where some leave the range of fp32 (elements past 2^64, or a row of
+// tiny ones over next to no eps), and what it is the mean for: the row times 2^k, which brings its
+// largest element, or sqrt(eps) if that is larger, next to 1.  h stays what it was,
+//   (2^k s) / sqrt(mean (2^k s)^2 + 2^2k eps).
+// A row with an infinity or NaN, or of zeros over nothing, stays as it is.  (A call, which takes a
+// copy of the row: as part of the kernel it cost every row of 5120 and 8192 columns 1 to 2 %.)
+template <int kN, bool kWarp>
+__device__ __noinline__ float2 wide_mean(const float (&v)[kN], float mean, int cols, float eps,
+                                         int t, int step) {
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int i = 0; i < kN; ++i) m = max(m, abs_bits(v[i]));
+  m = max(row_max<kWarp>(m, t, step), __float_as_uint(sqrtf(eps)));
+  if (m == 0 || m >= 0x7F800000u) return make_float2(mean, 1.f);
+  const int k = max(254 - static_cast<int>(m >> 23), 1);              // biased
+  const float up = __uint_as_float(static_cast<uint32_t>(k) << 23);
+  float ss = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < kN; ++i) ss = fmaf(v[i] * up, v[i] * up, ss);
+  return make_float2(row_sum<kWarp>(ss, t, step) / cols + eps * up * up, up);
+}
 
 // A row to a CTA (or, up to 512 columns, to a warp): kChunks pieces of 16 columns stay
 // in the thread's registers from the sum of squares to the codes, so the row is read once.
 template <int kChunks, bool kWarp>
-__global__ void norm_rows_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMostLanes)
+norm_rows_kernel(const NormParams p) {
   const int t = threadIdx.x, step = blockDim.x;
   const int row = kWarp ? blockIdx.x * kWarpRows + threadIdx.y : blockIdx.x;
   const int pieces = p.cols / 16;
@@ -78,17 +135,17 @@ __global__ void norm_rows_kernel(const NormParams p) {
     }
   }
   if (p.norm_w) {
+    float mean = row_sum<kWarp>(ss, t, step) / p.cols + p.eps;
+    if (!(mean >= least_mean() && mean < __uint_as_float(0x7F800000u))) {
+      float copy[kChunks * 16];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!kWarp) {
-      __shared__ float part[32];
-      if ((t & 31) == 0) part[t >> 5] = ss;
-      __syncthreads();
-      ss = (t & 31) < (step >> 5) ? part[t & 31] : 0.f;
+      for (int i = 0; i < kChunks * 16; ++i) copy[i] = v[i >> 4][i & 15];
+      const float2 wide = wide_mean<kChunks * 16, kWarp>(copy, mean, p.cols, p.eps, t, step);
+      mean = wide.x;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int i = 0; i < kChunks * 16; ++i) v[i >> 4][i & 15] *= wide.y;
     }
-    const float inv = rsqrtf(ss / p.cols + p.eps);
+    const float inv = rsqrtf(mean);
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int i = t + c * step;
@@ -220,7 +277,7 @@ __global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightPara
   if (t == 0) p.scale[blockIdx.x] = s;
 }
 
-constexpr int kMaxCols = 32768;   // of dflash_fp8_norm_rows: 512 threads x 4 pieces of 16
+constexpr int kMaxCols = 16 * 4 * kMostLanes;   // of dflash_fp8_norm_rows
 
 template <int kChunks>
 int launch_norm(const NormParams& p, cudaStream_t st) {
@@ -277,8 +334,8 @@ extern "C" int dflash_fp8_norm_rows(int32_t rows, int32_t cols, const void* x, i
     return launch(norm_rows_kernel<1, true>,
                   dim3((static_cast<unsigned>(rows) + kWarpRows - 1) / kWarpRows),
                   dim3(32, kWarpRows), 0, st, p);
-  if (cols <= 16 * 512) return launch_norm<1>(p, st);
-  if (cols <= 16 * 1024) return launch_norm<2>(p, st);
+  if (cols <= 16 * kMostLanes) return launch_norm<1>(p, st);
+  if (cols <= 16 * 2 * kMostLanes) return launch_norm<2>(p, st);
   return launch_norm<4>(p, st);
 }
 

@@ -613,7 +613,8 @@ DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
 /*
  * dflash_fp8_norm_rows — s = x + residual;  sum_out = s;
  *   h = s / sqrt(mean(s^2) + rms_eps) * norm_w;  (q, scale) = h in 8 bits
- * in fp32, s not rounded on the way to h.  residual NULL: s = x.  norm_w NULL: h = s (rows
+ * in fp32, s not rounded on the way to h (nor do its squares leave the range of fp32: a row
+ * of very large or very small elements is normed as any other).  residual NULL: s = x.  norm_w NULL: h = s (rows
  * rounded as they are, e.g. an attention's output).  sum_out NULL: not stored.
  *   x, residual, sum_out: bf16 [rows, cols], pitches a multiple of 8 and at least cols;
  *   sum_out may be x or residual themselves (same pitch), else overlaps nothing;
