@@ -17,6 +17,7 @@
 // at once read 16 KB less, but leave the epilogue half the time: 536 us.  The rest is power:
 // zeros as operands take 440 us.
 #include "fp8_linear.cuh"
+#include "per_device.h"
 
 namespace dflash {
 namespace fp8 {
@@ -473,14 +474,17 @@ int run(Linear p, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // clusters that fit at once (one CTA to an SM), once per process
-  static const int most = [&] {
+  // clusters that fit at once (one CTA to an SM)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH_E_CUDA;
+  static PerDevice fit;
+  const int most = fit.get(dev, [&] {
     cudaLaunchConfig_t q = cfg;
     q.gridDim = dim3(p.sms / kCtas * kCtas);
     q.dynamicSmemBytes = kSmemLimit;
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, kernel, &q) == cudaSuccess ? n : 0;
-  }();
+  });
   if (most < 1) return DFLASH_E_CUDA;
   const long long tiles = most_tiles(p, kTileRows * kCtas, kN);
   if (tiles > 0x7FFFFFFF - 256ll * kBand) return DFLASH_E_UNSUPPORTED;
