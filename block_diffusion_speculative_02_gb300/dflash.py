@@ -773,12 +773,19 @@ def _shape(t, dims: int, name: str):
     return shape
 
 
+def _past_31_bits(*sizes):
+    """The C calls take sizes of 31 bits; ctypes would cut off the rest."""
+    raise ValueError(f"sizes {list(sizes)}: none may be past 2^31 - 1")
+
+
 def dflash_fp8_norm_rows(x, residual, norm_w, rms_eps: float, sum_out, q, scale, stream=None):
     """q, scale = 8-bit rows of RMSNorm(x + residual) * norm_w; sum_out = x + residual.
 
     ``residual``, ``norm_w`` and ``sum_out`` may be None: nothing added, not normed, not stored."""
     dev, st = _here(stream)
     shape = rows, cols = _shape(x, 2, "x")
+    if (rows | cols) >> 31:
+        _past_31_bits(rows, cols)
     rc = load_library().dflash_fp8_norm_rows(
         rows, cols, *_matrix(x, dev, "x", shape),
         *((None, 0) if residual is None else _matrix(residual, dev, "residual", shape)),
@@ -796,6 +803,8 @@ def dflash_fp8_silu_mul(gate_up, q, scale, stream=None):
     if cols % 2:
         raise ValueError("gate_up must have an even number of columns: gate, then up")
     cols //= 2
+    if (rows | cols) >> 31:
+        _past_31_bits(rows, cols)
     rc = load_library().dflash_fp8_silu_mul(
         rows, cols, *_matrix(gate_up, dev, "gate_up", shape),
         *_codes(q, scale, dev, (rows, cols), (-(-cols // 128), rows), "q", "scale"), st)
@@ -810,8 +819,11 @@ def dflash_fp8_weight(w, q, scale, stream=None):
     if len(shape) not in (2, 3):
         raise ValueError("w must be a tensor [N, K] or [G, N, K]")
     *g, n, k = shape
+    groups = g[0] if g else 1
+    if (groups | n | k) >> 31:
+        _past_31_bits(groups, n, k)
     rc = load_library().dflash_fp8_weight(
-        g[0] if g else 1, n, k, _whole(w, dev, _BF, None, "w"),
+        groups, n, k, _whole(w, dev, _BF, None, "w"),
         *_codes(q, scale, dev, shape, (*g, -(-n // 128), -(-k // 128)), "q", "scale"), st)
     if rc:
         _check(rc, "dflash_fp8_weight")
@@ -847,6 +859,8 @@ def dflash_fp8_linear(x, x_scale, w, w_scale, out, ws, stream=None):
     n, kw = _shape(w, 2, "w")
     if kw != k:
         raise ValueError(f"x has {k} columns, w {kw}")
+    if (m | n | k) >> 31:
+        _past_31_bits(m, n, k)
     kb = -(-k // 128)
     rc = load_library().dflash_fp8_linear(
         m, n, k, *_product(x, x_scale, w, w_scale, out, ws, dev, (kb, m), (-(-n // 128), kb),
@@ -864,6 +878,8 @@ def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None
     if kw != k:
         raise ValueError(f"x has {k} columns, w {kw}")
     m, kb = _shape(out, 2, "out")[0], -(-k // 128)
+    if (m | src | e | n | k) >> 31:
+        _past_31_bits(m, src, e, n, k)
     if rows is None and m != src:
         raise ValueError(f"out has {m} rows, x {src}: rows must say which")
     xp, xsp, wp, wsp, op, pitch, sp, size = _product(
