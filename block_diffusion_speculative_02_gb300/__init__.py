@@ -24,7 +24,7 @@ from .dflash import (DFlashError, Dims, KV4Dims, KV4View, KVView,  # noqa: F401
                      alloc_prefill_workspace, alloc_workspace, dflash_block_attention,
                      dflash_ctx_prefill, dflash_ctx_project, dflash_cycle_sm_split,
                      dflash_draft_mlp, dflash_draft_qkv, dflash_draft_tokens, dflash_fp8_grouped,
-                     dflash_fp8_linear, dflash_fp8_norm_rows, dflash_fp8_silu_mul,
+                     dflash_fp8_linear, dflash_fp8_norm_rows, dflash_fp8_plan, dflash_fp8_silu_mul,
                      dflash_fp8_weight, dflash_gdn_replay,
                      dflash_kv4_append, dflash_kv4_attention, dflash_kv4_gather,
                      dflash_kv4_workspace_bytes, dflash_kv_crop, dflash_kv_reserve,

@@ -9,7 +9,8 @@ namespace dflash {
 namespace fp8 {
 namespace {
 
-// Which kernel takes a call; `rows`: of an expert, on average.
+// Which kernel takes a call (of p: sizes, whether there are start and rows, and the SMs); `rows`: of
+// an expert, on average.
 //
 // Up to 16 rows (32, if there is one expert) the weights are streamed with the smallest tile that
 // holds the rows: 128 experts of 4 rows by index x 1536 x 2048 take 53, 51, 52 us with tiles of 16,
@@ -26,12 +27,10 @@ namespace {
 // the tiles: 16 experts of 80 rows x 1536 x 2048 take 14.5 with 128 x 256 tiles, 16.9 streamed 32
 // rows at a time, 20 64 rows; in order 11.9, 16.3, 16.7; 64 experts of 400 rows 104, in order 91
 // (pairs 88).  (Pairs by index were slower at every size.)
-int choose(Linear& p, cudaStream_t st) {
-  p.sms = current_num_sms();
-  if (p.sms <= 0) return DFLASH_E_CUDA;
+Choice choose(const Linear& p) {
   const int rows = static_cast<int>((static_cast<long long>(p.m) + p.groups - 1) / p.groups);
-  if (rows <= (p.start ? 8 : 16)) return run_stream(p, 16, st);
-  if (rows <= (p.start ? 16 : 32)) return run_stream(p, 32, st);
+  if (rows <= (p.start ? 8 : 16)) return {16, 128};
+  if (rows <= (p.start ? 16 : 32)) return {32, 128};
   // us: the start, and the waves of a tile's blocks and its end
   const auto cost = [&](int tile_rows, int features, int at_once, double start, double block,
                         double end) {
@@ -45,9 +44,24 @@ int choose(Linear& p, cudaStream_t st) {
   const double tiles = std::min(small, std::min(wide, pair));
   const double thin = stream_cost(p, 32), thick = stream_cost(p, 64);
   if ((!p.start && rows <= 64) || std::min(thin, thick) < tiles)
-    return run_stream(p, thin < thick ? 32 : 64, st);
-  return run_tiles(p, tiles == small ? Tiles::k128x128
-                      : tiles == wide ? Tiles::k128x256 : Tiles::k256x256, st);
+    return {thin < thick ? 32 : 64, 128};
+  if (tiles == small && !p.rows) return {128, 128};
+  if (tiles == wide) return {128, 256};
+  return {256, 256};
+}
+
+int run(Linear& p, cudaStream_t st) {
+  p.sms = current_num_sms();
+  if (p.sms <= 0) return DFLASH_E_CUDA;
+  const Choice c = choose(p);
+  return c.rows < 128 ? run_stream(p, c.rows, st) : run_tiles(p, c, st);
+}
+
+// Sizes that the kernels do not take, of the product and of x (rows of the weights and tiles are
+// counted in 31 bits).
+bool too_large(int m, int n_src, int groups, int n, int k) {
+  return k % 16 || groups > kMaxGroups || static_cast<long long>(groups) * n > 0x7FFFFFFFll - 256 ||
+         m > 0x7FFFFFFF - 256 || n > 0x7FFFFFFF - 256 || n_src > 0x7FFFFFFF - 256;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -57,11 +71,7 @@ int check(int m, int n_src, int groups, int n, int k, const void* x, const float
           const void* w, const float* ws, void* out, int64_t out_pitch, void* wsp,
           size_t ws_bytes, Linear* p) {
   if (m < 0 || n_src < 0 || groups < 1 || n < 1 || k < 1) return DFLASH_E_ARG;
-  if (k % 16 || groups > kMaxGroups) return DFLASH_E_UNSUPPORTED;
-  // rows of the weights and tiles are counted in 31 bits
-  if (static_cast<long long>(groups) * n > 0x7FFFFFFFll - 256 || m > 0x7FFFFFFF - 256 ||
-      n > 0x7FFFFFFF - 256 || n_src > 0x7FFFFFFF - 256)
-    return DFLASH_E_UNSUPPORTED;
+  if (too_large(m, n_src, groups, n, k)) return DFLASH_E_UNSUPPORTED;
   if (m == 0) return DFLASH_OK;
   if (!x || !xs || !w || !ws || !out || out_pitch < n || n_src < 1) return DFLASH_E_ARG;
   if (!aligned16(x) || !aligned16(w) || !aligned4(xs) || !aligned4(ws) ||
@@ -104,7 +114,7 @@ extern "C" int dflash_fp8_linear(int32_t rows, int32_t n_out, int32_t n_in, cons
   const int rc = check(rows, rows, 1, n_out, n_in, x, x_scale, w, w_scale, out, out_pitch, ws,
                        ws_bytes, &p);
   if (rc || rows == 0) return rc;
-  return choose(p, reinterpret_cast<cudaStream_t>(stream));
+  return run(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int dflash_fp8_grouped(int32_t n_rows, int32_t n_src, int32_t n_groups, int32_t n_out,
@@ -124,5 +134,32 @@ extern "C" int dflash_fp8_grouped(int32_t n_rows, int32_t n_src, int32_t n_group
     return DFLASH_E_UNSUPPORTED;
   p.start = start;
   p.rows = rows;
-  return choose(p, reinterpret_cast<cudaStream_t>(stream));
+  return run(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dflash_fp8_plan(int32_t n_rows, int32_t n_groups, int32_t n_out, int32_t n_in,
+                               int by_index, int32_t num_sms, int32_t* tile_rows,
+                               int32_t* tile_features, int32_t* shares) {
+  static const int32_t some = 0;
+  const int groups = n_groups > 0 ? n_groups : 1;
+  if (n_rows < 1 || n_groups < 0 || n_out < 1 || n_in < 1 || num_sms < 0 || !tile_rows ||
+      !tile_features || !shares)
+    return DFLASH_E_ARG;
+  if (too_large(n_rows, 1, groups, n_out, n_in)) return DFLASH_E_UNSUPPORTED;
+  Linear p = {};
+  p.m = n_rows;
+  p.n = n_out;
+  p.k = n_in;
+  p.groups = groups;
+  p.k_blocks = static_cast<int>(blocks(n_in));
+  p.n_blocks = static_cast<int>(blocks(n_out));
+  p.start = n_groups > 0 ? &some : nullptr;
+  p.rows = n_groups > 0 && by_index ? &some : nullptr;
+  p.sms = num_sms > 0 ? num_sms : current_num_sms();
+  if (p.sms <= 0) return DFLASH_E_CUDA;
+  const Choice c = choose(p);
+  *tile_rows = c.rows;
+  *tile_features = c.features;
+  *shares = c.rows < 128 ? stream_shares(p, c.rows) : 1;
+  return DFLASH_OK;
 }

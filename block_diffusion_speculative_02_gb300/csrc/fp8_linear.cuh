@@ -465,13 +465,17 @@ inline double row_tiles(const Linear& p, int tile_rows) {
   return with_rows * (own > 1 ? own : 1);
 }
 
+// Rows and features of a tile.
+struct Choice {
+  int rows, features;
+};
 // Tiles of 128 rows x 128 or 256 features, or, of a pair of CTAs, 256 x 256; of rows by index
 // 128 x 256.
-enum class Tiles { k128x128, k128x256, k256x256 };
-int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st);
+int run_tiles(const Linear& p, Choice tile, cudaStream_t st);
 // At most `rows` (16, 32 or 64) rows at a time against weights streamed once.
 int run_stream(const Linear& p, int rows, cudaStream_t st);
-// About how many us that takes (32 or 64).
+// CTAs that share a tile's K there, and about how many us that takes (32 or 64).
+int stream_shares(const Linear& p, int rows);
 double stream_cost(const Linear& p, int rows);
 
 }  // namespace fp8

@@ -422,8 +422,7 @@ int run(Linear p, cudaStream_t st) {
   const int nsm = p.sms;
   const long long tiles = most_tiles(p, kT, 128);
   if (tiles > 0x7FFFFFFF / 16) return DFLASH_E_UNSUPPORTED;
-  int split;
-  stream_split(p, kT, static_cast<double>(tiles), &split);
+  const int split = stream_shares(p, kT);
   // shares of K: one tile to a cluster; whole tiles: two CTAs to an SM walk them
   const long long ctas = split > 1 ? tiles * split : tiles < 2 * nsm ? tiles : 2 * nsm;
   cudaLaunchConfig_t cfg = {};
@@ -444,6 +443,12 @@ int run(Linear p, cudaStream_t st) {
 }
 
 }  // namespace
+
+int stream_shares(const Linear& p, int rows) {
+  int split;
+  stream_split(p, rows, static_cast<double>(most_tiles(p, rows, 128)), &split);
+  return split;
+}
 
 double stream_cost(const Linear& p, int rows) {
   int split;

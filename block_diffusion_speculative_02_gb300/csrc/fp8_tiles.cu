@@ -495,10 +495,10 @@ int run(Linear p, cudaStream_t st) {
 
 }  // namespace
 
-int run_tiles(const Linear& p, Tiles tiles, cudaStream_t st) {
+int run_tiles(const Linear& p, Choice tile, cudaStream_t st) {
   if (p.rows) return run<false, 256, true>(p, st);
-  if (tiles == Tiles::k128x128) return run<false, 128, false>(p, st);
-  if (tiles == Tiles::k128x256) return run<false, 256, false>(p, st);
+  if (tile.features == 128) return run<false, 128, false>(p, st);
+  if (tile.rows == 128) return run<false, 256, false>(p, st);
   // Few tiles of many blocks: the way out in two halves leaves shared memory for a fifth stage (512
   // rows x 24576 x 4096 41 us, 45 with four; 700 x 12288 x 4096 27 and 28).  Else at once: 4000 x
   // 12288 x 768 40 us, 43.5 in halves, 2000 x 12288 x 256 13.2 and 14.5; 8191 x 24576 x 4096 alike

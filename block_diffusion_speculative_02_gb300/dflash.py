@@ -44,7 +44,7 @@ EXPORTED = ["dflash_workspace_bytes", "dflash_workspace_init", "dflash_ctx_proje
             "dflash_kv4_workspace_bytes", "dflash_kv_reserve", "dflash_qk_norm_rope",
             "dflash_kv4_append", "dflash_kv4_gather", "dflash_kv4_attention",
             "dflash_fp8_norm_rows", "dflash_fp8_silu_mul", "dflash_fp8_weight",
-            "dflash_fp8_linear", "dflash_fp8_grouped"]
+            "dflash_fp8_linear", "dflash_fp8_grouped", "dflash_fp8_plan"]
 
 
 class DFlashError(RuntimeError):
@@ -171,6 +171,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dflash_fp8_linear.argtypes = [i32] * 3 + [vp] * 5 + [i64, vp, sz, vp]
     lib.dflash_fp8_grouped.restype = ctypes.c_int
     lib.dflash_fp8_grouped.argtypes = [i32] * 5 + [vp] * 7 + [i64, vp, sz, vp]
+    lib.dflash_fp8_plan.restype = ctypes.c_int
+    lib.dflash_fp8_plan.argtypes = [i32] * 4 + [ctypes.c_int, i32] + [ctypes.POINTER(i32)] * 3
     lib.dflash_cycle_sm_split.restype = ctypes.c_int
     lib.dflash_cycle_sm_split.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(i32),
                                           ctypes.POINTER(i32)]
@@ -890,3 +892,15 @@ def dflash_fp8_grouped(x, x_scale, w, w_scale, start, rows, out, ws, stream=None
         size, st)
     if rc:
         _check(rc, "dflash_fp8_grouped")
+
+
+def dflash_fp8_plan(rows: int, n_out: int, n_in: int, n_groups: int = 0, by_index: bool = False,
+                    num_sms: int = 0):
+    """(tile rows, tile features, CTAs that share a tile's n_in) of the kernel that a product of these
+    sizes goes to: dflash_fp8_linear, or, of n_groups experts, dflash_fp8_grouped."""
+    if max(rows, n_out, n_in, n_groups, num_sms) >> 31:
+        _past_31_bits(rows, n_out, n_in, n_groups, num_sms)
+    got = [ctypes.c_int32() for _ in range(3)]
+    _check(load_library().dflash_fp8_plan(rows, n_groups, n_out, n_in, int(by_index), num_sms,
+                                          *map(ctypes.byref, got)), "dflash_fp8_plan")
+    return tuple(v.value for v in got)

@@ -673,6 +673,17 @@ DFLASH_API int dflash_fp8_grouped(int32_t n_rows, int32_t n_src, int32_t n_group
                                   const int32_t* rows, void* out, int64_t out_pitch, void* ws,
                                   size_t ws_bytes, dflash_stream_t stream);
 
+/*
+ * dflash_fp8_plan — which kernel a product of these sizes goes to, without a launch (for tests and
+ * profiles): of dflash_fp8_linear (n_groups = 0) or dflash_fp8_grouped, there with rows by index or
+ * not, on a device of num_sms SMs (0: the current one).
+ *   *tile_rows x *tile_features: of a tile: 16, 32 or 64 x 128 (the weights are streamed past few
+ *   rows), 128 x 128, 128 x 256, or 256 x 256 (of two SMs); *shares: CTAs that share a tile's n_in.
+ */
+DFLASH_API int dflash_fp8_plan(int32_t n_rows, int32_t n_groups, int32_t n_out, int32_t n_in,
+                               int by_index, int32_t num_sms, int32_t* tile_rows,
+                               int32_t* tile_features, int32_t* shares);
+
 /* Copy the status word to *host_status (synchronises `stream`); if clear != 0
  * reset it to zero afterwards. */
 DFLASH_API int dflash_read_status(void* ws, uint32_t* host_status, int clear, dflash_stream_t stream);
@@ -691,7 +702,7 @@ DFLASH_API const char* dflash_status_string(int code);
  */
 DFLASH_API int dflash_selftest_wait(int arrive, void* ws, size_t ws_bytes, dflash_stream_t stream);
 
-/* Library ABI version (major * 100 + minor): 110. */
+/* Library ABI version (major * 100 + minor): 111. */
 DFLASH_API int dflash_version(void);
 
 #ifdef __cplusplus
