@@ -17,9 +17,12 @@ namespace {
 // 32, 64 rows; 8 experts of 8 rows x 4096 x 2048 9.7, 10.7, 13.8; 24 rows x 4096 x 4096 7.9, 6.6,
 // 7.5.  More rows: whichever the estimates say is the fastest.  Of 264 sizes of products by expert
 // (4 to 128 experts of 1 to 1000 rows, by index and in order) the choice is 1.7 % slower on average
-// than the fastest kernel.
+// than the fastest kernel.  The estimates were fitted to bursts (one call again and again, weights in
+// L2 as far as they fit).  They order the kernels; as times they are low where many experts go to
+// pairs: 64 experts of 512 rows on average x 2048 x 1408 85 us, 104 measured (117 in continuous use);
+// 128 of 512 x 1536 x 2048 170, 208 (239).
 //
-// Examples, in us.  Few features leave SMs without a tile: 128 rows x 4096 x 12288 take 17 streamed
+// Examples, in us, of bursts.  Few features leave SMs without a tile: 128 rows x 4096 x 12288 take 17 streamed
 // in shares of K, 30 with tiles; x 2560 x 2560 8.1 and 8.4; 200 rows x 512 x 768 4.4 and 5.3.
 // Among tiles the fewest waves win, each worth its time: 512 rows x 4096 x 4096 take 12.6 with
 // 128 x 128 tiles, 14.6 with 128 x 256, 14.1 with pairs; 128 rows x 24576 27, 24, 33; 512 rows x

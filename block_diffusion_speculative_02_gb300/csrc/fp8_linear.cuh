@@ -353,8 +353,8 @@ struct Tile {
 // Tile t of the walk: groups one after the other, in a group bands of kBand row tiles, in a band
 // chunks of kChunk feature tiles, in a chunk the features fastest.  A wave shares weights, which
 // leave memory once a band; a band's rows stay in L2; neighbours ask for the same rows at the same
-// time.  (Rows fastest: 128 experts of 512 rows by index x 1536 x 2048 take 292 us, 267 this way,
-// 8192 rows x 4096 x 12288 295 and 284; chunks of 2 to 12 lie between, within the noise.)
+// time.  (8192 rows x 4096 x 12288 in continuous use: 313 us, 325 with the rows fastest; 128 experts
+// of 512 rows by index x 1536 x 2048 257 and 254, of 200 rows 125 and 126; other sizes alike.)
 template <int kRows>
 __device__ __forceinline__ Tile tile_at(const Linear& p, const Groups& g, int t) {
   const int e = p.groups > 1 ? group_of(g, p.groups, t / p.n_tiles) : 0;
@@ -417,7 +417,7 @@ __device__ __forceinline__ void copy_rows(const Linear& p, uint8_t* dst, int col
 // One warp's copies: each block into the next stage.  They arrive at the stage's barrier themselves
 // (landed, 32 for a warp) when they are there; who hands them on to the tensor cores fences.
 // (Announced by the warp itself two blocks later, 128 experts of 200 rows x 1536 x 2048 took 155
-// us, 112 this way.)
+// us, 112 this way, in bursts.)
 struct RowCopies {
   uint32_t stage = 0, phase = 0;   // of the next block to copy
 

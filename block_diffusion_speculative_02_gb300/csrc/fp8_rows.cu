@@ -185,7 +185,9 @@ struct SiluParams {
 constexpr int kSiluThreads = 256;
 
 // g / (1 + exp(-g)) as (g / 8) / (1 / 8 + exp(-g) / 8): a divisor past 2^126 has no reciprocal
-// but zero, and exp(-g) reaches 2^128.
+// but zero, and exp(-g) reaches 2^128.  Relative to it the result is off by at most 6 + |g| units of
+// 2^-23: the exponent |g| + 1 (the constant and the fma, 2^-24 of |g| log2 e each), the exponential
+// 2, the reciprocal 1, the sum and the product half a unit each.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kLog2e = 1.44269504f;
   const float t = g * 0.125f;

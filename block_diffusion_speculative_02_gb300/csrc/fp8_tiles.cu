@@ -6,16 +6,20 @@
 //
 // A block's sums leave TMEM in the time of the next block's products (512 cycles at 256
 // features): 16 warps take a quarter of the features of 32 rows each, so that four warps of
-// a scheduler cover each other's waits.  (8191 rows x 24576 x 4096: 504 us, 655 with 8 warps of
-// twice the features.)  They wait at named barriers, where a warp takes no turn: one more warp
-// watches the accumulators' mbarriers for them.  (With all of them trying an mbarrier 640 us: a try
-// took the warps that issue the products 400 clocks and more.)
+// a scheduler cover each other's waits.  (8191 rows x 24576 x 4096 in a burst: 504 us, 655 with 8
+// warps of twice the features.)  They wait at named barriers, where a warp takes no turn: one more
+// warp watches the accumulators' mbarriers for them.  (With all of them trying an mbarrier 640 us: a
+// try took the warps that issue the products 400 clocks and more.)
+//
+// A burst is twenty copies of one call in a graph, too short for the power limit, on tensors that
+// stay in L2 as far as they fit.  It compares two forms of a kernel; in continuous use, each call
+// with weights of its own, this one takes 606 to 610 us.
 //
 // What bounds it: a block of a pair takes some 640 clocks, of which its products take 513.  That is
 // what shared memory needs for them (48 KB read, the rows twice, once for each half of the
 // features, and 32 KB written by the copies, at 128 bytes a clock).  Products of all 256 features
 // at once read 16 KB less, but leave the epilogue half the time: 536 us.  The rest is power:
-// zeros as operands take 440 us.
+// zeros as operands take 440 us, in a burst, too.
 #include "fp8_linear.cuh"
 #include "per_device.h"
 
@@ -37,7 +41,7 @@ constexpr int kScaleRow = kTileRows + 2;        // of the rows, then of the weig
 constexpr int kSmemLimit = 227 * 1024;
 
 // Accumulators of each half of the features (all that TMEM holds: 512 rows x 12288 x 4096 in tiles
-// of 128 features take 30.5 us with four, 32.2 with two), and blocks whose scales are in shared
+// of 128 features take 30.5 us with four, 32.2 with two, in a burst), and blocks whose scales are in shared
 // memory.
 template <int kN>
 __host__ __device__ constexpr int slots() {
@@ -499,10 +503,12 @@ int run_tiles(const Linear& p, Choice tile, cudaStream_t st) {
   if (p.rows) return run<false, 256, true>(p, st);
   if (tile.features == 128) return run<false, 128, false>(p, st);
   if (tile.rows == 128) return run<false, 256, false>(p, st);
-  // Few tiles of many blocks: the way out in two halves leaves shared memory for a fifth stage (512
-  // rows x 24576 x 4096 41 us, 45 with four; 700 x 12288 x 4096 27 and 28).  Else at once: 4000 x
-  // 12288 x 768 40 us, 43.5 in halves, 2000 x 12288 x 256 13.2 and 14.5; 8191 x 24576 x 4096 alike
-  // in a burst, 601 and 607 at the power limit.
+  // Few tiles of many blocks: the way out in two halves leaves shared memory for a fifth stage.  In
+  // continuous use, each call with weights of its own, 512 rows x 24576 x 4096 take 46.5 us, 47.3 with
+  // four stages; between a norm and a silu_mul, all three, 53.1 and 55.4 (700 x 12288 x 4096 37.7 and
+  // 39.3, 1024 x 4096 x 12288 54.5 and 59.0); in a burst 41 and 45.  No size tried was slower, nor
+  // did K of 1408 to 2048 gain.  Else at once (in bursts): 4000 x 12288 x 768 40 us, 43.5 in halves,
+  // 2000 x 12288 x 256 13.2 and 14.5; 8191 x 24576 x 4096 alike, 601 and 607 at the power limit.
   return p.k_blocks >= 32 && most_tiles(p, 256, 256) <= 2ll * p.sms
              ? run<true, 256, false, 32>(p, st) : run<true, 256, false>(p, st);
 }

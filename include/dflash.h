@@ -627,7 +627,8 @@ DFLASH_API int dflash_fp8_norm_rows(int32_t rows, int32_t cols, const void* x, i
                                     dflash_stream_t stream);
 
 /*
- * dflash_fp8_silu_mul — h = g / (1 + exp(-g)) * u in fp32, (q, scale) = h in 8 bits.
+ * dflash_fp8_silu_mul — h = g / (1 + exp(-g)) * u in fp32 (0 below g = -89.4, where the
+ *   reciprocal leaves its range), (q, scale) = h in 8 bits.
  *   gate_up: bf16 [rows, 2 cols], g the first cols columns, u the others; pitch a multiple
  *   of 8, at least 2 cols; q: [rows, cols]; cols a multiple of 16.
  */
@@ -645,7 +646,7 @@ DFLASH_API int dflash_fp8_weight(int32_t n_groups, int32_t n_out, int32_t n_in, 
  * dflash_fp8_linear — out = x w^T:
  *   out[m, n] = sum_b x_scale[b, m] w_scale[n / 128, b] sum_{k in block b} x[m, k] w[n, k]
  * with fp32 sums, block by block, and one rounding to bf16.  The product of any two scales
- * that meet must be a finite fp32 number.
+ * that meet is rounded to fp32 first: it must be finite, and below 2^-126 it loses digits.
  *   x: [rows, n_in]; w: [n_out, n_in]; out: bf16 [rows, n_out], rows out_pitch >= n_out
  *   elements apart (fastest where the pitch is a multiple of 8 and out 16-byte aligned).
  * DFLASH_ST_TIMEOUT is the only bit that it can set.

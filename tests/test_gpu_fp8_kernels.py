@@ -195,3 +195,26 @@ def test_the_same_bits_again(plan, m, n, k):
         dfl.dflash_fp8_grouped(x, xs, w[None], wscale[None], i32([0, m]), None, again, ws)
         assert torch.equal(first.view(torch.int16), again.view(torch.int16))
     assert dfl.dflash_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("m", [1, 5, 40, 300])
+def test_buffers_for_the_most_rows_serve_fewer(m):
+    """Codes cut to their first rows, scales from a flat buffer; and some of the rows by an index."""
+    import block_diffusion_speculative_02_gb300 as dfl
+    rng = np.random.default_rng(m)
+    most, n, k = 320, 384, 400
+    h = torch.from_numpy(rng.normal(size=(most, k))).to(BF).cuda()
+    w, wscale, wv = random_w(rng, n, k)
+    x_all, s_all = dfl.alloc_fp8_rows(most, k)
+    x, xs = x_all[:m], s_all.view(-1)[:O.blocks(k) * m].view(O.blocks(k), m)
+    dfl.dflash_fp8_norm_rows(h[:m], None, None, 0.0, None, x, xs)
+    out, ws = Guarded((m, n), BF), dfl.alloc_fp8_workspace()
+    dfl.dflash_fp8_linear(x, xs, w, wscale, out.t, ws)
+    xv = O.rows_value(x.view(torch.uint8).cpu().numpy(), xs.cpu().numpy())
+    check_product(f64(out.t), xv, wv)
+    out.check()
+    rows = np.arange(m // 2, m)
+    part = torch.empty(len(rows), n, dtype=BF, device="cuda")
+    dfl.dflash_fp8_grouped(x, xs, w[None], wscale[None], i32([0, len(rows)]), i32(rows), part, ws)
+    check_product(f64(part), xv[rows], wv)
+    assert dfl.dflash_read_status(ws) == 0
