@@ -607,7 +607,9 @@ DFLASH_API int dflash_kv4_attention(const dflash_kv4_dims* dims, const void* q,
  * and codes of the whole block NaN.
  * No rows (M = 0) is a call that does nothing.  The calls keep nothing between them; the
  * workspace of the products (64 bytes, aligned to 4, zeroed once) is their status word only,
- * and calls on several streams may share it.
+ * and calls on several streams may share it.  DFLASH_E_UNSUPPORTED: products with rows, n_src or
+ * n_groups * n_out past 2^31 - 257, more than 2^27 to 2^31 tiles, or, with rows named by an index,
+ * x of 2^36 bytes or more.
  */
 
 /*
